@@ -12,6 +12,11 @@
  *   tv_commit_accepted_kv  keep the accepted path's cache rows (contiguous), drop the rest
  *   tv_frontier_topw / tv_expand_children  one single-drafter tree-expansion step
  *   tv_prune_tree       per-parent child cap and depth-window re-rooting of a tree
+ * and the same round over a cache held in pages, with a prefix length per sequence:
+ *   tv_rotary_frequencies / tv_rotary  rotary positions
+ *   tv_append_kv_paged  new keys (rotated) and values into the pages, queries rotated
+ *   tv_paged_attention  causal or tree-masked attention of the new rows over the pages
+ *   tv_commit_accepted_kv_paged  tv_commit_accepted_kv through the page table
  *
  * Conventions shared by every call
  *   - Every pointer argument is a DEVICE pointer owned by the caller, unless marked
@@ -42,8 +47,8 @@
  *     get no output (each call below says what it leaves in their output rows).  Their
  *     logits and cache rows are still addressed as [B][N] blocks.
  *   - Logits / activations are row-major and contiguous.  bf16 is IEEE bfloat16.
- *   - The kernels of tv_select_subtree*, tv_tree_attention (tensor-core path) and
- *     tv_verify_* are launched with programmatic stream serialization: their CTAs may
+ *   - The kernels of tv_select_subtree*, tv_tree_attention (tensor-core path), tv_verify_*,
+ *     tv_rotary and the paged calls are launched with programmatic stream serialization: their CTAs may
  *     become resident while the previous kernel of the stream is still finishing, and
  *     each waits (griddepcontrol.wait) for that kernel to complete, with its memory
  *     visible, before it reads or writes any global memory.  Stream order and results
@@ -96,6 +101,7 @@ typedef enum tv_status {
 #define TV_DEV_BAD_TREE 1   /* parent[] breaks parent[0] = -1, 0 <= parent[i] < i */
 #define TV_DEV_BAD_TOKEN 2  /* a draft token is outside [0, V) or pool token invalid */
 #define TV_DEV_TIMEOUT 4    /* a bounded wait inside a kernel ran out (pipeline stall) */
+#define TV_DEV_BAD_PAGE 8   /* rows outside the page table, or a page outside the pool */
 
 /* Human-readable name of a tv_status value (static string, never NULL). */
 TV_API const char* tv_status_string(int status);
@@ -498,6 +504,147 @@ TV_API tv_status tv_select_subtree_adaptive(const float* marg, const int32_t* po
                                      const int32_t* root_token, int32_t* parent, int32_t* tokens,
                                      int32_t* depth, float* score, int32_t* n_nodes, void* workspace,
                                      size_t ws_bytes, int32_t* dev_status, tv_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Rotary positions.  The first rot_dim elements of a head form rot_dim / 2 pairs; pair i
+ * of a row at position p turns by p f_i:
+ *   (x, y) -> amplitude * (x cos - y sin, y cos + x sin),
+ * with pairs (i, i + rot_dim / 2), or (2i, 2i + 1) where `interleaved` is nonzero.  The
+ * other elements are copied.  The arithmetic is fp32, rounded once to the output type.
+ */
+typedef enum tv_rope_scaling {
+  TV_ROPE_NONE = 0,   /* f_i = base^(-2i / rot_dim)                       params unused */
+  TV_ROPE_LINEAR = 1, /* f_i / s                                          {s} */
+  TV_ROPE_BASE = 2,   /* base s^(rot_dim / (rot_dim - 2)) for base        {s} */
+  TV_ROPE_BANDED = 3, /* pairs with fewer than lo turns in L positions are slowed by s,
+                         those with more than hi are kept, a linear blend of the two in
+                         between                                          {s, lo, hi, L} */
+  TV_ROPE_YARN = 4    /* a blend linear in the pair index between those that turn `fast`
+                         (kept) and `slow` (slowed by s) times in L positions; amplitude
+                         0.1 ln s + 1                                     {s, L, fast, slow} */
+} tv_rope_scaling;
+
+/* tv_rotary_frequencies - HOST pointers: freq [rot_dim / 2] uint64 out, f_i / 2 pi in units
+ * of 2^-64 (so that p f_i mod one turn is exact integer arithmetic at any position), and
+ * *amplitude out.  The caller copies freq to the device once and keeps it.  Launches
+ * nothing.
+ * Errors: NULL freq, amplitude or (for a scaling with params) params -> TV_ERR_NULL;
+ * rot_dim odd or outside 2..1024 -> TV_ERR_SHAPE; base <= 1 or not finite, an unknown
+ * scaling, s < 1, hi <= lo, L, fast or slow <= 0, fast < slow, a parameter not finite ->
+ * TV_ERR_VALUE.
+ */
+TV_API tv_status tv_rotary_frequencies(int rot_dim, double base, int scaling, const double* params,
+                                       uint64_t* freq, float* amplitude);
+
+/* Host structs, read during the call. */
+typedef struct tv_rope {
+  const uint64_t* freq; /* device, [rot_dim / 2], from tv_rotary_frequencies */
+  int rot_dim;          /* even, 0..D; 0 rotates nothing */
+  int interleaved;
+  float amplitude;
+} tv_rope;
+
+/* Rows [B][H][N][D] anywhere in device memory, such as a part of a fused projection's
+ * output: the D elements of a row are contiguous, the strides are in elements. */
+typedef struct tv_rows {
+  const void* data;
+  int64_t batch_stride, head_stride, row_stride;
+} tv_rows;
+
+/* tv_rotary - rotate rows.  PTD §3.1: a node's position follows |pi(v)|, which
+ * tv_tree_prep writes (pos, or depth with the sequence's length in pos_base).
+ *   x        rows [B][H][N][D] dtype (any strides)
+ *   out      [B][H][N][D] dtype, contiguous; may be x itself where x is contiguous
+ *   pos      [B][N] int32; rows with pos < 0 (padding) are not written
+ *   pos_base [B] int32 added to pos, or NULL
+ * Limits: D <= 1024, any alignment of the element type.  16-byte aligned rows with rot_dim
+ * a multiple of 16 (bf16) or 8 (fp32) move 16 bytes a thread; others one element.
+ * Errors: NULL x, rope, out or pos, or freq with rot_dim > 0 -> TV_ERR_NULL; dtype ->
+ * TV_ERR_DTYPE; sizes, rot_dim odd or above D -> TV_ERR_SHAPE; amplitude not finite ->
+ * TV_ERR_VALUE; a pointer not aligned to its element -> TV_ERR_ALIGN.
+ */
+TV_API tv_status tv_rotary(const tv_rows* x, void* out, const int32_t* pos, const int32_t* pos_base,
+                           const tv_rope* rope, int B, int H, int N, int D, tv_dtype dtype,
+                           tv_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Paged caches.  k, v: [num_pages][Hkv][page_size][D]; cache row r of sequence b is row
+ * r mod page_size of page page_table[b][r / page_size].  prefix_len[b] = P_b rows are
+ * committed; row P_b + t belongs to new row (tree node) t of the current call.
+ * page_size: a power of two, 8..1024; max_pages * page_size < 2^31.
+ * Sequences may share pages of committed rows; a page that receives rows of two
+ * sequences in one call holds either's.  Table entries that no row of the call needs may
+ * hold anything.  On the device: P_b < 0, rows past max_pages pages, n_rows[b] outside
+ * 0..N, or a needed page outside [0, num_pages) set TV_DEV_BAD_PAGE; nothing outside the
+ * pool is read or written, and the sequence's outputs are unspecified.
+ * n_rows [B] (or NULL: N) counts the active new rows of each sequence; those from
+ * n_rows[b] on, and in a tree those from the first padding row (parent -1) on, are
+ * inactive: not read, not written.
+ */
+typedef struct tv_paged_kv {
+  void* k;
+  void* v;
+  const int32_t* page_table; /* device, [B][max_pages] */
+  const int32_t* prefix_len; /* device, [B] */
+  int num_pages, page_size, max_pages;
+} tv_paged_kv;
+
+/* tv_append_kv_paged - write the new rows' keys and values into the pages, the keys rotated
+ * on the way, and (optionally) rotate their queries in the same pass.
+ *   k, v   rows [B][Hkv][N][D] dtype (any strides)
+ *   q      rows [B][Hq][N][D] or NULL; q_out [B][Hq][N][D] contiguous (with q)
+ *   depth  [B][N] int32: row t sits at position P_b + depth[b][t] (tv_tree_prep's depth;
+ *          -1 = padding, not written); NULL: P_b + t
+ *   rope   NULL: nothing is rotated (and q must be NULL)
+ * Row t goes to cache row P_b + t.  Limits: D <= 1024, rows of D elements a multiple of 16
+ * bytes, caches 16-byte aligned.
+ * Errors as tv_rotary, and: q without q_out or rope -> TV_ERR_NULL; cache alignment ->
+ * TV_ERR_ALIGN.
+ */
+TV_API tv_status tv_append_kv_paged(const tv_rows* k, const tv_rows* v, const tv_paged_kv* kv,
+                                    const int32_t* depth, const int32_t* n_rows, const tv_rope* rope,
+                                    const tv_rows* q, void* q_out, int B, int Hq, int Hkv, int N, int D,
+                                    tv_dtype dtype, int32_t* dev_status, tv_stream_t stream);
+
+/* tv_paged_attention - attention of the new rows over the paged cache (blog, "why target
+ * verification can be parallel"; PTD §3.1 for the tree mask).
+ *   out[b,h,i,:] = sum_j softmax_j(z_ij) v[b,h/G,j,:], G = Hq / Hkv,
+ *   z_ij = scale q_i . k_j, or softcap * tanh(scale q_i . k_j / softcap) where softcap > 0,
+ *   over the committed rows j < P_b and the new rows P_b + t with t <= i (parent NULL: a
+ *   causal chunk) or t in pi(i) (a tree); with window > 0 only those at most window - 1
+ *   positions before row i, a tree node's position being P_b + its depth.
+ *   q, out  [B][Hq][N][D] dtype, contiguous; the new rows' keys and values are in the cache
+ *   parent  [B][N] int32 (tree layout above) or NULL
+ *   scale   > 0, or 0 for 1/sqrt(D);  softcap, window: 0 = none
+ * The keys and values of active rows and of committed rows within the window must be
+ * finite; other cache rows may hold anything, NaN included.
+ * Precision as tv_tree_attention.  Limits: 32 <= D <= 256, D % 32 == 0, Hq % Hkv == 0,
+ * 1 <= N <= 65536 (trees 1024), G * N < 2^24.  q, out and the caches 16-byte aligned.
+ * Workspace: tv_paged_attention_workspace_size(...) bytes, 16-byte aligned, zero-filled
+ * once; calls that share it must not overlap on the GPU.
+ * Errors: as tv_tree_attention; scale, softcap < 0 or not finite, window < 0 ->
+ * TV_ERR_VALUE; workspace missing or small -> TV_ERR_WORKSPACE.
+ */
+TV_API size_t tv_paged_attention_workspace_size(int B, int Hq, int Hkv, int D, int N, int page_size,
+                                                int max_pages, tv_dtype dtype);
+TV_API tv_status tv_paged_attention(const void* q, void* out, const tv_paged_kv* kv, const int32_t* parent,
+                                    const int32_t* n_rows, int B, int Hq, int Hkv, int N, int D,
+                                    float scale, float softcap, int window, tv_dtype dtype,
+                                    void* workspace, size_t ws_bytes, int32_t* dev_status,
+                                    tv_stream_t stream);
+
+/* tv_commit_accepted_kv_paged - tv_commit_accepted_kv through the page table: row P_b + a_k
+ * of every KV head of both caches is copied to row P_b + k, k = 1..L_b.
+ *   accepted_nodes [B][N], accept_len [B] int32 as tv_verify_* write them
+ *   new_len [B] int32 out or NULL: P_b + L_b + 1, the next round's prefix_len (another
+ *   array than prefix_len)
+ * Device checks as tv_commit_accepted_kv (TV_DEV_BAD_TREE) and of pages (TV_DEV_BAD_PAGE).
+ * Host errors as there, and new_len == prefix_len -> TV_ERR_VALUE.  No workspace.
+ */
+TV_API tv_status tv_commit_accepted_kv_paged(const tv_paged_kv* kv, const int32_t* accepted_nodes,
+                                             const int32_t* accept_len, int32_t* new_len, int B, int Hkv,
+                                             int N, int D, tv_dtype dtype, int32_t* dev_status,
+                                             tv_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -8,6 +8,7 @@ read.  There is no CPU fallback: if the shared library is missing the first call
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -23,6 +24,7 @@ TV_BF16 = 1
 TV_DEV_BAD_TREE = 1
 TV_DEV_BAD_TOKEN = 2
 TV_DEV_TIMEOUT = 4
+TV_DEV_BAD_PAGE = 8
 
 
 class TreeVerifyError(RuntimeError):
@@ -32,12 +34,29 @@ class TreeVerifyError(RuntimeError):
 
 
 _lib = None
+_CURRENT = contextlib.nullcontext()
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
 _SZ = ctypes.c_size_t
 _U64 = ctypes.c_uint64
+_D = ctypes.c_double
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("freq", _P), ("rot_dim", _I), ("interleaved", _I), ("amplitude", _F)]
+
+
+class _Rows(ctypes.Structure):
+    _fields_ = [("data", _P), ("batch_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("row_stride", ctypes.c_int64)]
+
+
+class _PagedKv(ctypes.Structure):
+    _fields_ = [("k", _P), ("v", _P), ("page_table", _P), ("prefix_len", _P), ("num_pages", _I), ("page_size", _I),
+                ("max_pages", _I)]
+
 
 _SIGS = {
     "tv_status_string": (ctypes.c_char_p, [_I]),
@@ -63,6 +82,12 @@ _SIGS = {
     "tv_expand_children": (_I, [_P, _P, _I, _I, _I, _F, _I, _P, _P, _P, _P, _SZ, _P, _P]),
     "tv_select_workspace_size": (_SZ, [_I, _I, _I, _I]),
     "tv_select_subtree": (_I, [_P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _SZ, _P, _P]),
+    "tv_rotary_frequencies": (_I, [_I, _D, _I, _P, _P, _P]),
+    "tv_rotary": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P]),
+    "tv_append_kv_paged": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P]),
+    "tv_paged_attention_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I, _I]),
+    "tv_paged_attention": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _F, _I, _I, _P, _SZ, _P, _P]),
+    "tv_commit_accepted_kv_paged": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P]),
     "tv_select_subtree_adaptive": (_I, [_P, _P, _I, _I, _I, _I, _F, _F, _P, _P, _P, _P, _P, _P, _P, _SZ, _P, _P]),
 }
 
@@ -151,6 +176,8 @@ def _ndim(name, t, n):
 def _on(dev):
     """Context making ``dev`` the current CUDA device for one library call, so that the
     library's per-device state and torch's current stream are those of the tensors."""
+    if dev.index == torch.cuda.current_device():
+        return _CURRENT
     return torch.cuda.device(dev)
 
 
@@ -579,3 +606,201 @@ def select_subtree(marg, pool_tokens, budget: int, root_token, *, dev_status=Non
                                                   _ptr(tok), _ptr(dep), _ptr(sc), _ptr(nn), _ptr(ws),
                                                   0 if ws is None else ws.numel(), _ptr(st), _stream()))
     return {"parent": par, "tokens": tok, "depth": dep, "score": sc, "n_nodes": nn, "dev_status": st}
+
+
+# ---- rotary positions and paged caches
+
+
+_ROPE_SCALING = {"linear": (1, 1), "base": (2, 1), "banded": (3, 4), "yarn": (4, 4)}  # kind, parameters
+
+
+def rotary_frequencies(rot_dim: int, base: float = 10000.0, *, scaling=None, device="cuda"):
+    """Frequencies of rotary positions over the first ``rot_dim`` elements of a head: the
+    ``rope`` argument of rotary and append_kv_paged (made once per model and kept).
+    scaling, for contexts longer than the model was trained on: None, ("linear", s),
+    ("base", s), ("banded", s, lo, hi, length) or ("yarn", s, length, fast, slow).  Returns
+    dict freq (int64 bits of 2^-64 turns a position, [rot_dim / 2]), amplitude, rot_dim."""
+    kind, params = 0, None
+    if scaling is not None:
+        name, *values = scaling
+        if name not in _ROPE_SCALING:
+            raise ValueError(f"unknown scaling {name!r}; use one of {sorted(_ROPE_SCALING)}")
+        kind, count = _ROPE_SCALING[name]
+        if len(values) != count:
+            raise ValueError(f"scaling {name!r} takes {count} parameters, got {len(values)}")
+        params = (ctypes.c_double * count)(*map(float, values))
+    freq = torch.empty(max(int(rot_dim) // 2, 1), dtype=torch.int64)
+    amp = ctypes.c_float(0.0)
+    _check("tv_rotary_frequencies", load_library().tv_rotary_frequencies(
+        int(rot_dim), float(base), kind, params, freq.data_ptr(), ctypes.byref(amp)))
+    return {"freq": freq.to(device), "amplitude": amp.value, "rot_dim": int(rot_dim)}
+
+
+def _rope_arg(rope, interleaved):
+    freq, rot = rope["freq"], int(rope["rot_dim"])
+    _need("rope['freq']", freq, torch.int64, (rot // 2,))
+    return _Rope(freq.data_ptr(), rot, int(bool(interleaved)), float(rope["amplitude"]))
+
+
+def _rows_arg(name, t, shape, dtype, dev):
+    """Rows [B][H][N][D] with any strides but contiguous elements."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, other arguments on {dev}: one device per call")
+    _need(name, t, dtype, shape)
+    sb, sh, sn, sd = t.stride()
+    if sd != 1 and shape[3] > 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return _Rows(t.data_ptr(), sb, sh, sn)
+
+
+def _same_memory(a, b):
+    return a.data_ptr() == b.data_ptr()
+
+
+def rotary(x, pos, rope, *, interleaved: bool = False, pos_base=None, out=None):
+    """Rotate rows x [B][H][N][D] (any strides, contiguous elements) at positions
+    pos [B][N] int32 (+ pos_base [B] int32).  rope: from rotary_frequencies.  Pairs are
+    (i, i + rot_dim / 2), or (2i, 2i + 1) with interleaved.  Rows with pos < 0 are left as
+    they are in out (new storage when omitted; x itself, where contiguous, to work in
+    place)."""
+    dev = _need_cuda(pos=pos, pos_base=pos_base, freq=rope["freq"], out=out)
+    _ndim("x", x, 4)
+    B, H, N, D = x.shape
+    rows = _rows_arg("x", x, x.shape, x.dtype, dev)
+    code = _dtype_code(x)
+    _need("pos", pos, torch.int32, (B, N))
+    if pos_base is not None:
+        _need("pos_base", pos_base, torch.int32, (B,))
+    if out is None:
+        out = torch.empty((B, H, N, D), dtype=x.dtype, device=dev)
+    else:
+        _need("out", out, x.dtype, (B, H, N, D))
+        if _same_memory(out, x) and not x.is_contiguous():
+            raise ValueError("x must be contiguous to be rotated in place")
+    rp = _rope_arg(rope, interleaved)
+    with _on(dev):
+        _check("tv_rotary", load_library().tv_rotary(ctypes.byref(rows), _ptr(out), _ptr(pos), _ptr(pos_base),
+                                                     ctypes.byref(rp), B, H, N, D, code, _stream()))
+    return out
+
+
+def _paged_kv(k_cache, v_cache, page_table, prefix_len):
+    """The tv_paged_kv of checked tensors; returns (struct, B, Hkv, page_size, max_pages, D)."""
+    _ndim("k_cache", k_cache, 4)
+    _ndim("page_table", page_table, 2)
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache must match")
+    pages, Hkv, ps, D = k_cache.shape
+    B, width = page_table.shape
+    _need("page_table", page_table, torch.int32, (B, width))
+    _need("prefix_len", prefix_len, torch.int32, (B,))
+    kv = _PagedKv(k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), prefix_len.data_ptr(), pages, ps,
+                  width)
+    return kv, B, Hkv, ps, width, D
+
+
+def append_kv_paged(k, v, k_cache, v_cache, page_table, prefix_len, *, depth=None, n_rows=None, rope=None,
+                    interleaved: bool = False, q=None, q_out=None, dev_status=None):
+    """Write new rows k, v [B][Hkv][N][D] (any strides, contiguous elements) into the paged
+    caches [num_pages][Hkv][page_size][D] at cache rows prefix_len[b] + t, the keys rotated
+    (with rope) at position prefix_len[b] + depth[b][t] (depth: tree_prep's, -1 = padding;
+    omitted: t).  page_table [B][max_pages], prefix_len [B], n_rows [B] (omitted: N each) are
+    int32.  With q [B][Hq][N][D] its rows are rotated too, into q_out (returned)."""
+    dev = _need_cuda(k_cache=k_cache, v_cache=v_cache, page_table=page_table, prefix_len=prefix_len, depth=depth,
+                     n_rows=n_rows, q_out=q_out, freq=None if rope is None else rope["freq"])
+    kv, B, Hkv, _, _, D = _paged_kv(k_cache, v_cache, page_table, prefix_len)
+    _ndim("k", k, 4)
+    N = k.shape[2]
+    code = _dtype_code(k_cache)
+    kr = _rows_arg("k", k, (B, Hkv, N, D), k_cache.dtype, dev)
+    vr = _rows_arg("v", v, (B, Hkv, N, D), k_cache.dtype, dev)
+    if depth is not None:
+        _need("depth", depth, torch.int32, (B, N))
+    if n_rows is not None:
+        _need("n_rows", n_rows, torch.int32, (B,))
+    qr, Hq = None, 0
+    if q is not None:
+        if rope is None:
+            raise ValueError("q is rotated: rope is required with it")
+        _ndim("q", q, 4)
+        Hq = q.shape[1]
+        qr = _rows_arg("q", q, (B, Hq, N, D), k_cache.dtype, dev)
+        if q_out is None:
+            q_out = torch.empty((B, Hq, N, D), dtype=q.dtype, device=dev)
+        else:
+            _need("q_out", q_out, q.dtype, (B, Hq, N, D))
+            if _same_memory(q_out, q) and not q.is_contiguous():
+                raise ValueError("q must be contiguous to be rotated in place")
+    rp = None if rope is None else _rope_arg(rope, interleaved)
+    st = _status_tensor(dev_status, dev)
+    with _on(dev):
+        _check("tv_append_kv_paged", load_library().tv_append_kv_paged(
+            ctypes.byref(kr), ctypes.byref(vr), ctypes.byref(kv), _ptr(depth), _ptr(n_rows),
+            None if rp is None else ctypes.byref(rp), None if qr is None else ctypes.byref(qr),
+            None if qr is None else _ptr(q_out), B, Hq, Hkv, N, D, code, _ptr(st), _stream()))
+    return q_out if q is not None else None
+
+
+def paged_attention_workspace_size(B, Hq, Hkv, D, N, page_size, max_pages, dtype) -> int:
+    code = TV_BF16 if dtype == torch.bfloat16 else TV_F32
+    return int(load_library().tv_paged_attention_workspace_size(B, Hq, Hkv, D, N, page_size, max_pages, code))
+
+
+def paged_attention(q, k_cache, v_cache, page_table, prefix_len, *, parent=None, n_rows=None, scale: float = 0.0,
+                    softcap: float = 0.0, window: int = 0, out=None, workspace=None, dev_status=None):
+    """Attention of new rows q [B][Hq][N][D] over paged caches [num_pages][Hkv][page_size][D]
+    that already hold their keys and values (append_kv_paged): causal, or tree-masked with
+    parent [B][N].  page_table [B][max_pages], prefix_len [B], n_rows [B] int32.  softcap > 0
+    caps scores by softcap * tanh(score / softcap); window > 0 hides keys `window` or more
+    positions back.  workspace: paged_attention_workspace_size bytes, zero-filled once
+    (allocated here when omitted)."""
+    dev = _need_cuda(q=q, k_cache=k_cache, v_cache=v_cache, page_table=page_table, prefix_len=prefix_len,
+                     parent=parent, n_rows=n_rows, out=out)
+    kv, B, Hkv, ps, width, D = _paged_kv(k_cache, v_cache, page_table, prefix_len)
+    _ndim("q", q, 4)
+    Hq, N = q.shape[1], q.shape[2]
+    _need("q", q, k_cache.dtype, (B, Hq, N, D))
+    code = _dtype_code(q)
+    if parent is not None:
+        _tree_inputs(parent, None, B, N)
+    if n_rows is not None:
+        _need("n_rows", n_rows, torch.int32, (B,))
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _need("out", out, q.dtype, (B, Hq, N, D))
+    st = _status_tensor(dev_status, dev)
+    lib = load_library()
+    with _on(dev):
+        ws = _workspace(lib.tv_paged_attention_workspace_size(B, Hq, Hkv, D, N, ps, width, code), dev, workspace)
+        _check("tv_paged_attention", lib.tv_paged_attention(
+            _ptr(q), _ptr(out), ctypes.byref(kv), _ptr(parent), _ptr(n_rows), B, Hq, Hkv, N, D, float(scale),
+            float(softcap), int(window), code, _ptr(ws), ws.numel() * ws.element_size(), _ptr(st), _stream()))
+    return out
+
+
+def commit_accepted_kv_paged(k_cache, v_cache, page_table, prefix_len, accepted_nodes, accept_len, *, new_len=None,
+                             dev_status=None):
+    """commit_accepted_kv over paged caches [num_pages][Hkv][page_size][D], in place: rows
+    prefix_len[b] + a_k move to prefix_len[b] + k.  accepted_nodes [B][N], accept_len [B] as
+    returned by verify_greedy / verify_sample.  Returns new_len [B] int32, the sequences'
+    committed rows after the round (prefix_len + accept_len + 1)."""
+    dev = _need_cuda(k_cache=k_cache, v_cache=v_cache, page_table=page_table, prefix_len=prefix_len,
+                     accepted_nodes=accepted_nodes, accept_len=accept_len, new_len=new_len)
+    kv, B, Hkv, _, _, D = _paged_kv(k_cache, v_cache, page_table, prefix_len)
+    _ndim("accepted_nodes", accepted_nodes, 2)
+    N = accepted_nodes.shape[1]
+    _need("accepted_nodes", accepted_nodes, torch.int32, (B, N))
+    _need("accept_len", accept_len, torch.int32, (B,))
+    if new_len is None:
+        new_len = torch.empty(B, dtype=torch.int32, device=dev)
+    else:
+        _need("new_len", new_len, torch.int32, (B,))
+    st = _status_tensor(dev_status, dev)
+    with _on(dev):
+        _check("tv_commit_accepted_kv_paged", load_library().tv_commit_accepted_kv_paged(
+            ctypes.byref(kv), _ptr(accepted_nodes), _ptr(accept_len), _ptr(new_len), B, Hkv, N, D,
+            _dtype_code(k_cache), _ptr(st), _stream()))
+    return new_len

@@ -324,4 +324,169 @@ tv_status tv_select_subtree_adaptive(const float* marg, const int32_t* pool_toke
                                    st(stream)));
 }
 
+tv_status tv_rotary_frequencies(int rot_dim, double base, int scaling, const double* params, uint64_t* freq,
+                                float* amplitude) {
+  if (!freq || !amplitude) return TV_ERR_NULL;
+  if (rot_dim < 2 || rot_dim > kMaxRotaryDim || rot_dim % 2) return TV_ERR_SHAPE;
+  if (!(base > 1.0) || isinf(base)) return TV_ERR_VALUE;
+  if (scaling < TV_ROPE_NONE || scaling > TV_ROPE_YARN) return TV_ERR_VALUE;
+  if (scaling != TV_ROPE_NONE) {
+    if (!params) return TV_ERR_NULL;
+    const int n = scaling >= TV_ROPE_BANDED ? 4 : 1;
+    for (int i = 0; i < n; ++i)
+      if (!isfinite(params[i])) return TV_ERR_VALUE;
+    if (params[0] < 1.0) return TV_ERR_VALUE;
+    if (scaling == TV_ROPE_BASE && rot_dim < 4) return TV_ERR_SHAPE;
+    if (scaling == TV_ROPE_BANDED && (!(params[2] > params[1]) || !(params[3] > 0.0))) return TV_ERR_VALUE;
+    if (scaling == TV_ROPE_YARN && (!(params[1] > 0.0) || !(params[3] > 0.0) || params[2] < params[3]))
+      return TV_ERR_VALUE;
+  }
+  rotary_frequencies(rot_dim, base, scaling, params, freq, amplitude);
+  return TV_OK;
+}
+
+// rows: a pointer aligned to its element
+static bool rows_aligned(const tv_rows* r, tv_dtype dtype) {
+  return reinterpret_cast<uintptr_t>(r->data) % (dtype == TV_BF16 ? 2 : 4) == 0;
+}
+static void rows_arg(RotaryArgs* a, int part, const tv_rows* r) {
+  a->src[part] = r->data;
+  a->sb[part] = r->batch_stride;
+  a->sh[part] = r->head_stride;
+  a->sn[part] = r->row_stride;
+}
+static tv_status rope_checks(const tv_rope* rope, int D) {
+  if (rope->rot_dim < 0 || rope->rot_dim > D || rope->rot_dim % 2) return TV_ERR_SHAPE;
+  if (rope->rot_dim > 0 && !rope->freq) return TV_ERR_NULL;
+  if (!isfinite(rope->amplitude)) return TV_ERR_VALUE;
+  return TV_OK;
+}
+
+tv_status tv_rotary(const tv_rows* x, void* out, const int32_t* pos, const int32_t* pos_base, const tv_rope* rope,
+                    int B, int H, int N, int D, tv_dtype dtype, tv_stream_t stream) {
+  NvtxRange nvtx_range("tv_rotary");
+  if (!x || !x->data || !out || !pos || !rope) return TV_ERR_NULL;
+  if (!valid_dtype(dtype)) return TV_ERR_DTYPE;
+  if (B < 1 || H < 1 || H > kMaxRotaryHeads || N < 1 || D < 1 || D > kMaxRotaryDim) return TV_ERR_SHAPE;
+  if ((long long)B * N > kMaxRotaryRows) return TV_ERR_SHAPE;
+  const tv_status s = rope_checks(rope, D);
+  if (s != TV_OK) return s;
+  if (!rows_aligned(x, dtype) || reinterpret_cast<uintptr_t>(out) % (dtype == TV_BF16 ? 2 : 4)) return TV_ERR_ALIGN;
+  RotaryArgs a{};
+  rows_arg(&a, 0, x);
+  a.q_out = out;
+  a.pos = pos;
+  a.base = pos_base;
+  a.freq = rope->freq;
+  a.amplitude = rope->amplitude;
+  a.B = B, a.Hq = H, a.N = N, a.D = D, a.rot = rope->rot_dim, a.interleaved = rope->interleaved != 0;
+  return cuda_status(launch_rotary(a, dtype, st(stream)));
+}
+
+static int log2_exact(int x) {
+  int s = 0;
+  while ((1 << s) < x) ++s;
+  return s;
+}
+
+// The checks that every call over a paged cache shares.
+static tv_status paged_checks(const tv_paged_kv* kv, int B, int Hkv, int N, int D, tv_dtype dtype) {
+  if (!kv || !kv->k || !kv->v || !kv->page_table || !kv->prefix_len) return TV_ERR_NULL;
+  if (!valid_dtype(dtype)) return TV_ERR_DTYPE;
+  if (B < 1 || Hkv < 1 || Hkv > kMaxRotaryHeads || N < 1 || D < 1 || D > kMaxRotaryDim) return TV_ERR_SHAPE;
+  const int ps = kv->page_size;
+  if (ps < 8 || ps > 1024 || (ps & (ps - 1)) || kv->num_pages < 1 || kv->max_pages < 1) return TV_ERR_SHAPE;
+  if ((long long)kv->max_pages * ps > 0x7fffffffLL || (long long)kv->num_pages * Hkv > 0x7fffffffLL)
+    return TV_ERR_SHAPE;
+  if (!aligned16(kv->k) || !aligned16(kv->v) || (long long)D * (dtype == TV_BF16 ? 2 : 4) % 16) return TV_ERR_ALIGN;
+  return TV_OK;
+}
+
+tv_status tv_append_kv_paged(const tv_rows* k, const tv_rows* v, const tv_paged_kv* kv, const int32_t* depth,
+                             const int32_t* n_rows, const tv_rope* rope, const tv_rows* q, void* q_out, int B, int Hq,
+                             int Hkv, int N, int D, tv_dtype dtype, int32_t* dev_status, tv_stream_t stream) {
+  NvtxRange nvtx_range("tv_append_kv_paged");
+  if (!k || !k->data || !v || !v->data) return TV_ERR_NULL;
+  if (q && (!q->data || !q_out || !rope)) return TV_ERR_NULL;
+  tv_status s = paged_checks(kv, B, Hkv, N, D, dtype);
+  if (s != TV_OK) return s;
+  if (q && (Hq < 1 || Hq > kMaxRotaryHeads)) return TV_ERR_SHAPE;
+  if ((long long)B * N > kMaxRotaryRows) return TV_ERR_SHAPE;
+  if (rope) {
+    s = rope_checks(rope, D);
+    if (s != TV_OK) return s;
+  }
+  if (!rows_aligned(k, dtype) || !rows_aligned(v, dtype)) return TV_ERR_ALIGN;
+  if (q && (!rows_aligned(q, dtype) || reinterpret_cast<uintptr_t>(q_out) % (dtype == TV_BF16 ? 2 : 4)))
+    return TV_ERR_ALIGN;
+  RotaryArgs a{};
+  if (q) rows_arg(&a, 0, q);
+  rows_arg(&a, 1, k);
+  rows_arg(&a, 2, v);
+  a.q_out = q_out;
+  a.k_cache = kv->k;
+  a.v_cache = kv->v;
+  a.pos = depth;
+  a.base = kv->prefix_len;
+  a.n_rows = n_rows;
+  a.table = kv->page_table;
+  a.freq = rope ? rope->freq : nullptr;
+  a.amplitude = rope ? rope->amplitude : 1.f;
+  a.B = B, a.Hq = q ? Hq : 0, a.Hkv = Hkv, a.N = N, a.D = D;
+  a.rot = rope ? rope->rot_dim : 0, a.interleaved = rope && rope->interleaved != 0;
+  a.num_pages = kv->num_pages, a.page_shift = log2_exact(kv->page_size), a.max_pages = kv->max_pages;
+  a.dev_status = dev_status;
+  return cuda_status(launch_rotary(a, dtype, st(stream)));
+}
+
+static bool paged_attn_shape(int B, int Hq, int Hkv, int N, int D) {
+  return B >= 1 && Hq >= 1 && Hkv >= 1 && Hq % Hkv == 0 && N >= 1 && N <= kMaxChunk && D >= 32 && D <= 256 &&
+         D % 32 == 0 && (long long)(Hq / Hkv) * N < (1 << 24);
+}
+
+size_t tv_paged_attention_workspace_size(int B, int Hq, int Hkv, int D, int N, int page_size, int max_pages,
+                                         tv_dtype dtype) {
+  if (!paged_attn_shape(B, Hq, Hkv, N, D) || page_size < 8 || max_pages < 1 || !valid_dtype(dtype)) return 0;
+  return paged_attn_ws(B, Hq, Hkv, D, N, dtype);
+}
+
+tv_status tv_paged_attention(const void* q, void* out, const tv_paged_kv* kv, const int32_t* parent,
+                             const int32_t* n_rows, int B, int Hq, int Hkv, int N, int D, float scale, float softcap,
+                             int window, tv_dtype dtype, void* workspace, size_t ws_bytes, int32_t* dev_status,
+                             tv_stream_t stream) {
+  NvtxRange nvtx_range("tv_paged_attention");
+  if (!q || !out) return TV_ERR_NULL;
+  const tv_status s = paged_checks(kv, B, Hkv, N, D, dtype);
+  if (s != TV_OK) return s;
+  if (!paged_attn_shape(B, Hq, Hkv, N, D) || (parent && N > kMaxNodes)) return TV_ERR_SHAPE;
+  if (!(scale >= 0.f) || isinf(scale) || !(softcap >= 0.f) || isinf(softcap) || window < 0) return TV_ERR_VALUE;
+  if (!aligned16(q) || !aligned16(out)) return TV_ERR_ALIGN;
+  if (!workspace || ws_bytes < paged_attn_ws(B, Hq, Hkv, D, N, dtype)) return TV_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return TV_ERR_ALIGN;
+  PagedAttn a{};
+  a.q = q, a.out = out, a.k = kv->k, a.v = kv->v;
+  a.table = kv->page_table, a.prefix_len = kv->prefix_len, a.parent = parent, a.n_rows = n_rows;
+  a.B = B, a.Hq = Hq, a.Hkv = Hkv, a.G = Hq / Hkv, a.D = D, a.N = N;
+  a.num_pages = kv->num_pages, a.page_shift = log2_exact(kv->page_size), a.max_pages = kv->max_pages;
+  a.scale = scale == 0.f ? 1.f / sqrtf((float)D) : scale;
+  a.cap = softcap;
+  a.window = window;
+  a.dev_status = dev_status;
+  return cuda_status(launch_paged_attn(a, dtype, reinterpret_cast<char*>(workspace), st(stream)));
+}
+
+tv_status tv_commit_accepted_kv_paged(const tv_paged_kv* kv, const int32_t* accepted_nodes, const int32_t* accept_len,
+                                      int32_t* new_len, int B, int Hkv, int N, int D, tv_dtype dtype,
+                                      int32_t* dev_status, tv_stream_t stream) {
+  NvtxRange nvtx_range("tv_commit_accepted_kv_paged");
+  if (!accepted_nodes || !accept_len) return TV_ERR_NULL;
+  const tv_status s = paged_checks(kv, B, Hkv, N, D, dtype);
+  if (s != TV_OK) return s;
+  if (N > kMaxNodes || B > 65535) return TV_ERR_SHAPE;
+  if (new_len == kv->prefix_len) return TV_ERR_VALUE;
+  return cuda_status(launch_kv_commit_paged(kv->k, kv->v, kv->page_table, kv->prefix_len, accepted_nodes, accept_len,
+                                            new_len, B, Hkv, D, N, kv->num_pages, log2_exact(kv->page_size),
+                                            kv->max_pages, dtype, dev_status, st(stream)));
+}
+
 }  // extern "C"

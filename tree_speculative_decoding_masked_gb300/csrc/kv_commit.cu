@@ -6,7 +6,7 @@
 // Since a_k >= k, copying in increasing k never reads a row that an earlier copy of the
 // same column wrote; each thread owns one 16-byte column chunk of one (b, kv head, K or V)
 // plane, loads all its sources first and then stores, so there is no cross-thread hazard.
-#include "tv_kernels.cuh"
+#include "paged.cuh"
 
 namespace tv {
 
@@ -73,6 +73,82 @@ cudaError_t launch_kv_commit(void* k_cache, void* v_cache, const int32_t* accept
                                                          accept_len, B, Hkv, P, N, row_bytes, (long long)S * row_bytes,
                                                          chunks, dev_status);
   return cudaGetLastError();
+}
+
+// The same over a paged cache, with each sequence's own prefix length.  One CTA per (sequence,
+// KV head, K or V); its threads take (row, 16-byte chunk) pairs, kPagedBatch rows at a time:
+// all of a batch's sources are in registers before any is stored, and since a_k >= k and
+// the a_k increase, no later batch reads a row that an earlier one wrote.
+constexpr int kPagedBatch = 4;  // pairs a thread holds
+
+__global__ void __launch_bounds__(kCommitThreads)
+    kv_commit_paged_kernel(unsigned char* k_cache, unsigned char* v_cache, const int32_t* table,
+                           const int32_t* prefix_len, const int32_t* accepted, const int32_t* accept_len,
+                           int32_t* new_len, int Hkv, int N, int num_pages, int page_shift, int max_pages, int chunks,
+                           int32_t* dev_status) {
+  const int b = blockIdx.y;
+  const int h = blockIdx.x >> 1;
+  unsigned char* cache = (blockIdx.x & 1) ? v_cache : k_cache;
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int len = accept_len[b], P = prefix_len[b];
+  const int32_t* acc = accepted + (size_t)b * N;
+  const int32_t* tab = table + (size_t)b * max_pages;
+  if (len < 0 || len >= N || P < 0) {
+    if (threadIdx.x == 0) set_dev_status(dev_status, P < 0 ? TV_DEV_BAD_PAGE : TV_DEV_BAD_TREE);
+    return;
+  }
+  if (new_len && blockIdx.x == 0 && threadIdx.x == 0) new_len[b] = P + len + 1;
+  const long long row_bytes = (long long)chunks * 16;
+  auto place = [&](long long r) -> unsigned char* {  // row r's address, or NULL
+    const long long pg = r >> page_shift;
+    const int page = pg < max_pages ? tab[pg] : -1;
+    if (page < 0 || page >= num_pages) {
+      set_dev_status(dev_status, TV_DEV_BAD_PAGE);
+      return nullptr;
+    }
+    return cache + ((((long long)page * Hkv + h) << page_shift) + (r & ((1 << page_shift) - 1))) * row_bytes;
+  };
+  const int items = len * chunks;
+  for (int e0 = 0; e0 < items; e0 += kCommitThreads * kPagedBatch) {
+    uint4 val[kPagedBatch];
+    unsigned char* dst[kPagedBatch];
+#pragma unroll
+    for (int u = 0; u < kPagedBatch; ++u) {
+      const int e = e0 + u * kCommitThreads + threadIdx.x;
+      dst[u] = nullptr;
+      if (e < items) {
+        const int k = e / chunks + 1, ch = e - (k - 1) * chunks;
+        const int at = acc[k - 1], prev = k > 1 ? acc[k - 2] : 0;
+        if (at <= prev || at < k || at >= N) {  // a root path has increasing node ids
+          set_dev_status(dev_status, TV_DEV_BAD_TREE);
+        } else if (at != k) {
+          const unsigned char* src = place((long long)P + at);
+          unsigned char* to = place((long long)P + k);
+          if (src && to) {
+            val[u] = *reinterpret_cast<const uint4*>(src + ch * 16);
+            dst[u] = to + ch * 16;
+          }
+        }
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kPagedBatch; ++u)
+      if (dst[u]) *reinterpret_cast<uint4*>(dst[u]) = val[u];
+    __syncthreads();
+  }
+}
+
+cudaError_t launch_kv_commit_paged(void* k, void* v, const int32_t* table, const int32_t* prefix_len,
+                                   const int32_t* accepted, const int32_t* accept_len, int32_t* new_len, int B,
+                                   int Hkv, int D, int N, int num_pages, int page_shift, int max_pages,
+                                   tv_dtype dtype, int32_t* dev_status, cudaStream_t stream) {
+  const int chunks = (int)((long long)D * (dtype == TV_BF16 ? 2 : 4) / 16);
+  return launch_pdl(kv_commit_paged_kernel, dim3((unsigned)(2 * Hkv), (unsigned)B), dim3(kCommitThreads), 0, stream,
+                    nullptr, 0, reinterpret_cast<unsigned char*>(k), reinterpret_cast<unsigned char*>(v), table,
+                    prefix_len, accepted, accept_len, new_len, Hkv, N, num_pages, page_shift, max_pages, chunks,
+                    dev_status);
 }
 
 }  // namespace tv

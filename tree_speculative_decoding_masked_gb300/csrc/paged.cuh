@@ -1,0 +1,113 @@
+// Paged KV caches: page lookup, visibility of keys, and the division of attention work over
+// CTAs that the paged attention kernels share.
+//
+// A cache holds pages [num_pages][Hkv][page_size][D]; cache row r of sequence b is row
+// r mod page_size of page page_table[b][r / page_size].  Sequence b's committed rows are
+// 0..P_b-1 (P_b = prefix_len[b]) and its new rows P_b..P_b+n_b-1.
+#pragma once
+
+#include "tv_kernels.cuh"
+#include "tv_ptx.cuh"
+
+namespace tv {
+
+// New rows of sequence b that the call looks at: n_rows[b] clamped to 0..N (N without
+// n_rows), or 0 for a sequence whose rows do not fit its page table (*bad).
+__device__ __forceinline__ int paged_rows(const PagedAttn& a, int b, int P, bool* bad) {
+  int n = a.n_rows ? a.n_rows[b] : a.N;
+  const bool fits = P >= 0 && n >= 0 && n <= a.N && (long long)P + n <= (long long)a.max_pages << a.page_shift;
+  *bad = !fits;
+  return fits ? n : 0;
+}
+
+// One CTA's share of the attention work.  The work is cut into units (sequence b, KV head,
+// tile of RT query rows) of 'key tiles' (KT keys); the units' tiles laid end to end are
+// divided into equal contiguous ranges, one per CTA, so that ragged lengths known only
+// on the device load every SM alike.  Query row r of a KV head is head r % G of node
+// r / G, so that a row tile spans few nodes and its key range ends at its last one.
+struct PagedSpan {
+  long long W;      // key tiles in all
+  long long per;    // tiles per CTA
+  int b;            // where this CTA starts: sequence,
+  long long base;   // and that sequence's first tile
+};
+
+__device__ __forceinline__ int unit_rows(const PagedAttn& a, int n, int rt, int RT) {
+  return max(0, min(RT, n * a.G - rt * RT));
+}
+// first key that some row of row tile rt can see (trees: any node may sit at depth 0..)
+__device__ __forceinline__ int unit_lo(const PagedAttn& a, int P, int rt, int RT) {
+  if (a.window <= 0) return 0;
+  const int i = a.parent ? 0 : rt * RT / a.G;
+  return max(0, P + i - a.window + 1);
+}
+__device__ __forceinline__ int unit_tiles(const PagedAttn& a, int P, int n, int rt, int RT, int KT) {
+  const int rows = unit_rows(a, n, rt, RT);
+  if (rows == 0) return 0;
+  const int hi = P + (rt * RT + rows - 1) / a.G + 1;
+  return (hi + KT - 1) / KT - unit_lo(a, P, rt, RT) / KT;
+}
+// tiles of one KV head of sequence b
+__device__ inline long long seq_tiles(const PagedAttn& a, int b, int RT, int KT, bool* bad) {
+  const int P = a.prefix_len[b];
+  const int n = paged_rows(a, b, P, bad);
+  long long s = 0;
+  for (int rt = 0; rt * RT < n * a.G; ++rt) s += unit_tiles(a, P, n, rt, RT, KT);
+  return s;
+}
+
+// Every thread of the CTA calls it; red holds 34 entries.  per is at least min_per.
+__device__ inline PagedSpan paged_span(const PagedAttn& a, int RT, int KT, int min_per, unsigned long long* red) {
+  PagedSpan sp;
+  unsigned long long W = 0;
+  bool any_bad = false;
+  unsigned long long mine = 0;
+  for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {
+    const int b = b0 + threadIdx.x;
+    bool bad = false;
+    mine = b < a.B ? (unsigned long long)seq_tiles(a, b, RT, KT, &bad) * a.Hkv : 0ull;
+    any_bad |= bad;
+    unsigned long long part = 0;
+    block_scan_u64(mine, red, &part);
+    W += part;
+  }
+  if (any_bad && blockIdx.x == 0) set_dev_status(a.dev_status, TV_DEV_BAD_PAGE);
+  sp.W = (long long)W;
+  sp.per = max((long long)min_per, (sp.W + gridDim.x - 1) / gridDim.x);
+  const unsigned long long begin = (unsigned long long)sp.per * blockIdx.x;
+  sp.b = a.B;
+  sp.base = sp.W;
+  if (begin >= W) return sp;  // the same for the whole CTA
+  unsigned long long cum = 0;
+  for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {
+    const int b = b0 + threadIdx.x;
+    bool bad = false;
+    if (a.B > (int)blockDim.x) mine = b < a.B ? (unsigned long long)seq_tiles(a, b, RT, KT, &bad) * a.Hkv : 0ull;
+    unsigned long long part = 0;
+    const unsigned long long at = cum + block_scan_u64(mine, red, &part);
+    if (begin >= at && begin < at + mine) {
+      red[0] = (unsigned long long)b;
+      red[1] = at;
+    }
+    const bool here = begin < cum + part;
+    __syncthreads();
+    if (here) {
+      sp.b = (int)red[0];
+      sp.base = (long long)red[1];
+      __syncthreads();
+      break;
+    }
+    cum += part;
+  }
+  return sp;
+}
+
+// The ranges that share the unit of tiles [u0, u1): CTAs u0 / per .. (u1 - 1) / per.  A CTA
+// parks the partial result of a unit it began inside in slot 2c and of one it leaves
+// unfinished in slot 2c + 1; the unit's counter is that of its first CTA (a CTA is the
+// first of one cut unit at most).
+__device__ __forceinline__ int unit_slot(long long c, long long per, long long u0) {
+  return (int)(2 * c + (u0 < c * per ? 0 : 1));
+}
+
+}  // namespace tv

@@ -1,0 +1,387 @@
+// Attention of new rows (a causal chunk or a draft tree) over a paged KV cache, on CUDA
+// cores.
+//
+//   out[b,h,i,:] = sum_j softmax_j(z_ij) v_j,  z = scale q_i . k_j, or cap tanh(scale q_i . k_j / cap)
+//
+// over the keys j that row i sees: the committed rows 0..P_b-1 and, of the new rows, 0..i
+// (causal) or i and its ancestors (tree), less those `window` or more positions back.
+//
+// One CTA takes RT = 8 kRPW query rows of a KV head (row r is head r % G of node r / G) and
+// walks its range of 32-key tiles, which cp.async brings into a double buffer.  A warp
+// owns kRPW rows: lane j scores key j against each (K rows padded by 16 bytes, so the 8
+// lanes of a 128-bit phase hit different banks), the warp keeps the running maximum and sum
+// of each row in 32 bits, and P goes through shared memory so that four keys' weights
+// come in one broadcast load.  The units' tiles are divided equally over the CTAs
+// (paged.cuh); the CTA that finishes a cut unit last merges its parts in CTA order, so
+// results do not depend on which one that is.
+#include "paged.cuh"
+
+namespace tv {
+
+constexpr int kPsWarps = 8;
+constexpr int kPsKeys = 32;
+
+template <typename T>
+struct PsIo;
+template <>
+struct PsIo<float> {
+  static constexpr int kVec = 4;
+  static __device__ __forceinline__ void load(const float* p, float (&f)[4]) {
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+  }
+  static __device__ __forceinline__ float one(const float* p) { return *p; }
+  static __device__ __forceinline__ void put(float* p, float v) { *p = v; }
+};
+template <>
+struct PsIo<uint16_t> {
+  static constexpr int kVec = 8;
+  static __device__ __forceinline__ void load(const uint16_t* p, float (&f)[8]) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ float one(const uint16_t* p) { return bf16_to_f32(*p); }
+  static __device__ __forceinline__ void put(uint16_t* p, float v) { *p = f32_to_bf16_rn(v); }
+};
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_addr(dst)), "l"(src) : "memory");
+}
+
+template <typename T, int kDPL, int kRPW>
+struct PsSmem {
+  static constexpr int kD = kDPL * 32;
+  static constexpr int kRT = kPsWarps * kRPW;
+  static constexpr int kStride = kD + 16 / (int)sizeof(T);  // K row in smem, elements
+  static constexpr int kOffV = 2 * kPsKeys * kStride * (int)sizeof(T);
+  static constexpr int kOffQ = kOffV + 2 * kPsKeys * kD * (int)sizeof(T);
+  static constexpr int kOffP = kOffQ + kRT * kD * 4;
+  static constexpr int kOffVis = kOffP + kRT * kPsKeys * 4;
+  static constexpr int kOffPar = kOffVis + kRT * (kMaxNodes / 32) * 4;
+  static constexpr int kBytes = kOffPar + kMaxNodes * 4;
+};
+
+template <typename T, int kDPL, int kRPW>
+__global__ void __launch_bounds__(kPsWarps * 32) paged_simt_kernel(PagedAttn a) {
+  using S = PsSmem<T, kDPL, kRPW>;
+  using Io = PsIo<T>;
+  constexpr int kD = S::kD, kRT = S::kRT, kVec = Io::kVec;
+  extern __shared__ __align__(16) unsigned char ps_smem[];
+  T* s_k = reinterpret_cast<T*>(ps_smem);
+  T* s_v = reinterpret_cast<T*>(ps_smem + S::kOffV);
+  float* s_q = reinterpret_cast<float*>(ps_smem + S::kOffQ);
+  float* s_p = reinterpret_cast<float*>(ps_smem + S::kOffP);
+  uint32_t(*s_vis)[kMaxNodes / 32] = reinterpret_cast<uint32_t(*)[kMaxNodes / 32]>(ps_smem + S::kOffVis);
+  int* s_par = reinterpret_cast<int*>(ps_smem + S::kOffPar);
+  __shared__ unsigned long long s_red[34];
+  __shared__ int s_first_pad, s_last, s_depth[kRT];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const T* q = reinterpret_cast<const T*>(a.q);
+  T* out = reinterpret_cast<T*>(a.out);
+
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const PagedSpan sp = paged_span(a, kRT, kPsKeys, 1, s_red);
+  const long long c = blockIdx.x, end = min(sp.W, (c + 1) * sp.per);
+  long long pos = c * sp.per, base = sp.base;
+  for (int b = sp.b; b < a.B && pos < end; ++b) {
+    const int P = a.prefix_len[b];
+    bool bad = false;
+    const int n = paged_rows(a, b, P, &bad);
+    const int32_t* table = a.table + (size_t)b * a.max_pages;
+    int n_act = n;
+    if (a.parent && n > 0) {
+      // the tree, checked; its rows past the first padding row are inactive
+      __syncthreads();
+      if (threadIdx.x == 0) s_first_pad = n;
+      __syncthreads();
+      int wrong = 0;
+      for (int t = threadIdx.x; t < n; t += blockDim.x) {
+        const int p = a.parent[(size_t)b * a.N + t];
+        const bool prev_pad = t >= 2 && a.parent[(size_t)b * a.N + t - 1] == -1;
+        const bool ok = t == 0 ? p == -1 : (p == -1 || (p >= 0 && p < t && !prev_pad));
+        if (!ok) wrong = 1;
+        s_par[t] = ok ? p : -1;
+        if (t > 0 && p == -1) atomicMin(&s_first_pad, t);
+      }
+      if (wrong) set_dev_status(a.dev_status, TV_DEV_BAD_TREE);
+      __syncthreads();
+      n_act = s_first_pad;
+    }
+    for (int hk = 0; hk < a.Hkv && pos < end; ++hk) {
+      for (int rt = 0; rt * kRT < n * a.G && pos < end; ++rt) {
+        const int T_u = unit_tiles(a, P, n, rt, kRT, kPsKeys);
+        const long long u0 = base;
+        base += T_u;
+        if (pos >= base) continue;
+        const int t0 = (int)(pos - u0), t1 = (int)(min(base, end) - u0);
+        pos = u0 + t1;
+        const int rows = unit_rows(a, n, rt, kRT);
+        const int lo = unit_lo(a, P, rt, kRT), tile0 = lo / kPsKeys;
+        const int hi = min(P + n_act, P + (rt * kRT + rows - 1) / a.G + 1);
+        // ---- rows: query, depth and the tree nodes each sees
+        __syncthreads();
+        for (int rr = warp; rr < kRT; rr += kPsWarps) {
+          const int r = rt * kRT + rr, i = r / a.G, g = r % a.G;
+          const bool live = rr < rows && i < n_act;
+          const size_t qoff = (((size_t)b * a.Hq + hk * a.G + g) * a.N + i) * kD;
+          for (int d = lane; d < kD; d += 32) s_q[rr * kD + d] = live ? Io::one(q + qoff + d) * a.scale : 0.f;
+          if (!a.parent) {
+            if (lane == 0) s_depth[rr] = i;
+            continue;
+          }
+          for (int w = lane; w < kMaxNodes / 32; w += 32) s_vis[rr][w] = 0u;
+          __syncwarp();
+          if (lane == 0) {
+            int depth = 0;
+            for (int at = live ? i : -1; at >= 0; at = s_par[at], ++depth)  // parents fall: ends within n steps
+              if (a.window <= 0 || depth < a.window) s_vis[rr][at >> 5] |= 1u << (at & 31);
+            s_depth[rr] = max(0, depth - 1);
+          }
+        }
+        float m[kRPW], l[kRPW], acc[kRPW][kDPL];
+#pragma unroll
+        for (int rw = 0; rw < kRPW; ++rw) {
+          m[rw] = -INFINITY;
+          l[rw] = 0.f;
+#pragma unroll
+          for (int t = 0; t < kDPL; ++t) acc[rw][t] = 0.f;
+        }
+        // rows [lo, hi) of the tile; others (pages past the end, rows behind the window, whose
+        // contents may be anything) read as zero
+        auto load_tile = [&](int t, int buf) {
+          constexpr int kChunks = kD / kVec;
+          for (int e = threadIdx.x; e < kPsKeys * kChunks; e += blockDim.x) {
+            const int jj = e / kChunks, ch = e - jj * kChunks;
+            const int j = (tile0 + t) * kPsKeys + jj;
+            T* dk = s_k + (buf * kPsKeys + jj) * S::kStride + ch * kVec;
+            T* dv = s_v + (buf * kPsKeys + jj) * kD + ch * kVec;
+            int page = -1;
+            if (j >= lo && j < hi) {
+              page = table[j >> a.page_shift];
+              if (page < 0 || page >= a.num_pages) {
+                set_dev_status(a.dev_status, TV_DEV_BAD_PAGE);
+                page = -1;
+              }
+            }
+            if (page >= 0) {
+              const size_t off =
+                  ((((size_t)page * a.Hkv + hk) << a.page_shift) + (j & ((1 << a.page_shift) - 1))) * kD + ch * kVec;
+              cp_async16(dk, reinterpret_cast<const T*>(a.k) + off);
+              cp_async16(dv, reinterpret_cast<const T*>(a.v) + off);
+            } else {
+              *reinterpret_cast<uint4*>(dk) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(dv) = make_uint4(0, 0, 0, 0);
+            }
+          }
+          asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        load_tile(t0, 0);
+        for (int t = t0; t < t1; ++t) {
+          const int buf = (t - t0) & 1;
+          if (t + 1 < t1) {
+            load_tile(t + 1, buf ^ 1);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+          } else {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+          }
+          __syncthreads();
+          const int j = (tile0 + t) * kPsKeys + lane;
+          float dot[kRPW];
+#pragma unroll
+          for (int rw = 0; rw < kRPW; ++rw) dot[rw] = 0.f;
+          const T* kr = s_k + (buf * kPsKeys + lane) * S::kStride;
+#pragma unroll 4
+          for (int d = 0; d < kD; d += kVec) {
+            float kf[kVec];
+            Io::load(kr + d, kf);
+#pragma unroll
+            for (int rw = 0; rw < kRPW; ++rw) {
+              const float* qr = s_q + (warp * kRPW + rw) * kD + d;
+#pragma unroll
+              for (int u = 0; u < kVec; u += 4) {
+                const float4 qf = *reinterpret_cast<const float4*>(qr + u);
+                dot[rw] = fmaf(qf.x, kf[u], dot[rw]);
+                dot[rw] = fmaf(qf.y, kf[u + 1], dot[rw]);
+                dot[rw] = fmaf(qf.z, kf[u + 2], dot[rw]);
+                dot[rw] = fmaf(qf.w, kf[u + 3], dot[rw]);
+              }
+            }
+          }
+#pragma unroll
+          for (int rw = 0; rw < kRPW; ++rw) {
+            const int rr = warp * kRPW + rw, i = (rt * kRT + rr) / a.G;
+            bool vis = rr < rows && i < n_act && j < hi;
+            if (j < P) {
+              vis = vis && (a.window <= 0 || P - j + s_depth[rr] < a.window);
+            } else if (vis) {
+              const int t_new = j - P;
+              vis = a.parent ? (s_vis[rr][t_new >> 5] >> (t_new & 31)) & 1u
+                             : t_new <= i && (a.window <= 0 || i - t_new < a.window);
+            }
+            float z = dot[rw];
+            // expf of a difference, not 2^(z log2 e - m): the product's rounding would cost |z| 2^-24
+            if (a.cap > 0.f) z = a.cap * tanhf(z / a.cap);
+            z = vis ? z : -INFINITY;
+            const float mt = warp_max(z);
+            float p = 0.f;
+            if (mt != -INFINITY) {
+              const float mnew = fmaxf(m[rw], mt);
+              const float corr = expf(m[rw] - mnew);
+              p = expf(z - mnew);
+              l[rw] = l[rw] * corr + warp_sum(p);
+#pragma unroll
+              for (int u = 0; u < kDPL; ++u) acc[rw][u] *= corr;
+              m[rw] = mnew;
+            }
+            s_p[rr * kPsKeys + lane] = p;
+          }
+          __syncwarp();
+#pragma unroll 2
+          for (int jj = 0; jj < kPsKeys; jj += 4) {
+            float4 pf[kRPW];
+#pragma unroll
+            for (int rw = 0; rw < kRPW; ++rw)
+              pf[rw] = *reinterpret_cast<const float4*>(s_p + (warp * kRPW + rw) * kPsKeys + jj);
+#pragma unroll
+            for (int u = 0; u < kDPL; ++u) {
+              const T* vr = s_v + (buf * kPsKeys + jj) * kD + lane + 32 * u;
+              const float v0 = Io::one(vr), v1 = Io::one(vr + kD), v2 = Io::one(vr + 2 * kD), v3 = Io::one(vr + 3 * kD);
+#pragma unroll
+              for (int rw = 0; rw < kRPW; ++rw)
+                acc[rw][u] = fmaf(pf[rw].w, v3, fmaf(pf[rw].z, v2, fmaf(pf[rw].y, v1, fmaf(pf[rw].x, v0, acc[rw][u]))));
+            }
+          }
+          __syncthreads();
+        }
+        // ---- write the unit, or this CTA's part of it
+        const long long c0 = u0 / sp.per, c1 = (base - 1) / sp.per;
+        const int slot = unit_slot(c, sp.per, u0);
+#pragma unroll
+        for (int rw = 0; rw < kRPW; ++rw) {
+          const int rr = warp * kRPW + rw, r = rt * kRT + rr, i = r / a.G, g = r % a.G;
+          if (c0 == c1) {
+            if (rr >= rows || i >= n_act) continue;
+            const size_t off = (((size_t)b * a.Hq + hk * a.G + g) * a.N + i) * kD;
+            const float inv = 1.f / l[rw];
+#pragma unroll
+            for (int u = 0; u < kDPL; ++u) Io::put(out + off + lane + 32 * u, acc[rw][u] * inv);
+          } else {
+            const size_t row = (size_t)slot * kRT + rr;
+            if (lane == 0) a.ws_ml[row] = make_float2(m[rw], l[rw]);
+#pragma unroll
+            for (int u = 0; u < kDPL; ++u) a.ws_o[row * kD + lane + 32 * u] = acc[rw][u];
+          }
+        }
+        if (c0 == c1) continue;
+        __threadfence();
+        __syncthreads();
+        if (threadIdx.x == 0) {
+          s_last = ptx::atom_add_acq_rel_gpu(&a.cnt[c0], 1u) == (unsigned)(c1 - c0);
+          if (s_last) a.cnt[c0] = 0u;
+          __threadfence();
+        }
+        __syncthreads();
+        if (!s_last) continue;
+        for (int rr = warp; rr < rows; rr += kPsWarps) {
+          const int r = rt * kRT + rr, i = r / a.G, g = r % a.G;
+          if (i >= n_act) continue;
+          float M = -INFINITY;
+          for (long long cc = c0; cc <= c1; ++cc)
+            M = fmaxf(M, __ldcg(&a.ws_ml[(size_t)unit_slot(cc, sp.per, u0) * kRT + rr]).x);
+          float L = 0.f, o[kDPL];
+#pragma unroll
+          for (int u = 0; u < kDPL; ++u) o[u] = 0.f;
+          for (long long cc = c0; cc <= c1; ++cc) {
+            const size_t row = (size_t)unit_slot(cc, sp.per, u0) * kRT + rr;
+            const float2 ml = __ldcg(&a.ws_ml[row]);
+            const float w = ml.x == -INFINITY ? 0.f : expf(ml.x - M);
+            L = fmaf(w, ml.y, L);
+#pragma unroll
+            for (int u = 0; u < kDPL; ++u) o[u] = fmaf(w, __ldcg(&a.ws_o[row * kD + lane + 32 * u]), o[u]);
+          }
+          const size_t off = (((size_t)b * a.Hq + hk * a.G + g) * a.N + i) * kD;
+#pragma unroll
+          for (int u = 0; u < kDPL; ++u) Io::put(out + off + lane + 32 * u, o[u] / L);
+        }
+      }
+    }
+    // sequences wholly before this CTA's range do not occur: base is the range's sequence
+  }
+}
+
+// ---- host side
+
+static int paged_sms() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+      n <= 0)
+    n = 152;
+  return n;
+}
+
+constexpr int kPsMaxCtas = 2;   // CTAs per SM of the largest grid
+constexpr int kPsMaxSms = 160;  // sizes the workspace
+
+// counters, (m, l) and O of two partial units per CTA of the largest grid
+static size_t ps_cnt_bytes() { return (size_t)kPsMaxCtas * kPsMaxSms * 4; }
+
+size_t paged_attn_ws(int, int, int, int D, int, tv_dtype) {
+  const size_t rows = (size_t)2 * kPsMaxCtas * kPsMaxSms * kPsWarps * 4;
+  return ps_cnt_bytes() + rows * 8 + rows * D * 4;
+}
+
+template <typename T, int kDPL, int kRPW>
+static cudaError_t launch_ps(PagedAttn a, char* ws, cudaStream_t stream) {
+  using S = PsSmem<T, kDPL, kRPW>;
+  cudaError_t e = cudaFuncSetAttribute(paged_simt_kernel<T, kDPL, kRPW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       S::kBytes);
+  if (e != cudaSuccess) return e;
+  const size_t rows = (size_t)2 * kPsMaxCtas * kPsMaxSms * kPsWarps * 4;
+  a.cnt = reinterpret_cast<unsigned*>(ws);
+  a.ws_ml = reinterpret_cast<float2*>(ws + ps_cnt_bytes());
+  a.ws_o = reinterpret_cast<float*>(ws + ps_cnt_bytes() + rows * 8);
+  const int share = sm_share_attention();
+  int sms = min(paged_sms(), kPsMaxSms);
+  if (share > 0 && share < sms) sms = share;
+  return launch_pdl(paged_simt_kernel<T, kDPL, kRPW>, dim3((unsigned)(sms * kPsMaxCtas)), dim3(kPsWarps * 32), S::kBytes, stream,
+                    nullptr, 0, a);
+}
+
+template <typename T, int kRPW>
+static cudaError_t launch_ps_d(const PagedAttn& a, char* ws, cudaStream_t stream) {
+  switch (a.D / 32) {
+    case 1:
+      return launch_ps<T, 1, kRPW>(a, ws, stream);
+    case 2:
+      return launch_ps<T, 2, kRPW>(a, ws, stream);
+    case 3:
+      return launch_ps<T, 3, kRPW>(a, ws, stream);
+    case 4:
+      return launch_ps<T, 4, kRPW>(a, ws, stream);
+    case 5:
+      return launch_ps<T, 5, kRPW>(a, ws, stream);
+    case 6:
+      return launch_ps<T, 6, kRPW>(a, ws, stream);
+    case 7:
+      return launch_ps<T, 7, kRPW>(a, ws, stream);
+    case 8:
+      return launch_ps<T, 8, kRPW>(a, ws, stream);
+    default:
+      return cudaErrorInvalidValue;
+  }
+}
+
+cudaError_t launch_paged_attn(PagedAttn a, tv_dtype dtype, char* ws, cudaStream_t stream) {
+  const bool few = (long long)a.G * a.N <= kPsWarps;
+  if (dtype == TV_BF16)
+    return few ? launch_ps_d<uint16_t, 1>(a, ws, stream) : launch_ps_d<uint16_t, 4>(a, ws, stream);
+  return few ? launch_ps_d<float, 1>(a, ws, stream) : launch_ps_d<float, 4>(a, ws, stream);
+}
+
+}  // namespace tv

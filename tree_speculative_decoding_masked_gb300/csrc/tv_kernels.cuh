@@ -9,6 +9,10 @@ constexpr int kMaxNodes = 1024;  // N limit (tree nodes per sequence, root inclu
 constexpr int kMaxDepth = 16;    // selection pool depth d
 constexpr int kMaxRank = 256;    // selection pool width K
 constexpr int kMaxBudget = 4096; // selection budget (rows)
+constexpr int kMaxChunk = 65536; // new rows of a paged causal chunk
+constexpr int kMaxRotaryDim = 1024;
+constexpr int kMaxRotaryHeads = 16384;                 // one grid dimension
+constexpr long long kMaxRotaryRows = 0x7fffffffLL / 2; // B * N of the rotary and append calls
 
 // ---- verify (vocab pass + walks)
 struct VerifyWs {
@@ -91,5 +95,51 @@ void attn_tc_choice(int B, int Hkv, int D, int P, int N, const AttnPlan& plan, i
 cudaError_t launch_attn_tc(const void* q, const void* k, const void* v, void* out, const int32_t* parent,
                            int B, int Hq, int Hkv, int D, int P, int N, int S, float scale, const AttnPlan& plan,
                            char* ws, size_t ws_bytes, int32_t* dev_status, cudaStream_t stream);
+
+// ---- paged caches
+struct PagedAttn {
+  const void* q;
+  void* out;
+  const void* k;
+  const void* v;
+  const int32_t* table;
+  const int32_t* prefix_len;
+  const int32_t* parent;  // NULL: causal
+  const int32_t* n_rows;  // NULL: N rows each
+  int B, Hq, Hkv, G, D, N, num_pages, page_shift, max_pages;
+  float scale, cap;  // cap 0: scores are not capped
+  int window;        // 0: no window
+  float* ws_o;       // partial results of units shared by CTAs
+  float2* ws_ml;
+  unsigned* cnt;
+  int32_t* dev_status;
+};
+size_t paged_attn_ws(int B, int Hq, int Hkv, int D, int N, tv_dtype dtype);
+cudaError_t launch_paged_attn(PagedAttn a, tv_dtype dtype, char* ws, cudaStream_t stream);
+
+// ---- rotary positions and the paged append (Hq rows of q rotated into q_out, Hkv rows of k
+// rotated and of v copied into pages; any part may be absent)
+struct RotaryArgs {
+  const void* src[3];  // q, k, v
+  long long sb[3], sh[3], sn[3];
+  void* q_out;
+  void* k_cache;
+  void* v_cache;
+  const int32_t* pos;   // [B][N] or NULL: 0..N-1
+  const int32_t* base;  // [B] added to pos, or NULL
+  const int32_t* n_rows;
+  const int32_t* table;
+  const uint64_t* freq;
+  float amplitude;
+  int B, Hq, Hkv, N, D, rot, interleaved;
+  int num_pages, page_shift, max_pages;
+  int32_t* dev_status;
+};
+cudaError_t launch_rotary(const RotaryArgs& a, tv_dtype dtype, cudaStream_t stream);
+void rotary_frequencies(int rot, double base, int scaling, const double* params, uint64_t* freq, float* amplitude);
+cudaError_t launch_kv_commit_paged(void* k, void* v, const int32_t* table, const int32_t* prefix_len,
+                                   const int32_t* accepted, const int32_t* accept_len, int32_t* new_len, int B,
+                                   int Hkv, int D, int N, int num_pages, int page_shift, int max_pages,
+                                   tv_dtype dtype, int32_t* dev_status, cudaStream_t stream);
 
 }  // namespace tv
