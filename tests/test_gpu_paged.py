@@ -160,6 +160,31 @@ def test_trees(shape, bf16):
     _attend_check(g, B, Hq, Hkv, D, ps, prefix, N, parent=par, bf16=bf16)
 
 
+# row tile pairs enough for the persistent schedule, whose CTAs' ranges cross sequences, heads and pairs
+PERSISTENT = [
+    (3, 32, 32, 64, 16, [700, 10, 300], 40),
+    (10, 32, 8, 128, 16, [0, 900, 5, 64, 63, 300, 1, 128, 17, 250], 20),
+    (2, 32, 8, 128, 32, [3, 200], 300),
+    (100, 3, 1, 96, 8, [(37 * b) % 90 for b in range(100)], 12),
+]
+
+
+@pytest.mark.parametrize("window", [0, 50])
+@pytest.mark.parametrize("tree_", [False, True])
+@pytest.mark.parametrize("shape", PERSISTENT)
+def test_persistent_schedule(shape, tree_, window):
+    B, Hq, Hkv, D, ps, prefix, N = shape
+    g = synth.rng(1170 + N + window)
+    par, rows = None, [max(0, N - 3 * b) for b in range(B)]
+    if tree_:
+        par, _ = W.trees(g, B, N, 6, 50)
+        rows = None
+        for b in range(1, B):
+            par[b, max(1, N - 2 * b):] = -1
+    _attend_check(g, B, Hq, Hkv, D, ps, prefix, N, parent=par, n_rows=rows, window=window,
+                  softcap=20.0 if window else 0.0)
+
+
 @pytest.mark.parametrize("bf16", [True, False])
 def test_deep_and_wide_trees(bf16):
     g = synth.rng(1150)
@@ -247,10 +272,10 @@ def test_one_workspace_many_shapes(bf16, N):
 
 
 @pytest.mark.parametrize("bf16", [True, False])
-@pytest.mark.parametrize("N,tree_", [(1, False), (40, True), (150, False)])
-def test_repeats_are_bit_equal_and_replay(bf16, N, tree_):
+@pytest.mark.parametrize("N,Hkv,tree_", [(1, 2, False), (40, 2, True), (150, 2, False), (50, 40, True)])
+def test_repeats_are_bit_equal_and_replay(bf16, N, Hkv, tree_):
     g = synth.rng(1800 + N)
-    B, Hq, Hkv, D, ps, prefix = 2, 8, 2, 128, 16, [700, 321]
+    B, Hq, D, ps, prefix = 2, 4 * Hkv, 128, 16, [700, 321]
     kc, vc, table = _pages(g, B, Hkv, D, ps, [p + N for p in prefix], 900, bf16)
     par = W.trees(g, B, N, 6, 50)[0] if tree_ else None
     q = to_dev(synth.normal(g, (B, Hq, N, D), 1.0, bf16), bf16)

@@ -461,7 +461,8 @@ tv_status tv_paged_attention(const void* q, void* out, const tv_paged_kv* kv, co
   if (!paged_attn_shape(B, Hq, Hkv, N, D) || (parent && N > kMaxNodes)) return TV_ERR_SHAPE;
   if (!(scale >= 0.f) || isinf(scale) || !(softcap >= 0.f) || isinf(softcap) || window < 0) return TV_ERR_VALUE;
   if (!aligned16(q) || !aligned16(out)) return TV_ERR_ALIGN;
-  if (!workspace || ws_bytes < paged_attn_ws(B, Hq, Hkv, D, N, dtype)) return TV_ERR_WORKSPACE;
+  const size_t need = paged_attn_ws(B, Hq, Hkv, D, N, dtype);
+  if (need && (!workspace || ws_bytes < need)) return TV_ERR_WORKSPACE;
   if (!aligned16(workspace)) return TV_ERR_ALIGN;
   PagedAttn a{};
   a.q = q, a.out = out, a.k = kv->k, a.v = kv->v;

@@ -110,4 +110,16 @@ __device__ __forceinline__ int unit_slot(long long c, long long per, long long u
   return (int)(2 * c + (u0 < c * per ? 0 : 1));
 }
 
+// ---- host side
+constexpr int kPagedMaxSms = 160;  // sizes the workspaces
+constexpr int kPagedMaxCtas = 2;   // CTAs per SM of the largest persistent grid
+constexpr size_t kPagedCntBytes = kPagedMaxCtas * kPagedMaxSms * 4;
+constexpr int kPagedFewRows = 32;  // query rows of a KV head above which row tiles are used (bf16)
+
+int paged_device_sms();
+int paged_grid_sms();  // less where tv_set_sm_partition says so
+bool paged_tc_takes(int Hq, int Hkv, int D, int N);
+size_t paged_tc_ws(int B, int Hq, int Hkv, int D, int N);
+cudaError_t launch_paged_tc(PagedAttn a, char* ws, cudaStream_t stream);
+
 }  // namespace tv

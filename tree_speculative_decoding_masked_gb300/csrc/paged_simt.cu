@@ -14,6 +14,8 @@
 // come in one broadcast load.  The units' tiles are divided equally over the CTAs
 // (paged.cuh); the CTA that finishes a cut unit last merges its parts in CTA order, so
 // results do not depend on which one that is.
+#include <atomic>
+
 #include "paged.cuh"
 
 namespace tv {
@@ -311,29 +313,34 @@ __global__ void __launch_bounds__(kPsWarps * 32) paged_simt_kernel(PagedAttn a) 
         }
       }
     }
-    // sequences wholly before this CTA's range do not occur: base is the range's sequence
   }
 }
 
 // ---- host side
 
-static int paged_sms() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-      n <= 0)
-    n = 152;
-  return n;
+int paged_device_sms() {
+  static std::atomic<int> known[64];  // 0 = not asked yet
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (!n) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 152;
+    known[dev].store(n, std::memory_order_relaxed);
+  }
+  return min(n, kPagedMaxSms);
 }
 
-constexpr int kPsMaxCtas = 2;   // CTAs per SM of the largest grid
-constexpr int kPsMaxSms = 160;  // sizes the workspace
+int paged_grid_sms() {
+  const int n = paged_device_sms(), share = sm_share_attention();
+  return share > 0 && share < n ? share : n;
+}
 
 // counters, (m, l) and O of two partial units per CTA of the largest grid
-static size_t ps_cnt_bytes() { return (size_t)kPsMaxCtas * kPsMaxSms * 4; }
+constexpr size_t kPsRows = (size_t)2 * kPagedMaxCtas * kPagedMaxSms * kPsWarps * 4;
 
-size_t paged_attn_ws(int, int, int, int D, int, tv_dtype) {
-  const size_t rows = (size_t)2 * kPsMaxCtas * kPsMaxSms * kPsWarps * 4;
-  return ps_cnt_bytes() + rows * 8 + rows * D * 4;
+size_t paged_attn_ws(int B, int Hq, int Hkv, int D, int N, tv_dtype dtype) {
+  if (dtype == TV_BF16 && paged_tc_takes(Hq, Hkv, D, N)) return paged_tc_ws(B, Hq, Hkv, D, N);
+  return kPagedCntBytes + kPsRows * 8 + kPsRows * D * 4;
 }
 
 template <typename T, int kDPL, int kRPW>
@@ -342,15 +349,11 @@ static cudaError_t launch_ps(PagedAttn a, char* ws, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(paged_simt_kernel<T, kDPL, kRPW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        S::kBytes);
   if (e != cudaSuccess) return e;
-  const size_t rows = (size_t)2 * kPsMaxCtas * kPsMaxSms * kPsWarps * 4;
   a.cnt = reinterpret_cast<unsigned*>(ws);
-  a.ws_ml = reinterpret_cast<float2*>(ws + ps_cnt_bytes());
-  a.ws_o = reinterpret_cast<float*>(ws + ps_cnt_bytes() + rows * 8);
-  const int share = sm_share_attention();
-  int sms = min(paged_sms(), kPsMaxSms);
-  if (share > 0 && share < sms) sms = share;
-  return launch_pdl(paged_simt_kernel<T, kDPL, kRPW>, dim3((unsigned)(sms * kPsMaxCtas)), dim3(kPsWarps * 32), S::kBytes, stream,
-                    nullptr, 0, a);
+  a.ws_ml = reinterpret_cast<float2*>(ws + kPagedCntBytes);
+  a.ws_o = reinterpret_cast<float*>(ws + kPagedCntBytes + kPsRows * 8);
+  return launch_pdl(paged_simt_kernel<T, kDPL, kRPW>, dim3((unsigned)(paged_grid_sms() * kPagedMaxCtas)),
+                    dim3(kPsWarps * 32), S::kBytes, stream, nullptr, 0, a);
 }
 
 template <typename T, int kRPW>
@@ -378,6 +381,7 @@ static cudaError_t launch_ps_d(const PagedAttn& a, char* ws, cudaStream_t stream
 }
 
 cudaError_t launch_paged_attn(PagedAttn a, tv_dtype dtype, char* ws, cudaStream_t stream) {
+  if (dtype == TV_BF16 && paged_tc_takes(a.Hq, a.Hkv, a.D, a.N)) return launch_paged_tc(a, ws, stream);
   const bool few = (long long)a.G * a.N <= kPsWarps;
   if (dtype == TV_BF16)
     return few ? launch_ps_d<uint16_t, 1>(a, ws, stream) : launch_ps_d<uint16_t, 4>(a, ws, stream);

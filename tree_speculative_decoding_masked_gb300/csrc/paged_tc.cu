@@ -1,0 +1,844 @@
+// Attention of new rows over a paged KV cache on the 5th-generation tensor cores (tcgen05,
+// TMEM, TMA), for chunks and trees whose rows fill row tiles.
+//
+//   S = Q K^T,  P = 2^(c S - m) over the visible keys,  O += P V,  out = O / sum P
+//
+// with the softmax's maximum and sum in 32 bits and P rounded to bf16 for the second product
+// (2^-8 of each weight, the tensor core's input type).  One CTA owns two 128-row tiles A and
+// B of one (sequence, KV head) - the G query heads of NT = 128 / G nodes each - and streams a
+// range of 64-key tiles once for both, so a page fetched from L2 serves 256 rows.
+//
+// Pages: the producer's lanes each fetch one box (64 columns x min(page_size, 64) rows) of a
+// tile from the page that their own table entry names, read one tile ahead; 64 keys of 16-row
+// pages are 8 boxes of 2 KB.  Boxes that hold no needed row are not fetched and their table
+// entries not looked at.  V rows outside the needed range (the tail of a sequence's last
+// page, rows behind the window) may hold anything, NaN included, which a zero weight would
+// not remove: the PV issuer's warp zeroes them in shared memory first.
+//
+// Warps: 0 producer (lanes 0-15 Q and K, 16-31 V), 1 S issuer of tile A and TMEM owner,
+// 2-9 softmax (four per tile, one row a thread), 10 PV issuer, 11 S issuer of tile B.
+// TMEM columns: S_A[0] 0.., S_A[1] 64.., S_B[0] 128.., S_B[1] 192.., O_A 256.., O_B 384...
+// P_X (bf16, 32 columns) overwrites the first half of its own S buffer.
+//
+// Two schedules.  Where the row tile pairs are fewer than half the SMs, each pair's keys are
+// cut into equal parts that run as one thread-block cluster and merge through distributed
+// shared memory.  Otherwise a persistent grid of one CTA per SM divides all pairs' 64-key
+// steps equally (paged.cuh), which keeps ragged batches and causal triangles balanced; a
+// pair cut between CTAs is merged through the workspace, in CTA order, by the CTA that
+// finishes last.
+#include <cuda.h>
+
+#include <atomic>
+
+#include "paged.cuh"
+
+namespace tv {
+
+constexpr int kPtRows = 128;
+constexpr int kPtKeys = 64;
+constexpr int kPtSlots = 4;      // K ring and V ring depth
+constexpr int kPtThreads = 384;  // 12 warps
+constexpr int kPtMaxSplits = 8;  // portable cluster size
+constexpr float kPtRescaleLog2 = 8.f;
+constexpr float kPtRescaleSum = 256.f;
+
+template <int D>
+struct PtCfg {
+  static constexpr int kDB = D / 64;
+  static constexpr int kQBlock = kPtRows * 128;      // bytes per 64-column block of one Q tile
+  static constexpr int kQTile = kDB * kQBlock;
+  static constexpr int kKVBlock = kPtKeys * 128;     // bytes per 64-column block of a K or V tile
+  static constexpr int kTileBytes = kDB * kKVBlock;
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffK = kOffQ + 2 * kQTile;
+  static constexpr int kOffV = kOffK + kPtSlots * kTileBytes;
+  static constexpr int kOffPar = kOffV + kPtSlots * kTileBytes;
+  static constexpr int kOffBar = kOffPar + kMaxNodes * 4;
+  static constexpr int kSmemAlloc = kOffBar + 512 + 1024;  // slack for 1024-byte alignment
+  static constexpr uint32_t kColO = 256;
+  static_assert(2 * kPtSlots * kTileBytes >= 2 * kPtRows * D * 4, "split partials fit in the drained rings");
+  static_assert(2 * kQTile >= 2 * kPtRows * 8, "(m, l) of both tiles fit in the drained Q tiles");
+  static_assert(kSmemAlloc <= 232448, "shared memory per CTA");
+};
+
+struct PtBars {
+  uint64_t q_full;
+  uint64_t k_full[kPtSlots];
+  uint64_t k_empty[kPtSlots];
+  uint64_t v_full[kPtSlots];
+  uint64_t v_empty[kPtSlots];
+  uint64_t s_full[2][2];
+  uint64_t p_full[2][2];
+  uint64_t pv_done[2][2];
+  uint64_t o_done;
+  uint64_t s_done[2];
+  uint32_t tmem_base;
+  int abort;
+};
+constexpr int kPtBarWords = 1 + 4 * kPtSlots + 12 + 3;
+
+struct PtArgs {
+  int NT;      // nodes per row tile
+  int MP;      // row tile pairs per (sequence, KV head)
+  int splits;  // cluster schedule: parts of a pair's keys
+};
+
+__device__ __forceinline__ float pt_max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float pt_max64(const float (&sv)[64]) {
+  float c[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) c[k] = fmaxf(sv[2 * k], sv[2 * k + 1]);
+#pragma unroll
+  for (int j = 8; j < 64; j += 8)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) c[k] = pt_max3(c[k], sv[j + 2 * k], sv[j + 2 * k + 1]);
+  return fmaxf(fmaxf(c[0], c[1]), fmaxf(c[2], c[3]));
+}
+// P = 2^(s c - m) as bf16 pairs; returns the sum of the unrounded values.  m = -inf: no key
+// has been visible yet and every s is -inf, so P is 0 with any finite offset.
+__device__ __forceinline__ float pt_exp64(const float (&sv)[64], float c, float m, uint32_t (&pw)[32]) {
+  const float nm = m == -INFINITY ? 0.f : -m;
+  const float2 cc = make_float2(c, c), nm2 = make_float2(nm, nm);
+  float2 acc[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) acc[k] = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int k = 0; k < 32; ++k) {
+    const float2 t = __ffma2_rn(make_float2(sv[2 * k], sv[2 * k + 1]), cc, nm2);
+    const float e0 = ptx::ex2(t.x), e1 = ptx::ex2(t.y);
+    acc[k & 3] = __fadd2_rn(acc[k & 3], make_float2(e0, e1));
+    pw[k] = ptx::cvt_bf16x2(e0, e1);
+  }
+  const float2 s2 = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
+  return s2.x + s2.y;
+}
+// tanh(x / 2 ln 2 ...) of a score already in units where 2^x = e^(2 z / cap): 1 - 2 / (1 + 2^x),
+// off by an ulp or two of 1
+__device__ __forceinline__ float pt_tanh2(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ptx::ex2(x)));
+  return fmaf(-2.f, r, 1.f);
+}
+
+// bits [lo, hi) of a 64-bit word
+__device__ __forceinline__ uint64_t pt_bits(int lo, int hi) {
+  lo = max(lo, 0);
+  hi = min(hi, 64);
+  if (hi <= lo) return 0ull;
+  const uint64_t up = hi == 64 ? ~0ull : (1ull << hi) - 1ull;
+  return up & ~((1ull << lo) - 1ull);
+}
+
+__device__ __forceinline__ void pt_mbar_inval(uint64_t* bar) {
+  asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(ptx::smem_addr(bar)) : "memory");
+}
+
+// Wait for this piece's own copies or products even when another wait has run out.
+__device__ __forceinline__ void pt_drain(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  int quiet = 0;
+  if (!ptx::mbar_wait(bar, parity, &quiet)) *abort_flag = 1;
+}
+
+template <int D, bool kCap, bool kStream>
+__global__ void __launch_bounds__(kPtThreads, 1)
+    paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                    const __grid_constant__ CUtensorMap tmV, PagedAttn a, PtArgs pa) {
+  ptx::griddep_launch_dependents();
+  using C = PtCfg<D>;
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t mis = ptx::smem_addr(smem_raw) & 1023u;
+  unsigned char* sm = smem_raw + ((1024u - mis) & 1023u);
+  unsigned char* sQ = sm + C::kOffQ;
+  unsigned char* sK = sm + C::kOffK;
+  unsigned char* sV = sm + C::kOffV;
+  int* s_par = reinterpret_cast<int*>(sm + C::kOffPar);
+  PtBars* bars = reinterpret_cast<PtBars*>(sm + C::kOffBar);
+  volatile int* abort_flag = &bars->abort;
+  __shared__ unsigned long long s_red[34];
+  __shared__ int s_first_pad, s_last;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int NT = pa.NT, rows_used = a.G * NT, RT = 2 * rows_used;
+  if (warp == 1) {
+    ptx::tmem_alloc(&bars->tmem_base, 512);
+    ptx::tmem_relinquish();
+  }
+  if (threadIdx.x == 0) {
+    ptx::prefetch_tmap(&tmQ);
+    ptx::prefetch_tmap(&tmK);
+    ptx::prefetch_tmap(&tmV);
+    bars->abort = 0;
+  }
+  // the Q rows that no box fills
+  for (int r = rows_used + threadIdx.x; r < 2 * kPtRows; r += kPtThreads) {
+    const int x = r >= kPtRows ? 1 : 0, rr = r - x * kPtRows;
+    if (rr < rows_used) continue;
+    for (int db = 0; db < C::kDB; ++db) {
+      uint4* row = reinterpret_cast<uint4*>(sQ + x * C::kQTile + db * C::kQBlock + rr * 128);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) row[k] = make_uint4(0, 0, 0, 0);
+    }
+  }
+  ptx::fence_proxy_async_smem();
+  // shared memory, TMEM and parameters only so far: this overlaps the previous kernel's tail
+  ptx::griddep_wait();
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+
+  // ---- this CTA's pieces
+  PagedSpan sp{};
+  long long pos = 0, end = 0, base = 0;
+  int b = 0, hk = 0, mp = 0;
+  if constexpr (kStream) {
+    sp = paged_span(a, RT, kPtKeys, 1, s_red);
+    pos = (long long)blockIdx.x * sp.per;
+    end = min(sp.W, pos + sp.per);
+    base = sp.base;
+    b = sp.b;
+  } else {
+    b = blockIdx.z, hk = blockIdx.y, mp = pa.MP - 1 - (int)blockIdx.x / pa.splits;
+  }
+  int loaded_b = -1, P = 0, n = 0, n_act = 0;
+  bool first_piece = true;
+  while (kStream ? pos < end && b < a.B : first_piece) {
+    if (b != loaded_b) {
+      P = a.prefix_len[b];
+      bool bad = false;
+      n = n_act = paged_rows(a, b, P, &bad);
+      if (bad && threadIdx.x == 0) set_dev_status(a.dev_status, TV_DEV_BAD_PAGE);
+      if (a.parent && n > 0) {
+        __syncthreads();
+        if (threadIdx.x == 0) s_first_pad = n;
+        __syncthreads();
+        int wrong = 0;
+        for (int t = threadIdx.x; t < n; t += kPtThreads) {
+          const int p = a.parent[(size_t)b * a.N + t];
+          const bool prev_pad = t >= 2 && a.parent[(size_t)b * a.N + t - 1] == -1;
+          const bool ok = t == 0 ? p == -1 : (p == -1 || (p >= 0 && p < t && !prev_pad));
+          if (!ok) wrong = 1;
+          s_par[t] = ok ? p : -1;
+          if (t > 0 && p == -1) atomicMin(&s_first_pad, t);
+        }
+        if (wrong) set_dev_status(a.dev_status, TV_DEV_BAD_TREE);
+        __syncthreads();
+        n_act = s_first_pad;
+      }
+      loaded_b = b;
+    }
+    // the next unit of this CTA's range, and its key tiles [t_begin, t_begin + nt)
+    long long u0 = 0;
+    const int T_u = unit_tiles(a, P, n, mp, RT, kPtKeys);
+    const int lo = unit_lo(a, P, mp, RT);
+    int t_begin = lo / kPtKeys, nt_all = T_u;
+    int split = 0;
+    if constexpr (kStream) {
+      u0 = base;
+      base += T_u;
+      if (pos >= base) {  // not this one
+        if (++mp * 2 * NT >= n) {
+          mp = 0;
+          if (++hk >= a.Hkv) hk = 0, ++b;
+        }
+        continue;
+      }
+      t_begin += (int)(pos - u0);
+      nt_all = (int)(min(base, end) - pos);
+      pos += nt_all;
+    } else {
+      split = blockIdx.x % pa.splits;
+      const int tps = (T_u + pa.splits - 1) / pa.splits;
+      t_begin += split * tps;
+      nt_all = max(0, min(tps, T_u - split * tps));
+    }
+    if (*abort_flag) nt_all = 0;  // a wait ran out: nothing more is computed, but cut units still count their parts
+    const int key_end = P + n_act;  // rows from here on, and before lo, may hold anything
+    int i0[2], ntx[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      i0[x] = (2 * mp + x) * NT;
+      const int hi = i0[x] < n_act ? P + min(n_act, i0[x] + NT) : 0;
+      ntx[x] = max(0, min(nt_all, (hi + kPtKeys - 1) / kPtKeys - t_begin));
+    }
+    const int nt = max(ntx[0], ntx[1]);
+
+    // ---- barriers of this piece
+    if (threadIdx.x == 0) {
+      if (!first_piece) {
+        uint64_t* w = &bars->q_full;
+        for (int k = 0; k < kPtBarWords; ++k) pt_mbar_inval(w + k);
+      }
+      ptx::mbar_init(&bars->q_full, 1);
+      for (int s = 0; s < kPtSlots; ++s) {
+        ptx::mbar_init(&bars->k_full[s], 1);
+        ptx::mbar_init(&bars->k_empty[s], 2);  // both S issuers
+        ptx::mbar_init(&bars->v_full[s], 1);
+        ptx::mbar_init(&bars->v_empty[s], 1);
+      }
+      for (int x = 0; x < 2; ++x)
+        for (int u = 0; u < 2; ++u) {
+          ptx::mbar_init(&bars->s_full[x][u], 1);
+          ptx::mbar_init(&bars->p_full[x][u], 4);
+          ptx::mbar_init(&bars->pv_done[x][u], 1);
+        }
+      ptx::mbar_init(&bars->o_done, 1);
+      ptx::mbar_init(&bars->s_done[0], 1);
+      ptx::mbar_init(&bars->s_done[1], 1);
+      ptx::fence_mbar_init();
+    }
+    first_piece = false;
+    __syncthreads();
+
+    float m_run = -INFINITY, l_run = 0.f;
+    bool have_o = false;
+    if (warp == 0) {
+      // ---------------------------------------------------------------- producer
+      // lanes 0-15 load Q and K, lanes 16-31 V; a lane's box is column block db of page piece pi
+      const bool is_v = lane >= 16;
+      const uint32_t half = is_v ? 0xffff0000u : 0x0000ffffu;
+      const int l16 = lane & 15;
+      const int box_shift = min(a.page_shift, 6);  // box rows: min(page_size, 64)
+      const int db = l16 % C::kDB, pi = l16 / C::kDB;
+      const bool in_tile = (pi << box_shift) < kPtKeys;
+      const uint32_t box_bytes = 128u << box_shift;
+      const int32_t* table = a.table + (size_t)b * a.max_pages;
+      unsigned char* ring = is_v ? sV : sK;
+      uint64_t* full = is_v ? bars->v_full : bars->k_full;
+      uint64_t* empty = is_v ? bars->v_empty : bars->k_empty;
+      // page of this lane's box in tile t, -1 where the box holds no needed row (or a bad page)
+      auto lookup = [&](int t) -> int {
+        const int j = (t_begin + t) * kPtKeys + (pi << box_shift);
+        if (t >= nt || !in_tile || j >= key_end || j + (1 << box_shift) <= lo) return -1;
+        const int page = table[j >> a.page_shift];
+        if (page < 0 || page >= a.num_pages) {
+          set_dev_status(a.dev_status, TV_DEV_BAD_PAGE);
+          return -1;
+        }
+        return page;
+      };
+      int page = lookup(0);
+      if (lane == 0 && nt > 0) {
+        uint32_t qbytes = 0;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          if (ntx[x] > 0) qbytes += (uint32_t)(rows_used * 128 * C::kDB);
+        ptx::mbar_arrive_expect_tx(&bars->q_full, qbytes);
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          if (ntx[x] > 0)
+            for (int g = 0; g < a.G; ++g)
+              for (int d = 0; d < C::kDB; ++d)
+                ptx::tma_load_3d(sQ + x * C::kQTile + d * C::kQBlock + g * NT * 128, &tmQ, &bars->q_full, d * 64, i0[x],
+                                 b * a.Hq + hk * a.G + g);
+      }
+      __syncwarp();
+      int issued = 0;
+      if (!is_v) {
+        for (int t = 0; t < nt; ++t) {
+          const int slot = t % kPtSlots;
+          bool ok = true;
+          if (t >= kPtSlots) ok = ptx::mbar_wait(&empty[slot], ((t / kPtSlots) - 1) & 1, abort_flag);
+          if (!__all_sync(half, ok)) break;
+          const uint32_t boxes = __ballot_sync(half, page >= 0);
+          if (l16 == 0) ptx::mbar_arrive_expect_tx(&full[slot], __popc(boxes) * box_bytes);
+          __syncwarp(half);
+          if (page >= 0)
+            ptx::tma_load_3d(ring + slot * C::kTileBytes + db * C::kKVBlock + (pi << box_shift) * 128, &tmK, &full[slot],
+                             db * 64, ((t_begin + t) * kPtKeys + (pi << box_shift)) & ((1 << a.page_shift) - 1),
+                             page * a.Hkv + hk);
+          issued = t + 1;
+          page = lookup(t + 1);
+        }
+      } else {
+        for (int t = 0; t < nt; ++t) {
+          const int slot = t % kPtSlots;
+          bool ok = true;
+          if (t >= kPtSlots) ok = ptx::mbar_wait(&empty[slot], ((t / kPtSlots) - 1) & 1, abort_flag);
+          if (!__all_sync(half, ok)) break;
+          const uint32_t boxes = __ballot_sync(half, page >= 0);
+          if (l16 == 0) ptx::mbar_arrive_expect_tx(&full[slot], __popc(boxes) * box_bytes);
+          __syncwarp(half);
+          if (page >= 0)
+            ptx::tma_load_3d(ring + slot * C::kTileBytes + db * C::kKVBlock + (pi << box_shift) * 128, &tmV, &full[slot],
+                             db * 64, ((t_begin + t) * kPtKeys + (pi << box_shift)) & ((1 << a.page_shift) - 1),
+                             page * a.Hkv + hk);
+          issued = t + 1;
+          page = lookup(t + 1);
+        }
+      }
+      // never leave the piece with copies in flight
+      if (l16 == 0) {
+        if (!is_v && nt > 0) pt_drain(&bars->q_full, 0, abort_flag);
+        for (int s = 0; s < kPtSlots && s < issued; ++s)
+          pt_drain(&full[s], ((issued - 1 - s) / kPtSlots) & 1, abort_flag);
+      }
+      __syncwarp();
+    } else if (warp == 1 || warp == 11) {
+      // ---------------------------------------------------------------- S issuer of tile x
+      const int x = warp == 1 ? 0 : 1;
+      if (lane == 0) {
+        if (nt > 0 && ptx::mbar_wait(&bars->q_full, 0, abort_flag)) {
+          constexpr uint32_t idS = ptx::idesc_bf16(kPtRows, kPtKeys, false, false);
+          const uint32_t qaddr = ptx::smem_addr(sQ + x * C::kQTile);
+          uint64_t adq[D / 16];
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            adq[kk] = ptx::sdesc_sw128(qaddr + (kk >> 2) * C::kQBlock + (kk & 3) * 32, 16, 1024);
+          for (int t = 0; t < nt; ++t) {
+            const int ks = t % kPtSlots, buf = t & 1;
+            if (!ptx::mbar_wait(&bars->k_full[ks], (t / kPtSlots) & 1, abort_flag)) break;
+            if (t < ntx[x]) {
+              // S_X(t) overwrites P_X(t - 2) in this buffer
+              if (t >= 2 && !ptx::mbar_wait(&bars->pv_done[x][buf], ((t - 2) >> 1) & 1, abort_flag)) break;
+              ptx::tc_fence_after();
+              const uint64_t bd = ptx::sdesc_sw128(ptx::smem_addr(sK + ks * C::kTileBytes), 16, 1024);
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk)  // 32 bytes a K step, 8 KB to the second column block
+                ptx::mma_bf16_ss(tmem + x * kPtRows + buf * kPtKeys, adq[kk], bd + (kk >> 2) * 512 + (kk & 3) * 2, idS,
+                                 kk > 0 ? 1u : 0u);
+              ptx::mma_commit(&bars->s_full[x][buf]);
+            }
+            ptx::mma_commit(&bars->k_empty[ks]);
+          }
+        }
+        ptx::mma_commit(&bars->s_done[x]);
+        pt_drain(&bars->s_done[x], 0, abort_flag);
+      }
+      __syncwarp();
+    } else if (warp == 10) {
+      // ---------------------------------------------------------------- PV issuer
+      constexpr uint32_t idO = ptx::idesc_bf16(kPtRows, D, false, true);
+      bool ok = true;
+      for (int t = 0; t < nt; ++t) {
+        const int vs = t % kPtSlots, buf = t & 1;
+        const int j0 = (t_begin + t) * kPtKeys;
+        if (j0 < lo || j0 + kPtKeys > key_end) {
+          // V rows that may hold anything: zero (their weights are zero too)
+          ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars->v_full[vs], (t / kPtSlots) & 1, abort_flag));
+          if (!ok) break;
+          for (int r = lane; r < kPtKeys; r += 32)
+            if (j0 + r < lo || j0 + r >= key_end)
+              for (int db = 0; db < C::kDB; ++db) {
+                uint4* row = reinterpret_cast<uint4*>(sV + vs * C::kTileBytes + db * C::kKVBlock + r * 128);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) row[k] = make_uint4(0, 0, 0, 0);
+              }
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (lane == 0) {
+          ok = ptx::mbar_wait(&bars->v_full[vs], (t / kPtSlots) & 1, abort_flag);
+          const uint64_t vd = ptx::sdesc_sw128(ptx::smem_addr(sV + vs * C::kTileBytes), C::kKVBlock, 1024);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (t >= ntx[x] || !ok) continue;
+            ok = ptx::mbar_wait(&bars->p_full[x][buf], (t >> 1) & 1, abort_flag);
+            if (!ok) continue;
+            ptx::tc_fence_after();
+            const uint32_t pcol = tmem + x * kPtRows + buf * kPtKeys;  // P: 8 columns per 16 keys
+#pragma unroll
+            for (int kk = 0; kk < kPtKeys / 16; ++kk)
+              ptx::mma_bf16_ts(tmem + C::kColO + x * kPtRows, pcol + kk * 8, vd + kk * 128, idO,
+                               (t > 0 || kk > 0) ? 1u : 0u);
+            ptx::mma_commit(&bars->pv_done[x][buf]);
+          }
+          if (ok) ptx::mma_commit(&bars->v_empty[vs]);
+        }
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        if (!ok) break;
+      }
+      if (lane == 0) {
+        ptx::mma_commit(&bars->o_done);
+        pt_drain(&bars->o_done, 0, abort_flag);
+      }
+      __syncwarp();
+    } else {
+      // ---------------------------------------------------------------- softmax rows
+      const int x = (warp - 2) >> 2;
+      const int q4 = warp & 3;
+      const int r = q4 * 32 + lane;
+      const int g = r / NT, node = i0[x] + r % NT;
+      const bool valid = r < rows_used && node < n_act;
+      const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
+      const uint32_t colS = tmem + lane_base + x * kPtRows;
+      const uint32_t colO = tmem + lane_base + C::kColO + x * kPtRows;
+      const int ntm = ntx[x];
+      // the row sees [wlo, whi) and, in a tree, its ancestors; rows that are no row see everything
+      // (their results go nowhere)
+      int wlo = 0, whi = 0x7fffffff;
+      if (valid) {
+        int depth = node;
+        if (a.parent) {
+          whi = P;
+          if (a.window > 0) {
+            depth = 0;
+            for (int at = s_par[node]; at >= 0; at = s_par[at]) ++depth;  // parents fall: it ends
+          }
+        } else {
+          whi = P + node + 1;
+        }
+        if (a.window > 0) wlo = P + depth - a.window + 1;
+      }
+      const float c = kCap ? a.cap * kLog2e : a.scale * kLog2e;
+      const float ck = kCap ? 2.f * kLog2e * a.scale / a.cap : 0.f;
+      bool ok = true;
+      for (int t = 0; t < ntm; ++t) {
+        const int buf = t & 1;
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars->s_full[x][buf], (t >> 1) & 1, abort_flag));
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const int j0 = (t_begin + t) * kPtKeys;
+        uint64_t vis = ~0ull;
+        if (j0 < wlo || j0 + kPtKeys > whi) {
+          vis = pt_bits(wlo - j0, whi - j0);
+          if (a.parent) {
+            int steps = a.window > 0 ? a.window : kMaxNodes + 1;
+            for (int at = node; at >= 0 && steps > 0; at = s_par[at], --steps) {
+              const int j = P + at - j0;
+              if (j < 0) break;  // ancestors only go down from here
+              if (j < kPtKeys) vis |= 1ull << j;
+            }
+          }
+        }
+        float sv[64];
+        ptx::tmem_ld32(colS + buf * kPtKeys, sv);
+        ptx::tmem_ld32(colS + buf * kPtKeys + 32, sv + 32);
+        ptx::tmem_wait_ld();
+        if constexpr (kCap) {
+#pragma unroll
+          for (int j = 0; j < 64; ++j) sv[j] = pt_tanh2(sv[j] * ck);
+        }
+        if (vis != ~0ull) {
+#pragma unroll
+          for (int j = 0; j < 64; ++j)
+            if (!((vis >> j) & 1ull)) sv[j] = -INFINITY;
+        }
+        // P = 2^(c S - m_run) against a running reference that moves (with a rescale of O) only
+        // when a score exceeds it by 2^8: such a score brings the tile's sum to 2^8, so the
+        // maximum is taken only then and for the first tile with a visible key
+        float alpha = 1.f;
+        bool need = false, checked = false;
+        if (m_run == -INFINITY) {
+          m_run = pt_max64(sv) * c;
+          checked = true;
+        }
+        uint32_t pw[32];
+        float lsum;
+        for (;;) {
+          lsum = pt_exp64(sv, c, m_run, pw);
+          if (checked || lsum < kPtRescaleSum) break;
+          checked = true;
+          const float tms = pt_max64(sv) * c;
+          if (!(tms > m_run + kPtRescaleLog2)) break;
+          alpha = ptx::ex2(m_run - tms);
+          need = true;
+          m_run = tms;
+        }
+        ptx::tmem_st32u(colS + buf * kPtKeys, pw);
+        if (__any_sync(0xffffffffu, need) && t > 0) {
+          // O_X must hold all of PV_X(t - 1) before it is rescaled
+          ok = __all_sync(0xffffffffu,
+                          ptx::mbar_wait(&bars->pv_done[x][(t - 1) & 1], ((t - 1) >> 1) & 1, abort_flag));
+          if (!ok) break;
+          ptx::tc_fence_after();
+#pragma unroll
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            float ov[32];
+            ptx::tmem_ld32(colO + c0, ov);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) ov[k] *= alpha;
+            ptx::tmem_st32(colO + c0, ov);
+          }
+        }
+        l_run = l_run * alpha + lsum;
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&bars->p_full[x][buf]);
+      }
+      // ---- epilogue: every MMA is complete at o_done
+      if (nt > 0) {
+        const bool done = __all_sync(0xffffffffu, ptx::mbar_wait(&bars->o_done, 0, abort_flag));
+        have_o = done && ok && ntm > 0;
+        if (done) ptx::tc_fence_after();
+      }
+      const bool whole = kStream ? u0 / sp.per == (base - 1) / sp.per : pa.splits == 1;
+      const int R = x * kPtRows + r;
+      const float inv = whole && l_run > 0.f ? 1.f / l_run : 0.f;
+      const size_t orow = (((size_t)b * a.Hq + hk * a.G + g) * a.N + node) * a.D;
+      float4* part = kStream && !whole ? reinterpret_cast<float4*>(a.ws_o) +
+                                             (size_t)unit_slot(blockIdx.x, sp.per, u0) * (D / 4) * 2 * kPtRows + R
+                                       : nullptr;
+#pragma unroll
+      for (int c0 = 0; c0 < D; c0 += 32) {
+        float ov[32];
+        if (have_o) {
+          ptx::tmem_ld32(colO + c0, ov);
+          ptx::tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) ov[k] = 0.f;
+        }
+        if (whole) {
+          if (valid && c0 < a.D) {
+            uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + orow + c0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              dst[k] = make_uint4(ptx::cvt_bf16x2(ov[8 * k + 0] * inv, ov[8 * k + 1] * inv),
+                                  ptx::cvt_bf16x2(ov[8 * k + 2] * inv, ov[8 * k + 3] * inv),
+                                  ptx::cvt_bf16x2(ov[8 * k + 4] * inv, ov[8 * k + 5] * inv),
+                                  ptx::cvt_bf16x2(ov[8 * k + 6] * inv, ov[8 * k + 7] * inv));
+          }
+        } else if constexpr (kStream) {
+          // partial O as [D / 4][256 rows] of four columns: a warp stores 512 bytes in a row
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            __stcg(part + (size_t)(c0 / 4 + k) * 2 * kPtRows,
+                   make_float4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]));
+        } else {
+          // row-major [256][D] with the 16-byte chunks XOR-swizzled by the row, in the drained rings
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int chunk = c0 / 4 + k;
+            *reinterpret_cast<float4*>(sK + (size_t)R * D * 4 + ((chunk ^ (R & 7)) << 4)) =
+                make_float4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]);
+          }
+        }
+      }
+      if (!whole) {
+        const float2 ml = make_float2(have_o ? m_run : -INFINITY, have_o ? l_run : 0.f);
+        if constexpr (kStream)
+          __stcg(a.ws_ml + (size_t)unit_slot(blockIdx.x, sp.per, u0) * 2 * kPtRows + R, ml);
+        else
+          reinterpret_cast<float2*>(sQ)[R] = ml;
+      }
+      ptx::tc_fence_before();
+    }
+    __syncwarp();
+
+    if constexpr (kStream) {
+      const long long c0 = u0 / sp.per, c1 = (base - 1) / sp.per;
+      if (c0 != c1) {
+        __threadfence();
+        __syncthreads();
+        if (threadIdx.x == 0) {
+          s_last = ptx::atom_add_acq_rel_gpu(&a.cnt[c0], 1u) == (unsigned)(c1 - c0);
+          if (s_last) a.cnt[c0] = 0u;
+          __threadfence();
+        }
+        __syncthreads();
+        if (s_last && warp >= 2 && warp < 10) {
+          const int x = (warp - 2) >> 2, r = (warp & 3) * 32 + lane, R = x * kPtRows + r;
+          const int g = r / NT, node = i0[x] + r % NT;
+          if (r < rows_used && node < n_act) {
+            float M = -INFINITY, L = 0.f;
+            for (long long cc = c0; cc <= c1; ++cc)
+              M = fmaxf(M, __ldcg(&a.ws_ml[(size_t)unit_slot(cc, sp.per, u0) * 2 * kPtRows + R]).x);
+            for (long long cc = c0; cc <= c1; ++cc) {
+              const float2 ml = __ldcg(&a.ws_ml[(size_t)unit_slot(cc, sp.per, u0) * 2 * kPtRows + R]);
+              if (ml.x != -INFINITY) L = fmaf(ptx::ex2(ml.x - M), ml.y, L);
+            }
+            const float inv = L > 0.f ? 1.f / L : 0.f;
+            const size_t orow = (((size_t)b * a.Hq + hk * a.G + g) * a.N + node) * a.D;
+#pragma unroll 1
+            for (int col = 0; col < a.D; col += 32) {
+              float ov[32];
+#pragma unroll
+              for (int k = 0; k < 32; ++k) ov[k] = 0.f;
+              for (long long cc = c0; cc <= c1; ++cc) {
+                const int slot = unit_slot(cc, sp.per, u0);
+                const float2 ml = __ldcg(&a.ws_ml[(size_t)slot * 2 * kPtRows + R]);
+                if (ml.x == -INFINITY) continue;
+                const float w = ptx::ex2(ml.x - M);
+                const float4* src =
+                    reinterpret_cast<const float4*>(a.ws_o) + ((size_t)slot * (D / 4) + col / 4) * 2 * kPtRows + R;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const float4 v = __ldcg(src + (size_t)k * 2 * kPtRows);
+                  ov[4 * k] = fmaf(w, v.x, ov[4 * k]);
+                  ov[4 * k + 1] = fmaf(w, v.y, ov[4 * k + 1]);
+                  ov[4 * k + 2] = fmaf(w, v.z, ov[4 * k + 2]);
+                  ov[4 * k + 3] = fmaf(w, v.w, ov[4 * k + 3]);
+                }
+              }
+              uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + orow + col);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                dst[k] = make_uint4(ptx::cvt_bf16x2(ov[8 * k + 0] * inv, ov[8 * k + 1] * inv),
+                                    ptx::cvt_bf16x2(ov[8 * k + 2] * inv, ov[8 * k + 3] * inv),
+                                    ptx::cvt_bf16x2(ov[8 * k + 4] * inv, ov[8 * k + 5] * inv),
+                                    ptx::cvt_bf16x2(ov[8 * k + 6] * inv, ov[8 * k + 7] * inv));
+            }
+          }
+        }
+      }
+      // the next unit
+      if (++mp * 2 * NT >= n) {
+        mp = 0;
+        if (++hk >= a.Hkv) hk = 0, ++b;
+      }
+    } else if (pa.splits > 1) {
+      // the parts of this pair form one cluster: CTA `split` merges its share of the rows from
+      // all parts' shared memory, and nobody leaves before every peer has read
+      ptx::cluster_sync();
+      const int S = pa.splits;
+      const int share = (2 * kPtRows + S - 1) / S;
+      const int r0 = split * share, r1 = min(2 * kPtRows, r0 + share);
+      constexpr int kChunks = D / 4;
+      const uint32_t part_local = ptx::smem_addr(sK), ml_local = ptx::smem_addr(sQ);
+      for (int item = threadIdx.x; item < max(0, r1 - r0) * kChunks; item += kPtThreads) {
+        const int R = r0 + item / kChunks, ch = item % kChunks;
+        const int x = R >= kPtRows ? 1 : 0, r = R - x * kPtRows;
+        const int g = r / NT, node = i0[x] + r % NT;
+        if (r >= rows_used || node >= n_act || ch * 4 >= a.D) continue;
+        float2 mlv[kPtMaxSplits];
+        float4 xv[kPtMaxSplits];
+        const uint32_t xoff = (uint32_t)(R * D * 4 + ((ch ^ (R & 7)) << 4));
+#pragma unroll
+        for (int s2 = 0; s2 < kPtMaxSplits; ++s2)
+          if (s2 < S) {
+            mlv[s2] = ptx::ld_cluster_f32x2(ptx::map_cluster(ml_local, s2) + R * 8);
+            xv[s2] = ptx::ld_cluster_f32x4(ptx::map_cluster(part_local, s2) + xoff);
+          }
+        float M = -INFINITY;
+#pragma unroll
+        for (int s2 = 0; s2 < kPtMaxSplits; ++s2)
+          if (s2 < S) M = fmaxf(M, mlv[s2].x);
+        float L = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int s2 = 0; s2 < kPtMaxSplits; ++s2)
+          if (s2 < S && mlv[s2].x != -INFINITY) {
+            const float w = ptx::ex2(mlv[s2].x - M);
+            L = fmaf(mlv[s2].y, w, L);
+            acc.x = fmaf(w, xv[s2].x, acc.x);
+            acc.y = fmaf(w, xv[s2].y, acc.y);
+            acc.z = fmaf(w, xv[s2].z, acc.z);
+            acc.w = fmaf(w, xv[s2].w, acc.w);
+          }
+        const float inv = L > 0.f ? 1.f / L : 0.f;
+        const size_t o = (((size_t)b * a.Hq + hk * a.G + g) * a.N + node) * a.D + ch * 4;
+        *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + o) =
+            make_uint2(ptx::cvt_bf16x2(acc.x * inv, acc.y * inv), ptx::cvt_bf16x2(acc.z * inv, acc.w * inv));
+      }
+      __syncwarp();
+      ptx::cluster_sync();
+    }
+    __syncthreads();  // every role is done with this piece's barriers, rings and TMEM
+    ptx::tc_fence_after();
+  }
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+  if (threadIdx.x == 0 && bars->abort) set_dev_status(a.dev_status, TV_DEV_TIMEOUT);
+}
+
+// ---- host side
+
+typedef CUresult (*PtEncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                               const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+bool paged_tmap(CUtensorMap* m, const void* base, int D, int rows, long long planes, int box_rows) {
+  static std::atomic<PtEncodeFn> known{nullptr};
+  PtEncodeFn fn = known.load(std::memory_order_relaxed);
+  if (!fn) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return false;
+    fn = reinterpret_cast<PtEncodeFn>(p);
+    known.store(fn, std::memory_order_relaxed);
+  }
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)rows, (cuuint64_t)planes};
+  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)rows * D * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
+  const cuuint32_t step[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct PtPlan {
+  int NT, MP, splits;  // splits 0: persistent grid
+  size_t bytes;        // workspace
+};
+
+static PtPlan pt_plan(int B, int Hq, int Hkv, int D, int N) {
+  PtPlan p{};
+  const int G = Hq / Hkv;
+  p.NT = (kPtRows / G) / 8 * 8;
+  p.MP = (N + 2 * p.NT - 1) / (2 * p.NT);
+  const int sms = paged_device_sms();
+  const long long units = (long long)B * Hkv * p.MP;
+  // up to half as many pairs as SMs: each runs as a cluster of parts that merge on chip
+  if (units * 2 <= sms && B <= 65535 && Hkv <= 65535) p.splits = (int)min((long long)kPtMaxSplits, sms / units);
+  if (p.splits == 0) {
+    const size_t slots = (size_t)2 * kPagedMaxSms;
+    p.bytes = kPagedCntBytes + slots * 2 * kPtRows * 8 + slots * 2 * kPtRows * (D <= 64 ? 64 : 128) * 4;
+  }
+  return p;
+}
+
+bool paged_tc_takes(int Hq, int Hkv, int D, int N) {
+  const int G = Hq / Hkv;
+  return D <= 128 && G <= 16 && (long long)G * N > kPagedFewRows;
+}
+
+size_t paged_tc_ws(int B, int Hq, int Hkv, int D, int N) { return pt_plan(B, Hq, Hkv, D, N).bytes; }
+
+template <int D, bool kCap, bool kStream>
+static cudaError_t launch_pt(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a,
+                             const PtPlan& p, cudaStream_t stream) {
+  constexpr int smem = PtCfg<D>::kSmemAlloc;
+  cudaError_t e = cudaFuncSetAttribute(paged_tc_kernel<D, kCap, kStream>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       smem);
+  if (e != cudaSuccess) return e;
+  const PtArgs pa{p.NT, p.MP, p.splits};
+  if (kStream)
+    return launch_pdl(paged_tc_kernel<D, kCap, kStream>, dim3((unsigned)paged_grid_sms()), dim3(kPtThreads), smem, stream,
+                      nullptr, 0, mq, mk, mv, a, pa);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)p.splits;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  return launch_pdl(paged_tc_kernel<D, kCap, kStream>, dim3((unsigned)(p.MP * p.splits), (unsigned)a.Hkv, (unsigned)a.B),
+                    dim3(kPtThreads), smem, stream, attr, 1, mq, mk, mv, a, pa);
+}
+
+cudaError_t launch_paged_tc(PagedAttn a, char* ws, cudaStream_t stream) {
+  const PtPlan p = pt_plan(a.B, a.Hq, a.Hkv, a.D, a.N);
+  const size_t slots = (size_t)2 * kPagedMaxSms;
+  a.cnt = reinterpret_cast<unsigned*>(ws);
+  a.ws_ml = reinterpret_cast<float2*>(ws + kPagedCntBytes);
+  a.ws_o = reinterpret_cast<float*>(ws + kPagedCntBytes + slots * 2 * kPtRows * 8);
+  const int ps = 1 << a.page_shift, box = min(ps, kPtKeys);
+  CUtensorMap mq, mk, mv;
+  if (!paged_tmap(&mq, a.q, a.D, a.N, (long long)a.B * a.Hq, p.NT) ||
+      !paged_tmap(&mk, a.k, a.D, ps, (long long)a.num_pages * a.Hkv, box) ||
+      !paged_tmap(&mv, a.v, a.D, ps, (long long)a.num_pages * a.Hkv, box))
+    return cudaErrorInvalidValue;
+  const bool cap = a.cap > 0.f, str = p.splits == 0;
+  if (a.D <= 64) {
+    if (cap) return str ? launch_pt<64, true, true>(mq, mk, mv, a, p, stream)
+                        : launch_pt<64, true, false>(mq, mk, mv, a, p, stream);
+    return str ? launch_pt<64, false, true>(mq, mk, mv, a, p, stream)
+               : launch_pt<64, false, false>(mq, mk, mv, a, p, stream);
+  }
+  if (cap) return str ? launch_pt<128, true, true>(mq, mk, mv, a, p, stream)
+                      : launch_pt<128, true, false>(mq, mk, mv, a, p, stream);
+  return str ? launch_pt<128, false, true>(mq, mk, mv, a, p, stream)
+             : launch_pt<128, false, false>(mq, mk, mv, a, p, stream);
+}
+
+}  // namespace tv
