@@ -6,6 +6,8 @@
 // 0..P_b-1 (P_b = prefix_len[b]) and its new rows P_b..P_b+n_b-1.
 #pragma once
 
+#include <cuda.h>
+
 #include "tv_kernels.cuh"
 #include "tv_ptx.cuh"
 
@@ -110,6 +112,13 @@ __device__ __forceinline__ int unit_slot(long long c, long long per, long long u
   return (int)(2 * c + (u0 < c * per ? 0 : 1));
 }
 
+// tanh(y / 2) with y given as x = y log2 e: 1 - 2 / (1 + 2^x), off by an ulp or two of 1
+__device__ __forceinline__ float soft_tanh(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ptx::ex2(x)));
+  return fmaf(-2.f, r, 1.f);
+}
+
 // ---- host side
 constexpr int kPagedMaxSms = 160;  // sizes the workspaces
 constexpr int kPagedMaxCtas = 2;   // CTAs per SM of the largest persistent grid
@@ -121,5 +130,11 @@ int paged_grid_sms();  // less where tv_set_sm_partition says so
 bool paged_tc_takes(int Hq, int Hkv, int D, int N);
 size_t paged_tc_ws(int B, int Hq, int Hkv, int D, int N);
 cudaError_t launch_paged_tc(PagedAttn a, char* ws, cudaStream_t stream);
+size_t paged_mma_ws(int Hq, int Hkv, int D, int N);
+cudaError_t launch_paged_mma(PagedAttn a, char* ws, cudaStream_t stream);
+size_t paged_simt_ws(int D);
+cudaError_t launch_paged_simt(PagedAttn a, char* ws, cudaStream_t stream);
+// bf16 rows [planes][rows][D] as boxes of 64 columns x box_rows, 128-byte swizzle
+bool paged_tmap(CUtensorMap* m, const void* base, int D, int rows, long long planes, int box_rows);
 
 }  // namespace tv

@@ -1,0 +1,39 @@
+// Paged attention's entry: the kernel for a call.
+//   fp32                                     paged_simt_kernel
+//   bf16, more than 32 query rows a KV head,
+//     D <= 128, G <= 16                      paged_tc_kernel (row tiles on tcgen05)
+//   other bf16                               paged_mma_kernel (a stream of keys past few rows)
+#include <atomic>
+
+#include "paged.cuh"
+
+namespace tv {
+
+int paged_device_sms() {
+  static std::atomic<int> known[64];  // 0 = not asked yet
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (!n) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 152;
+    known[dev].store(n, std::memory_order_relaxed);
+  }
+  return min(n, kPagedMaxSms);
+}
+
+int paged_grid_sms() {
+  const int n = paged_device_sms(), share = sm_share_attention();
+  return share > 0 && share < n ? share : n;
+}
+
+size_t paged_attn_ws(int B, int Hq, int Hkv, int D, int N, tv_dtype dtype) {
+  if (dtype == TV_F32) return paged_simt_ws(D);
+  return paged_tc_takes(Hq, Hkv, D, N) ? paged_tc_ws(B, Hq, Hkv, D, N) : paged_mma_ws(Hq, Hkv, D, N);
+}
+
+cudaError_t launch_paged_attn(PagedAttn a, tv_dtype dtype, char* ws, cudaStream_t stream) {
+  if (dtype == TV_F32) return launch_paged_simt(a, ws, stream);
+  return paged_tc_takes(a.Hq, a.Hkv, a.D, a.N) ? launch_paged_tc(a, ws, stream) : launch_paged_mma(a, ws, stream);
+}
+
+}  // namespace tv

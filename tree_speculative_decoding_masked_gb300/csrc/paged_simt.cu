@@ -1,4 +1,4 @@
-// Attention of new rows (a causal chunk or a draft tree) over a paged KV cache, on CUDA
+// Attention of new rows (a causal chunk or a draft tree) over a paged fp32 KV cache, on CUDA
 // cores.
 //
 //   out[b,h,i,:] = sum_j softmax_j(z_ij) v_j,  z = scale q_i . k_j, or cap tanh(scale q_i . k_j / cap)
@@ -14,8 +14,6 @@
 // come in one broadcast load.  The units' tiles are divided equally over the CTAs
 // (paged.cuh); the CTA that finishes a cut unit last merges its parts in CTA order, so
 // results do not depend on which one that is.
-#include <atomic>
-
 #include "paged.cuh"
 
 namespace tv {
@@ -23,59 +21,30 @@ namespace tv {
 constexpr int kPsWarps = 8;
 constexpr int kPsKeys = 32;
 
-template <typename T>
-struct PsIo;
-template <>
-struct PsIo<float> {
-  static constexpr int kVec = 4;
-  static __device__ __forceinline__ void load(const float* p, float (&f)[4]) {
-    const float4 v = *reinterpret_cast<const float4*>(p);
-    f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
-  }
-  static __device__ __forceinline__ float one(const float* p) { return *p; }
-  static __device__ __forceinline__ void put(float* p, float v) { *p = v; }
-};
-template <>
-struct PsIo<uint16_t> {
-  static constexpr int kVec = 8;
-  static __device__ __forceinline__ void load(const uint16_t* p, float (&f)[8]) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  }
-  static __device__ __forceinline__ float one(const uint16_t* p) { return bf16_to_f32(*p); }
-  static __device__ __forceinline__ void put(uint16_t* p, float v) { *p = f32_to_bf16_rn(v); }
-};
-
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_addr(dst)), "l"(src) : "memory");
 }
 
-template <typename T, int kDPL, int kRPW>
+template <int kDPL, int kRPW>
 struct PsSmem {
   static constexpr int kD = kDPL * 32;
   static constexpr int kRT = kPsWarps * kRPW;
-  static constexpr int kStride = kD + 16 / (int)sizeof(T);  // K row in smem, elements
-  static constexpr int kOffV = 2 * kPsKeys * kStride * (int)sizeof(T);
-  static constexpr int kOffQ = kOffV + 2 * kPsKeys * kD * (int)sizeof(T);
+  static constexpr int kStride = kD + 4;  // K row in smem, elements
+  static constexpr int kOffV = 2 * kPsKeys * kStride * 4;
+  static constexpr int kOffQ = kOffV + 2 * kPsKeys * kD * 4;
   static constexpr int kOffP = kOffQ + kRT * kD * 4;
   static constexpr int kOffVis = kOffP + kRT * kPsKeys * 4;
   static constexpr int kOffPar = kOffVis + kRT * (kMaxNodes / 32) * 4;
   static constexpr int kBytes = kOffPar + kMaxNodes * 4;
 };
 
-template <typename T, int kDPL, int kRPW>
-__global__ void __launch_bounds__(kPsWarps * 32) paged_simt_kernel(PagedAttn a) {
-  using S = PsSmem<T, kDPL, kRPW>;
-  using Io = PsIo<T>;
-  constexpr int kD = S::kD, kRT = S::kRT, kVec = Io::kVec;
+template <int kDPL, int kRPW>
+__global__ void __launch_bounds__(kPsWarps * 32, kDPL <= 4 ? 2 : 1) paged_simt_kernel(PagedAttn a) {
+  using S = PsSmem<kDPL, kRPW>;
+  constexpr int kD = S::kD, kRT = S::kRT, kVec = 4;
   extern __shared__ __align__(16) unsigned char ps_smem[];
-  T* s_k = reinterpret_cast<T*>(ps_smem);
-  T* s_v = reinterpret_cast<T*>(ps_smem + S::kOffV);
+  float* s_k = reinterpret_cast<float*>(ps_smem);
+  float* s_v = reinterpret_cast<float*>(ps_smem + S::kOffV);
   float* s_q = reinterpret_cast<float*>(ps_smem + S::kOffQ);
   float* s_p = reinterpret_cast<float*>(ps_smem + S::kOffP);
   uint32_t(*s_vis)[kMaxNodes / 32] = reinterpret_cast<uint32_t(*)[kMaxNodes / 32]>(ps_smem + S::kOffVis);
@@ -83,8 +52,8 @@ __global__ void __launch_bounds__(kPsWarps * 32) paged_simt_kernel(PagedAttn a) 
   __shared__ unsigned long long s_red[34];
   __shared__ int s_first_pad, s_last, s_depth[kRT];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const T* q = reinterpret_cast<const T*>(a.q);
-  T* out = reinterpret_cast<T*>(a.out);
+  const float* q = reinterpret_cast<const float*>(a.q);
+  float* out = reinterpret_cast<float*>(a.out);
 
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
@@ -132,7 +101,7 @@ __global__ void __launch_bounds__(kPsWarps * 32) paged_simt_kernel(PagedAttn a) 
           const int r = rt * kRT + rr, i = r / a.G, g = r % a.G;
           const bool live = rr < rows && i < n_act;
           const size_t qoff = (((size_t)b * a.Hq + hk * a.G + g) * a.N + i) * kD;
-          for (int d = lane; d < kD; d += 32) s_q[rr * kD + d] = live ? Io::one(q + qoff + d) * a.scale : 0.f;
+          for (int d = lane; d < kD; d += 32) s_q[rr * kD + d] = live ? q[qoff + d] * a.scale : 0.f;
           if (!a.parent) {
             if (lane == 0) s_depth[rr] = i;
             continue;
@@ -161,8 +130,8 @@ __global__ void __launch_bounds__(kPsWarps * 32) paged_simt_kernel(PagedAttn a) 
           for (int e = threadIdx.x; e < kPsKeys * kChunks; e += blockDim.x) {
             const int jj = e / kChunks, ch = e - jj * kChunks;
             const int j = (tile0 + t) * kPsKeys + jj;
-            T* dk = s_k + (buf * kPsKeys + jj) * S::kStride + ch * kVec;
-            T* dv = s_v + (buf * kPsKeys + jj) * kD + ch * kVec;
+            float* dk = s_k + (buf * kPsKeys + jj) * S::kStride + ch * kVec;
+            float* dv = s_v + (buf * kPsKeys + jj) * kD + ch * kVec;
             int page = -1;
             if (j >= lo && j < hi) {
               page = table[j >> a.page_shift];
@@ -174,8 +143,8 @@ __global__ void __launch_bounds__(kPsWarps * 32) paged_simt_kernel(PagedAttn a) 
             if (page >= 0) {
               const size_t off =
                   ((((size_t)page * a.Hkv + hk) << a.page_shift) + (j & ((1 << a.page_shift) - 1))) * kD + ch * kVec;
-              cp_async16(dk, reinterpret_cast<const T*>(a.k) + off);
-              cp_async16(dv, reinterpret_cast<const T*>(a.v) + off);
+              cp_async16(dk, reinterpret_cast<const float*>(a.k) + off);
+              cp_async16(dv, reinterpret_cast<const float*>(a.v) + off);
             } else {
               *reinterpret_cast<uint4*>(dk) = make_uint4(0, 0, 0, 0);
               *reinterpret_cast<uint4*>(dv) = make_uint4(0, 0, 0, 0);
@@ -197,22 +166,18 @@ __global__ void __launch_bounds__(kPsWarps * 32) paged_simt_kernel(PagedAttn a) 
           float dot[kRPW];
 #pragma unroll
           for (int rw = 0; rw < kRPW; ++rw) dot[rw] = 0.f;
-          const T* kr = s_k + (buf * kPsKeys + lane) * S::kStride;
+          const float* kr = s_k + (buf * kPsKeys + lane) * S::kStride;
 #pragma unroll 4
           for (int d = 0; d < kD; d += kVec) {
-            float kf[kVec];
-            Io::load(kr + d, kf);
+            const float4 kf = *reinterpret_cast<const float4*>(kr + d);
 #pragma unroll
             for (int rw = 0; rw < kRPW; ++rw) {
               const float* qr = s_q + (warp * kRPW + rw) * kD + d;
-#pragma unroll
-              for (int u = 0; u < kVec; u += 4) {
-                const float4 qf = *reinterpret_cast<const float4*>(qr + u);
-                dot[rw] = fmaf(qf.x, kf[u], dot[rw]);
-                dot[rw] = fmaf(qf.y, kf[u + 1], dot[rw]);
-                dot[rw] = fmaf(qf.z, kf[u + 2], dot[rw]);
-                dot[rw] = fmaf(qf.w, kf[u + 3], dot[rw]);
-              }
+              const float4 qf = *reinterpret_cast<const float4*>(qr);
+              dot[rw] = fmaf(qf.x, kf.x, dot[rw]);
+              dot[rw] = fmaf(qf.y, kf.y, dot[rw]);
+              dot[rw] = fmaf(qf.z, kf.z, dot[rw]);
+              dot[rw] = fmaf(qf.w, kf.w, dot[rw]);
             }
           }
 #pragma unroll
@@ -252,8 +217,8 @@ __global__ void __launch_bounds__(kPsWarps * 32) paged_simt_kernel(PagedAttn a) 
               pf[rw] = *reinterpret_cast<const float4*>(s_p + (warp * kRPW + rw) * kPsKeys + jj);
 #pragma unroll
             for (int u = 0; u < kDPL; ++u) {
-              const T* vr = s_v + (buf * kPsKeys + jj) * kD + lane + 32 * u;
-              const float v0 = Io::one(vr), v1 = Io::one(vr + kD), v2 = Io::one(vr + 2 * kD), v3 = Io::one(vr + 3 * kD);
+              const float* vr = s_v + (buf * kPsKeys + jj) * kD + lane + 32 * u;
+              const float v0 = vr[0], v1 = vr[kD], v2 = vr[2 * kD], v3 = vr[3 * kD];
 #pragma unroll
               for (int rw = 0; rw < kRPW; ++rw)
                 acc[rw][u] = fmaf(pf[rw].w, v3, fmaf(pf[rw].z, v2, fmaf(pf[rw].y, v1, fmaf(pf[rw].x, v0, acc[rw][u]))));
@@ -272,7 +237,7 @@ __global__ void __launch_bounds__(kPsWarps * 32) paged_simt_kernel(PagedAttn a) 
             const size_t off = (((size_t)b * a.Hq + hk * a.G + g) * a.N + i) * kD;
             const float inv = 1.f / l[rw];
 #pragma unroll
-            for (int u = 0; u < kDPL; ++u) Io::put(out + off + lane + 32 * u, acc[rw][u] * inv);
+            for (int u = 0; u < kDPL; ++u) out[off + lane + 32 * u] = acc[rw][u] * inv;
           } else {
             const size_t row = (size_t)slot * kRT + rr;
             if (lane == 0) a.ws_ml[row] = make_float2(m[rw], l[rw]);
@@ -309,7 +274,7 @@ __global__ void __launch_bounds__(kPsWarps * 32) paged_simt_kernel(PagedAttn a) 
           }
           const size_t off = (((size_t)b * a.Hq + hk * a.G + g) * a.N + i) * kD;
 #pragma unroll
-          for (int u = 0; u < kDPL; ++u) Io::put(out + off + lane + 32 * u, o[u] / L);
+          for (int u = 0; u < kDPL; ++u) out[off + lane + 32 * u] = o[u] / L;
         }
       }
     }
@@ -318,74 +283,51 @@ __global__ void __launch_bounds__(kPsWarps * 32) paged_simt_kernel(PagedAttn a) 
 
 // ---- host side
 
-int paged_device_sms() {
-  static std::atomic<int> known[64];  // 0 = not asked yet
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
-  int n = known[dev].load(std::memory_order_relaxed);
-  if (!n) {
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 152;
-    known[dev].store(n, std::memory_order_relaxed);
-  }
-  return min(n, kPagedMaxSms);
-}
-
-int paged_grid_sms() {
-  const int n = paged_device_sms(), share = sm_share_attention();
-  return share > 0 && share < n ? share : n;
-}
-
 // counters, (m, l) and O of two partial units per CTA of the largest grid
 constexpr size_t kPsRows = (size_t)2 * kPagedMaxCtas * kPagedMaxSms * kPsWarps * 4;
 
-size_t paged_attn_ws(int B, int Hq, int Hkv, int D, int N, tv_dtype dtype) {
-  if (dtype == TV_BF16 && paged_tc_takes(Hq, Hkv, D, N)) return paged_tc_ws(B, Hq, Hkv, D, N);
-  return kPagedCntBytes + kPsRows * 8 + kPsRows * D * 4;
-}
+size_t paged_simt_ws(int D) { return kPagedCntBytes + kPsRows * 8 + kPsRows * D * 4; }
 
-template <typename T, int kDPL, int kRPW>
+template <int kDPL, int kRPW>
 static cudaError_t launch_ps(PagedAttn a, char* ws, cudaStream_t stream) {
-  using S = PsSmem<T, kDPL, kRPW>;
-  cudaError_t e = cudaFuncSetAttribute(paged_simt_kernel<T, kDPL, kRPW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  using S = PsSmem<kDPL, kRPW>;
+  cudaError_t e = cudaFuncSetAttribute(paged_simt_kernel<kDPL, kRPW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        S::kBytes);
   if (e != cudaSuccess) return e;
   a.cnt = reinterpret_cast<unsigned*>(ws);
   a.ws_ml = reinterpret_cast<float2*>(ws + kPagedCntBytes);
   a.ws_o = reinterpret_cast<float*>(ws + kPagedCntBytes + kPsRows * 8);
-  return launch_pdl(paged_simt_kernel<T, kDPL, kRPW>, dim3((unsigned)(paged_grid_sms() * kPagedMaxCtas)),
+  return launch_pdl(paged_simt_kernel<kDPL, kRPW>, dim3((unsigned)(paged_grid_sms() * kPagedMaxCtas)),
                     dim3(kPsWarps * 32), S::kBytes, stream, nullptr, 0, a);
 }
 
-template <typename T, int kRPW>
+template <int kRPW>
 static cudaError_t launch_ps_d(const PagedAttn& a, char* ws, cudaStream_t stream) {
   switch (a.D / 32) {
     case 1:
-      return launch_ps<T, 1, kRPW>(a, ws, stream);
+      return launch_ps<1, kRPW>(a, ws, stream);
     case 2:
-      return launch_ps<T, 2, kRPW>(a, ws, stream);
+      return launch_ps<2, kRPW>(a, ws, stream);
     case 3:
-      return launch_ps<T, 3, kRPW>(a, ws, stream);
+      return launch_ps<3, kRPW>(a, ws, stream);
     case 4:
-      return launch_ps<T, 4, kRPW>(a, ws, stream);
+      return launch_ps<4, kRPW>(a, ws, stream);
     case 5:
-      return launch_ps<T, 5, kRPW>(a, ws, stream);
+      return launch_ps<5, kRPW>(a, ws, stream);
     case 6:
-      return launch_ps<T, 6, kRPW>(a, ws, stream);
+      return launch_ps<6, kRPW>(a, ws, stream);
     case 7:
-      return launch_ps<T, 7, kRPW>(a, ws, stream);
+      return launch_ps<7, kRPW>(a, ws, stream);
     case 8:
-      return launch_ps<T, 8, kRPW>(a, ws, stream);
+      return launch_ps<8, kRPW>(a, ws, stream);
     default:
       return cudaErrorInvalidValue;
   }
 }
 
-cudaError_t launch_paged_attn(PagedAttn a, tv_dtype dtype, char* ws, cudaStream_t stream) {
-  if (dtype == TV_BF16 && paged_tc_takes(a.Hq, a.Hkv, a.D, a.N)) return launch_paged_tc(a, ws, stream);
-  const bool few = (long long)a.G * a.N <= kPsWarps;
-  if (dtype == TV_BF16)
-    return few ? launch_ps_d<uint16_t, 1>(a, ws, stream) : launch_ps_d<uint16_t, 4>(a, ws, stream);
-  return few ? launch_ps_d<float, 1>(a, ws, stream) : launch_ps_d<float, 4>(a, ws, stream);
+cudaError_t launch_paged_simt(PagedAttn a, char* ws, cudaStream_t stream) {
+  // few rows: one a warp, so that a KV head's rows spread over a CTA's warps
+  return a.G * a.N <= kPsWarps ? launch_ps_d<1>(a, ws, stream) : launch_ps_d<4>(a, ws, stream);
 }
 
 }  // namespace tv

@@ -26,8 +26,6 @@
 // steps equally (paged.cuh), which keeps ragged batches and causal triangles balanced; a
 // pair cut between CTAs is merged through the workspace, in CTA order, by the CTA that
 // finishes last.
-#include <cuda.h>
-
 #include <atomic>
 
 #include "paged.cuh"
@@ -116,14 +114,6 @@ __device__ __forceinline__ float pt_exp64(const float (&sv)[64], float c, float 
   const float2 s2 = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
   return s2.x + s2.y;
 }
-// tanh(x / 2 ln 2 ...) of a score already in units where 2^x = e^(2 z / cap): 1 - 2 / (1 + 2^x),
-// off by an ulp or two of 1
-__device__ __forceinline__ float pt_tanh2(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ptx::ex2(x)));
-  return fmaf(-2.f, r, 1.f);
-}
-
 // bits [lo, hi) of a 64-bit word
 __device__ __forceinline__ uint64_t pt_bits(int lo, int hi) {
   lo = max(lo, 0);
@@ -511,7 +501,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         ptx::tmem_wait_ld();
         if constexpr (kCap) {
 #pragma unroll
-          for (int j = 0; j < 64; ++j) sv[j] = pt_tanh2(sv[j] * ck);
+          for (int j = 0; j < 64; ++j) sv[j] = soft_tanh(sv[j] * ck);
         }
         if (vis != ~0ull) {
 #pragma unroll
