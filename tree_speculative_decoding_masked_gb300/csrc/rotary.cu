@@ -18,49 +18,50 @@
 namespace tv {
 
 constexpr int kRotThreads = 256;
+constexpr int kRotHeads = 4;  // heads whose loads are in flight together
 
-// kVec contiguous elements as floats
+// kVec contiguous elements in one load or store
 template <typename T, int kVec>
-__device__ __forceinline__ void rot_load(const T* p, float (&f)[kVec]) {
+struct RotRaw {
+  using type = uint4;
+};
+template <typename T>
+struct RotRaw<T, 1> {
+  using type = T;
+};
+template <typename T, int kVec>
+__device__ __forceinline__ void rot_unpack(const typename RotRaw<T, kVec>::type& r, float (&f)[kVec]) {
   if constexpr (kVec == 1) {
     if constexpr (sizeof(T) == 2)
-      f[0] = bf16_to_f32(*p);
+      f[0] = bf16_to_f32(r);
     else
-      f[0] = *p;
-  } else if constexpr (sizeof(T) == 2) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      f[0] = r;
+  } else {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      if constexpr (sizeof(T) == 2) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      } else {
+        f[i] = __uint_as_float(w[i]);
+      }
     }
-  } else {
-    const float4 v = *reinterpret_cast<const float4*>(p);
-    f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
   }
 }
 template <typename T, int kVec>
-__device__ __forceinline__ void rot_store(T* p, const float (&f)[kVec]) {
+__device__ __forceinline__ typename RotRaw<T, kVec>::type rot_pack(const float (&f)[kVec]) {
   if constexpr (kVec == 1) {
     if constexpr (sizeof(T) == 2)
-      *p = (T)(ptx::cvt_bf16x2(f[0], 0.f) & 0xffffu);
+      return (T)(ptx::cvt_bf16x2(f[0], 0.f) & 0xffffu);
     else
-      *p = f[0];
+      return f[0];
   } else if constexpr (sizeof(T) == 2) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(ptx::cvt_bf16x2(f[0], f[1]), ptx::cvt_bf16x2(f[2], f[3]),
-                                              ptx::cvt_bf16x2(f[4], f[5]), ptx::cvt_bf16x2(f[6], f[7]));
+    return make_uint4(ptx::cvt_bf16x2(f[0], f[1]), ptx::cvt_bf16x2(f[2], f[3]), ptx::cvt_bf16x2(f[4], f[5]),
+                      ptx::cvt_bf16x2(f[6], f[7]));
   } else {
-    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
   }
-}
-// kVec contiguous elements unchanged (a NaN's bits survive)
-template <typename T, int kVec>
-__device__ __forceinline__ void rot_copy(T* dst, const T* src) {
-  if constexpr (kVec == 1)
-    *dst = *src;
-  else
-    *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
 }
 
 // Grid: x over (token, column) pairs, y over groups of `hg` of the Hq + 2 Hkv heads.  A column
@@ -93,21 +94,24 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(RotaryArgs a, int c
       set_dev_status(a.dev_status, TV_DEV_BAD_PAGE);
   }
   if (p < 0) return;  // a negative base
-  // this thread's elements: ea.. and eb.. (eb == D: none)
+  // this thread's elements: ea.. and eb.. (eb >= D: none)
   const bool turn = col < rot_cols;
+  const bool pairs_inside = a.interleaved && kVec > 1;  // x and y hold kVec / 2 whole pairs each
   int ea, eb;
   if (turn) {
-    ea = a.interleaved ? 2 * kVec * col : kVec * col;
-    eb = a.interleaved ? ea + kVec : ea + a.rot / 2;
+    ea = a.interleaved && kVec == 1 ? 2 * col : kVec * col;
+    eb = a.interleaved && kVec == 1 ? ea + 1 : ea + a.rot / 2;
   } else {
-    ea = a.rot + 2 * kVec * (col - rot_cols);
-    eb = min(a.D, ea + kVec);
+    ea = a.rot + kVec * (col - rot_cols);
+    eb = ea + kVec * (cols - rot_cols);
   }
   float cs[kVec], sn[kVec];
   if (turn && h0 < a.Hq + a.Hkv) {
 #pragma unroll
     for (int u = 0; u < kVec; ++u) {
-      const uint64_t turns = (uint64_t)p * a.freq[kVec * col + u];
+      int pair = kVec * col + u;
+      if (pairs_inside) pair = (u < kVec / 2 ? 0 : a.rot / 4 - kVec / 2) + kVec / 2 * col + u;
+      const uint64_t turns = (uint64_t)p * a.freq[pair];
       // a signed half turn in 2^-31 steps: within 2^-31 pi of the angle
       const float half = (float)(int)(turns >> 32) * 0x1p-31f;
       sincospif(half, &sn[u], &cs[u]);
@@ -115,46 +119,64 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(RotaryArgs a, int c
       cs[u] *= a.amplitude;
     }
   }
-  for (int h = h0; h < h1; ++h) {
+  auto source = [&](int h) -> const T* {
     const int part = h < a.Hq ? 0 : h < a.Hq + a.Hkv ? 1 : 2;
     const int hh = part == 0 ? h : part == 1 ? h - a.Hq : h - a.Hq - a.Hkv;
-    const T* src = reinterpret_cast<const T*>(a.src[part]) + b * a.sb[part] + hh * a.sh[part] + t * a.sn[part];
-    T* dst;
-    if (part == 0) {
-      dst = reinterpret_cast<T*>(a.q_out) + (((long long)b * a.Hq + hh) * a.N + t) * a.D;
-    } else {
-      if (page_row < 0) continue;
-      dst = reinterpret_cast<T*>(part == 1 ? a.k_cache : a.v_cache) +
-            (page_row + ((long long)hh << a.page_shift)) * a.D;
-    }
-    if (part == 2 || !turn) {
-      rot_copy<T, kVec>(dst + ea, src + ea);
-      if (eb < a.D) rot_copy<T, kVec>(dst + eb, src + eb);
-      continue;
-    }
-    float x[kVec], y[kVec];
-    rot_load<T, kVec>(src + ea, x);
-    rot_load<T, kVec>(src + eb, y);
-    if (a.interleaved && kVec > 1) {
-      // x, y hold 2 kVec contiguous elements: pair u is elements 2u, 2u + 1
+    return reinterpret_cast<const T*>(a.src[part]) + b * a.sb[part] + hh * a.sh[part] + t * a.sn[part];
+  };
+  auto target = [&](int h) -> T* {
+    if (h < a.Hq) return reinterpret_cast<T*>(a.q_out) + (((long long)b * a.Hq + h) * a.N + t) * a.D;
+    if (page_row < 0) return nullptr;
+    const bool is_v = h >= a.Hq + a.Hkv;
+    const int hh = is_v ? h - a.Hq - a.Hkv : h - a.Hq;
+    return reinterpret_cast<T*>(is_v ? a.v_cache : a.k_cache) + (page_row + ((long long)hh << a.page_shift)) * a.D;
+  };
+  const bool two = eb < a.D;
+  using Raw = typename RotRaw<T, kVec>::type;
+  for (int hb = h0; hb < h1; hb += kRotHeads) {
+    // the batch's loads first: they are in flight together (a row may be rotated in place, so the
+    // compiler would not move a load past an earlier head's store)
+    Raw ra[kRotHeads], rb[kRotHeads];
 #pragma unroll
-      for (int u = 0; u < kVec / 2; ++u) {
-        const float e0 = x[2 * u], o0 = x[2 * u + 1], e1 = y[2 * u], o1 = y[2 * u + 1];
-        x[2 * u] = e0 * cs[u] - o0 * sn[u];
-        x[2 * u + 1] = o0 * cs[u] + e0 * sn[u];
-        y[2 * u] = e1 * cs[kVec / 2 + u] - o1 * sn[kVec / 2 + u];
-        y[2 * u + 1] = o1 * cs[kVec / 2 + u] + e1 * sn[kVec / 2 + u];
+    for (int u = 0; u < kRotHeads; ++u)
+      if (hb + u < h1) {
+        const T* src = source(hb + u);
+        ra[u] = *reinterpret_cast<const Raw*>(src + ea);
+        if (two) rb[u] = *reinterpret_cast<const Raw*>(src + eb);
       }
-    } else {
 #pragma unroll
-      for (int u = 0; u < kVec; ++u) {
-        const float e = x[u], o = y[u];
-        x[u] = e * cs[u] - o * sn[u];
-        y[u] = o * cs[u] + e * sn[u];
+    for (int u = 0; u < kRotHeads; ++u) {
+      if (hb + u >= h1) break;
+      T* dst = target(hb + u);
+      if (!dst) continue;
+      if (turn && hb + u < a.Hq + a.Hkv) {
+        float x[kVec], y[kVec];
+        rot_unpack<T, kVec>(ra[u], x);
+        rot_unpack<T, kVec>(rb[u], y);
+        if (pairs_inside) {
+#pragma unroll
+          for (int k = 0; k < kVec / 2; ++k) {
+            const float e0 = x[2 * k], o0 = x[2 * k + 1], e1 = y[2 * k], o1 = y[2 * k + 1];
+            x[2 * k] = e0 * cs[k] - o0 * sn[k];
+            x[2 * k + 1] = o0 * cs[k] + e0 * sn[k];
+            y[2 * k] = e1 * cs[kVec / 2 + k] - o1 * sn[kVec / 2 + k];
+            y[2 * k + 1] = o1 * cs[kVec / 2 + k] + e1 * sn[kVec / 2 + k];
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < kVec; ++k) {
+            const float e = x[k], o = y[k];
+            x[k] = e * cs[k] - o * sn[k];
+            y[k] = o * cs[k] + e * sn[k];
+          }
+        }
+        ra[u] = rot_pack<T, kVec>(x);
+        rb[u] = rot_pack<T, kVec>(y);
       }
+      // values and the elements behind the rotated part go through unchanged (a NaN's bits survive)
+      *reinterpret_cast<Raw*>(dst + ea) = ra[u];
+      if (two) *reinterpret_cast<Raw*>(dst + eb) = rb[u];
     }
-    rot_store<T, kVec>(dst + ea, x);
-    rot_store<T, kVec>(dst + eb, y);
   }
 }
 
