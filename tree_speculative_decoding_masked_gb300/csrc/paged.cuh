@@ -58,19 +58,22 @@ __device__ inline long long seq_tiles(const PagedAttn& a, int b, int RT, int KT,
   return s;
 }
 
-// Every thread of the CTA calls it; red holds 34 entries.  per is at least min_per.
+// Every thread of the CTA calls it; red holds 34 entries.  A CTA takes min_per tiles or more.
 __device__ inline PagedSpan paged_span(const PagedAttn& a, int RT, int KT, int min_per, unsigned long long* red) {
   PagedSpan sp;
-  unsigned long long W = 0;
+  unsigned long long W = 0, mine = 0, at = 0;
   bool any_bad = false;
-  unsigned long long mine = 0;
-  for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {
-    const int b = b0 + threadIdx.x;
+  auto tiles_of = [&](int b) -> unsigned long long {
+    if (b >= a.B) return 0ull;
     bool bad = false;
-    mine = b < a.B ? (unsigned long long)seq_tiles(a, b, RT, KT, &bad) * a.Hkv : 0ull;
+    const unsigned long long t = (unsigned long long)seq_tiles(a, b, RT, KT, &bad) * a.Hkv;
     any_bad |= bad;
+    return t;
+  };
+  for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {
+    mine = tiles_of(b0 + threadIdx.x);
     unsigned long long part = 0;
-    block_scan_u64(mine, red, &part);
+    at = W + block_scan_u64(mine, red, &part);
     W += part;
   }
   if (any_bad && blockIdx.x == 0) set_dev_status(a.dev_status, TV_DEV_BAD_PAGE);
@@ -80,26 +83,29 @@ __device__ inline PagedSpan paged_span(const PagedAttn& a, int RT, int KT, int m
   sp.b = a.B;
   sp.base = sp.W;
   if (begin >= W) return sp;  // the same for the whole CTA
+  // the sequence that holds tile `begin`; with more sequences than threads their tiles are
+  // counted once more
   unsigned long long cum = 0;
   for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {
-    const int b = b0 + threadIdx.x;
-    bool bad = false;
-    if (a.B > (int)blockDim.x) mine = b < a.B ? (unsigned long long)seq_tiles(a, b, RT, KT, &bad) * a.Hkv : 0ull;
     unsigned long long part = 0;
-    const unsigned long long at = cum + block_scan_u64(mine, red, &part);
+    if (a.B > (int)blockDim.x) {
+      mine = tiles_of(b0 + threadIdx.x);
+      at = cum + block_scan_u64(mine, red, &part);
+      cum += part;
+    } else {
+      cum = W;
+    }
     if (begin >= at && begin < at + mine) {
-      red[0] = (unsigned long long)b;
+      red[0] = (unsigned long long)(b0 + threadIdx.x);
       red[1] = at;
     }
-    const bool here = begin < cum + part;
     __syncthreads();
-    if (here) {
+    if (begin < cum) {
       sp.b = (int)red[0];
       sp.base = (long long)red[1];
       __syncthreads();
       break;
     }
-    cum += part;
   }
   return sp;
 }

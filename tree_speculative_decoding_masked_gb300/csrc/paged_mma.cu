@@ -18,6 +18,8 @@
 namespace tv {
 
 constexpr int kPmKeys = 64;
+constexpr int kPmMerge = 8;   // parts whose loads are in flight together
+constexpr int kPmMinTiles = 2;  // tiles of a CTA's range: fewer only add parts to merge
 
 template <int kD, int kMT>
 struct PmCfg {
@@ -135,7 +137,7 @@ __global__ void __launch_bounds__(PmCfg<kD, kMT>::kThreads, PmCfg<kD, kMT>::kCta
   }
   ptx::griddep_wait();
   __syncthreads();
-  const PagedSpan sp = paged_span(a, C::kRT, kPmKeys, 1, s_red);
+  const PagedSpan sp = paged_span(a, C::kRT, kPmKeys, kPmMinTiles, s_red);
   __syncthreads();
   PmWalk w{};
   w.pos = sp.per * blockIdx.x;
@@ -475,21 +477,37 @@ __global__ void __launch_bounds__(PmCfg<kD, kMT>::kThreads, PmCfg<kD, kMT>::kCta
           for (int e = ct; e < rows * quads; e += C::kConsumers) {
             const int rr = e / quads, ch = e % quads, i = (r0 + rr) / a.G, g = (r0 + rr) % a.G;
             if (i >= n_act) continue;
+            // one pass in batches of independent loads, with a running maximum
             float M = -INFINITY, L = 0.f;
-            for (long long cc = c0; cc <= c1; ++cc)
-              M = fmaxf(M, __ldcg(&a.ws_ml[(size_t)unit_slot(cc, sp.per, w.u0) * C::kRT + rr]).x);
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (long long cc = c0; cc <= c1; ++cc) {
-              const size_t row = (size_t)unit_slot(cc, sp.per, w.u0) * C::kRT + rr;
-              const float2 ml = __ldcg(&a.ws_ml[row]);
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(a.ws_o + row * a.D + ch * 4));
-              const float f2 = ml.x == -INFINITY ? 0.f : ptx::ex2(ml.x - M);
-              L = fmaf(f2, ml.y, L);
-              acc.x = fmaf(f2, v.x, acc.x);
-              acc.y = fmaf(f2, v.y, acc.y);
-              acc.z = fmaf(f2, v.z, acc.z);
-              acc.w = fmaf(f2, v.w, acc.w);
+            for (long long cc = c0; cc <= c1; cc += kPmMerge) {
+              float2 ml[kPmMerge];
+              float4 v[kPmMerge];
+#pragma unroll
+              for (int k = 0; k < kPmMerge; ++k) {
+                const size_t row = (size_t)unit_slot(min(cc + k, c1), sp.per, w.u0) * C::kRT + rr;
+                ml[k] = __ldcg(&a.ws_ml[row]);
+                v[k] = __ldcg(reinterpret_cast<const float4*>(a.ws_o + row * a.D + ch * 4));
+                if (cc + k > c1) ml[k].x = -INFINITY;
+              }
+              float Mn = M;
+#pragma unroll
+              for (int k = 0; k < kPmMerge; ++k) Mn = fmaxf(Mn, ml[k].x);
+              if (Mn == -INFINITY) continue;
+              const float f0 = ptx::ex2(M - Mn);
+              M = Mn;
+              L *= f0;
+              acc.x *= f0, acc.y *= f0, acc.z *= f0, acc.w *= f0;
+#pragma unroll
+              for (int k = 0; k < kPmMerge; ++k) {
+                if (ml[k].x == -INFINITY) continue;
+                const float f2 = ptx::ex2(ml[k].x - M);
+                L = fmaf(f2, ml[k].y, L);
+                acc.x = fmaf(f2, v[k].x, acc.x);
+                acc.y = fmaf(f2, v[k].y, acc.y);
+                acc.z = fmaf(f2, v[k].z, acc.z);
+                acc.w = fmaf(f2, v[k].w, acc.w);
+              }
             }
             const float inv = 1.f / L;
             *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) +

@@ -20,6 +20,7 @@ namespace tv {
 
 constexpr int kPsWarps = 8;
 constexpr int kPsKeys = 32;
+constexpr int kPsMerge = 4;  // parts whose loads are in flight together
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_addr(dst)), "l"(src) : "memory");
@@ -258,19 +259,38 @@ __global__ void __launch_bounds__(kPsWarps * 32, kDPL <= 4 ? 2 : 1) paged_simt_k
         for (int rr = warp; rr < rows; rr += kPsWarps) {
           const int r = rt * kRT + rr, i = r / a.G, g = r % a.G;
           if (i >= n_act) continue;
-          float M = -INFINITY;
-          for (long long cc = c0; cc <= c1; ++cc)
-            M = fmaxf(M, __ldcg(&a.ws_ml[(size_t)unit_slot(cc, sp.per, u0) * kRT + rr]).x);
-          float L = 0.f, o[kDPL];
+          // one pass in batches of independent loads, with a running maximum
+          float M = -INFINITY, L = 0.f, o[kDPL];
 #pragma unroll
           for (int u = 0; u < kDPL; ++u) o[u] = 0.f;
-          for (long long cc = c0; cc <= c1; ++cc) {
-            const size_t row = (size_t)unit_slot(cc, sp.per, u0) * kRT + rr;
-            const float2 ml = __ldcg(&a.ws_ml[row]);
-            const float w = ml.x == -INFINITY ? 0.f : expf(ml.x - M);
-            L = fmaf(w, ml.y, L);
+          for (long long cc = c0; cc <= c1; cc += kPsMerge) {
+            float2 ml[kPsMerge];
+            float x[kPsMerge][kDPL];
 #pragma unroll
-            for (int u = 0; u < kDPL; ++u) o[u] = fmaf(w, __ldcg(&a.ws_o[row * kD + lane + 32 * u]), o[u]);
+            for (int k = 0; k < kPsMerge; ++k) {
+              const size_t row = (size_t)unit_slot(min(cc + k, c1), sp.per, u0) * kRT + rr;
+              ml[k] = __ldcg(&a.ws_ml[row]);
+#pragma unroll
+              for (int u = 0; u < kDPL; ++u) x[k][u] = __ldcg(&a.ws_o[row * kD + lane + 32 * u]);
+              if (cc + k > c1) ml[k].x = -INFINITY;
+            }
+            float Mn = M;
+#pragma unroll
+            for (int k = 0; k < kPsMerge; ++k) Mn = fmaxf(Mn, ml[k].x);
+            if (Mn == -INFINITY) continue;
+            const float f0 = expf(M - Mn);
+            M = Mn;
+            L *= f0;
+#pragma unroll
+            for (int u = 0; u < kDPL; ++u) o[u] *= f0;
+#pragma unroll
+            for (int k = 0; k < kPsMerge; ++k) {
+              if (ml[k].x == -INFINITY) continue;
+              const float f = expf(ml[k].x - M);
+              L = fmaf(f, ml[k].y, L);
+#pragma unroll
+              for (int u = 0; u < kDPL; ++u) o[u] = fmaf(f, x[k][u], o[u]);
+            }
           }
           const size_t off = (((size_t)b * a.Hq + hk * a.G + g) * a.N + i) * kD;
 #pragma unroll

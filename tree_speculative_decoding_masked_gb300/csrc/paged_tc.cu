@@ -8,14 +8,18 @@
 // B of one (sequence, KV head) - the G query heads of NT = 128 / G nodes each - and streams a
 // range of 64-key tiles once for both, so a page fetched from L2 serves 256 rows.
 //
-// Pages: the producer's lanes each fetch one box (64 columns x min(page_size, 64) rows) of a
-// tile from the page that their own table entry names, read one tile ahead; 64 keys of 16-row
-// pages are 8 boxes of 2 KB.  Boxes that hold no needed row are not fetched and their table
-// entries not looked at.  V rows outside the needed range (the tail of a sequence's last
-// page, rows behind the window) may hold anything, NaN included, which a zero weight would
-// not remove: the PV issuer's warp zeroes them in shared memory first.
+// Pages: a tile is fetched in boxes of min(page_size, 64) rows, each by a lane of the producer
+// warp from the page that its own table entry names, read ahead.  At D = 128 a box is 5-D
+// (64 columns, 8 rows, 2 column halves, row groups of 8): both halves come in one copy, laid
+// out as 8-row groups of [half][8 rows][128 bytes], whose group stride of 2 KB the products'
+// descriptors carry.  Boxes of 64 columns each would be twice as many, and at 16-row pages
+// the copies' issue, not their bytes, set the pace (590 us for eight 128-node trees over
+// 32768 tokens against 428 at 64-row pages).  Boxes that hold no needed row are not fetched
+// and their table entries not used.  V rows outside the needed range (the tail of a
+// sequence's last page, rows behind the window) may hold anything, NaN included, which a
+// zero weight would not remove: the PV issuer's warp zeroes them in shared memory first.
 //
-// Warps: 0 producer (lanes 0-15 Q and K, 16-31 V), 1 S issuer of tile A and TMEM owner,
+// Warps: 0 producer (V a tile behind K), 1 S issuer of tile A and TMEM owner,
 // 2-9 softmax (four per tile, one row a thread), 10 PV issuer, 11 S issuer of tile B.
 // TMEM columns: S_A[0] 0.., S_A[1] 64.., S_B[0] 128.., S_B[1] 192.., O_A 256.., O_B 384...
 // P_X (bf16, 32 columns) overwrites the first half of its own S buffer.
@@ -45,8 +49,8 @@ struct PtCfg {
   static constexpr int kDB = D / 64;
   static constexpr int kQBlock = kPtRows * 128;      // bytes per 64-column block of one Q tile
   static constexpr int kQTile = kDB * kQBlock;
-  static constexpr int kKVBlock = kPtKeys * 128;     // bytes per 64-column block of a K or V tile
-  static constexpr int kTileBytes = kDB * kKVBlock;
+  static constexpr int kGroup = kDB * 1024;          // a K or V tile's 8-row group: [column block][8][128 bytes]
+  static constexpr int kTileBytes = kPtKeys / 8 * kGroup;
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kOffQ + 2 * kQTile;
   static constexpr int kOffV = kOffK + kPtSlots * kTileBytes;
@@ -79,6 +83,7 @@ struct PtArgs {
   int NT;      // nodes per row tile
   int MP;      // row tile pairs per (sequence, KV head)
   int splits;  // cluster schedule: parts of a pair's keys
+  int wide;    // K and V boxes span both column blocks (5-D maps)
 };
 
 __device__ __forceinline__ float pt_max3(float a, float b, float c) {
@@ -127,10 +132,67 @@ __device__ __forceinline__ void pt_mbar_inval(uint64_t* bar) {
   asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(ptx::smem_addr(bar)) : "memory");
 }
 
+// S of one row tile (K = D in steps of 16) as one asm block: an issuing thread shares its
+// sub-partition with softmax warps, and fewer instructions per product issue the short
+// (N = 64) products sooner.  bd steps 32 bytes inside a 128-byte row, 1 KB to the second
+// column block.
+__device__ __forceinline__ void pt_s_product(uint32_t d, const uint64_t (&ad)[8], uint64_t bd, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p0, p1;\n\t.reg .b32 z;\n\tmov.b32 z, 0;\n\tsetp.ne.b32 p0, z, 0;\n\tsetp.eq.b32 p1, z, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %9, %17, p0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %2, %10, %17, p1;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %3, %11, %17, p1;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %4, %12, %17, p1;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %5, %13, %17, p1;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %6, %14, %17, p1;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %7, %15, %17, p1;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %8, %16, %17, p1;\n\t}" ::"r"(d),
+      "l"(ad[0]), "l"(ad[1]), "l"(ad[2]), "l"(ad[3]), "l"(ad[4]), "l"(ad[5]), "l"(ad[6]), "l"(ad[7]), "l"(bd),
+      "l"(bd + 2), "l"(bd + 4), "l"(bd + 6), "l"(bd + 64), "l"(bd + 66), "l"(bd + 68), "l"(bd + 70), "r"(idesc)
+      : "memory");
+}
+__device__ __forceinline__ void pt_s_product(uint32_t d, const uint64_t (&ad)[4], uint64_t bd, uint32_t idesc) {
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk) ptx::mma_bf16_ss(d, ad[kk], bd + kk * 2, idesc, kk > 0 ? 1u : 0u);
+}
+// O += P V of 64 keys: P from TMEM (8 columns per 16 keys), V rows 16 apart (`step` 16-byte units)
+__device__ __forceinline__ void pt_pv_product(uint32_t d, uint32_t p, uint64_t vd, uint32_t step, uint32_t idesc,
+                                              uint32_t acc0) {
+  asm volatile(
+      "{\n\t.reg .pred p0, p1;\n\t.reg .b32 z;\n\tmov.b32 z, 0;\n\tsetp.ne.b32 p0, %10, 0;\n\tsetp.eq.b32 p1, z, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %5, %9, p0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%2], %6, %9, p1;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%3], %7, %9, p1;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%4], %8, %9, p1;\n\t}" ::"r"(d),
+      "r"(p), "r"(p + 8), "r"(p + 16), "r"(p + 24), "l"(vd), "l"(vd + step), "l"(vd + 2 * step), "l"(vd + 3 * step),
+      "r"(idesc), "r"(acc0)
+      : "memory");
+}
+
 // Wait for this piece's own copies or products even when another wait has run out.
 __device__ __forceinline__ void pt_drain(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   int quiet = 0;
   if (!ptx::mbar_wait(bar, parity, &quiet)) *abort_flag = 1;
+}
+
+__device__ __forceinline__ void pt_bars_init(PtBars* bars) {
+  ptx::mbar_init(&bars->q_full, 1);
+  for (int s = 0; s < kPtSlots; ++s) {
+    ptx::mbar_init(&bars->k_full[s], 1);
+    ptx::mbar_init(&bars->k_empty[s], 2);  // both S issuers
+    ptx::mbar_init(&bars->v_full[s], 1);
+    ptx::mbar_init(&bars->v_empty[s], 1);
+  }
+  for (int x = 0; x < 2; ++x)
+    for (int u = 0; u < 2; ++u) {
+      ptx::mbar_init(&bars->s_full[x][u], 1);
+      ptx::mbar_init(&bars->p_full[x][u], 4);
+      ptx::mbar_init(&bars->pv_done[x][u], 1);
+    }
+  ptx::mbar_init(&bars->o_done, 1);
+  ptx::mbar_init(&bars->s_done[0], 1);
+  ptx::mbar_init(&bars->s_done[1], 1);
+  ptx::fence_mbar_init();
 }
 
 template <int D, bool kCap, bool kStream>
@@ -149,7 +211,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   PtBars* bars = reinterpret_cast<PtBars*>(sm + C::kOffBar);
   volatile int* abort_flag = &bars->abort;
   __shared__ unsigned long long s_red[34];
-  __shared__ int s_first_pad, s_last;
+  __shared__ int s_last;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int NT = pa.NT, rows_used = a.G * NT, RT = 2 * rows_used;
@@ -162,6 +224,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     ptx::prefetch_tmap(&tmK);
     ptx::prefetch_tmap(&tmV);
     bars->abort = 0;
+    pt_bars_init(bars);
   }
   // the Q rows that no box fills
   for (int r = rows_used + threadIdx.x; r < 2 * kPtRows; r += kPtThreads) {
@@ -203,21 +266,22 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       n = n_act = paged_rows(a, b, P, &bad);
       if (bad && threadIdx.x == 0) set_dev_status(a.dev_status, TV_DEV_BAD_PAGE);
       if (a.parent && n > 0) {
-        __syncthreads();
-        if (threadIdx.x == 0) s_first_pad = n;
-        __syncthreads();
+        // rows up to the first padding row (a tree with rows behind it is bad)
         int wrong = 0;
-        for (int t = threadIdx.x; t < n; t += kPtThreads) {
-          const int p = a.parent[(size_t)b * a.N + t];
-          const bool prev_pad = t >= 2 && a.parent[(size_t)b * a.N + t - 1] == -1;
-          const bool ok = t == 0 ? p == -1 : (p == -1 || (p >= 0 && p < t && !prev_pad));
-          if (!ok) wrong = 1;
-          s_par[t] = ok ? p : -1;
-          if (t > 0 && p == -1) atomicMin(&s_first_pad, t);
+        n_act = 1;
+        for (int t0 = 0; t0 < n; t0 += kPtThreads) {
+          const int t = t0 + threadIdx.x;
+          int p = -1;
+          if (t < n) {
+            p = a.parent[(size_t)b * a.N + t];
+            const bool prev_pad = t >= 2 && a.parent[(size_t)b * a.N + t - 1] == -1;
+            const bool ok = t == 0 ? p == -1 : (p == -1 || (p >= 0 && p < t && !prev_pad));
+            if (!ok) wrong = 1;
+            s_par[t] = ok ? p : -1;
+          }
+          n_act += __syncthreads_count(t > 0 && p != -1);
         }
         if (wrong) set_dev_status(a.dev_status, TV_DEV_BAD_TREE);
-        __syncthreads();
-        n_act = s_first_pad;
       }
       loaded_b = b;
     }
@@ -257,49 +321,27 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     }
     const int nt = max(ntx[0], ntx[1]);
 
-    // ---- barriers of this piece
-    if (threadIdx.x == 0) {
-      if (!first_piece) {
+    if (!first_piece) {  // the first one's barriers are ready
+      if (threadIdx.x == 0) {
         uint64_t* w = &bars->q_full;
         for (int k = 0; k < kPtBarWords; ++k) pt_mbar_inval(w + k);
+        pt_bars_init(bars);
       }
-      ptx::mbar_init(&bars->q_full, 1);
-      for (int s = 0; s < kPtSlots; ++s) {
-        ptx::mbar_init(&bars->k_full[s], 1);
-        ptx::mbar_init(&bars->k_empty[s], 2);  // both S issuers
-        ptx::mbar_init(&bars->v_full[s], 1);
-        ptx::mbar_init(&bars->v_empty[s], 1);
-      }
-      for (int x = 0; x < 2; ++x)
-        for (int u = 0; u < 2; ++u) {
-          ptx::mbar_init(&bars->s_full[x][u], 1);
-          ptx::mbar_init(&bars->p_full[x][u], 4);
-          ptx::mbar_init(&bars->pv_done[x][u], 1);
-        }
-      ptx::mbar_init(&bars->o_done, 1);
-      ptx::mbar_init(&bars->s_done[0], 1);
-      ptx::mbar_init(&bars->s_done[1], 1);
-      ptx::fence_mbar_init();
+      __syncthreads();
     }
     first_piece = false;
-    __syncthreads();
 
     float m_run = -INFINITY, l_run = 0.f;
     bool have_o = false;
     if (warp == 0) {
       // ---------------------------------------------------------------- producer
-      // lanes 0-15 load Q and K, lanes 16-31 V; a lane's box is column block db of page piece pi
-      const bool is_v = lane >= 16;
-      const uint32_t half = is_v ? 0xffff0000u : 0x0000ffffu;
-      const int l16 = lane & 15;
-      const int box_shift = min(a.page_shift, 6);  // box rows: min(page_size, 64)
-      const int db = l16 % C::kDB, pi = l16 / C::kDB;
+      // lane: row piece pi of a tile (and, without 5-D boxes, its column block db)
+      const int per_piece = pa.wide ? 1 : C::kDB;
+      const int box_shift = min(a.page_shift, C::kDB == 1 || pa.wide ? 6 : 3);
+      const int db = lane % per_piece, pi = lane / per_piece;
       const bool in_tile = (pi << box_shift) < kPtKeys;
-      const uint32_t box_bytes = 128u << box_shift;
+      const uint32_t box_bytes = (uint32_t)(128 * C::kDB / per_piece) << box_shift;
       const int32_t* table = a.table + (size_t)b * a.max_pages;
-      unsigned char* ring = is_v ? sV : sK;
-      uint64_t* full = is_v ? bars->v_full : bars->k_full;
-      uint64_t* empty = is_v ? bars->v_empty : bars->k_empty;
       // page of this lane's box in tile t, -1 where the box holds no needed row (or a bad page)
       auto lookup = [&](int t) -> int {
         const int j = (t_begin + t) * kPtKeys + (pi << box_shift);
@@ -311,7 +353,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         }
         return page;
       };
-      int page = lookup(0);
+      int page = lookup(0), next = lookup(1), before = -1;
       if (lane == 0 && nt > 0) {
         uint32_t qbytes = 0;
 #pragma unroll
@@ -327,45 +369,47 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                                  b * a.Hq + hk * a.G + g);
       }
       __syncwarp();
-      int issued = 0;
-      if (!is_v) {
-        for (int t = 0; t < nt; ++t) {
-          const int slot = t % kPtSlots;
-          bool ok = true;
-          if (t >= kPtSlots) ok = ptx::mbar_wait(&empty[slot], ((t / kPtSlots) - 1) & 1, abort_flag);
-          if (!__all_sync(half, ok)) break;
-          const uint32_t boxes = __ballot_sync(half, page >= 0);
-          if (l16 == 0) ptx::mbar_arrive_expect_tx(&full[slot], __popc(boxes) * box_bytes);
-          __syncwarp(half);
-          if (page >= 0)
-            ptx::tma_load_3d(ring + slot * C::kTileBytes + db * C::kKVBlock + (pi << box_shift) * 128, &tmK, &full[slot],
-                             db * 64, ((t_begin + t) * kPtKeys + (pi << box_shift)) & ((1 << a.page_shift) - 1),
-                             page * a.Hkv + hk);
-          issued = t + 1;
-          page = lookup(t + 1);
+      // this lane's box of tile t into ring slot t % kPtSlots; false after an abort
+      auto fetch = [&](unsigned char* ring, const CUtensorMap* tm, uint64_t* full, uint64_t* empty, int t,
+                       int pg) -> bool {
+        const int slot = t % kPtSlots;
+        bool ok = true;
+        if (t >= kPtSlots) ok = ptx::mbar_wait(&empty[slot], ((t / kPtSlots) - 1) & 1, abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        const uint32_t boxes = __ballot_sync(0xffffffffu, pg >= 0);
+        if (lane == 0) ptx::mbar_arrive_expect_tx(&full[slot], __popc(boxes) * box_bytes);
+        __syncwarp();
+        if (pg >= 0) {
+          const int row = ((t_begin + t) * kPtKeys + (pi << box_shift)) & ((1 << a.page_shift) - 1);
+          unsigned char* dst = ring + slot * C::kTileBytes + ((pi << box_shift) >> 3) * C::kGroup + db * 1024;
+          if (C::kDB > 1 && pa.wide)
+            ptx::tma_load_5d(dst, tm, &full[slot], 0, 0, 0, row >> 3, pg * a.Hkv + hk);
+          else
+            ptx::tma_load_3d(dst, tm, &full[slot], db * 64, row, pg * a.Hkv + hk);
         }
-      } else {
-        for (int t = 0; t < nt; ++t) {
-          const int slot = t % kPtSlots;
-          bool ok = true;
-          if (t >= kPtSlots) ok = ptx::mbar_wait(&empty[slot], ((t / kPtSlots) - 1) & 1, abort_flag);
-          if (!__all_sync(half, ok)) break;
-          const uint32_t boxes = __ballot_sync(half, page >= 0);
-          if (l16 == 0) ptx::mbar_arrive_expect_tx(&full[slot], __popc(boxes) * box_bytes);
-          __syncwarp(half);
-          if (page >= 0)
-            ptx::tma_load_3d(ring + slot * C::kTileBytes + db * C::kKVBlock + (pi << box_shift) * 128, &tmV, &full[slot],
-                             db * 64, ((t_begin + t) * kPtKeys + (pi << box_shift)) & ((1 << a.page_shift) - 1),
-                             page * a.Hkv + hk);
-          issued = t + 1;
-          page = lookup(t + 1);
+        return true;
+      };
+      int k_issued = 0, v_issued = 0;
+      for (int t = 0; t <= nt && nt > 0; ++t) {
+        if (t < nt) {
+          if (!fetch(sK, &tmK, bars->k_full, bars->k_empty, t, page)) break;
+          k_issued = t + 1;
         }
+        if (t > 0) {
+          if (!fetch(sV, &tmV, bars->v_full, bars->v_empty, t - 1, before)) break;
+          v_issued = t;
+        }
+        before = page;
+        page = next;
+        next = lookup(t + 2);
       }
       // never leave the piece with copies in flight
-      if (l16 == 0) {
-        if (!is_v && nt > 0) pt_drain(&bars->q_full, 0, abort_flag);
-        for (int s = 0; s < kPtSlots && s < issued; ++s)
-          pt_drain(&full[s], ((issued - 1 - s) / kPtSlots) & 1, abort_flag);
+      if (lane == 0) {
+        if (nt > 0) pt_drain(&bars->q_full, 0, abort_flag);
+        for (int s = 0; s < kPtSlots; ++s) {
+          if (s < k_issued) pt_drain(&bars->k_full[s], ((k_issued - 1 - s) / kPtSlots) & 1, abort_flag);
+          if (s < v_issued) pt_drain(&bars->v_full[s], ((v_issued - 1 - s) / kPtSlots) & 1, abort_flag);
+        }
       }
       __syncwarp();
     } else if (warp == 1 || warp == 11) {
@@ -386,11 +430,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
               // S_X(t) overwrites P_X(t - 2) in this buffer
               if (t >= 2 && !ptx::mbar_wait(&bars->pv_done[x][buf], ((t - 2) >> 1) & 1, abort_flag)) break;
               ptx::tc_fence_after();
-              const uint64_t bd = ptx::sdesc_sw128(ptx::smem_addr(sK + ks * C::kTileBytes), 16, 1024);
-#pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk)  // 32 bytes a K step, 8 KB to the second column block
-                ptx::mma_bf16_ss(tmem + x * kPtRows + buf * kPtKeys, adq[kk], bd + (kk >> 2) * 512 + (kk & 3) * 2, idS,
-                                 kk > 0 ? 1u : 0u);
+              pt_s_product(tmem + x * kPtRows + buf * kPtKeys, adq,
+                           ptx::sdesc_sw128(ptx::smem_addr(sK + ks * C::kTileBytes), 16, C::kGroup), idS);
               ptx::mma_commit(&bars->s_full[x][buf]);
             }
             ptx::mma_commit(&bars->k_empty[ks]);
@@ -414,7 +455,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
           for (int r = lane; r < kPtKeys; r += 32)
             if (j0 + r < lo || j0 + r >= key_end)
               for (int db = 0; db < C::kDB; ++db) {
-                uint4* row = reinterpret_cast<uint4*>(sV + vs * C::kTileBytes + db * C::kKVBlock + r * 128);
+                uint4* row =
+                    reinterpret_cast<uint4*>(sV + vs * C::kTileBytes + (r >> 3) * C::kGroup + db * 1024 + (r & 7) * 128);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) row[k] = make_uint4(0, 0, 0, 0);
               }
@@ -423,7 +465,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         }
         if (lane == 0) {
           ok = ptx::mbar_wait(&bars->v_full[vs], (t / kPtSlots) & 1, abort_flag);
-          const uint64_t vd = ptx::sdesc_sw128(ptx::smem_addr(sV + vs * C::kTileBytes), C::kKVBlock, 1024);
+          const uint64_t vd = ptx::sdesc_sw128(ptx::smem_addr(sV + vs * C::kTileBytes), 1024, C::kGroup);
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             if (t >= ntx[x] || !ok) continue;
@@ -431,10 +473,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             if (!ok) continue;
             ptx::tc_fence_after();
             const uint32_t pcol = tmem + x * kPtRows + buf * kPtKeys;  // P: 8 columns per 16 keys
-#pragma unroll
-            for (int kk = 0; kk < kPtKeys / 16; ++kk)
-              ptx::mma_bf16_ts(tmem + C::kColO + x * kPtRows, pcol + kk * 8, vd + kk * 128, idO,
-                               (t > 0 || kk > 0) ? 1u : 0u);
+            pt_pv_product(tmem + C::kColO + x * kPtRows, pcol, vd, 2 * C::kGroup / 16, idO, t > 0 ? 1u : 0u);
             ptx::mma_commit(&bars->pv_done[x][buf]);
           }
           if (ok) ptx::mma_commit(&bars->v_empty[vs]);
@@ -737,7 +776,8 @@ typedef CUresult (*PtEncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, vo
                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-bool paged_tmap(CUtensorMap* m, const void* base, int D, int rows, long long planes, int box_rows) {
+static bool pt_encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                      const cuuint32_t* box) {
   static std::atomic<PtEncodeFn> known{nullptr};
   PtEncodeFn fn = known.load(std::memory_order_relaxed);
   if (!fn) {
@@ -749,13 +789,25 @@ bool paged_tmap(CUtensorMap* m, const void* base, int D, int rows, long long pla
     fn = reinterpret_cast<PtEncodeFn>(p);
     known.store(fn, std::memory_order_relaxed);
   }
+  const cuuint32_t step[5] = {1, 1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool paged_tmap(CUtensorMap* m, const void* base, int D, int rows, long long planes, int box_rows) {
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)rows, (cuuint64_t)planes};
   const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)rows * D * 2};
   const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
-  const cuuint32_t step[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, step,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return pt_encode(m, base, 3, dims, strides, box);
+}
+
+// pages of D = 128 as {64 columns, 8 rows, 2 column blocks, row groups, planes}
+static bool pt_tmap_wide(CUtensorMap* m, const void* base, int rows, long long planes, int box_rows) {
+  const cuuint64_t dims[5] = {64, 8, 2, (cuuint64_t)rows / 8, (cuuint64_t)planes};
+  const cuuint64_t strides[4] = {256, 128, 2048, (cuuint64_t)rows * 256};
+  const cuuint32_t box[5] = {64, 8, 2, (cuuint32_t)box_rows / 8, 1};
+  return pt_encode(m, base, 5, dims, strides, box);
 }
 
 struct PtPlan {
@@ -793,7 +845,7 @@ static cudaError_t launch_pt(const CUtensorMap& mq, const CUtensorMap& mk, const
   cudaError_t e = cudaFuncSetAttribute(paged_tc_kernel<D, kCap, kStream>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        smem);
   if (e != cudaSuccess) return e;
-  const PtArgs pa{p.NT, p.MP, p.splits};
+  const PtArgs pa{p.NT, p.MP, p.splits, a.D == 128};
   if (kStream)
     return launch_pdl(paged_tc_kernel<D, kCap, kStream>, dim3((unsigned)paged_grid_sms()), dim3(kPtThreads), smem, stream,
                       nullptr, 0, mq, mk, mv, a, pa);
@@ -813,11 +865,15 @@ cudaError_t launch_paged_tc(PagedAttn a, char* ws, cudaStream_t stream) {
   a.ws_ml = reinterpret_cast<float2*>(ws + kPagedCntBytes);
   a.ws_o = reinterpret_cast<float*>(ws + kPagedCntBytes + slots * 2 * kPtRows * 8);
   const int ps = 1 << a.page_shift, box = min(ps, kPtKeys);
+  const long long planes = (long long)a.num_pages * a.Hkv;
   CUtensorMap mq, mk, mv;
-  if (!paged_tmap(&mq, a.q, a.D, a.N, (long long)a.B * a.Hq, p.NT) ||
-      !paged_tmap(&mk, a.k, a.D, ps, (long long)a.num_pages * a.Hkv, box) ||
-      !paged_tmap(&mv, a.v, a.D, ps, (long long)a.num_pages * a.Hkv, box))
-    return cudaErrorInvalidValue;
+  bool ok = paged_tmap(&mq, a.q, a.D, a.N, (long long)a.B * a.Hq, p.NT);
+  if (a.D == 128)
+    ok = ok && pt_tmap_wide(&mk, a.k, ps, planes, box) && pt_tmap_wide(&mv, a.v, ps, planes, box);
+  else  // 64 < D < 128: the second block is narrower, so a box is one 8-row group of a block
+    ok = ok && paged_tmap(&mk, a.k, a.D, ps, planes, a.D <= 64 ? box : 8) &&
+         paged_tmap(&mv, a.v, a.D, ps, planes, a.D <= 64 ? box : 8);
+  if (!ok) return cudaErrorInvalidValue;
   const bool cap = a.cap > 0.f, str = p.splits == 0;
   if (a.D <= 64) {
     if (cap) return str ? launch_pt<64, true, true>(mq, mk, mv, a, p, stream)
