@@ -166,6 +166,13 @@ PERSISTENT = [
     (10, 32, 8, 128, 16, [0, 900, 5, 64, 63, 300, 1, 128, 17, 250], 20),
     (2, 32, 8, 128, 32, [3, 200], 300),
     (100, 3, 1, 96, 8, [(37 * b) % 90 for b in range(100)], 12),
+    # few rows a head: 8, 16, 24 and 32 of them, and heads of 256
+    (40, 16, 4, 128, 16, [(211 * b) % 1500 for b in range(40)], 2),
+    (40, 16, 4, 128, 16, [(211 * b) % 1500 for b in range(40)], 4),
+    (40, 16, 4, 64, 32, [(211 * b) % 1500 for b in range(40)], 6),
+    (20, 32, 8, 128, 64, [(211 * b) % 900 for b in range(20)], 8),
+    (20, 16, 8, 256, 16, [(211 * b) % 900 for b in range(20)], 4),
+    (20, 16, 8, 256, 16, [(211 * b) % 900 for b in range(20)], 9),
 ]
 
 

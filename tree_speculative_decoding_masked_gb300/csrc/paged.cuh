@@ -129,18 +129,20 @@ __device__ __forceinline__ float soft_tanh(float x) {
 constexpr int kPagedMaxSms = 160;  // sizes the workspaces
 constexpr int kPagedMaxCtas = 2;   // CTAs per SM of the largest persistent grid
 constexpr size_t kPagedCntBytes = kPagedMaxCtas * kPagedMaxSms * 4;
-constexpr int kPagedFewRows = 32;  // query rows of a KV head above which row tiles are used (bf16)
+constexpr int kPagedFewRows = 16;  // query rows of a KV head above which row tiles are used (bf16)
 
 int paged_device_sms();
 int paged_grid_sms();  // less where tv_set_sm_partition says so
 bool paged_tc_takes(int Hq, int Hkv, int D, int N);
 size_t paged_tc_ws(int B, int Hq, int Hkv, int D, int N);
 cudaError_t launch_paged_tc(PagedAttn a, char* ws, cudaStream_t stream);
-size_t paged_mma_ws(int Hq, int Hkv, int D, int N);
+size_t paged_mma_ws(int B, int Hq, int Hkv, int D, int N);
 cudaError_t launch_paged_mma(PagedAttn a, char* ws, cudaStream_t stream);
 size_t paged_simt_ws(int D);
 cudaError_t launch_paged_simt(PagedAttn a, char* ws, cudaStream_t stream);
-// bf16 rows [planes][rows][D] as boxes of 64 columns x box_rows, 128-byte swizzle
-bool paged_tmap(CUtensorMap* m, const void* base, int D, int rows, long long planes, int box_rows);
+// Tensor map of bf16 pages, 128-byte swizzle.  D = 128 and 256: 5-D, a box spans all column
+// blocks and min(page_size, 64) rows, as 8-row groups [block][8][128 bytes].  Other D: 3-D boxes
+// of one column block, of min(page_size, 64) rows (D <= 64) or 8.
+bool paged_kv_tmap(CUtensorMap* m, const void* base, const PagedAttn& a);
 
 }  // namespace tv

@@ -24,9 +24,10 @@
 // TMEM columns: S_A[0] 0.., S_A[1] 64.., S_B[0] 128.., S_B[1] 192.., O_A 256.., O_B 384...
 // P_X (bf16, 32 columns) overwrites the first half of its own S buffer.
 //
-// Two schedules.  Where the row tile pairs are fewer than half the SMs, each pair's keys are
-// cut into equal parts that run as one thread-block cluster and merge through distributed
-// shared memory.  Otherwise a persistent grid of one CTA per SM divides all pairs' 64-key
+// Two schedules.  Where clusters of two or more CTAs hold all row tiles (or pairs) at once, each
+// one's keys are cut into equal parts that run as one thread-block cluster and merge
+// through distributed shared memory; a CTA with one tile has half the partial rows to park
+// and merge, which costs a short range more than K and V read twice.  Otherwise a persistent grid of one CTA per SM divides all pairs' 64-key
 // steps equally (paged.cuh), which keeps ragged batches and causal triangles balanced; a
 // pair cut between CTAs is merged through the workspace, in CTA order, by the CTA that
 // finishes last.
@@ -81,7 +82,8 @@ constexpr int kPtBarWords = 1 + 4 * kPtSlots + 12 + 3;
 
 struct PtArgs {
   int NT;      // nodes per row tile
-  int MP;      // row tile pairs per (sequence, KV head)
+  int tiles;   // row tiles per unit: 2, or 1 (cluster schedule of few tiles)
+  int MP;      // units per (sequence, KV head)
   int splits;  // cluster schedule: parts of a pair's keys
   int wide;    // K and V boxes span both column blocks (5-D maps)
 };
@@ -214,7 +216,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   __shared__ int s_last;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int NT = pa.NT, rows_used = a.G * NT, RT = 2 * rows_used;
+  const int NT = pa.NT, rows_used = a.G * NT, RT = pa.tiles * rows_used;
   if (warp == 1) {
     ptx::tmem_alloc(&bars->tmem_base, 512);
     ptx::tmem_relinquish();
@@ -261,6 +263,13 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   bool first_piece = true;
   while (kStream ? pos < end && b < a.B : first_piece) {
     if (b != loaded_b) {
+      // the first pass's tree rows are read beside the lengths, not after them
+      const int t_first = min((int)threadIdx.x, a.N - 1);
+      int p_first = -1, p_before = -1;
+      if (a.parent) {
+        p_first = a.parent[(size_t)b * a.N + t_first];
+        if (t_first > 0) p_before = a.parent[(size_t)b * a.N + t_first - 1];
+      }
       P = a.prefix_len[b];
       bool bad = false;
       n = n_act = paged_rows(a, b, P, &bad);
@@ -273,8 +282,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
           const int t = t0 + threadIdx.x;
           int p = -1;
           if (t < n) {
-            p = a.parent[(size_t)b * a.N + t];
-            const bool prev_pad = t >= 2 && a.parent[(size_t)b * a.N + t - 1] == -1;
+            p = t0 == 0 ? p_first : a.parent[(size_t)b * a.N + t];
+            const bool prev_pad = t >= 2 && (t0 == 0 ? p_before : a.parent[(size_t)b * a.N + t - 1]) == -1;
             const bool ok = t == 0 ? p == -1 : (p == -1 || (p >= 0 && p < t && !prev_pad));
             if (!ok) wrong = 1;
             s_par[t] = ok ? p : -1;
@@ -295,7 +304,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       u0 = base;
       base += T_u;
       if (pos >= base) {  // not this one
-        if (++mp * 2 * NT >= n) {
+        if (++mp * pa.tiles * NT >= n) {
           mp = 0;
           if (++hk >= a.Hkv) hk = 0, ++b;
         }
@@ -306,17 +315,17 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       pos += nt_all;
     } else {
       split = blockIdx.x % pa.splits;
-      const int tps = (T_u + pa.splits - 1) / pa.splits;
-      t_begin += split * tps;
-      nt_all = max(0, min(tps, T_u - split * tps));
+      const int first = (int)((long long)T_u * split / pa.splits);
+      t_begin += first;
+      nt_all = (int)((long long)T_u * (split + 1) / pa.splits) - first;
     }
     if (*abort_flag) nt_all = 0;  // a wait ran out: nothing more is computed, but cut units still count their parts
     const int key_end = P + n_act;  // rows from here on, and before lo, may hold anything
     int i0[2], ntx[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      i0[x] = (2 * mp + x) * NT;
-      const int hi = i0[x] < n_act ? P + min(n_act, i0[x] + NT) : 0;
+      i0[x] = (pa.tiles * mp + x) * NT;
+      const int hi = x < pa.tiles && i0[x] < n_act ? P + min(n_act, i0[x] + NT) : 0;
       ntx[x] = max(0, min(nt_all, (hi + kPtKeys - 1) / kPtKeys - t_begin));
     }
     const int nt = max(ntx[0], ntx[1]);
@@ -342,18 +351,22 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       const bool in_tile = (pi << box_shift) < kPtKeys;
       const uint32_t box_bytes = (uint32_t)(128 * C::kDB / per_piece) << box_shift;
       const int32_t* table = a.table + (size_t)b * a.max_pages;
-      // page of this lane's box in tile t, -1 where the box holds no needed row (or a bad page)
-      auto lookup = [&](int t) -> int {
+      // whether this lane's box in tile t holds a needed row, and its table entry (read two tiles
+      // ahead, checked when it is used)
+      auto needed = [&](int t) -> bool {
         const int j = (t_begin + t) * kPtKeys + (pi << box_shift);
-        if (t >= nt || !in_tile || j >= key_end || j + (1 << box_shift) <= lo) return -1;
-        const int page = table[j >> a.page_shift];
-        if (page < 0 || page >= a.num_pages) {
-          set_dev_status(a.dev_status, TV_DEV_BAD_PAGE);
-          return -1;
-        }
-        return page;
+        return t < nt && in_tile && j < key_end && j + (1 << box_shift) > lo;
       };
-      int page = lookup(0), next = lookup(1), before = -1;
+      auto entry = [&](int t) -> int {
+        return needed(t) ? __ldg(table + (((t_begin + t) * kPtKeys + (pi << box_shift)) >> a.page_shift)) : 0;
+      };
+      auto checked = [&](int t, int page) -> int {
+        if (!needed(t)) return -1;
+        if (page >= 0 && page < a.num_pages) return page;
+        set_dev_status(a.dev_status, TV_DEV_BAD_PAGE);
+        return -1;
+      };
+      int raw0 = entry(0), raw1 = entry(1), before = -1;
       if (lane == 0 && nt > 0) {
         uint32_t qbytes = 0;
 #pragma unroll
@@ -391,6 +404,9 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       };
       int k_issued = 0, v_issued = 0;
       for (int t = 0; t <= nt && nt > 0; ++t) {
+        const int page = checked(t, raw0);
+        raw0 = raw1;
+        raw1 = entry(t + 2);
         if (t < nt) {
           if (!fetch(sK, &tmK, bars->k_full, bars->k_empty, t, page)) break;
           k_issued = t + 1;
@@ -400,8 +416,6 @@ __global__ void __launch_bounds__(kPtThreads, 1)
           v_issued = t;
         }
         before = page;
-        page = next;
-        next = lookup(t + 2);
       }
       // never leave the piece with copies in flight
       if (lane == 0) {
@@ -492,7 +506,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       const int q4 = warp & 3;
       const int r = q4 * 32 + lane;
       const int g = r / NT, node = i0[x] + r % NT;
-      const bool valid = r < rows_used && node < n_act;
+      const bool valid = x < pa.tiles && r < rows_used && node < n_act;
       const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
       const uint32_t colS = tmem + lane_base + x * kPtRows;
       const uint32_t colO = tmem + lane_base + C::kColO + x * kPtRows;
@@ -606,6 +620,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                                        : nullptr;
 #pragma unroll
       for (int c0 = 0; c0 < D; c0 += 32) {
+        if (x >= pa.tiles) break;
         float ov[32];
         if (have_o) {
           ptx::tmem_ld32(colO + c0, ov);
@@ -708,7 +723,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         }
       }
       // the next unit
-      if (++mp * 2 * NT >= n) {
+      if (++mp * pa.tiles * NT >= n) {
         mp = 0;
         if (++hk >= a.Hkv) hk = 0, ++b;
       }
@@ -717,44 +732,53 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       // all parts' shared memory, and nobody leaves before every peer has read
       ptx::cluster_sync();
       const int S = pa.splits;
-      const int share = (2 * kPtRows + S - 1) / S;
-      const int r0 = split * share, r1 = min(2 * kPtRows, r0 + share);
+      const int share = (pa.tiles * kPtRows + S - 1) / S;
+      const int r0 = split * share, r1 = min(pa.tiles * kPtRows, r0 + share);
       constexpr int kChunks = D / 4;
       const uint32_t part_local = ptx::smem_addr(sK), ml_local = ptx::smem_addr(sQ);
-      for (int item = threadIdx.x; item < max(0, r1 - r0) * kChunks; item += kPtThreads) {
-        const int R = r0 + item / kChunks, ch = item % kChunks;
-        const int x = R >= kPtRows ? 1 : 0, r = R - x * kPtRows;
-        const int g = r / NT, node = i0[x] + r % NT;
-        if (r >= rows_used || node >= n_act || ch * 4 >= a.D) continue;
-        float2 mlv[kPtMaxSplits];
-        float4 xv[kPtMaxSplits];
-        const uint32_t xoff = (uint32_t)(R * D * 4 + ((ch ^ (R & 7)) << 4));
+      const int items = max(0, r1 - r0) * kChunks;
+      for (int item0 = threadIdx.x; item0 < items; item0 += 2 * kPtThreads) {
+        // two items' loads in flight together
+        float2 mlv[2][kPtMaxSplits];
+        float4 xv[2][kPtMaxSplits];
 #pragma unroll
-        for (int s2 = 0; s2 < kPtMaxSplits; ++s2)
-          if (s2 < S) {
-            mlv[s2] = ptx::ld_cluster_f32x2(ptx::map_cluster(ml_local, s2) + R * 8);
-            xv[s2] = ptx::ld_cluster_f32x4(ptx::map_cluster(part_local, s2) + xoff);
-          }
-        float M = -INFINITY;
+        for (int u = 0; u < 2; ++u) {
+          const int item = min(item0 + u * kPtThreads, items - 1), R = r0 + item / kChunks, ch = item % kChunks;
+          const uint32_t xoff = (uint32_t)(R * D * 4 + ((ch ^ (R & 7)) << 4));
 #pragma unroll
-        for (int s2 = 0; s2 < kPtMaxSplits; ++s2)
-          if (s2 < S) M = fmaxf(M, mlv[s2].x);
-        float L = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int s2 = 0; s2 < kPtMaxSplits; ++s2)
+            if (s2 < S) {
+              mlv[u][s2] = ptx::ld_cluster_f32x2(ptx::map_cluster(ml_local, s2) + R * 8);
+              xv[u][s2] = ptx::ld_cluster_f32x4(ptx::map_cluster(part_local, s2) + xoff);
+            }
+        }
 #pragma unroll
-        for (int s2 = 0; s2 < kPtMaxSplits; ++s2)
-          if (s2 < S && mlv[s2].x != -INFINITY) {
-            const float w = ptx::ex2(mlv[s2].x - M);
-            L = fmaf(mlv[s2].y, w, L);
-            acc.x = fmaf(w, xv[s2].x, acc.x);
-            acc.y = fmaf(w, xv[s2].y, acc.y);
-            acc.z = fmaf(w, xv[s2].z, acc.z);
-            acc.w = fmaf(w, xv[s2].w, acc.w);
-          }
-        const float inv = L > 0.f ? 1.f / L : 0.f;
-        const size_t o = (((size_t)b * a.Hq + hk * a.G + g) * a.N + node) * a.D + ch * 4;
-        *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + o) =
-            make_uint2(ptx::cvt_bf16x2(acc.x * inv, acc.y * inv), ptx::cvt_bf16x2(acc.z * inv, acc.w * inv));
+        for (int u = 0; u < 2; ++u) {
+          const int item = item0 + u * kPtThreads, R = r0 + item / kChunks, ch = item % kChunks;
+          const int x = R >= kPtRows ? 1 : 0, r = R - x * kPtRows;
+          const int g = r / NT, node = i0[x] + r % NT;
+          if (item >= items || r >= rows_used || node >= n_act || ch * 4 >= a.D) continue;
+          float M = -INFINITY;
+#pragma unroll
+          for (int s2 = 0; s2 < kPtMaxSplits; ++s2)
+            if (s2 < S) M = fmaxf(M, mlv[u][s2].x);
+          float L = 0.f;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int s2 = 0; s2 < kPtMaxSplits; ++s2)
+            if (s2 < S && mlv[u][s2].x != -INFINITY) {
+              const float w = ptx::ex2(mlv[u][s2].x - M);
+              L = fmaf(mlv[u][s2].y, w, L);
+              acc.x = fmaf(w, xv[u][s2].x, acc.x);
+              acc.y = fmaf(w, xv[u][s2].y, acc.y);
+              acc.z = fmaf(w, xv[u][s2].z, acc.z);
+              acc.w = fmaf(w, xv[u][s2].w, acc.w);
+            }
+          const float inv = L > 0.f ? 1.f / L : 0.f;
+          const size_t o = (((size_t)b * a.Hq + hk * a.G + g) * a.N + node) * a.D + ch * 4;
+          *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + o) =
+              make_uint2(ptx::cvt_bf16x2(acc.x * inv, acc.y * inv), ptx::cvt_bf16x2(acc.z * inv, acc.w * inv));
+        }
       }
       __syncwarp();
       ptx::cluster_sync();
@@ -795,35 +819,80 @@ static bool pt_encode(CUtensorMap* m, const void* base, int rank, const cuuint64
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool paged_tmap(CUtensorMap* m, const void* base, int D, int rows, long long planes, int box_rows) {
+// rows [planes][rows][D] as boxes of 64 columns x box_rows
+static bool pt_tmap(CUtensorMap* m, const void* base, int D, int rows, long long planes, int box_rows) {
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)rows, (cuuint64_t)planes};
   const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)rows * D * 2};
   const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
   return pt_encode(m, base, 3, dims, strides, box);
 }
 
-// pages of D = 128 as {64 columns, 8 rows, 2 column blocks, row groups, planes}
-static bool pt_tmap_wide(CUtensorMap* m, const void* base, int rows, long long planes, int box_rows) {
-  const cuuint64_t dims[5] = {64, 8, 2, (cuuint64_t)rows / 8, (cuuint64_t)planes};
-  const cuuint64_t strides[4] = {256, 128, 2048, (cuuint64_t)rows * 256};
-  const cuuint32_t box[5] = {64, 8, 2, (cuuint32_t)box_rows / 8, 1};
-  return pt_encode(m, base, 5, dims, strides, box);
+bool paged_kv_tmap(CUtensorMap* m, const void* base, const PagedAttn& a) {
+  const int ps = 1 << a.page_shift, box = min(ps, 64);
+  const long long planes = (long long)a.num_pages * a.Hkv;
+  if (a.D == 128 || a.D == 256) {
+    // {64 columns, 8 rows, column blocks, row groups, planes}
+    const cuuint64_t blocks = (cuuint64_t)a.D / 64;
+    const cuuint64_t dims[5] = {64, 8, blocks, (cuuint64_t)ps / 8, (cuuint64_t)planes};
+    const cuuint64_t strides[4] = {(cuuint64_t)a.D * 2, 128, (cuuint64_t)a.D * 16, (cuuint64_t)ps * a.D * 2};
+    const cuuint32_t boxes[5] = {64, 8, (cuuint32_t)blocks, (cuuint32_t)box / 8, 1};
+    return pt_encode(m, base, 5, dims, strides, boxes);
+  }
+  // one column block, or a narrower last one: then a box is one 8-row group of a block
+  return pt_tmap(m, base, a.D, ps, planes, a.D <= 64 ? box : 8);
 }
 
 struct PtPlan {
-  int NT, MP, splits;  // splits 0: persistent grid
+  int NT, tiles, MP, splits;  // splits 0: persistent grid
   size_t bytes;        // workspace
 };
+
+// Clusters of s CTAs that can be resident at once on the current device (known per device and s).
+static int pt_clusters(int D, int s) {
+  static std::atomic<int> known[64][kPtMaxSplits + 1];  // count + 1; 0 = not asked yet
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return paged_device_sms() / s;
+  int n = known[dev][s].load(std::memory_order_relaxed) - 1;
+  if (n < 0) {
+    // every instance takes one CTA per SM, so one stands for all
+    const void* fn = reinterpret_cast<const void*>(paged_tc_kernel<128, false, false>);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(s * 64, 1, 1);
+    cfg.blockDim = dim3(kPtThreads, 1, 1);
+    cfg.dynamicSmemBytes = PtCfg<128>::kSmemAlloc;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)s;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, PtCfg<128>::kSmemAlloc) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess)
+      n = paged_device_sms() / s;
+    known[dev][s].store(n + 1, std::memory_order_relaxed);
+  }
+  return n;
+}
 
 static PtPlan pt_plan(int B, int Hq, int Hkv, int D, int N) {
   PtPlan p{};
   const int G = Hq / Hkv;
   p.NT = (kPtRows / G) / 8 * 8;
-  p.MP = (N + 2 * p.NT - 1) / (2 * p.NT);
-  const int sms = paged_device_sms();
-  const long long units = (long long)B * Hkv * p.MP;
-  // up to half as many pairs as SMs: each runs as a cluster of parts that merge on chip
-  if (units * 2 <= sms && B <= 65535 && Hkv <= 65535) p.splits = (int)min((long long)kPtMaxSplits, sms / units);
+  const int sms = paged_device_sms(), row_tiles = (N + p.NT - 1) / p.NT;
+  // the most parts that leave all units resident at once: of single tiles, of pairs
+  auto parts = [&](int tiles) -> int {
+    const long long units = (long long)B * Hkv * ((row_tiles + tiles - 1) / tiles);
+    if (units * 2 > sms || B > 65535 || Hkv > 65535) return 0;
+    for (int s = kPtMaxSplits; s >= 2; --s)
+      if (units <= pt_clusters(D, s)) return s;
+    return 0;
+  };
+  const int one = parts(1), two = parts(2);
+  // a 64-key step takes 1.0 us for a pair and 0.8 for a single tile, whose merge is 2 us shorter
+  p.tiles = one >= 2 && one * 4 >= two * 3 ? 1 : 2;
+  p.splits = p.tiles == 1 ? one : two;
+  p.MP = (row_tiles + p.tiles - 1) / p.tiles;
   if (p.splits == 0) {
     const size_t slots = (size_t)2 * kPagedMaxSms;
     p.bytes = kPagedCntBytes + slots * 2 * kPtRows * 8 + slots * 2 * kPtRows * (D <= 64 ? 64 : 128) * 4;
@@ -845,7 +914,7 @@ static cudaError_t launch_pt(const CUtensorMap& mq, const CUtensorMap& mk, const
   cudaError_t e = cudaFuncSetAttribute(paged_tc_kernel<D, kCap, kStream>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        smem);
   if (e != cudaSuccess) return e;
-  const PtArgs pa{p.NT, p.MP, p.splits, a.D == 128};
+  const PtArgs pa{p.NT, p.tiles, p.MP, p.splits, a.D == 128};
   if (kStream)
     return launch_pdl(paged_tc_kernel<D, kCap, kStream>, dim3((unsigned)paged_grid_sms()), dim3(kPtThreads), smem, stream,
                       nullptr, 0, mq, mk, mv, a, pa);
@@ -864,16 +933,10 @@ cudaError_t launch_paged_tc(PagedAttn a, char* ws, cudaStream_t stream) {
   a.cnt = reinterpret_cast<unsigned*>(ws);
   a.ws_ml = reinterpret_cast<float2*>(ws + kPagedCntBytes);
   a.ws_o = reinterpret_cast<float*>(ws + kPagedCntBytes + slots * 2 * kPtRows * 8);
-  const int ps = 1 << a.page_shift, box = min(ps, kPtKeys);
-  const long long planes = (long long)a.num_pages * a.Hkv;
   CUtensorMap mq, mk, mv;
-  bool ok = paged_tmap(&mq, a.q, a.D, a.N, (long long)a.B * a.Hq, p.NT);
-  if (a.D == 128)
-    ok = ok && pt_tmap_wide(&mk, a.k, ps, planes, box) && pt_tmap_wide(&mv, a.v, ps, planes, box);
-  else  // 64 < D < 128: the second block is narrower, so a box is one 8-row group of a block
-    ok = ok && paged_tmap(&mk, a.k, a.D, ps, planes, a.D <= 64 ? box : 8) &&
-         paged_tmap(&mv, a.v, a.D, ps, planes, a.D <= 64 ? box : 8);
-  if (!ok) return cudaErrorInvalidValue;
+  if (!pt_tmap(&mq, a.q, a.D, a.N, (long long)a.B * a.Hq, p.NT) || !paged_kv_tmap(&mk, a.k, a) ||
+      !paged_kv_tmap(&mv, a.v, a))
+    return cudaErrorInvalidValue;
   const bool cap = a.cap > 0.f, str = p.splits == 0;
   if (a.D <= 64) {
     if (cap) return str ? launch_pt<64, true, true>(mq, mk, mv, a, p, stream)
