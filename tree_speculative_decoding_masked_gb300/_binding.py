@@ -761,7 +761,7 @@ def paged_attention(q, k_cache, v_cache, page_table, prefix_len, *, parent=None,
                      parent=parent, n_rows=n_rows, out=out)
     kv, B, Hkv, ps, width, D = _paged_kv(k_cache, v_cache, page_table, prefix_len)
     _ndim("q", q, 4)
-    Hq, N = q.shape[1], q.shape[2]
+    _, Hq, N, _ = q.shape
     _need("q", q, k_cache.dtype, (B, Hq, N, D))
     code = _dtype_code(q)
     if parent is not None:
@@ -775,7 +775,9 @@ def paged_attention(q, k_cache, v_cache, page_table, prefix_len, *, parent=None,
     st = _status_tensor(dev_status, dev)
     lib = load_library()
     with _on(dev):
-        ws = _workspace(lib.tv_paged_attention_workspace_size(B, Hq, Hkv, D, N, ps, width, code), dev, workspace)
+        # a given workspace's size is checked by the call itself
+        ws = _workspace(0 if workspace is not None else
+                        lib.tv_paged_attention_workspace_size(B, Hq, Hkv, D, N, ps, width, code), dev, workspace)
         _check("tv_paged_attention", lib.tv_paged_attention(
             _ptr(q), _ptr(out), ctypes.byref(kv), _ptr(parent), _ptr(n_rows), B, Hq, Hkv, N, D, float(scale),
             float(softcap), int(window), code, _ptr(ws), ws.numel() * ws.element_size(), _ptr(st), _stream()))

@@ -19,15 +19,15 @@
 // sequence's last page, rows behind the window) may hold anything, NaN included, which a
 // zero weight would not remove: the PV issuer's warp zeroes them in shared memory first.
 //
-// Warps: 0 producer (V a tile behind K), 1 S issuer of tile A and TMEM owner,
+// Warps: 0 producer (V a tile behind K), 1 S issuer of tile A (loads its Q) and TMEM owner,
 // 2-9 softmax (four per tile, one row a thread), 10 PV issuer, 11 S issuer of tile B.
 // TMEM columns: S_A[0] 0.., S_A[1] 64.., S_B[0] 128.., S_B[1] 192.., O_A 256.., O_B 384...
 // P_X (bf16, 32 columns) overwrites the first half of its own S buffer.
 //
 // Two schedules.  Where clusters of two or more CTAs hold all row tiles (or pairs) at once, each
-// one's keys are cut into equal parts that run as one thread-block cluster and merge
-// through distributed shared memory; a CTA with one tile has half the partial rows to park
-// and merge, which costs a short range more than K and V read twice.  Otherwise a persistent grid of one CTA per SM divides all pairs' 64-key
+// one's keys are cut into equal parts that run as one thread-block cluster and merge behind its
+// barrier; a CTA with one tile has half the partial rows to park and merge, which costs a
+// short range more than K and V read twice.  Otherwise a persistent grid of one CTA per SM divides all pairs' 64-key
 // steps equally (paged.cuh), which keeps ragged batches and causal triangles balanced; a
 // pair cut between CTAs is merged through the workspace, in CTA order, by the CTA that
 // finishes last.
@@ -59,13 +59,11 @@ struct PtCfg {
   static constexpr int kOffBar = kOffPar + kMaxNodes * 4;
   static constexpr int kSmemAlloc = kOffBar + 512 + 1024;  // slack for 1024-byte alignment
   static constexpr uint32_t kColO = 256;
-  static_assert(2 * kPtSlots * kTileBytes >= 2 * kPtRows * D * 4, "split partials fit in the drained rings");
-  static_assert(2 * kQTile >= 2 * kPtRows * 8, "(m, l) of both tiles fit in the drained Q tiles");
   static_assert(kSmemAlloc <= 232448, "shared memory per CTA");
 };
 
 struct PtBars {
-  uint64_t q_full;
+  uint64_t q_full[2];
   uint64_t k_full[kPtSlots];
   uint64_t k_empty[kPtSlots];
   uint64_t v_full[kPtSlots];
@@ -78,7 +76,7 @@ struct PtBars {
   uint32_t tmem_base;
   int abort;
 };
-constexpr int kPtBarWords = 1 + 4 * kPtSlots + 12 + 3;
+constexpr int kPtBarWords = 2 + 4 * kPtSlots + 12 + 3;
 
 struct PtArgs {
   int NT;      // nodes per row tile
@@ -178,7 +176,8 @@ __device__ __forceinline__ void pt_drain(uint64_t* bar, uint32_t parity, volatil
 }
 
 __device__ __forceinline__ void pt_bars_init(PtBars* bars) {
-  ptx::mbar_init(&bars->q_full, 1);
+  ptx::mbar_init(&bars->q_full[0], 1);
+  ptx::mbar_init(&bars->q_full[1], 1);
   for (int s = 0; s < kPtSlots; ++s) {
     ptx::mbar_init(&bars->k_full[s], 1);
     ptx::mbar_init(&bars->k_empty[s], 2);  // both S issuers
@@ -250,6 +249,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   PagedSpan sp{};
   long long pos = 0, end = 0, base = 0;
   int b = 0, hk = 0, mp = 0;
+  const size_t cta = ((size_t)blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;  // cluster schedule
   if constexpr (kStream) {
     sp = paged_span(a, RT, kPtKeys, 1, s_red);
     pos = (long long)blockIdx.x * sp.per;
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
 
     if (!first_piece) {  // the first one's barriers are ready
       if (threadIdx.x == 0) {
-        uint64_t* w = &bars->q_full;
+        uint64_t* w = &bars->q_full[0];
         for (int k = 0; k < kPtBarWords; ++k) pt_mbar_inval(w + k);
         pt_bars_init(bars);
       }
@@ -367,21 +367,6 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         return -1;
       };
       int raw0 = entry(0), raw1 = entry(1), before = -1;
-      if (lane == 0 && nt > 0) {
-        uint32_t qbytes = 0;
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-          if (ntx[x] > 0) qbytes += (uint32_t)(rows_used * 128 * C::kDB);
-        ptx::mbar_arrive_expect_tx(&bars->q_full, qbytes);
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-          if (ntx[x] > 0)
-            for (int g = 0; g < a.G; ++g)
-              for (int d = 0; d < C::kDB; ++d)
-                ptx::tma_load_3d(sQ + x * C::kQTile + d * C::kQBlock + g * NT * 128, &tmQ, &bars->q_full, d * 64, i0[x],
-                                 b * a.Hq + hk * a.G + g);
-      }
-      __syncwarp();
       // this lane's box of tile t into ring slot t % kPtSlots; false after an abort
       auto fetch = [&](unsigned char* ring, const CUtensorMap* tm, uint64_t* full, uint64_t* empty, int t,
                        int pg) -> bool {
@@ -419,7 +404,6 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       }
       // never leave the piece with copies in flight
       if (lane == 0) {
-        if (nt > 0) pt_drain(&bars->q_full, 0, abort_flag);
         for (int s = 0; s < kPtSlots; ++s) {
           if (s < k_issued) pt_drain(&bars->k_full[s], ((k_issued - 1 - s) / kPtSlots) & 1, abort_flag);
           if (s < v_issued) pt_drain(&bars->v_full[s], ((v_issued - 1 - s) / kPtSlots) & 1, abort_flag);
@@ -430,7 +414,15 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       // ---------------------------------------------------------------- S issuer of tile x
       const int x = warp == 1 ? 0 : 1;
       if (lane == 0) {
-        if (nt > 0 && ptx::mbar_wait(&bars->q_full, 0, abort_flag)) {
+        if (ntx[x] > 0) {
+          ptx::mbar_arrive_expect_tx(&bars->q_full[x], (uint32_t)(rows_used * 128 * C::kDB));
+          for (int g = 0; g < a.G; ++g)
+            for (int d = 0; d < C::kDB; ++d)
+              ptx::tma_load_3d(sQ + x * C::kQTile + d * C::kQBlock + g * NT * 128, &tmQ, &bars->q_full[x], d * 64, i0[x],
+                               b * a.Hq + hk * a.G + g);
+          pt_drain(&bars->q_full[x], 0, abort_flag);
+        }
+        if (nt > 0) {
           constexpr uint32_t idS = ptx::idesc_bf16(kPtRows, kPtKeys, false, false);
           const uint32_t qaddr = ptx::smem_addr(sQ + x * C::kQTile);
           uint64_t adq[D / 16];
@@ -611,13 +603,12 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         have_o = done && ok && ntm > 0;
         if (done) ptx::tc_fence_after();
       }
-      const bool whole = kStream ? u0 / sp.per == (base - 1) / sp.per : pa.splits == 1;
+      const bool whole = kStream && u0 / sp.per == (base - 1) / sp.per;
       const int R = x * kPtRows + r;
+      const size_t slot = kStream ? (size_t)unit_slot(blockIdx.x, sp.per, u0) : cta;
       const float inv = whole && l_run > 0.f ? 1.f / l_run : 0.f;
       const size_t orow = (((size_t)b * a.Hq + hk * a.G + g) * a.N + node) * a.D;
-      float4* part = kStream && !whole ? reinterpret_cast<float4*>(a.ws_o) +
-                                             (size_t)unit_slot(blockIdx.x, sp.per, u0) * (D / 4) * 2 * kPtRows + R
-                                       : nullptr;
+      float4* part = whole ? nullptr : reinterpret_cast<float4*>(a.ws_o) + slot * (D / 4) * 2 * kPtRows + R;
 #pragma unroll
       for (int c0 = 0; c0 < D; c0 += 32) {
         if (x >= pa.tiles) break;
@@ -639,29 +630,16 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                                   ptx::cvt_bf16x2(ov[8 * k + 4] * inv, ov[8 * k + 5] * inv),
                                   ptx::cvt_bf16x2(ov[8 * k + 6] * inv, ov[8 * k + 7] * inv));
           }
-        } else if constexpr (kStream) {
+        } else {
           // partial O as [D / 4][256 rows] of four columns: a warp stores 512 bytes in a row
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             __stcg(part + (size_t)(c0 / 4 + k) * 2 * kPtRows,
                    make_float4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]));
-        } else {
-          // row-major [256][D] with the 16-byte chunks XOR-swizzled by the row, in the drained rings
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int chunk = c0 / 4 + k;
-            *reinterpret_cast<float4*>(sK + (size_t)R * D * 4 + ((chunk ^ (R & 7)) << 4)) =
-                make_float4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]);
-          }
         }
       }
-      if (!whole) {
-        const float2 ml = make_float2(have_o ? m_run : -INFINITY, have_o ? l_run : 0.f);
-        if constexpr (kStream)
-          __stcg(a.ws_ml + (size_t)unit_slot(blockIdx.x, sp.per, u0) * 2 * kPtRows + R, ml);
-        else
-          reinterpret_cast<float2*>(sQ)[R] = ml;
-      }
+      if (!whole)
+        __stcg(a.ws_ml + slot * 2 * kPtRows + R, make_float2(have_o ? m_run : -INFINITY, have_o ? l_run : 0.f));
       ptx::tc_fence_before();
     }
     __syncwarp();
@@ -727,61 +705,47 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         mp = 0;
         if (++hk >= a.Hkv) hk = 0, ++b;
       }
-    } else if (pa.splits > 1) {
-      // the parts of this pair form one cluster: CTA `split` merges its share of the rows from
-      // all parts' shared memory, and nobody leaves before every peer has read
+    } else {
+      // the parts form one cluster, and each CTA merges its share of the rows.  They meet in L2, not in
+      // distributed shared memory: 64 KB a CTA through a cluster took 2.8 us, stored or read
       ptx::cluster_sync();
       const int S = pa.splits;
       const int share = (pa.tiles * kPtRows + S - 1) / S;
-      const int r0 = split * share, r1 = min(pa.tiles * kPtRows, r0 + share);
-      constexpr int kChunks = D / 4;
-      const uint32_t part_local = ptx::smem_addr(sK), ml_local = ptx::smem_addr(sQ);
-      const int items = max(0, r1 - r0) * kChunks;
-      for (int item0 = threadIdx.x; item0 < items; item0 += 2 * kPtThreads) {
-        // two items' loads in flight together
-        float2 mlv[2][kPtMaxSplits];
-        float4 xv[2][kPtMaxSplits];
+      const int r0 = split * share, rows = min(pa.tiles * kPtRows, r0 + share) - r0;
+      const size_t first = cta - split;
+      for (int item = threadIdx.x; item < rows * (a.D / 4); item += kPtThreads) {
+        const int ch = item / rows, R = r0 + item - ch * rows;
+        const int x = R >= kPtRows ? 1 : 0, r = R - x * kPtRows;
+        const int g = r / NT, node = i0[x] + r % NT;
+        if (r >= rows_used || node >= n_act) continue;
+        float2 mlv[kPtMaxSplits];
+        float4 xv[kPtMaxSplits];
+        float M = -INFINITY, L = 0.f;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int item = min(item0 + u * kPtThreads, items - 1), R = r0 + item / kChunks, ch = item % kChunks;
-          const uint32_t xoff = (uint32_t)(R * D * 4 + ((ch ^ (R & 7)) << 4));
+        for (int s2 = 0; s2 < kPtMaxSplits; ++s2)
+          if (s2 < S) {
+            mlv[s2] = __ldcg(a.ws_ml + (first + s2) * 2 * kPtRows + R);
+            xv[s2] = __ldcg(reinterpret_cast<const float4*>(a.ws_o) + ((first + s2) * (D / 4) + ch) * 2 * kPtRows + R);
+          }
 #pragma unroll
-          for (int s2 = 0; s2 < kPtMaxSplits; ++s2)
-            if (s2 < S) {
-              mlv[u][s2] = ptx::ld_cluster_f32x2(ptx::map_cluster(ml_local, s2) + R * 8);
-              xv[u][s2] = ptx::ld_cluster_f32x4(ptx::map_cluster(part_local, s2) + xoff);
-            }
-        }
+        for (int s2 = 0; s2 < kPtMaxSplits; ++s2)
+          if (s2 < S) M = fmaxf(M, mlv[s2].x);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int item = item0 + u * kPtThreads, R = r0 + item / kChunks, ch = item % kChunks;
-          const int x = R >= kPtRows ? 1 : 0, r = R - x * kPtRows;
-          const int g = r / NT, node = i0[x] + r % NT;
-          if (item >= items || r >= rows_used || node >= n_act || ch * 4 >= a.D) continue;
-          float M = -INFINITY;
-#pragma unroll
-          for (int s2 = 0; s2 < kPtMaxSplits; ++s2)
-            if (s2 < S) M = fmaxf(M, mlv[u][s2].x);
-          float L = 0.f;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int s2 = 0; s2 < kPtMaxSplits; ++s2)
-            if (s2 < S && mlv[u][s2].x != -INFINITY) {
-              const float w = ptx::ex2(mlv[u][s2].x - M);
-              L = fmaf(mlv[u][s2].y, w, L);
-              acc.x = fmaf(w, xv[u][s2].x, acc.x);
-              acc.y = fmaf(w, xv[u][s2].y, acc.y);
-              acc.z = fmaf(w, xv[u][s2].z, acc.z);
-              acc.w = fmaf(w, xv[u][s2].w, acc.w);
-            }
-          const float inv = L > 0.f ? 1.f / L : 0.f;
-          const size_t o = (((size_t)b * a.Hq + hk * a.G + g) * a.N + node) * a.D + ch * 4;
-          *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + o) =
-              make_uint2(ptx::cvt_bf16x2(acc.x * inv, acc.y * inv), ptx::cvt_bf16x2(acc.z * inv, acc.w * inv));
-        }
+        for (int s2 = 0; s2 < kPtMaxSplits; ++s2)
+          if (s2 < S && mlv[s2].x != -INFINITY) {
+            const float w = ptx::ex2(mlv[s2].x - M);
+            L = fmaf(mlv[s2].y, w, L);
+            acc.x = fmaf(w, xv[s2].x, acc.x);
+            acc.y = fmaf(w, xv[s2].y, acc.y);
+            acc.z = fmaf(w, xv[s2].z, acc.z);
+            acc.w = fmaf(w, xv[s2].w, acc.w);
+          }
+        const float inv = L > 0.f ? 1.f / L : 0.f;
+        const size_t o = (((size_t)b * a.Hq + hk * a.G + g) * a.N + node) * a.D + ch * 4;
+        *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + o) =
+            make_uint2(ptx::cvt_bf16x2(acc.x * inv, acc.y * inv), ptx::cvt_bf16x2(acc.z * inv, acc.w * inv));
       }
-      __syncwarp();
-      ptx::cluster_sync();
     }
     __syncthreads();  // every role is done with this piece's barriers, rings and TMEM
     ptx::tc_fence_after();
@@ -844,7 +808,7 @@ bool paged_kv_tmap(CUtensorMap* m, const void* base, const PagedAttn& a) {
 
 struct PtPlan {
   int NT, tiles, MP, splits;  // splits 0: persistent grid
-  size_t bytes;        // workspace
+  size_t slots, bytes;        // workspace: partial results
 };
 
 // Clusters of s CTAs that can be resident at once on the current device (known per device and s).
@@ -893,10 +857,9 @@ static PtPlan pt_plan(int B, int Hq, int Hkv, int D, int N) {
   p.tiles = one >= 2 && one * 4 >= two * 3 ? 1 : 2;
   p.splits = p.tiles == 1 ? one : two;
   p.MP = (row_tiles + p.tiles - 1) / p.tiles;
-  if (p.splits == 0) {
-    const size_t slots = (size_t)2 * kPagedMaxSms;
-    p.bytes = kPagedCntBytes + slots * 2 * kPtRows * 8 + slots * 2 * kPtRows * (D <= 64 ? 64 : 128) * 4;
-  }
+  // one part per CTA of the clusters, two per CTA of the persistent grid
+  p.slots = p.splits ? (size_t)p.splits * p.MP * B * Hkv : (size_t)2 * kPagedMaxSms;
+  p.bytes = kPagedCntBytes + p.slots * 2 * kPtRows * (8 + (D <= 64 ? 64 : 128) * 4);
   return p;
 }
 
@@ -929,10 +892,9 @@ static cudaError_t launch_pt(const CUtensorMap& mq, const CUtensorMap& mk, const
 
 cudaError_t launch_paged_tc(PagedAttn a, char* ws, cudaStream_t stream) {
   const PtPlan p = pt_plan(a.B, a.Hq, a.Hkv, a.D, a.N);
-  const size_t slots = (size_t)2 * kPagedMaxSms;
   a.cnt = reinterpret_cast<unsigned*>(ws);
   a.ws_ml = reinterpret_cast<float2*>(ws + kPagedCntBytes);
-  a.ws_o = reinterpret_cast<float*>(ws + kPagedCntBytes + slots * 2 * kPtRows * 8);
+  a.ws_o = reinterpret_cast<float*>(ws + kPagedCntBytes + p.slots * 2 * kPtRows * 8);
   CUtensorMap mq, mk, mv;
   if (!pt_tmap(&mq, a.q, a.D, a.N, (long long)a.B * a.Hq, p.NT) || !paged_kv_tmap(&mk, a.k, a) ||
       !paged_kv_tmap(&mv, a.v, a))
