@@ -19,6 +19,7 @@ class _Fake:
     def __init__(self, shape, dtype=torch.bfloat16, device="cpu", stride=None, ptr=0x1000):
         self.shape, self.dtype, self.is_cuda, self.device = tuple(shape), dtype, True, torch.device(device)
         dense = [math.prod(shape[i + 1:]) for i in range(len(shape))]
+        self.ndim = len(shape)
         self._stride, self._dense, self._ptr = tuple(stride or dense), tuple(dense), ptr
 
     def is_contiguous(self):
@@ -26,6 +27,9 @@ class _Fake:
 
     def stride(self):
         return self._stride
+
+    def get_device(self):
+        return self.device.index or 0
 
     def data_ptr(self):
         return self._ptr
@@ -39,17 +43,41 @@ class _Fake:
 
 def _rows(data=0x1000, strides=(64, 64, 64)):
     from tree_speculative_decoding_masked_gb300 import _binding as b
-    return ctypes.byref(b._Rows(data, *strides))
+    return b._pack_rows(data or 0, *strides)
 
 
 def _rope(freq=0x1000, rot=64, amp=1.0):
     from tree_speculative_decoding_masked_gb300 import _binding as b
-    return ctypes.byref(b._Rope(freq, rot, 0, amp))
+    return b._pack_rope(freq or 0, rot, 0, amp)
 
 
 def _kv(k=0x1000, v=0x1000, table=0x1000, prefix=0x1000, pages=4, ps=16, width=4):
     from tree_speculative_decoding_masked_gb300 import _binding as b
-    return ctypes.byref(b._PagedKv(k, v, table, prefix, pages, ps, width))
+    return b._pack_paged_kv(k or 0, v or 0, table or 0, prefix or 0, pages, ps, width)
+
+
+def test_packed_structs_have_the_headers_layout(tmp_path):
+    # sizes and offsets of the host structs, asked of the C compiler
+    import os
+    import shutil
+    import struct
+    import subprocess
+    from tree_speculative_decoding_masked_gb300 import _binding as b
+    gcc = shutil.which("gcc")
+    if gcc is None:
+        pytest.skip("gcc not available")
+    src, exe = tmp_path / "s.c", tmp_path / "s"
+    src.write_text('#include <stdio.h>\n#include <stddef.h>\n#include "treeverify.h"\n'
+                   'int main(void) { printf("%zu %zu %zu %zu %zu %zu %zu\\n", sizeof(tv_rope), offsetof(tv_rope, amplitude),\n'
+                   'sizeof(tv_rows), offsetof(tv_rows, row_stride), sizeof(tv_paged_kv), offsetof(tv_paged_kv, prefix_len),\n'
+                   'offsetof(tv_paged_kv, max_pages)); return 0; }\n')
+    inc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include")
+    subprocess.run([gcc, "-I", inc, str(src), "-o", str(exe)], check=True)
+    got = [int(x) for x in subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split()]
+    assert got == [len(_rope()), 16, len(_rows()), 24, len(_kv()), 24, 40]
+    assert struct.unpack_from("@f", _rope(amp=2.5), 16) == (2.5,)
+    assert struct.unpack_from("@q", b._pack_rows(1, 2, 3, 4), 24) == (4,)
+    assert struct.unpack_from("@iii", _kv(pages=5, ps=8, width=7), 32) == (5, 8, 7)
 
 
 def test_frequencies(lib):  # noqa: F811

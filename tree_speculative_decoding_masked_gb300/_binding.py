@@ -12,6 +12,7 @@ import contextlib
 import ctypes
 import math
 import os
+import struct
 
 import torch
 
@@ -44,19 +45,10 @@ _U64 = ctypes.c_uint64
 _D = ctypes.c_double
 
 
-class _Rope(ctypes.Structure):
-    _fields_ = [("freq", _P), ("rot_dim", _I), ("interleaved", _I), ("amplitude", _F)]
-
-
-class _Rows(ctypes.Structure):
-    _fields_ = [("data", _P), ("batch_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
-                ("row_stride", ctypes.c_int64)]
-
-
-class _PagedKv(ctypes.Structure):
-    _fields_ = [("k", _P), ("v", _P), ("page_table", _P), ("prefix_len", _P), ("num_pages", _I), ("page_size", _I),
-                ("max_pages", _I)]
-
+# host structs of the paged calls, packed: tv_rope, tv_rows, tv_paged_kv
+_pack_rope = struct.Struct("@Piif0q").pack
+_pack_rows = struct.Struct("@Pqqq").pack
+_pack_paged_kv = struct.Struct("@PPPPiii0q").pack
 
 _SIGS = {
     "tv_status_string": (ctypes.c_char_p, [_I]),
@@ -637,27 +629,74 @@ def rotary_frequencies(rot_dim: int, base: float = 10000.0, *, scaling=None, dev
     return {"freq": freq.to(device), "amplitude": amp.value, "rot_dim": int(rot_dim)}
 
 
-def _rope_arg(rope, interleaved):
-    freq, rot = rope["freq"], int(rope["rot_dim"])
-    _need("rope['freq']", freq, torch.int64, (rot // 2,))
-    return _Rope(freq.data_ptr(), rot, int(bool(interleaved)), float(rope["amplitude"]))
+# A call's checks are a large part of a small call's time, so they look at each tensor once:
+# the first one names the device, the others go through _tensor.
 
 
-def _rows_arg(name, t, shape, dtype, dev):
-    """Rows [B][H][N][D] with any strides but contiguous elements."""
+def _device_index(name, t):
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return index
+
+
+def _wrong_device(name, t, index):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, other arguments on {dev}: one device per call")
-    _need(name, t, dtype, shape)
+    raise ValueError(f"{name} is on {t.device}, other arguments on cuda:{index}: one device per call")
+
+
+def _tensor(name, t, dtype, shape, index):
+    """The address of a contiguous tensor of exactly this dtype and shape (None: NULL)."""
+    if t is None:
+        return None
+    if t.get_device() != index:
+        _wrong_device(name, t, index)
+    if t.dtype is not dtype or t.shape != shape:
+        _need(name, t, dtype, shape)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(name, t, dtype, shape, index):
+    """tv_rows of [B][H][N][D] with any strides but contiguous elements."""
+    if t.get_device() != index:
+        _wrong_device(name, t, index)
+    if t.dtype is not dtype or t.shape != shape:
+        _need(name, t, dtype, shape)
     sb, sh, sn, sd = t.stride()
     if sd != 1 and shape[3] > 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
-    return _Rows(t.data_ptr(), sb, sh, sn)
+    return _pack_rows(t.data_ptr(), sb, sh, sn)
 
 
-def _same_memory(a, b):
-    return a.data_ptr() == b.data_ptr()
+def _rope(rope, interleaved, index):
+    rot = rope["rot_dim"]
+    return _pack_rope(_tensor("rope['freq']", rope["freq"], torch.int64, (rot // 2,), index), rot, 1 if interleaved else 0,
+                      rope["amplitude"])
+
+
+def _status(dev_status, index):
+    if dev_status is None:
+        return torch.zeros(1, dtype=torch.int32, device=index)
+    if dev_status.get_device() != index:
+        _wrong_device("dev_status", dev_status, index)
+    if dev_status.dtype is not torch.int32 or dev_status.numel() < 1:
+        raise ValueError("dev_status must be an int32 tensor of at least one element")
+    return dev_status
+
+
+def _launch(name, index, *args):
+    """The library call on the device's current stream, with the device current."""
+    fn = getattr(load_library(), name)
+    if torch._C._cuda_getDevice() == index:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status != 0:
+        _check(name, status)
 
 
 def rotary(x, pos, rope, *, interleaved: bool = False, pos_base=None, out=None):
@@ -666,39 +705,41 @@ def rotary(x, pos, rope, *, interleaved: bool = False, pos_base=None, out=None):
     (i, i + rot_dim / 2), or (2i, 2i + 1) with interleaved.  Rows with pos < 0 are left as
     they are in out (new storage when omitted; x itself, where contiguous, to work in
     place)."""
-    dev = _need_cuda(pos=pos, pos_base=pos_base, freq=rope["freq"], out=out)
-    _ndim("x", x, 4)
-    B, H, N, D = x.shape
-    rows = _rows_arg("x", x, x.shape, x.dtype, dev)
+    index = _device_index("pos", pos)
+    if x.ndim != 4:
+        _ndim("x", x, 4)
+    B, H, N, D = shape = tuple(x.shape)
+    dtype = x.dtype
     code = _dtype_code(x)
-    _need("pos", pos, torch.int32, (B, N))
-    if pos_base is not None:
-        _need("pos_base", pos_base, torch.int32, (B,))
+    rows = _rows("x", x, dtype, shape, index)
+    pos_p = _tensor("pos", pos, torch.int32, (B, N), index)
+    base_p = _tensor("pos_base", pos_base, torch.int32, (B,), index)
+    packed = _rope(rope, interleaved, index)
     if out is None:
-        out = torch.empty((B, H, N, D), dtype=x.dtype, device=dev)
-    else:
-        _need("out", out, x.dtype, (B, H, N, D))
-        if _same_memory(out, x) and not x.is_contiguous():
-            raise ValueError("x must be contiguous to be rotated in place")
-    rp = _rope_arg(rope, interleaved)
-    with _on(dev):
-        _check("tv_rotary", load_library().tv_rotary(ctypes.byref(rows), _ptr(out), _ptr(pos), _ptr(pos_base),
-                                                     ctypes.byref(rp), B, H, N, D, code, _stream()))
+        out = torch.empty(shape, dtype=dtype, device=x.device)
+    out_p = _tensor("out", out, dtype, shape, index)
+    if out_p == x.data_ptr() and not x.is_contiguous():
+        raise ValueError("x must be contiguous to be rotated in place")
+    _launch("tv_rotary", index, rows, out_p, pos_p, base_p, packed, B, H, N, D, code)
     return out
 
 
-def _paged_kv(k_cache, v_cache, page_table, prefix_len):
-    """The tv_paged_kv of checked tensors; returns (struct, B, Hkv, page_size, max_pages, D)."""
-    _ndim("k_cache", k_cache, 4)
-    _ndim("page_table", page_table, 2)
-    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+def _paged_kv(k_cache, v_cache, page_table, prefix_len, index):
+    """(tv_paged_kv, B, Hkv, page_size, max_pages, D) of the checked tensors."""
+    if k_cache.ndim != 4:
+        _ndim("k_cache", k_cache, 4)
+    if page_table.ndim != 2:
+        _ndim("page_table", page_table, 2)
+    shape = tuple(k_cache.shape)
+    dtype = k_cache.dtype
+    if v_cache.dtype is not dtype or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must match")
-    pages, Hkv, ps, D = k_cache.shape
+    pages, Hkv, ps, D = shape
     B, width = page_table.shape
-    _need("page_table", page_table, torch.int32, (B, width))
-    _need("prefix_len", prefix_len, torch.int32, (B,))
-    kv = _PagedKv(k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), prefix_len.data_ptr(), pages, ps,
-                  width)
+    kv = _pack_paged_kv(_tensor("k_cache", k_cache, dtype, shape, index),
+                        _tensor("v_cache", v_cache, dtype, shape, index),
+                        _tensor("page_table", page_table, torch.int32, (B, width), index),
+                        _tensor("prefix_len", prefix_len, torch.int32, (B,), index), pages, ps, width)
     return kv, B, Hkv, ps, width, D
 
 
@@ -709,38 +750,36 @@ def append_kv_paged(k, v, k_cache, v_cache, page_table, prefix_len, *, depth=Non
     (with rope) at position prefix_len[b] + depth[b][t] (depth: tree_prep's, -1 = padding;
     omitted: t).  page_table [B][max_pages], prefix_len [B], n_rows [B] (omitted: N each) are
     int32.  With q [B][Hq][N][D] its rows are rotated too, into q_out (returned)."""
-    dev = _need_cuda(k_cache=k_cache, v_cache=v_cache, page_table=page_table, prefix_len=prefix_len, depth=depth,
-                     n_rows=n_rows, q_out=q_out, freq=None if rope is None else rope["freq"])
-    kv, B, Hkv, _, _, D = _paged_kv(k_cache, v_cache, page_table, prefix_len)
-    _ndim("k", k, 4)
+    index = _device_index("k_cache", k_cache)
+    kv, B, Hkv, _, _, D = _paged_kv(k_cache, v_cache, page_table, prefix_len, index)
+    if k.ndim != 4:
+        _ndim("k", k, 4)
     N = k.shape[2]
+    dtype = k_cache.dtype
     code = _dtype_code(k_cache)
-    kr = _rows_arg("k", k, (B, Hkv, N, D), k_cache.dtype, dev)
-    vr = _rows_arg("v", v, (B, Hkv, N, D), k_cache.dtype, dev)
-    if depth is not None:
-        _need("depth", depth, torch.int32, (B, N))
-    if n_rows is not None:
-        _need("n_rows", n_rows, torch.int32, (B,))
-    qr, Hq = None, 0
+    shape = (B, Hkv, N, D)
+    k_rows = _rows("k", k, dtype, shape, index)
+    v_rows = _rows("v", v, dtype, shape, index)
+    depth_p = _tensor("depth", depth, torch.int32, (B, N), index)
+    rows_p = _tensor("n_rows", n_rows, torch.int32, (B,), index)
+    q_rows = out_p = None
+    Hq = 0
     if q is not None:
         if rope is None:
             raise ValueError("q is rotated: rope is required with it")
-        _ndim("q", q, 4)
+        if q.ndim != 4:
+            _ndim("q", q, 4)
         Hq = q.shape[1]
-        qr = _rows_arg("q", q, (B, Hq, N, D), k_cache.dtype, dev)
+        shape = (B, Hq, N, D)
+        q_rows = _rows("q", q, dtype, shape, index)
         if q_out is None:
-            q_out = torch.empty((B, Hq, N, D), dtype=q.dtype, device=dev)
-        else:
-            _need("q_out", q_out, q.dtype, (B, Hq, N, D))
-            if _same_memory(q_out, q) and not q.is_contiguous():
-                raise ValueError("q must be contiguous to be rotated in place")
-    rp = None if rope is None else _rope_arg(rope, interleaved)
-    st = _status_tensor(dev_status, dev)
-    with _on(dev):
-        _check("tv_append_kv_paged", load_library().tv_append_kv_paged(
-            ctypes.byref(kr), ctypes.byref(vr), ctypes.byref(kv), _ptr(depth), _ptr(n_rows),
-            None if rp is None else ctypes.byref(rp), None if qr is None else ctypes.byref(qr),
-            None if qr is None else _ptr(q_out), B, Hq, Hkv, N, D, code, _ptr(st), _stream()))
+            q_out = torch.empty(shape, dtype=dtype, device=k_cache.device)
+        out_p = _tensor("q_out", q_out, dtype, shape, index)
+        if out_p == q.data_ptr() and not q.is_contiguous():
+            raise ValueError("q must be contiguous to be rotated in place")
+    st = _status(dev_status, index)
+    _launch("tv_append_kv_paged", index, k_rows, v_rows, kv, depth_p, rows_p,
+            None if rope is None else _rope(rope, interleaved, index), q_rows, out_p, B, Hq, Hkv, N, D, code, st.data_ptr())
     return q_out if q is not None else None
 
 
@@ -756,31 +795,30 @@ def paged_attention(q, k_cache, v_cache, page_table, prefix_len, *, parent=None,
     parent [B][N].  page_table [B][max_pages], prefix_len [B], n_rows [B] int32.  softcap > 0
     caps scores by softcap * tanh(score / softcap); window > 0 hides keys `window` or more
     positions back.  workspace: paged_attention_workspace_size bytes, zero-filled once
-    (allocated here when omitted)."""
-    dev = _need_cuda(q=q, k_cache=k_cache, v_cache=v_cache, page_table=page_table, prefix_len=prefix_len,
-                     parent=parent, n_rows=n_rows, out=out)
-    kv, B, Hkv, ps, width, D = _paged_kv(k_cache, v_cache, page_table, prefix_len)
-    _ndim("q", q, 4)
+    (allocated here when omitted; its size is checked by the library)."""
+    index = _device_index("q", q)
+    kv, B, Hkv, ps, width, D = _paged_kv(k_cache, v_cache, page_table, prefix_len, index)
+    if q.ndim != 4:
+        _ndim("q", q, 4)
     _, Hq, N, _ = q.shape
-    _need("q", q, k_cache.dtype, (B, Hq, N, D))
-    code = _dtype_code(q)
-    if parent is not None:
-        _tree_inputs(parent, None, B, N)
-    if n_rows is not None:
-        _need("n_rows", n_rows, torch.int32, (B,))
+    dtype = k_cache.dtype
+    code = _dtype_code(k_cache)
+    shape = (B, Hq, N, D)
+    q_p = _tensor("q", q, dtype, shape, index)
+    parent_p = _tensor("parent", parent, torch.int32, (B, N), index)
+    rows_p = _tensor("n_rows", n_rows, torch.int32, (B,), index)
     if out is None:
-        out = torch.empty_like(q)
-    else:
-        _need("out", out, q.dtype, (B, Hq, N, D))
-    st = _status_tensor(dev_status, dev)
-    lib = load_library()
-    with _on(dev):
-        # a given workspace's size is checked by the call itself
-        ws = _workspace(0 if workspace is not None else
-                        lib.tv_paged_attention_workspace_size(B, Hq, Hkv, D, N, ps, width, code), dev, workspace)
-        _check("tv_paged_attention", lib.tv_paged_attention(
-            _ptr(q), _ptr(out), ctypes.byref(kv), _ptr(parent), _ptr(n_rows), B, Hq, Hkv, N, D, float(scale),
-            float(softcap), int(window), code, _ptr(ws), ws.numel() * ws.element_size(), _ptr(st), _stream()))
+        out = torch.empty(shape, dtype=dtype, device=q.device)
+    out_p = _tensor("out", out, dtype, shape, index)
+    st = _status(dev_status, index)
+    if workspace is None:
+        with torch.cuda.device(index):
+            n = load_library().tv_paged_attention_workspace_size(B, Hq, Hkv, D, N, ps, width, code)
+        workspace = torch.zeros(max(int(n), 256), dtype=torch.uint8, device=index)
+    elif workspace.get_device() != index:
+        _wrong_device("workspace", workspace, index)
+    _launch("tv_paged_attention", index, q_p, out_p, kv, parent_p, rows_p, B, Hq, Hkv, N, D, scale, softcap, int(window),
+            code, workspace.data_ptr(), workspace.numel() * workspace.element_size(), st.data_ptr())
     return out
 
 
@@ -790,20 +828,17 @@ def commit_accepted_kv_paged(k_cache, v_cache, page_table, prefix_len, accepted_
     prefix_len[b] + a_k move to prefix_len[b] + k.  accepted_nodes [B][N], accept_len [B] as
     returned by verify_greedy / verify_sample.  Returns new_len [B] int32, the sequences'
     committed rows after the round (prefix_len + accept_len + 1)."""
-    dev = _need_cuda(k_cache=k_cache, v_cache=v_cache, page_table=page_table, prefix_len=prefix_len,
-                     accepted_nodes=accepted_nodes, accept_len=accept_len, new_len=new_len)
-    kv, B, Hkv, _, _, D = _paged_kv(k_cache, v_cache, page_table, prefix_len)
-    _ndim("accepted_nodes", accepted_nodes, 2)
+    index = _device_index("k_cache", k_cache)
+    kv, B, Hkv, _, _, D = _paged_kv(k_cache, v_cache, page_table, prefix_len, index)
+    if accepted_nodes.ndim != 2:
+        _ndim("accepted_nodes", accepted_nodes, 2)
     N = accepted_nodes.shape[1]
-    _need("accepted_nodes", accepted_nodes, torch.int32, (B, N))
-    _need("accept_len", accept_len, torch.int32, (B,))
+    nodes_p = _tensor("accepted_nodes", accepted_nodes, torch.int32, (B, N), index)
+    len_p = _tensor("accept_len", accept_len, torch.int32, (B,), index)
     if new_len is None:
-        new_len = torch.empty(B, dtype=torch.int32, device=dev)
-    else:
-        _need("new_len", new_len, torch.int32, (B,))
-    st = _status_tensor(dev_status, dev)
-    with _on(dev):
-        _check("tv_commit_accepted_kv_paged", load_library().tv_commit_accepted_kv_paged(
-            ctypes.byref(kv), _ptr(accepted_nodes), _ptr(accept_len), _ptr(new_len), B, Hkv, N, D,
-            _dtype_code(k_cache), _ptr(st), _stream()))
+        new_len = torch.empty(B, dtype=torch.int32, device=k_cache.device)
+    new_p = _tensor("new_len", new_len, torch.int32, (B,), index)
+    st = _status(dev_status, index)
+    _launch("tv_commit_accepted_kv_paged", index, kv, nodes_p, len_p, new_p, B, Hkv, N, D, _dtype_code(k_cache),
+            st.data_ptr())
     return new_len
