@@ -125,11 +125,40 @@ __device__ __forceinline__ float soft_tanh(float x) {
   return fmaf(-2.f, r, 1.f);
 }
 
+// tanh to an ulp or two: its Taylor series up to x^13 below 0.45 (the next term is 2^-25 of x),
+// where capped scores mostly lie, else the library's
+__device__ __forceinline__ float tanh_f32(float x) {
+  const float z = x * x;
+  if (z >= 0.2025f || isnan(x)) return tanhf(x);
+  float p = fmaf(z, 3.5921280e-3f, -8.8632355e-3f);  // 21844 / 6081075, -1382 / 155925
+  p = fmaf(z, p, 2.1869489e-2f);                     // 62 / 2835
+  p = fmaf(z, p, -5.3968254e-2f);                    // -17 / 315
+  p = fmaf(z, p, 1.3333333e-1f);
+  p = fmaf(z, p, -3.3333333e-1f);
+  return fmaf(x * z, p, x);
+}
+
+// four soft_tanh with one reciprocal: 1 / a = (1 / abcd) (b cd).  2^x is held below 2^30, where tanh
+// has long been 1, so the product stays finite; a NaN makes its neighbours NaN, which only keys
+// that may not be seen hold, and their scores are replaced.
+__device__ __forceinline__ void soft_tanh4(float* s, float k) {
+  float a[4], r;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) a[u] = 1.f + ptx::ex2(fminf(s[u] * k, 30.f));
+  const float ab = a[0] * a[1], cd = a[2] * a[3];
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ab * cd));
+  const float rab = -2.f * r * cd, rcd = -2.f * r * ab;
+  s[0] = fmaf(rab, a[1], 1.f);
+  s[1] = fmaf(rab, a[0], 1.f);
+  s[2] = fmaf(rcd, a[3], 1.f);
+  s[3] = fmaf(rcd, a[2], 1.f);
+}
+
 // ---- host side
 constexpr int kPagedMaxSms = 160;  // sizes the workspaces
 constexpr int kPagedMaxCtas = 2;   // CTAs per SM of the largest persistent grid
 constexpr size_t kPagedCntBytes = kPagedMaxCtas * kPagedMaxSms * 4;
-constexpr int kPagedFewRows = 16;  // query rows of a KV head above which row tiles are used (bf16)
+constexpr int kPagedFewRows = 16;  // query rows of a KV head above which row tiles are used
 
 int paged_device_sms();
 int paged_grid_sms();  // less where tv_set_sm_partition says so
@@ -138,6 +167,8 @@ size_t paged_tc_ws(int B, int Hq, int Hkv, int D, int N);
 cudaError_t launch_paged_tc(PagedAttn a, char* ws, cudaStream_t stream);
 size_t paged_mma_ws(int B, int Hq, int Hkv, int D, int N);
 cudaError_t launch_paged_mma(PagedAttn a, char* ws, cudaStream_t stream);
+size_t paged_f32_ws(int B, int Hq, int Hkv, int D, int N);
+cudaError_t launch_paged_f32(PagedAttn a, char* ws, cudaStream_t stream);
 size_t paged_simt_ws(int D);
 cudaError_t launch_paged_simt(PagedAttn a, char* ws, cudaStream_t stream);
 // Tensor map of bf16 pages, 128-byte swizzle.  D = 128 and 256: 5-D, a box spans all column

@@ -1,5 +1,6 @@
 // Paged attention's entry: the kernel for a call.
-//   fp32                                     paged_simt_kernel
+//   fp32, more than 16 query rows a KV head  paged_f32_kernel (row tiles on CUDA cores)
+//   other fp32                               paged_simt_kernel
 //   bf16, more than 16 query rows a KV head,
 //     D <= 128, G <= 16                      paged_tc_kernel (row tiles on tcgen05)
 //   other bf16                               paged_mma_kernel (a stream of keys past few rows)
@@ -29,13 +30,16 @@ int paged_grid_sms() {
   return share > 0 && share < n ? share : n;
 }
 
+static bool f32_tiles(int Hq, int Hkv, int N) { return (long long)(Hq / Hkv) * N > kPagedFewRows; }
+
 size_t paged_attn_ws(int B, int Hq, int Hkv, int D, int N, tv_dtype dtype) {
-  if (dtype == TV_F32) return paged_simt_ws(D);
+  if (dtype == TV_F32) return f32_tiles(Hq, Hkv, N) ? paged_f32_ws(B, Hq, Hkv, D, N) : paged_simt_ws(D);
   return paged_tc_takes(Hq, Hkv, D, N) ? paged_tc_ws(B, Hq, Hkv, D, N) : paged_mma_ws(B, Hq, Hkv, D, N);
 }
 
 cudaError_t launch_paged_attn(PagedAttn a, tv_dtype dtype, char* ws, cudaStream_t stream) {
-  if (dtype == TV_F32) return launch_paged_simt(a, ws, stream);
+  if (dtype == TV_F32)
+    return f32_tiles(a.Hq, a.Hkv, a.N) ? launch_paged_f32(a, ws, stream) : launch_paged_simt(a, ws, stream);
   return paged_tc_takes(a.Hq, a.Hkv, a.D, a.N) ? launch_paged_tc(a, ws, stream) : launch_paged_mma(a, ws, stream);
 }
 

@@ -1,5 +1,5 @@
-// Attention of new rows (a causal chunk or a draft tree) over a paged fp32 KV cache, on CUDA
-// cores.
+// Attention of few new rows (single tokens, short chunks, small trees) over a paged fp32 KV
+// cache, on CUDA cores (more rows: paged_f32.cu).
 //
 //   out[b,h,i,:] = sum_j softmax_j(z_ij) v_j,  z = scale q_i . k_j, or cap tanh(scale q_i . k_j / cap)
 //
@@ -7,7 +7,7 @@
 // (causal) or i and its ancestors (tree), less those `window` or more positions back.
 //
 // One CTA takes RT = 8 kRPW query rows of a KV head (row r is head r % G of node r / G) and
-// walks its range of 32-key tiles, which cp.async brings into a double buffer.  A warp
+// walks its range of 32-key tiles, which cp.async brings into three buffers.  A warp
 // owns kRPW rows: lane j scores key j against each (K rows padded by 16 bytes, so the 8
 // lanes of a 128-bit phase hit different banks), the warp keeps the running maximum and sum
 // of each row in 32 bits, and P goes through shared memory so that four keys' weights
@@ -20,6 +20,7 @@ namespace tv {
 
 constexpr int kPsWarps = 8;
 constexpr int kPsKeys = 32;
+constexpr int kPsStages = 3;  // K and V tiles in shared memory: two on their way while one is used
 constexpr int kPsMerge = 4;  // parts whose loads are in flight together
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
@@ -31,8 +32,8 @@ struct PsSmem {
   static constexpr int kD = kDPL * 32;
   static constexpr int kRT = kPsWarps * kRPW;
   static constexpr int kStride = kD + 4;  // K row in smem, elements
-  static constexpr int kOffV = 2 * kPsKeys * kStride * 4;
-  static constexpr int kOffQ = kOffV + 2 * kPsKeys * kD * 4;
+  static constexpr int kOffV = kPsStages * kPsKeys * kStride * 4;
+  static constexpr int kOffQ = kOffV + kPsStages * kPsKeys * kD * 4;
   static constexpr int kOffP = kOffQ + kRT * kD * 4;
   static constexpr int kOffVis = kOffP + kRT * kPsKeys * 4;
   static constexpr int kOffPar = kOffVis + kRT * (kMaxNodes / 32) * 4;
@@ -51,7 +52,8 @@ __global__ void __launch_bounds__(kPsWarps * 32, kDPL <= 4 ? 2 : 1) paged_simt_k
   uint32_t(*s_vis)[kMaxNodes / 32] = reinterpret_cast<uint32_t(*)[kMaxNodes / 32]>(ps_smem + S::kOffVis);
   int* s_par = reinterpret_cast<int*>(ps_smem + S::kOffPar);
   __shared__ unsigned long long s_red[34];
-  __shared__ int s_first_pad, s_last, s_depth[kRT];
+  __shared__ int s_first_pad, s_last, s_depth[kRT], s_page[4][kPsKeys / 8];
+  const int box_shift = min(a.page_shift, 5), pages_tile = kPsKeys >> box_shift;  // a tile's row pieces, each in one page
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float* q = reinterpret_cast<const float*>(a.q);
   float* out = reinterpret_cast<float*>(a.out);
@@ -126,21 +128,26 @@ __global__ void __launch_bounds__(kPsWarps * 32, kDPL <= 4 ? 2 : 1) paged_simt_k
         }
         // rows [lo, hi) of the tile; others (pages past the end, rows behind the window, whose
         // contents may be anything) read as zero
+        auto page_of = [&](int t) -> int {
+          const int j = (tile0 + t) * kPsKeys + ((int)threadIdx.x << box_shift);
+          if ((int)threadIdx.x >= pages_tile || t >= t1 || j >= hi || j + (1 << box_shift) <= lo) return -1;
+          const int page = table[j >> a.page_shift];
+          if (page >= 0 && page < a.num_pages) return page;
+          set_dev_status(a.dev_status, TV_DEV_BAD_PAGE);
+          return -1;
+        };
         auto load_tile = [&](int t, int buf) {
+          if (t >= t1) {  // an empty group keeps the count
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            return;
+          }
           constexpr int kChunks = kD / kVec;
           for (int e = threadIdx.x; e < kPsKeys * kChunks; e += blockDim.x) {
             const int jj = e / kChunks, ch = e - jj * kChunks;
             const int j = (tile0 + t) * kPsKeys + jj;
             float* dk = s_k + (buf * kPsKeys + jj) * S::kStride + ch * kVec;
             float* dv = s_v + (buf * kPsKeys + jj) * kD + ch * kVec;
-            int page = -1;
-            if (j >= lo && j < hi) {
-              page = table[j >> a.page_shift];
-              if (page < 0 || page >= a.num_pages) {
-                set_dev_status(a.dev_status, TV_DEV_BAD_PAGE);
-                page = -1;
-              }
-            }
+            const int page = j >= lo && j < hi ? s_page[t & 3][jj >> box_shift] : -1;
             if (page >= 0) {
               const size_t off =
                   ((((size_t)page * a.Hkv + hk) << a.page_shift) + (j & ((1 << a.page_shift) - 1))) * kD + ch * kVec;
@@ -153,32 +160,34 @@ __global__ void __launch_bounds__(kPsWarps * 32, kDPL <= 4 ? 2 : 1) paged_simt_k
           }
           asm volatile("cp.async.commit_group;" ::: "memory");
         };
+        if ((int)threadIdx.x < pages_tile) {
+          for (int u = 0; u < 3; ++u) s_page[(t0 + u) & 3][threadIdx.x] = page_of(t0 + u);
+        }
+        __syncthreads();
         load_tile(t0, 0);
+        load_tile(t0 + 1, 1);
         for (int t = t0; t < t1; ++t) {
-          const int buf = (t - t0) & 1;
-          if (t + 1 < t1) {
-            load_tile(t + 1, buf ^ 1);
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
-          } else {
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-          }
+          const int buf = (t - t0) % kPsStages;
+          load_tile(t + 2, (t + 2 - t0) % kPsStages);
+          const int ahead = page_of(t + 3);
+          asm volatile("cp.async.wait_group 2;" ::: "memory");
           __syncthreads();
+          if ((int)threadIdx.x < pages_tile) s_page[(t + 3) & 3][threadIdx.x] = ahead;
           const int j = (tile0 + t) * kPsKeys + lane;
-          float dot[kRPW];
+          float4 part[kRPW];  // four chains
 #pragma unroll
-          for (int rw = 0; rw < kRPW; ++rw) dot[rw] = 0.f;
+          for (int rw = 0; rw < kRPW; ++rw) part[rw] = make_float4(0.f, 0.f, 0.f, 0.f);
           const float* kr = s_k + (buf * kPsKeys + lane) * S::kStride;
-#pragma unroll 4
+#pragma unroll 8
           for (int d = 0; d < kD; d += kVec) {
             const float4 kf = *reinterpret_cast<const float4*>(kr + d);
 #pragma unroll
             for (int rw = 0; rw < kRPW; ++rw) {
-              const float* qr = s_q + (warp * kRPW + rw) * kD + d;
-              const float4 qf = *reinterpret_cast<const float4*>(qr);
-              dot[rw] = fmaf(qf.x, kf.x, dot[rw]);
-              dot[rw] = fmaf(qf.y, kf.y, dot[rw]);
-              dot[rw] = fmaf(qf.z, kf.z, dot[rw]);
-              dot[rw] = fmaf(qf.w, kf.w, dot[rw]);
+              const float4 qf = *reinterpret_cast<const float4*>(s_q + (warp * kRPW + rw) * kD + d);
+              part[rw].x = fmaf(qf.x, kf.x, part[rw].x);
+              part[rw].y = fmaf(qf.y, kf.y, part[rw].y);
+              part[rw].z = fmaf(qf.z, kf.z, part[rw].z);
+              part[rw].w = fmaf(qf.w, kf.w, part[rw].w);
             }
           }
 #pragma unroll
@@ -192,9 +201,9 @@ __global__ void __launch_bounds__(kPsWarps * 32, kDPL <= 4 ? 2 : 1) paged_simt_k
               vis = a.parent ? (s_vis[rr][t_new >> 5] >> (t_new & 31)) & 1u
                              : t_new <= i && (a.window <= 0 || i - t_new < a.window);
             }
-            float z = dot[rw];
+            float z = (part[rw].x + part[rw].y) + (part[rw].z + part[rw].w);
             // expf of a difference, not 2^(z log2 e - m): the product's rounding would cost |z| 2^-24
-            if (a.cap > 0.f) z = a.cap * tanhf(z / a.cap);
+            if (a.cap > 0.f) z = a.cap * tanh_f32(z / a.cap);
             z = vis ? z : -INFINITY;
             const float mt = warp_max(z);
             float p = 0.f;
@@ -304,7 +313,7 @@ __global__ void __launch_bounds__(kPsWarps * 32, kDPL <= 4 ? 2 : 1) paged_simt_k
 // ---- host side
 
 // counters, (m, l) and O of two partial units per CTA of the largest grid
-constexpr size_t kPsRows = (size_t)2 * kPagedMaxCtas * kPagedMaxSms * kPsWarps * 4;
+constexpr size_t kPsRows = (size_t)2 * kPagedMaxCtas * kPagedMaxSms * kPsWarps * 2;
 
 size_t paged_simt_ws(int D) { return kPagedCntBytes + kPsRows * 8 + kPsRows * D * 4; }
 
@@ -347,7 +356,7 @@ static cudaError_t launch_ps_d(const PagedAttn& a, char* ws, cudaStream_t stream
 
 cudaError_t launch_paged_simt(PagedAttn a, char* ws, cudaStream_t stream) {
   // few rows: one a warp, so that a KV head's rows spread over a CTA's warps
-  return a.G * a.N <= kPsWarps ? launch_ps_d<1>(a, ws, stream) : launch_ps_d<4>(a, ws, stream);
+  return a.G * a.N <= kPsWarps ? launch_ps_d<1>(a, ws, stream) : launch_ps_d<2>(a, ws, stream);
 }
 
 }  // namespace tv

@@ -546,7 +546,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         ptx::tmem_wait_ld();
         if constexpr (kCap) {
 #pragma unroll
-          for (int j = 0; j < 64; ++j) sv[j] = soft_tanh(sv[j] * ck);
+          for (int j = 0; j < 64; j += 4) soft_tanh4(sv + j, ck);
         }
         if (vis != ~0ull) {
 #pragma unroll
