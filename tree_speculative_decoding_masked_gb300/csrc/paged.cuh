@@ -33,6 +33,7 @@ struct PagedSpan {
   int b;            // where this CTA starts: sequence,
   long long base;   // and that sequence's first tile
 };
+constexpr int kPagedRed = 34 + 512;  // scratch of paged_span: CTAs of up to 512 threads
 
 __device__ __forceinline__ int unit_rows(const PagedAttn& a, int n, int rt, int RT) {
   return max(0, min(RT, n * a.G - rt * RT));
@@ -49,29 +50,49 @@ __device__ __forceinline__ int unit_tiles(const PagedAttn& a, int P, int n, int 
   const int hi = P + (rt * RT + rows - 1) / a.G + 1;
   return (hi + KT - 1) / KT - unit_lo(a, P, rt, RT) / KT;
 }
-// tiles of one KV head of sequence b
-__device__ inline long long seq_tiles(const PagedAttn& a, int b, int RT, int KT, bool* bad) {
-  const int P = a.prefix_len[b];
-  const int n = paged_rows(a, b, P, bad);
-  long long s = 0;
-  for (int rt = 0; rt * RT < n * a.G; ++rt) s += unit_tiles(a, P, n, rt, RT, KT);
-  return s;
+// Tiles of one KV head of a sequence; a warp's lanes share the sum over its row tiles.
+__device__ inline long long head_tiles_warp(const PagedAttn& a, int P, int n, int RT, int KT) {
+  unsigned long long s = 0;
+  for (int rt = threadIdx.x & 31; rt * RT < n * a.G; rt += 32) s += unit_tiles(a, P, n, rt, RT, KT);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return (long long)s;
 }
 
-// Every thread of the CTA calls it; red holds 34 entries.  A CTA takes min_per tiles or more.
+// Every thread of the CTA calls it; red holds kPagedRed entries.  A CTA takes min_per tiles or more.
 __device__ inline PagedSpan paged_span(const PagedAttn& a, int RT, int KT, int min_per, unsigned long long* red) {
   PagedSpan sp;
   unsigned long long W = 0, mine = 0, at = 0;
   bool any_bad = false;
-  auto tiles_of = [&](int b) -> unsigned long long {
-    if (b >= a.B) return 0ull;
-    bool bad = false;
-    const unsigned long long t = (unsigned long long)seq_tiles(a, b, RT, KT, &bad) * a.Hkv;
-    any_bad |= bad;
+  // tiles of sequence b0 + threadIdx.x: by its own thread, or with many row tiles a warp each
+  const bool many = a.N * a.G > 4 * RT;
+  auto tiles_of = [&](int b0) -> unsigned long long {
+    const int b = b0 + threadIdx.x;
+    unsigned long long t = 0;
+    if (many) {
+      const int count = min((int)blockDim.x, a.B - b0);
+      for (int k = threadIdx.x >> 5; k < count; k += blockDim.x >> 5) {
+        const int P = a.prefix_len[b0 + k];
+        bool bad = false;
+        const int n = paged_rows(a, b0 + k, P, &bad);
+        any_bad |= bad;
+        const long long head = head_tiles_warp(a, P, n, RT, KT);
+        if ((threadIdx.x & 31) == 0) red[34 + k] = (unsigned long long)head;
+      }
+      __syncthreads();
+      if (b < a.B) t = red[34 + threadIdx.x] * a.Hkv;
+    } else if (b < a.B) {
+      const int P = a.prefix_len[b];
+      bool bad = false;
+      const int n = paged_rows(a, b, P, &bad);
+      any_bad |= bad;
+      for (int rt = 0; rt * RT < n * a.G; ++rt) t += unit_tiles(a, P, n, rt, RT, KT);
+      t *= a.Hkv;
+    }
     return t;
   };
   for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {
-    mine = tiles_of(b0 + threadIdx.x);
+    mine = tiles_of(b0);
     unsigned long long part = 0;
     at = W + block_scan_u64(mine, red, &part);
     W += part;
@@ -89,7 +110,7 @@ __device__ inline PagedSpan paged_span(const PagedAttn& a, int RT, int KT, int m
   for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {
     unsigned long long part = 0;
     if (a.B > (int)blockDim.x) {
-      mine = tiles_of(b0 + threadIdx.x);
+      mine = tiles_of(b0);
       at = cum + block_scan_u64(mine, red, &part);
       cum += part;
     } else {
@@ -108,6 +129,70 @@ __device__ inline PagedSpan paged_span(const PagedAttn& a, int RT, int KT, int m
     }
   }
   return sp;
+}
+
+// The units of a CTA's range, one after another.  A warp's lanes call unit_next together.
+struct UnitWalk {
+  long long pos, end;       // tiles still to take
+  long long seq, head;      // first tile of sequence b; tiles of one of its KV heads
+  long long u0, u1;         // the unit's tiles
+  int b, hk, rt, P, n;      // the unit; the sequence's committed and new rows
+  int t0, t1;               // of the unit's tiles, those to take
+  int loaded;
+};
+__device__ __forceinline__ UnitWalk unit_walk(const PagedSpan& sp) {
+  UnitWalk w{};
+  w.pos = sp.per * blockIdx.x;
+  w.end = min(sp.W, w.pos + sp.per);
+  w.seq = sp.base;
+  w.b = sp.b;
+  w.loaded = -1;
+  return w;
+}
+__device__ inline bool unit_next(const PagedAttn& a, UnitWalk& w, int RT, int KT) {
+  const int lane = threadIdx.x & 31;
+  while (w.pos < w.end && w.b < a.B) {
+    if (w.loaded != w.b) {
+      bool bad;
+      w.P = a.prefix_len[w.b];
+      w.n = paged_rows(a, w.b, w.P, &bad);
+      w.head = head_tiles_warp(a, w.P, w.n, RT, KT);
+      w.loaded = w.b;
+    }
+    long long rel = w.pos - w.seq;
+    if (rel >= w.head * a.Hkv) {
+      w.seq += w.head * a.Hkv;
+      ++w.b;
+      continue;
+    }
+    w.hk = (int)(rel / w.head);
+    rel -= w.hk * w.head;
+    for (int rt0 = 0;; rt0 += 32) {  // ends: rel lies below the head's sum
+      const unsigned t = unit_tiles(a, w.P, w.n, rt0 + lane, RT, KT);
+      unsigned incl = t;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const unsigned total = __shfl_sync(0xffffffffu, incl, 31);
+      if (rel >= (long long)total && (rt0 + 32) * RT < w.n * a.G) {
+        rel -= total;
+        continue;
+      }
+      const int k = max(0, __ffs(__ballot_sync(0xffffffffu, (long long)incl > rel)) - 1);
+      const unsigned T = __shfl_sync(0xffffffffu, t, k), upto = __shfl_sync(0xffffffffu, incl, k);
+      w.rt = rt0 + k;
+      w.u0 = w.pos - (rel - (long long)(upto - T));
+      w.u1 = w.u0 + T;
+      break;
+    }
+    w.t0 = (int)(w.pos - w.u0);
+    w.t1 = (int)(min(w.u1, w.end) - w.u0);
+    w.pos = w.u0 + w.t1;
+    return true;
+  }
+  return false;
 }
 
 // The ranges that share the unit of tiles [u0, u1): CTAs u0 / per .. (u1 - 1) / per.  A CTA

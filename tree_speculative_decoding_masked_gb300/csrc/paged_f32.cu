@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(kPfThreads, kD <= 64 ? 2 : 1)
   float* s_k = pf_smem + S::kOffK;
   float* s_v = pf_smem + S::kOffV;
   float* s_p = pf_smem + S::kOffP;
-  __shared__ unsigned long long s_red[34];
+  __shared__ unsigned long long s_red[kPagedRed];
   __shared__ uint32_t s_vis[kPfRows][kMaxNodes / 32];
   __shared__ int s_par[kMaxNodes];
   __shared__ int s_lo[kPfRows], s_hi[kPfRows], s_page[2][kPfKeys / 8], s_first_pad, s_last;
@@ -60,21 +60,28 @@ __global__ void __launch_bounds__(kPfThreads, kD <= 64 ? 2 : 1)
   const float inv_cap = a.cap > 0.f ? 1.f / a.cap : 0.f;
   const size_t cta = ((size_t)blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
   PagedSpan sp{};
-  long long pos = 0, end = 1, base = 0;
+  UnitWalk w{};
   if constexpr (kStream) {
     sp = paged_span(a, kPfRows, kPfKeys, 1, s_red);
-    pos = blockIdx.x * sp.per;
-    end = min(sp.W, pos + sp.per);
-    base = sp.base;
-  }
-  for (int b = kStream ? sp.b : blockIdx.z; b < a.B && pos < end; ++b) {
-    const int P = a.prefix_len[b];
+    w = unit_walk(sp);
+  } else {
+    // the cluster's unit, and this CTA's part of its tiles
     bool bad = false;
-    const int n = paged_rows(a, b, P, &bad);
-    if (!kStream && bad && threadIdx.x == 0) set_dev_status(a.dev_status, TV_DEV_BAD_PAGE);
+    w.b = blockIdx.z, w.hk = blockIdx.y / row_tiles, w.rt = blockIdx.y % row_tiles;
+    w.P = a.prefix_len[w.b];
+    w.n = paged_rows(a, w.b, w.P, &bad);
+    if (bad && threadIdx.x == 0) set_dev_status(a.dev_status, TV_DEV_BAD_PAGE);
+    const int T_u = unit_tiles(a, w.P, w.n, w.rt, kPfRows, kPfKeys), part = blockIdx.x;
+    w.t0 = (int)((long long)T_u * part / splits);
+    w.t1 = (int)((long long)T_u * (part + 1) / splits);
+  }
+  int tree = -1, n_act = 0;
+  for (bool once = true; kStream ? unit_next(a, w, kPfRows, kPfKeys) : once; once = false) {
+    const int b = w.b, hk = w.hk, rt = w.rt, P = w.P, n = w.n, t0 = w.t0, t1 = w.t1;
+    const long long u0 = w.u0, u1 = w.u1;
     const int32_t* table = a.table + (size_t)b * a.max_pages;
-    int n_act = n;
-    if (a.parent && n > 0) {
+    if (tree != b) n_act = n;
+    if (a.parent && n > 0 && tree != b) {
       __syncthreads();
       if (threadIdx.x == 0) s_first_pad = n;
       __syncthreads();
@@ -91,8 +98,7 @@ __global__ void __launch_bounds__(kPfThreads, kD <= 64 ? 2 : 1)
       __syncthreads();
       n_act = s_first_pad;
     }
-    // key tiles [t0, t1) of one unit, whose tiles are [u0, u1) of all
-    auto unit = [&](int hk, int rt, int t0, int t1, long long u0, long long u1) {
+    tree = b;
         const int rows = unit_rows(a, n, rt, kPfRows), r0 = rt * kPfRows;
         const int lo = unit_lo(a, P, rt, kPfRows), tile0 = lo / kPfKeys;
         const int hi = min(P + n_act, P + (r0 + rows - 1) / a.G + 1);
@@ -301,7 +307,7 @@ __global__ void __launch_bounds__(kPfThreads, kD <= 64 ? 2 : 1)
           for (int u = 0; u < kU; ++u)
             __stcg(reinterpret_cast<float2*>(to + tx * 2 + 32 * u), make_float2(acc[x][u][0] * f, acc[x][u][1] * f));
         }
-        if (c0 == c1) return;
+        if (c0 == c1) continue;
         // this CTA's rows of the merge: all of them as the last to finish, or its share of a cluster's
         int m0 = 0, m1 = rows, parts = splits;
         if constexpr (kStream) {
@@ -313,7 +319,7 @@ __global__ void __launch_bounds__(kPfThreads, kD <= 64 ? 2 : 1)
             __threadfence();
           }
           __syncthreads();
-          if (!s_last) return;
+          if (!s_last) continue;
           parts = (int)(c1 - c0) + 1;
         } else {
           __syncwarp();
@@ -361,30 +367,6 @@ __global__ void __launch_bounds__(kPfThreads, kD <= 64 ? 2 : 1)
           *reinterpret_cast<float4*>(out + (((size_t)b * a.Hq + hk * a.G + g) * a.N + i) * kD + ch * 4) =
               make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
         }
-    };
-    if constexpr (!kStream) {
-      const int rt = blockIdx.y % row_tiles, T_u = unit_tiles(a, P, n, rt, kPfRows, kPfKeys), part = blockIdx.x;
-      unit(blockIdx.y / row_tiles, rt, (int)((long long)T_u * part / splits), (int)((long long)T_u * (part + 1) / splits),
-           0, 0);
-      return;
-    }
-    // tiles of one KV head, to step over whole heads
-    long long head = 0;
-    for (int rt = 0; rt * kPfRows < n * a.G; ++rt) head += unit_tiles(a, P, n, rt, kPfRows, kPfKeys);
-    for (int hk = 0; hk < a.Hkv && pos < end; ++hk) {
-      if (pos >= base + head) {
-        base += head;
-        continue;
-      }
-      for (int rt = 0; rt * kPfRows < n * a.G && pos < end; ++rt) {
-        const long long u0 = base;
-        base += unit_tiles(a, P, n, rt, kPfRows, kPfKeys);
-        if (pos >= base) continue;
-        const int t0 = (int)(pos - u0), t1 = (int)(min(base, end) - u0);
-        pos = u0 + t1;
-        unit(hk, rt, t0, t1, u0, base);
-      }
-    }
   }
 }
 

@@ -94,62 +94,21 @@ __device__ __forceinline__ void pm_mma(float (&d)[4], const uint32_t (&a)[4], ui
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The next unit with work in this CTA's range [pos, end): its sequence, KV head, row tile and
-// tiles [t0, t1).  The producer and the consumers walk the same sequence of them.
-struct PmWalk {
-  long long pos, end, base, u0, u1;
-  int b, hk, rt, P, n, n_act, loaded, t0, t1;
-  bool done;
-};
-
+// The next unit of this CTA: of its range, or the cluster's one unit, whether it has work or not.
+// The producers and the consumers walk the same sequence of them.
 template <int kRT, bool kStream>
-__device__ __forceinline__ bool pm_next(const PagedAttn& a, PmWalk& w, int splits) {
-  if constexpr (!kStream) {  // this cluster's unit, whether it has work or not
-    if (w.done) return false;
-    bool bad;
-    w.done = true;
-    w.P = a.prefix_len[w.b];
-    w.n = paged_rows(a, w.b, w.P, &bad);
-    if (bad) set_dev_status(a.dev_status, TV_DEV_BAD_PAGE);
-    w.n_act = -1;
-    const int T_u = unit_tiles(a, w.P, w.n, w.rt, kRT, kPmKeys), part = blockIdx.x;
-    w.t0 = (int)((long long)T_u * part / splits);
-    w.t1 = (int)((long long)T_u * (part + 1) / splits);
-    return true;
-  } else {
-    while (w.pos < w.end && w.b < a.B) {
-      if (w.loaded != w.b) {
-        bool bad;
-        w.P = a.prefix_len[w.b];
-        w.n = paged_rows(a, w.b, w.P, &bad);
-        w.loaded = w.b;
-        w.n_act = -1;
-      }
-      const int T_u = unit_tiles(a, w.P, w.n, w.rt, kRT, kPmKeys);
-      w.u0 = w.base;
-      w.base += T_u;
-      if (w.pos < w.base) {
-        w.u1 = w.base;
-        w.t0 = (int)(w.pos - w.u0);
-        w.t1 = (int)(min(w.base, w.end) - w.u0);
-        w.pos = w.u0 + w.t1;
-        return true;
-      }
-      if (++w.rt * kRT >= w.n * a.G) {
-        w.rt = 0;
-        if (++w.hk >= a.Hkv) w.hk = 0, ++w.b;
-      }
-    }
-    return false;
-  }
-}
-// step over the unit that pm_next returned
-template <int kRT>
-__device__ __forceinline__ void pm_step(const PagedAttn& a, PmWalk& w) {
-  if (++w.rt * kRT >= w.n * a.G) {
-    w.rt = 0;
-    if (++w.hk >= a.Hkv) w.hk = 0, ++w.b;
-  }
+__device__ __forceinline__ bool pm_next(const PagedAttn& a, UnitWalk& w, int splits) {
+  if constexpr (kStream) return unit_next(a, w, kRT, kPmKeys);
+  if (w.loaded == w.b) return false;
+  bool bad;
+  w.loaded = w.b;
+  w.P = a.prefix_len[w.b];
+  w.n = paged_rows(a, w.b, w.P, &bad);
+  if (bad) set_dev_status(a.dev_status, TV_DEV_BAD_PAGE);
+  const int T_u = unit_tiles(a, w.P, w.n, w.rt, kRT, kPmKeys), part = blockIdx.x;
+  w.t0 = (int)((long long)T_u * part / splits);
+  w.t1 = (int)((long long)T_u * (part + 1) / splits);
+  return true;
 }
 
 template <int kD, int kRT, bool kCap, bool kStream>
@@ -162,7 +121,7 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT>::kThreads, 1)
   unsigned char* sm = pm_raw + ((1024u - (ptx::smem_addr(pm_raw) & 1023u)) & 1023u);
   PmBars* bars = reinterpret_cast<PmBars*>(sm + C::kOffBar);
   volatile int* abort_flag = &bars->abort;
-  __shared__ unsigned long long s_red[34];
+  __shared__ unsigned long long s_red[kPagedRed];
   __shared__ int s_lo[kRT], s_hi[kRT], s_first_pad, s_last;
   __shared__ float s_m[C::kWarps][kRT], s_l[C::kWarps][kRT];
   __shared__ __align__(8) float2 s_ml[kRT];
@@ -180,15 +139,12 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT>::kThreads, 1)
   ptx::griddep_wait();
   __syncthreads();
   PagedSpan sp{};
-  PmWalk w{};
+  UnitWalk w{};
   w.loaded = -1;
   if constexpr (kStream) {
     sp = paged_span(a, kRT, kPmKeys, kPmMinTiles, s_red);
     __syncthreads();
-    w.pos = sp.per * blockIdx.x;
-    w.end = min(sp.W, w.pos + sp.per);
-    w.base = sp.base;
-    w.b = sp.b;
+    w = unit_walk(sp);
   } else {
     w.b = blockIdx.z;
     w.hk = blockIdx.y / row_tiles;
@@ -210,18 +166,19 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT>::kThreads, 1)
     const uint32_t box_bytes = (uint32_t)(256 * C::kDB / per_piece) << box_shift;
     // where it goes in a stage: K or V, 8-row group, column block
     const int off = (part & 1) * C::kTile + ((pi << box_shift) >> 3) * C::kGroup + (part >> 1) * 1024;
-    int issued = 0;
+    int issued = 0, counted = -1, active = 0;  // a sequence's active rows, once counted
     while (pm_next<kRT, kStream>(a, w, splits)) {
-      if (w.n_act < 0) {
+      if (counted != w.b) {
         int pad = w.n;
         if (a.parent)
           for (int t = lane; t < w.n; t += 32)
             if (t > 0 && t < pad && a.parent[(size_t)w.b * a.N + t] == -1) pad = t;
-        w.n_act = __reduce_min_sync(0xffffffffu, pad);
+        active = __reduce_min_sync(0xffffffffu, pad);
+        counted = w.b;
       }
       const int unit = unit_rows(a, w.n, w.rt, kRT);
       const int lo = unit_lo(a, w.P, w.rt, kRT), tile0 = lo / kPmKeys;
-      const int hi = min(w.P + w.n_act, w.P + (w.rt * kRT + unit - 1) / a.G + 1);
+      const int hi = min(w.P + active, w.P + (w.rt * kRT + unit - 1) / a.G + 1);
       const int32_t* table = a.table + (size_t)w.b * a.max_pages;
       // the table entry of this lane's box in tile t, -1 where the box holds no needed row
       auto needed = [&](int t) -> bool {
@@ -258,7 +215,6 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT>::kThreads, 1)
         }
         __syncwarp();
       }
-      pm_step<kRT>(a, w);
     }
     // every tile's copies have landed before the CTA ends (the consumers waited for each; after an
     // abort they did not)
@@ -648,7 +604,6 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT>::kThreads, 1)
           }
         }
       }
-      pm_step<kRT>(a, w);
     }
   }
   if constexpr (!kStream) {

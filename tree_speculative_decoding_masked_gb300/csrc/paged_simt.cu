@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(kPsWarps * 32, kDPL <= 4 ? 2 : 1) paged_simt_k
   float* s_p = reinterpret_cast<float*>(ps_smem + S::kOffP);
   uint32_t(*s_vis)[kMaxNodes / 32] = reinterpret_cast<uint32_t(*)[kMaxNodes / 32]>(ps_smem + S::kOffVis);
   int* s_par = reinterpret_cast<int*>(ps_smem + S::kOffPar);
-  __shared__ unsigned long long s_red[34];
+  __shared__ unsigned long long s_red[kPagedRed];
   __shared__ int s_first_pad, s_last, s_depth[kRT], s_page[4][kPsKeys / 8];
   const int box_shift = min(a.page_shift, 5), pages_tile = kPsKeys >> box_shift;  // a tile's row pieces, each in one page
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -61,15 +61,14 @@ __global__ void __launch_bounds__(kPsWarps * 32, kDPL <= 4 ? 2 : 1) paged_simt_k
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const PagedSpan sp = paged_span(a, kRT, kPsKeys, 1, s_red);
-  const long long c = blockIdx.x, end = min(sp.W, (c + 1) * sp.per);
-  long long pos = c * sp.per, base = sp.base;
-  for (int b = sp.b; b < a.B && pos < end; ++b) {
-    const int P = a.prefix_len[b];
-    bool bad = false;
-    const int n = paged_rows(a, b, P, &bad);
+  UnitWalk w = unit_walk(sp);
+  int tree = -1, n_act = 0;
+  while (unit_next(a, w, kRT, kPsKeys)) {
+    const int b = w.b, hk = w.hk, rt = w.rt, P = w.P, n = w.n, t0 = w.t0, t1 = w.t1;
+    const long long u0 = w.u0;
     const int32_t* table = a.table + (size_t)b * a.max_pages;
-    int n_act = n;
-    if (a.parent && n > 0) {
+    if (tree != b) n_act = n;
+    if (a.parent && tree != b) {
       // the tree, checked; its rows past the first padding row are inactive
       __syncthreads();
       if (threadIdx.x == 0) s_first_pad = n;
@@ -87,14 +86,7 @@ __global__ void __launch_bounds__(kPsWarps * 32, kDPL <= 4 ? 2 : 1) paged_simt_k
       __syncthreads();
       n_act = s_first_pad;
     }
-    for (int hk = 0; hk < a.Hkv && pos < end; ++hk) {
-      for (int rt = 0; rt * kRT < n * a.G && pos < end; ++rt) {
-        const int T_u = unit_tiles(a, P, n, rt, kRT, kPsKeys);
-        const long long u0 = base;
-        base += T_u;
-        if (pos >= base) continue;
-        const int t0 = (int)(pos - u0), t1 = (int)(min(base, end) - u0);
-        pos = u0 + t1;
+    tree = b;
         const int rows = unit_rows(a, n, rt, kRT);
         const int lo = unit_lo(a, P, rt, kRT), tile0 = lo / kPsKeys;
         const int hi = min(P + n_act, P + (rt * kRT + rows - 1) / a.G + 1);
@@ -237,8 +229,8 @@ __global__ void __launch_bounds__(kPsWarps * 32, kDPL <= 4 ? 2 : 1) paged_simt_k
           __syncthreads();
         }
         // ---- write the unit, or this CTA's part of it
-        const long long c0 = u0 / sp.per, c1 = (base - 1) / sp.per;
-        const int slot = unit_slot(c, sp.per, u0);
+        const long long c0 = u0 / sp.per, c1 = (w.u1 - 1) / sp.per;
+        const int slot = unit_slot(blockIdx.x, sp.per, u0);
 #pragma unroll
         for (int rw = 0; rw < kRPW; ++rw) {
           const int rr = warp * kRPW + rw, r = rt * kRT + rr, i = r / a.G, g = r % a.G;
@@ -305,8 +297,6 @@ __global__ void __launch_bounds__(kPsWarps * 32, kDPL <= 4 ? 2 : 1) paged_simt_k
 #pragma unroll
           for (int u = 0; u < kDPL; ++u) out[off + lane + 32 * u] = o[u] / L;
         }
-      }
-    }
   }
 }
 

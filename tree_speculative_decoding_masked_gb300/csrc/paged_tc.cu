@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   int* s_par = reinterpret_cast<int*>(sm + C::kOffPar);
   PtBars* bars = reinterpret_cast<PtBars*>(sm + C::kOffBar);
   volatile int* abort_flag = &bars->abort;
-  __shared__ unsigned long long s_red[34];
+  __shared__ unsigned long long s_red[kPagedRed];
   __shared__ int s_last;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -247,21 +247,18 @@ __global__ void __launch_bounds__(kPtThreads, 1)
 
   // ---- this CTA's pieces
   PagedSpan sp{};
-  long long pos = 0, end = 0, base = 0;
-  int b = 0, hk = 0, mp = 0;
+  UnitWalk w{};
   const size_t cta = ((size_t)blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;  // cluster schedule
   if constexpr (kStream) {
     sp = paged_span(a, RT, kPtKeys, 1, s_red);
-    pos = (long long)blockIdx.x * sp.per;
-    end = min(sp.W, pos + sp.per);
-    base = sp.base;
-    b = sp.b;
+    w = unit_walk(sp);
   } else {
-    b = blockIdx.z, hk = blockIdx.y, mp = pa.MP - 1 - (int)blockIdx.x / pa.splits;
+    w.b = blockIdx.z, w.hk = blockIdx.y, w.rt = pa.MP - 1 - (int)blockIdx.x / pa.splits;
   }
-  int loaded_b = -1, P = 0, n = 0, n_act = 0;
+  int loaded_b = -1, n_act = 0;
   bool first_piece = true;
-  while (kStream ? pos < end && b < a.B : first_piece) {
+  while (kStream ? unit_next(a, w, RT, kPtKeys) : first_piece) {
+    const int b = w.b, hk = w.hk, mp = w.rt;
     if (b != loaded_b) {
       // the first pass's tree rows are read beside the lengths, not after them
       const int t_first = min((int)threadIdx.x, a.N - 1);
@@ -270,10 +267,14 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         p_first = a.parent[(size_t)b * a.N + t_first];
         if (t_first > 0) p_before = a.parent[(size_t)b * a.N + t_first - 1];
       }
-      P = a.prefix_len[b];
-      bool bad = false;
-      n = n_act = paged_rows(a, b, P, &bad);
-      if (bad && threadIdx.x == 0) set_dev_status(a.dev_status, TV_DEV_BAD_PAGE);
+      if constexpr (!kStream) {
+        bool bad = false;
+        w.P = a.prefix_len[b];
+        w.n = paged_rows(a, b, w.P, &bad);
+        if (bad && threadIdx.x == 0) set_dev_status(a.dev_status, TV_DEV_BAD_PAGE);
+      }
+      const int n = w.n;
+      n_act = n;
       if (a.parent && n > 0) {
         // rows up to the first padding row (a tree with rows behind it is bad)
         int wrong = 0;
@@ -294,31 +295,18 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       }
       loaded_b = b;
     }
-    // the next unit of this CTA's range, and its key tiles [t_begin, t_begin + nt)
-    long long u0 = 0;
-    const int T_u = unit_tiles(a, P, n, mp, RT, kPtKeys);
+    const int P = w.P, n = w.n;
     const int lo = unit_lo(a, P, mp, RT);
-    int t_begin = lo / kPtKeys, nt_all = T_u;
     int split = 0;
-    if constexpr (kStream) {
-      u0 = base;
-      base += T_u;
-      if (pos >= base) {  // not this one
-        if (++mp * pa.tiles * NT >= n) {
-          mp = 0;
-          if (++hk >= a.Hkv) hk = 0, ++b;
-        }
-        continue;
-      }
-      t_begin += (int)(pos - u0);
-      nt_all = (int)(min(base, end) - pos);
-      pos += nt_all;
-    } else {
+    if constexpr (!kStream) {
+      const int T_u = unit_tiles(a, P, n, mp, RT, kPtKeys);
       split = blockIdx.x % pa.splits;
-      const int first = (int)((long long)T_u * split / pa.splits);
-      t_begin += first;
-      nt_all = (int)((long long)T_u * (split + 1) / pa.splits) - first;
+      w.t0 = (int)((long long)T_u * split / pa.splits);
+      w.t1 = (int)((long long)T_u * (split + 1) / pa.splits);
     }
+    const long long u0 = w.u0;
+    const int t_begin = lo / kPtKeys + w.t0;  // this piece's key tiles
+    int nt_all = w.t1 - w.t0;
     if (*abort_flag) nt_all = 0;  // a wait ran out: nothing more is computed, but cut units still count their parts
     const int key_end = P + n_act;  // rows from here on, and before lo, may hold anything
     int i0[2], ntx[2];
@@ -603,7 +591,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         have_o = done && ok && ntm > 0;
         if (done) ptx::tc_fence_after();
       }
-      const bool whole = kStream && u0 / sp.per == (base - 1) / sp.per;
+      const bool whole = kStream && u0 / sp.per == (w.u1 - 1) / sp.per;
       const int R = x * kPtRows + r;
       const size_t slot = kStream ? (size_t)unit_slot(blockIdx.x, sp.per, u0) : cta;
       const float inv = whole && l_run > 0.f ? 1.f / l_run : 0.f;
@@ -645,7 +633,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     __syncwarp();
 
     if constexpr (kStream) {
-      const long long c0 = u0 / sp.per, c1 = (base - 1) / sp.per;
+      const long long c0 = u0 / sp.per, c1 = (w.u1 - 1) / sp.per;
       if (c0 != c1) {
         __threadfence();
         __syncthreads();
@@ -659,11 +647,15 @@ __global__ void __launch_bounds__(kPtThreads, 1)
           const int x = (warp - 2) >> 2, r = (warp & 3) * 32 + lane, R = x * kPtRows + r;
           const int g = r / NT, node = i0[x] + r % NT;
           if (r < rows_used && node < n_act) {
+            auto stats = [&](long long cc) -> float2 {
+              return __ldcg(&a.ws_ml[(size_t)unit_slot(cc, sp.per, u0) * 2 * kPtRows + R]);
+            };
             float M = -INFINITY, L = 0.f;
-            for (long long cc = c0; cc <= c1; ++cc)
-              M = fmaxf(M, __ldcg(&a.ws_ml[(size_t)unit_slot(cc, sp.per, u0) * 2 * kPtRows + R]).x);
+#pragma unroll 4
+            for (long long cc = c0; cc <= c1; ++cc) M = fmaxf(M, stats(cc).x);
+#pragma unroll 4
             for (long long cc = c0; cc <= c1; ++cc) {
-              const float2 ml = __ldcg(&a.ws_ml[(size_t)unit_slot(cc, sp.per, u0) * 2 * kPtRows + R]);
+              const float2 ml = stats(cc);
               if (ml.x != -INFINITY) L = fmaf(ptx::ex2(ml.x - M), ml.y, L);
             }
             const float inv = L > 0.f ? 1.f / L : 0.f;
@@ -673,21 +665,29 @@ __global__ void __launch_bounds__(kPtThreads, 1)
               float ov[32];
 #pragma unroll
               for (int k = 0; k < 32; ++k) ov[k] = 0.f;
-              for (long long cc = c0; cc <= c1; ++cc) {
-                const int slot = unit_slot(cc, sp.per, u0);
-                const float2 ml = __ldcg(&a.ws_ml[(size_t)slot * 2 * kPtRows + R]);
-                if (ml.x == -INFINITY) continue;
-                const float w = ptx::ex2(ml.x - M);
-                const float4* src =
-                    reinterpret_cast<const float4*>(a.ws_o) + ((size_t)slot * (D / 4) + col / 4) * 2 * kPtRows + R;
+              // two parts' loads in flight together
+              for (long long cc = c0; cc <= c1; cc += 2) {
+                float wt[2];
+                float4 v[2][8];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  const float4 v = __ldcg(src + (size_t)k * 2 * kPtRows);
-                  ov[4 * k] = fmaf(w, v.x, ov[4 * k]);
-                  ov[4 * k + 1] = fmaf(w, v.y, ov[4 * k + 1]);
-                  ov[4 * k + 2] = fmaf(w, v.z, ov[4 * k + 2]);
-                  ov[4 * k + 3] = fmaf(w, v.w, ov[4 * k + 3]);
+                for (int u = 0; u < 2; ++u) {
+                  const long long from = min(cc + u, c1);
+                  const float2 ml = stats(from);
+                  wt[u] = cc + u > c1 || ml.x == -INFINITY ? 0.f : ptx::ex2(ml.x - M);
+                  const float4* src = reinterpret_cast<const float4*>(a.ws_o) +
+                                      ((size_t)unit_slot(from, sp.per, u0) * (D / 4) + col / 4) * 2 * kPtRows + R;
+#pragma unroll
+                  for (int k = 0; k < 8; ++k) v[u][k] = __ldcg(src + (size_t)k * 2 * kPtRows);
                 }
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                  for (int k = 0; k < 8; ++k) {
+                    ov[4 * k] = fmaf(wt[u], v[u][k].x, ov[4 * k]);
+                    ov[4 * k + 1] = fmaf(wt[u], v[u][k].y, ov[4 * k + 1]);
+                    ov[4 * k + 2] = fmaf(wt[u], v[u][k].z, ov[4 * k + 2]);
+                    ov[4 * k + 3] = fmaf(wt[u], v[u][k].w, ov[4 * k + 3]);
+                  }
               }
               uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + orow + col);
 #pragma unroll
@@ -699,11 +699,6 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             }
           }
         }
-      }
-      // the next unit
-      if (++mp * pa.tiles * NT >= n) {
-        mp = 0;
-        if (++hk >= a.Hkv) hk = 0, ++b;
       }
     } else {
       // the parts form one cluster, and each CTA merges its share of the rows.  They meet in L2, not in
