@@ -571,7 +571,7 @@ TV_API tv_status tv_rotary(const tv_rows* x, void* out, const int32_t* pos, cons
  * Paged caches.  k, v: [num_pages][Hkv][page_size][D]; cache row r of sequence b is row
  * r mod page_size of page page_table[b][r / page_size].  prefix_len[b] = P_b rows are
  * committed; row P_b + t belongs to new row (tree node) t of the current call.
- * page_size: a power of two, 8..1024; max_pages * page_size < 2^31.
+ * page_size: a power of two, 8..1024; max_pages * page_size <= 2^30.
  * Sequences may share pages of committed rows; a page that receives rows of two
  * sequences in one call holds either's.  Table entries that no row of the call needs may
  * hold anything.  On the device: P_b < 0, rows past max_pages pages, n_rows[b] outside
@@ -622,8 +622,8 @@ TV_API tv_status tv_append_kv_paged(const tv_rows* k, const tv_rows* v, const tv
  * 1 <= N <= 65536 (trees 1024), G * N < 2^24.  q, out and the caches 16-byte aligned.
  * Workspace: tv_paged_attention_workspace_size(...) bytes, 16-byte aligned, zero-filled
  * once; calls that share it must not overlap on the GPU.
- * Errors: as tv_tree_attention; scale, softcap < 0 or not finite, window < 0 ->
- * TV_ERR_VALUE; workspace missing or small -> TV_ERR_WORKSPACE.
+ * Errors: as tv_tree_attention; scale, softcap < 0 or not finite, scale / softcap beyond fp32,
+ * window < 0 -> TV_ERR_VALUE; workspace missing or small -> TV_ERR_WORKSPACE.
  */
 TV_API size_t tv_paged_attention_workspace_size(int B, int Hq, int Hkv, int D, int N, int page_size,
                                                 int max_pages, tv_dtype dtype);

@@ -135,7 +135,7 @@ def test_rotary_and_append_refusals(lib):  # noqa: F811
     assert app(q=_rows()) == app(q=_rows(), qo=FAKE, rope=NULL) == app(q=_rows(None), qo=FAKE) == -1
     assert app(dt=9) == -3
     for kw in (dict(kv=_kv(ps=4)), dict(kv=_kv(ps=24)), dict(kv=_kv(ps=2048)), dict(kv=_kv(pages=0)),
-               dict(kv=_kv(width=0)), dict(kv=_kv(width=1 << 28)), dict(kv=_kv(pages=1 << 30), Hkv=4), dict(N=0),
+               dict(kv=_kv(width=0)), dict(kv=_kv(width=1 << 28)), dict(kv=_kv(width=(1 << 26) + 1)), dict(kv=_kv(pages=1 << 30), Hkv=4), dict(N=0),
                dict(q=_rows(), qo=FAKE, Hq=0), dict(rope=_rope(rot=128))):
         assert app(**kw) == -2, kw
     assert app(kv=_kv(k=0x1008)) == app(kv=_kv(v=0x1004)) == app(D=12, rope=NULL) == app(k=_rows(0x1001)) == -5
@@ -156,7 +156,7 @@ def test_attention_and_commit_refusals(lib):  # noqa: F811
                dict(kv=_kv(ps=12)), dict(Hq=2048, N=65536)):
         assert att(**kw) == -2, kw
     for kw in (dict(scale=-1.0), dict(scale=math.inf), dict(scale=math.nan), dict(cap=-1.0), dict(cap=math.nan),
-               dict(cap=math.inf), dict(win=-1)):
+               dict(cap=math.inf), dict(win=-1), dict(cap=1e-45), dict(scale=1e30, cap=1e-20)):
         assert att(**kw) == -8, kw
     assert att(q=ODD) == att(out=ctypes.c_void_p(0x1008)) == att(kv=_kv(k=0x1004)) == -5
     need = size(1, 4, 2, 64, 3, 16, 4, 0)

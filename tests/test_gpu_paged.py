@@ -193,6 +193,24 @@ def test_persistent_schedule(shape, tree_, window):
 
 
 @pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("N", [1, 11])
+@pytest.mark.parametrize("D", [32, 64, 96, 128, 160, 192, 224, 256])
+def test_persistent_schedule_of_every_head_size(D, N, bf16):
+    g = synth.rng(1190 + D + N)
+    B = 170 if D <= 64 else 80
+    prefix = [(53 * b) % 150 for b in range(B)]
+    _attend_check(g, B, 2, 1, D, 8, prefix, N, n_rows=[(b % (N + 1)) for b in range(B)], bf16=bf16, window=100,
+                  softcap=15.0)
+
+
+def test_equal_units_are_taken_whole():
+    # 80 units of one length: one a CTA, uncut; a lone longer one changes that
+    g = synth.rng(1195)
+    for longest in (330, 1500):
+        _attend_check(g, 10, 32, 8, 64, 64, [longest] + [330] * 9, 20)
+
+
+@pytest.mark.parametrize("bf16", [True, False])
 def test_deep_and_wide_trees(bf16):
     g = synth.rng(1150)
     N = 200

@@ -396,7 +396,7 @@ static tv_status paged_checks(const tv_paged_kv* kv, int B, int Hkv, int N, int 
   if (B < 1 || Hkv < 1 || Hkv > kMaxRotaryHeads || N < 1 || D < 1 || D > kMaxRotaryDim) return TV_ERR_SHAPE;
   const int ps = kv->page_size;
   if (ps < 8 || ps > 1024 || (ps & (ps - 1)) || kv->num_pages < 1 || kv->max_pages < 1) return TV_ERR_SHAPE;
-  if ((long long)kv->max_pages * ps > 0x7fffffffLL || (long long)kv->num_pages * Hkv > 0x7fffffffLL)
+  if ((long long)kv->max_pages * ps > (1LL << 30) || (long long)kv->num_pages * Hkv > 0x7fffffffLL)
     return TV_ERR_SHAPE;
   if (!aligned16(kv->k) || !aligned16(kv->v) || (long long)D * (dtype == TV_BF16 ? 2 : 4) % 16) return TV_ERR_ALIGN;
   return TV_OK;
@@ -460,6 +460,8 @@ tv_status tv_paged_attention(const void* q, void* out, const tv_paged_kv* kv, co
   if (s != TV_OK) return s;
   if (!paged_attn_shape(B, Hq, Hkv, N, D) || (parent && N > kMaxNodes)) return TV_ERR_SHAPE;
   if (!(scale >= 0.f) || isinf(scale) || !(softcap >= 0.f) || isinf(softcap) || window < 0) return TV_ERR_VALUE;
+  if (scale == 0.f) scale = 1.f / sqrtf((float)D);
+  if (softcap > 0.f && isinf(4.f * scale / softcap)) return TV_ERR_VALUE;
   if (!aligned16(q) || !aligned16(out)) return TV_ERR_ALIGN;
   const size_t need = paged_attn_ws(B, Hq, Hkv, D, N, dtype);
   if (need && (!workspace || ws_bytes < need)) return TV_ERR_WORKSPACE;
@@ -469,7 +471,7 @@ tv_status tv_paged_attention(const void* q, void* out, const tv_paged_kv* kv, co
   a.table = kv->page_table, a.prefix_len = kv->prefix_len, a.parent = parent, a.n_rows = n_rows;
   a.B = B, a.Hq = Hq, a.Hkv = Hkv, a.G = Hq / Hkv, a.D = D, a.N = N;
   a.num_pages = kv->num_pages, a.page_shift = log2_exact(kv->page_size), a.max_pages = kv->max_pages;
-  a.scale = scale == 0.f ? 1.f / sqrtf((float)D) : scale;
+  a.scale = scale;
   a.cap = softcap;
   a.window = window;
   a.dev_status = dev_status;

@@ -46,8 +46,9 @@ __global__ void __launch_bounds__(kPfThreads, kD <= 64 ? 2 : 1)
   float* s_k = pf_smem + S::kOffK;
   float* s_v = pf_smem + S::kOffV;
   float* s_p = pf_smem + S::kOffP;
-  __shared__ unsigned long long s_red[kPagedRed];
-  __shared__ uint32_t s_vis[kPfRows][kMaxNodes / 32];
+  __shared__ __align__(8) uint32_t s_vis[kPfRows][kMaxNodes / 32];
+  unsigned long long* s_red = reinterpret_cast<unsigned long long*>(s_vis);  // before the first unit
+  static_assert(sizeof(s_vis) >= kPagedRed * 8, "scratch of the division");
   __shared__ int s_par[kMaxNodes];
   __shared__ int s_lo[kPfRows], s_hi[kPfRows], s_page[2][kPfKeys / 8], s_first_pad, s_last;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
@@ -63,6 +64,7 @@ __global__ void __launch_bounds__(kPfThreads, kD <= 64 ? 2 : 1)
   UnitWalk w{};
   if constexpr (kStream) {
     sp = paged_span(a, kPfRows, kPfKeys, 1, s_red);
+    __syncthreads();
     w = unit_walk(sp);
   } else {
     // the cluster's unit, and this CTA's part of its tiles

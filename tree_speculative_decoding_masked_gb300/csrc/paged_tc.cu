@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   UnitWalk w{};
   const size_t cta = ((size_t)blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;  // cluster schedule
   if constexpr (kStream) {
-    sp = paged_span(a, RT, kPtKeys, 1, s_red);
+    sp = paged_span<true>(a, RT, kPtKeys, 1, s_red);
     w = unit_walk(sp);
   } else {
     w.b = blockIdx.z, w.hk = blockIdx.y, w.rt = pa.MP - 1 - (int)blockIdx.x / pa.splits;
@@ -438,43 +438,52 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     } else if (warp == 10) {
       // ---------------------------------------------------------------- PV issuer
       constexpr uint32_t idO = ptx::idesc_bf16(kPtRows, D, false, true);
-      bool ok = true;
-      for (int t = 0; t < nt; ++t) {
-        const int vs = t % kPtSlots, buf = t & 1;
+      // only the first and last tile can hold V rows that may be anything; the warp zeroes them
+      // (their weights are zero too) before its lane 0 issues that tile.  A loop that kept all
+      // lanes together for every tile cost 3 %
+      auto edge = [&](int t) -> bool {
         const int j0 = (t_begin + t) * kPtKeys;
-        if (j0 < lo || j0 + kPtKeys > key_end) {
-          // V rows that may hold anything: zero (their weights are zero too)
-          ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars->v_full[vs], (t / kPtSlots) & 1, abort_flag));
-          if (!ok) break;
-          for (int r = lane; r < kPtKeys; r += 32)
-            if (j0 + r < lo || j0 + r >= key_end)
-              for (int db = 0; db < C::kDB; ++db) {
-                uint4* row =
-                    reinterpret_cast<uint4*>(sV + vs * C::kTileBytes + (r >> 3) * C::kGroup + db * 1024 + (r & 7) * 128);
+        return t >= 0 && t < nt && (j0 < lo || j0 + kPtKeys > key_end);
+      };
+      auto zero_rows = [&](int t) {
+        const int vs = t % kPtSlots, j0 = (t_begin + t) * kPtKeys;
+        if (!ptx::mbar_wait(&bars->v_full[vs], (t / kPtSlots) & 1, abort_flag)) return;
+        for (int r = lane; r < kPtKeys; r += 32)
+          if (j0 + r < lo || j0 + r >= key_end)
+            for (int db = 0; db < C::kDB; ++db) {
+              uint4* row =
+                  reinterpret_cast<uint4*>(sV + vs * C::kTileBytes + (r >> 3) * C::kGroup + db * 1024 + (r & 7) * 128);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) row[k] = make_uint4(0, 0, 0, 0);
-              }
-          ptx::fence_proxy_async_smem();
-          __syncwarp();
-        }
-        if (lane == 0) {
-          ok = ptx::mbar_wait(&bars->v_full[vs], (t / kPtSlots) & 1, abort_flag);
-          const uint64_t vd = ptx::sdesc_sw128(ptx::smem_addr(sV + vs * C::kTileBytes), 1024, C::kGroup);
+              for (int k = 0; k < 8; ++k) row[k] = make_uint4(0, 0, 0, 0);
+            }
+        ptx::fence_proxy_async_smem();
+      };
+      auto issue = [&](int t) -> bool {
+        const int vs = t % kPtSlots, buf = t & 1;
+        if (!ptx::mbar_wait(&bars->v_full[vs], (t / kPtSlots) & 1, abort_flag)) return false;
+        const uint64_t vd = ptx::sdesc_sw128(ptx::smem_addr(sV + vs * C::kTileBytes), 1024, C::kGroup);
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (t >= ntx[x] || !ok) continue;
-            ok = ptx::mbar_wait(&bars->p_full[x][buf], (t >> 1) & 1, abort_flag);
-            if (!ok) continue;
-            ptx::tc_fence_after();
-            const uint32_t pcol = tmem + x * kPtRows + buf * kPtKeys;  // P: 8 columns per 16 keys
-            pt_pv_product(tmem + C::kColO + x * kPtRows, pcol, vd, 2 * C::kGroup / 16, idO, t > 0 ? 1u : 0u);
-            ptx::mma_commit(&bars->pv_done[x][buf]);
-          }
-          if (ok) ptx::mma_commit(&bars->v_empty[vs]);
+        for (int x = 0; x < 2; ++x) {
+          if (t >= ntx[x]) continue;
+          if (!ptx::mbar_wait(&bars->p_full[x][buf], (t >> 1) & 1, abort_flag)) return false;
+          ptx::tc_fence_after();
+          pt_pv_product(tmem + C::kColO + x * kPtRows, tmem + x * kPtRows + buf * kPtKeys, vd, 2 * C::kGroup / 16, idO,
+                        t > 0 ? 1u : 0u);  // P: 8 columns per 16 keys
+          ptx::mma_commit(&bars->pv_done[x][buf]);
         }
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-        if (!ok) break;
-      }
+        ptx::mma_commit(&bars->v_empty[vs]);
+        return true;
+      };
+      const int last = nt - 1;
+      if (edge(0)) zero_rows(0);
+      __syncwarp();
+      bool ok = true;
+      if (lane == 0)
+        for (int t = 0; ok && t < last; ++t) ok = issue(t);
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      if (ok && last > 0 && edge(last)) zero_rows(last);
+      __syncwarp();
+      if (lane == 0 && ok && last >= 0) issue(last);
       if (lane == 0) {
         ptx::mma_commit(&bars->o_done);
         pt_drain(&bars->o_done, 0, abort_flag);
