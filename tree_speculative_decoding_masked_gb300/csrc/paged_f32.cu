@@ -180,6 +180,7 @@ __global__ void __launch_bounds__(kPfThreads, kD <= 64 ? 2 : 1)
 #pragma unroll
           for (int u = 0; u < kU; ++u) acc[x][u][0] = acc[x][u][1] = 0.f;
         }
+        const bool live = (ty & ~1) * 4 < rows;  // some of this warp's eight rows are rows
         load_tile(t0, 0);
         for (int t = t0; t < t1; ++t) {
           const int buf = S::kBufs == 2 ? (t - t0) & 1 : 0;
@@ -194,6 +195,11 @@ __global__ void __launch_bounds__(kPfThreads, kD <= 64 ? 2 : 1)
           }
           __syncthreads();
           if ((int)threadIdx.x < pages_tile) s_page[t & 1][threadIdx.x] = ahead;  // tile t + 2's; t's are used up
+          if (!live) {
+            __syncthreads();
+            if (S::kBufs == 1 && t + 1 < t1) load_tile(t + 1, 0);
+            continue;
+          }
           // ---- scores
           float s[4][4];
 #pragma unroll
@@ -219,8 +225,10 @@ __global__ void __launch_bounds__(kPfThreads, kD <= 64 ? 2 : 1)
                 s[x][y] = fmaf(qf[x].w, kf[y].w, s[x][y]);
               }
           }
-          // ---- weights
+          // ---- weights, against a running reference that moves when a score exceeds it by 5.5 (e^5.5
+          // = 245): the maximum over a row's 16 threads is taken only then
           const int j0 = (tile0 + t) * kPfKeys;
+          bool grow = false;
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             if (a.cap > 0.f) {
@@ -238,18 +246,27 @@ __global__ void __launch_bounds__(kPfThreads, kD <= 64 ? 2 : 1)
                 if (!vis) s[x][y] = -INFINITY;
               }
             }
-            float mx = fmaxf(fmaxf(s[x][0], s[x][1]), fmaxf(s[x][2], s[x][3]));
+            grow |= fmaxf(fmaxf(s[x][0], s[x][1]), fmaxf(s[x][2], s[x][3])) > m[x] + 5.5f;
+          }
+          if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-            for (int o = 1; o < 16; o *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            // expf of a difference, not 2^(z log2 e - m): the product's rounding would cost |z| 2^-24
-            const float mnew = fmaxf(m[x], mx), ref = mnew == -INFINITY ? 0.f : mnew;
-            if (mnew > m[x]) {
-              const float f = expf(m[x] - ref);  // 0 from -inf
-              l[x] *= f;
+            for (int x = 0; x < 4; ++x) {
+              float mx = fmaxf(fmaxf(s[x][0], s[x][1]), fmaxf(s[x][2], s[x][3]));
 #pragma unroll
-              for (int u = 0; u < kU; ++u) acc[x][u][0] *= f, acc[x][u][1] *= f;
-              m[x] = mnew;
+              for (int o = 1; o < 16; o *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+              if (mx > m[x]) {
+                const float f = expf(m[x] - mx);  // 0 from -inf
+                l[x] *= f;
+#pragma unroll
+                for (int u = 0; u < kU; ++u) acc[x][u][0] *= f, acc[x][u][1] *= f;
+                m[x] = mx;
+              }
             }
+          }
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            // expf of a difference, not 2^(z log2 e - m): the product's rounding would cost |z| 2^-24
+            const float ref = m[x] == -INFINITY ? 0.f : m[x];
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
               const float p = expf(s[x][y] - ref);
