@@ -197,6 +197,10 @@ def test_binding_refusals(lib):  # noqa: F811
     kc, table, pre = _Fake((9, 2, 16, 64)), _Fake((2, 4), i32), _Fake((2,), i32)
     k = _Fake((2, 2, 3, 64))
     refuse("k_cache and v_cache", tv.append_kv_paged, k, k, kc, _Fake((9, 2, 8, 64)), table, pre)
+    refuse("must be contiguous", tv.append_kv_paged, k, k, kc,
+           _Fake((9, 2, 16, 64), stride=(2048, 64, 128, 1)), table, pre)
+    refuse("one device", tv.append_kv_paged, k, k, kc, _Fake((9, 2, 16, 64), device="cuda:1"), table, pre)
+    refuse("CUDA", tv.append_kv_paged, k, k, kc, torch.zeros((9, 2, 16, 64), dtype=torch.bfloat16), table, pre)
     refuse("k must have shape", tv.append_kv_paged, _Fake((2, 3, 3, 64)), k, kc, kc, table, pre)
     refuse("v must have shape", tv.append_kv_paged, k, _Fake((2, 2, 4, 64)), kc, kc, table, pre)
     refuse("v must be torch.bfloat16", tv.append_kv_paged, k, _Fake((2, 2, 3, 64), f32), kc, kc, table, pre)

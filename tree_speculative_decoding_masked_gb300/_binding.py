@@ -734,10 +734,15 @@ def _paged_kv(k_cache, v_cache, page_table, prefix_len, index):
     dtype = k_cache.dtype
     if v_cache.dtype is not dtype or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must match")
+    if k_cache.get_device() != index:
+        _wrong_device("k_cache", k_cache, index)
+    if v_cache.get_device() != index:
+        _wrong_device("v_cache", v_cache, index)
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise ValueError("k_cache and v_cache must be contiguous")
     pages, Hkv, ps, D = shape
     B, width = page_table.shape
-    kv = _pack_paged_kv(_tensor("k_cache", k_cache, dtype, shape, index),
-                        _tensor("v_cache", v_cache, dtype, shape, index),
+    kv = _pack_paged_kv(k_cache.data_ptr(), v_cache.data_ptr(),
                         _tensor("page_table", page_table, torch.int32, (B, width), index),
                         _tensor("prefix_len", prefix_len, torch.int32, (B,), index), pages, ps, width)
     return kv, B, Hkv, ps, width, D
