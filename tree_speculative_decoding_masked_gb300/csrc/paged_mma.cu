@@ -3,9 +3,10 @@
 // With few query rows a KV head every key is read for a handful of products: the
 // work is a stream of K and V pages from HBM and the kernel's job is to keep enough of
 // them in flight.  Four warps fetch 64-key tiles by TMA (a box per page piece, dealt to them
-// in turn: one warp's issue of the 8 boxes of 16-row pages took 0.65 us a tile, twice what
-// an SM's share of HBM needs) into a ring and run ahead across sequences and heads; groups of four warps take the tiles in
-// turn, a warp 16 keys of a tile, by warp-level MMAs on shared memory:
+// in turn: one warp's issue of the 8 boxes of 16-row pages took 0.65 us a tile, as long as
+// an SM's share of HBM takes to bring them) into a ring and run ahead across sequences and
+// heads; groups of four warps take the tiles in turn, a warp 16 keys of a tile, by warp-level
+// MMAs on shared memory:
 //   S^T = K Q^T  (16 keys x 8 rows a product),  O^T += V^T P^T  (16 columns x 8 rows).
 // With the rows on the products' short side their number follows R / 8: at 4 rows a
 // 128-column tile costs a warp 16 MMAs, where rows on the long side would take 32 (and a
@@ -14,7 +15,7 @@
 // bf16 for the second product.  The warps' O's are added in warp order when the unit ends,
 // so results do not depend on timing.
 //
-// Two schedules.  Units (sequence, KV head, row tile) up to the SM count run as one cluster
+// Two schedules.  Units (sequence, KV head, row tile) up to half the SMs run as one cluster
 // each, whose CTAs take equal parts of the unit's keys and merge through distributed shared
 // memory (the copies of short and long units share the memory system, so ragged lengths
 // cost little).  More units are divided equally, tile by tile, over a persistent grid
@@ -26,8 +27,8 @@ namespace tv {
 constexpr int kPmKeys = 64;
 constexpr int kPmProducers = 4;
 constexpr int kPmMaxSplits = 8;  // portable cluster size
-constexpr int kPmMerge = 8;   // parts whose loads are in flight together
-constexpr int kPmMinTiles = 2;  // tiles of a CTA's range: fewer only add parts to merge
+constexpr int kPmMerge = 8;      // parts whose loads are in flight together
+constexpr int kPmMinTiles = 2;   // tiles of a CTA's range: fewer only add parts to merge
 
 template <int kD, int kRT>
 struct PmCfg {
@@ -49,14 +50,16 @@ struct PmCfg {
   static constexpr int kOffPar = kOffVis + kRT * (kMaxNodes / 32) * 4;
   static constexpr int kInBytes = kOffPar + kMaxNodes * 4 - kOffU;
   static constexpr int kOStride = kD + 4;               // floats: a store's four row pairs on different banks
-  static constexpr int kRegions = kD == 256 ? 1 : kD == 128 && kRT == 16 ? 2 : kWarps / 2;  // warps that hand over their O at once
+  // warps that hand over their O at once
+  static constexpr int kRegions = kD == 256 ? 1 : kD == 128 && kRT == 16 ? 2 : kWarps / 2;
   static constexpr int kOBytes = kRegions * kRT * kOStride * 4;
   static constexpr int kOffBar = kOffU + (kInBytes > kOBytes ? kInBytes : kOBytes);
   static constexpr int kSmem = kOffBar + 256 + 1024;
   // a slot's tiles alternate between no two groups: a group that skipped a slot's earlier tile
   // could take that tile's unfinished phase for its own finished one
   static_assert(kWarps == 4 || kStages % 2 == 0, "each slot belongs to one group");
-  static_assert(kSmem + 4096 <= 232448, "shared memory per CTA");
+  static_assert(kSmem + 8192 <= 232448,  // beside the static arrays
+                "shared memory per CTA");
   static_assert(kD / 16 * kNT * 4 <= 128, "O fits in registers");
 };
 
@@ -160,7 +163,8 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT>::kThreads, 1)
     // ahead and checked when it is used
     const int per_piece = 2 * (wide ? 1 : C::kDB);
     const int box_shift = min(a.page_shift, C::kDB == 1 || wide ? 6 : 3);
-    const int boxes = (kPmKeys >> box_shift) * per_piece, mine = boxes / kPmProducers + (warp - C::kWarps < boxes % kPmProducers);
+    const int boxes = (kPmKeys >> box_shift) * per_piece;
+    const int mine = boxes / kPmProducers + (warp - C::kWarps < boxes % kPmProducers);
     const int box = lane * kPmProducers + warp - C::kWarps;  // this lane's
     const int pi = box / per_piece, part = box % per_piece;
     const uint32_t box_bytes = (uint32_t)(256 * C::kDB / per_piece) << box_shift;
@@ -180,13 +184,13 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT>::kThreads, 1)
       const int lo = unit_lo(a, w.P, w.rt, kRT), tile0 = lo / kPmKeys;
       const int hi = min(w.P + active, w.P + (w.rt * kRT + unit - 1) / a.G + 1);
       const int32_t* table = a.table + (size_t)w.b * a.max_pages;
-      // the table entry of this lane's box in tile t, -1 where the box holds no needed row
+      // whether this lane's box in tile t holds a needed row, and its table entry
       auto needed = [&](int t) -> bool {
         const int j = (tile0 + t) * kPmKeys + (pi << box_shift);
         return t < w.t1 && lane < mine && j < hi && j + (1 << box_shift) > lo;
       };
       auto entry = [&](int t) -> int {
-        return needed(t) ? __ldg(table + (((tile0 + t) * kPmKeys + (pi << box_shift)) >> a.page_shift)) : 0;
+        return needed(t) ? table[((tile0 + t) * kPmKeys + (pi << box_shift)) >> a.page_shift] : 0;
       };
       int next = entry(w.t0);
       for (int t = w.t0; t < w.t1; ++t, ++it) {

@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         return t < nt && in_tile && j < key_end && j + (1 << box_shift) > lo;
       };
       auto entry = [&](int t) -> int {
-        return needed(t) ? __ldg(table + (((t_begin + t) * kPtKeys + (pi << box_shift)) >> a.page_shift)) : 0;
+        return needed(t) ? table[((t_begin + t) * kPtKeys + (pi << box_shift)) >> a.page_shift] : 0;
       };
       auto checked = [&](int t, int page) -> int {
         if (!needed(t)) return -1;
