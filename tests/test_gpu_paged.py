@@ -589,6 +589,190 @@ def test_commit_reports_bad_paths_and_pages():
         assert int(st.item()) == want, (acc, n, t1)
 
 
+# ---- calls that the tests above do not make
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("N", [1, 60])
+def test_no_active_rows_at_all(bf16, N):
+    g = synth.rng(3000)
+    _attend_check(g, 3, 8, 2, 64, 16, [0, 5, 200], N, n_rows=[0, 0, 0], bf16=bf16)
+    pool = torch.full((4, 2, 16, 64), 2.0, dtype=torch.bfloat16 if bf16 else torch.float32, device=dev())
+    x = torch.ones((1, 2, N, 64), dtype=pool.dtype, device=dev())
+    st = _status()
+    tv.append_kv_paged(x, x, pool, pool.clone(), i32([[0, 1, 2, 3, 0, 0]]), i32([3]), n_rows=i32([0]), dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0 and bool((pool == 2.0).all())
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("N", [1, 40])
+def test_shared_and_repeated_pages(bf16, N):
+    # two sequences with one prefix's pages, and a table that names a page twice
+    g = synth.rng(3050 + N)
+    B, Hq, Hkv, D, ps, P = 2, 8, 2, 64, 16, 64
+    kc, vc, table = _pages(g, 1, Hkv, D, ps, [P + 5 * ps], P + 5 * ps, bf16)
+    first = table[0, :9]
+    shared = np.stack([np.concatenate([first[:4], first[4:7]]), np.concatenate([first[[0, 1, 0, 1]], first[6:9]])])
+    shared = shared.astype(np.int32)
+    q = synth.normal(g, (B, Hq, N, D), 1.0, bf16)
+    got = host(tv.paged_attention(to_dev(q, bf16), to_dev(kc, bf16), to_dev(vc, bf16), i32(shared), i32([P, P])))
+    ref, mass, big = paged.attention(q, kc, vc, shared, [P, P])
+    e = 2 * D * 2.0 ** -23 * big[..., None] + 2.0 ** -22 + (P + N) * 2.0 ** -23
+    tol = (2 * e + (2.0 ** -8 if bf16 else 0)) * mass + _unit(bf16) * np.abs(ref)
+    assert np.max(np.abs(got - ref) / tol) <= 1.0
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("N", [1, 100])
+def test_pages_past_the_31st_bit(bf16, N):
+    # a cache of more than 2^31 elements; the sequence sits in its last pages.  The calls on the last
+    # pages give what they give on a small cache, bit for bit
+    g = synth.rng(3100 + N)
+    Hq, Hkv, D, ps, P = 16, 8, 128, 1024, 1500
+    dt = torch.bfloat16 if bf16 else torch.float32
+    big = (1 << 31) // (Hkv * ps * D) + 4
+    gen = torch.Generator(device=dev())
+    gen.manual_seed(5)
+    small_k, small_v = (torch.randn((3, Hkv, ps, D), generator=gen, device=dev()).to(dt) for _ in range(2))
+    qkv = torch.randn((1, N, Hq + 2 * Hkv, D), generator=gen, device=dev()).to(dt).transpose(1, 2)
+    rope = tv.rotary_frequencies(D)
+    acc = i32([sorted(g.choice(np.arange(1, max(N, 2)), min(N - 1, 12), replace=False)) + [-1] * (N - min(N - 1, 12))])
+    results = []
+    for pages, at in ((3, 0), (big, big - 3)):
+        kc, vc = (torch.zeros((pages, Hkv, ps, D), dtype=dt, device=dev()) for _ in range(2))
+        kc[at:at + 3], vc[at:at + 3] = small_k, small_v
+        table, pre, st = i32([[at + 2, at]]), i32([P]), _status()
+        q = tv.append_kv_paged(qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:], kc, vc, table, pre, rope=rope, q=qkv[:, :Hq],
+                               dev_status=st)
+        out = tv.paged_attention(q, kc, vc, table, pre, dev_status=st)
+        tv.commit_accepted_kv_paged(kc, vc, table, pre, acc, i32([min(N - 1, 12)]), dev_status=st)
+        torch.cuda.synchronize()
+        assert int(st.item()) == 0
+        results.append((q, out, kc[at:at + 3].clone(), vc[at:at + 3].clone()))
+        del kc, vc
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+def test_two_calls_at_once(bf16):
+    # two streams, a workspace each
+    g = synth.rng(3150)
+    dt = torch.bfloat16 if bf16 else torch.float32
+    calls = []
+    for N, Hkv in ((1, 2), (70, 2), (30, 32), (1, 40)):
+        kc, vc, table = _pages(g, 3, Hkv, 64, 16, [600, 40, 333 + N], 700, bf16)
+        args = (to_dev(synth.normal(g, (3, 2 * Hkv, N, 64), 1.0, bf16), bf16), to_dev(kc, bf16), to_dev(vc, bf16),
+                i32(table), i32([600 - N, 40 - min(N, 30), 333]))
+        n = tv.paged_attention_workspace_size(3, 2 * Hkv, Hkv, 64, N, 16, table.shape[1], dt)
+        kw = dict(workspace=torch.zeros(max(n, 256), dtype=torch.uint8, device=dev()), n_rows=i32([N, min(N, 30), N]),
+                  out=torch.zeros_like(args[0]))
+        calls.append((args, kw, tv.paged_attention(*args, **dict(kw, out=torch.zeros_like(args[0]))).clone()))
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (args, kw, _), s in zip(calls, streams):
+            with torch.cuda.stream(s):
+                tv.paged_attention(*args, **kw)
+    torch.cuda.synchronize()
+    for _, kw, ref in calls:
+        assert torch.equal(kw["out"], ref)
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+def test_on_a_share_of_the_device(bf16):
+    try:
+        tv.set_sm_partition(0, 17)
+        g = synth.rng(3200)
+        for N in (1, 50):
+            _attend_check(g, 12, 16, 8, 64, 16, [(97 * b) % 400 for b in range(12)], N, bf16=bf16)
+    finally:
+        tv.set_sm_partition(0, 0)
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("Hq,Hkv,D,N,P", [(1, 1, 32, 65536, 3), (2, 1, 64, 20000, 777)])
+def test_long_chunks(bf16, Hq, Hkv, D, N, P):
+    # rows from all over a long chunk against 64-bit sums
+    ps = 128
+    dt = torch.bfloat16 if bf16 else torch.float32
+    gen = torch.Generator(device=dev())
+    gen.manual_seed(N)
+    width = (P + N + ps - 1) // ps
+    table = torch.randperm(width, generator=gen, device=dev()).int()[None]
+    kc, vc = (torch.randn((width, Hkv, ps, D), generator=gen, device=dev()).to(dt) for _ in range(2))
+    q = torch.randn((1, Hq, N, D), generator=gen, device=dev()).to(dt)
+    st = _status()
+    out = tv.paged_attention(q, kc, vc, table, i32([P]), dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    k, v = (c[table[0].long()].permute(1, 0, 2, 3).reshape(Hkv, width * ps, D).double() for c in (kc, vc))
+    for i in (0, 1, 62, 63, 64, 127, 128, 4095, 4096, 9999, N - 65, N - 64, N - 2, N - 1):
+        for h in range(Hq):
+            kk, vv, qi = k[0, :P + i + 1], v[0, :P + i + 1], q[0, h, i].double()
+            z = kk @ qi / math.sqrt(D)
+            p = torch.softmax(z, 0)
+            ref, mass = p @ vv, p @ vv.abs()
+            big = float((kk.abs() @ qi.abs()).max()) / math.sqrt(D)
+            # sums over a long row: partial sums of tiles, so the keys of a tile and the tiles count
+            e = 2 * D * 2.0 ** -23 * big + 2.0 ** -22 + (64 + (P + i) / 32) * 2.0 ** -23
+            tol = (2 * e + (2.0 ** -8 if bf16 else 0)) * mass + _unit(bf16) * ref.abs()
+            assert bool(((out[0, h, i].double() - ref).abs() <= tol).all()), (i, h)
+
+
+def test_a_captured_round_replays():
+    """append -> attention -> greedy verification -> commit, captured once; every replay is a round on
+    the lengths that the last one left, and equals the same calls made eagerly."""
+    g = synth.rng(3250)
+    B, Hq, Hkv, D, ps, N, V = 2, 8, 2, 64, 16, 20, 50
+    kc, vc, table = _pages(g, B, Hkv, D, ps, [300, 300], 300, True)
+    rope, st = tv.rotary_frequencies(D), _status()
+    par, tok = W.trees(g, B, N, 5, V)
+    logits = to_dev(W.planted_logits(g, par, tok, V, False, prob=0.9), False)
+    x = to_dev(synth.normal(g, (B, N, Hq + 2 * Hkv, D), 1.0, True), True).transpose(1, 2)
+    pard, tokd, td = i32(par), i32(tok), i32(table)
+
+    def setup():
+        s = dict(k=to_dev(kc, True), v=to_dev(vc, True), lens=i32([7, 40]))
+        s["q"] = torch.zeros((B, Hq, N, D), dtype=torch.bfloat16, device=dev())
+        s["out"], s["new"] = torch.zeros_like(s["q"]), i32([0, 0])
+        n = tv.paged_attention_workspace_size(B, Hq, Hkv, D, N, ps, table.shape[1], torch.bfloat16)
+        s["ws"] = torch.zeros(max(n, 256), dtype=torch.uint8, device=dev())
+        s["vws"] = torch.zeros(tv.verify_workspace_size(B, N, V, torch.float32, False), dtype=torch.uint8, device=dev())
+        s["prep"] = {}
+        return s
+
+    def one(s):
+        prep = tv.tree_prep(pard, 0, dev_status=st)
+        tv.append_kv_paged(x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], s["k"], s["v"], td, s["lens"], depth=prep["depth"],
+                           rope=rope, q=x[:, :Hq], q_out=s["q"], dev_status=st)
+        tv.paged_attention(s["q"], s["k"], s["v"], td, s["lens"], parent=pard, out=s["out"], workspace=s["ws"],
+                           dev_status=st)
+        res = tv.verify_greedy(logits, pard, tokd, workspace=s["vws"], dev_status=st)
+        tv.commit_accepted_kv_paged(s["k"], s["v"], td, s["lens"], res["accepted_nodes"], res["accept_len"],
+                                    new_len=s["new"], dev_status=st)
+        s["lens"].copy_(s["new"])
+
+    eager, captured, warm = setup(), setup(), setup()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        one(warm)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        one(captured)
+    for _ in range(4):
+        one(eager)
+        graph.replay()
+        torch.cuda.synchronize()
+        for key in ("lens", "q", "out"):
+            assert torch.equal(eager[key], captured[key]), key
+        for key in ("k", "v"):
+            assert torch.equal(eager[key].view(torch.int16), captured[key].view(torch.int16)), key
+    assert int(st.item()) == 0 and host(eager["lens"])[0] > 7 + 4
+
+
 # ---- the calls together
 
 @pytest.mark.parametrize("bf16", [True, False])
