@@ -33,6 +33,7 @@ struct PagedSpan {
   int b;            // where this CTA starts: sequence,
   long long base;   // and that sequence's first tile
   int whole;        // not 0: every unit counts as this many tiles, one unit per CTA
+  int tol;          // a cut this near to a unit's edge moves to the edge
 };
 constexpr int kPagedRed = 34 + 512;  // scratch of paged_span: CTAs of up to 512 threads
 
@@ -68,9 +69,11 @@ __device__ inline long long head_tiles_warp(const PagedAttn& a, int P, int n, in
 // whole against cut: 16 x 64 nodes over 1000 tokens 27.9 / 47.5 us, 8 x 128 nodes over 8000
 // 113.6 / 124.2, over 32768 413 / 424.
 template <bool kWhole = false>
-__device__ inline PagedSpan paged_span(const PagedAttn& a, int RT, int KT, int min_per, unsigned long long* red) {
+__device__ inline PagedSpan paged_span(const PagedAttn& a, int RT, int KT, int min_per, unsigned long long* red,
+                                       int tol = 0) {
   PagedSpan sp;
   sp.whole = 0;
+  sp.tol = tol;
   unsigned long long W = 0, mine = 0, at = 0;
   bool any_bad = false;
   // tiles of sequence b0 + threadIdx.x: by its own thread, or with many row tiles a warp each
@@ -178,8 +181,25 @@ struct UnitWalk {
   long long u0, u1;         // the unit's tiles
   int b, hk, rt, P, n;      // the unit; the sequence's committed and new rows
   int t0, t1;               // of the unit's tiles, those to take
-  int loaded, whole;
+  int loaded, whole, tol;
+  bool begun;
 };
+
+// Where the boundary p of two ranges, strictly inside unit [u0, u1), cuts it: at p, or at the nearer
+// edge if that is at most tol tiles away.
+__device__ __forceinline__ long long unit_cut(long long p, long long u0, long long u1, int tol) {
+  const long long l = p - u0, r = u1 - p;
+  return l <= min((long long)tol, r) ? u0 : r <= tol ? u1 : p;
+}
+// The CTAs c0..c1 that share the unit; c1 <= c0 where none cuts it.
+struct UnitCtas {
+  long long c0, c1;
+};
+__device__ __forceinline__ UnitCtas unit_ctas(const PagedSpan& sp, long long u0, long long u1) {
+  const long long l = min((long long)sp.tol, (u1 - u0) / 2), r = min((long long)sp.tol, (u1 - u0 - 1) / 2);
+  return {(u0 + l) / sp.per, (u1 - r - 1) / sp.per};
+}
+
 __device__ __forceinline__ UnitWalk unit_walk(const PagedSpan& sp) {
   UnitWalk w{};
   w.pos = sp.per * blockIdx.x;
@@ -188,6 +208,7 @@ __device__ __forceinline__ UnitWalk unit_walk(const PagedSpan& sp) {
   w.b = sp.b;
   w.loaded = -1;
   w.whole = sp.whole;
+  w.tol = sp.tol;
   return w;
 }
 __device__ inline bool unit_next(const PagedAttn& a, UnitWalk& w, int RT, int KT) {
@@ -229,19 +250,27 @@ __device__ inline bool unit_next(const PagedAttn& a, UnitWalk& w, int RT, int KT
       w.u1 = w.u0 + T;
       break;
     }
+    if (!w.begun) {
+      w.begun = true;
+      if (w.pos > w.u0) w.pos = unit_cut(w.pos, w.u0, w.u1, w.tol);
+      if (w.pos == w.u1) continue;
+    }
+    long long end = w.u1;
+    if (w.end < w.u1) end = unit_cut(w.end, w.u0, w.u1, w.tol);
+    if (end <= w.pos) return false;
     w.t0 = (int)(w.pos - w.u0);
-    w.t1 = (int)(min(w.u1, w.end) - w.u0);
-    w.pos = w.u0 + w.t1;
+    w.t1 = (int)(end - w.u0);
+    w.pos = end;
     if (w.whole) w.t1 = unit_tiles(a, w.P, w.n, w.rt, RT, KT);
     return true;
   }
   return false;
 }
 
-// The ranges that share the unit of tiles [u0, u1): CTAs u0 / per .. (u1 - 1) / per.  A CTA
-// parks the partial result of a unit it began inside in slot 2c and of one it leaves
-// unfinished in slot 2c + 1; the unit's counter is that of its first CTA (a CTA is the
-// first of one cut unit at most).
+// Of a cut unit [u0, u1), CTA c parks its partial result in slot 2c if the unit begins before the
+// CTA's range and in slot 2c + 1 if not: a CTA has one piece that a cut begins and one that a cut ends,
+// and if its range's first cut has moved to u0, none that a cut begins.  The unit's counter is
+// that of its first CTA (a CTA is the first of one cut unit at most).
 __device__ __forceinline__ int unit_slot(long long c, long long per, long long u0) {
   return (int)(2 * c + (u0 < c * per ? 0 : 1));
 }
