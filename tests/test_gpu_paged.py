@@ -296,6 +296,33 @@ def test_one_workspace_many_shapes(bf16, N):
         _attend_check(g, 1, 16, 1, 64, 16, [333], N, bf16=bf16, workspace=ws)
 
 
+# more units than CTAs, short and long ones mixed, empty sequences between them: ranges of several
+# pieces, cuts that move to a unit's edge and cuts that stay
+MANY = [(60, 16, 4, 128, 16, 24, 40, True), (500, 4, 1, 64, 8, 1, 80, False), (9, 8, 2, 128, 64, 300, 30, False),
+        (30, 8, 8, 64, 16, 33, 400, True), (420, 1, 1, 32, 8, 17, 60, False), (40, 8, 8, 128, 32, 3, 900, False),
+        (3, 8, 4, 64, 128, 700, 700, False), (150, 16, 2, 256, 64, 1, 500, False), (25, 8, 4, 128, 8, 60, 2500, True)]
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("B,Hq,Hkv,D,ps,N,P,tree_", MANY)
+def test_many_short_units(B, Hq, Hkv, D, ps, N, P, tree_, bf16):
+    g = synth.rng(23)
+    prefix = [int(x) for x in g.integers(0, P + 1, B)]
+    prefix[:3] = [0, P, 1]
+    n_rows = [int(x) for x in g.integers(0, N + 1, B)]
+    n_rows[0] = N
+    parent = np.stack([synth.random_parents(g, N, 8) for _ in range(B)]).astype(np.int32) if tree_ else None
+    if tree_:
+        for b in range(B):
+            parent[b, max(n_rows[b], 1):] = -1
+    window = 100 if N == 33 else 0
+    first = _attend_check(synth.rng(24), B, Hq, Hkv, D, ps, prefix, N, parent=parent, n_rows=n_rows, window=window,
+                          bf16=bf16)
+    again = _attend_check(synth.rng(24), B, Hq, Hkv, D, ps, prefix, N, parent=parent, n_rows=n_rows, window=window,
+                          bf16=bf16)
+    assert np.array_equal(first, again)
+
+
 @pytest.mark.parametrize("bf16", [True, False])
 @pytest.mark.parametrize("N,Hkv,tree_", [(1, 2, False), (40, 2, True), (150, 2, False), (50, 40, True)])
 def test_repeats_are_bit_equal_and_replay(bf16, N, Hkv, tree_):

@@ -34,6 +34,7 @@ struct PagedSpan {
   long long base;   // and that sequence's first tile
   int whole;        // not 0: every unit counts as this many tiles, one unit per CTA
   int tol;          // a cut this near to a unit's edge moves to the edge
+  int fix;          // what a unit costs beside its tiles, in tiles: each counts as so many more
 };
 constexpr int kPagedRed = 34 + 512;  // scratch of paged_span: CTAs of up to 512 threads
 
@@ -53,27 +54,28 @@ __device__ __forceinline__ int unit_tiles(const PagedAttn& a, int P, int n, int 
   return (hi + KT - 1) / KT - unit_lo(a, P, rt, RT) / KT;
 }
 // Tiles of one KV head of a sequence; a warp's lanes share the sum over its row tiles.
-__device__ inline long long head_tiles_warp(const PagedAttn& a, int P, int n, int RT, int KT, int whole) {
-  if (whole) return (long long)whole * ((n * a.G + RT - 1) / RT);
+__device__ inline long long head_tiles_warp(const PagedAttn& a, int P, int n, int RT, int KT, int whole, int fix) {
+  const int row_tiles = (n * a.G + RT - 1) / RT;
+  if (whole) return (long long)whole * row_tiles;
   unsigned long long s = 0;
   for (int rt = threadIdx.x & 31; rt * RT < n * a.G; rt += 32) s += unit_tiles(a, P, n, rt, RT, KT);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return (long long)s;
+  return (long long)s + (long long)fix * row_tiles;
 }
 
 // Every thread of the CTA calls it; red holds kPagedRed entries.  A CTA takes min_per tiles or more.
-// kWhole: where the units are at most the CTAs and the longest is at most 5/4 of an equal share and
-// 12 tiles, each CTA takes one unit whole instead.  Cutting costs a second set-up and a merge,
-// 10 to 20 us, and at the power limit the more busy SMs only clock lower.  128 units on 152 SMs,
-// whole against cut: 16 x 64 nodes over 1000 tokens 27.9 / 47.5 us, 8 x 128 nodes over 8000
-// 113.6 / 124.2, over 32768 413 / 424.
+// kWhole: where the units are at most the CTAs and the longest is little longer than an equal share (by
+// a quarter and 8 tiles, or 30), each CTA takes one unit whole instead: no merge, and at the power limit
+// more busy SMs only clock lower.  128 units on 152 SMs, whole / cut: 16 x 64 nodes over 1000
+// tokens 28.6 / 41.0 us, 8 x 128 nodes over 8000 117.6 / 121.9, over 32768 425.9 / 408.7.
 template <bool kWhole = false>
 __device__ inline PagedSpan paged_span(const PagedAttn& a, int RT, int KT, int min_per, unsigned long long* red,
-                                       int tol = 0) {
+                                       int tol = 0, int fix = 0) {
   PagedSpan sp;
   sp.whole = 0;
   sp.tol = tol;
+  sp.fix = fix;
   unsigned long long W = 0, mine = 0, at = 0;
   bool any_bad = false;
   // tiles of sequence b0 + threadIdx.x: by its own thread, or with many row tiles a warp each
@@ -88,7 +90,7 @@ __device__ inline PagedSpan paged_span(const PagedAttn& a, int RT, int KT, int m
         bool bad = false;
         const int n = paged_rows(a, b0 + k, P, &bad);
         any_bad |= bad;
-        const long long head = head_tiles_warp(a, P, n, RT, KT, sp.whole);
+        const long long head = head_tiles_warp(a, P, n, RT, KT, sp.whole, fix);
         if ((threadIdx.x & 31) == 0) red[34 + k] = (unsigned long long)head;
       }
       __syncthreads();
@@ -98,7 +100,7 @@ __device__ inline PagedSpan paged_span(const PagedAttn& a, int RT, int KT, int m
       bool bad = false;
       const int n = paged_rows(a, b, P, &bad);
       any_bad |= bad;
-      for (int rt = 0; rt * RT < n * a.G; ++rt) t += sp.whole ? sp.whole : unit_tiles(a, P, n, rt, RT, KT);
+      for (int rt = 0; rt * RT < n * a.G; ++rt) t += sp.whole ? sp.whole : unit_tiles(a, P, n, rt, RT, KT) + fix;
       t *= a.Hkv;
     }
     return t;
@@ -131,7 +133,7 @@ __device__ inline PagedSpan paged_span(const PagedAttn& a, int RT, int KT, int m
     __syncthreads();
     longest = red[0];
     __syncthreads();
-    if (all <= gridDim.x && longest <= (unsigned long long)(sp.per + sp.per / 4 + 12)) {
+    if (all <= gridDim.x && longest + fix <= (unsigned long long)(sp.per + min(sp.per / 4 + 8, 30ll))) {
       sp.whole = (int)longest;
       sp.per = sp.whole;
       W = all * longest;
@@ -176,32 +178,42 @@ __device__ inline PagedSpan paged_span(const PagedAttn& a, int RT, int KT, int m
 
 // The units of a CTA's range, one after another.  A warp's lanes call unit_next together.
 struct UnitWalk {
-  long long pos, end;       // tiles still to take
+  long long pos, end, per;  // tiles still to take; tiles per CTA
   long long seq, head;      // first tile of sequence b; tiles of one of its KV heads
   long long u0, u1;         // the unit's tiles
   int b, hk, rt, P, n;      // the unit; the sequence's committed and new rows
   int t0, t1;               // of the unit's tiles, those to take
-  int loaded, whole, tol;
+  int loaded, whole, tol, fix;
   bool begun;
 };
 
-// Where the boundary p of two ranges, strictly inside unit [u0, u1), cuts it: at p, or at the nearer
-// edge if that is at most tol tiles away.
-__device__ __forceinline__ long long unit_cut(long long p, long long u0, long long u1, int tol) {
-  const long long l = p - u0, r = u1 - p;
-  return l <= min((long long)tol, r) ? u0 : r <= tol ? u1 : p;
+// a / b of numbers >= 0, in 32 bits where they fit
+__device__ __forceinline__ long long div_ll(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
 }
-// The CTAs c0..c1 that share the unit; c1 <= c0 where none cuts it.
+// How near to the left (.x) and right edge of a unit of U tiles a cut moves to it.  Units no longer than
+// a CTA's share: tol, or half the unit.  Longer ones are cut anyhow, and moved cuts only unbalance
+// the ranges: what leaves next to no tiles on one side.
+__device__ __forceinline__ int2 unit_tol(long long U, long long per, int tol, int fix) {
+  const long long l = U <= per ? tol : min(tol, fix + 2), r = U <= per ? tol : min(tol, 4);
+  return make_int2((int)min(l, U / 2), (int)min(r, (U - 1) / 2));
+}
+// Where the boundary p of two ranges, strictly inside unit [u0, u1), cuts it.
+__device__ __forceinline__ long long unit_cut(long long p, long long u0, long long u1, const UnitWalk& w) {
+  const int2 tol = unit_tol(u1 - u0, w.per, w.tol, w.fix);
+  return p - u0 <= tol.x ? u0 : u1 - p <= tol.y ? u1 : p;
+}
+// The CTAs c0..c1 that share the walk's unit; c1 <= c0 where none cuts it.
 struct UnitCtas {
   long long c0, c1;
 };
-__device__ __forceinline__ UnitCtas unit_ctas(const PagedSpan& sp, long long u0, long long u1) {
-  const long long l = min((long long)sp.tol, (u1 - u0) / 2), r = min((long long)sp.tol, (u1 - u0 - 1) / 2);
-  return {(u0 + l) / sp.per, (u1 - r - 1) / sp.per};
+__device__ __forceinline__ UnitCtas unit_ctas(const UnitWalk& w) {
+  const int2 tol = unit_tol(w.u1 - w.u0, w.per, w.tol, w.fix);
+  return {div_ll(w.u0 + tol.x, w.per), div_ll(w.u1 - tol.y - 1, w.per)};
 }
-
 __device__ __forceinline__ UnitWalk unit_walk(const PagedSpan& sp) {
   UnitWalk w{};
+  w.per = sp.per;
   w.pos = sp.per * blockIdx.x;
   w.end = min(sp.W, w.pos + sp.per);
   w.seq = sp.base;
@@ -209,6 +221,7 @@ __device__ __forceinline__ UnitWalk unit_walk(const PagedSpan& sp) {
   w.loaded = -1;
   w.whole = sp.whole;
   w.tol = sp.tol;
+  w.fix = sp.fix;
   return w;
 }
 __device__ inline bool unit_next(const PagedAttn& a, UnitWalk& w, int RT, int KT) {
@@ -218,7 +231,7 @@ __device__ inline bool unit_next(const PagedAttn& a, UnitWalk& w, int RT, int KT
       bool bad;
       w.P = a.prefix_len[w.b];
       w.n = paged_rows(a, w.b, w.P, &bad);
-      w.head = head_tiles_warp(a, w.P, w.n, RT, KT, w.whole);
+      w.head = head_tiles_warp(a, w.P, w.n, RT, KT, w.whole, w.fix);
       w.loaded = w.b;
     }
     long long rel = w.pos - w.seq;
@@ -227,11 +240,11 @@ __device__ inline bool unit_next(const PagedAttn& a, UnitWalk& w, int RT, int KT
       ++w.b;
       continue;
     }
-    w.hk = (int)(rel / w.head);
+    w.hk = (int)div_ll(rel, w.head);
     rel -= w.hk * w.head;
     for (int rt0 = 0;; rt0 += 32) {  // ends: rel lies below the head's sum
       unsigned t = unit_tiles(a, w.P, w.n, rt0 + lane, RT, KT);
-      if (w.whole && t) t = w.whole;
+      if (t) t = w.whole ? w.whole : t + w.fix;
       unsigned incl = t;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -252,14 +265,14 @@ __device__ inline bool unit_next(const PagedAttn& a, UnitWalk& w, int RT, int KT
     }
     if (!w.begun) {
       w.begun = true;
-      if (w.pos > w.u0) w.pos = unit_cut(w.pos, w.u0, w.u1, w.tol);
+      if (w.pos > w.u0) w.pos = unit_cut(w.pos, w.u0, w.u1, w);
       if (w.pos == w.u1) continue;
     }
     long long end = w.u1;
-    if (w.end < w.u1) end = unit_cut(w.end, w.u0, w.u1, w.tol);
+    if (w.end < w.u1) end = unit_cut(w.end, w.u0, w.u1, w);
     if (end <= w.pos) return false;
-    w.t0 = (int)(w.pos - w.u0);
-    w.t1 = (int)(end - w.u0);
+    w.t0 = max(0, (int)(w.pos - w.u0) - w.fix);
+    w.t1 = max(0, (int)(end - w.u0) - w.fix);
     w.pos = end;
     if (w.whole) w.t1 = unit_tiles(a, w.P, w.n, w.rt, RT, KT);
     return true;

@@ -27,10 +27,14 @@
 // Two schedules.  Where clusters of two or more CTAs hold all row tiles (or pairs) at once, each
 // one's keys are cut into equal parts that run as one thread-block cluster and merge behind its
 // barrier; a CTA with one tile has half the partial rows to park and merge, which costs a
-// short range more than K and V read twice.  Otherwise a persistent grid of one CTA per SM divides all pairs' 64-key
-// steps equally (paged.cuh), which keeps ragged batches and causal triangles balanced; a
-// pair cut between CTAs is merged through the workspace, in CTA order, by the CTA that
-// finishes last.
+// short range more than K and V read twice.  Otherwise a persistent grid of one CTA per SM divides
+// all pairs' 64-key steps equally (paged.cuh), which keeps ragged batches and causal triangles
+// balanced; a pair cut between CTAs is merged through the workspace, in CTA order, by the CTA that
+// finishes last.  There the pieces follow one another without a stop: the producer finds each
+// and posts it, keeps the rings filled across pieces, and Q and the first scores of the next
+// are there when the softmax warps have written a piece out.  With a stop and a fresh set-up
+// at each piece, and every warp finding it for itself, 16 chunks of 512 rows over 1000 to 2000
+// tokens took 264 us, now 238; two of 2048 rows over 3000 to 6000 326, now 310.
 #include <atomic>
 
 #include "paged.cuh"
@@ -41,12 +45,14 @@ constexpr int kPtRows = 128;
 constexpr int kPtKeys = 64;
 constexpr int kPtSlots = 4;      // K ring and V ring depth
 constexpr int kPtThreads = 384;  // 12 warps
+constexpr int kPtPieces = 4;     // pieces known ahead
 constexpr int kPtMaxSplits = 8;  // portable cluster size
-// Cuts this near to a unit's edge move to it.  One costs 10 to 20 steps of set-up and merging, so a
-// longest range longer by two such moves is still the shorter one.  Without / with: nine causal
-// chunks of 1510 to 1758 rows on empty caches 85 / 62 us, 64 trees of 16 nodes over 1000 tokens
-// 97.5 / 79.3, 19 of 81 nodes over 15 tokens 31.9 / 21.2; ranges of 100 steps and more alike.
+// A unit's set-up and end count as 8 steps, and cuts less than 12 from a unit's edge move to it
+// (paged.cuh).  0 and 0 / 12 and 0 / 12 and 8: nine causal chunks of 1510 to 1758 rows on empty caches
+// 72.5 / 61.3 / 56.2 us, one of 2048 rows 81.5 / 68.2 / 57.9, 64 trees of 16 nodes over 1000 tokens
+// 92.7 / 77.0 / 77.4.
 constexpr int kPtTol = 12;
+constexpr int kPtFix = 8;
 constexpr float kPtRescaleLog2 = 8.f;
 constexpr float kPtRescaleSum = 256.f;
 
@@ -64,7 +70,7 @@ struct PtCfg {
   static constexpr int kOffBar = kOffPar + kMaxNodes * 4;
   static constexpr int kSmemAlloc = kOffBar + 512 + 1024;  // slack for 1024-byte alignment
   static constexpr uint32_t kColO = 256;
-  static_assert(kSmemAlloc <= 232448, "shared memory per CTA");
+  static_assert(kSmemAlloc + 8192 <= 232448, "shared memory per CTA");  // 8192: paged_span's and the pieces'
 };
 
 struct PtBars {
@@ -78,11 +84,23 @@ struct PtBars {
   uint64_t pv_done[2][2];
   uint64_t o_done;
   uint64_t s_done[2];
+  uint64_t o_free[2];  // tile x's warps have read O
+  uint64_t piece_full[kPtPieces];
+  uint64_t piece_empty[kPtPieces];
   uint32_t tmem_base;
   int abort;
 };
-constexpr int kPtBarWords = 2 + 4 * kPtSlots + 12 + 3;
+static_assert(sizeof(PtBars) <= 512);
 
+// One piece of work, a range of a unit's key tiles: what the producer finds and every warp goes by.
+struct PtPiece {
+  int b, hk, rt, P, n;  // unit; the sequence's committed and new rows
+  int t0, t1;           // of the unit's tiles, those to take
+  int c0, c1;           // CTAs that share the unit, c1 <= c0: it is this CTA's alone
+  int slot0;            // where CTA c0 parks its part (the others: 2 c)
+  int slot;             // and this one
+  int more;             // 0: there is none
+};
 struct PtArgs {
   int NT;      // nodes per row tile
   int tiles;   // row tiles per unit: 2, or 1 (cluster schedule of few tiles)
@@ -124,6 +142,12 @@ __device__ __forceinline__ float pt_exp64(const float (&sv)[64], float c, float 
   const float2 s2 = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
   return s2.x + s2.y;
 }
+// v[x] of two by selection: a runtime index would put them in local memory, which every step's
+// waits would then read again (0.1 us a step)
+template <typename T>
+__device__ __forceinline__ T pt_of(const T (&v)[2], int x) {
+  return x ? v[1] : v[0];
+}
 // bits [lo, hi) of a 64-bit word
 __device__ __forceinline__ uint64_t pt_bits(int lo, int hi) {
   lo = max(lo, 0);
@@ -131,10 +155,6 @@ __device__ __forceinline__ uint64_t pt_bits(int lo, int hi) {
   if (hi <= lo) return 0ull;
   const uint64_t up = hi == 64 ? ~0ull : (1ull << hi) - 1ull;
   return up & ~((1ull << lo) - 1ull);
-}
-
-__device__ __forceinline__ void pt_mbar_inval(uint64_t* bar) {
-  asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(ptx::smem_addr(bar)) : "memory");
 }
 
 // S of one row tile (K = D in steps of 16) as one asm block: an issuing thread shares its
@@ -183,6 +203,10 @@ __device__ __forceinline__ void pt_drain(uint64_t* bar, uint32_t parity, volatil
 __device__ __forceinline__ void pt_bars_init(PtBars* bars) {
   ptx::mbar_init(&bars->q_full[0], 1);
   ptx::mbar_init(&bars->q_full[1], 1);
+  for (int s = 0; s < kPtPieces; ++s) {
+    ptx::mbar_init(&bars->piece_full[s], 1);
+    ptx::mbar_init(&bars->piece_empty[s], kPtThreads / 32 - 1);
+  }
   for (int s = 0; s < kPtSlots; ++s) {
     ptx::mbar_init(&bars->k_full[s], 1);
     ptx::mbar_init(&bars->k_empty[s], 2);  // both S issuers
@@ -198,6 +222,8 @@ __device__ __forceinline__ void pt_bars_init(PtBars* bars) {
   ptx::mbar_init(&bars->o_done, 1);
   ptx::mbar_init(&bars->s_done[0], 1);
   ptx::mbar_init(&bars->s_done[1], 1);
+  ptx::mbar_init(&bars->o_free[0], 4);
+  ptx::mbar_init(&bars->o_free[1], 4);
   ptx::fence_mbar_init();
 }
 
@@ -218,6 +244,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   volatile int* abort_flag = &bars->abort;
   __shared__ unsigned long long s_red[kPagedRed];
   __shared__ int s_last;
+  __shared__ PtPiece s_piece[kPtPieces];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int NT = pa.NT, rows_used = a.G * NT, RT = pa.tiles * rows_used;
@@ -251,68 +278,122 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   const uint32_t tmem = bars->tmem_base;
 
   // ---- this CTA's pieces
-  PagedSpan sp{};
-  UnitWalk w{};
+  UnitWalk w{};  // the producer's
   const size_t cta = ((size_t)blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;  // cluster schedule
   if constexpr (kStream) {
-    sp = paged_span<true>(a, RT, kPtKeys, 1, s_red, kPtTol);
+    const PagedSpan sp = paged_span<true>(a, RT, kPtKeys, 1, s_red, kPtTol, kPtFix);
     w = unit_walk(sp);
-  } else {
-    w.b = blockIdx.z, w.hk = blockIdx.y, w.rt = pa.MP - 1 - (int)blockIdx.x / pa.splits;
   }
+  auto softmax_sync = [] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
   int loaded_b = -1, n_act = 0;
-  bool first_piece = true;
-  while (kStream ? unit_next(a, w, RT, kPtKeys) : first_piece) {
-    const int b = w.b, hk = w.hk, mp = w.rt;
+  // tiles, and tiles with rows of A and B, of the pieces before this one, and how many those were: what
+  // the rings' slots and the barriers' phases go by.  Every role counts them alike.
+  unsigned kt = 0, done_x[2] = {0, 0}, pieces = 0;
+  unsigned k_issued = 0, v_issued = 0;  // the producer's copies
+  unsigned q_loads = 0;                 // an S issuer's
+  bool ok = true;                       // no wait of this role has run out
+  auto drain = [&] {  // the producer: no copy is in flight when the CTA ends
+    for (unsigned s = 0; s < kPtSlots; ++s) {
+      if (s < k_issued) pt_drain(&bars->k_full[s], ((k_issued - 1 - s) / kPtSlots) & 1, abort_flag);
+      if (s < v_issued) pt_drain(&bars->v_full[s], ((v_issued - 1 - s) / kPtSlots) & 1, abort_flag);
+    }
+  };
+  for (unsigned np = 0;; ++np) {
+    PtPiece pc;
+    if constexpr (kStream) {
+      // the producer runs ahead of the others: it finds the pieces and posts them
+      const int ps = np % kPtPieces;
+      int quiet = 0;  // pieces come after an abort too, so that each cut unit's parts are counted
+      if (warp == 0) {
+        pc.more = unit_next(a, w, RT, kPtKeys);
+        pc.b = w.b, pc.hk = w.hk, pc.rt = w.rt, pc.P = w.P, pc.n = w.n, pc.t0 = w.t0, pc.t1 = w.t1;
+        const UnitCtas by = unit_ctas(w);
+        pc.c0 = (int)by.c0, pc.c1 = (int)by.c1;
+        pc.slot0 = unit_slot(by.c0, w.per, w.u0), pc.slot = unit_slot(blockIdx.x, w.per, w.u0);
+        bool got = true;
+        if (np >= kPtPieces)
+          got = ptx::mbar_wait_limit(&bars->piece_empty[ps], (np / kPtPieces - 1) & 1, &quiet, 8 * TV_WAIT_NS);
+        if (!__all_sync(0xffffffffu, got)) {
+          *abort_flag = 1;
+          break;
+        }
+        if (lane == 0) {
+          s_piece[ps] = pc;
+          ptx::mbar_arrive(&bars->piece_full[ps]);
+        }
+        __syncwarp();
+      } else {
+        const bool got =
+            ptx::mbar_wait_limit(&bars->piece_full[ps], (np / kPtPieces) & 1, &quiet, 8 * TV_WAIT_NS);
+        if (!__all_sync(0xffffffffu, got)) {
+          *abort_flag = 1;
+          break;
+        }
+        const PtPiece& at = s_piece[ps];
+        pc.b = at.b, pc.hk = at.hk, pc.rt = at.rt, pc.P = at.P, pc.n = at.n, pc.t0 = at.t0, pc.t1 = at.t1;
+        pc.more = at.more;
+      }
+      if (!pc.more) break;
+    } else {
+      pc.b = blockIdx.z, pc.hk = blockIdx.y, pc.rt = pa.MP - 1 - (int)blockIdx.x / pa.splits;
+    }
+    const int b = pc.b, hk = pc.hk, mp = pc.rt;
     if (b != loaded_b) {
-      // the first pass's tree rows are read beside the lengths, not after them
-      const int t_first = min((int)threadIdx.x, a.N - 1);
-      int p_first = -1, p_before = -1;
-      if (a.parent) {
-        p_first = a.parent[(size_t)b * a.N + t_first];
-        if (t_first > 0) p_before = a.parent[(size_t)b * a.N + t_first - 1];
+      // Tree rows count up to the first padding row (a tree with rows behind it is bad).  Every warp
+      // counts for itself, and the softmax warps check and keep the parents.  The first reads
+      // run beside those of the lengths.
+      const int32_t* par = a.parent ? a.parent + (size_t)b * a.N : nullptr;
+      const int st = (int)threadIdx.x - 64;
+      const bool rows_warp = warp >= 2 && warp < 10;
+      int first[4], p_first = -1, p_before = -1;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) first[k] = par && k * 32 + lane < a.N ? par[k * 32 + lane] : -1;
+      if (par && rows_warp && st < a.N) {
+        p_first = par[st];
+        if (st > 0) p_before = par[st - 1];
       }
       if constexpr (!kStream) {
         bool bad = false;
-        w.P = a.prefix_len[b];
-        w.n = paged_rows(a, b, w.P, &bad);
+        pc.P = a.prefix_len[b];
+        pc.n = paged_rows(a, b, pc.P, &bad);
         if (bad && threadIdx.x == 0) set_dev_status(a.dev_status, TV_DEV_BAD_PAGE);
       }
-      const int n = w.n;
+      const int n = pc.n;
       n_act = n;
-      if (a.parent && n > 0) {
-        // rows up to the first padding row (a tree with rows behind it is bad)
-        int wrong = 0;
-        n_act = 1;
-        for (int t0 = 0; t0 < n; t0 += kPtThreads) {
-          const int t = t0 + threadIdx.x;
-          int p = -1;
-          if (t < n) {
-            p = t0 == 0 ? p_first : a.parent[(size_t)b * a.N + t];
-            const bool prev_pad = t >= 2 && (t0 == 0 ? p_before : a.parent[(size_t)b * a.N + t - 1]) == -1;
-            const bool ok = t == 0 ? p == -1 : (p == -1 || (p >= 0 && p < t && !prev_pad));
-            if (!ok) wrong = 1;
-            s_par[t] = ok ? p : -1;
-          }
-          n_act += __syncthreads_count(t > 0 && p != -1);
+      if (par && n > 0) {
+        int count = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int t = k * 32 + lane;
+          count += t > 0 && t < n && first[k] != -1;
         }
-        if (wrong) set_dev_status(a.dev_status, TV_DEV_BAD_TREE);
+        for (int t = 128 + lane; t < n; t += 32) count += par[t] != -1;
+        n_act = 1 + __reduce_add_sync(0xffffffffu, count);
+        if (rows_warp) {
+          if (loaded_b >= 0) softmax_sync();  // the piece before's rows have read s_par
+          for (int t = st; t < n; t += 256) {
+            const int p = t == st ? p_first : par[t];
+            const bool prev_pad = t >= 2 && (t == st ? p_before : par[t - 1]) == -1;
+            const bool fits = t == 0 ? p == -1 : (p == -1 || (p >= 0 && p < t && !prev_pad));
+            if (!fits) set_dev_status(a.dev_status, TV_DEV_BAD_TREE);
+            s_par[t] = fits ? p : -1;
+          }
+          softmax_sync();
+        }
       }
       loaded_b = b;
     }
-    const int P = w.P, n = w.n;
+    const int P = pc.P, n = pc.n;
     const int lo = unit_lo(a, P, mp, RT);
     int split = 0;
     if constexpr (!kStream) {
       const int T_u = unit_tiles(a, P, n, mp, RT, kPtKeys);
       split = blockIdx.x % pa.splits;
-      w.t0 = (int)((long long)T_u * split / pa.splits);
-      w.t1 = (int)((long long)T_u * (split + 1) / pa.splits);
+      pc.t0 = (int)((long long)T_u * split / pa.splits);
+      pc.t1 = (int)((long long)T_u * (split + 1) / pa.splits);
     }
-    const long long u0 = w.u0;
-    const int t_begin = lo / kPtKeys + w.t0;  // this piece's key tiles
-    int nt_all = w.t1 - w.t0;
-    if (*abort_flag) nt_all = 0;  // a wait ran out: nothing more is computed, but cut units still count their parts
+    const int t_begin = lo / kPtKeys + pc.t0;  // this piece's key tiles
+    const int nt_all = pc.t1 - pc.t0;
     const int key_end = P + n_act;  // rows from here on, and before lo, may hold anything
     int i0[2], ntx[2];
 #pragma unroll
@@ -322,16 +403,6 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       ntx[x] = max(0, min(nt_all, (hi + kPtKeys - 1) / kPtKeys - t_begin));
     }
     const int nt = max(ntx[0], ntx[1]);
-
-    if (!first_piece) {  // the first one's barriers are ready
-      if (threadIdx.x == 0) {
-        uint64_t* w = &bars->q_full[0];
-        for (int k = 0; k < kPtBarWords; ++k) pt_mbar_inval(w + k);
-        pt_bars_init(bars);
-      }
-      __syncthreads();
-    }
-    first_piece = false;
 
     float m_run = -INFINITY, l_run = 0.f;
     bool have_o = false;
@@ -360,13 +431,14 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         return -1;
       };
       int raw0 = entry(0), raw1 = entry(1), before = -1;
-      // this lane's box of tile t into ring slot t % kPtSlots; false after an abort
+      // this lane's box of tile t into its ring slot; false after an abort
       auto fetch = [&](unsigned char* ring, const CUtensorMap* tm, uint64_t* full, uint64_t* empty, int t,
                        int pg) -> bool {
-        const int slot = t % kPtSlots;
-        bool ok = true;
-        if (t >= kPtSlots) ok = ptx::mbar_wait(&empty[slot], ((t / kPtSlots) - 1) & 1, abort_flag);
-        if (!__all_sync(0xffffffffu, ok)) return false;
+        const unsigned gt = kt + t;
+        const int slot = gt % kPtSlots;
+        bool got = true;
+        if (gt >= kPtSlots) got = ptx::mbar_wait(&empty[slot], ((gt / kPtSlots) - 1) & 1, abort_flag);
+        if (!__all_sync(0xffffffffu, got)) return false;
         const uint32_t boxes = __ballot_sync(0xffffffffu, pg >= 0);
         if (lane == 0) ptx::mbar_arrive_expect_tx(&full[slot], __popc(boxes) * box_bytes);
         __syncwarp();
@@ -380,40 +452,34 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         }
         return true;
       };
-      int k_issued = 0, v_issued = 0;
-      for (int t = 0; t <= nt && nt > 0; ++t) {
+      for (int t = 0; ok && t <= nt && nt > 0; ++t) {
         const int page = checked(t, raw0);
         raw0 = raw1;
         raw1 = entry(t + 2);
         if (t < nt) {
-          if (!fetch(sK, &tmK, bars->k_full, bars->k_empty, t, page)) break;
-          k_issued = t + 1;
+          if (!(ok = fetch(sK, &tmK, bars->k_full, bars->k_empty, t, page))) break;
+          k_issued = kt + t + 1;
         }
         if (t > 0) {
-          if (!fetch(sV, &tmV, bars->v_full, bars->v_empty, t - 1, before)) break;
-          v_issued = t;
+          if (!(ok = fetch(sV, &tmV, bars->v_full, bars->v_empty, t - 1, before))) break;
+          v_issued = kt + t;
         }
         before = page;
       }
-      // never leave the piece with copies in flight
-      if (lane == 0) {
-        for (int s = 0; s < kPtSlots; ++s) {
-          if (s < k_issued) pt_drain(&bars->k_full[s], ((k_issued - 1 - s) / kPtSlots) & 1, abort_flag);
-          if (s < v_issued) pt_drain(&bars->v_full[s], ((v_issued - 1 - s) / kPtSlots) & 1, abort_flag);
-        }
-      }
-      __syncwarp();
+      if (!kStream && lane == 0) drain();
     } else if (warp == 1 || warp == 11) {
       // ---------------------------------------------------------------- S issuer of tile x
       const int x = warp == 1 ? 0 : 1;
       if (lane == 0) {
-        if (ntx[x] > 0) {
+        const int ntm = pt_of(ntx, x);
+        const unsigned dx = pt_of(done_x, x);
+        if (ntm > 0) {
           ptx::mbar_arrive_expect_tx(&bars->q_full[x], (uint32_t)(rows_used * 128 * C::kDB));
           for (int g = 0; g < a.G; ++g)
             for (int d = 0; d < C::kDB; ++d)
-              ptx::tma_load_3d(sQ + x * C::kQTile + d * C::kQBlock + g * NT * 128, &tmQ, &bars->q_full[x], d * 64, i0[x],
-                               b * a.Hq + hk * a.G + g);
-          pt_drain(&bars->q_full[x], 0, abort_flag);
+              ptx::tma_load_3d(sQ + x * C::kQTile + d * C::kQBlock + g * NT * 128, &tmQ, &bars->q_full[x], d * 64,
+                               pt_of(i0, x), b * a.Hq + hk * a.G + g);
+          pt_drain(&bars->q_full[x], q_loads++ & 1, abort_flag);
         }
         if (nt > 0) {
           constexpr uint32_t idS = ptx::idesc_bf16(kPtRows, kPtKeys, false, false);
@@ -422,12 +488,14 @@ __global__ void __launch_bounds__(kPtThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
             adq[kk] = ptx::sdesc_sw128(qaddr + (kk >> 2) * C::kQBlock + (kk & 3) * 32, 16, 1024);
-          for (int t = 0; t < nt; ++t) {
-            const int ks = t % kPtSlots, buf = t & 1;
-            if (!ptx::mbar_wait(&bars->k_full[ks], (t / kPtSlots) & 1, abort_flag)) break;
-            if (t < ntx[x]) {
-              // S_X(t) overwrites P_X(t - 2) in this buffer
-              if (t >= 2 && !ptx::mbar_wait(&bars->pv_done[x][buf], ((t - 2) >> 1) & 1, abort_flag)) break;
+          for (int t = 0; ok && t < nt; ++t) {
+            const int ks = (kt + t) % kPtSlots;
+            if (!(ok = ptx::mbar_wait(&bars->k_full[ks], ((kt + t) / kPtSlots) & 1, abort_flag))) break;
+            if (t < ntm) {
+              // S_X(t) overwrites P_X of two tiles before in this buffer
+              const unsigned tx = dx + t;
+              const int buf = tx & 1;
+              if (tx >= 2 && !(ok = ptx::mbar_wait(&bars->pv_done[x][buf], ((tx - 2) >> 1) & 1, abort_flag))) break;
               ptx::tc_fence_after();
               pt_s_product(tmem + x * kPtRows + buf * kPtKeys, adq,
                            ptx::sdesc_sw128(ptx::smem_addr(sK + ks * C::kTileBytes), 16, C::kGroup), idS);
@@ -435,9 +503,10 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             }
             ptx::mma_commit(&bars->k_empty[ks]);
           }
+          // Q's place is free again behind its products
+          ptx::mma_commit(&bars->s_done[x]);
+          pt_drain(&bars->s_done[x], pieces & 1, abort_flag);
         }
-        ptx::mma_commit(&bars->s_done[x]);
-        pt_drain(&bars->s_done[x], 0, abort_flag);
       }
       __syncwarp();
     } else if (warp == 10) {
@@ -451,8 +520,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         return t >= 0 && t < nt && (j0 < lo || j0 + kPtKeys > key_end);
       };
       auto zero_rows = [&](int t) {
-        const int vs = t % kPtSlots, j0 = (t_begin + t) * kPtKeys;
-        if (!ptx::mbar_wait(&bars->v_full[vs], (t / kPtSlots) & 1, abort_flag)) return;
+        const int vs = (kt + t) % kPtSlots, j0 = (t_begin + t) * kPtKeys;
+        if (!ptx::mbar_wait(&bars->v_full[vs], ((kt + t) / kPtSlots) & 1, abort_flag)) return;
         for (int r = lane; r < kPtKeys; r += 32)
           if (j0 + r < lo || j0 + r >= key_end)
             for (int db = 0; db < C::kDB; ++db) {
@@ -464,13 +533,15 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         ptx::fence_proxy_async_smem();
       };
       auto issue = [&](int t) -> bool {
-        const int vs = t % kPtSlots, buf = t & 1;
-        if (!ptx::mbar_wait(&bars->v_full[vs], (t / kPtSlots) & 1, abort_flag)) return false;
+        const int vs = (kt + t) % kPtSlots;
+        if (!ptx::mbar_wait(&bars->v_full[vs], ((kt + t) / kPtSlots) & 1, abort_flag)) return false;
         const uint64_t vd = ptx::sdesc_sw128(ptx::smem_addr(sV + vs * C::kTileBytes), 1024, C::kGroup);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           if (t >= ntx[x]) continue;
-          if (!ptx::mbar_wait(&bars->p_full[x][buf], (t >> 1) & 1, abort_flag)) return false;
+          const unsigned tx = done_x[x] + t;
+          const int buf = tx & 1;
+          if (!ptx::mbar_wait(&bars->p_full[x][buf], (tx >> 1) & 1, abort_flag)) return false;
           ptx::tc_fence_after();
           pt_pv_product(tmem + C::kColO + x * kPtRows, tmem + x * kPtRows + buf * kPtKeys, vd, 2 * C::kGroup / 16, idO,
                         t > 0 ? 1u : 0u);  // P: 8 columns per 16 keys
@@ -480,18 +551,23 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         return true;
       };
       const int last = nt - 1;
-      if (edge(0)) zero_rows(0);
-      __syncwarp();
-      bool ok = true;
-      if (lane == 0)
-        for (int t = 0; ok && t < last; ++t) ok = issue(t);
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-      if (ok && last > 0 && edge(last)) zero_rows(last);
-      __syncwarp();
-      if (lane == 0 && ok && last >= 0) issue(last);
-      if (lane == 0) {
+      // one copy of the loop's code: a kernel of few steps pays for each line that it fetches first
+#pragma unroll 1
+      for (int part = 0, t = 0; part < 2; ++part) {
+        const int from = part == 0 ? 0 : last, to = part == 0 ? last : nt;
+        if (from < to && edge(from)) zero_rows(from);
+        __syncwarp();
+        // the piece before's O has been read
+        if (kStream && part == 0 && pieces > 0 && nt > 0)
+          for (int x = 0; x < 2; ++x)
+            ok = __all_sync(0xffffffffu, ok && ptx::mbar_wait(&bars->o_free[x], (pieces - 1) & 1, abort_flag));
+        if (lane == 0)
+          for (; ok && t < to; ++t) ok = issue(t);
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      }
+      if (lane == 0 && nt > 0) {
         ptx::mma_commit(&bars->o_done);
-        pt_drain(&bars->o_done, 0, abort_flag);
+        pt_drain(&bars->o_done, pieces & 1, abort_flag);
       }
       __syncwarp();
     } else {
@@ -499,12 +575,13 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       const int x = (warp - 2) >> 2;
       const int q4 = warp & 3;
       const int r = q4 * 32 + lane;
-      const int g = r / NT, node = i0[x] + r % NT;
+      const int g = r / NT, node = pt_of(i0, x) + r % NT;
       const bool valid = x < pa.tiles && r < rows_used && node < n_act;
       const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
       const uint32_t colS = tmem + lane_base + x * kPtRows;
       const uint32_t colO = tmem + lane_base + C::kColO + x * kPtRows;
-      const int ntm = ntx[x];
+      const int ntm = pt_of(ntx, x);
+      const unsigned dx = pt_of(done_x, x);
       // the row sees [wlo, whi) and, in a tree, its ancestors; rows that are no row see everything
       // (their results go nowhere)
       int wlo = 0, whi = 0x7fffffff;
@@ -523,10 +600,10 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       }
       const float c = kCap ? a.cap * kLog2e : a.scale * kLog2e;
       const float ck = kCap ? 2.f * kLog2e * a.scale / a.cap : 0.f;
-      bool ok = true;
-      for (int t = 0; t < ntm; ++t) {
-        const int buf = t & 1;
-        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars->s_full[x][buf], (t >> 1) & 1, abort_flag));
+      for (int t = 0; ok && t < ntm; ++t) {
+        const unsigned tx = dx + t;
+        const int buf = tx & 1;
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars->s_full[x][buf], (tx >> 1) & 1, abort_flag));
         if (!ok) break;
         ptx::tc_fence_after();
         const int j0 = (t_begin + t) * kPtKeys;
@@ -580,7 +657,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         if (__any_sync(0xffffffffu, need) && t > 0) {
           // O_X must hold all of PV_X(t - 1) before it is rescaled
           ok = __all_sync(0xffffffffu,
-                          ptx::mbar_wait(&bars->pv_done[x][(t - 1) & 1], ((t - 1) >> 1) & 1, abort_flag));
+                          ptx::mbar_wait(&bars->pv_done[x][(tx - 1) & 1], ((tx - 1) >> 1) & 1, abort_flag));
           if (!ok) break;
           ptx::tc_fence_after();
 #pragma unroll
@@ -601,17 +678,15 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       }
       // ---- epilogue: every MMA is complete at o_done
       if (nt > 0) {
-        const bool done = __all_sync(0xffffffffu, ptx::mbar_wait(&bars->o_done, 0, abort_flag));
-        have_o = done && ok && ntm > 0;
-        if (done) ptx::tc_fence_after();
+        ok = ok && __all_sync(0xffffffffu, ptx::mbar_wait(&bars->o_done, pieces & 1, abort_flag));
+        have_o = ok && ntm > 0;
+        if (ok) ptx::tc_fence_after();
       }
-      bool whole = false;
-      if constexpr (kStream) {
-        const UnitCtas by = unit_ctas(sp, u0, w.u1);
-        whole = by.c1 <= by.c0;
-      }
+      // read here, not kept through the loop
+      const volatile PtPiece& at = s_piece[np % kPtPieces];
+      const bool whole = kStream && at.c1 <= at.c0;
       const int R = x * kPtRows + r;
-      const size_t slot = kStream ? (size_t)unit_slot(blockIdx.x, sp.per, u0) : cta;
+      const size_t slot = kStream ? (size_t)at.slot : cta;
       const float inv = whole && l_run > 0.f ? 1.f / l_run : 0.f;
       const size_t orow = (((size_t)b * a.Hq + hk * a.G + g) * a.N + node) * a.D;
       float4* part = whole ? nullptr : reinterpret_cast<float4*>(a.ws_o) + slot * (D / 4) * 2 * kPtRows + R;
@@ -647,32 +722,35 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       if (!whole)
         __stcg(a.ws_ml + slot * 2 * kPtRows + R, make_float2(have_o ? m_run : -INFINITY, have_o ? l_run : 0.f));
       ptx::tc_fence_before();
+      __syncwarp();
+      if (kStream && nt > 0 && lane == 0) ptx::mbar_arrive(&bars->o_free[x]);
     }
     __syncwarp();
 
     if constexpr (kStream) {
-      const auto [c0, c1] = unit_ctas(sp, u0, w.u1);
-      if (c0 < c1) {
+      // only the softmax warps take part; the others go on to the next piece
+      const volatile PtPiece& at = s_piece[np % kPtPieces];
+      const int c0 = at.c0, c1 = at.c1;
+      if (c0 < c1 && warp >= 2 && warp < 10) {
         __threadfence();
-        __syncthreads();
-        if (threadIdx.x == 0) {
+        softmax_sync();
+        if (threadIdx.x == 64) {
           s_last = ptx::atom_add_acq_rel_gpu(&a.cnt[c0], 1u) == (unsigned)(c1 - c0);
           if (s_last) a.cnt[c0] = 0u;
           __threadfence();
         }
-        __syncthreads();
-        if (s_last && warp >= 2 && warp < 10) {
+        softmax_sync();
+        if (s_last) {
           const int x = (warp - 2) >> 2, r = (warp & 3) * 32 + lane, R = x * kPtRows + r;
-          const int g = r / NT, node = i0[x] + r % NT;
+          const int g = r / NT, node = pt_of(i0, x) + r % NT;
           if (r < rows_used && node < n_act) {
-            auto stats = [&](long long cc) -> float2 {
-              return __ldcg(&a.ws_ml[(size_t)unit_slot(cc, sp.per, u0) * 2 * kPtRows + R]);
-            };
+            auto place = [&](int cc) -> size_t { return cc == c0 ? at.slot0 : 2 * cc; };
+            auto stats = [&](int cc) -> float2 { return __ldcg(&a.ws_ml[place(cc) * 2 * kPtRows + R]); };
             float M = -INFINITY, L = 0.f;
 #pragma unroll 4
-            for (long long cc = c0; cc <= c1; ++cc) M = fmaxf(M, stats(cc).x);
+            for (int cc = c0; cc <= c1; ++cc) M = fmaxf(M, stats(cc).x);
 #pragma unroll 4
-            for (long long cc = c0; cc <= c1; ++cc) {
+            for (int cc = c0; cc <= c1; ++cc) {
               const float2 ml = stats(cc);
               if (ml.x != -INFINITY) L = fmaf(ptx::ex2(ml.x - M), ml.y, L);
             }
@@ -684,16 +762,16 @@ __global__ void __launch_bounds__(kPtThreads, 1)
 #pragma unroll
               for (int k = 0; k < 32; ++k) ov[k] = 0.f;
               // two parts' loads in flight together
-              for (long long cc = c0; cc <= c1; cc += 2) {
+              for (int cc = c0; cc <= c1; cc += 2) {
                 float wt[2];
                 float4 v[2][8];
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                  const long long from = min(cc + u, c1);
+                  const int from = min(cc + u, c1);
                   const float2 ml = stats(from);
                   wt[u] = cc + u > c1 || ml.x == -INFINITY ? 0.f : ptx::ex2(ml.x - M);
                   const float4* src = reinterpret_cast<const float4*>(a.ws_o) +
-                                      ((size_t)unit_slot(from, sp.per, u0) * (D / 4) + col / 4) * 2 * kPtRows + R;
+                                      (place(from) * (D / 4) + col / 4) * 2 * kPtRows + R;
 #pragma unroll
                   for (int k = 0; k < 8; ++k) v[u][k] = __ldcg(src + (size_t)k * 2 * kPtRows);
                 }
@@ -729,7 +807,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       for (int item = threadIdx.x; item < rows * (a.D / 4); item += kPtThreads) {
         const int ch = item / rows, R = r0 + item - ch * rows;
         const int x = R >= kPtRows ? 1 : 0, r = R - x * kPtRows;
-        const int g = r / NT, node = i0[x] + r % NT;
+        const int g = r / NT, node = pt_of(i0, x) + r % NT;
         if (r >= rows_used || node >= n_act) continue;
         float2 mlv[kPtMaxSplits];
         float4 xv[kPtMaxSplits];
@@ -760,9 +838,18 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             make_uint2(ptx::cvt_bf16x2(acc.x * inv, acc.y * inv), ptx::cvt_bf16x2(acc.z * inv, acc.w * inv));
       }
     }
-    __syncthreads();  // every role is done with this piece's barriers, rings and TMEM
-    ptx::tc_fence_after();
+    if constexpr (kStream) {
+      __syncwarp();
+      if (warp != 0 && lane == 0) ptx::mbar_arrive(&bars->piece_empty[np % kPtPieces]);
+    }
+    kt += nt;
+    done_x[0] += ntx[0];
+    done_x[1] += ntx[1];
+    pieces += nt > 0;
+    if (!kStream) break;
   }
+  if (kStream && threadIdx.x == 0) drain();
+  ptx::tc_fence_before();
   __syncthreads();
   if (warp == 1) {
     ptx::tc_fence_after();
