@@ -85,6 +85,7 @@ struct PtBars {
   uint64_t o_done;
   uint64_t s_done[2];
   uint64_t o_free[2];  // tile x's warps have read O
+  uint64_t rows_met;   // the softmax warps meet
   uint64_t piece_full[kPtPieces];
   uint64_t piece_empty[kPtPieces];
   uint32_t tmem_base;
@@ -203,6 +204,7 @@ __device__ __forceinline__ void pt_drain(uint64_t* bar, uint32_t parity, volatil
 __device__ __forceinline__ void pt_bars_init(PtBars* bars) {
   ptx::mbar_init(&bars->q_full[0], 1);
   ptx::mbar_init(&bars->q_full[1], 1);
+  ptx::mbar_init(&bars->rows_met, 8);
   for (int s = 0; s < kPtPieces; ++s) {
     ptx::mbar_init(&bars->piece_full[s], 1);
     ptx::mbar_init(&bars->piece_empty[s], kPtThreads / 32 - 1);
@@ -284,7 +286,21 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     const PagedSpan sp = paged_span<true>(a, RT, kPtKeys, 1, s_red, kPtTol, kPtFix);
     w = unit_walk(sp);
   }
-  auto softmax_sync = [] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
+  // the softmax warps meet.  Between pieces by an mbarrier: a hardware barrier would hang if the wait for a
+  // piece ran out in some of them only
+  unsigned met = 0;
+  auto softmax_sync = [&] {
+    if constexpr (kStream) {
+      int quiet = 0;
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&bars->rows_met);
+      if (!ptx::mbar_wait(&bars->rows_met, met & 1, &quiet)) *abort_flag = 1;
+      ++met;
+      __syncwarp();
+    } else {
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+    }
+  };
   int loaded_b = -1, n_act = 0;
   // tiles, and tiles with rows of A and B, of the pieces before this one, and how many those were: what
   // the rings' slots and the barriers' phases go by.  Every role counts them alike.
