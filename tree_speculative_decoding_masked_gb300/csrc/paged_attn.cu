@@ -1,6 +1,7 @@
 // Paged attention's entry: the kernel for a call.
 //   fp32, more than 16 query rows a KV head  paged_f32_kernel (row tiles on CUDA cores)
-//   other fp32                               paged_simt_kernel
+//   fp32, at most 4                          paged_rows_kernel (keys over the warps)
+//   other fp32                               paged_simt_kernel (a row or two a warp)
 //   bf16, more than 16 query rows a KV head,
 //     D <= 128, G <= 16                      paged_tc_kernel (row tiles on tcgen05)
 //   other bf16                               paged_mma_kernel (a stream of keys past few rows)
