@@ -29,6 +29,10 @@ frontier   TreeGraft §3.1 single-drafter expansion: frontier Top_W by s(v), the
            tokens of each frontier node's drafter distribution attached as children.
 prune      PTD §3.1 "overhead constraints": a per-parent child cap and the sliding-window
            stepping of the root when the tree gets too deep (page truncated there).
+rotary     rotary positions: pair rotation by position times frequency, and the frequency
+           scalings long-context models use (linear, base, banded, yarn).
+paged      the round over a cache in pages: append of rotated rows, causal and tree attention
+           with a window and a score cap over ragged lengths, commit of the accepted path.
 
 Readings taken where the pages are silent are listed in each module's docstring.
 Parity status: every function is pinned by tests under ``tests/test_oracle_*.py``
