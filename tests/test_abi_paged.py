@@ -223,3 +223,16 @@ def test_binding_refusals(lib):  # noqa: F811
            _Fake((3,), i32))
     refuse("new_len must be", tv.commit_accepted_kv_paged, kc, kc, table, pre, _Fake((2, 5), i32), pre,
            new_len=_Fake((2,), f32))
+
+
+def test_attention_output_and_workspace_refusals(lib):  # noqa: F811
+    import tree_speculative_decoding_masked_gb300 as tv
+    for dt in (0, 1):  # q itself: other CTAs may still read it
+        assert lib.tv_paged_attention(FAKE, FAKE, _kv(), NULL, NULL, 1, 4, 2, 3, 64, 0.0, 0.0, 0, dt,
+                                      ctypes.c_void_p(0x2000), 1 << 40, NULL, NULL) == -8
+    x, kc, table, pre = _Fake((2, 4, 3, 64)), _Fake((9, 2, 16, 64)), _Fake((2, 4), torch.int32), _Fake((2,), torch.int32)
+    # an expanded workspace holds fewer bytes than its elements count
+    ws = _Fake((1 << 30,), torch.uint8, stride=(0,))
+    with pytest.raises(ValueError, match="workspace must be contiguous"):
+        tv.paged_attention(x, kc, kc, table, pre, out=_Fake((2, 4, 3, 64), ptr=0x9000), workspace=ws,
+                           dev_status=_Fake((1,), torch.int32))

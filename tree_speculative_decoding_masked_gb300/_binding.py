@@ -822,6 +822,8 @@ def paged_attention(q, k_cache, v_cache, page_table, prefix_len, *, parent=None,
         workspace = torch.zeros(max(int(n), 256), dtype=torch.uint8, device=index)
     elif workspace.get_device() != index:
         _wrong_device("workspace", workspace, index)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     _launch("tv_paged_attention", index, q_p, out_p, kv, parent_p, rows_p, B, Hq, Hkv, N, D, scale, softcap, int(window),
             code, workspace.data_ptr(), workspace.numel() * workspace.element_size(), st.data_ptr())
     return out
