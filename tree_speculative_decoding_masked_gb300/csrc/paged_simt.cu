@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kPsWarps * 32, kDPL <= 4 ? 2 : 1) paged_simt_k
 // above, leaves most warps without work here: 32 sequences of 4000 to 8000 tokens, 8 heads of 128,
 // one row each 583 us that way and 234 this (6.8 TB/s, the copy rate); 64 of them with four rows
 // a head 1151 and 680 (4.7 TB/s: at 255 registers one CTA an SM with two tiles in flight; two CTAs
-// with one tile each 723).
+// with one tile each 723).  Eight rows, 32 sequences of 2000 to 4000: a row a warp 311, this 433.
 template <int kDPL, int kR>
 struct PrCfg {
   static constexpr int kD = kDPL * 32;
