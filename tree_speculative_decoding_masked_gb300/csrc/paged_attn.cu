@@ -5,9 +5,10 @@
 //   bf16, more than 16 query rows a KV head,
 //     D <= 128, G <= 16                      paged_tc_kernel (row tiles on tcgen05)
 //   other bf16                               paged_mma_kernel (a stream of keys past few rows)
-// 64 sequences of 8192 to 16384 tokens, G = 4: at 16 rows (4 nodes) the stream takes 483 us and
-// row tiles 590; at 32 (8 nodes) the stream's warp-level products set the pace, 754 us
-// against 593.  One sequence of 2048: 32 rows 14.3 against 12.9 us.
+// 64 sequences of 8192 to 16384 tokens, G = 4: at 16 rows (4 nodes) the stream takes 486 us and
+// row tiles 539; at 32 (8 nodes) the stream's warp-level products set the pace, 768 us against
+// 540.  Over 500 to 1000 tokens 75 against 69 us at 16 rows and 115 against 69 at 32; one sequence
+// of 2048 12.0 against 11.5 and 15.2 against 11.5: the rule gives short ranges' 5 % for long ones' 10.
 #include <atomic>
 
 #include "paged.cuh"
