@@ -98,14 +98,14 @@ __global__ void __launch_bounds__(kRotThreads, 4) rotary_kernel(RotaryArgs a, in
   if (token >= (long long)a.B * a.N) return;
   const int col = (int)(id - token * cols);
   const int b = (int)(token / a.N), t = (int)(token - (long long)b * a.N);
-  const int off = a.pos ? a.pos[token] : t;
-  const int base = a.base ? a.base[b] : 0;
-  const int n = a.n_rows ? a.n_rows[b] : a.N;
-  if (a.table && (base < 0 || n < 0 || n > a.N)) {  // also where no row is active
-    set_dev_status(a.dev_status, TV_DEV_BAD_PAGE);
-    return;
+  if (a.table && t == 0 && col == 0 && blockIdx.y == 0) {  // counts and lengths, also where no row is active
+    const int n = a.n_rows ? a.n_rows[b] : 0;
+    if (n < 0 || n > a.N || a.base[b] < 0) set_dev_status(a.dev_status, TV_DEV_BAD_PAGE);
   }
-  if (t >= n || off < 0) return;  // inactive
+  const int off = a.pos ? a.pos[token] : t;
+  if (off < 0) return;  // padding
+  const int base = a.base ? a.base[b] : 0;
+  if (a.n_rows && (t >= a.n_rows[b] || a.n_rows[b] > a.N)) return;
   const long long p = (long long)base + off;
   const int heads = a.Hq + 2 * a.Hkv;
   const int h0 = blockIdx.y * hg, h1 = min(heads, h0 + hg);
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kRotThreads, 4) rotary_kernel(RotaryArgs a, in
   if (h1 > a.Hq) {
     const long long r = (long long)base + t;
     const long long pg = r >> a.page_shift;
-    const int page = pg < a.max_pages ? a.table[(size_t)b * a.max_pages + pg] : -1;
+    const int page = base >= 0 && pg < a.max_pages ? a.table[(size_t)b * a.max_pages + pg] : -1;
     if (page >= 0 && page < a.num_pages)
       page_row = ((long long)page * a.Hkv << a.page_shift) + (r & ((1 << a.page_shift) - 1));
     else
