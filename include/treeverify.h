@@ -578,8 +578,9 @@ TV_API tv_status tv_rotary(const tv_rows* x, void* out, const int32_t* pos, cons
  * 0..N, or a needed page outside [0, num_pages) set TV_DEV_BAD_PAGE; nothing outside the
  * pool is read or written, and the sequence's outputs are unspecified.
  * n_rows [B] (or NULL: N) counts the active new rows of each sequence; those from
- * n_rows[b] on, and in a tree those from the first padding row (parent -1) on, are
- * inactive: not read, not written.
+ * n_rows[b] on are inactive: not read, not written.  So are a tree's padding rows: where
+ * `parent` is passed those from the first parent -1 on; the append, which sees no parent,
+ * goes by each row's own depth, and tv_tree_prep's is -1 from the first padding row on.
  */
 typedef struct tv_paged_kv {
   void* k;
@@ -593,8 +594,8 @@ typedef struct tv_paged_kv {
  * on the way, and (optionally) rotate their queries in the same pass.
  *   k, v   rows [B][Hkv][N][D] dtype (any strides)
  *   q      rows [B][Hq][N][D] or NULL; q_out [B][Hq][N][D] contiguous (with q)
- *   depth  [B][N] int32: row t sits at position P_b + depth[b][t] (tv_tree_prep's depth;
- *          -1 = padding, not written); NULL: P_b + t
+ *   depth  [B][N] int32: row t sits at position P_b + depth[b][t] (tv_tree_prep's depth);
+ *          a row of negative depth is not written, whatever the others hold; NULL: P_b + t
  *   rope   NULL: nothing is rotated (and q must be NULL)
  * Row t goes to cache row P_b + t.  Limits: D <= 1024, rows of D elements a multiple of 16
  * bytes, caches 16-byte aligned.

@@ -1,8 +1,10 @@
 """GPU tests of what the header promises for calls over pages beside their results."""
+import numpy as np
 import pytest
 
 import synth
-from test_gpu_paged import _status
+from oracle import paged, rotary
+from test_gpu_paged import _status, _unit
 
 pytestmark = pytest.mark.gpu
 
@@ -11,7 +13,7 @@ if not torch.cuda.is_available():
     pytest.skip("needs a GPU", allow_module_level=True)
 
 import tree_speculative_decoding_masked_gb300 as tv  # noqa: E402
-from gpu_util import dev, i32, to_dev  # noqa: E402
+from gpu_util import dev, host, i32, to_dev  # noqa: E402
 
 
 # ---- append: counts and padding
@@ -44,3 +46,39 @@ def test_append_reports_a_negative_length_without_rows():
                            dev_status=st)
         torch.cuda.synchronize()
         assert int(st.item()) == want and not pool.any()
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("D", [64, 40])
+@pytest.mark.parametrize("N,pad", [(5, 2), (70, 1), (70, 33), (70, 69), (300, 130)])
+def test_append_goes_by_each_rows_depth(N, pad, D, bf16):
+    # sequence 0 has no padding, 1 a row of negative depth among others, 2 what tree_prep makes of a
+    # padded tree: -1 from the first padding row on
+    g = synth.rng(4100 + N + pad)
+    B, ps = 3, 8
+    prefix = [3, 16, 9]
+    dep = np.stack([np.minimum(np.arange(N), 7)] * B).astype(np.int32)
+    dep[1, pad] = -5
+    par = synth.chain_parents(N)[None].astype(np.int32)
+    par[0, pad:] = -1
+    dep[2] = host(tv.tree_prep(i32(par), 0)["depth"])[0]
+    assert np.array_equal(dep[2] < 0, np.arange(N) >= pad)
+    width = (max(prefix) + N + ps - 1) // ps
+    table = g.permutation(B * width).reshape(B, width).astype(np.int32)
+    k, v = (synth.normal(g, (B, 2, N, D), 1.0, bf16) for _ in range(2))
+    q = synth.normal(g, (B, 4, N, D), 1.0, bf16)
+    rope, (f, amp) = tv.rotary_frequencies(20), rotary.frequencies(20)
+    kd = torch.full((B * width, 2, ps, D), 1024.0, dtype=torch.bfloat16 if bf16 else torch.float32, device=dev())
+    vd, st, qo = kd.clone(), _status(), torch.full(q.shape, 1024.0, dtype=kd.dtype, device=dev())
+    tv.append_kv_paged(to_dev(k, bf16), to_dev(v, bf16), kd, vd, i32(table), i32(prefix), depth=i32(dep), rope=rope,
+                       q=to_dev(q, bf16), q_out=qo, dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    fresh = np.full(kd.shape, 1024.0)
+    kr, vr = paged.append(k, v, fresh, fresh, table, prefix, dep, None, f, amp)
+    assert np.array_equal(host(vd), vr)
+    kg, qg = host(kd).astype(np.float64), host(qo).astype(np.float64)
+    bound = amp * 2.0 ** -21 * 2 * np.max(np.abs(k)) + _unit(bf16) * np.abs(kr)
+    assert np.array_equal(kg == 1024.0, kr == 1024.0) and np.all(np.abs(kg - kr) <= bound)
+    off = np.broadcast_to((dep < 0)[:, None, :, None], qg.shape)
+    assert np.all(qg[off] == 1024.0) and not np.any(qg[~off] == 1024.0)

@@ -752,8 +752,8 @@ def append_kv_paged(k, v, k_cache, v_cache, page_table, prefix_len, *, depth=Non
                     interleaved: bool = False, q=None, q_out=None, dev_status=None):
     """Write new rows k, v [B][Hkv][N][D] (any strides, contiguous elements) into the paged
     caches [num_pages][Hkv][page_size][D] at cache rows prefix_len[b] + t, the keys rotated
-    (with rope) at position prefix_len[b] + depth[b][t] (depth: tree_prep's, -1 = padding;
-    omitted: t).  page_table [B][max_pages], prefix_len [B], n_rows [B] (omitted: N each) are
+    (with rope) at position prefix_len[b] + depth[b][t] (depth: tree_prep's; a row of negative
+    depth is not written; omitted: t).  page_table [B][max_pages], prefix_len [B], n_rows [B] (omitted: N each) are
     int32.  With q [B][Hq][N][D] its rows are rotated too, into q_out (returned)."""
     index = _device_index("k_cache", k_cache)
     kv, B, Hkv, _, _, D = _paged_kv(k_cache, v_cache, page_table, prefix_len, index)
