@@ -4,7 +4,7 @@ import pytest
 
 import synth
 from oracle import paged, rotary
-from test_gpu_paged import _status, _unit
+from test_gpu_paged import _pages, _status, _unit
 
 pytestmark = pytest.mark.gpu
 
@@ -82,3 +82,42 @@ def test_append_goes_by_each_rows_depth(N, pad, D, bf16):
     assert np.array_equal(kg == 1024.0, kr == 1024.0) and np.all(np.abs(kg - kr) <= bound)
     off = np.broadcast_to((dep < 0)[:, None, :, None], qg.shape)
     assert np.all(qg[off] == 1024.0) and not np.any(qg[~off] == 1024.0)
+
+
+# ---- caps of any size
+
+def _capped(g, B, Hq, Hkv, D, ps, prefix, N, softcap, std, bf16):
+    """Largest error over tolerance.  A row's scores are at most Z = max_j scale |q| . |k_j|, and the cap makes
+    them no larger: its error is relative, 2^-21 of min(softcap, Z), however large the cap.  The rest as in
+    test_gpu_paged.py."""
+    kc, vc, table = _pages(g, B, Hkv, D, ps, [p + N for p in prefix], max(prefix) + N, bf16, None, std)
+    q = synth.normal(g, (B, Hq, N, D), std, bf16)
+    st = _status()
+    out = tv.paged_attention(to_dev(q, bf16), to_dev(kc, bf16), to_dev(vc, bf16), i32(table), i32(prefix),
+                             softcap=softcap, dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    ref, mass, big = paged.attention(q, kc, vc, table, prefix, softcap=softcap)
+    keys = np.array(prefix)[:, None, None, None] + N
+    e = (2 * D * 2.0 ** -23 + 2.0 ** -21) * big[..., None] + 2.0 ** -22 + keys * 2.0 ** -23
+    tol = (2 * e + (2.0 ** -8 if bf16 else 0)) * mass + _unit(bf16) * np.abs(ref)
+    return np.max(np.abs(host(out) - ref) / tol)
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("softcap", [300.0, 1e4, 1e6, 1e8, 1e30, 3.2e38])
+@pytest.mark.parametrize("Hq,Hkv,D,N", [(8, 2, 128, 1), (8, 2, 64, 70), (2, 1, 256, 20), (32, 1, 96, 3)])
+def test_large_caps_cost_no_precision(Hq, Hkv, D, N, softcap, bf16):
+    g = synth.rng(4200 + D + N)
+    for std in (1.0, 2.5):
+        assert _capped(g, 2, Hq, Hkv, D, 16, [50, 133], N, softcap, std, bf16) <= 1.0
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("softcap", [1e4, 1e8])
+@pytest.mark.parametrize("N", [1, 11])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_large_caps_on_the_persistent_schedule(D, N, softcap, bf16):
+    g = synth.rng(4250 + D + N)
+    B = 170 if D <= 64 else 80
+    assert _capped(g, B, 2, 1, D, 8, [(53 * b) % 150 for b in range(B)], N, softcap, 1.0, bf16) <= 1.0

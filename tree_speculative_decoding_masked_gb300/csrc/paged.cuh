@@ -288,6 +288,14 @@ __device__ __forceinline__ int unit_slot(long long c, long long per, long long u
   return (int)(2 * c + (u0 < c * per ? 0 : 1));
 }
 
+// How scores are capped in the bf16 kernels: not at all; by soft_tanh; or, past kPlainCap, by capped_score.
+// soft_tanh is off by some 2^-22 of 1 however small its argument, and a score by that times the cap:
+// at 256 a weight by 2^-14, little beside its rounding to bf16.  Two chunks of 2048 rows over 3000 to 6000
+// tokens: 526 us by soft_tanh4, 1096 by capped_score; one token each of 32 sequences 125 by either.
+enum { kNoCap, kTanhCap, kLargeCap };
+constexpr float kPlainCap = 256.f;
+inline int cap_mode(float cap) { return cap > kPlainCap ? kLargeCap : cap > 0.f ? kTanhCap : kNoCap; }
+
 // tanh(y / 2) with y given as x = y log2 e: 1 - 2 / (1 + 2^x), off by an ulp or two of 1
 __device__ __forceinline__ float soft_tanh(float x) {
   float r;
@@ -295,17 +303,28 @@ __device__ __forceinline__ float soft_tanh(float x) {
   return fmaf(-2.f, r, 1.f);
 }
 
-// tanh to an ulp or two: its Taylor series up to x^13 below 0.45 (the next term is 2^-25 of x),
-// where capped scores mostly lie, else the library's
-__device__ __forceinline__ float tanh_f32(float x) {
-  const float z = x * x;
-  if (z >= 0.2025f || isnan(x)) return tanhf(x);
+// (tanh x - x) / x^3 for z = x^2 below 0.45^2: the Taylor series up to x^13 (the next term is 2^-25 of x)
+__device__ __forceinline__ float tanh_tail(float z) {
   float p = fmaf(z, 3.5921280e-3f, -8.8632355e-3f);  // 21844 / 6081075, -1382 / 155925
   p = fmaf(z, p, 2.1869489e-2f);                     // 62 / 2835
   p = fmaf(z, p, -5.3968254e-2f);                    // -17 / 315
   p = fmaf(z, p, 1.3333333e-1f);
-  p = fmaf(z, p, -3.3333333e-1f);
-  return fmaf(x * z, p, x);
+  return fmaf(z, p, -3.3333333e-1f);
+}
+constexpr float kTanhNear = 0.2025f;
+
+// tanh to an ulp or two: the series below 0.45, where capped scores mostly lie, else the library's
+__device__ __forceinline__ float tanh_f32(float x) {
+  const float z = x * x;
+  if (z >= kTanhNear || isnan(x)) return tanhf(x);
+  return fmaf(x * z, tanh_tail(z), x);
+}
+
+// cap tanh(t / cap) to some 2^-21 of itself, at any cap: below 0.45 cap the series as a correction of t
+__device__ __forceinline__ float capped_score(float t, float cap, float inv_cap) {
+  const float x = t * inv_cap, z = x * x;
+  const float far = cap * soft_tanh(x * (2.f * kLog2e));
+  return z >= kTanhNear ? far : fmaf(t * z, tanh_tail(z), t);
 }
 
 // four soft_tanh with one reciprocal: 1 / a = (1 / abcd) (b cd).  2^x is held below 2^30, where tanh

@@ -118,7 +118,7 @@ __device__ __forceinline__ bool pm_next(const PagedAttn& a, UnitWalk& w, int spl
   return true;
 }
 
-template <int kD, int kRT, bool kCap, bool kStream>
+template <int kD, int kRT, int kCap, bool kStream>
 __global__ void __launch_bounds__(PmCfg<kD, kRT>::kThreads, 1)
     paged_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, PagedAttn a,
                      int splits, int row_tiles, int wide) {
@@ -242,8 +242,8 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT>::kThreads, 1)
     int* s_par = reinterpret_cast<int*>(sm + C::kOffPar);
     float* sO = reinterpret_cast<float*>(sm + C::kOffU);
     const int kg = lane >> 2, rg = (lane & 3) * 2;  // this lane's keys (columns) kg, kg + 8 and rows rg, rg + 1
-    const float c = kCap ? a.cap * kLog2e : a.scale * kLog2e;
-    const float ck = kCap ? 2.f * kLog2e * a.scale / a.cap : 0.f;
+    const float c = kCap == kLargeCap ? kLog2e : kCap ? a.cap * kLog2e : a.scale * kLog2e;
+    const float ck = kCap == kLargeCap ? 1.f / a.cap : kCap ? 2.f * kLog2e * a.scale / a.cap : 0.f;
     bool ok = true;
     // (maximum, sum) of row rr over the warps
     auto row_max = [&](int rr) -> float {
@@ -413,7 +413,8 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT>::kThreads, 1)
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             float z = s[nt][0][u] + s[nt][1][u];
-            if constexpr (kCap) z = soft_tanh(z * ck);
+            if constexpr (kCap == kTanhCap) z = soft_tanh(z * ck);
+            if constexpr (kCap == kLargeCap) z = capped_score(z * a.scale, a.cap, ck);
             z *= c;
             if (masked) {
               const int rr = nt * 8 + rg + (u & 1), j = j0 + kg + (u >> 1) * 8;
@@ -686,7 +687,7 @@ static PmPlan pm_plan(int B, int Hq, int Hkv, int D, int N) {
 
 size_t paged_mma_ws(int B, int Hq, int Hkv, int D, int N) { return pm_plan(B, Hq, Hkv, D, N).bytes; }
 
-template <int kD, int kRT, bool kCap, bool kStream>
+template <int kD, int kRT, int kCap, bool kStream>
 static cudaError_t launch_pm(const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a, const PmPlan& p,
                              cudaStream_t stream) {
   using C = PmCfg<kD, kRT>;
@@ -706,14 +707,24 @@ static cudaError_t launch_pm(const CUtensorMap& mk, const CUtensorMap& mv, const
                     C::kSmem, stream, attr, 1, mk, mv, a, p.splits, p.row_tiles, wide);
 }
 
+template <int kD, int kRT, int kCap>
+static cudaError_t launch_pm_s(const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a, const PmPlan& p,
+                               cudaStream_t stream) {
+  return p.splits ? launch_pm<kD, kRT, kCap, false>(mk, mv, a, p, stream)
+                  : launch_pm<kD, kRT, kCap, true>(mk, mv, a, p, stream);
+}
+
 template <int kD, int kRT>
 static cudaError_t launch_pm_c(const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a, const PmPlan& p,
                                cudaStream_t stream) {
-  if (a.cap > 0.f)
-    return p.splits ? launch_pm<kD, kRT, true, false>(mk, mv, a, p, stream)
-                    : launch_pm<kD, kRT, true, true>(mk, mv, a, p, stream);
-  return p.splits ? launch_pm<kD, kRT, false, false>(mk, mv, a, p, stream)
-                  : launch_pm<kD, kRT, false, true>(mk, mv, a, p, stream);
+  switch (cap_mode(a.cap)) {
+    case kLargeCap:
+      return launch_pm_s<kD, kRT, kLargeCap>(mk, mv, a, p, stream);
+    case kTanhCap:
+      return launch_pm_s<kD, kRT, kTanhCap>(mk, mv, a, p, stream);
+    default:
+      return launch_pm_s<kD, kRT, kNoCap>(mk, mv, a, p, stream);
+  }
 }
 
 template <int kD>

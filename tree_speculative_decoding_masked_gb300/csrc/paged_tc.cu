@@ -229,7 +229,7 @@ __device__ __forceinline__ void pt_bars_init(PtBars* bars) {
   ptx::fence_mbar_init();
 }
 
-template <int D, bool kCap, bool kStream>
+template <int D, int kCap, bool kStream>
 __global__ void __launch_bounds__(kPtThreads, 1)
     paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, PagedAttn a, PtArgs pa) {
@@ -614,8 +614,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         }
         if (a.window > 0) wlo = P + depth - a.window + 1;
       }
-      const float c = kCap ? a.cap * kLog2e : a.scale * kLog2e;
-      const float ck = kCap ? 2.f * kLog2e * a.scale / a.cap : 0.f;
+      const float c = kCap == kLargeCap ? kLog2e : kCap ? a.cap * kLog2e : a.scale * kLog2e;
+      const float ck = kCap == kLargeCap ? 1.f / a.cap : kCap ? 2.f * kLog2e * a.scale / a.cap : 0.f;
       for (int t = 0; ok && t < ntm; ++t) {
         const unsigned tx = dx + t;
         const int buf = tx & 1;
@@ -639,9 +639,12 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         ptx::tmem_ld32(colS + buf * kPtKeys, sv);
         ptx::tmem_ld32(colS + buf * kPtKeys + 32, sv + 32);
         ptx::tmem_wait_ld();
-        if constexpr (kCap) {
+        if constexpr (kCap == kTanhCap) {
 #pragma unroll
           for (int j = 0; j < 64; j += 4) soft_tanh4(sv + j, ck);
+        } else if constexpr (kCap == kLargeCap) {
+#pragma unroll
+          for (int j = 0; j < 64; ++j) sv[j] = capped_score(sv[j] * a.scale, a.cap, ck);
         }
         if (vis != ~0ull) {
 #pragma unroll
@@ -935,7 +938,7 @@ static int pt_clusters(int D, int s) {
   int n = known[dev][s].load(std::memory_order_relaxed) - 1;
   if (n < 0) {
     // every instance takes one CTA per SM, so one stands for all
-    const void* fn = reinterpret_cast<const void*>(paged_tc_kernel<128, false, false>);
+    const void* fn = reinterpret_cast<const void*>(paged_tc_kernel<128, kNoCap, false>);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(s * 64, 1, 1);
     cfg.blockDim = dim3(kPtThreads, 1, 1);
@@ -986,7 +989,7 @@ bool paged_tc_takes(int Hq, int Hkv, int D, int N) {
 
 size_t paged_tc_ws(int B, int Hq, int Hkv, int D, int N) { return pt_plan(B, Hq, Hkv, D, N).bytes; }
 
-template <int D, bool kCap, bool kStream>
+template <int D, int kCap, bool kStream>
 static cudaError_t launch_pt(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a,
                              const PtPlan& p, cudaStream_t stream) {
   constexpr int smem = PtCfg<D>::kSmemAlloc;
@@ -1006,6 +1009,25 @@ static cudaError_t launch_pt(const CUtensorMap& mq, const CUtensorMap& mk, const
                     dim3(kPtThreads), smem, stream, attr, 1, mq, mk, mv, a, pa);
 }
 
+template <int D, int kCap>
+static cudaError_t launch_pt_c(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a,
+                               const PtPlan& p, cudaStream_t stream) {
+  return p.splits ? launch_pt<D, kCap, false>(mq, mk, mv, a, p, stream)
+                  : launch_pt<D, kCap, true>(mq, mk, mv, a, p, stream);
+}
+template <int D>
+static cudaError_t launch_pt_d(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a,
+                               const PtPlan& p, cudaStream_t stream) {
+  switch (cap_mode(a.cap)) {
+    case kLargeCap:
+      return launch_pt_c<D, kLargeCap>(mq, mk, mv, a, p, stream);
+    case kTanhCap:
+      return launch_pt_c<D, kTanhCap>(mq, mk, mv, a, p, stream);
+    default:
+      return launch_pt_c<D, kNoCap>(mq, mk, mv, a, p, stream);
+  }
+}
+
 cudaError_t launch_paged_tc(PagedAttn a, char* ws, cudaStream_t stream) {
   const PtPlan p = pt_plan(a.B, a.Hq, a.Hkv, a.D, a.N);
   a.cnt = reinterpret_cast<unsigned*>(ws);
@@ -1015,17 +1037,7 @@ cudaError_t launch_paged_tc(PagedAttn a, char* ws, cudaStream_t stream) {
   if (!pt_tmap(&mq, a.q, a.D, a.N, (long long)a.B * a.Hq, p.NT) || !paged_kv_tmap(&mk, a.k, a) ||
       !paged_kv_tmap(&mv, a.v, a))
     return cudaErrorInvalidValue;
-  const bool cap = a.cap > 0.f, str = p.splits == 0;
-  if (a.D <= 64) {
-    if (cap) return str ? launch_pt<64, true, true>(mq, mk, mv, a, p, stream)
-                        : launch_pt<64, true, false>(mq, mk, mv, a, p, stream);
-    return str ? launch_pt<64, false, true>(mq, mk, mv, a, p, stream)
-               : launch_pt<64, false, false>(mq, mk, mv, a, p, stream);
-  }
-  if (cap) return str ? launch_pt<128, true, true>(mq, mk, mv, a, p, stream)
-                      : launch_pt<128, true, false>(mq, mk, mv, a, p, stream);
-  return str ? launch_pt<128, false, true>(mq, mk, mv, a, p, stream)
-             : launch_pt<128, false, false>(mq, mk, mv, a, p, stream);
+  return a.D <= 64 ? launch_pt_d<64>(mq, mk, mv, a, p, stream) : launch_pt_d<128>(mq, mk, mv, a, p, stream);
 }
 
 }  // namespace tv
