@@ -619,7 +619,7 @@ TV_API tv_status tv_append_kv_paged(const tv_rows* k, const tv_rows* v, const tv
  *   parent  [B][N] int32 (tree layout above) or NULL
  *   scale   > 0, or 0 for 1/sqrt(D);  softcap, window: 0 = none
  * The keys and values of active rows and of committed rows within the window must be
- * finite; other cache rows may hold anything, NaN included.
+ * finite; other cache rows may hold anything, NaN included.  A query row with a NaN gives a NaN row.
  * Precision as tv_tree_attention; a capped score is off by up to 2^-20 of itself or, bf16 with
  * softcap <= 256, by 2^-13.  Limits: 32 <= D <= 256, D % 32 == 0, Hq % Hkv == 0,
  * 1 <= N <= 65536 (trees 1024), G * N < 2^24.  q, out and the caches 16-byte aligned.

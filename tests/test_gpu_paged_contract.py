@@ -121,3 +121,25 @@ def test_large_caps_on_the_persistent_schedule(D, N, softcap, bf16):
     g = synth.rng(4250 + D + N)
     B = 170 if D <= 64 else 80
     assert _capped(g, B, 2, 1, D, 8, [(53 * b) % 150 for b in range(B)], N, softcap, 1.0, bf16) <= 1.0
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("softcap", [0.0, 20.0, 1e6])
+@pytest.mark.parametrize("B,Hkv,N", [(2, 2, 1), (2, 2, 7), (2, 2, 70), (30, 8, 45)])
+def test_a_nan_query_gives_a_nan_row_and_no_other(B, Hkv, N, softcap, bf16):
+    g = synth.rng(4300 + N)
+    Hq, D, ps = 2 * Hkv, 64, 16
+    prefix = [(41 * b) % 200 + 1 for b in range(B)]
+    kc, vc, table = _pages(g, B, Hkv, D, ps, [p + N for p in prefix], 201 + N, bf16)
+    q = to_dev(synth.normal(g, (B, Hq, N, D), 1.0, bf16), bf16)
+    args = (to_dev(kc, bf16), to_dev(vc, bf16), i32(table), i32(prefix))
+    clean = tv.paged_attention(q, *args, softcap=softcap)
+    assert bool(torch.isfinite(clean).all())
+    sick = q.clone()
+    where = torch.zeros((B, Hq, N), dtype=torch.bool, device=dev())
+    for b, h, i in ((0, 1, N - 1), (1, 0, N // 2), (B - 1, Hq - 1, 0)):
+        where[b, h, i] = True
+        sick[b, h, i, (7 * i + h) % D] = float("nan")
+    got = tv.paged_attention(sick, *args, softcap=softcap)
+    assert bool(torch.isnan(got[where]).all())
+    assert torch.equal(got[~where], clean[~where])

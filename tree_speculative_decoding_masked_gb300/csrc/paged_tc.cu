@@ -640,6 +640,11 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         ptx::tmem_ld32(colS + buf * kPtKeys + 32, sv + 32);
         ptx::tmem_wait_ld();
         if constexpr (kCap == kTanhCap) {
+          if (vis != ~0ull) {
+#pragma unroll
+            for (int j = 0; j < 64; ++j)
+              if (!((vis >> j) & 1ull)) sv[j] = 0.f;
+          }
 #pragma unroll
           for (int j = 0; j < 64; j += 4) soft_tanh4(sv + j, ck);
         } else if constexpr (kCap == kLargeCap) {
@@ -696,6 +701,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         if (lane == 0) ptx::mbar_arrive(&bars->p_full[x][buf]);
       }
       // ---- epilogue: every MMA is complete at o_done
+      if (isnan(l_run)) m_run = l_run;  // a NaN query's part: no part without a visible key, which merges leave out
       if (nt > 0) {
         ok = ok && __all_sync(0xffffffffu, ptx::mbar_wait(&bars->o_done, pieces & 1, abort_flag));
         have_o = ok && ntm > 0;
