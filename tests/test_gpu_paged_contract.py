@@ -4,7 +4,7 @@ import pytest
 
 import synth
 from oracle import paged, rotary
-from test_gpu_paged import _pages, _status, _unit
+from test_gpu_paged import _attend_check, _pages, _status, _unit
 
 pytestmark = pytest.mark.gpu
 
@@ -143,3 +143,21 @@ def test_a_nan_query_gives_a_nan_row_and_no_other(B, Hkv, N, softcap, bf16):
     got = tv.paged_attention(sick, *args, softcap=softcap)
     assert bool(torch.isnan(got[where]).all())
     assert torch.equal(got[~where], clean[~where])
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("parent", [False, True])
+@pytest.mark.parametrize("N", [1, 7, 60])
+def test_no_active_rows_on_the_persistent_schedule(N, parent, bf16):
+    # 320 units; then one row in the middle of them, and none again on the same workspace
+    g = synth.rng(4400 + N)
+    B, Hkv, D, ps = 40, 8, 64, 16
+    par = np.stack([synth.chain_parents(N)] * B).astype(np.int32) if parent else None
+    prefix = [(31 * b) % 100 for b in range(B)]
+    rows = [0] * B
+    ws = torch.zeros(tv.paged_attention_workspace_size(B, 2 * Hkv, Hkv, D, N, ps, 200 // ps + 2,
+                                                       torch.bfloat16 if bf16 else torch.float32),
+                     dtype=torch.uint8, device=dev())
+    for n in (0, 1, 0):
+        rows[17] = n
+        _attend_check(g, B, 2 * Hkv, Hkv, D, ps, prefix, N, parent=par, n_rows=rows, bf16=bf16, workspace=ws)

@@ -29,7 +29,7 @@ __device__ __forceinline__ int paged_rows(const PagedAttn& a, int b, int P, bool
 // r / G, so that a row tile spans few nodes and its key range ends at its last one.
 struct PagedSpan {
   long long W;      // key tiles in all
-  long long per;    // tiles per CTA
+  long long per;    // tiles per CTA, at least 1
   int b;            // where this CTA starts: sequence,
   long long base;   // and that sequence's first tile
   int whole;        // not 0: every unit counts as this many tiles, one unit per CTA
@@ -133,7 +133,7 @@ __device__ inline PagedSpan paged_span(const PagedAttn& a, int RT, int KT, int m
     __syncthreads();
     longest = red[0];
     __syncthreads();
-    if (all <= gridDim.x && longest + fix <= (unsigned long long)(sp.per + min(sp.per / 4 + 8, 30ll))) {
+    if (all > 0 && all <= gridDim.x && longest + fix <= (unsigned long long)(sp.per + min(sp.per / 4 + 8, 30ll))) {
       sp.whole = (int)longest;
       sp.per = sp.whole;
       W = all * longest;
