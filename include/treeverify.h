@@ -574,9 +574,9 @@ TV_API tv_status tv_rotary(const tv_rows* x, void* out, const int32_t* pos, cons
  * page_size: a power of two, 8..1024; max_pages * page_size <= 2^30.
  * Sequences may share pages of committed rows; a page that receives rows of two
  * sequences in one call holds either's.  Table entries that no row of the call needs may
- * hold anything.  On the device: P_b < 0, rows past max_pages pages, n_rows[b] outside
- * 0..N, or a needed page outside [0, num_pages) set TV_DEV_BAD_PAGE; nothing outside the
- * pool is read or written, and the sequence's outputs are unspecified.
+ * hold anything.  On the device: P_b < 0, an active row past max_pages pages, n_rows[b]
+ * outside 0..N, or a needed page outside [0, num_pages) set TV_DEV_BAD_PAGE; nothing outside
+ * the pool is read or written, and the sequence's outputs are unspecified.
  * n_rows [B] (or NULL: N) counts the active new rows of each sequence; those from
  * n_rows[b] on are inactive: not read, not written.  So are a tree's padding rows: where
  * `parent` is passed those from the first parent -1 on; the append, which sees no parent,

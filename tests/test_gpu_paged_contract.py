@@ -161,3 +161,37 @@ def test_no_active_rows_on_the_persistent_schedule(N, parent, bf16):
     for n in (0, 1, 0):
         rows[17] = n
         _attend_check(g, B, 2 * Hkv, Hkv, D, ps, prefix, N, parent=par, n_rows=rows, bf16=bf16, workspace=ws)
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("B,Hkv", [(3, 2), (45, 8)])
+@pytest.mark.parametrize("N,act", [(4, 1), (4, 3), (12, 5), (90, 8), (90, 23), (90, 77)])
+def test_padding_rows_need_no_pages(N, act, B, Hkv, bf16):
+    # every table ends with a sequence's last active row or the page that holds it
+    g = synth.rng(4500 + N + act)
+    D, ps, width = 64, 8, 24
+    prefix = [width * ps - act - (b % 3) for b in range(B)]
+    par = np.stack([synth.random_parents(synth.rng(b), N, 8) for b in range(B)]).astype(np.int32)
+    par[:, act:] = -1
+    count = B * width
+    table = g.permutation(count).reshape(B, width).astype(np.int32)
+    kc, vc = (synth.normal(g, (count, Hkv, ps, D), 1.0, bf16) for _ in range(2))
+    q = synth.normal(g, (B, 2 * Hkv, N, D), 1.0, bf16)
+    args = [to_dev(x, bf16) for x in (q, kc, vc)]
+    out, st = torch.full_like(args[0], 7.0), _status()
+    tv.paged_attention(*args, i32(table), i32(prefix), parent=i32(par), out=out, dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    got = host(out)
+    assert np.all(got[:, :, act:] == 7.0)
+    some = [0, 1, B - 1]  # the oracle's loops are slow
+    ref, mass, big = paged.attention(q[some], kc, vc, table[some], [prefix[b] for b in some], par[some])
+    e = 2 * D * 2.0 ** -23 * big[..., None] + 2.0 ** -22 + width * ps * 2.0 ** -23
+    tol = (2 * e + (2.0 ** -8 if bf16 else 0)) * mass + _unit(bf16) * np.abs(ref)
+    assert np.all(np.abs(got[some] - ref)[:, :, :act] <= tol[:, :, :act])
+    # an active row that does not fit
+    st = _status()
+    prefix[1] = width * ps - act + 1
+    tv.paged_attention(*args, i32(table), i32(prefix), parent=i32(par), dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == tv.TV_DEV_BAD_PAGE

@@ -13,13 +13,17 @@
 
 namespace tv {
 
-// New rows of sequence b that the call looks at: n_rows[b] clamped to 0..N (N without
-// n_rows), or 0 for a sequence whose rows do not fit its page table (*bad).
+// New rows of sequence b that the call looks at: n_rows[b] (N without n_rows), or 0 for a sequence with a
+// row that does not fit its page table (*bad).  A padded tree's inactive rows need no place: where the
+// table ends at one, the rows in front of it count.
 __device__ __forceinline__ int paged_rows(const PagedAttn& a, int b, int P, bool* bad) {
-  int n = a.n_rows ? a.n_rows[b] : a.N;
-  const bool fits = P >= 0 && n >= 0 && n <= a.N && (long long)P + n <= (long long)a.max_pages << a.page_shift;
-  *bad = !fits;
-  return fits ? n : 0;
+  const int n = a.n_rows ? a.n_rows[b] : a.N;
+  *bad = P < 0 || n < 0 || n > a.N;
+  if (*bad) return 0;
+  const long long room = ((long long)a.max_pages << a.page_shift) - P;
+  if (n <= room) return n;
+  *bad = !a.parent || room < 1 || a.parent[(size_t)b * a.N + room] != -1;
+  return *bad ? 0 : (int)room;
 }
 
 // One CTA's share of the attention work.  The work is cut into units (sequence b, KV head,
