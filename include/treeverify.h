@@ -639,10 +639,10 @@ TV_API tv_status tv_paged_attention(const void* q, void* out, const tv_paged_kv*
 /* tv_commit_accepted_kv_paged - tv_commit_accepted_kv through the page table: row P_b + a_k
  * of every KV head of both caches is copied to row P_b + k, k = 1..L_b.
  *   accepted_nodes [B][N], accept_len [B] int32 as tv_verify_* write them
- *   new_len [B] int32 out or NULL: P_b + L_b + 1, the next round's prefix_len (another
- *   array than prefix_len)
+ *   new_len [B] int32 out or NULL: P_b + L_b + 1, the next round's prefix_len; it may not
+ *   overlap prefix_len, accept_len, accepted_nodes or page_table, which are read meanwhile
  * Device checks as tv_commit_accepted_kv (TV_DEV_BAD_TREE) and of pages (TV_DEV_BAD_PAGE).
- * Host errors as there, and new_len == prefix_len -> TV_ERR_VALUE.  No workspace.
+ * Host errors as there, and new_len over one of those -> TV_ERR_VALUE.  No workspace.
  */
 TV_API tv_status tv_commit_accepted_kv_paged(const tv_paged_kv* kv, const int32_t* accepted_nodes,
                                              const int32_t* accept_len, int32_t* new_len, int B, int Hkv,

@@ -195,3 +195,18 @@ def test_padding_rows_need_no_pages(N, act, B, Hkv, bf16):
     tv.paged_attention(*args, i32(table), i32(prefix), parent=i32(par), dev_status=st)
     torch.cuda.synchronize()
     assert int(st.item()) == tv.TV_DEV_BAD_PAGE
+
+
+# ---- outputs over inputs
+
+def test_commit_refuses_new_len_over_its_inputs():
+    kc = torch.zeros((4, 2, 8, 64), dtype=torch.bfloat16, device=dev())
+    words = i32([5, 9, 1, 0, 0, 0, 7])  # lengths, accepted counts, one more
+    pre, n, st = words[0:2], words[2:4], _status()
+    table, acc = i32([[0, 1], [2, 3]]), i32([[2, -1, -1, -1], [-1, -1, -1, -1]])
+    for new in (pre, n, words[1:3], words[3:5], acc[1, :2], acc[0, 2:], table[0]):
+        with pytest.raises(tv.TreeVerifyError, match="TV_ERR_VALUE"):
+            tv.commit_accepted_kv_paged(kc, kc.clone(), table, pre, acc, n, new_len=new, dev_status=st)
+    got = tv.commit_accepted_kv_paged(kc, kc.clone(), table, pre, acc, n, new_len=words[4:6], dev_status=st)
+    torch.cuda.synchronize()
+    assert host(got).tolist() == [7, 10] and int(st.item()) == 0

@@ -834,7 +834,8 @@ def commit_accepted_kv_paged(k_cache, v_cache, page_table, prefix_len, accepted_
     """commit_accepted_kv over paged caches [num_pages][Hkv][page_size][D], in place: rows
     prefix_len[b] + a_k move to prefix_len[b] + k.  accepted_nodes [B][N], accept_len [B] as
     returned by verify_greedy / verify_sample.  Returns new_len [B] int32, the sequences'
-    committed rows after the round (prefix_len + accept_len + 1)."""
+    committed rows after the round (prefix_len + accept_len + 1): storage of its own, none of
+    the call's other tensors."""
     index = _device_index("k_cache", k_cache)
     kv, B, Hkv, _, _, D = _paged_kv(k_cache, v_cache, page_table, prefix_len, index)
     if accepted_nodes.ndim != 2:

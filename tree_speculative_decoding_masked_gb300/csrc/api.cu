@@ -383,6 +383,11 @@ tv_status tv_rotary(const tv_rows* x, void* out, const int32_t* pos, const int32
   return cuda_status(launch_rotary(a, dtype, st(stream)));
 }
 
+static bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + b_bytes && y < x + a_bytes;
+}
+
 static int log2_exact(int x) {
   int s = 0;
   while ((1 << s) < x) ++s;
@@ -487,7 +492,11 @@ tv_status tv_commit_accepted_kv_paged(const tv_paged_kv* kv, const int32_t* acce
   const tv_status s = paged_checks(kv, B, Hkv, N, D, dtype);
   if (s != TV_OK) return s;
   if (N > kMaxNodes || B > 65535) return TV_ERR_SHAPE;
-  if (new_len == kv->prefix_len) return TV_ERR_VALUE;
+  // a sequence's CTAs read these while its first one writes new_len
+  const size_t b4 = (size_t)B * 4;
+  if (new_len && (overlap(new_len, b4, kv->prefix_len, b4) || overlap(new_len, b4, accept_len, b4) ||
+                  overlap(new_len, b4, accepted_nodes, b4 * N) || overlap(new_len, b4, kv->page_table, b4 * kv->max_pages)))
+    return TV_ERR_VALUE;
   return cuda_status(launch_kv_commit_paged(kv->k, kv->v, kv->page_table, kv->prefix_len, accepted_nodes, accept_len,
                                             new_len, B, Hkv, D, N, kv->num_pages, log2_exact(kv->page_size),
                                             kv->max_pages, dtype, dev_status, st(stream)));
