@@ -614,8 +614,8 @@ TV_API tv_status tv_append_kv_paged(const tv_rows* k, const tv_rows* v, const tv
  *   over the committed rows j < P_b and the new rows P_b + t with t <= i (parent NULL: a
  *   causal chunk) or t in pi(i) (a tree); with window > 0 only those at most window - 1
  *   positions before row i, a tree node's position being P_b + its depth.
- *   q, out  [B][Hq][N][D] dtype, contiguous, not the same array (a row's queries may be read after
- *           another part of its keys is done); the new rows' keys and values are in the cache
+ *   q, out  [B][Hq][N][D] dtype, contiguous, without a common byte (a row's queries may be read
+ *           after another part of its keys is done); the new rows' keys and values are in the cache
  *   parent  [B][N] int32 (tree layout above) or NULL
  *   scale   > 0, or 0 for 1/sqrt(D);  softcap, window: 0 = none
  * The keys and values of active rows and of committed rows within the window must be
@@ -626,7 +626,7 @@ TV_API tv_status tv_append_kv_paged(const tv_rows* k, const tv_rows* v, const tv
  * Workspace: tv_paged_attention_workspace_size(...) bytes, 16-byte aligned, zero-filled
  * once; calls that share it must not overlap on the GPU.
  * Errors: as tv_tree_attention; scale, softcap < 0 or not finite, scale / softcap beyond fp32,
- * window < 0, out == q -> TV_ERR_VALUE; workspace missing or small -> TV_ERR_WORKSPACE.
+ * window < 0, out over q -> TV_ERR_VALUE; workspace missing or small -> TV_ERR_WORKSPACE.
  */
 TV_API size_t tv_paged_attention_workspace_size(int B, int Hq, int Hkv, int D, int N, int page_size,
                                                 int max_pages, tv_dtype dtype);

@@ -18,3 +18,12 @@ def test_new_len_may_not_lie_over_what_the_commit_reads(lib):  # noqa: F811
     for name, start in at.items():
         for new in (start, start + 4, start - 4, start - 4 * B + 4, start + size[name] - 4):
             assert call(new) == -8, (name, hex(new))
+
+
+def test_attentions_output_may_not_lie_over_its_queries(lib):  # noqa: F811
+    B, Hq, N, D = 2, 4, 3, 64
+    q = 0x100000
+    for dt, size in ((0, 4 * B * Hq * N * D), (1, 2 * B * Hq * N * D)):
+        for out in (q, q + 16, q - 16, q + size - 16, q - size + 16):
+            assert lib.tv_paged_attention(ctypes.c_void_p(q), ctypes.c_void_p(out), _kv(), NULL, NULL, B, Hq, 2, N, D, 0.0,
+                                          0.0, 0, dt, ctypes.c_void_p(0x200000), 1 << 40, NULL, NULL) == -8

@@ -210,3 +210,17 @@ def test_commit_refuses_new_len_over_its_inputs():
     got = tv.commit_accepted_kv_paged(kc, kc.clone(), table, pre, acc, n, new_len=words[4:6], dev_status=st)
     torch.cuda.synchronize()
     assert host(got).tolist() == [7, 10] and int(st.item()) == 0
+
+
+def test_attention_refuses_an_output_over_its_queries():
+    B, Hq, N, D = 2, 4, 3, 64
+    count = B * Hq * N * D
+    room = torch.zeros(2 * count, dtype=torch.bfloat16, device=dev())
+    kc = torch.ones((4, 2, 8, D), dtype=torch.bfloat16, device=dev())
+    args = (kc, kc.clone(), i32([[0, 1], [2, 3]]), i32([5, 9]))
+    q = room[:count].view(B, Hq, N, D)
+    for at in (0, 8, count - 8):
+        with pytest.raises(tv.TreeVerifyError, match="TV_ERR_VALUE"):
+            tv.paged_attention(q, *args, out=room[at:at + count].view(B, Hq, N, D))
+    got = tv.paged_attention(q, *args, out=room[count:].view(B, Hq, N, D))  # side by side
+    assert bool((got == 1.0).all()) and not room[:count].any()

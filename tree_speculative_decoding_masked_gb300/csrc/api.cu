@@ -471,7 +471,8 @@ tv_status tv_paged_attention(const void* q, void* out, const tv_paged_kv* kv, co
   const size_t need = paged_attn_ws(B, Hq, Hkv, D, N, dtype);
   if (need && (!workspace || ws_bytes < need)) return TV_ERR_WORKSPACE;
   if (!aligned16(workspace)) return TV_ERR_ALIGN;
-  if (q == out) return TV_ERR_VALUE;
+  const size_t rows_bytes = (size_t)B * Hq * N * D * (dtype == TV_BF16 ? 2 : 4);
+  if (overlap(q, rows_bytes, out, rows_bytes)) return TV_ERR_VALUE;
   PagedAttn a{};
   a.q = q, a.out = out, a.k = kv->k, a.v = kv->v;
   a.table = kv->page_table, a.prefix_len = kv->prefix_len, a.parent = parent, a.n_rows = n_rows;
