@@ -132,10 +132,11 @@ TV_API tv_status tv_philox4x32_10(uint64_t seed, const uint32_t* counters, int n
 TV_API tv_status tv_selftest_bounded_wait(int wait_us, int32_t* dev_status, tv_stream_t stream);
 
 /* ------------------------------------------------------------------------------------
- * tv_set_sm_partition - SM shares for running tv_tree_attention and tv_verify_* at the
- * same time on two streams.  The vocab pass then launches at most verify_sms CTAs (one
+ * tv_set_sm_partition - SM shares for running tree or paged attention and tv_verify_* at
+ * the same time on two streams.  The vocab pass then launches at most verify_sms CTAs (one
  * per SM) and the tensor-core attention plans its KV splits for attention_sms SMs, so
  * that the two grids can be resident together instead of queueing behind each other.
+ * tv_paged_attention launches no more CTAs than fit on attention_sms SMs.
  * 0 (the default) means the whole device.  Process-wide, host-side; affects launches
  * made after the call.  Results do not depend on it beyond fp32 summation order.
  * Errors: a negative count -> TV_ERR_VALUE.
@@ -624,7 +625,7 @@ TV_API tv_status tv_append_kv_paged(const tv_rows* k, const tv_rows* v, const tv
  * softcap <= 256, by 2^-13.  Limits: 32 <= D <= 256, D % 32 == 0, Hq % Hkv == 0,
  * 1 <= N <= 65536 (trees 1024), G * N < 2^24.  q, out and the caches 16-byte aligned.
  * Workspace: tv_paged_attention_workspace_size(...) bytes, 16-byte aligned, zero-filled
- * once; calls that share it must not overlap on the GPU.
+ * once, enough under any tv_set_sm_partition; calls that share it must not overlap on the GPU.
  * Errors: as tv_tree_attention; scale, softcap < 0 or not finite, scale / softcap beyond fp32,
  * window < 0, out over q -> TV_ERR_VALUE; workspace missing or small -> TV_ERR_WORKSPACE.
  */

@@ -1,4 +1,6 @@
 """GPU tests of what the header promises for calls over pages beside their results."""
+import ctypes
+
 import numpy as np
 import pytest
 
@@ -224,3 +226,49 @@ def test_attention_refuses_an_output_over_its_queries():
             tv.paged_attention(q, *args, out=room[at:at + count].view(B, Hq, N, D))
     got = tv.paged_attention(q, *args, out=room[count:].view(B, Hq, N, D))  # side by side
     assert bool((got == 1.0).all()) and not room[:count].any()
+
+
+# ---- a share of the device
+
+def _grids(call):
+    """CTAs of each kernel that a call launches, asked of the driver."""
+    graph = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(graph):
+        call()
+    cuda = ctypes.CDLL("libcuda.so.1")
+    raw, count = ctypes.c_void_p(graph.raw_cuda_graph()), ctypes.c_size_t(0)
+    assert cuda.cuGraphGetNodes(raw, None, ctypes.byref(count)) == 0
+    nodes = (ctypes.c_void_p * count.value)()
+    assert cuda.cuGraphGetNodes(raw, nodes, ctypes.byref(count)) == 0
+    out = []
+    for node in nodes:
+        kind, params = ctypes.c_int(-1), (ctypes.c_uint32 * 64)()
+        assert cuda.cuGraphNodeGetType(ctypes.c_void_p(node), ctypes.byref(kind)) == 0
+        if kind.value == 0:  # a kernel: function, grid, block, ...
+            assert cuda.cuGraphKernelNodeGetParams_v2(ctypes.c_void_p(node), params) == 0
+            out.append(params[2] * params[3] * params[4])
+    return out
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("B,Hq,Hkv,D,N", [(1, 8, 2, 128, 1), (1, 32, 8, 64, 60), (4, 16, 8, 64, 1), (2, 16, 8, 128, 100),
+                                          (1, 2, 1, 256, 90), (4, 32, 16, 96, 2), (1, 64, 8, 64, 5), (3, 40, 20, 32, 33)])
+def test_few_units_keep_to_the_share(B, Hq, Hkv, D, N, bf16):
+    # units that run as clusters on the whole device: fewer parts, or the persistent grid; one workspace for all
+    g = synth.rng(4600 + D + N)
+    dt = torch.bfloat16 if bf16 else torch.float32
+    prefix = [700 - 111 * b for b in range(B)]
+    ws = torch.zeros(tv.paged_attention_workspace_size(B, Hq, Hkv, D, N, 16, 60, dt) + 16, dtype=torch.uint8, device=dev())
+    ws[-16:] = 77
+    x = [torch.randn(s, device=dev()).to(dt) for s in ((B, Hq, N, D), (60, Hkv, 16, D), (60, Hkv, 16, D))]
+    out, st, pre = torch.zeros_like(x[0]), _status(), i32(prefix)
+    table = i32(np.stack([np.arange(60) for _ in range(B)]))
+    try:
+        for share in (0, 1, 7, 17, 40, 77, 120, 0):
+            tv.set_sm_partition(0, share)
+            _attend_check(g, B, Hq, Hkv, D, 16, prefix, N, bf16=bf16, workspace=ws[:-16])
+            ctas = _grids(lambda: tv.paged_attention(*x, table, pre, out=out, workspace=ws[:-16], dev_status=st))
+            assert len(ctas) == 1 and ctas[0] <= (share or 152) * (1 if bf16 else 2), (share, ctas)
+            assert bool((ws[-16:] == 77).all())
+    finally:
+        tv.set_sm_partition(0, 0)

@@ -452,7 +452,7 @@ static bool paged_attn_shape(int B, int Hq, int Hkv, int N, int D) {
 size_t tv_paged_attention_workspace_size(int B, int Hq, int Hkv, int D, int N, int page_size, int max_pages,
                                          tv_dtype dtype) {
   if (!paged_attn_shape(B, Hq, Hkv, N, D) || page_size < 8 || max_pages < 1 || !valid_dtype(dtype)) return 0;
-  return paged_attn_ws(B, Hq, Hkv, D, N, dtype);
+  return paged_attn_ws(B, Hq, Hkv, D, N, dtype, paged_grid_sms()).bytes;
 }
 
 tv_status tv_paged_attention(const void* q, void* out, const tv_paged_kv* kv, const int32_t* parent,
@@ -468,7 +468,8 @@ tv_status tv_paged_attention(const void* q, void* out, const tv_paged_kv* kv, co
   if (scale == 0.f) scale = 1.f / sqrtf((float)D);
   if (softcap > 0.f && isinf(4.f * scale / softcap)) return TV_ERR_VALUE;
   if (!aligned16(q) || !aligned16(out)) return TV_ERR_ALIGN;
-  const size_t need = paged_attn_ws(B, Hq, Hkv, D, N, dtype);
+  const int sms = paged_grid_sms();  // read once: the schedule and its workspace go by it
+  const size_t need = paged_attn_ws(B, Hq, Hkv, D, N, dtype, sms).need;
   if (need && (!workspace || ws_bytes < need)) return TV_ERR_WORKSPACE;
   if (!aligned16(workspace)) return TV_ERR_ALIGN;
   const size_t rows_bytes = (size_t)B * Hq * N * D * (dtype == TV_BF16 ? 2 : 4);
@@ -481,6 +482,7 @@ tv_status tv_paged_attention(const void* q, void* out, const tv_paged_kv* kv, co
   a.scale = scale;
   a.cap = softcap;
   a.window = window;
+  a.sms = sms;
   a.dev_status = dev_status;
   return cuda_status(launch_paged_attn(a, dtype, reinterpret_cast<char*>(workspace), st(stream)));
 }

@@ -363,15 +363,14 @@ constexpr size_t kPagedCntBytes = kPagedMaxCtas * kPagedMaxSms * 4;
 constexpr int kPagedFewRows = 16;  // query rows of a KV head above which row tiles are used
 
 int paged_device_sms();
-int paged_grid_sms();  // less where tv_set_sm_partition says so
 bool paged_tc_takes(int Hq, int Hkv, int D, int N);
-size_t paged_tc_ws(int B, int Hq, int Hkv, int D, int N);
+PagedWs paged_tc_ws(int B, int Hq, int Hkv, int D, int N);
 cudaError_t launch_paged_tc(PagedAttn a, char* ws, cudaStream_t stream);
-size_t paged_mma_ws(int B, int Hq, int Hkv, int D, int N);
+PagedWs paged_mma_ws(int B, int Hq, int Hkv, int D, int N, int sms);
 cudaError_t launch_paged_mma(PagedAttn a, char* ws, cudaStream_t stream);
-size_t paged_f32_ws(int B, int Hq, int Hkv, int D, int N);
+PagedWs paged_f32_ws(int B, int Hq, int Hkv, int D, int N);
 cudaError_t launch_paged_f32(PagedAttn a, char* ws, cudaStream_t stream);
-size_t paged_simt_ws(int D);
+PagedWs paged_simt_ws(int D);
 cudaError_t launch_paged_simt(PagedAttn a, char* ws, cudaStream_t stream);
 // Tensor map of bf16 pages, 128-byte swizzle.  D = 128 and 256: 5-D, a box spans all column
 // blocks and min(page_size, 64) rows, as 8-row groups [block][8][128 bytes].  Other D: 3-D boxes

@@ -34,9 +34,9 @@ int paged_grid_sms() {
 
 static bool f32_tiles(int Hq, int Hkv, int N) { return (long long)(Hq / Hkv) * N > kPagedFewRows; }
 
-size_t paged_attn_ws(int B, int Hq, int Hkv, int D, int N, tv_dtype dtype) {
+PagedWs paged_attn_ws(int B, int Hq, int Hkv, int D, int N, tv_dtype dtype, int sms) {
   if (dtype == TV_F32) return f32_tiles(Hq, Hkv, N) ? paged_f32_ws(B, Hq, Hkv, D, N) : paged_simt_ws(D);
-  return paged_tc_takes(Hq, Hkv, D, N) ? paged_tc_ws(B, Hq, Hkv, D, N) : paged_mma_ws(B, Hq, Hkv, D, N);
+  return paged_tc_takes(Hq, Hkv, D, N) ? paged_tc_ws(B, Hq, Hkv, D, N) : paged_mma_ws(B, Hq, Hkv, D, N, sms);
 }
 
 cudaError_t launch_paged_attn(PagedAttn a, tv_dtype dtype, char* ws, cudaStream_t stream) {

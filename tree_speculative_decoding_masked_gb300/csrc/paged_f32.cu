@@ -392,23 +392,33 @@ __global__ void __launch_bounds__(kPfThreads, kD <= 64 ? 2 : 1)
 // ---- host side
 
 struct PfPlan {
-  int row_tiles, splits;  // splits 0: persistent grid
-  size_t rows, bytes;     // workspace: partial rows
+  int row_tiles, splits, grid;  // splits 0: persistent grid
+  size_t rows, bytes;           // workspace: partial rows
 };
 
-static PfPlan pf_plan(int B, int Hq, int Hkv, int D, int N) {
+static PfPlan pf_plan(int B, int Hq, int Hkv, int D, int N, int sms) {
   PfPlan p{};
   p.row_tiles = (Hq / Hkv * N + kPfRows - 1) / kPfRows;
   const long long units = (long long)B * Hkv * p.row_tiles;
-  const int ctas = paged_device_sms() * (D <= 64 ? 2 : 1);
-  if (units * 2 <= ctas && B <= 65535 && units / B <= 65535)
-    p.splits = (int)min((long long)kPfMaxSplits, ctas / units);
-  p.rows = (p.splits ? (size_t)p.splits * units : (size_t)2 * kPagedMaxCtas * kPagedMaxSms) * kPfRows;
+  auto parts = [&](int n) -> int {
+    const int ctas = n * (D <= 64 ? 2 : 1);
+    return units * 2 <= ctas && B <= 65535 && units / B <= 65535 ? (int)min((long long)kPfMaxSplits, ctas / units) : 0;
+  };
+  // the workspace goes by the whole device: a share's clusters have fewer parts, and its
+  // persistent grid takes two slots a CTA of what there is
+  const int whole = parts(paged_device_sms());
+  const size_t slots = whole ? (size_t)whole * units : (size_t)2 * kPagedMaxCtas * kPagedMaxSms;
+  p.splits = parts(sms);
+  p.grid = (int)min((size_t)sms * (D <= 64 ? 2 : 1), slots / 2);
+  p.rows = slots * kPfRows;
   p.bytes = kPagedCntBytes + p.rows * 8 + p.rows * D * 4;
   return p;
 }
 
-size_t paged_f32_ws(int B, int Hq, int Hkv, int D, int N) { return pf_plan(B, Hq, Hkv, D, N).bytes; }
+PagedWs paged_f32_ws(int B, int Hq, int Hkv, int D, int N) {
+  const size_t n = pf_plan(B, Hq, Hkv, D, N, paged_device_sms()).bytes;
+  return {n, n};
+}
 
 template <int kD, bool kStream>
 static cudaError_t launch_pf_s(PagedAttn a, const PfPlan& p, cudaStream_t stream) {
@@ -416,7 +426,7 @@ static cudaError_t launch_pf_s(PagedAttn a, const PfPlan& p, cudaStream_t stream
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, PfSmem<kD>::kBytes);
   if (e != cudaSuccess) return e;
   if (kStream)
-    return launch_pdl(fn, dim3((unsigned)(paged_grid_sms() * (kD <= 64 ? 2 : 1))), dim3(kPfThreads), PfSmem<kD>::kBytes,
+    return launch_pdl(fn, dim3((unsigned)p.grid), dim3(kPfThreads), PfSmem<kD>::kBytes,
                       stream, nullptr, 0, a, 0, p.row_tiles);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -429,7 +439,7 @@ static cudaError_t launch_pf_s(PagedAttn a, const PfPlan& p, cudaStream_t stream
 
 template <int kD>
 static cudaError_t launch_pf(PagedAttn a, char* ws, cudaStream_t stream) {
-  const PfPlan p = pf_plan(a.B, a.Hq, a.Hkv, a.D, a.N);
+  const PfPlan p = pf_plan(a.B, a.Hq, a.Hkv, a.D, a.N, a.sms);
   a.cnt = reinterpret_cast<unsigned*>(ws);
   a.ws_ml = reinterpret_cast<float2*>(ws + kPagedCntBytes);
   a.ws_o = reinterpret_cast<float*>(ws + kPagedCntBytes + p.rows * 8);

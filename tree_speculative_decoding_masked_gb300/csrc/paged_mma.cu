@@ -666,26 +666,28 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT>::kThreads, 1)
 
 struct PmPlan {
   int RT, row_tiles, splits;  // splits 0: persistent grid
-  size_t rows, bytes;     // workspace
+  size_t rows, bytes;         // workspace of the persistent grid; clusters use none
 };
 
-static PmPlan pm_plan(int B, int Hq, int Hkv, int D, int N) {
+static PmPlan pm_plan(int B, int Hq, int Hkv, int D, int N, int sms) {
   PmPlan p{};
   const int R = Hq / Hkv * N;
   p.RT = R <= 8 ? 8 : R <= 16 || D > 128 ? 16 : 32;  // O of 32 rows x 256 columns would not fit in registers
   p.row_tiles = (R + p.RT - 1) / p.RT;
-  const int sms = paged_device_sms();
   const long long units = (long long)B * Hkv * p.row_tiles;
-  if (units * 2 <= sms && B <= 65535 && units / B <= 65535)
-    p.splits = (int)min((long long)kPmMaxSplits, sms / units);
-  if (p.splits == 0) {
-    p.rows = (size_t)2 * kPagedMaxSms * p.RT;
-    p.bytes = kPagedCntBytes + p.rows * 8 + p.rows * D * 4;
-  }
+  const bool few = units * 2 <= paged_device_sms() && B <= 65535 && units / B <= 65535;
+  // units that run as clusters on the whole device do so on a share too, in fewer parts, unless the share
+  // has fewer SMs than units: then its persistent grid has two slots a CTA, fewer than two a unit
+  if (few) p.splits = (int)min((long long)kPmMaxSplits, sms / units);
+  p.rows = 2 * (few ? (size_t)units : (size_t)kPagedMaxSms) * p.RT;
+  p.bytes = kPagedCntBytes + p.rows * 8 + p.rows * D * 4;
   return p;
 }
 
-size_t paged_mma_ws(int B, int Hq, int Hkv, int D, int N) { return pm_plan(B, Hq, Hkv, D, N).bytes; }
+PagedWs paged_mma_ws(int B, int Hq, int Hkv, int D, int N, int sms) {
+  const PmPlan p = pm_plan(B, Hq, Hkv, D, N, sms);
+  return {p.bytes, p.splits ? 0 : p.bytes};
+}
 
 template <int kD, int kRT, int kCap, bool kStream>
 static cudaError_t launch_pm(const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a, const PmPlan& p,
@@ -696,7 +698,7 @@ static cudaError_t launch_pm(const CUtensorMap& mk, const CUtensorMap& mv, const
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   if (kStream)
-    return launch_pdl(fn, dim3((unsigned)paged_grid_sms()), dim3(C::kThreads), C::kSmem, stream, nullptr, 0,
+    return launch_pdl(fn, dim3((unsigned)a.sms), dim3(C::kThreads), C::kSmem, stream, nullptr, 0,
                       mk, mv, a, 0, p.row_tiles, wide);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -737,7 +739,7 @@ static cudaError_t launch_pm_d(const CUtensorMap& mk, const CUtensorMap& mv, con
 }
 
 cudaError_t launch_paged_mma(PagedAttn a, char* ws, cudaStream_t stream) {
-  const PmPlan p = pm_plan(a.B, a.Hq, a.Hkv, a.D, a.N);
+  const PmPlan p = pm_plan(a.B, a.Hq, a.Hkv, a.D, a.N, a.sms);
   if (!p.splits) {
     a.cnt = reinterpret_cast<unsigned*>(ws);
     a.ws_ml = reinterpret_cast<float2*>(ws + kPagedCntBytes);

@@ -567,7 +567,10 @@ __global__ void __launch_bounds__(kPsWarps * 32, 1) paged_rows_kernel(PagedAttn 
 // counters, (m, l) and O of two partial units per CTA of the largest grid
 constexpr size_t kPsRows = (size_t)2 * kPagedMaxCtas * kPagedMaxSms * kPsWarps * 2;
 
-size_t paged_simt_ws(int D) { return kPagedCntBytes + kPsRows * 8 + kPsRows * D * 4; }
+PagedWs paged_simt_ws(int D) {
+  const size_t n = kPagedCntBytes + kPsRows * 8 + kPsRows * D * 4;
+  return {n, n};
+}
 
 template <int kDPL, int kRPW>
 static cudaError_t launch_ps(PagedAttn a, char* ws, cudaStream_t stream) {
@@ -578,7 +581,7 @@ static cudaError_t launch_ps(PagedAttn a, char* ws, cudaStream_t stream) {
   a.cnt = reinterpret_cast<unsigned*>(ws);
   a.ws_ml = reinterpret_cast<float2*>(ws + kPagedCntBytes);
   a.ws_o = reinterpret_cast<float*>(ws + kPagedCntBytes + kPsRows * 8);
-  return launch_pdl(paged_simt_kernel<kDPL, kRPW>, dim3((unsigned)(paged_grid_sms() * kPagedMaxCtas)),
+  return launch_pdl(paged_simt_kernel<kDPL, kRPW>, dim3((unsigned)(a.sms * kPagedMaxCtas)),
                     dim3(kPsWarps * 32), S::kBytes, stream, nullptr, 0, a);
 }
 
@@ -591,7 +594,7 @@ static cudaError_t launch_pr(PagedAttn a, char* ws, cudaStream_t stream) {
   a.cnt = reinterpret_cast<unsigned*>(ws);
   a.ws_ml = reinterpret_cast<float2*>(ws + kPagedCntBytes);
   a.ws_o = reinterpret_cast<float*>(ws + kPagedCntBytes + kPsRows * 8);
-  return launch_pdl(paged_rows_kernel<kDPL, kR>, dim3((unsigned)paged_grid_sms()), dim3(kPsWarps * 32), S::kBytes,
+  return launch_pdl(paged_rows_kernel<kDPL, kR>, dim3((unsigned)a.sms), dim3(kPsWarps * 32), S::kBytes,
                     stream, nullptr, 0, a);
 }
 

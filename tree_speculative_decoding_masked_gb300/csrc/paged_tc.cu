@@ -932,7 +932,7 @@ bool paged_kv_tmap(CUtensorMap* m, const void* base, const PagedAttn& a) {
 }
 
 struct PtPlan {
-  int NT, tiles, MP, splits;  // splits 0: persistent grid
+  int NT, tiles, MP, splits, grid;  // splits 0: persistent grid
   size_t slots, bytes;        // workspace: partial results
 };
 
@@ -964,26 +964,37 @@ static int pt_clusters(int D, int s) {
   return n;
 }
 
-static PtPlan pt_plan(int B, int Hq, int Hkv, int D, int N) {
+static PtPlan pt_plan(int B, int Hq, int Hkv, int D, int N, int share) {
   PtPlan p{};
   const int G = Hq / Hkv;
   p.NT = (kPtRows / G) / 8 * 8;
   const int sms = paged_device_sms(), row_tiles = (N + p.NT - 1) / p.NT;
-  // the most parts that leave all units resident at once: of single tiles, of pairs
-  auto parts = [&](int tiles) -> int {
+  // the most parts that leave all units resident on `on` SMs at once: of single tiles, of pairs
+  auto parts = [&](int tiles, int on) -> int {
     const long long units = (long long)B * Hkv * ((row_tiles + tiles - 1) / tiles);
-    if (units * 2 > sms || B > 65535 || Hkv > 65535) return 0;
+    if (units * 2 > on || B > 65535 || Hkv > 65535) return 0;
     for (int s = kPtMaxSplits; s >= 2; --s)
-      if (units <= pt_clusters(D, s)) return s;
+      if (units * s <= on && units <= pt_clusters(D, s)) return s;
     return 0;
   };
-  const int one = parts(1), two = parts(2);
+  const int one = parts(1, sms), two = parts(2, sms);
   // a 64-key step takes 1.0 us for a pair and 0.8 for a single tile, whose merge is 2 us shorter
   p.tiles = one >= 2 && one * 4 >= two * 3 ? 1 : 2;
   p.splits = p.tiles == 1 ? one : two;
   p.MP = (row_tiles + p.tiles - 1) / p.tiles;
   // one part per CTA of the clusters, two per CTA of the persistent grid
   p.slots = p.splits ? (size_t)p.splits * p.MP * B * Hkv : (size_t)2 * kPagedMaxSms;
+  if (p.splits && share < sms) {
+    // on a share: fewer parts of the same units, else of pairs, else the persistent grid.  The workspace stays
+    // the whole device's, which holds them: pairs have parts <= share < 2 units of single tiles
+    p.splits = parts(p.tiles, share);
+    if (!p.splits) {
+      p.tiles = 2;
+      p.splits = parts(2, share);
+      p.MP = (row_tiles + 1) / 2;
+    }
+  }
+  p.grid = (int)min((size_t)share, p.slots / 2);
   p.bytes = kPagedCntBytes + p.slots * 2 * kPtRows * (8 + (D <= 64 ? 64 : 128) * 4);
   return p;
 }
@@ -993,7 +1004,10 @@ bool paged_tc_takes(int Hq, int Hkv, int D, int N) {
   return D <= 128 && G <= 16 && (long long)G * N > kPagedFewRows;
 }
 
-size_t paged_tc_ws(int B, int Hq, int Hkv, int D, int N) { return pt_plan(B, Hq, Hkv, D, N).bytes; }
+PagedWs paged_tc_ws(int B, int Hq, int Hkv, int D, int N) {
+  const size_t n = pt_plan(B, Hq, Hkv, D, N, paged_device_sms()).bytes;
+  return {n, n};
+}
 
 template <int D, int kCap, bool kStream>
 static cudaError_t launch_pt(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a,
@@ -1004,7 +1018,7 @@ static cudaError_t launch_pt(const CUtensorMap& mq, const CUtensorMap& mk, const
   if (e != cudaSuccess) return e;
   const PtArgs pa{p.NT, p.tiles, p.MP, p.splits, a.D == 128};
   if (kStream)
-    return launch_pdl(paged_tc_kernel<D, kCap, kStream>, dim3((unsigned)paged_grid_sms()), dim3(kPtThreads), smem, stream,
+    return launch_pdl(paged_tc_kernel<D, kCap, kStream>, dim3((unsigned)p.grid), dim3(kPtThreads), smem, stream,
                       nullptr, 0, mq, mk, mv, a, pa);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1035,7 +1049,7 @@ static cudaError_t launch_pt_d(const CUtensorMap& mq, const CUtensorMap& mk, con
 }
 
 cudaError_t launch_paged_tc(PagedAttn a, char* ws, cudaStream_t stream) {
-  const PtPlan p = pt_plan(a.B, a.Hq, a.Hkv, a.D, a.N);
+  const PtPlan p = pt_plan(a.B, a.Hq, a.Hkv, a.D, a.N, a.sms);
   a.cnt = reinterpret_cast<unsigned*>(ws);
   a.ws_ml = reinterpret_cast<float2*>(ws + kPagedCntBytes);
   a.ws_o = reinterpret_cast<float*>(ws + kPagedCntBytes + p.slots * 2 * kPtRows * 8);

@@ -109,12 +109,18 @@ struct PagedAttn {
   int B, Hq, Hkv, G, D, N, num_pages, page_shift, max_pages;
   float scale, cap;  // cap 0: scores are not capped
   int window;        // 0: no window
+  int sms;           // SMs that the call may take (host)
   float* ws_o;       // partial results of units shared by CTAs
   float2* ws_ml;
   unsigned* cnt;
   int32_t* dev_status;
 };
-size_t paged_attn_ws(int B, int Hq, int Hkv, int D, int N, tv_dtype dtype);
+// Workspace bytes of a call on any share of the device, and of one on `sms` SMs.
+struct PagedWs {
+  size_t bytes, need;
+};
+PagedWs paged_attn_ws(int B, int Hq, int Hkv, int D, int N, tv_dtype dtype, int sms);
+int paged_grid_sms();  // SMs that tv_set_sm_partition leaves paged attention
 cudaError_t launch_paged_attn(PagedAttn a, tv_dtype dtype, char* ws, cudaStream_t stream);
 
 // ---- rotary positions and the paged append (Hq rows of q rotated into q_out, Hkv rows of k
