@@ -4,6 +4,7 @@ import ctypes
 import numpy as np
 import pytest
 
+import paged_precision
 import synth
 from oracle import paged, rotary
 from test_gpu_paged import _attend_check, _pages, _status, _unit
@@ -272,3 +273,17 @@ def test_few_units_keep_to_the_share(B, Hq, Hkv, D, N, bf16):
             assert bool((ws[-16:] == 77).all())
     finally:
         tv.set_sm_partition(0, 0)
+
+
+# ---- fp32 stays fp32
+
+@pytest.mark.parametrize("case", paged_precision.CASES, ids=str)
+def test_fp32_attention_is_off_by_fp32_roundings_only(case):
+    data = paged_precision.inputs(case)
+    q, kc, vc, table, par = data
+    st = _status()
+    got = tv.paged_attention(to_dev(q, False), to_dev(kc, False), to_dev(vc, False), i32(table), i32(case[5]),
+                             parent=None if par is None else i32(par), softcap=case[8], window=case[9], dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    assert paged_precision.worst(case, data, host(got).astype(np.float64), paged_precision.reference(case, data)) <= 1.0
