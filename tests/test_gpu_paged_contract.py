@@ -287,3 +287,16 @@ def test_fp32_attention_is_off_by_fp32_roundings_only(case):
     torch.cuda.synchronize()
     assert int(st.item()) == 0
     assert paged_precision.worst(case, data, host(got).astype(np.float64), paged_precision.reference(case, data)) <= 1.0
+
+
+# ---- windows as wide as an int
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("window", [(1 << 31) - 1, (1 << 31) - 200])
+@pytest.mark.parametrize("N,tree_", [(1, False), (6, True), (80, False), (80, True), (300, False)])
+def test_a_window_of_any_size(N, tree_, window, bf16):
+    g = synth.rng(4700 + N)
+    par = np.stack([synth.random_parents(synth.rng(b), N, 8) for b in range(2)]).astype(np.int32) if tree_ else None
+    wide = _attend_check(g, 2, 8, 2, 128, 16, [260, 33], N, parent=par, bf16=bf16, window=window)
+    g = synth.rng(4700 + N)
+    assert np.array_equal(wide, _attend_check(g, 2, 8, 2, 128, 16, [260, 33], N, parent=par, bf16=bf16))

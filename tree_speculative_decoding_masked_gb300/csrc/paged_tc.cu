@@ -612,7 +612,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         } else {
           whi = P + node + 1;
         }
-        if (a.window > 0) wlo = P + depth - a.window + 1;
+        if (a.window > 0) wlo = max(0, P + depth - a.window + 1);  // at least 0: wlo - j0 fits an int
       }
       const float c = kCap == kLargeCap ? kLog2e : kCap ? a.cap * kLog2e : a.scale * kLog2e;
       const float ck = kCap == kLargeCap ? 1.f / a.cap : kCap ? 2.f * kLog2e * a.scale / a.cap : 0.f;
