@@ -300,3 +300,31 @@ def test_a_window_of_any_size(N, tree_, window, bf16):
     wide = _attend_check(g, 2, 8, 2, 128, 16, [260, 33], N, parent=par, bf16=bf16, window=window)
     g = synth.rng(4700 + N)
     assert np.array_equal(wide, _attend_check(g, 2, 8, 2, 128, 16, [260, 33], N, parent=par, bf16=bf16))
+
+
+# ---- idle sequences
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("Hkv,N", [(2, 1), (2, 6), (2, 70), (60, 1), (60, 6), (60, 50)])
+def test_a_sequence_without_rows_may_have_any_length(Hkv, N, bf16):
+    # nothing of it is looked at; a negative length is reported all the same
+    g = synth.rng(4800 + N)
+    B, D, ps, prefix = 4, 64, 16, [30, 5, 77, 0]
+    kc, vc, table = _pages(g, B, Hkv, D, ps, [p + N for p in prefix], 77 + N, bf16)
+    q = to_dev(synth.normal(g, (B, 2 * Hkv, N, D), 1.0, bf16), bf16)
+    args = (q, to_dev(kc, bf16), to_dev(vc, bf16), i32(table))
+    rows = i32([N, 0, N, N])
+    want = torch.full_like(q, 7.0)
+    tv.paged_attention(*args, i32(prefix), n_rows=rows, out=want)
+    for idle in (0, table.shape[1] * ps, table.shape[1] * ps + 1, 1 << 30, (1 << 31) - 1, -1):
+        prefix[1] = idle
+        st, got, pool = _status(), torch.full_like(q, 7.0), [args[1].clone(), args[2].clone()]
+        tv.paged_attention(*args, i32(prefix), n_rows=rows, window=0, out=got, dev_status=st)
+        torch.cuda.synchronize()
+        assert int(st.item()) == (tv.TV_DEV_BAD_PAGE if idle < 0 else 0), idle
+        assert torch.equal(got, want)
+        st = _status()
+        k = q[:, ::2].clone()
+        tv.append_kv_paged(k, k, *pool, i32(table), i32(prefix), n_rows=rows, dev_status=st)
+        torch.cuda.synchronize()
+        assert int(st.item()) == (tv.TV_DEV_BAD_PAGE if idle < 0 else 0), idle

@@ -21,7 +21,7 @@ __device__ __forceinline__ int paged_rows(const PagedAttn& a, int b, int P, bool
   *bad = P < 0 || n < 0 || n > a.N;
   if (*bad) return 0;
   const long long room = ((long long)a.max_pages << a.page_shift) - P;
-  if (n <= room) return n;
+  if (n <= room || n == 0) return n;  // without rows any length will do
   *bad = !a.parent || room < 1 || a.parent[(size_t)b * a.N + room] != -1;
   return *bad ? 0 : (int)room;
 }
