@@ -356,6 +356,10 @@ __device__ __forceinline__ void soft_tanh4(float* s, float k) {
   s[0] = t0.x, s[1] = t0.y, s[2] = t1.x, s[3] = t1.y;
 }
 
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_addr(dst)), "l"(src) : "memory");
+}
+
 // ---- host side
 constexpr int kPagedMaxSms = 160;  // sizes the workspaces
 constexpr int kPagedMaxCtas = 2;   // CTAs per SM of the largest persistent grid

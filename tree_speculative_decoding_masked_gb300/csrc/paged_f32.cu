@@ -32,10 +32,6 @@ struct PfSmem {
   static constexpr int kBytes = (kOffP + kPfRows * kPStride) * 4;
 };
 
-__device__ __forceinline__ void pf_cp16(float* dst, const float* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_addr(dst)), "l"(src) : "memory");
-}
-
 template <int kD, bool kStream>
 __global__ void __launch_bounds__(kPfThreads, kD <= 64 ? 2 : 1)
     paged_f32_kernel(PagedAttn a, int splits, int row_tiles) {
@@ -102,291 +98,291 @@ __global__ void __launch_bounds__(kPfThreads, kD <= 64 ? 2 : 1)
       n_act = s_first_pad;
     }
     tree = b;
-        const int rows = unit_rows(a, n, rt, kPfRows), r0 = rt * kPfRows;
-        const int lo = unit_lo(a, P, rt, kPfRows), tile0 = lo / kPfKeys;
-        const int hi = min(P + n_act, P + (r0 + rows - 1) / a.G + 1);
-        // page of piece `threadIdx.x` of tile t, -1 where no row is needed
-        auto page_of = [&](int t) -> int {
-          const int j = (tile0 + t) * kPfKeys + ((int)threadIdx.x << min(a.page_shift, 6));
-          if ((int)threadIdx.x >= pages_tile || t >= t1 || j >= hi || j + (1 << min(a.page_shift, 6)) <= lo) return -1;
-          const int page = table[j >> a.page_shift];
-          if (page >= 0 && page < a.num_pages) return page;
-          set_dev_status(a.dev_status, TV_DEV_BAD_PAGE);
-          return -1;
-        };
-        // rows [lo, hi) of tile t; others (pages past the end, rows behind the window, whose contents
-        // may be anything) read as zero
-        auto load_tile = [&](int t, int buf) {
-          for (int e = threadIdx.x; e < kPfKeys * (kD / 4); e += kPfThreads) {
-            const int jj = e / (kD / 4), ch = e - jj * (kD / 4);
-            const int j = (tile0 + t) * kPfKeys + jj;
-            float* dk = s_k + (buf * kPfKeys + jj) * S::kStride + ch * 4;
-            float* dv = s_v + (buf * kPfKeys + jj) * kD + ch * 4;
-            const int page = j >= lo && j < hi ? s_page[t & 1][jj >> min(a.page_shift, 6)] : -1;
-            if (page >= 0) {
-              const size_t off =
-                  ((((size_t)page * a.Hkv + hk) << a.page_shift) + (j & ((1 << a.page_shift) - 1))) * kD + ch * 4;
-              pf_cp16(dk, reinterpret_cast<const float*>(a.k) + off);
-              pf_cp16(dv, reinterpret_cast<const float*>(a.v) + off);
-            } else {
-              *reinterpret_cast<float4*>(dk) = make_float4(0.f, 0.f, 0.f, 0.f);
-              *reinterpret_cast<float4*>(dv) = make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-          }
-          asm volatile("cp.async.commit_group;" ::: "memory");
-        };
-        __syncthreads();
-        // ---- rows: queries, bounds and the tree nodes each sees
-        if ((int)threadIdx.x < pages_tile) {
-          s_page[t0 & 1][threadIdx.x] = page_of(t0);
-          s_page[(t0 + 1) & 1][threadIdx.x] = page_of(t0 + 1);
-        }
-        for (int e = threadIdx.x; e < kPfRows * (kD / 4); e += kPfThreads) {
-          const int rr = e / (kD / 4), ch = e - rr * (kD / 4), i = (r0 + rr) / a.G, g = (r0 + rr) % a.G;
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (rr < rows && i < n_act) {
-            v = *reinterpret_cast<const float4*>(q + (((size_t)b * a.Hq + hk * a.G + g) * a.N + i) * kD + ch * 4);
-            v.x *= a.scale, v.y *= a.scale, v.z *= a.scale, v.w *= a.scale;
-          }
-          *reinterpret_cast<float4*>(s_q + rr * S::kStride + ch * 4) = v;
-        }
-        if (threadIdx.x < kPfRows) {
-          const int rr = threadIdx.x, i = (r0 + rr) / a.G;
-          int wlo = 0, whi = -1;  // what is no row sees nothing
-          if (rr < rows && i < n_act) {
-            int depth = i;
-            whi = a.parent ? P : P + i + 1;
-            if (a.parent) {
-              depth = -1;
-              for (int w = 0; w < (n + 31) / 32; ++w) s_vis[rr][w] = 0u;
-              for (int at = i; at >= 0; at = s_par[at]) {  // parents fall: it ends
-                ++depth;
-                if (a.window <= 0 || depth < a.window) s_vis[rr][at >> 5] |= 1u << (at & 31);
-              }
-            }
-            if (a.window > 0) wlo = P + depth - a.window + 1;
-          }
-          s_lo[rr] = wlo;
-          s_hi[rr] = whi;
-        }
-        __syncthreads();
-        float m[4], l[4], acc[4][kU][2];
-        int wlo[4], whi[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          m[x] = -INFINITY;
-          l[x] = 0.f;
-          wlo[x] = s_lo[ty * 4 + x];
-          whi[x] = s_hi[ty * 4 + x];
-#pragma unroll
-          for (int u = 0; u < kU; ++u) acc[x][u][0] = acc[x][u][1] = 0.f;
-        }
-        const bool live = (ty & ~1) * 4 < rows;  // some of this warp's eight rows are rows
-        load_tile(t0, 0);
-        for (int t = t0; t < t1; ++t) {
-          const int buf = S::kBufs == 2 ? (t - t0) & 1 : 0;
-          int ahead = -1;
-          if (S::kBufs == 2 && t + 1 < t1) {
-            load_tile(t + 1, buf ^ 1);
-            ahead = page_of(t + 2);
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
-          } else {
-            ahead = page_of(t + 2);
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-          }
-          __syncthreads();
-          if ((int)threadIdx.x < pages_tile) s_page[t & 1][threadIdx.x] = ahead;  // tile t + 2's; t's are used up
-          if (!live) {
-            __syncthreads();
-            if (S::kBufs == 1 && t + 1 < t1) load_tile(t + 1, 0);
-            continue;
-          }
-          // ---- scores
-          float s[4][4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-#pragma unroll
-            for (int y = 0; y < 4; ++y) s[x][y] = 0.f;
-          const float* qr = s_q + ty * 4 * S::kStride;
-          const float* kr = s_k + (buf * kPfKeys + tx) * S::kStride;
-#pragma unroll 4
-          for (int d = 0; d < kD; d += 4) {
-            float4 qf[4], kf[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) qf[x] = *reinterpret_cast<const float4*>(qr + x * S::kStride + d);
-#pragma unroll
-            for (int y = 0; y < 4; ++y) kf[y] = *reinterpret_cast<const float4*>(kr + y * 16 * S::kStride + d);
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-#pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                s[x][y] = fmaf(qf[x].x, kf[y].x, s[x][y]);
-                s[x][y] = fmaf(qf[x].y, kf[y].y, s[x][y]);
-                s[x][y] = fmaf(qf[x].z, kf[y].z, s[x][y]);
-                s[x][y] = fmaf(qf[x].w, kf[y].w, s[x][y]);
-              }
-          }
-          // ---- weights, against a running reference that moves when a score exceeds it by 5.5 (e^5.5
-          // = 245): the maximum over a row's 16 threads is taken only then
-          const int j0 = (tile0 + t) * kPfKeys;
-          bool grow = false;
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            if (a.cap > 0.f) {
-#pragma unroll
-              for (int y = 0; y < 4; ++y) s[x][y] = a.cap * tanh_f32(s[x][y] * inv_cap);
-            }
-            if (j0 < wlo[x] || j0 + kPfKeys > whi[x]) {
-              const int rr = ty * 4 + x;
-#pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                const int j = j0 + tx + 16 * y;
-                bool vis = j >= wlo[x] && j < whi[x];
-                if (!vis && a.parent && whi[x] >= 0 && j >= P && j < hi)
-                  vis = (s_vis[rr][(j - P) >> 5] >> ((j - P) & 31)) & 1u;
-                if (!vis) s[x][y] = -INFINITY;
-              }
-            }
-            grow |= fmaxf(fmaxf(s[x][0], s[x][1]), fmaxf(s[x][2], s[x][3])) > m[x] + 5.5f;
-          }
-          if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              float mx = fmaxf(fmaxf(s[x][0], s[x][1]), fmaxf(s[x][2], s[x][3]));
-#pragma unroll
-              for (int o = 1; o < 16; o *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-              if (mx > m[x]) {
-                const float f = expf(m[x] - mx);  // 0 from -inf
-                l[x] *= f;
-#pragma unroll
-                for (int u = 0; u < kU; ++u) acc[x][u][0] *= f, acc[x][u][1] *= f;
-                m[x] = mx;
-              }
-            }
-          }
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            // expf of a difference, not 2^(z log2 e - m): the product's rounding would cost |z| 2^-24
-            const float ref = m[x] == -INFINITY ? 0.f : m[x];
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const float p = expf(s[x][y] - ref);
-              l[x] += p;
-              s_p[(ty * 4 + x) * S::kPStride + tx + 16 * y] = p;
-            }
-          }
-          __syncwarp();  // a warp's rows are its own: 2 ty, 8 rows
-          // ---- O += P V
-          const float* pr = s_p + ty * 4 * S::kPStride;
-          const float* vr = s_v + buf * kPfKeys * kD + tx * 2;
-#pragma unroll 2
-          for (int j = 0; j < kPfKeys; j += 4) {
-            float4 pf[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) pf[x] = *reinterpret_cast<const float4*>(pr + x * S::kPStride + j);
-#pragma unroll
-            for (int u = 0; u < kU; ++u) {
-              float2 v[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const float2*>(vr + (j + k) * kD + 32 * u);
-#pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                acc[x][u][0] = fmaf(pf[x].x, v[0].x, acc[x][u][0]);
-                acc[x][u][1] = fmaf(pf[x].x, v[0].y, acc[x][u][1]);
-                acc[x][u][0] = fmaf(pf[x].y, v[1].x, acc[x][u][0]);
-                acc[x][u][1] = fmaf(pf[x].y, v[1].y, acc[x][u][1]);
-                acc[x][u][0] = fmaf(pf[x].z, v[2].x, acc[x][u][0]);
-                acc[x][u][1] = fmaf(pf[x].z, v[2].y, acc[x][u][1]);
-                acc[x][u][0] = fmaf(pf[x].w, v[3].x, acc[x][u][0]);
-                acc[x][u][1] = fmaf(pf[x].w, v[3].y, acc[x][u][1]);
-              }
-            }
-          }
-          __syncthreads();
-          if (S::kBufs == 1 && t + 1 < t1) load_tile(t + 1, 0);
-        }
-        // ---- write the unit, or this CTA's part of it
-        const long long c0 = kStream ? u0 / sp.per : 0, c1 = kStream ? (u1 - 1) / sp.per : 1;
-        const size_t slot = kStream ? (size_t)unit_slot(blockIdx.x, sp.per, u0) : cta;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int rr = ty * 4 + x, i = (r0 + rr) / a.G, g = (r0 + rr) % a.G;
-#pragma unroll
-          for (int o = 1; o < 16; o *= 2) l[x] += __shfl_xor_sync(0xffffffffu, l[x], o);
-          if (rr >= rows || i >= n_act) continue;
-          float* to;
-          float f = 1.f;
-          if (c0 == c1) {
-            to = out + (((size_t)b * a.Hq + hk * a.G + g) * a.N + i) * kD;
-            f = 1.f / l[x];
-          } else {
-            to = a.ws_o + (slot * kPfRows + rr) * kD;
-            if (tx == 0) __stcg(&a.ws_ml[slot * kPfRows + rr], make_float2(m[x], l[x]));
-          }
-#pragma unroll
-          for (int u = 0; u < kU; ++u)
-            __stcg(reinterpret_cast<float2*>(to + tx * 2 + 32 * u), make_float2(acc[x][u][0] * f, acc[x][u][1] * f));
-        }
-        if (c0 == c1) continue;
-        // this CTA's rows of the merge: all of them as the last to finish, or its share of a cluster's
-        int m0 = 0, m1 = rows, parts = splits;
-        if constexpr (kStream) {
-          __threadfence();
-          __syncthreads();
-          if (threadIdx.x == 0) {
-            s_last = ptx::atom_add_acq_rel_gpu(&a.cnt[c0], 1u) == (unsigned)(c1 - c0);
-            if (s_last) a.cnt[c0] = 0u;
-            __threadfence();
-          }
-          __syncthreads();
-          if (!s_last) continue;
-          parts = (int)(c1 - c0) + 1;
+    const int rows = unit_rows(a, n, rt, kPfRows), r0 = rt * kPfRows;
+    const int lo = unit_lo(a, P, rt, kPfRows), tile0 = lo / kPfKeys;
+    const int hi = min(P + n_act, P + (r0 + rows - 1) / a.G + 1);
+    // page of piece `threadIdx.x` of tile t, -1 where no row is needed
+    auto page_of = [&](int t) -> int {
+      const int j = (tile0 + t) * kPfKeys + ((int)threadIdx.x << min(a.page_shift, 6));
+      if ((int)threadIdx.x >= pages_tile || t >= t1 || j >= hi || j + (1 << min(a.page_shift, 6)) <= lo) return -1;
+      const int page = table[j >> a.page_shift];
+      if (page >= 0 && page < a.num_pages) return page;
+      set_dev_status(a.dev_status, TV_DEV_BAD_PAGE);
+      return -1;
+    };
+    // rows [lo, hi) of tile t; others (pages past the end, rows behind the window, whose contents
+    // may be anything) read as zero
+    auto load_tile = [&](int t, int buf) {
+      for (int e = threadIdx.x; e < kPfKeys * (kD / 4); e += kPfThreads) {
+        const int jj = e / (kD / 4), ch = e - jj * (kD / 4);
+        const int j = (tile0 + t) * kPfKeys + jj;
+        float* dk = s_k + (buf * kPfKeys + jj) * S::kStride + ch * 4;
+        float* dv = s_v + (buf * kPfKeys + jj) * kD + ch * 4;
+        const int page = j >= lo && j < hi ? s_page[t & 1][jj >> min(a.page_shift, 6)] : -1;
+        if (page >= 0) {
+          const size_t off =
+              ((((size_t)page * a.Hkv + hk) << a.page_shift) + (j & ((1 << a.page_shift) - 1))) * kD + ch * 4;
+          cp_async16(dk, reinterpret_cast<const float*>(a.k) + off);
+          cp_async16(dv, reinterpret_cast<const float*>(a.v) + off);
         } else {
-          __syncwarp();
-          ptx::cluster_sync();
-          m0 = rows * (int)blockIdx.x / splits;
-          m1 = rows * ((int)blockIdx.x + 1) / splits;
+          *reinterpret_cast<float4*>(dk) = make_float4(0.f, 0.f, 0.f, 0.f);
+          *reinterpret_cast<float4*>(dv) = make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        for (int e = threadIdx.x; e < (m1 - m0) * (kD / 4); e += kPfThreads) {
-          const int rr = m0 + e / (kD / 4), ch = e % (kD / 4), i = (r0 + rr) / a.G, g = (r0 + rr) % a.G;
-          if (i >= n_act) continue;
-          // one pass in batches of independent loads, with a running maximum
-          float M = -INFINITY, L = 0.f;
-          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int p0 = 0; p0 < parts; p0 += kPfMerge) {
-            float2 ml[kPfMerge];
-            float4 v[kPfMerge];
-#pragma unroll
-            for (int k = 0; k < kPfMerge; ++k) {
-              const int part = min(p0 + k, parts - 1);
-              const size_t from = kStream ? (size_t)unit_slot(c0 + part, sp.per, u0) : cta - blockIdx.x + part;
-              ml[k] = __ldcg(&a.ws_ml[from * kPfRows + rr]);
-              v[k] = __ldcg(reinterpret_cast<const float4*>(a.ws_o + (from * kPfRows + rr) * kD + ch * 4));
-              if (p0 + k >= parts) ml[k].x = -INFINITY;
-            }
-            float Mn = M;
-#pragma unroll
-            for (int k = 0; k < kPfMerge; ++k) Mn = fmaxf(Mn, ml[k].x);
-            if (Mn == -INFINITY) continue;
-            const float f0 = expf(M - Mn);
-            M = Mn;
-            L *= f0;
-            o.x *= f0, o.y *= f0, o.z *= f0, o.w *= f0;
-#pragma unroll
-            for (int k = 0; k < kPfMerge; ++k) {
-              if (ml[k].x == -INFINITY) continue;
-              const float f = expf(ml[k].x - M);
-              L = fmaf(f, ml[k].y, L);
-              o.x = fmaf(f, v[k].x, o.x);
-              o.y = fmaf(f, v[k].y, o.y);
-              o.z = fmaf(f, v[k].z, o.z);
-              o.w = fmaf(f, v[k].w, o.w);
-            }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    __syncthreads();
+    // ---- rows: queries, bounds and the tree nodes each sees
+    if ((int)threadIdx.x < pages_tile) {
+      s_page[t0 & 1][threadIdx.x] = page_of(t0);
+      s_page[(t0 + 1) & 1][threadIdx.x] = page_of(t0 + 1);
+    }
+    for (int e = threadIdx.x; e < kPfRows * (kD / 4); e += kPfThreads) {
+      const int rr = e / (kD / 4), ch = e - rr * (kD / 4), i = (r0 + rr) / a.G, g = (r0 + rr) % a.G;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (rr < rows && i < n_act) {
+        v = *reinterpret_cast<const float4*>(q + (((size_t)b * a.Hq + hk * a.G + g) * a.N + i) * kD + ch * 4);
+        v.x *= a.scale, v.y *= a.scale, v.z *= a.scale, v.w *= a.scale;
+      }
+      *reinterpret_cast<float4*>(s_q + rr * S::kStride + ch * 4) = v;
+    }
+    if (threadIdx.x < kPfRows) {
+      const int rr = threadIdx.x, i = (r0 + rr) / a.G;
+      int wlo = 0, whi = -1;  // what is no row sees nothing
+      if (rr < rows && i < n_act) {
+        int depth = i;
+        whi = a.parent ? P : P + i + 1;
+        if (a.parent) {
+          depth = -1;
+          for (int w = 0; w < (n + 31) / 32; ++w) s_vis[rr][w] = 0u;
+          for (int at = i; at >= 0; at = s_par[at]) {  // parents fall: it ends
+            ++depth;
+            if (a.window <= 0 || depth < a.window) s_vis[rr][at >> 5] |= 1u << (at & 31);
           }
-          const float f = 1.f / L;
-          *reinterpret_cast<float4*>(out + (((size_t)b * a.Hq + hk * a.G + g) * a.N + i) * kD + ch * 4) =
-              make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
         }
+        if (a.window > 0) wlo = P + depth - a.window + 1;
+      }
+      s_lo[rr] = wlo;
+      s_hi[rr] = whi;
+    }
+    __syncthreads();
+    float m[4], l[4], acc[4][kU][2];
+    int wlo[4], whi[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      m[x] = -INFINITY;
+      l[x] = 0.f;
+      wlo[x] = s_lo[ty * 4 + x];
+      whi[x] = s_hi[ty * 4 + x];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) acc[x][u][0] = acc[x][u][1] = 0.f;
+    }
+    const bool live = (ty & ~1) * 4 < rows;  // some of this warp's eight rows are rows
+    load_tile(t0, 0);
+    for (int t = t0; t < t1; ++t) {
+      const int buf = S::kBufs == 2 ? (t - t0) & 1 : 0;
+      int ahead = -1;
+      if (S::kBufs == 2 && t + 1 < t1) {
+        load_tile(t + 1, buf ^ 1);
+        ahead = page_of(t + 2);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+      } else {
+        ahead = page_of(t + 2);
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+      }
+      __syncthreads();
+      if ((int)threadIdx.x < pages_tile) s_page[t & 1][threadIdx.x] = ahead;  // tile t + 2's; t's are used up
+      if (!live) {
+        __syncthreads();
+        if (S::kBufs == 1 && t + 1 < t1) load_tile(t + 1, 0);
+        continue;
+      }
+      // ---- scores
+      float s[4][4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) s[x][y] = 0.f;
+      const float* qr = s_q + ty * 4 * S::kStride;
+      const float* kr = s_k + (buf * kPfKeys + tx) * S::kStride;
+#pragma unroll 4
+      for (int d = 0; d < kD; d += 4) {
+        float4 qf[4], kf[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) qf[x] = *reinterpret_cast<const float4*>(qr + x * S::kStride + d);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) kf[y] = *reinterpret_cast<const float4*>(kr + y * 16 * S::kStride + d);
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            s[x][y] = fmaf(qf[x].x, kf[y].x, s[x][y]);
+            s[x][y] = fmaf(qf[x].y, kf[y].y, s[x][y]);
+            s[x][y] = fmaf(qf[x].z, kf[y].z, s[x][y]);
+            s[x][y] = fmaf(qf[x].w, kf[y].w, s[x][y]);
+          }
+      }
+      // ---- weights, against a running reference that moves when a score exceeds it by 5.5 (e^5.5
+      // = 245): the maximum over a row's 16 threads is taken only then
+      const int j0 = (tile0 + t) * kPfKeys;
+      bool grow = false;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        if (a.cap > 0.f) {
+#pragma unroll
+          for (int y = 0; y < 4; ++y) s[x][y] = a.cap * tanh_f32(s[x][y] * inv_cap);
+        }
+        if (j0 < wlo[x] || j0 + kPfKeys > whi[x]) {
+          const int rr = ty * 4 + x;
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const int j = j0 + tx + 16 * y;
+            bool vis = j >= wlo[x] && j < whi[x];
+            if (!vis && a.parent && whi[x] >= 0 && j >= P && j < hi)
+              vis = (s_vis[rr][(j - P) >> 5] >> ((j - P) & 31)) & 1u;
+            if (!vis) s[x][y] = -INFINITY;
+          }
+        }
+        grow |= fmaxf(fmaxf(s[x][0], s[x][1]), fmaxf(s[x][2], s[x][3])) > m[x] + 5.5f;
+      }
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          float mx = fmaxf(fmaxf(s[x][0], s[x][1]), fmaxf(s[x][2], s[x][3]));
+#pragma unroll
+          for (int o = 1; o < 16; o *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          if (mx > m[x]) {
+            const float f = expf(m[x] - mx);  // 0 from -inf
+            l[x] *= f;
+#pragma unroll
+            for (int u = 0; u < kU; ++u) acc[x][u][0] *= f, acc[x][u][1] *= f;
+            m[x] = mx;
+          }
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        // expf of a difference, not 2^(z log2 e - m): the product's rounding would cost |z| 2^-24
+        const float ref = m[x] == -INFINITY ? 0.f : m[x];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const float p = expf(s[x][y] - ref);
+          l[x] += p;
+          s_p[(ty * 4 + x) * S::kPStride + tx + 16 * y] = p;
+        }
+      }
+      __syncwarp();  // a warp's rows are its own: 2 ty, 8 rows
+      // ---- O += P V
+      const float* pr = s_p + ty * 4 * S::kPStride;
+      const float* vr = s_v + buf * kPfKeys * kD + tx * 2;
+#pragma unroll 2
+      for (int j = 0; j < kPfKeys; j += 4) {
+        float4 pf[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) pf[x] = *reinterpret_cast<const float4*>(pr + x * S::kPStride + j);
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          float2 v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const float2*>(vr + (j + k) * kD + 32 * u);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            acc[x][u][0] = fmaf(pf[x].x, v[0].x, acc[x][u][0]);
+            acc[x][u][1] = fmaf(pf[x].x, v[0].y, acc[x][u][1]);
+            acc[x][u][0] = fmaf(pf[x].y, v[1].x, acc[x][u][0]);
+            acc[x][u][1] = fmaf(pf[x].y, v[1].y, acc[x][u][1]);
+            acc[x][u][0] = fmaf(pf[x].z, v[2].x, acc[x][u][0]);
+            acc[x][u][1] = fmaf(pf[x].z, v[2].y, acc[x][u][1]);
+            acc[x][u][0] = fmaf(pf[x].w, v[3].x, acc[x][u][0]);
+            acc[x][u][1] = fmaf(pf[x].w, v[3].y, acc[x][u][1]);
+          }
+        }
+      }
+      __syncthreads();
+      if (S::kBufs == 1 && t + 1 < t1) load_tile(t + 1, 0);
+    }
+    // ---- write the unit, or this CTA's part of it
+    const long long c0 = kStream ? u0 / sp.per : 0, c1 = kStream ? (u1 - 1) / sp.per : 1;
+    const size_t slot = kStream ? (size_t)unit_slot(blockIdx.x, sp.per, u0) : cta;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int rr = ty * 4 + x, i = (r0 + rr) / a.G, g = (r0 + rr) % a.G;
+#pragma unroll
+      for (int o = 1; o < 16; o *= 2) l[x] += __shfl_xor_sync(0xffffffffu, l[x], o);
+      if (rr >= rows || i >= n_act) continue;
+      float* to;
+      float f = 1.f;
+      if (c0 == c1) {
+        to = out + (((size_t)b * a.Hq + hk * a.G + g) * a.N + i) * kD;
+        f = 1.f / l[x];
+      } else {
+        to = a.ws_o + (slot * kPfRows + rr) * kD;
+        if (tx == 0) __stcg(&a.ws_ml[slot * kPfRows + rr], make_float2(m[x], l[x]));
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+        __stcg(reinterpret_cast<float2*>(to + tx * 2 + 32 * u), make_float2(acc[x][u][0] * f, acc[x][u][1] * f));
+    }
+    if (c0 == c1) continue;
+    // this CTA's rows of the merge: all of them as the last to finish, or its share of a cluster's
+    int m0 = 0, m1 = rows, parts = splits;
+    if constexpr (kStream) {
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        s_last = ptx::atom_add_acq_rel_gpu(&a.cnt[c0], 1u) == (unsigned)(c1 - c0);
+        if (s_last) a.cnt[c0] = 0u;
+        __threadfence();
+      }
+      __syncthreads();
+      if (!s_last) continue;
+      parts = (int)(c1 - c0) + 1;
+    } else {
+      __syncwarp();
+      ptx::cluster_sync();
+      m0 = rows * (int)blockIdx.x / splits;
+      m1 = rows * ((int)blockIdx.x + 1) / splits;
+    }
+    for (int e = threadIdx.x; e < (m1 - m0) * (kD / 4); e += kPfThreads) {
+      const int rr = m0 + e / (kD / 4), ch = e % (kD / 4), i = (r0 + rr) / a.G, g = (r0 + rr) % a.G;
+      if (i >= n_act) continue;
+      // one pass in batches of independent loads, with a running maximum
+      float M = -INFINITY, L = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int p0 = 0; p0 < parts; p0 += kPfMerge) {
+        float2 ml[kPfMerge];
+        float4 v[kPfMerge];
+#pragma unroll
+        for (int k = 0; k < kPfMerge; ++k) {
+          const int part = min(p0 + k, parts - 1);
+          const size_t from = kStream ? (size_t)unit_slot(c0 + part, sp.per, u0) : cta - blockIdx.x + part;
+          ml[k] = __ldcg(&a.ws_ml[from * kPfRows + rr]);
+          v[k] = __ldcg(reinterpret_cast<const float4*>(a.ws_o + (from * kPfRows + rr) * kD + ch * 4));
+          if (p0 + k >= parts) ml[k].x = -INFINITY;
+        }
+        float Mn = M;
+#pragma unroll
+        for (int k = 0; k < kPfMerge; ++k) Mn = fmaxf(Mn, ml[k].x);
+        if (Mn == -INFINITY) continue;
+        const float f0 = expf(M - Mn);
+        M = Mn;
+        L *= f0;
+        o.x *= f0, o.y *= f0, o.z *= f0, o.w *= f0;
+#pragma unroll
+        for (int k = 0; k < kPfMerge; ++k) {
+          if (ml[k].x == -INFINITY) continue;
+          const float f = expf(ml[k].x - M);
+          L = fmaf(f, ml[k].y, L);
+          o.x = fmaf(f, v[k].x, o.x);
+          o.y = fmaf(f, v[k].y, o.y);
+          o.z = fmaf(f, v[k].z, o.z);
+          o.w = fmaf(f, v[k].w, o.w);
+        }
+      }
+      const float f = 1.f / L;
+      *reinterpret_cast<float4*>(out + (((size_t)b * a.Hq + hk * a.G + g) * a.N + i) * kD + ch * 4) =
+          make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+    }
   }
 }
 

@@ -26,10 +26,6 @@ constexpr int kPsStages = 3;  // K and V tiles in shared memory: two on their wa
 constexpr int kPrTol = 8, kPrFix = 4;
 constexpr int kPsMerge = 4;  // parts whose loads are in flight together
 
-__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_addr(dst)), "l"(src) : "memory");
-}
-
 template <int kDPL, int kRPW>
 struct PsSmem {
   static constexpr int kD = kDPL * 32;
@@ -50,46 +46,46 @@ __device__ __forceinline__ void ps_merge(const PagedAttn& a, int b, int hk, int 
   constexpr int kD = kDPL * 32;
   const int lane = threadIdx.x & 31;
   float* out = reinterpret_cast<float*>(a.out);
-          for (int rr = threadIdx.x >> 5; rr < rows; rr += kPsWarps) {
-            const int r = rt * RT + rr, i = r / a.G, g = r % a.G;
-            if (i >= n_act) continue;
-            // one pass in batches of independent loads, with a running maximum
-            float M = -INFINITY, L = 0.f, o[kDPL];
-  #pragma unroll
-            for (int u = 0; u < kDPL; ++u) o[u] = 0.f;
-            for (long long cc = c0; cc <= c1; cc += kPsMerge) {
-              float2 ml[kPsMerge];
-              float x[kPsMerge][kDPL];
-  #pragma unroll
-              for (int k = 0; k < kPsMerge; ++k) {
-                const size_t row = (size_t)unit_slot(min(cc + k, c1), per, u0) * RT + rr;
-                ml[k] = __ldcg(&a.ws_ml[row]);
-  #pragma unroll
-                for (int u = 0; u < kDPL; ++u) x[k][u] = __ldcg(&a.ws_o[row * kD + lane + 32 * u]);
-                if (cc + k > c1) ml[k].x = -INFINITY;
-              }
-              float Mn = M;
-  #pragma unroll
-              for (int k = 0; k < kPsMerge; ++k) Mn = fmaxf(Mn, ml[k].x);
-              if (Mn == -INFINITY) continue;
-              const float f0 = expf(M - Mn);
-              M = Mn;
-              L *= f0;
-  #pragma unroll
-              for (int u = 0; u < kDPL; ++u) o[u] *= f0;
-  #pragma unroll
-              for (int k = 0; k < kPsMerge; ++k) {
-                if (ml[k].x == -INFINITY) continue;
-                const float f = expf(ml[k].x - M);
-                L = fmaf(f, ml[k].y, L);
-  #pragma unroll
-                for (int u = 0; u < kDPL; ++u) o[u] = fmaf(f, x[k][u], o[u]);
-              }
-            }
-            const size_t off = (((size_t)b * a.Hq + hk * a.G + g) * a.N + i) * kD;
-  #pragma unroll
-            for (int u = 0; u < kDPL; ++u) out[off + lane + 32 * u] = o[u] / L;
-          }
+  for (int rr = threadIdx.x >> 5; rr < rows; rr += kPsWarps) {
+    const int r = rt * RT + rr, i = r / a.G, g = r % a.G;
+    if (i >= n_act) continue;
+    // one pass in batches of independent loads, with a running maximum
+    float M = -INFINITY, L = 0.f, o[kDPL];
+#pragma unroll
+    for (int u = 0; u < kDPL; ++u) o[u] = 0.f;
+    for (long long cc = c0; cc <= c1; cc += kPsMerge) {
+      float2 ml[kPsMerge];
+      float x[kPsMerge][kDPL];
+#pragma unroll
+      for (int k = 0; k < kPsMerge; ++k) {
+        const size_t row = (size_t)unit_slot(min(cc + k, c1), per, u0) * RT + rr;
+        ml[k] = __ldcg(&a.ws_ml[row]);
+#pragma unroll
+        for (int u = 0; u < kDPL; ++u) x[k][u] = __ldcg(&a.ws_o[row * kD + lane + 32 * u]);
+        if (cc + k > c1) ml[k].x = -INFINITY;
+      }
+      float Mn = M;
+#pragma unroll
+      for (int k = 0; k < kPsMerge; ++k) Mn = fmaxf(Mn, ml[k].x);
+      if (Mn == -INFINITY) continue;
+      const float f0 = expf(M - Mn);
+      M = Mn;
+      L *= f0;
+#pragma unroll
+      for (int u = 0; u < kDPL; ++u) o[u] *= f0;
+#pragma unroll
+      for (int k = 0; k < kPsMerge; ++k) {
+        if (ml[k].x == -INFINITY) continue;
+        const float f = expf(ml[k].x - M);
+        L = fmaf(f, ml[k].y, L);
+#pragma unroll
+        for (int u = 0; u < kDPL; ++u) o[u] = fmaf(f, x[k][u], o[u]);
+      }
+    }
+    const size_t off = (((size_t)b * a.Hq + hk * a.G + g) * a.N + i) * kD;
+#pragma unroll
+    for (int u = 0; u < kDPL; ++u) out[off + lane + 32 * u] = o[u] / L;
+  }
 }
 
 template <int kDPL, int kRPW>
@@ -139,177 +135,177 @@ __global__ void __launch_bounds__(kPsWarps * 32, kDPL <= 4 ? 2 : 1) paged_simt_k
       n_act = s_first_pad;
     }
     tree = b;
-        const int rows = unit_rows(a, n, rt, kRT);
-        const int lo = unit_lo(a, P, rt, kRT), tile0 = lo / kPsKeys;
-        const int hi = min(P + n_act, P + (rt * kRT + rows - 1) / a.G + 1);
-        // ---- rows: query, depth and the tree nodes each sees
-        __syncthreads();
-        for (int rr = warp; rr < kRT; rr += kPsWarps) {
-          const int r = rt * kRT + rr, i = r / a.G, g = r % a.G;
-          const bool live = rr < rows && i < n_act;
-          const size_t qoff = (((size_t)b * a.Hq + hk * a.G + g) * a.N + i) * kD;
-          for (int d = lane; d < kD; d += 32) s_q[rr * kD + d] = live ? q[qoff + d] * a.scale : 0.f;
-          if (!a.parent) {
-            if (lane == 0) s_depth[rr] = i;
-            continue;
-          }
-          for (int w = lane; w < kMaxNodes / 32; w += 32) s_vis[rr][w] = 0u;
-          __syncwarp();
-          if (lane == 0) {
-            int depth = 0;
-            for (int at = live ? i : -1; at >= 0; at = s_par[at], ++depth)  // parents fall: ends within n steps
-              if (a.window <= 0 || depth < a.window) s_vis[rr][at >> 5] |= 1u << (at & 31);
-            s_depth[rr] = max(0, depth - 1);
-          }
-        }
-        float m[kRPW], l[kRPW], acc[kRPW][kDPL];
+    const int rows = unit_rows(a, n, rt, kRT);
+    const int lo = unit_lo(a, P, rt, kRT), tile0 = lo / kPsKeys;
+    const int hi = min(P + n_act, P + (rt * kRT + rows - 1) / a.G + 1);
+    // ---- rows: query, depth and the tree nodes each sees
+    __syncthreads();
+    for (int rr = warp; rr < kRT; rr += kPsWarps) {
+      const int r = rt * kRT + rr, i = r / a.G, g = r % a.G;
+      const bool live = rr < rows && i < n_act;
+      const size_t qoff = (((size_t)b * a.Hq + hk * a.G + g) * a.N + i) * kD;
+      for (int d = lane; d < kD; d += 32) s_q[rr * kD + d] = live ? q[qoff + d] * a.scale : 0.f;
+      if (!a.parent) {
+        if (lane == 0) s_depth[rr] = i;
+        continue;
+      }
+      for (int w = lane; w < kMaxNodes / 32; w += 32) s_vis[rr][w] = 0u;
+      __syncwarp();
+      if (lane == 0) {
+        int depth = 0;
+        for (int at = live ? i : -1; at >= 0; at = s_par[at], ++depth)  // parents fall: ends within n steps
+          if (a.window <= 0 || depth < a.window) s_vis[rr][at >> 5] |= 1u << (at & 31);
+        s_depth[rr] = max(0, depth - 1);
+      }
+    }
+    float m[kRPW], l[kRPW], acc[kRPW][kDPL];
 #pragma unroll
-        for (int rw = 0; rw < kRPW; ++rw) {
-          m[rw] = -INFINITY;
-          l[rw] = 0.f;
+    for (int rw = 0; rw < kRPW; ++rw) {
+      m[rw] = -INFINITY;
+      l[rw] = 0.f;
 #pragma unroll
-          for (int t = 0; t < kDPL; ++t) acc[rw][t] = 0.f;
+      for (int t = 0; t < kDPL; ++t) acc[rw][t] = 0.f;
+    }
+    // rows [lo, hi) of the tile; others (pages past the end, rows behind the window, whose
+    // contents may be anything) read as zero
+    auto page_of = [&](int t) -> int {
+      const int j = (tile0 + t) * kPsKeys + ((int)threadIdx.x << box_shift);
+      if ((int)threadIdx.x >= pages_tile || t >= t1 || j >= hi || j + (1 << box_shift) <= lo) return -1;
+      const int page = table[j >> a.page_shift];
+      if (page >= 0 && page < a.num_pages) return page;
+      set_dev_status(a.dev_status, TV_DEV_BAD_PAGE);
+      return -1;
+    };
+    auto load_tile = [&](int t, int buf) {
+      if (t >= t1) {  // an empty group keeps the count
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        return;
+      }
+      constexpr int kChunks = kD / kVec;
+      for (int e = threadIdx.x; e < kPsKeys * kChunks; e += blockDim.x) {
+        const int jj = e / kChunks, ch = e - jj * kChunks;
+        const int j = (tile0 + t) * kPsKeys + jj;
+        float* dk = s_k + (buf * kPsKeys + jj) * S::kStride + ch * kVec;
+        float* dv = s_v + (buf * kPsKeys + jj) * kD + ch * kVec;
+        const int page = j >= lo && j < hi ? s_page[t & 3][jj >> box_shift] : -1;
+        if (page >= 0) {
+          const size_t off =
+              ((((size_t)page * a.Hkv + hk) << a.page_shift) + (j & ((1 << a.page_shift) - 1))) * kD + ch * kVec;
+          cp_async16(dk, reinterpret_cast<const float*>(a.k) + off);
+          cp_async16(dv, reinterpret_cast<const float*>(a.v) + off);
+        } else {
+          *reinterpret_cast<uint4*>(dk) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(dv) = make_uint4(0, 0, 0, 0);
         }
-        // rows [lo, hi) of the tile; others (pages past the end, rows behind the window, whose
-        // contents may be anything) read as zero
-        auto page_of = [&](int t) -> int {
-          const int j = (tile0 + t) * kPsKeys + ((int)threadIdx.x << box_shift);
-          if ((int)threadIdx.x >= pages_tile || t >= t1 || j >= hi || j + (1 << box_shift) <= lo) return -1;
-          const int page = table[j >> a.page_shift];
-          if (page >= 0 && page < a.num_pages) return page;
-          set_dev_status(a.dev_status, TV_DEV_BAD_PAGE);
-          return -1;
-        };
-        auto load_tile = [&](int t, int buf) {
-          if (t >= t1) {  // an empty group keeps the count
-            asm volatile("cp.async.commit_group;" ::: "memory");
-            return;
-          }
-          constexpr int kChunks = kD / kVec;
-          for (int e = threadIdx.x; e < kPsKeys * kChunks; e += blockDim.x) {
-            const int jj = e / kChunks, ch = e - jj * kChunks;
-            const int j = (tile0 + t) * kPsKeys + jj;
-            float* dk = s_k + (buf * kPsKeys + jj) * S::kStride + ch * kVec;
-            float* dv = s_v + (buf * kPsKeys + jj) * kD + ch * kVec;
-            const int page = j >= lo && j < hi ? s_page[t & 3][jj >> box_shift] : -1;
-            if (page >= 0) {
-              const size_t off =
-                  ((((size_t)page * a.Hkv + hk) << a.page_shift) + (j & ((1 << a.page_shift) - 1))) * kD + ch * kVec;
-              cp_async16(dk, reinterpret_cast<const float*>(a.k) + off);
-              cp_async16(dv, reinterpret_cast<const float*>(a.v) + off);
-            } else {
-              *reinterpret_cast<uint4*>(dk) = make_uint4(0, 0, 0, 0);
-              *reinterpret_cast<uint4*>(dv) = make_uint4(0, 0, 0, 0);
-            }
-          }
-          asm volatile("cp.async.commit_group;" ::: "memory");
-        };
-        if ((int)threadIdx.x < pages_tile) {
-          for (int u = 0; u < 3; ++u) s_page[(t0 + u) & 3][threadIdx.x] = page_of(t0 + u);
-        }
-        __syncthreads();
-        load_tile(t0, 0);
-        load_tile(t0 + 1, 1);
-        for (int t = t0; t < t1; ++t) {
-          const int buf = (t - t0) % kPsStages;
-          load_tile(t + 2, (t + 2 - t0) % kPsStages);
-          const int ahead = page_of(t + 3);
-          asm volatile("cp.async.wait_group 2;" ::: "memory");
-          __syncthreads();
-          if ((int)threadIdx.x < pages_tile) s_page[(t + 3) & 3][threadIdx.x] = ahead;
-          const int j = (tile0 + t) * kPsKeys + lane;
-          float4 part[kRPW];  // four chains
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    if ((int)threadIdx.x < pages_tile) {
+      for (int u = 0; u < 3; ++u) s_page[(t0 + u) & 3][threadIdx.x] = page_of(t0 + u);
+    }
+    __syncthreads();
+    load_tile(t0, 0);
+    load_tile(t0 + 1, 1);
+    for (int t = t0; t < t1; ++t) {
+      const int buf = (t - t0) % kPsStages;
+      load_tile(t + 2, (t + 2 - t0) % kPsStages);
+      const int ahead = page_of(t + 3);
+      asm volatile("cp.async.wait_group 2;" ::: "memory");
+      __syncthreads();
+      if ((int)threadIdx.x < pages_tile) s_page[(t + 3) & 3][threadIdx.x] = ahead;
+      const int j = (tile0 + t) * kPsKeys + lane;
+      float4 part[kRPW];  // four chains
 #pragma unroll
-          for (int rw = 0; rw < kRPW; ++rw) part[rw] = make_float4(0.f, 0.f, 0.f, 0.f);
-          const float* kr = s_k + (buf * kPsKeys + lane) * S::kStride;
+      for (int rw = 0; rw < kRPW; ++rw) part[rw] = make_float4(0.f, 0.f, 0.f, 0.f);
+      const float* kr = s_k + (buf * kPsKeys + lane) * S::kStride;
 #pragma unroll 8
-          for (int d = 0; d < kD; d += kVec) {
-            const float4 kf = *reinterpret_cast<const float4*>(kr + d);
-#pragma unroll
-            for (int rw = 0; rw < kRPW; ++rw) {
-              const float4 qf = *reinterpret_cast<const float4*>(s_q + (warp * kRPW + rw) * kD + d);
-              part[rw].x = fmaf(qf.x, kf.x, part[rw].x);
-              part[rw].y = fmaf(qf.y, kf.y, part[rw].y);
-              part[rw].z = fmaf(qf.z, kf.z, part[rw].z);
-              part[rw].w = fmaf(qf.w, kf.w, part[rw].w);
-            }
-          }
-#pragma unroll
-          for (int rw = 0; rw < kRPW; ++rw) {
-            const int rr = warp * kRPW + rw, i = (rt * kRT + rr) / a.G;
-            bool vis = rr < rows && i < n_act && j < hi;
-            if (j < P) {
-              vis = vis && (a.window <= 0 || P - j + s_depth[rr] < a.window);
-            } else if (vis) {
-              const int t_new = j - P;
-              vis = a.parent ? (s_vis[rr][t_new >> 5] >> (t_new & 31)) & 1u
-                             : t_new <= i && (a.window <= 0 || i - t_new < a.window);
-            }
-            float z = (part[rw].x + part[rw].y) + (part[rw].z + part[rw].w);
-            // expf of a difference, not 2^(z log2 e - m): the product's rounding would cost |z| 2^-24
-            if (a.cap > 0.f) z = a.cap * tanh_f32(z / a.cap);
-            z = vis ? z : -INFINITY;
-            const float mt = warp_max(z);
-            float p = 0.f;
-            if (mt != -INFINITY) {
-              const float mnew = fmaxf(m[rw], mt);
-              const float corr = expf(m[rw] - mnew);
-              p = expf(z - mnew);
-              l[rw] = l[rw] * corr + warp_sum(p);
-#pragma unroll
-              for (int u = 0; u < kDPL; ++u) acc[rw][u] *= corr;
-              m[rw] = mnew;
-            }
-            s_p[rr * kPsKeys + lane] = p;
-          }
-          __syncwarp();
-#pragma unroll 2
-          for (int jj = 0; jj < kPsKeys; jj += 4) {
-            float4 pf[kRPW];
-#pragma unroll
-            for (int rw = 0; rw < kRPW; ++rw)
-              pf[rw] = *reinterpret_cast<const float4*>(s_p + (warp * kRPW + rw) * kPsKeys + jj);
-#pragma unroll
-            for (int u = 0; u < kDPL; ++u) {
-              const float* vr = s_v + (buf * kPsKeys + jj) * kD + lane + 32 * u;
-              const float v0 = vr[0], v1 = vr[kD], v2 = vr[2 * kD], v3 = vr[3 * kD];
-#pragma unroll
-              for (int rw = 0; rw < kRPW; ++rw)
-                acc[rw][u] = fmaf(pf[rw].w, v3, fmaf(pf[rw].z, v2, fmaf(pf[rw].y, v1, fmaf(pf[rw].x, v0, acc[rw][u]))));
-            }
-          }
-          __syncthreads();
-        }
-        // ---- write the unit, or this CTA's part of it
-        const long long c0 = u0 / sp.per, c1 = (w.u1 - 1) / sp.per;
-        const int slot = unit_slot(blockIdx.x, sp.per, u0);
+      for (int d = 0; d < kD; d += kVec) {
+        const float4 kf = *reinterpret_cast<const float4*>(kr + d);
 #pragma unroll
         for (int rw = 0; rw < kRPW; ++rw) {
-          const int rr = warp * kRPW + rw, r = rt * kRT + rr, i = r / a.G, g = r % a.G;
-          if (c0 == c1) {
-            if (rr >= rows || i >= n_act) continue;
-            const size_t off = (((size_t)b * a.Hq + hk * a.G + g) * a.N + i) * kD;
-            const float inv = 1.f / l[rw];
-#pragma unroll
-            for (int u = 0; u < kDPL; ++u) out[off + lane + 32 * u] = acc[rw][u] * inv;
-          } else {
-            const size_t row = (size_t)slot * kRT + rr;
-            if (lane == 0) a.ws_ml[row] = make_float2(m[rw], l[rw]);
-#pragma unroll
-            for (int u = 0; u < kDPL; ++u) a.ws_o[row * kD + lane + 32 * u] = acc[rw][u];
-          }
+          const float4 qf = *reinterpret_cast<const float4*>(s_q + (warp * kRPW + rw) * kD + d);
+          part[rw].x = fmaf(qf.x, kf.x, part[rw].x);
+          part[rw].y = fmaf(qf.y, kf.y, part[rw].y);
+          part[rw].z = fmaf(qf.z, kf.z, part[rw].z);
+          part[rw].w = fmaf(qf.w, kf.w, part[rw].w);
         }
-        if (c0 == c1) continue;
-        __threadfence();
-        __syncthreads();
-        if (threadIdx.x == 0) {
-          s_last = ptx::atom_add_acq_rel_gpu(&a.cnt[c0], 1u) == (unsigned)(c1 - c0);
-          if (s_last) a.cnt[c0] = 0u;
-          __threadfence();
+      }
+#pragma unroll
+      for (int rw = 0; rw < kRPW; ++rw) {
+        const int rr = warp * kRPW + rw, i = (rt * kRT + rr) / a.G;
+        bool vis = rr < rows && i < n_act && j < hi;
+        if (j < P) {
+          vis = vis && (a.window <= 0 || P - j + s_depth[rr] < a.window);
+        } else if (vis) {
+          const int t_new = j - P;
+          vis = a.parent ? (s_vis[rr][t_new >> 5] >> (t_new & 31)) & 1u
+                         : t_new <= i && (a.window <= 0 || i - t_new < a.window);
         }
-        __syncthreads();
-        if (!s_last) continue;
-        ps_merge<kDPL>(a, b, hk, rt, kRT, rows, n_act, c0, c1, sp.per, u0);
+        float z = (part[rw].x + part[rw].y) + (part[rw].z + part[rw].w);
+        // expf of a difference, not 2^(z log2 e - m): the product's rounding would cost |z| 2^-24
+        if (a.cap > 0.f) z = a.cap * tanh_f32(z / a.cap);
+        z = vis ? z : -INFINITY;
+        const float mt = warp_max(z);
+        float p = 0.f;
+        if (mt != -INFINITY) {
+          const float mnew = fmaxf(m[rw], mt);
+          const float corr = expf(m[rw] - mnew);
+          p = expf(z - mnew);
+          l[rw] = l[rw] * corr + warp_sum(p);
+#pragma unroll
+          for (int u = 0; u < kDPL; ++u) acc[rw][u] *= corr;
+          m[rw] = mnew;
+        }
+        s_p[rr * kPsKeys + lane] = p;
+      }
+      __syncwarp();
+#pragma unroll 2
+      for (int jj = 0; jj < kPsKeys; jj += 4) {
+        float4 pf[kRPW];
+#pragma unroll
+        for (int rw = 0; rw < kRPW; ++rw)
+          pf[rw] = *reinterpret_cast<const float4*>(s_p + (warp * kRPW + rw) * kPsKeys + jj);
+#pragma unroll
+        for (int u = 0; u < kDPL; ++u) {
+          const float* vr = s_v + (buf * kPsKeys + jj) * kD + lane + 32 * u;
+          const float v0 = vr[0], v1 = vr[kD], v2 = vr[2 * kD], v3 = vr[3 * kD];
+#pragma unroll
+          for (int rw = 0; rw < kRPW; ++rw)
+            acc[rw][u] = fmaf(pf[rw].w, v3, fmaf(pf[rw].z, v2, fmaf(pf[rw].y, v1, fmaf(pf[rw].x, v0, acc[rw][u]))));
+        }
+      }
+      __syncthreads();
+    }
+    // ---- write the unit, or this CTA's part of it
+    const long long c0 = u0 / sp.per, c1 = (w.u1 - 1) / sp.per;
+    const int slot = unit_slot(blockIdx.x, sp.per, u0);
+#pragma unroll
+    for (int rw = 0; rw < kRPW; ++rw) {
+      const int rr = warp * kRPW + rw, r = rt * kRT + rr, i = r / a.G, g = r % a.G;
+      if (c0 == c1) {
+        if (rr >= rows || i >= n_act) continue;
+        const size_t off = (((size_t)b * a.Hq + hk * a.G + g) * a.N + i) * kD;
+        const float inv = 1.f / l[rw];
+#pragma unroll
+        for (int u = 0; u < kDPL; ++u) out[off + lane + 32 * u] = acc[rw][u] * inv;
+      } else {
+        const size_t row = (size_t)slot * kRT + rr;
+        if (lane == 0) a.ws_ml[row] = make_float2(m[rw], l[rw]);
+#pragma unroll
+        for (int u = 0; u < kDPL; ++u) a.ws_o[row * kD + lane + 32 * u] = acc[rw][u];
+      }
+    }
+    if (c0 == c1) continue;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      s_last = ptx::atom_add_acq_rel_gpu(&a.cnt[c0], 1u) == (unsigned)(c1 - c0);
+      if (s_last) a.cnt[c0] = 0u;
+      __threadfence();
+    }
+    __syncthreads();
+    if (!s_last) continue;
+    ps_merge<kDPL>(a, b, hk, rt, kRT, rows, n_act, c0, c1, sp.per, u0);
   }
 }
 
