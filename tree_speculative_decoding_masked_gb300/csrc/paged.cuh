@@ -71,8 +71,9 @@ __device__ inline long long head_tiles_warp(const PagedAttn& a, int P, int n, in
 // Every thread of the CTA calls it; red holds kPagedRed entries.  A CTA takes min_per tiles or more.
 // kWhole: where the units are at most the CTAs and the longest is little longer than an equal share (by
 // a quarter and 8 tiles, or 30), each CTA takes one unit whole instead: no merge, and at the power limit
-// more busy SMs only clock lower.  128 units on 152 SMs, whole / cut: 16 x 64 nodes over 1000
-// tokens 28.6 / 41.0 us, 8 x 128 nodes over 8000 117.6 / 121.9, over 32768 425.9 / 408.7.
+// more busy SMs only clock lower.  128 units on 152 SMs, whole / cut: 16 x 64 nodes over 1000 tokens
+// 29.8 / 45.2 us, over 4000 70.0 / 80.2, 8 x 128 nodes over 8000 120 / 126 (cut by the rule from 11600 on);
+// 80 units over 1000 tokens 30.5 / 33.3 (from 3500 on).
 template <bool kWhole = false>
 __device__ inline PagedSpan paged_span(const PagedAttn& a, int RT, int KT, int min_per, unsigned long long* red,
                                        int tol = 0, int fix = 0) {

@@ -979,7 +979,12 @@ static PtPlan pt_plan(int B, int Hq, int Hkv, int D, int N, int share) {
     return 0;
   };
   const int one = parts(1, sms), two = parts(2, sms);
-  // a 64-key step takes 1.0 us for a pair and 0.8 for a single tile, whose merge is 2 us shorter
+  // Single tiles merge half the rows, 2 us less, but read K and V once for each: a 64-key step of 64 CTAs
+  // takes 0.75 us, of 128 1.0, a pair's 0.8.  32 heads over 8, single / pair: 64 nodes (8 parts either
+  // way) over 512 tokens 10.4 / 12.4 us, 2048 12.8 / 14.7, 8192 24.8 / 24.1, 32768 73.5 / 64.0; 128 nodes
+  // (4 parts or 8) 12.0 / 13.9, 16.0 / 17.0, 34.0 / 29.7, 107 / 83; 96 nodes (6 or 8) 11.6 / 13.6,
+  // 14.7 / 16.5, 28.9 / 29.3, 87.6 / 81.6.  Lengths are not known here: the rule goes by short ranges
+  // where the parts are nearly as many, and gives long ones up to 15 %
   p.tiles = one >= 2 && one * 4 >= two * 3 ? 1 : 2;
   p.splits = p.tiles == 1 ? one : two;
   p.MP = (row_tiles + p.tiles - 1) / p.tiles;
