@@ -231,8 +231,8 @@ def test_attention_refuses_an_output_over_its_queries():
 
 # ---- a share of the device
 
-def _grids(call):
-    """CTAs of each kernel that a call launches, asked of the driver."""
+def _grids(call, fit=False):
+    """CTAs of each kernel that a call launches, asked of the driver; with fit and how many an SM holds."""
     graph = torch.cuda.CUDAGraph(keep_graph=True)
     with torch.cuda.graph(graph):
         call()
@@ -245,9 +245,22 @@ def _grids(call):
     for node in nodes:
         kind, params = ctypes.c_int(-1), (ctypes.c_uint32 * 64)()
         assert cuda.cuGraphNodeGetType(ctypes.c_void_p(node), ctypes.byref(kind)) == 0
-        if kind.value == 0:  # a kernel: function, grid, block, ...
-            assert cuda.cuGraphKernelNodeGetParams_v2(ctypes.c_void_p(node), params) == 0
-            out.append(params[2] * params[3] * params[4])
+        if kind.value != 0:
+            continue
+        # a kernel: function, grid, block, shared memory, arguments, extra, kernel
+        assert cuda.cuGraphKernelNodeGetParams_v2(ctypes.c_void_p(node), params) == 0
+        ctas = params[2] * params[3] * params[4]
+        if fit:
+            func = ctypes.c_void_p(params[0] | params[1] << 32)
+            if not func.value:
+                kern = ctypes.c_void_p(params[14] | params[15] << 32)
+                assert cuda.cuKernelGetFunction(ctypes.byref(func), kern) == 0
+            n = ctypes.c_int(0)
+            assert cuda.cuOccupancyMaxActiveBlocksPerMultiprocessor(ctypes.byref(n), func, params[5] * params[6] * params[7],
+                                                                    ctypes.c_size_t(params[8])) == 0
+            out.append((ctas, n.value))
+        else:
+            out.append(ctas)
     return out
 
 
@@ -328,3 +341,22 @@ def test_a_sequence_without_rows_may_have_any_length(Hkv, N, bf16):
         tv.append_kv_paged(k, k, *pool, i32(table), i32(prefix), n_rows=rows, dev_status=st)
         torch.cuda.synchronize()
         assert int(st.item()) == (tv.TV_DEV_BAD_PAGE if idle < 0 else 0), idle
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("B,Hq,Hkv,D,N", [(40, 8, 8, 256, 1), (40, 32, 8, 256, 2), (40, 64, 8, 128, 1), (40, 64, 8, 128, 2),
+                                          (40, 32, 8, 96, 4), (40, 16, 8, 64, 20), (40, 16, 8, 160, 20), (3, 16, 2, 256, 2)])
+def test_a_share_holds_every_cta_at_once(B, Hq, Hkv, D, N, bf16):
+    # by the driver's count of the CTAs that fit on an SM
+    dt = torch.bfloat16 if bf16 else torch.float32
+    x = [torch.randn(s, device=dev()).to(dt) for s in ((B, Hq, N, D), (20, Hkv, 16, D), (20, Hkv, 16, D))]
+    table, pre = i32(np.stack([np.arange(20) for _ in range(B)])), i32([300 - N - b for b in range(B)])
+    out, st = torch.zeros_like(x[0]), _status()
+    ws = torch.zeros(tv.paged_attention_workspace_size(B, Hq, Hkv, D, N, 16, 20, dt), dtype=torch.uint8, device=dev())
+    try:
+        for share in (9, 60):
+            tv.set_sm_partition(0, share)
+            for ctas, fit in _grids(lambda: tv.paged_attention(*x, table, pre, out=out, workspace=ws, dev_status=st), True):
+                assert fit >= 1 and ctas <= share * fit, (share, ctas, fit)
+    finally:
+        tv.set_sm_partition(0, 0)

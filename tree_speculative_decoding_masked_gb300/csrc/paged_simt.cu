@@ -37,6 +37,10 @@ struct PsSmem {
   static constexpr int kOffVis = kOffP + kRT * kPsKeys * 4;
   static constexpr int kOffPar = kOffVis + kRT * (kMaxNodes / 32) * 4;
   static constexpr int kBytes = kOffPar + kMaxNodes * 4;
+  // CTAs that an SM's 228 KB hold, with 1 KB each of the system's: the grid has no more, so that a share
+  // of the device keeps to its SMs
+  static constexpr int kStatic = 4608;
+  static constexpr int kPerSm = kDPL <= 4 && 2 * (kBytes + kStatic + 1024) <= 228 * 1024 ? 2 : 1;
 };
 
 // Output of a unit's rows from its parts, in CTA order; a warp per row.
@@ -89,7 +93,7 @@ __device__ __forceinline__ void ps_merge(const PagedAttn& a, int b, int hk, int 
 }
 
 template <int kDPL, int kRPW>
-__global__ void __launch_bounds__(kPsWarps * 32, kDPL <= 4 ? 2 : 1) paged_simt_kernel(PagedAttn a) {
+__global__ void __launch_bounds__(kPsWarps * 32, PsSmem<kDPL, kRPW>::kPerSm) paged_simt_kernel(PagedAttn a) {
   using S = PsSmem<kDPL, kRPW>;
   constexpr int kD = S::kD, kRT = S::kRT, kVec = 4;
   extern __shared__ __align__(16) unsigned char ps_smem[];
@@ -101,6 +105,7 @@ __global__ void __launch_bounds__(kPsWarps * 32, kDPL <= 4 ? 2 : 1) paged_simt_k
   int* s_par = reinterpret_cast<int*>(ps_smem + S::kOffPar);
   __shared__ unsigned long long s_red[kPagedRed];
   __shared__ int s_first_pad, s_last, s_depth[kRT], s_page[4][kPsKeys / 8];
+  static_assert(sizeof(s_red) + sizeof(s_depth) + sizeof(s_page) + 8 <= S::kStatic, "static arrays");
   const int box_shift = min(a.page_shift, 5), pages_tile = kPsKeys >> box_shift;  // a tile's row pieces, each in one page
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float* q = reinterpret_cast<const float*>(a.q);
@@ -577,7 +582,7 @@ static cudaError_t launch_ps(PagedAttn a, char* ws, cudaStream_t stream) {
   a.cnt = reinterpret_cast<unsigned*>(ws);
   a.ws_ml = reinterpret_cast<float2*>(ws + kPagedCntBytes);
   a.ws_o = reinterpret_cast<float*>(ws + kPagedCntBytes + kPsRows * 8);
-  return launch_pdl(paged_simt_kernel<kDPL, kRPW>, dim3((unsigned)(a.sms * kPagedMaxCtas)),
+  return launch_pdl(paged_simt_kernel<kDPL, kRPW>, dim3((unsigned)(a.sms * S::kPerSm)),
                     dim3(kPsWarps * 32), S::kBytes, stream, nullptr, 0, a);
 }
 
