@@ -625,7 +625,8 @@ TV_API tv_status tv_append_kv_paged(const tv_rows* k, const tv_rows* v, const tv
  * softcap <= 256, by 2^-13.  Limits: 32 <= D <= 256, D % 32 == 0, Hq % Hkv == 0,
  * 1 <= N <= 65536 (trees 1024), G * N < 2^24.  q, out and the caches 16-byte aligned.
  * Workspace: tv_paged_attention_workspace_size(...) bytes, 16-byte aligned, zero-filled
- * once, enough under any tv_set_sm_partition; calls that share it must not overlap on the GPU.
+ * once (and again after a call that set TV_DEV_TIMEOUT), enough under any tv_set_sm_partition;
+ * calls that share it must not overlap on the GPU.
  * Errors: as tv_tree_attention; scale, softcap < 0 or not finite, scale / softcap beyond fp32,
  * window < 0, out over q -> TV_ERR_VALUE; workspace missing or small -> TV_ERR_WORKSPACE.
  */
