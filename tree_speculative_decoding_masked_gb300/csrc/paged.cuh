@@ -14,16 +14,19 @@
 namespace tv {
 
 // New rows of sequence b that the call looks at: n_rows[b] (N without n_rows), or 0 for a sequence with a
-// row that does not fit its page table (*bad).  A padded tree's inactive rows need no place: where the
-// table ends at one, the rows in front of it count.
+// row that does not fit its page table (*bad).  A padded tree's inactive rows need no place: its rows
+// count up to the table's end, and paged_cut looks at the first behind it.
 __device__ __forceinline__ int paged_rows(const PagedAttn& a, int b, int P, bool* bad) {
-  const int n = a.n_rows ? a.n_rows[b] : a.N;
-  *bad = P < 0 || n < 0 || n > a.N;
-  if (*bad) return 0;
-  const long long room = ((long long)a.max_pages << a.page_shift) - P;
-  if (n <= room || n == 0) return n;  // without rows any length will do
-  *bad = !a.parent || room < 1 || a.parent[(size_t)b * a.N + room] != -1;
-  return *bad ? 0 : (int)room;
+  const int n = a.n_rows ? a.n_rows[b] : a.N, room = max((a.max_pages << a.page_shift) - max(P, 0), 0);
+  const int m = a.parent ? min(n, room) : n;
+  const bool fits = P >= 0 && n >= 0 && n <= a.N && m <= room && (m > 0 || n == 0);
+  *bad = !fits;
+  return fits ? m : 0;
+}
+// Whether the table's end cuts off an active row of a tree.
+__device__ __forceinline__ bool paged_cut(const PagedAttn& a, int b, int P, int n) {
+  return a.parent && n > 0 && P + n == a.max_pages << a.page_shift && n < (a.n_rows ? a.n_rows[b] : a.N) &&
+         a.parent[(size_t)b * a.N + n] != -1;
 }
 
 // One CTA's share of the attention work.  The work is cut into units (sequence b, KV head,
@@ -33,7 +36,7 @@ __device__ __forceinline__ int paged_rows(const PagedAttn& a, int b, int P, bool
 // r / G, so that a row tile spans few nodes and its key range ends at its last one.
 struct PagedSpan {
   long long W;      // key tiles in all
-  long long per;    // tiles per CTA, at least 1
+  long long per;    // tiles per CTA
   int b;            // where this CTA starts: sequence,
   long long base;   // and that sequence's first tile
   int whole;        // not 0: every unit counts as this many tiles, one unit per CTA
@@ -94,7 +97,7 @@ __device__ inline PagedSpan paged_span(const PagedAttn& a, int RT, int KT, int m
         const int P = a.prefix_len[b0 + k];
         bool bad = false;
         const int n = paged_rows(a, b0 + k, P, &bad);
-        any_bad |= bad;
+        any_bad |= bad || paged_cut(a, b0 + k, P, n);
         const long long head = head_tiles_warp(a, P, n, RT, KT, sp.whole, fix);
         if ((threadIdx.x & 31) == 0) red[34 + k] = (unsigned long long)head;
       }
@@ -104,7 +107,7 @@ __device__ inline PagedSpan paged_span(const PagedAttn& a, int RT, int KT, int m
       const int P = a.prefix_len[b];
       bool bad = false;
       const int n = paged_rows(a, b, P, &bad);
-      any_bad |= bad;
+      any_bad |= bad || paged_cut(a, b, P, n);
       for (int rt = 0; rt * RT < n * a.G; ++rt) t += sp.whole ? sp.whole : unit_tiles(a, P, n, rt, RT, KT) + fix;
       t *= a.Hkv;
     }
@@ -138,7 +141,7 @@ __device__ inline PagedSpan paged_span(const PagedAttn& a, int RT, int KT, int m
     __syncthreads();
     longest = red[0];
     __syncthreads();
-    if (all > 0 && all <= gridDim.x && longest + fix <= (unsigned long long)(sp.per + min(sp.per / 4 + 8, 30ll))) {
+    if (all <= gridDim.x && longest + fix <= (unsigned long long)(sp.per + min(sp.per / 4 + 8, 30ll))) {
       sp.whole = (int)longest;
       sp.per = sp.whole;
       W = all * longest;
@@ -218,7 +221,7 @@ __device__ __forceinline__ UnitCtas unit_ctas(const UnitWalk& w) {
 }
 __device__ __forceinline__ UnitWalk unit_walk(const PagedSpan& sp) {
   UnitWalk w{};
-  w.per = sp.per;
+  w.per = max(1ll, sp.per);  // sp.per: 0 where no row is active
   w.pos = sp.per * blockIdx.x;
   w.end = min(sp.W, w.pos + sp.per);
   w.seq = sp.base;

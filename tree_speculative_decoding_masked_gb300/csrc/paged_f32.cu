@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kPfThreads, kD <= 64 ? 2 : 1)
     w.P = a.prefix_len[w.b];
     w.n = paged_rows(a, w.b, w.P, &bad);
     if (w.n == 0) w.P = 0;
-    if (bad && threadIdx.x == 0) set_dev_status(a.dev_status, TV_DEV_BAD_PAGE);
+    if (threadIdx.x == 0 && (bad || paged_cut(a, w.b, w.P, w.n))) set_dev_status(a.dev_status, TV_DEV_BAD_PAGE);
     const int T_u = unit_tiles(a, w.P, w.n, w.rt, kPfRows, kPfKeys), part = blockIdx.x;
     w.t0 = (int)((long long)T_u * part / splits);
     w.t1 = (int)((long long)T_u * (part + 1) / splits);

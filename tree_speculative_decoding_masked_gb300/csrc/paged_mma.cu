@@ -112,7 +112,7 @@ __device__ __forceinline__ bool pm_next(const PagedAttn& a, UnitWalk& w, int spl
   w.P = a.prefix_len[w.b];
   w.n = paged_rows(a, w.b, w.P, &bad);
   if (w.n == 0) w.P = 0;
-  if (bad) set_dev_status(a.dev_status, TV_DEV_BAD_PAGE);
+  if (threadIdx.x == 0 && (bad || paged_cut(a, w.b, w.P, w.n))) set_dev_status(a.dev_status, TV_DEV_BAD_PAGE);
   const int T_u = unit_tiles(a, w.P, w.n, w.rt, kRT, kPmKeys), part = blockIdx.x;
   w.t0 = (int)((long long)T_u * part / splits);
   w.t1 = (int)((long long)T_u * (part + 1) / splits);

@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         pc.P = a.prefix_len[b];
         pc.n = paged_rows(a, b, pc.P, &bad);
         if (pc.n == 0) pc.P = 0;
-        if (bad && threadIdx.x == 0) set_dev_status(a.dev_status, TV_DEV_BAD_PAGE);
+        if (threadIdx.x == 0 && (bad || paged_cut(a, b, pc.P, pc.n))) set_dev_status(a.dev_status, TV_DEV_BAD_PAGE);
       }
       const int n = pc.n;
       n_act = n;
