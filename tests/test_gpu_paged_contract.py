@@ -117,6 +117,15 @@ def test_large_caps_cost_no_precision(Hq, Hkv, D, N, softcap, bf16):
 
 
 @pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("softcap,std", [(300.0, 8.0), (300.0, 16.0), (1000.0, 16.0), (1e4, 40.0)])
+@pytest.mark.parametrize("Hq,Hkv,D,N", [(8, 2, 128, 1), (8, 2, 64, 70), (2, 1, 256, 20), (8, 2, 128, 130)])
+def test_scores_that_a_large_cap_bends(Hq, Hkv, D, N, softcap, std, bf16):
+    # some scores below 0.45 of the cap, some past it
+    g = synth.rng(4230 + D + N)
+    assert _capped(g, 2, Hq, Hkv, D, 16, [50, 133], N, softcap, std, bf16) <= 1.0
+
+
+@pytest.mark.parametrize("bf16", [True, False])
 @pytest.mark.parametrize("softcap", [1e4, 1e8])
 @pytest.mark.parametrize("N", [1, 11])
 @pytest.mark.parametrize("D", [64, 128, 256])
