@@ -649,8 +649,21 @@ __global__ void __launch_bounds__(kPtThreads, 1)
 #pragma unroll
           for (int j = 0; j < 64; j += 4) soft_tanh4(sv + j, ck);
         } else if constexpr (kCap == kLargeCap) {
+          // nearly all scores lie below 0.45 of such a cap; where one does not, the tile is read again
+          float z_max = 0.f;
 #pragma unroll
-          for (int j = 0; j < 64; ++j) sv[j] = capped_score(sv[j] * a.scale, a.cap, ck);
+          for (int j = 0; j < 64; ++j) {
+            const float t = sv[j] * a.scale, x = t * ck, z = x * x;
+            z_max = fmaxf(z_max, z);
+            sv[j] = fmaf(t * z, tanh_tail(z), t);
+          }
+          if (__any_sync(0xffffffffu, z_max >= kTanhNear)) {
+            ptx::tmem_ld32(colS + buf * kPtKeys, sv);
+            ptx::tmem_ld32(colS + buf * kPtKeys + 32, sv + 32);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 64; ++j) sv[j] = capped_score(sv[j] * a.scale, a.cap, ck);
+          }
         }
         if (vis != ~0ull) {
 #pragma unroll
