@@ -801,7 +801,7 @@ def paged_attention(q, k_cache, v_cache, page_table, prefix_len, *, parent=None,
     caps scores by softcap * tanh(score / softcap); window > 0 hides keys `window` or more
     positions back.  workspace: paged_attention_workspace_size bytes, zero-filled once and
     kept between calls (omitted, it is allocated and zero-filled at each, which takes some
-    15 us; its size is checked by the library).  out: other storage than q's."""
+    20 us; its size is checked by the library).  out: other storage than q's."""
     index = _device_index("q", q)
     kv, B, Hkv, ps, width, D = _paged_kv(k_cache, v_cache, page_table, prefix_len, index)
     if q.ndim != 4:
