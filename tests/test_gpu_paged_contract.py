@@ -241,7 +241,7 @@ def test_attention_refuses_an_output_over_its_queries():
 # ---- a share of the device
 
 def _grids(call, fit=False):
-    """CTAs of each kernel that a call launches, asked of the driver; with fit and how many an SM holds."""
+    """CTAs of each kernel that a call launches, asked of libcuda; with fit and how many an SM holds."""
     graph = torch.cuda.CUDAGraph(keep_graph=True)
     with torch.cuda.graph(graph):
         call()
@@ -356,7 +356,7 @@ def test_a_sequence_without_rows_may_have_any_length(Hkv, N, bf16):
 @pytest.mark.parametrize("B,Hq,Hkv,D,N", [(40, 8, 8, 256, 1), (40, 32, 8, 256, 2), (40, 64, 8, 128, 1), (40, 64, 8, 128, 2),
                                           (40, 32, 8, 96, 4), (40, 16, 8, 64, 20), (40, 16, 8, 160, 20), (3, 16, 2, 256, 2)])
 def test_a_share_holds_every_cta_at_once(B, Hq, Hkv, D, N, bf16):
-    # by the driver's count of the CTAs that fit on an SM
+    # by libcuda's count of the CTAs that fit on an SM
     dt = torch.bfloat16 if bf16 else torch.float32
     x = [torch.randn(s, device=dev()).to(dt) for s in ((B, Hq, N, D), (20, Hkv, 16, D), (20, Hkv, 16, D))]
     table, pre = i32(np.stack([np.arange(20) for _ in range(B)])), i32([300 - N - b for b in range(B)])
