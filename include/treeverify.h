@@ -17,6 +17,9 @@
  *   tv_append_kv_paged  new keys (rotated) and values into the pages, queries rotated
  *   tv_paged_attention  causal or tree-masked attention of the new rows over the pages
  *   tv_commit_accepted_kv_paged  tv_commit_accepted_kv through the page table
+ *   tv_norm_rotary / tv_norm_append_kv_paged  the first two with a norm of every query and key
+ *   tv_append_kv_paged_q8, tv_paged_attention_q8, tv_commit_accepted_kv_paged_q8  the round
+ *                       over pages that are held in 8 bits, tv_read_kv_paged_q8 reads them back
  *
  * Conventions shared by every call
  *   - Every pointer argument is a DEVICE pointer owned by the caller, unless marked
@@ -568,6 +571,25 @@ TV_API tv_status tv_rotary(const tv_rows* x, void* out, const int32_t* pos, cons
                            const tv_rope* rope, int B, int H, int N, int D, tv_dtype dtype,
                            tv_stream_t stream);
 
+/* Host struct, read during the call.  A norm of every head: x -> w x / sqrt(mean of x^2 + eps),
+ * the mean over the head's D elements; fp32 arithmetic, not rounded before the rotation. */
+typedef struct tv_head_norm {
+  const void* q_weight; /* device, [D] of the call's dtype; needed where there are queries */
+  const void* k_weight; /* likewise for keys */
+  float eps;            /* >= 0, finite */
+} tv_head_norm;
+
+/* tv_norm_rotary - tv_rotary with norm->q_weight's norm of every head before the rotation.
+ *   rope NULL: the norm alone; pos may then be NULL too (no row is padding)
+ * 16-byte columns need D / 16 (bf16) or D / 8 (fp32) to be a power of two up to 32 and an aligned
+ * weight besides; other calls take a slower kernel.
+ * Errors as tv_rotary, and: NULL norm or q_weight -> TV_ERR_NULL; eps < 0 or not finite ->
+ * TV_ERR_VALUE; a weight not aligned to its element -> TV_ERR_ALIGN.
+ */
+TV_API tv_status tv_norm_rotary(const tv_rows* x, void* out, const int32_t* pos, const int32_t* pos_base,
+                                const tv_head_norm* norm, const tv_rope* rope, int B, int H, int N, int D,
+                                tv_dtype dtype, tv_stream_t stream);
+
 /* ------------------------------------------------------------------------------------
  * Paged caches.  k, v: [num_pages][Hkv][page_size][D]; cache row r of sequence b is row
  * r mod page_size of page page_table[b][r / page_size].  prefix_len[b] = P_b rows are
@@ -607,6 +629,15 @@ TV_API tv_status tv_append_kv_paged(const tv_rows* k, const tv_rows* v, const tv
                                     const int32_t* depth, const int32_t* n_rows, const tv_rope* rope,
                                     const tv_rows* q, void* q_out, int B, int Hq, int Hkv, int N, int D,
                                     tv_dtype dtype, int32_t* dev_status, tv_stream_t stream);
+
+/* tv_norm_append_kv_paged - tv_append_kv_paged with a norm of every query and key before its
+ * rotation (rope NULL: the norm alone).
+ * Errors as there and as tv_norm_rotary; NULL k_weight -> TV_ERR_NULL.
+ */
+TV_API tv_status tv_norm_append_kv_paged(const tv_rows* k, const tv_rows* v, const tv_paged_kv* kv,
+                                         const int32_t* depth, const int32_t* n_rows, const tv_head_norm* norm,
+                                         const tv_rope* rope, const tv_rows* q, void* q_out, int B, int Hq, int Hkv,
+                                         int N, int D, tv_dtype dtype, int32_t* dev_status, tv_stream_t stream);
 
 /* tv_paged_attention - attention of the new rows over the paged cache (blog, "why target
  * verification can be parallel"; PTD §3.1 for the tree mask).
@@ -650,6 +681,76 @@ TV_API tv_status tv_commit_accepted_kv_paged(const tv_paged_kv* kv, const int32_
                                              const int32_t* accept_len, int32_t* new_len, int B, int Hkv,
                                              int N, int D, tv_dtype dtype, int32_t* dev_status,
                                              tv_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Paged caches in 8 bits.  k, v of tv_paged_kv hold e4m3 codes (1 sign, 4 exponent and 3 mantissa
+ * bits, bias 7, up to 448, no infinity), one byte an element.  Of each page and KV head, `block`
+ * rows in turn share a scale 2^(s - 127), held as the byte s; a cached number is code * 2^(s - 127),
+ * which bf16 holds exactly.  block: a power of two, 1..64, at most page_size.  D: a multiple of
+ * 32, 32..256.  B <= 65535.  The rest is as for other paged caches.
+ *
+ * Scales as the append writes them are 2^-117 or more (the codes' smallest step is then a normal
+ * bf16 number); other writers may use any s in 10..254.  A block that holds rows which a call needs must have
+ * such a scale, one that holds none may have any.
+ */
+typedef struct tv_kv_scale { /* host struct, read during the call */
+  uint8_t* k; /* device, [num_pages][Hkv][page_size / block] */
+  uint8_t* v;
+  int block;
+} tv_kv_scale;
+
+/* tv_append_kv_paged_q8 - tv_append_kv_paged (with norm: tv_norm_append_kv_paged) into pages in 8
+ * bits.  The rows are k, v, q of dtype as there; q_out is of dtype too.
+ * A block that receives rows takes the smallest scale of at least 2^-117 under which none of
+ * them exceeds 448.  A block that begins with committed rows (before P_b) keeps at least the scale it has,
+ * and where that grows the codes of those rows are written anew: the same numbers, but those that
+ * fall below 2^-6 of the new scale, which are rounded to its multiples of 2^-9.  Codes are
+ * the nearest to the turned (fp32) number, ties to even; what is not finite becomes NaN and does not
+ * count for the scale.  No other byte of the cache is written.
+ * A block that receives rows, or whose committed rows are written anew, may belong to one
+ * sequence of the call only.
+ * Errors as tv_append_kv_paged and tv_norm_rotary, and: NULL scale or arrays -> TV_ERR_NULL;
+ * block, D or B -> TV_ERR_SHAPE.
+ */
+TV_API tv_status tv_append_kv_paged_q8(const tv_rows* k, const tv_rows* v, const tv_paged_kv* kv,
+                                       const tv_kv_scale* scale, const int32_t* depth, const int32_t* n_rows,
+                                       const tv_head_norm* norm, const tv_rope* rope, const tv_rows* q, void* q_out,
+                                       int B, int Hq, int Hkv, int N, int D, tv_dtype dtype, int32_t* dev_status,
+                                       tv_stream_t stream);
+
+/* tv_read_kv_paged_q8 - the numbers of cache rows, as dtype.
+ *   k_out, v_out  [B][Hkv][rows][D] dtype, 16-byte aligned: row r holds cache row first[b] + r
+ *   first         [B] int32, or NULL: 0.  Only rows before prefix_len[b] are read; the output rows of
+ *                 others are not written
+ * Errors as the append's; a negative first or length, or a page outside the pool ->
+ * TV_DEV_BAD_PAGE.  No workspace.
+ */
+TV_API tv_status tv_read_kv_paged_q8(const tv_paged_kv* kv, const tv_kv_scale* scale, const int32_t* first,
+                                     void* k_out, void* v_out, int B, int Hkv, int rows, int D, tv_dtype dtype,
+                                     int32_t* dev_status, tv_stream_t stream);
+
+/* tv_paged_attention_q8 - tv_paged_attention over pages in 8 bits; q and out are of dtype.
+ * Precision as there, the cached numbers taken as they are.  Limits, workspace (of
+ * tv_paged_attention_q8_workspace_size bytes) and errors as there, and those of kv_scale.
+ */
+TV_API size_t tv_paged_attention_q8_workspace_size(int B, int Hq, int Hkv, int D, int N, int page_size,
+                                                   int max_pages, tv_dtype dtype);
+TV_API tv_status tv_paged_attention_q8(const void* q, void* out, const tv_paged_kv* kv,
+                                       const tv_kv_scale* kv_scale, const int32_t* parent, const int32_t* n_rows,
+                                       int B, int Hq, int Hkv, int N, int D, float scale, float softcap, int window,
+                                       tv_dtype dtype, void* workspace, size_t ws_bytes, int32_t* dev_status,
+                                       tv_stream_t stream);
+
+/* tv_commit_accepted_kv_paged_q8 - tv_commit_accepted_kv_paged over pages in 8 bits.  A block that
+ * receives rows takes the largest of its own scale and those of the blocks they come from; its
+ * rows up to P_b + L_b are written anew for a larger scale, as the append does.  Rows behind P_b +
+ * L_b are left as they are, and no longer count.
+ * Errors as there, and those of scale.
+ */
+TV_API tv_status tv_commit_accepted_kv_paged_q8(const tv_paged_kv* kv, const tv_kv_scale* scale,
+                                                const int32_t* accepted_nodes, const int32_t* accept_len,
+                                                int32_t* new_len, int B, int Hkv, int N, int D, int32_t* dev_status,
+                                                tv_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -45,10 +45,12 @@ _U64 = ctypes.c_uint64
 _D = ctypes.c_double
 
 
-# host structs of the paged calls, packed: tv_rope, tv_rows, tv_paged_kv
+# host structs of the paged calls, packed: tv_rope, tv_rows, tv_paged_kv, tv_head_norm, tv_kv_scale
 _pack_rope = struct.Struct("@Piif0q").pack
 _pack_rows = struct.Struct("@Pqqq").pack
 _pack_paged_kv = struct.Struct("@PPPPiii0q").pack
+_pack_norm = struct.Struct("@PPf0q").pack
+_pack_scale = struct.Struct("@PPi0q").pack
 
 _SIGS = {
     "tv_status_string": (ctypes.c_char_p, [_I]),
@@ -80,6 +82,13 @@ _SIGS = {
     "tv_paged_attention_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I, _I]),
     "tv_paged_attention": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _F, _I, _I, _P, _SZ, _P, _P]),
     "tv_commit_accepted_kv_paged": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P]),
+    "tv_norm_rotary": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P]),
+    "tv_norm_append_kv_paged": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P]),
+    "tv_append_kv_paged_q8": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P]),
+    "tv_read_kv_paged_q8": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P]),
+    "tv_paged_attention_q8_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I, _I]),
+    "tv_paged_attention_q8": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _F, _I, _I, _P, _SZ, _P, _P]),
+    "tv_commit_accepted_kv_paged_q8": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P]),
     "tv_select_subtree_adaptive": (_I, [_P, _P, _I, _I, _I, _I, _F, _F, _P, _P, _P, _P, _P, _P, _P, _SZ, _P, _P]),
 }
 
@@ -724,6 +733,32 @@ def rotary(x, pos, rope, *, interleaved: bool = False, pos_base=None, out=None):
     return out
 
 
+def norm_rotary(x, weight, pos, rope, *, eps: float = 1e-6, interleaved: bool = False, pos_base=None, out=None):
+    """rotary of rows x [B][H][N][D] that are first normed: each head over its root mean square,
+    times weight [D] (of x's dtype), x -> weight x / sqrt(mean of x^2 + eps).  rope None: the norm
+    alone (pos may then be None)."""
+    index = _device_index("x", x)
+    if x.ndim != 4:
+        _ndim("x", x, 4)
+    B, H, N, D = shape = tuple(x.shape)
+    dtype = x.dtype
+    code = _dtype_code(x)
+    rows = _rows("x", x, dtype, shape, index)
+    norm = _pack_norm(_tensor("weight", weight, dtype, (D,), index), 0, eps)
+    if rope is not None and pos is None:
+        raise ValueError("pos is required with rope")
+    pos_p = _tensor("pos", pos, torch.int32, (B, N), index)
+    base_p = _tensor("pos_base", pos_base, torch.int32, (B,), index)
+    packed = None if rope is None else _rope(rope, interleaved, index)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=x.device)
+    out_p = _tensor("out", out, dtype, shape, index)
+    if out_p == x.data_ptr() and not x.is_contiguous():
+        raise ValueError("x must be contiguous to be rotated in place")
+    _launch("tv_norm_rotary", index, rows, out_p, pos_p, base_p, norm, packed, B, H, N, D, code)
+    return out
+
+
 def _paged_kv(k_cache, v_cache, page_table, prefix_len, index):
     """(tv_paged_kv, B, Hkv, page_size, max_pages, D) of the checked tensors."""
     if k_cache.ndim != 4:
@@ -748,20 +783,50 @@ def _paged_kv(k_cache, v_cache, page_table, prefix_len, index):
     return kv, B, Hkv, ps, width, D
 
 
+_SCALE_TYPES = (torch.uint8, torch.float8_e8m0fnu)
+
+
+def _scales(k_cache, k_scale, v_scale, index):
+    """tv_kv_scale of an 8-bit cache's scales [num_pages][Hkv][page_size / block]; None for other caches."""
+    if k_cache.dtype is not torch.float8_e4m3fn:
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("k_scale and v_scale belong to caches of torch.float8_e4m3fn")
+        return None
+    if k_scale is None or v_scale is None:
+        raise ValueError("caches of torch.float8_e4m3fn need k_scale and v_scale")
+    if k_scale.dtype not in _SCALE_TYPES or k_scale.ndim != 3:
+        raise ValueError("k_scale must be torch.uint8 or torch.float8_e8m0fnu [num_pages][Hkv][page_size / block]")
+    pages, Hkv, ps, _ = k_cache.shape
+    blocks = k_scale.shape[2]
+    if blocks < 1 or ps % blocks:
+        raise ValueError(f"k_scale has {blocks} blocks a page of {ps} rows")
+    shape = (pages, Hkv, blocks)
+    dtype = k_scale.dtype
+    return _pack_scale(_tensor("k_scale", k_scale, dtype, shape, index), _tensor("v_scale", v_scale, dtype, shape, index),
+                       ps // blocks)
+
+
 def append_kv_paged(k, v, k_cache, v_cache, page_table, prefix_len, *, depth=None, n_rows=None, rope=None,
-                    interleaved: bool = False, q=None, q_out=None, dev_status=None):
+                    interleaved: bool = False, q=None, q_out=None, dev_status=None, norm=None, k_scale=None,
+                    v_scale=None):
     """Write new rows k, v [B][Hkv][N][D] (any strides, contiguous elements) into the paged
     caches [num_pages][Hkv][page_size][D] at cache rows prefix_len[b] + t, the keys rotated
     (with rope) at position prefix_len[b] + depth[b][t] (depth: tree_prep's; a row of negative
     depth is not written; omitted: t).  page_table [B][max_pages], prefix_len [B], n_rows [B] (omitted: N each) are
-    int32.  With q [B][Hq][N][D] its rows are rotated too, into q_out (returned)."""
+    int32.  With q [B][Hq][N][D] its rows are rotated too, into q_out (returned).  norm =
+    (q_weight, k_weight, eps): queries and keys are normed first, as by norm_rotary (q_weight may
+    be None without q).  Caches of torch.float8_e4m3fn are written in 8 bits, with k_scale and
+    v_scale [num_pages][Hkv][page_size / block] (uint8 or float8_e8m0fnu): a block takes the scale
+    that its rows need, 2^(byte - 127); a block that begins with committed rows keeps at least
+    theirs, and where it grows their codes are written anew."""
     index = _device_index("k_cache", k_cache)
     kv, B, Hkv, _, _, D = _paged_kv(k_cache, v_cache, page_table, prefix_len, index)
     if k.ndim != 4:
         _ndim("k", k, 4)
     N = k.shape[2]
-    dtype = k_cache.dtype
-    code = _dtype_code(k_cache)
+    scale = _scales(k_cache, k_scale, v_scale, index)
+    dtype = k_cache.dtype if scale is None else k.dtype
+    code = _dtype_code(k_cache if scale is None else k)
     shape = (B, Hkv, N, D)
     k_rows = _rows("k", k, dtype, shape, index)
     v_rows = _rows("v", v, dtype, shape, index)
@@ -770,7 +835,7 @@ def append_kv_paged(k, v, k_cache, v_cache, page_table, prefix_len, *, depth=Non
     q_rows = out_p = None
     Hq = 0
     if q is not None:
-        if rope is None:
+        if rope is None and norm is None:
             raise ValueError("q is rotated: rope is required with it")
         if q.ndim != 4:
             _ndim("q", q, 4)
@@ -783,32 +848,84 @@ def append_kv_paged(k, v, k_cache, v_cache, page_table, prefix_len, *, depth=Non
         if out_p == q.data_ptr() and not q.is_contiguous():
             raise ValueError("q must be contiguous to be rotated in place")
     st = _status(dev_status, index)
-    _launch("tv_append_kv_paged", index, k_rows, v_rows, kv, depth_p, rows_p,
-            None if rope is None else _rope(rope, interleaved, index), q_rows, out_p, B, Hq, Hkv, N, D, code, st.data_ptr())
+    packed = None if rope is None else _rope(rope, interleaved, index)
+    if norm is not None:
+        q_weight, k_weight, eps = norm
+        norm = _pack_norm(_tensor("q_weight", q_weight, dtype, (D,), index) or 0,
+                          _tensor("k_weight", k_weight, dtype, (D,), index) or 0, eps)
+    if scale is not None:
+        _launch("tv_append_kv_paged_q8", index, k_rows, v_rows, kv, scale, depth_p, rows_p, norm, packed, q_rows, out_p,
+                B, Hq, Hkv, N, D, code, st.data_ptr())
+    elif norm is not None:
+        _launch("tv_norm_append_kv_paged", index, k_rows, v_rows, kv, depth_p, rows_p, norm, packed, q_rows, out_p, B,
+                Hq, Hkv, N, D, code, st.data_ptr())
+    else:
+        _launch("tv_append_kv_paged", index, k_rows, v_rows, kv, depth_p, rows_p, packed, q_rows, out_p, B, Hq, Hkv, N,
+                D, code, st.data_ptr())
     return q_out if q is not None else None
 
 
-def paged_attention_workspace_size(B, Hq, Hkv, D, N, page_size, max_pages, dtype) -> int:
+def read_kv_paged(k_cache, v_cache, page_table, length, k_scale, v_scale, *, first=None, rows=None,
+                  dtype=torch.bfloat16, k_out=None, v_out=None, dev_status=None):
+    """The numbers of an 8-bit paged cache (append_kv_paged with scales): (k, v), each
+    [B][Hkv][rows][D] of dtype (bf16: exactly), row r holding cache row first[b] + r (first [B]
+    int32, omitted: 0).  Rows from length[b] (int32) on are not written.  rows: k_out's, else
+    what the page table spans."""
+    index = _device_index("k_cache", k_cache)
+    kv, B, Hkv, ps, width, D = _paged_kv(k_cache, v_cache, page_table, length, index)
+    scale = _scales(k_cache, k_scale, v_scale, index)
+    if scale is None:
+        raise ValueError("read_kv_paged reads caches of torch.float8_e4m3fn")
+    if k_out is not None:
+        if k_out.ndim != 4:
+            _ndim("k_out", k_out, 4)
+        dtype = k_out.dtype
+        if rows is None:
+            rows = k_out.shape[2]
+    elif rows is None:
+        rows = ps * width
+    shape = (B, Hkv, int(rows), D)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dtype, device=k_cache.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=dtype, device=k_cache.device)
+    first_p = _tensor("first", first, torch.int32, (B,), index)
+    k_p, v_p = _tensor("k_out", k_out, dtype, shape, index), _tensor("v_out", v_out, dtype, shape, index)
+    st = _status(dev_status, index)
+    _launch("tv_read_kv_paged_q8", index, kv, scale, first_p, k_p, v_p, B, Hkv, int(rows), D, _dtype_code(k_out),
+            st.data_ptr())
+    return k_out, v_out
+
+
+def paged_attention_workspace_size(B, Hq, Hkv, D, N, page_size, max_pages, dtype, *, cache_dtype=None) -> int:
+    """Bytes for paged_attention of queries of dtype; cache_dtype=torch.float8_e4m3fn: over an 8-bit cache."""
     code = TV_BF16 if dtype == torch.bfloat16 else TV_F32
-    return int(load_library().tv_paged_attention_workspace_size(B, Hq, Hkv, D, N, page_size, max_pages, code))
+    lib = load_library()
+    if cache_dtype == torch.float8_e4m3fn:
+        return int(lib.tv_paged_attention_q8_workspace_size(B, Hq, Hkv, D, N, page_size, max_pages, code))
+    return int(lib.tv_paged_attention_workspace_size(B, Hq, Hkv, D, N, page_size, max_pages, code))
 
 
 def paged_attention(q, k_cache, v_cache, page_table, prefix_len, *, parent=None, n_rows=None, scale: float = 0.0,
-                    softcap: float = 0.0, window: int = 0, out=None, workspace=None, dev_status=None):
+                    softcap: float = 0.0, window: int = 0, out=None, workspace=None, dev_status=None, k_scale=None,
+                    v_scale=None):
     """Attention of new rows q [B][Hq][N][D] over paged caches [num_pages][Hkv][page_size][D]
     that already hold their keys and values (append_kv_paged): causal, or tree-masked with
     parent [B][N].  page_table [B][max_pages], prefix_len [B], n_rows [B] int32.  softcap > 0
     caps scores by softcap * tanh(score / softcap); window > 0 hides keys `window` or more
     positions back.  workspace: paged_attention_workspace_size bytes, zero-filled once and
     kept between calls (omitted, it is allocated and zero-filled at each, which takes some
-    20 us; its size is checked by the library).  out: other storage than q's."""
+    20 us; its size is checked by the library).  out: other storage than q's.  Caches of
+    torch.float8_e4m3fn come with k_scale and v_scale, as append_kv_paged writes them (workspace:
+    the query's with cache_dtype)."""
     index = _device_index("q", q)
     kv, B, Hkv, ps, width, D = _paged_kv(k_cache, v_cache, page_table, prefix_len, index)
     if q.ndim != 4:
         _ndim("q", q, 4)
     _, Hq, N, _ = q.shape
-    dtype = k_cache.dtype
-    code = _dtype_code(k_cache)
+    kv_scale = _scales(k_cache, k_scale, v_scale, index)
+    dtype = k_cache.dtype if kv_scale is None else q.dtype
+    code = _dtype_code(k_cache if kv_scale is None else q)
     shape = (B, Hq, N, D)
     q_p = _tensor("q", q, dtype, shape, index)
     parent_p = _tensor("parent", parent, torch.int32, (B, N), index)
@@ -818,25 +935,33 @@ def paged_attention(q, k_cache, v_cache, page_table, prefix_len, *, parent=None,
     out_p = _tensor("out", out, dtype, shape, index)
     st = _status(dev_status, index)
     if workspace is None:
+        lib = load_library()
+        size = lib.tv_paged_attention_workspace_size if kv_scale is None else lib.tv_paged_attention_q8_workspace_size
         with torch.cuda.device(index):
-            n = load_library().tv_paged_attention_workspace_size(B, Hq, Hkv, D, N, ps, width, code)
+            n = size(B, Hq, Hkv, D, N, ps, width, code)
         workspace = torch.zeros(max(int(n), 256), dtype=torch.uint8, device=index)
     elif workspace.get_device() != index:
         _wrong_device("workspace", workspace, index)
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    _launch("tv_paged_attention", index, q_p, out_p, kv, parent_p, rows_p, B, Hq, Hkv, N, D, scale, softcap, int(window),
-            code, workspace.data_ptr(), workspace.numel() * workspace.element_size(), st.data_ptr())
+    if kv_scale is None:
+        _launch("tv_paged_attention", index, q_p, out_p, kv, parent_p, rows_p, B, Hq, Hkv, N, D, scale, softcap,
+                int(window), code, workspace.data_ptr(), workspace.numel() * workspace.element_size(), st.data_ptr())
+    else:
+        _launch("tv_paged_attention_q8", index, q_p, out_p, kv, kv_scale, parent_p, rows_p, B, Hq, Hkv, N, D, scale,
+                softcap, int(window), code, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                st.data_ptr())
     return out
 
 
 def commit_accepted_kv_paged(k_cache, v_cache, page_table, prefix_len, accepted_nodes, accept_len, *, new_len=None,
-                             dev_status=None):
+                             dev_status=None, k_scale=None, v_scale=None):
     """commit_accepted_kv over paged caches [num_pages][Hkv][page_size][D], in place: rows
     prefix_len[b] + a_k move to prefix_len[b] + k.  accepted_nodes [B][N], accept_len [B] as
     returned by verify_greedy / verify_sample.  Returns new_len [B] int32, the sequences'
     committed rows after the round (prefix_len + accept_len + 1): storage of its own, none of
-    the call's other tensors."""
+    the call's other tensors.  Caches of torch.float8_e4m3fn come with k_scale and v_scale: a
+    block that receives rows takes the largest scale of what it then holds."""
     index = _device_index("k_cache", k_cache)
     kv, B, Hkv, _, _, D = _paged_kv(k_cache, v_cache, page_table, prefix_len, index)
     if accepted_nodes.ndim != 2:
@@ -848,6 +973,10 @@ def commit_accepted_kv_paged(k_cache, v_cache, page_table, prefix_len, accepted_
         new_len = torch.empty(B, dtype=torch.int32, device=k_cache.device)
     new_p = _tensor("new_len", new_len, torch.int32, (B,), index)
     st = _status(dev_status, index)
-    _launch("tv_commit_accepted_kv_paged", index, kv, nodes_p, len_p, new_p, B, Hkv, N, D, _dtype_code(k_cache),
-            st.data_ptr())
+    scale = _scales(k_cache, k_scale, v_scale, index)
+    if scale is None:
+        _launch("tv_commit_accepted_kv_paged", index, kv, nodes_p, len_p, new_p, B, Hkv, N, D, _dtype_code(k_cache),
+                st.data_ptr())
+    else:
+        _launch("tv_commit_accepted_kv_paged_q8", index, kv, scale, nodes_p, len_p, new_p, B, Hkv, N, D, st.data_ptr())
     return new_len

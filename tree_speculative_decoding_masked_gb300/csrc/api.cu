@@ -6,6 +6,7 @@
 
 #include <nvtx3/nvToolsExt.h>
 
+#include "q8.cuh"
 #include "tv_kernels.cuh"
 
 using namespace tv;
@@ -383,6 +384,41 @@ tv_status tv_rotary(const tv_rows* x, void* out, const int32_t* pos, const int32
   return cuda_status(launch_rotary(a, dtype, st(stream)));
 }
 
+static tv_status norm_checks(const tv_head_norm* norm, bool q, bool k, tv_dtype dtype) {
+  if ((q && !norm->q_weight) || (k && !norm->k_weight)) return TV_ERR_NULL;
+  if (!(norm->eps >= 0.f) || isinf(norm->eps)) return TV_ERR_VALUE;
+  for (const void* w : {norm->q_weight, norm->k_weight})
+    if (reinterpret_cast<uintptr_t>(w) % (dtype == TV_BF16 ? 2 : 4)) return TV_ERR_ALIGN;
+  return TV_OK;
+}
+
+tv_status tv_norm_rotary(const tv_rows* x, void* out, const int32_t* pos, const int32_t* pos_base,
+                         const tv_head_norm* norm, const tv_rope* rope, int B, int H, int N, int D, tv_dtype dtype,
+                         tv_stream_t stream) {
+  NvtxRange nvtx_range("tv_norm_rotary");
+  if (!x || !x->data || !out || !norm) return TV_ERR_NULL;
+  if (rope && !pos) return TV_ERR_NULL;
+  if (!valid_dtype(dtype)) return TV_ERR_DTYPE;
+  if (B < 1 || H < 1 || H > kMaxRotaryHeads || N < 1 || D < 1 || D > kMaxRotaryDim) return TV_ERR_SHAPE;
+  if ((long long)B * N > kMaxRotaryRows) return TV_ERR_SHAPE;
+  tv_status s = norm_checks(norm, true, false, dtype);
+  if (s == TV_OK && rope) s = rope_checks(rope, D);
+  if (s != TV_OK) return s;
+  if (!rows_aligned(x, dtype) || reinterpret_cast<uintptr_t>(out) % (dtype == TV_BF16 ? 2 : 4)) return TV_ERR_ALIGN;
+  RotaryArgs a{};
+  rows_arg(&a, 0, x);
+  a.q_out = out;
+  a.pos = pos;
+  a.base = pos_base;
+  a.weight[0] = norm->q_weight;
+  a.eps = norm->eps;
+  a.freq = rope ? rope->freq : nullptr;
+  a.amplitude = rope ? rope->amplitude : 1.f;
+  a.B = B, a.Hq = H, a.N = N, a.D = D;
+  a.rot = rope ? rope->rot_dim : 0, a.interleaved = rope && rope->interleaved != 0;
+  return cuda_status(launch_rotary(a, dtype, st(stream)));
+}
+
 static bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + b_bytes && y < x + a_bytes;
@@ -394,8 +430,8 @@ static int log2_exact(int x) {
   return s;
 }
 
-// The checks that every call over a paged cache shares.
-static tv_status paged_checks(const tv_paged_kv* kv, int B, int Hkv, int N, int D, tv_dtype dtype) {
+// The checks that every call over a paged cache shares; elt: bytes of a cache element.
+static tv_status pool_checks(const tv_paged_kv* kv, int B, int Hkv, int N, int D, tv_dtype dtype, int elt) {
   if (!kv || !kv->k || !kv->v || !kv->page_table || !kv->prefix_len) return TV_ERR_NULL;
   if (!valid_dtype(dtype)) return TV_ERR_DTYPE;
   if (B < 1 || Hkv < 1 || Hkv > kMaxRotaryHeads || N < 1 || D < 1 || D > kMaxRotaryDim) return TV_ERR_SHAPE;
@@ -403,22 +439,42 @@ static tv_status paged_checks(const tv_paged_kv* kv, int B, int Hkv, int N, int 
   if (ps < 8 || ps > 1024 || (ps & (ps - 1)) || kv->num_pages < 1 || kv->max_pages < 1) return TV_ERR_SHAPE;
   if ((long long)kv->max_pages * ps > (1LL << 30) || (long long)kv->num_pages * Hkv > 0x7fffffffLL)
     return TV_ERR_SHAPE;
-  if (!aligned16(kv->k) || !aligned16(kv->v) || (long long)D * (dtype == TV_BF16 ? 2 : 4) % 16) return TV_ERR_ALIGN;
+  if (!aligned16(kv->k) || !aligned16(kv->v) || (long long)D * elt % 16) return TV_ERR_ALIGN;
   return TV_OK;
 }
+static tv_status paged_checks(const tv_paged_kv* kv, int B, int Hkv, int N, int D, tv_dtype dtype) {
+  return pool_checks(kv, B, Hkv, N, D, dtype, dtype == TV_BF16 ? 2 : 4);
+}
+// and those over one in 8 bits
+static tv_status q8_checks(const tv_paged_kv* kv, const tv_kv_scale* scale, int B, int Hkv, int N, int D,
+                           tv_dtype dtype) {
+  if (!scale || !scale->k || !scale->v) return TV_ERR_NULL;
+  const tv_status s = pool_checks(kv, B, Hkv, N, D, dtype, 1);
+  if (s != TV_OK && s != TV_ERR_ALIGN) return s;
+  if (D < 32 || D > 256 || D % 32 || B > 65535) return TV_ERR_SHAPE;
+  const int blk = scale->block;
+  if (blk < 1 || blk > kQ8MaxBlock || (blk & (blk - 1)) || blk > kv->page_size) return TV_ERR_SHAPE;
+  return s;
+}
+static Q8Pages q8_pages(const tv_kv_scale* scale) { return {scale->k, scale->v, log2_exact(scale->block), 0}; }
 
-tv_status tv_append_kv_paged(const tv_rows* k, const tv_rows* v, const tv_paged_kv* kv, const int32_t* depth,
-                             const int32_t* n_rows, const tv_rope* rope, const tv_rows* q, void* q_out, int B, int Hq,
-                             int Hkv, int N, int D, tv_dtype dtype, int32_t* dev_status, tv_stream_t stream) {
-  NvtxRange nvtx_range("tv_append_kv_paged");
+// What the appends share: scale NULL for pages of dtype, norm NULL for none.
+static tv_status append(const tv_rows* k, const tv_rows* v, const tv_paged_kv* kv, const tv_kv_scale* scale, bool q8,
+                        const int32_t* depth, const int32_t* n_rows, const tv_head_norm* norm, const tv_rope* rope,
+                        const tv_rows* q, void* q_out, int B, int Hq, int Hkv, int N, int D, tv_dtype dtype,
+                        int32_t* dev_status, tv_stream_t stream) {
   if (!k || !k->data || !v || !v->data) return TV_ERR_NULL;
-  if (q && (!q->data || !q_out || !rope)) return TV_ERR_NULL;
-  tv_status s = paged_checks(kv, B, Hkv, N, D, dtype);
+  if (q && (!q->data || !q_out || (!rope && !norm))) return TV_ERR_NULL;
+  tv_status s = q8 ? q8_checks(kv, scale, B, Hkv, N, D, dtype) : paged_checks(kv, B, Hkv, N, D, dtype);
   if (s != TV_OK) return s;
   if (q && (Hq < 1 || Hq > kMaxRotaryHeads)) return TV_ERR_SHAPE;
   if ((long long)B * N > kMaxRotaryRows) return TV_ERR_SHAPE;
   if (rope) {
     s = rope_checks(rope, D);
+    if (s != TV_OK) return s;
+  }
+  if (norm) {
+    s = norm_checks(norm, q != nullptr, true, dtype);
     if (s != TV_OK) return s;
   }
   if (!rows_aligned(k, dtype) || !rows_aligned(v, dtype)) return TV_ERR_ALIGN;
@@ -437,11 +493,61 @@ tv_status tv_append_kv_paged(const tv_rows* k, const tv_rows* v, const tv_paged_
   a.table = kv->page_table;
   a.freq = rope ? rope->freq : nullptr;
   a.amplitude = rope ? rope->amplitude : 1.f;
+  if (norm) a.weight[0] = norm->q_weight, a.weight[1] = norm->k_weight, a.eps = norm->eps;
   a.B = B, a.Hq = q ? Hq : 0, a.Hkv = Hkv, a.N = N, a.D = D;
   a.rot = rope ? rope->rot_dim : 0, a.interleaved = rope && rope->interleaved != 0;
   a.num_pages = kv->num_pages, a.page_shift = log2_exact(kv->page_size), a.max_pages = kv->max_pages;
   a.dev_status = dev_status;
+  if (q8) return cuda_status(launch_q8_append(a, q8_pages(scale), dtype, st(stream)));
   return cuda_status(launch_rotary(a, dtype, st(stream)));
+}
+
+tv_status tv_append_kv_paged(const tv_rows* k, const tv_rows* v, const tv_paged_kv* kv, const int32_t* depth,
+                             const int32_t* n_rows, const tv_rope* rope, const tv_rows* q, void* q_out, int B, int Hq,
+                             int Hkv, int N, int D, tv_dtype dtype, int32_t* dev_status, tv_stream_t stream) {
+  NvtxRange nvtx_range("tv_append_kv_paged");
+  return append(k, v, kv, nullptr, false, depth, n_rows, nullptr, rope, q, q_out, B, Hq, Hkv, N, D, dtype, dev_status,
+                stream);
+}
+
+tv_status tv_norm_append_kv_paged(const tv_rows* k, const tv_rows* v, const tv_paged_kv* kv, const int32_t* depth,
+                                  const int32_t* n_rows, const tv_head_norm* norm, const tv_rope* rope,
+                                  const tv_rows* q, void* q_out, int B, int Hq, int Hkv, int N, int D, tv_dtype dtype,
+                                  int32_t* dev_status, tv_stream_t stream) {
+  NvtxRange nvtx_range("tv_norm_append_kv_paged");
+  if (!norm) return TV_ERR_NULL;
+  return append(k, v, kv, nullptr, false, depth, n_rows, norm, rope, q, q_out, B, Hq, Hkv, N, D, dtype, dev_status,
+                stream);
+}
+
+tv_status tv_append_kv_paged_q8(const tv_rows* k, const tv_rows* v, const tv_paged_kv* kv, const tv_kv_scale* scale,
+                                const int32_t* depth, const int32_t* n_rows, const tv_head_norm* norm,
+                                const tv_rope* rope, const tv_rows* q, void* q_out, int B, int Hq, int Hkv, int N,
+                                int D, tv_dtype dtype, int32_t* dev_status, tv_stream_t stream) {
+  NvtxRange nvtx_range("tv_append_kv_paged_q8");
+  return append(k, v, kv, scale, true, depth, n_rows, norm, rope, q, q_out, B, Hq, Hkv, N, D, dtype, dev_status,
+                stream);
+}
+
+tv_status tv_read_kv_paged_q8(const tv_paged_kv* kv, const tv_kv_scale* scale, const int32_t* first, void* k_out,
+                              void* v_out, int B, int Hkv, int rows, int D, tv_dtype dtype, int32_t* dev_status,
+                              tv_stream_t stream) {
+  NvtxRange nvtx_range("tv_read_kv_paged_q8");
+  if (!k_out || !v_out) return TV_ERR_NULL;
+  const tv_status s = q8_checks(kv, scale, B, Hkv, rows, D, dtype);
+  if (s != TV_OK) return s;
+  if (Hkv > 65535) return TV_ERR_SHAPE;
+  if (!aligned16(k_out) || !aligned16(v_out)) return TV_ERR_ALIGN;
+  Q8Read a{};
+  a.k = reinterpret_cast<const unsigned char*>(kv->k), a.v = reinterpret_cast<const unsigned char*>(kv->v);
+  a.ks = scale->k, a.vs = scale->v;
+  a.table = kv->page_table, a.first = first, a.length = kv->prefix_len;
+  a.k_out = k_out, a.v_out = v_out;
+  a.B = B, a.Hkv = Hkv, a.D = D, a.rows = rows;
+  a.num_pages = kv->num_pages, a.page_shift = log2_exact(kv->page_size), a.max_pages = kv->max_pages;
+  a.block_shift = log2_exact(scale->block);
+  a.dev_status = dev_status;
+  return cuda_status(launch_q8_read(a, dtype, st(stream)));
 }
 
 static bool paged_attn_shape(int B, int Hq, int Hkv, int N, int D) {
@@ -455,13 +561,13 @@ size_t tv_paged_attention_workspace_size(int B, int Hq, int Hkv, int D, int N, i
   return paged_attn_ws(B, Hq, Hkv, D, N, dtype, paged_grid_sms()).bytes;
 }
 
-tv_status tv_paged_attention(const void* q, void* out, const tv_paged_kv* kv, const int32_t* parent,
-                             const int32_t* n_rows, int B, int Hq, int Hkv, int N, int D, float scale, float softcap,
-                             int window, tv_dtype dtype, void* workspace, size_t ws_bytes, int32_t* dev_status,
-                             tv_stream_t stream) {
-  NvtxRange nvtx_range("tv_paged_attention");
+// scale NULL and q8 false: pages of dtype.
+static tv_status attention(const void* q, void* out, const tv_paged_kv* kv, const tv_kv_scale* kv_scale, bool q8,
+                           const int32_t* parent, const int32_t* n_rows, int B, int Hq, int Hkv, int N, int D,
+                           float scale, float softcap, int window, tv_dtype dtype, void* workspace, size_t ws_bytes,
+                           int32_t* dev_status, tv_stream_t stream) {
   if (!q || !out) return TV_ERR_NULL;
-  const tv_status s = paged_checks(kv, B, Hkv, N, D, dtype);
+  const tv_status s = q8 ? q8_checks(kv, kv_scale, B, Hkv, N, D, dtype) : paged_checks(kv, B, Hkv, N, D, dtype);
   if (s != TV_OK) return s;
   if (!paged_attn_shape(B, Hq, Hkv, N, D) || (parent && N > kMaxNodes)) return TV_ERR_SHAPE;
   if (!(scale >= 0.f) || isinf(scale) || !(softcap >= 0.f) || isinf(softcap) || window < 0) return TV_ERR_VALUE;
@@ -469,7 +575,7 @@ tv_status tv_paged_attention(const void* q, void* out, const tv_paged_kv* kv, co
   if (softcap > 0.f && isinf(4.f * scale / softcap)) return TV_ERR_VALUE;
   if (!aligned16(q) || !aligned16(out)) return TV_ERR_ALIGN;
   const int sms = paged_grid_sms();  // read once: the schedule and its workspace go by it
-  const size_t need = paged_attn_ws(B, Hq, Hkv, D, N, dtype, sms).need;
+  const size_t need = (q8 ? paged_q8_attn_ws(B, Hq, Hkv, D, N, dtype, sms) : paged_attn_ws(B, Hq, Hkv, D, N, dtype, sms)).need;
   if (need && (!workspace || ws_bytes < need)) return TV_ERR_WORKSPACE;
   if (!aligned16(workspace)) return TV_ERR_ALIGN;
   const size_t rows_bytes = (size_t)B * Hq * N * D * (dtype == TV_BF16 ? 2 : 4);
@@ -484,7 +590,42 @@ tv_status tv_paged_attention(const void* q, void* out, const tv_paged_kv* kv, co
   a.window = window;
   a.sms = sms;
   a.dev_status = dev_status;
-  return cuda_status(launch_paged_attn(a, dtype, reinterpret_cast<char*>(workspace), st(stream)));
+  char* ws = reinterpret_cast<char*>(workspace);
+  if (!q8) return cuda_status(launch_paged_attn(a, dtype, ws, st(stream)));
+  a.ks = kv_scale->k, a.vs = kv_scale->v, a.block_shift = log2_exact(kv_scale->block);
+  return cuda_status(launch_paged_q8_attn(a, dtype, ws, st(stream)));
+}
+
+tv_status tv_paged_attention(const void* q, void* out, const tv_paged_kv* kv, const int32_t* parent,
+                             const int32_t* n_rows, int B, int Hq, int Hkv, int N, int D, float scale, float softcap,
+                             int window, tv_dtype dtype, void* workspace, size_t ws_bytes, int32_t* dev_status,
+                             tv_stream_t stream) {
+  NvtxRange nvtx_range("tv_paged_attention");
+  return attention(q, out, kv, nullptr, false, parent, n_rows, B, Hq, Hkv, N, D, scale, softcap, window, dtype,
+                   workspace, ws_bytes, dev_status, stream);
+}
+
+size_t tv_paged_attention_q8_workspace_size(int B, int Hq, int Hkv, int D, int N, int page_size, int max_pages,
+                                            tv_dtype dtype) {
+  if (!paged_attn_shape(B, Hq, Hkv, N, D) || page_size < 8 || max_pages < 1 || !valid_dtype(dtype)) return 0;
+  return paged_q8_attn_ws(B, Hq, Hkv, D, N, dtype, paged_grid_sms()).bytes;
+}
+
+tv_status tv_paged_attention_q8(const void* q, void* out, const tv_paged_kv* kv, const tv_kv_scale* kv_scale,
+                                const int32_t* parent, const int32_t* n_rows, int B, int Hq, int Hkv, int N, int D,
+                                float scale, float softcap, int window, tv_dtype dtype, void* workspace,
+                                size_t ws_bytes, int32_t* dev_status, tv_stream_t stream) {
+  NvtxRange nvtx_range("tv_paged_attention_q8");
+  return attention(q, out, kv, kv_scale, true, parent, n_rows, B, Hq, Hkv, N, D, scale, softcap, window, dtype,
+                   workspace, ws_bytes, dev_status, stream);
+}
+
+// A sequence's CTAs read these while its first one writes new_len.
+static bool new_len_clear(const int32_t* new_len, const tv_paged_kv* kv, const int32_t* nodes, const int32_t* len,
+                          int B, int N) {
+  const size_t b4 = (size_t)B * 4;
+  return !new_len || !(overlap(new_len, b4, kv->prefix_len, b4) || overlap(new_len, b4, len, b4) ||
+                       overlap(new_len, b4, nodes, b4 * N) || overlap(new_len, b4, kv->page_table, b4 * kv->max_pages));
 }
 
 tv_status tv_commit_accepted_kv_paged(const tv_paged_kv* kv, const int32_t* accepted_nodes, const int32_t* accept_len,
@@ -495,14 +636,24 @@ tv_status tv_commit_accepted_kv_paged(const tv_paged_kv* kv, const int32_t* acce
   const tv_status s = paged_checks(kv, B, Hkv, N, D, dtype);
   if (s != TV_OK) return s;
   if (N > kMaxNodes || B > 65535) return TV_ERR_SHAPE;
-  // a sequence's CTAs read these while its first one writes new_len
-  const size_t b4 = (size_t)B * 4;
-  if (new_len && (overlap(new_len, b4, kv->prefix_len, b4) || overlap(new_len, b4, accept_len, b4) ||
-                  overlap(new_len, b4, accepted_nodes, b4 * N) || overlap(new_len, b4, kv->page_table, b4 * kv->max_pages)))
-    return TV_ERR_VALUE;
+  if (!new_len_clear(new_len, kv, accepted_nodes, accept_len, B, N)) return TV_ERR_VALUE;
   return cuda_status(launch_kv_commit_paged(kv->k, kv->v, kv->page_table, kv->prefix_len, accepted_nodes, accept_len,
                                             new_len, B, Hkv, D, N, kv->num_pages, log2_exact(kv->page_size),
                                             kv->max_pages, dtype, dev_status, st(stream)));
+}
+
+tv_status tv_commit_accepted_kv_paged_q8(const tv_paged_kv* kv, const tv_kv_scale* scale,
+                                         const int32_t* accepted_nodes, const int32_t* accept_len, int32_t* new_len,
+                                         int B, int Hkv, int N, int D, int32_t* dev_status, tv_stream_t stream) {
+  NvtxRange nvtx_range("tv_commit_accepted_kv_paged_q8");
+  if (!accepted_nodes || !accept_len) return TV_ERR_NULL;
+  const tv_status s = q8_checks(kv, scale, B, Hkv, N, D, TV_BF16);
+  if (s != TV_OK) return s;
+  if (N > kMaxNodes) return TV_ERR_SHAPE;
+  if (!new_len_clear(new_len, kv, accepted_nodes, accept_len, B, N)) return TV_ERR_VALUE;
+  return cuda_status(launch_q8_commit(kv->k, kv->v, q8_pages(scale), kv->page_table, kv->prefix_len, accepted_nodes,
+                                      accept_len, new_len, B, Hkv, D, N, kv->num_pages, log2_exact(kv->page_size),
+                                      kv->max_pages, dev_status, st(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,73 @@
+// Paged caches held in 8 bits: e4m3 codes, and for each KV head a block of 2^block_shift rows of a
+// page shares one scale 2^(s - 127), held as the byte s.  A cached number is code * 2^(s - 127).
+//
+// Powers of two, because then a block that takes a larger scale can code its rows anew by moving
+// their exponents, without a rounding but where a code falls below e4m3's normal numbers, and a
+// cached number is a bf16 number exactly, which is what the attention's products take.  e4m3 is a
+// floating format: a scale off by up to 2 costs no precision, as it would with integer codes.
+#pragma once
+
+#include "tv_common.cuh"
+
+namespace tv {
+
+// Smallest scale exponent that is written: the codes' smallest step, 2^-9, then stands for a normal
+// number in 32 bits and in bf16.
+constexpr int kQ8Least = -117;
+constexpr int kQ8MaxBlock = 64;  // rows that share a scale
+
+// 2^e for e in -149..127 (0 below, infinite above)
+__device__ __forceinline__ float q8_two(int e) {
+  if (e < -126) return e < -149 ? 0.f : __uint_as_float(1u << (e + 149));
+  return e > 127 ? INFINITY : __uint_as_float((uint32_t)(e + 127) << 23);
+}
+// the number that a scale byte stands for; 255 is no number
+__device__ __forceinline__ float q8_scale(unsigned s) { return s == 255u ? __uint_as_float(0x7fffffffu) : q8_two((int)s - 127); }
+
+// The smallest e >= kQ8Least with amax <= 448 * 2^e, amax >= 0 and finite: 448 = 1.75 * 2^8.
+__device__ __forceinline__ int q8_exponent(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  const int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u);
+  return max(e, kQ8Least);
+}
+
+// two numbers to e4m3 (nearest, ties to even), `lo` in the low byte; what is not finite becomes NaN
+__device__ __forceinline__ uint32_t q8_code2(float lo, float hi) {
+  const float big = 3.4028234e38f;
+  lo = fabsf(lo) <= big ? lo : __uint_as_float(0x7fffffffu);
+  hi = fabsf(hi) <= big ? hi : __uint_as_float(0x7fffffffu);
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// two codes to f16x2, exact
+__device__ __forceinline__ uint32_t q8_half2(uint16_t codes) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(codes));
+  return r;
+}
+__device__ __forceinline__ float q8_half_lo(uint32_t h) {
+  float f;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 %0, lo;\n\t}" : "=f"(f) : "r"(h));
+  return f;
+}
+__device__ __forceinline__ float q8_half_hi(uint32_t h) {
+  float f;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 %0, hi;\n\t}" : "=f"(f) : "r"(h));
+  return f;
+}
+// four codes times a scale
+__device__ __forceinline__ float4 q8_numbers(uint32_t w, float scale) {
+  const uint32_t a = q8_half2((uint16_t)w), b = q8_half2((uint16_t)(w >> 16));
+  return make_float4(q8_half_lo(a) * scale, q8_half_hi(a) * scale, q8_half_lo(b) * scale, q8_half_hi(b) * scale);
+}
+__device__ __forceinline__ uint32_t q8_code4(float a, float b, float c, float d) {
+  return q8_code2(a, b) | q8_code2(c, d) << 16;
+}
+// four codes under the scale 2^from, coded for 2^to >= 2^from
+__device__ __forceinline__ uint32_t q8_recode(uint32_t w, float ratio) {
+  const float4 f = q8_numbers(w, ratio);
+  return q8_code4(f.x, f.y, f.z, f.w);
+}
+
+}  // namespace tv

@@ -16,7 +16,7 @@
 // and 6 blocks 73.8; half as many groups 47.7, twice as many 56.2.  64 tokens: 2.7 us.
 #include <math.h>
 
-#include "paged.cuh"
+#include "rotary.cuh"
 
 namespace tv {
 
@@ -24,73 +24,13 @@ constexpr int kRotThreads = 256;
 constexpr int kRotHeads = 3;  // heads whose loads are in flight together
 constexpr long long kRotBlocks = 152 * 16;  // blocks up to which a token's heads go to separate ones
 
-// kVec contiguous elements in one load or store
-template <typename T, int kVec>
-struct RotRaw {
-  using type = uint4;
-};
-template <typename T>
-struct RotRaw<T, 1> {
-  using type = T;
-};
-template <typename T, int kVec>
-__device__ __forceinline__ void rot_unpack(const typename RotRaw<T, kVec>::type& r, float (&f)[kVec]) {
-  if constexpr (kVec == 1) {
-    if constexpr (sizeof(T) == 2)
-      f[0] = bf16_to_f32(r);
-    else
-      f[0] = r;
-  } else {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (sizeof(T) == 2) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      } else {
-        f[i] = __uint_as_float(w[i]);
-      }
-    }
-  }
-}
-template <typename T, int kVec>
-__device__ __forceinline__ typename RotRaw<T, kVec>::type rot_pack(const float (&f)[kVec]) {
-  if constexpr (kVec == 1) {
-    if constexpr (sizeof(T) == 2)
-      return (T)(ptx::cvt_bf16x2(f[0], 0.f) & 0xffffu);
-    else
-      return f[0];
-  } else if constexpr (sizeof(T) == 2) {
-    return make_uint4(ptx::cvt_bf16x2(f[0], f[1]), ptx::cvt_bf16x2(f[2], f[3]), ptx::cvt_bf16x2(f[4], f[5]),
-                      ptx::cvt_bf16x2(f[6], f[7]));
-  } else {
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-  }
-}
-
-// sin and cos of an angle in 2^-64 turns.  The nearest quarter turn goes exactly (integers);
-// what is left, at most pi / 4, goes through the Taylor polynomials of degree 9 and 8, off by
-// less than 2e-9 and 3e-8.
-__device__ __forceinline__ float2 sincos_turns(uint64_t turns) {
-  const uint32_t quarter = (uint32_t)((turns + (1ull << 61)) >> 62);
-  const float x = (float)(int32_t)((turns - ((uint64_t)quarter << 62)) >> 32) * 1.4629180792671596e-09f;  // 2 pi 2^-32
-  const float z = x * x;
-  float s = fmaf(z, 2.7557319e-6f, -1.9841270e-4f);  // 1 / 9!, -1 / 7!
-  s = fmaf(z, s, 8.3333333e-3f);
-  s = fmaf(z, s, -1.6666667e-1f);
-  s = fmaf(x * z, s, x);
-  float c = fmaf(z, 2.4801587e-5f, -1.3888889e-3f);  // 1 / 8!, -1 / 6!
-  c = fmaf(z, c, 4.1666667e-2f);
-  c = fmaf(z, c, -0.5f);
-  c = fmaf(z, c, 1.f);
-  const float sn = quarter & 1 ? c : s, cs = quarter & 1 ? s : c;
-  return make_float2(quarter & 2 ? -sn : sn, (quarter + 1) & 2 ? -cs : cs);
-}
-
 // Grid: x over (token, column) pairs, y over groups of `hg` of the Hq + 2 Hkv heads.  A column
 // is kVec pairs (rotated part) or up to 2 kVec elements behind it.
-template <typename T, int kVec>
-__global__ void __launch_bounds__(kRotThreads, 4) rotary_kernel(RotaryArgs a, int cols, int rot_cols, int hg) {
+// kNorm: queries and keys are first divided by their root mean square over the head and multiplied by a
+// weight, in 32 bits; the `cols` (a power of two up to 32) threads of a token are neighbours in a warp and
+// add up their squares by shuffles.
+template <typename T, int kVec, bool kNorm>
+__global__ void __launch_bounds__(kRotThreads, kNorm ? 3 : 4) rotary_kernel(RotaryArgs a, int cols, int rot_cols, int hg) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const long long id = (long long)blockIdx.x * kRotThreads + threadIdx.x;
@@ -98,29 +38,11 @@ __global__ void __launch_bounds__(kRotThreads, 4) rotary_kernel(RotaryArgs a, in
   if (token >= (long long)a.B * a.N) return;
   const int col = (int)(id - token * cols);
   const int b = (int)(token / a.N), t = (int)(token - (long long)b * a.N);
-  if (a.table && t == 0 && col == 0 && blockIdx.y == 0) {  // counts and lengths, also where no row is active
-    const int n = a.n_rows ? a.n_rows[b] : 0;
-    if (n < 0 || n > a.N || a.base[b] < 0) set_dev_status(a.dev_status, TV_DEV_BAD_PAGE);
-  }
-  const int off = a.pos ? a.pos[token] : t;
-  if (off < 0) return;  // padding
-  const int base = a.base ? a.base[b] : 0;
-  if (a.n_rows && (t >= a.n_rows[b] || a.n_rows[b] > a.N)) return;
-  const long long p = (long long)base + off;
   const int heads = a.Hq + 2 * a.Hkv;
   const int h0 = blockIdx.y * hg, h1 = min(heads, h0 + hg);
-  // where this token's row goes in a page
-  long long page_row = -1;
-  if (h1 > a.Hq) {
-    const long long r = (long long)base + t;
-    const long long pg = r >> a.page_shift;
-    const int page = base >= 0 && pg < a.max_pages ? a.table[(size_t)b * a.max_pages + pg] : -1;
-    if (page >= 0 && page < a.num_pages)
-      page_row = ((long long)page * a.Hkv << a.page_shift) + (r & ((1 << a.page_shift) - 1));
-    else
-      set_dev_status(a.dev_status, TV_DEV_BAD_PAGE);
-  }
-  if (p < 0) return;  // a negative base
+  const RotPlace at = rot_place(a, token, b, t, col == 0 && blockIdx.y == 0, h1 > a.Hq);
+  if (!at.live) return;
+  const long long p = at.pos, page_row = at.page_row;
   // this thread's elements: ea.. and eb.. (eb >= D: none)
   const bool turn = col < rot_cols;
   const bool pairs_inside = a.interleaved && kVec > 1;  // x and y hold kVec / 2 whole pairs each
@@ -157,6 +79,7 @@ __global__ void __launch_bounds__(kRotThreads, 4) rotary_kernel(RotaryArgs a, in
   };
   const bool two = eb < a.D;
   using Raw = typename RotRaw<T, kVec>::type;
+  const uint32_t peers = kNorm ? (cols == 32 ? ~0u : ((1u << cols) - 1u) << (threadIdx.x & 31 & -cols)) : 0u;
   for (int hb = h0; hb < h1; hb += kRotHeads) {
     // the batch's loads first: they are in flight together (a row may be rotated in place, so the
     // compiler would not move a load past an earlier head's store)
@@ -173,11 +96,18 @@ __global__ void __launch_bounds__(kRotThreads, 4) rotary_kernel(RotaryArgs a, in
       if (hb + u >= h1) break;
       T* dst = target(hb + u);
       if (!dst) continue;
-      if (turn && hb + u < a.Hq + a.Hkv) {
+      const bool normed = kNorm && hb + u < a.Hq + a.Hkv;
+      if (normed || (turn && hb + u < a.Hq + a.Hkv)) {
         float x[kVec], y[kVec];
         rot_unpack<T, kVec>(ra[u], x);
-        rot_unpack<T, kVec>(rb[u], y);
-        if (pairs_inside) {
+        if (turn || two) {
+          rot_unpack<T, kVec>(rb[u], y);
+        } else {
+#pragma unroll
+          for (int k = 0; k < kVec; ++k) y[k] = 0.f;
+        }
+        if constexpr (kNorm) rot_norm<T, kVec>(a, hb + u < a.Hq ? 0 : 1, ea, eb, two, cols, peers, x, y);
+        if (turn && pairs_inside) {
 #pragma unroll
           for (int k = 0; k < kVec / 2; ++k) {
             const float e0 = x[2 * k], o0 = x[2 * k + 1], e1 = y[2 * k], o1 = y[2 * k + 1];
@@ -186,7 +116,7 @@ __global__ void __launch_bounds__(kRotThreads, 4) rotary_kernel(RotaryArgs a, in
             y[2 * k] = e1 * cs[kVec / 2 + k] - o1 * sn[kVec / 2 + k];
             y[2 * k + 1] = o1 * cs[kVec / 2 + k] + e1 * sn[kVec / 2 + k];
           }
-        } else {
+        } else if (turn) {
 #pragma unroll
           for (int k = 0; k < kVec; ++k) {
             const float e = x[k], o = y[k];
@@ -204,7 +134,63 @@ __global__ void __launch_bounds__(kRotThreads, 4) rotary_kernel(RotaryArgs a, in
   }
 }
 
-template <typename T, int kVec>
+// The same with norms for heads and rows that rotary_kernel's columns do not fit (no power of two of
+// columns, or not 16 bytes each): a warp a row, an element and its pair partner a lane.
+template <typename T>
+__global__ void __launch_bounds__(kRotThreads) norm_rows_kernel(RotaryArgs a) {
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int lane = threadIdx.x & 31, heads = a.Hq + 2 * a.Hkv;
+  const long long token = (long long)blockIdx.x * (kRotThreads / 32) + (threadIdx.x >> 5);
+  if (token >= (long long)a.B * a.N) return;
+  const int b = (int)(token / a.N), t = (int)(token - (long long)b * a.N);
+  const RotPlace at = rot_place(a, token, b, t, lane == 0 && blockIdx.y == 0, a.Hkv > 0 && blockIdx.y >= a.Hq);
+  if (!at.live) return;
+  for (int h = blockIdx.y; h < heads; h += gridDim.y) {
+    const int part = h < a.Hq ? 0 : h < a.Hq + a.Hkv ? 1 : 2;
+    const int hh = part == 0 ? h : part == 1 ? h - a.Hq : h - a.Hq - a.Hkv;
+    if (part && at.page_row < 0) continue;
+    const T* src = reinterpret_cast<const T*>(a.src[part]) + b * a.sb[part] + hh * a.sh[part] + t * a.sn[part];
+    T* dst = part == 0 ? reinterpret_cast<T*>(a.q_out) + (((long long)b * a.Hq + h) * a.N + t) * a.D
+                       : reinterpret_cast<T*>(part == 1 ? a.k_cache : a.v_cache) +
+                             (at.page_row + ((long long)hh << a.page_shift)) * a.D;
+    if (part == 2) {
+      for (int d = lane; d < a.D; d += 32) dst[d] = src[d];
+      continue;
+    }
+    auto num = [](T v) -> float {
+      if constexpr (sizeof(T) == 2)
+        return bf16_to_f32(v);
+      else
+        return v;
+    };
+    auto put = [&](int d, float f) {
+      if constexpr (sizeof(T) == 2)
+        dst[d] = (T)(ptx::cvt_bf16x2(f, 0.f) & 0xffffu);
+      else
+        dst[d] = f;
+    };
+    float ss = 0.f;
+    for (int d = lane; d < a.D; d += 32) ss = fmaf(num(src[d]), num(src[d]), ss);
+    const float r = 1.f / sqrtf(warp_sum(ss) / a.D + a.eps);
+    const T* weight = reinterpret_cast<const T*>(a.weight[part]);
+    for (int i = lane; i < a.rot / 2 + (a.D - a.rot); i += 32) {
+      if (i >= a.rot / 2) {
+        const int d = i + a.rot / 2;
+        put(d, num(src[d]) * r * num(weight[d]));
+        continue;
+      }
+      const int d0 = a.interleaved ? 2 * i : i, d1 = a.interleaved ? 2 * i + 1 : i + a.rot / 2;
+      const float2 sc = sincos_turns((uint64_t)at.pos * a.freq[i]);
+      const float x = num(src[d0]) * r * num(weight[d0]), y = num(src[d1]) * r * num(weight[d1]);
+      const float c = sc.y * a.amplitude, s = sc.x * a.amplitude;
+      put(d0, x * c - y * s);
+      put(d1, y * c + x * s);
+    }
+  }
+}
+
+template <typename T, int kVec, bool kNorm>
 static cudaError_t launch_rot(const RotaryArgs& a, cudaStream_t stream) {
   const int rot_cols = a.rot / (2 * kVec);
   const int rest = a.D - a.rot;
@@ -216,7 +202,7 @@ static cudaError_t launch_rot(const RotaryArgs& a, cudaStream_t stream) {
   int hg = 1;
   while (hg < heads && blocks * ((heads + hg - 1) / hg) > kRotBlocks) hg *= 2;
   const dim3 grid((unsigned)blocks, (unsigned)((heads + hg - 1) / hg));
-  return launch_pdl(rotary_kernel<T, kVec>, grid, dim3(kRotThreads), 0, stream, nullptr, 0, a, cols, rot_cols, hg);
+  return launch_pdl(rotary_kernel<T, kVec, kNorm>, grid, dim3(kRotThreads), 0, stream, nullptr, 0, a, cols, rot_cols, hg);
 }
 
 cudaError_t launch_rotary(const RotaryArgs& a, tv_dtype dtype, cudaStream_t stream) {
@@ -230,8 +216,21 @@ cudaError_t launch_rotary(const RotaryArgs& a, tv_dtype dtype, cudaStream_t stre
              a.sn[i] % vec == 0;
   for (const void* p : {(const void*)a.q_out, (const void*)a.k_cache, (const void*)a.v_cache})
     wide = wide && reinterpret_cast<uintptr_t>(p) % 16 == 0;
-  if (dtype == TV_BF16) return wide ? launch_rot<uint16_t, 8>(a, stream) : launch_rot<uint16_t, 1>(a, stream);
-  return wide ? launch_rot<float, 4>(a, stream) : launch_rot<float, 1>(a, stream);
+  if (a.weight[0] || a.weight[1]) {
+    for (const void* p : a.weight) wide = wide && reinterpret_cast<uintptr_t>(p) % 16 == 0;
+    const int cols = a.D / (2 * vec);
+    // the columns of a head: a power of two up to a warp, none of them half empty
+    if (wide && a.D % (2 * vec) == 0 && cols <= 32 && (cols & (cols - 1)) == 0)
+      return dtype == TV_BF16 ? launch_rot<uint16_t, 8, true>(a, stream) : launch_rot<float, 4, true>(a, stream);
+    const long long blocks = ((long long)a.B * a.N + kRotThreads / 32 - 1) / (kRotThreads / 32);
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    const dim3 grid((unsigned)blocks, (unsigned)(a.Hq + 2 * a.Hkv));
+    return launch_pdl(dtype == TV_BF16 ? norm_rows_kernel<uint16_t> : norm_rows_kernel<float>, grid,
+                      dim3(kRotThreads), 0, stream, nullptr, 0, a);
+  }
+  if (dtype == TV_BF16)
+    return wide ? launch_rot<uint16_t, 8, false>(a, stream) : launch_rot<uint16_t, 1, false>(a, stream);
+  return wide ? launch_rot<float, 4, false>(a, stream) : launch_rot<float, 1, false>(a, stream);
 }
 
 // Frequencies in 2^-64 turns a position.  With r_i = base^(-2i/R) radians:

@@ -109,6 +109,9 @@ struct PagedAttn {
   int B, Hq, Hkv, G, D, N, num_pages, page_shift, max_pages;
   float scale, cap;  // cap 0: scores are not capped
   int window;        // 0: no window
+  const uint8_t* ks;  // 8-bit pages: the blocks' scales (q8.cuh)
+  const uint8_t* vs;
+  int block_shift;
   int sms;           // SMs that the call may take (host)
   float* ws_o;       // partial results of units shared by CTAs
   float2* ws_ml;
@@ -122,6 +125,9 @@ struct PagedWs {
 PagedWs paged_attn_ws(int B, int Hq, int Hkv, int D, int N, tv_dtype dtype, int sms);
 int paged_grid_sms();  // SMs that tv_set_sm_partition leaves paged attention
 cudaError_t launch_paged_attn(PagedAttn a, tv_dtype dtype, char* ws, cudaStream_t stream);
+// the same over 8-bit pages
+PagedWs paged_q8_attn_ws(int B, int Hq, int Hkv, int D, int N, tv_dtype dtype, int sms);
+cudaError_t launch_paged_q8_attn(PagedAttn a, tv_dtype dtype, char* ws, cudaStream_t stream);
 
 // ---- rotary positions and the paged append (Hq rows of q rotated into q_out, Hkv rows of k
 // rotated and of v copied into pages; any part may be absent)
@@ -137,11 +143,40 @@ struct RotaryArgs {
   const int32_t* table;
   const uint64_t* freq;
   float amplitude;
+  const void* weight[2];  // norm of q and of k, NULL: none
+  float eps;
   int B, Hq, Hkv, N, D, rot, interleaved;
   int num_pages, page_shift, max_pages;
   int32_t* dev_status;
 };
 cudaError_t launch_rotary(const RotaryArgs& a, tv_dtype dtype, cudaStream_t stream);
+// ---- paged caches in 8 bits (q8.cuh)
+struct Q8Pages {
+  uint8_t* ks;  // [num_pages][Hkv][page_size >> block_shift]
+  uint8_t* vs;
+  int block_shift;
+  int wide_out;  // q_out takes 16-byte stores
+};
+struct Q8Read {
+  const unsigned char* k;
+  const unsigned char* v;
+  const uint8_t* ks;
+  const uint8_t* vs;
+  const int32_t* table;
+  const int32_t* first;  // or NULL: 0
+  const int32_t* length;
+  void* k_out;
+  void* v_out;
+  int B, Hkv, D, rows, num_pages, page_shift, max_pages, block_shift;
+  int32_t* dev_status;
+};
+cudaError_t launch_q8_append(const RotaryArgs& a, const Q8Pages& p, tv_dtype dtype, cudaStream_t stream);
+cudaError_t launch_q8_read(const Q8Read& a, tv_dtype dtype, cudaStream_t stream);
+cudaError_t launch_q8_commit(void* k, void* v, const Q8Pages& p, const int32_t* table, const int32_t* prefix_len,
+                             const int32_t* accepted, const int32_t* accept_len, int32_t* new_len, int B, int Hkv,
+                             int D, int N, int num_pages, int page_shift, int max_pages, int32_t* dev_status,
+                             cudaStream_t stream);
+
 void rotary_frequencies(int rot, double base, int scaling, const double* params, uint64_t* freq, float* amplitude);
 cudaError_t launch_kv_commit_paged(void* k, void* v, const int32_t* table, const int32_t* prefix_len,
                                    const int32_t* accepted, const int32_t* accept_len, int32_t* new_len, int B,
