@@ -374,8 +374,15 @@ int paged_device_sms();
 bool paged_tc_takes(int Hq, int Hkv, int D, int N);
 PagedWs paged_tc_ws(int B, int Hq, int Hkv, int D, int N);
 cudaError_t launch_paged_tc(PagedAttn a, char* ws, cudaStream_t stream);
+cudaError_t launch_paged_q8_tc(PagedAttn a, char* ws, cudaStream_t stream);
+struct PtPlan {
+  int NT, tiles, MP, splits, grid;  // splits 0: persistent grid
+  size_t slots, bytes;        // workspace: partial results
+};
+PtPlan paged_tc_plan(int B, int Hq, int Hkv, int D, int N, int share);
 PagedWs paged_mma_ws(int B, int Hq, int Hkv, int D, int N, int sms);
 cudaError_t launch_paged_mma(PagedAttn a, char* ws, cudaStream_t stream);
+cudaError_t launch_paged_q8_mma(PagedAttn a, char* ws, cudaStream_t stream);
 PagedWs paged_f32_ws(int B, int Hq, int Hkv, int D, int N);
 cudaError_t launch_paged_f32(PagedAttn a, char* ws, cudaStream_t stream);
 cudaError_t launch_paged_q8_f32(PagedAttn a, char* ws, tv_dtype dtype, cudaStream_t stream);
@@ -385,5 +392,11 @@ cudaError_t launch_paged_simt(PagedAttn a, char* ws, cudaStream_t stream);
 // blocks and min(page_size, 64) rows, as 8-row groups [block][8][128 bytes].  Other D: 3-D boxes
 // of one column block, of min(page_size, 64) rows (D <= 64) or 8.
 bool paged_kv_tmap(CUtensorMap* m, const void* base, const PagedAttn& a);
+// Likewise of 8-bit pages, in column blocks of 64 bytes; with a 64-byte swizzle or none.
+bool paged_q8_tmap(CUtensorMap* m, const void* base, const PagedAttn& a, bool swizzled);
+// Likewise in rows of 128 bytes (zeros behind D), 128-byte swizzle.
+bool paged_q8_rows_tmap(CUtensorMap* m, const void* base, const PagedAttn& a);
+// Tensor map of queries, in boxes of 64 columns and `rows` rows.
+bool paged_q_tmap(CUtensorMap* m, const PagedAttn& a, int rows);
 
 }  // namespace tv

@@ -1,0 +1,8 @@
+// Paged attention of few rows over pages in 8 bits: paged_mma.cuh's kernel.
+#include "paged_mma.cuh"
+
+namespace tv {
+
+cudaError_t launch_paged_q8_mma(PagedAttn a, char* ws, cudaStream_t stream) { return launch_pm_all<true>(a, ws, stream); }
+
+}  // namespace tv
