@@ -68,6 +68,7 @@ struct PmCfg {
   static constexpr int kQStride = kD * 2 + (kQ8 ? 8 : 16);
   // K or V fragments loaded at once (kQ8: of V; as registers allow)
   static constexpr int kBatch = kQ8 && kNT > 2 ? 2 : kQ8 && kNT > 1 ? 4 : kD == 64 || kNT > 2 ? 4 : 8;
+  static constexpr int kAhead = kNT == 1 ? 4 : 2;       // kQ8: turns that scales are looked up ahead
   static constexpr bool kQRegs = kNT * kD <= 256;       // queries stay in registers
   // the unit's queries, masks and tree; its O at the end
   static constexpr int kOffU = kStages * 2 * kTile;
@@ -135,13 +136,6 @@ __device__ __forceinline__ uint32_t pm_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// the two 16-bit halves of a word of codes as f16x2
-__device__ __forceinline__ void pm_codes(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(w));
-}
-
 // Queries are held times 2^this, by the largest exponent field of their row: below 2^14.  A row that is not
 // finite stays as it is.
 __device__ __forceinline__ int pm_query_shift(int exponent) { return exponent == 255 ? 0 : min(127, 140 - exponent); }
@@ -444,8 +438,8 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
           for (int u = 0; u < 4; ++u) o[k][nt][u] = 0.f;
       }
 
-      // kQ8: the scale bytes of this warp's 16 keys (lanes 0..15 keys', 16..31 values'), read a turn of the warp
-      // ahead, and their pages, two turns
+      // kQ8: the scale bytes of this warp's 16 keys (lanes 0..15 keys', 16..31 values'), read kAhead turns of the
+      // warp ahead, and their pages, twice that.  One turn and two, 64 tokens over 8192 to 16384: 368 us
       constexpr int kTurn = C::kWarps == 8 ? 2 : 1;
       const int32_t* table = a.table + (size_t)w.b * a.max_pages;
       auto scale_key = [&](int t) -> int { return (tile0 + t) * kPmKeys + wk * 16 + (lane & 15); };
@@ -459,20 +453,27 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
         const size_t block = (((size_t)page * a.Hkv + w.hk) << (a.page_shift - a.block_shift)) + (in_page >> a.block_shift);
         return lane < 16 ? a.ks[block] : a.vs[block];
       };
-      int page_next = -1, scale_next = 127;
+      constexpr int kAhead = C::kAhead;
+      int pages_to[2 * kAhead], scales_to[kAhead];
       if constexpr (kQ8) {
         const int first = w.t0 + (C::kWarps == 8 && (it & 1) != group ? 1 : 0);
-        const int page_first = scale_page(first);
-        page_next = scale_page(first + kTurn);
-        scale_next = scale_byte(first, page_first);
+#pragma unroll
+        for (int k = 0; k < 2 * kAhead; ++k) pages_to[k] = scale_page(first + k * kTurn);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) scales_to[k] = scale_byte(first + k * kTurn, pages_to[k]);
       }
       for (int t = w.t0; t < w.t1; ++t, ++it) {
         if (C::kWarps == 8 && (it & 1) != group) continue;
         const int slot = it % C::kStages;
-        const int scale_now = scale_next;
+        int scale_now = 127;
         if constexpr (kQ8) {
-          scale_next = scale_byte(t + kTurn, page_next);
-          page_next = scale_page(t + 2 * kTurn);
+          scale_now = scales_to[0];
+#pragma unroll
+          for (int k = 0; k + 1 < kAhead; ++k) scales_to[k] = scales_to[k + 1];
+          scales_to[kAhead - 1] = scale_byte(t + kAhead * kTurn, pages_to[kAhead]);
+#pragma unroll
+          for (int k = kAhead; k + 1 < 2 * kAhead; ++k) pages_to[k] = pages_to[k + 1];
+          pages_to[2 * kAhead - 1] = scale_page(t + 2 * kAhead * kTurn);
         }
         if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars->full[slot], (it / C::kStages) & 1, abort_flag));
         if (!ok) continue;
@@ -516,8 +517,8 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
             for (int st = 0; st < 4; ++st) {
               const int kk = 4 * j + st;
               uint32_t kf[4];
-              pm_codes(w0[st], kf[0], kf[2]);
-              pm_codes(w1[st], kf[1], kf[3]);
+              q8_half4(w0[st], kf[0], kf[2]);
+              q8_half4(w1[st], kf[1], kf[3]);
 #pragma unroll
               for (int nt = 0; nt < C::kNT; ++nt) {
                 if constexpr (C::kQRegs) {
@@ -570,7 +571,7 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
               for (int u = 0; u < 4; ++u) {
                 // bytes: column 2g of keys 2c, 2c + 1, then column 2g + 1 of them
                 const uint32_t by_column = __byte_perm(r[u], 0, 0x3120);
-                pm_codes(by_column, vf[i + (u >> 1)][(u & 1) * 2], vf[i + (u >> 1)][(u & 1) * 2 + 1]);
+                q8_half4(by_column, vf[i + (u >> 1)][(u & 1) * 2], vf[i + (u >> 1)][(u & 1) * 2 + 1]);
               }
             }
           } else {

@@ -90,11 +90,11 @@ static int pt_clusters(int D, int s) {
   int n = known[dev][s].load(std::memory_order_relaxed) - 1;
   if (n < 0) {
     // every instance takes one CTA per SM, so one stands for all
-    const void* fn = reinterpret_cast<const void*>(paged_tc_kernel<128, kNoCap, false, false>);
+    const void* fn = reinterpret_cast<const void*>(paged_tc_kernel<128, kNoCap, false, kPtBf16>);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(s * 64, 1, 1);
-    cfg.blockDim = dim3(PtCfg<128, false>::kThreads, 1, 1);
-    cfg.dynamicSmemBytes = PtCfg<128, false>::kSmemAlloc;
+    cfg.blockDim = dim3(PtCfg<128, kPtBf16>::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = PtCfg<128, kPtBf16>::kSmemAlloc;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)s;
@@ -102,7 +102,7 @@ static int pt_clusters(int D, int s) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, PtCfg<128, false>::kSmemAlloc) != cudaSuccess ||
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, PtCfg<128, kPtBf16>::kSmemAlloc) != cudaSuccess ||
         cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess)
       n = paged_device_sms() / s;
     known[dev][s].store(n + 1, std::memory_order_relaxed);
@@ -160,6 +160,6 @@ PagedWs paged_tc_ws(int B, int Hq, int Hkv, int D, int N) {
   return {n, n};
 }
 
-cudaError_t launch_paged_tc(PagedAttn a, char* ws, cudaStream_t stream) { return launch_pt_all<false>(a, ws, stream); }
+cudaError_t launch_paged_tc(PagedAttn a, char* ws, cudaStream_t stream) { return launch_pt_all<kPtBf16>(a, ws, stream); }
 
 }  // namespace tv

@@ -40,12 +40,17 @@
 // times a power of two that brings its largest element below 448, is the sum of two rows of e4m3
 // numbers, the nearest ones and the nearest to what those leave, off by 2^-18 of the largest element at most
 // (bf16 elements down to 2^-10 of it exactly).  Two products at twice the rate take what one in bf16 did, and
-// K's half comes through L2 and shared memory in half the bytes.  The keys' scales, one for 16 keys where
-// blocks are that long, multiply with the row's power of two where the softmax multiplies anyhow.  V has to
-// be bf16, since P's small weights would not survive e4m3: four converter warps turn V's codes and scales,
-// exactly, into a second ring, zero the rows that no row needs, and bring Q and the keys' scales besides.
-// Warps then: 0 producer, 1 S issuer A, 2 PV issuer, 3 S issuer B, 4-11 softmax, 12-15 converters, with
-// registers moved from the others to the softmax's (168 and 88 a thread).
+// K's half comes through L2 and shared memory in half the bytes.  A block's scale of K joins the row's
+// power of two in the factor that the softmax multiplies by anyhow, one for 16 keys.  V's codes become fp16
+// numbers, which hold them exactly (a conversion for two codes), in a second ring, which four converter
+// warps fill; they also zero the rows that no row needs, and bring Q and the scales.  fp16's range is not
+// that of the numbers, so V's scales stay out of it: with e the exponent of the value block, P = 2^(z + e - m) and m
+// is the running reference of z + e, so that P is at most 2^8 (held times 2^7) and is lost only below 2^-32 of
+// the row's largest term; the sum takes 2^-e times a block's P.  Warps then: 0 producer, 1 S issuer A,
+// 2 PV issuer, 3 S issuer B, 4-11 softmax, 12-15 converters, with registers moved from the others to the
+// softmax's (168 and 88 a thread).  V in bf16 with its scales, four times the conversion's instructions, and a
+// factor a key or 16 keys by a branch in one kernel: eight 128-node trees 612 us.  Blocks of less than 16
+// rows have an instance of their own.
 #pragma once
 
 #include <atomic>
@@ -60,6 +65,7 @@ constexpr int kPtRows = 128;
 constexpr int kPtKeys = 64;
 constexpr int kPtSlots = 4;      // K ring and V ring depth
 constexpr int kPtVbSlots = 3;    // kQ8: ring of converted V tiles
+constexpr int kPtAhead = 4;      // kQ8: tiles that scales are looked up ahead
 constexpr int kPtPieces = 4;     // pieces known ahead
 constexpr int kPtMaxSplits = 8;  // portable cluster size
 // A unit's set-up and end count as 8 steps, and cuts less than 12 from a unit's edge move to it
@@ -71,8 +77,12 @@ constexpr int kPtFix = 8;
 constexpr float kPtRescaleLog2 = 8.f;
 constexpr float kPtRescaleSum = 256.f;
 
-template <int D, bool kQ8>
+// What the pages hold: bf16; 8 bits with blocks of 16 rows or more; with shorter blocks.
+enum { kPtBf16, kPtQ8, kPtQ8Fine };
+
+template <int D, int kQ>
 struct PtCfg {
+  static constexpr bool kQ8 = kQ != kPtBf16;
   static constexpr int kThreads = kQ8 ? 512 : 384;
   static constexpr int kDB = D / 64;
   // bytes per 64-column block of one Q tile; kQ8: per e4m3 part, 128-byte rows
@@ -88,8 +98,11 @@ struct PtCfg {
   static constexpr int kOffV = kOffK + kPtSlots * kKTile;
   static constexpr int kOffVb = kOffV + kPtSlots * kVTile;
   static constexpr int kOffPar = kOffVb + (kQ8 ? kPtVbSlots * kTileBytes : 0);
-  static constexpr int kOffScale = kOffPar + kMaxNodes * 4;  // kQ8: keys' scales of a tile, rows' of a piece
-  static constexpr int kOffBar = kOffScale + (kQ8 ? (kPtSlots * kPtKeys + 2 * kPtRows) * 4 : 0);
+  // kQ8: scales, and those of a piece's rows.  Blocks of 16 rows or more: four rounds of 8 tiles, of each four of
+  // K's and four of V's exponents e; shorter ones: a tile in each ring slot, {K's, e, 2^-e} of every key
+  static constexpr int kOffScale = kOffPar + kMaxNodes * 4;
+  static constexpr int kScaleBytes = !kQ8 ? 0 : kQ == kPtQ8Fine ? kPtSlots * kPtKeys * 16 : 4 * 8 * 32;
+  static constexpr int kOffBar = kOffScale + kScaleBytes + (kQ8 ? 2 * kPtRows * 4 : 0);
   static constexpr int kSmemAlloc = kOffBar + 640 + 1024;  // slack for 1024-byte alignment
   static constexpr uint32_t kColO = 256;
   static_assert(kSmemAlloc + 8192 <= 232448, "shared memory per CTA");  // 8192: paged_span's and the pieces'
@@ -110,7 +123,7 @@ struct PtBars {
   uint64_t rows_met;   // the softmax warps meet
   uint64_t vb_full[kPtVbSlots];   // kQ8: V tiles as bf16
   uint64_t vb_empty[kPtVbSlots];
-  uint64_t scale_full[kPtSlots];  // the keys' scales
+  uint64_t scale_full[kPtSlots];  // the keys' scales: a tile's, or a round's
   uint64_t rows_read[2];          // tile x's warps have read their rows' scales
   uint64_t piece_full[kPtPieces];
   uint64_t piece_empty[kPtPieces];
@@ -221,52 +234,100 @@ __device__ __forceinline__ void pt_pv_product(uint32_t d, uint32_t p, uint64_t v
       : "memory");
 }
 
-// kQ8: S of one row tile in e4m3: both parts of Q (kQBlock bytes apart) against the same K
+// kQ8: S of one row tile in e4m3: both parts of Q (16 KB apart) against the same K, 32 columns a step.  One asm
+// block at 128 columns, as above
 __device__ __forceinline__ void pt_s_product_q8(uint32_t d, uint64_t qd, uint64_t kd, int steps, uint32_t idesc) {
-#pragma unroll
-  for (int part = 0; part < 2; ++part)
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk)
-      if (kk < steps)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-            "l"(qd + part * (kPtRows * 128 / 16) + kk * 2), "l"(kd + kk * 2), "r"(idesc), "r"(part + kk > 0 ? 1u : 0u)
-            : "memory");
-}
-// P = 2^(s c_g - m) with a factor for each 16 keys; as pt_exp64 otherwise
-__device__ __forceinline__ float pt_exp64(const float (&sv)[64], const float (&c)[4], float m, uint32_t (&pw)[32]) {
-  const float nm = m == -INFINITY ? 0.f : -m;
-  const float2 nm2 = make_float2(nm, nm);
-  float2 acc[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) acc[k] = make_float2(0.f, 0.f);
-#pragma unroll
-  for (int k = 0; k < 32; ++k) {
-    const float2 t = __ffma2_rn(make_float2(sv[2 * k], sv[2 * k + 1]), make_float2(c[k >> 3], c[k >> 3]), nm2);
-    const float e0 = ptx::ex2(t.x), e1 = ptx::ex2(t.y);
-    acc[k & 3] = __fadd2_rn(acc[k & 3], make_float2(e0, e1));
-    pw[k] = ptx::cvt_bf16x2(e0, e1);
+  constexpr uint64_t kPart = kPtRows * 128 / 16;
+  if (steps == 4) {
+    asm volatile(
+        "{\n\t.reg .pred p0, p1;\n\t.reg .b32 z;\n\tmov.b32 z, 0;\n\tsetp.ne.b32 p0, z, 0;\n\tsetp.eq.b32 p1, z, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %9, %13, p0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %2, %10, %13, p1;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %3, %11, %13, p1;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %4, %12, %13, p1;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %5, %9, %13, p1;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %6, %10, %13, p1;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %7, %11, %13, p1;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %8, %12, %13, p1;\n\t}" ::"r"(d),
+        "l"(qd), "l"(qd + 2), "l"(qd + 4), "l"(qd + 6), "l"(qd + kPart), "l"(qd + kPart + 2), "l"(qd + kPart + 4),
+        "l"(qd + kPart + 6), "l"(kd), "l"(kd + 2), "l"(kd + 4), "l"(kd + 6), "r"(idesc)
+        : "memory");
+    return;
   }
-  const float2 s2 = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
-  return s2.x + s2.y;
+#pragma unroll 1
+  for (int i = 0; i < 2 * steps; ++i) {
+    const int kk = i < steps ? i : i - steps;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(qd + (i < steps ? 0 : kPart) + kk * 2), "l"(kd + kk * 2), "r"(idesc), "r"(i > 0 ? 1u : 0u)
+        : "memory");
+  }
 }
-// the largest score of a tile, likewise
-__device__ __forceinline__ float pt_max64(const float (&sv)[64], const float (&c)[4]) {
+__device__ __forceinline__ uint32_t pt_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+constexpr float kPtShift = 7.f;  // P is held times 2^7
+// kQ8: P = 2^(s c + e - m) as fp16 pairs, c and e of 16 keys each.  Returns the sum of P's, and in lsum that of
+// 2^-e P's
+__device__ __forceinline__ float pt_exp64_q8(const float (&sv)[64], const float (&gf)[4], const float (&ge)[4], float m,
+                                             uint32_t (&pw)[32], float& lsum) {
+  const float nm = m == -INFINITY ? 0.f : kPtShift - m;
+  float psum = 0.f;
+  lsum = 0.f;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const float2 cc = make_float2(gf[g], gf[g]), add = make_float2(ge[g] + nm, ge[g] + nm);
+    float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+    for (int k = 8 * g; k < 8 * g + 8; ++k) {
+      const float2 t = __ffma2_rn(make_float2(sv[2 * k], sv[2 * k + 1]), cc, add);
+      const float e0 = ptx::ex2(t.x), e1 = ptx::ex2(t.y);
+      acc[k & 1] = __fadd2_rn(acc[k & 1], make_float2(e0, e1));
+      pw[k] = pt_f16x2(e0, e1);
+    }
+    const float2 both = __fadd2_rn(acc[0], acc[1]);
+    const float all = both.x + both.y;
+    psum += all;
+    lsum = fmaf(all, ptx::ex2(-ge[g]), lsum);
+  }
+  return psum;
+}
+__device__ __forceinline__ float pt_max64_q8(const float (&sv)[64], const float (&gf)[4], const float (&ge)[4]) {
   float m = -INFINITY;
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
     float x = pt_max3(sv[16 * g], sv[16 * g + 1], sv[16 * g + 2]);
 #pragma unroll
     for (int j = 3; j < 15; j += 2) x = pt_max3(x, sv[16 * g + j], sv[16 * g + j + 1]);
-    m = fmaxf(m, fmaxf(x, sv[16 * g + 15]) * c[g]);
+    m = fmaxf(m, fmaf(fmaxf(x, sv[16 * g + 15]), gf[g], ge[g]));
   }
   return m;
 }
-__device__ __forceinline__ float pt_exp64(const float (&sv)[64], const float (&c)[1], float m, uint32_t (&pw)[32]) {
-  return pt_exp64(sv, c[0], m, pw);
+// the same with sc[j] of every key (the factor is in sv already)
+__device__ __forceinline__ float pt_exp64_fine(const float (&sv)[64], float c, const float4* sc, float m,
+                                               uint32_t (&pw)[32], float& lsum) {
+  const float nm = m == -INFINITY ? 0.f : kPtShift - m;
+  float psum = 0.f;
+  lsum = 0.f;
+#pragma unroll
+  for (int k = 0; k < 32; ++k) {
+    const volatile float4* at = sc + 2 * k;  // read here: 64 keys' would not fit the registers
+    const float e0 = ptx::ex2(fmaf(sv[2 * k], c, at[0].y + nm)), e1 = ptx::ex2(fmaf(sv[2 * k + 1], c, at[1].y + nm));
+    psum += e0 + e1;
+    lsum = fmaf(e0, at[0].z, fmaf(e1, at[1].z, lsum));
+    pw[k] = pt_f16x2(e0, e1);
+  }
+  return psum;
 }
-__device__ __forceinline__ float pt_max64(const float (&sv)[64], const float (&c)[1]) { return pt_max64(sv) * c[0]; }
+__device__ __forceinline__ float pt_max64_fine(const float (&sv)[64], float c, const float4* sc) {
+  float m = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < 64; ++j) m = fmaxf(m, fmaf(sv[j], c, ((const volatile float4*)sc)[j].y));
+  return m;
+}
 
 // Wait for this piece's own copies or products even when another wait has run out.
 __device__ __forceinline__ void pt_drain(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
@@ -274,7 +335,23 @@ __device__ __forceinline__ void pt_drain(uint64_t* bar, uint32_t parity, volatil
   if (!ptx::mbar_wait(bar, parity, &quiet)) *abort_flag = 1;
 }
 
-__device__ __forceinline__ void pt_bars_init(PtBars* bars, bool q8, int warps) {
+// mbar_wait of a role that runs ahead of the others: asleep between looks, so that it leaves the issue
+// slots, and the instruction caches, to them
+__device__ __forceinline__ bool pt_wait_ahead(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  uint64_t t0 = 0;
+  while (!ptx::mbar_try_wait(bar, parity)) {
+    __nanosleep(64);
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if (*abort || now - t0 > TV_WAIT_NS) {
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
+__device__ __forceinline__ void pt_bars_init(PtBars* bars, bool q8, bool fine, int warps) {
   ptx::mbar_init(&bars->q_full[0], q8 ? 4 : 1);  // converter warps, or the copies
   ptx::mbar_init(&bars->q_full[1], q8 ? 4 : 1);
   ptx::mbar_init(&bars->rows_met, 8);
@@ -282,7 +359,7 @@ __device__ __forceinline__ void pt_bars_init(PtBars* bars, bool q8, int warps) {
     ptx::mbar_init(&bars->vb_full[s], 4);
     ptx::mbar_init(&bars->vb_empty[s], 1);
   }
-  for (int s = 0; s < kPtSlots; ++s) ptx::mbar_init(&bars->scale_full[s], 4);
+  for (int s = 0; s < kPtSlots; ++s) ptx::mbar_init(&bars->scale_full[s], fine ? 4 : 1);
   ptx::mbar_init(&bars->rows_read[0], 4);
   ptx::mbar_init(&bars->rows_read[1], 4);
   for (int s = 0; s < kPtPieces; ++s) {
@@ -309,12 +386,13 @@ __device__ __forceinline__ void pt_bars_init(PtBars* bars, bool q8, int warps) {
   ptx::fence_mbar_init();
 }
 
-template <int D, int kCap, bool kStream, bool kQ8>
-__global__ void __launch_bounds__(PtCfg<D, kQ8>::kThreads, 1)
+template <int D, int kCap, bool kStream, int kQ>
+__global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
     paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, PagedAttn a, PtArgs pa) {
   ptx::griddep_launch_dependents();
-  using C = PtCfg<D, kQ8>;
+  using C = PtCfg<D, kQ>;
+  constexpr bool kQ8 = C::kQ8, kFine = kQ == kPtQ8Fine;
   extern __shared__ unsigned char smem_raw[];
   const uint32_t mis = ptx::smem_addr(smem_raw) & 1023u;
   unsigned char* sm = smem_raw + ((1024u - mis) & 1023u);
@@ -331,8 +409,8 @@ __global__ void __launch_bounds__(PtCfg<D, kQ8>::kThreads, 1)
   // warp: the role, in the order of the bf16 kernel's warps (12..15: converters)
   const int hw_warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int warp = !kQ8 || hw_warp >= 12 ? hw_warp : hw_warp < 2 ? hw_warp : hw_warp < 4 ? hw_warp + 8 : hw_warp - 2;
-  float* s_kscale = reinterpret_cast<float*>(sm + C::kOffScale);
-  float* s_rscale = s_kscale + kPtSlots * kPtKeys;
+  float4* s_scale = reinterpret_cast<float4*>(sm + C::kOffScale);
+  float* s_rscale = reinterpret_cast<float*>(sm + C::kOffScale + C::kScaleBytes);
   const int NT = pa.NT, rows_used = a.G * NT, RT = pa.tiles * rows_used;
   if (warp == 1) {
     ptx::tmem_alloc(&bars->tmem_base, 512);
@@ -343,7 +421,7 @@ __global__ void __launch_bounds__(PtCfg<D, kQ8>::kThreads, 1)
     ptx::prefetch_tmap(&tmK);
     ptx::prefetch_tmap(&tmV);
     bars->abort = 0;
-    pt_bars_init(bars, kQ8, C::kThreads / 32);
+    pt_bars_init(bars, kQ8, kFine, C::kThreads / 32);
   }
   // the Q rows that no box fills
   for (int r = rows_used + threadIdx.x; !kQ8 && r < 2 * kPtRows; r += C::kThreads) {
@@ -393,7 +471,7 @@ __global__ void __launch_bounds__(PtCfg<D, kQ8>::kThreads, 1)
   int loaded_b = -1, n_act = 0;
   // tiles, and tiles with rows of A and B, of the pieces before this one, and how many those were: what
   // the rings' slots and the barriers' phases go by.  Every role counts them alike.
-  unsigned kt = 0, done_x[2] = {0, 0}, pieces = 0;
+  unsigned kt = 0, done_x[2] = {0, 0}, pieces = 0, rounds = 0;  // rounds: of 8 tiles
   unsigned k_issued = 0, v_issued = 0;  // the producer's copies
   unsigned q_loads = 0;                 // an S issuer's
   bool ok = true;                       // no wait of this role has run out
@@ -543,7 +621,12 @@ __global__ void __launch_bounds__(PtCfg<D, kQ8>::kThreads, 1)
         const unsigned gt = kt + t;
         const int slot = gt % kPtSlots;
         bool got = true;
-        if (gt >= kPtSlots) got = ptx::mbar_wait(&empty[slot], ((gt / kPtSlots) - 1) & 1, abort_flag);
+        if (gt >= kPtSlots) {
+          if constexpr (kQ8)
+            got = pt_wait_ahead(&empty[slot], ((gt / kPtSlots) - 1) & 1, abort_flag);
+          else
+            got = ptx::mbar_wait(&empty[slot], ((gt / kPtSlots) - 1) & 1, abort_flag);
+        }
         if (!__all_sync(0xffffffffu, got)) return false;
         // kQ8: a K box holds whole 128-byte rows, column blocks or not
         const bool mine = pg >= 0 && !(kQ8 && is_k && db > 0);
@@ -632,7 +715,8 @@ __global__ void __launch_bounds__(PtCfg<D, kQ8>::kThreads, 1)
       __syncwarp();
     } else if (kWho != kSoftmax && warp == 10) {
       // ---------------------------------------------------------------- PV issuer
-      constexpr uint32_t idO = ptx::idesc_bf16(kPtRows, D, false, true);
+      // kQ8: fp16 operands
+      constexpr uint32_t idO = ptx::idesc_bf16(kPtRows, D, false, true) & (kQ8 ? ~(7u << 7 | 7u << 10) : ~0u);
       // only the first and last tile can hold V rows that may be anything; the warp zeroes them
       // (their weights are zero too) before its lane 0 issues that tile.  A loop that kept all
       // lanes together for every tile cost 3 %
@@ -754,65 +838,90 @@ __global__ void __launch_bounds__(PtCfg<D, kQ8>::kThreads, 1)
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&bars->q_full[x]);
       }
-      // K's scales and V, 16 keys of a tile a warp: lanes 0..15 look up the values' scale bytes, 16..31 the
-      // keys', a tile ahead, and their pages, two
+      // Scales.  Blocks of 16 keys or more: warp 12 alone brings those of 8 tiles at once (lane: tile lane / 4, keys
+      // 16 (lane % 4)..), looked up a round ahead, their pages two.  Shorter ones: each warp those of its 16
+      // keys (lanes 0..15 V's, 16..31 K's), looked up kPtAhead tiles ahead, their pages twice that.
       const int32_t* table = a.table + (size_t)b * a.max_pages;
-      auto key_of = [&](int t) -> int { return (t_begin + t) * kPtKeys + cw * 16 + (lane & 15); };
-      // blocks of 16 keys or more: the warp's keys share one, which counts if any of them is needed
-      const int block_keys = a.block_shift >= 4 ? 15 : 0;
+      auto key_of = [&](int t) -> int {  // this lane's in tile t (or, in rounds, from t on)
+        return kFine ? (t_begin + t) * kPtKeys + cw * 16 + (lane & 15)
+                     : (t_begin + t + (lane >> 2)) * kPtKeys + (lane & 3) * 16;
+      };
       auto page_of = [&](int t) -> int {
         const int j = key_of(t);
-        return t < nt && (j | block_keys) >= lo && (j & ~block_keys) < key_end ? table[j >> a.page_shift] : -1;
+        const bool in = kFine ? t < nt : t + (lane >> 2) < nt;
+        return in && j + (kFine ? 0 : 15) >= lo && j < key_end ? table[j >> a.page_shift] : -1;
       };
-      auto byte_of = [&](int t, int page) -> int {
-        if (page < 0 || page >= a.num_pages) return 127;  // rows that no row needs: any finite scale
+      // K's byte and V's, in bits 8..15, or one of them; 127 where no row needs it
+      auto bytes_of = [&](int t, int page) -> int {
+        if (page < 0 || page >= a.num_pages) return 127 | 127 << 8;
         const size_t block = (((size_t)page * a.Hkv + hk) << (a.page_shift - a.block_shift)) +
                              ((key_of(t) & ((1 << a.page_shift) - 1)) >> a.block_shift);
-        return lane < 16 ? a.vs[block] : a.ks[block];
+        if (kFine) return lane < 16 ? a.vs[block] : a.ks[block];
+        return a.ks[block] | a.vs[block] << 8;
       };
-      int page_next = page_of(1), byte_next = byte_of(0, page_of(0));
+      constexpr int kAhead = kFine ? kPtAhead : 1, kStep = kFine ? 1 : 8;
+      const bool looks = kFine || cw == 0;
+      int pages_to[2 * kAhead], bytes_to[kAhead];
+#pragma unroll
+      for (int k = 0; k < 2 * kAhead; ++k) pages_to[k] = looks ? page_of(k * kStep) : -1;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) bytes_to[k] = bytes_of(k * kStep, pages_to[k]);
+      // the next bytes in line, behind which another step's are looked up, for tile t on
+      auto next_bytes = [&](int t) -> int {
+        const int bytes = bytes_to[0];
+#pragma unroll
+        for (int k = 0; k + 1 < kAhead; ++k) bytes_to[k] = bytes_to[k + 1];
+        bytes_to[kAhead - 1] = bytes_of(t + kAhead * kStep, pages_to[kAhead]);
+#pragma unroll
+        for (int k = kAhead; k + 1 < 2 * kAhead; ++k) pages_to[k] = pages_to[k + 1];
+        pages_to[2 * kAhead - 1] = page_of(t + 2 * kAhead * kStep);
+        return bytes;
+      };
       for (int t = 0; ok && t < nt; ++t) {
         const unsigned gt = kt + t;
-        const int byte = byte_next;
-        byte_next = byte_of(t + 1, page_next);
-        page_next = page_of(t + 2);
         const int vs = gt % kPtSlots, vb = gt % kPtVbSlots;
         bool got = true;
-        if (gt >= kPtVbSlots) got = ptx::mbar_wait(&bars->vb_empty[vb], (gt / kPtVbSlots - 1) & 1, abort_flag);
-        if (lane >= 16) s_kscale[vs * kPtKeys + cw * 16 + (lane & 15)] = q8_scale(byte);
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&bars->scale_full[vs]);
-        got = got && ptx::mbar_wait(&bars->v_full[vs], (gt / kPtSlots) & 1, abort_flag);
+        if (gt >= kPtVbSlots) got = pt_wait_ahead(&bars->vb_empty[vb], (gt / kPtVbSlots - 1) & 1, abort_flag);
+        if constexpr (kFine) {
+          const int bytes = next_bytes(t), ks = __shfl_sync(0xffffffffu, bytes, 16 + (lane & 15));
+          if (lane < 16)
+            s_scale[vs * kPtKeys + cw * 16 + lane] =
+                make_float4(q8_scale(ks), (float)(bytes - 127), q8_two(127 - bytes), 0.f);
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&bars->scale_full[vs]);
+        } else if (cw == 0 && (t == 0 || t % 8 == 4)) {
+          // the first round, then each in the middle of the one before.  Its place is that of four rounds before, a
+          // tile or more each, of which no tile is later than that whose ring slot has just been seen free
+#pragma unroll 1
+          for (int r = t == 0 ? 0 : t + 4; r < nt && r <= t + 4; r += 8) {
+            const int bytes = next_bytes(r);
+            float* to = reinterpret_cast<float*>(s_scale) + ((rounds + r / 8) & 3) * 64 + (lane >> 2) * 8 + (lane & 3);
+            to[0] = q8_scale(bytes & 255);
+            to[4] = (float)((bytes >> 8) - 127);
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&bars->scale_full[(rounds + r / 8) & 3]);
+          }
+        }
+        got = got && pt_wait_ahead(&bars->v_full[vs], (gt / kPtSlots) & 1, abort_flag);
         ok = __all_sync(0xffffffffu, got);
         if (!ok) break;
         const int j0 = (t_begin + t) * kPtKeys + cw * 16;
         const unsigned char* from = sV + vs * C::kVTile + cw * C::kGroup + (lane >> 2) * 64 + (lane & 3) * 16;
         unsigned char* to = sm + C::kOffVb + vb * C::kTileBytes + cw * 2 * C::kGroup + (lane >> 2) * 128;
         const int r7 = lane >> 2;
-#pragma unroll
+#pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           const int row = half * 8 + r7, j = j0 + row;
-          const int s = __shfl_sync(0xffffffffu, byte, row);
           const bool needed = j >= lo && j < key_end;
-          // code * 2^(s - 127): a code's bits, as bf16's, stand for 2^-120 of it; past 2^7 in two steps
-          const uint32_t f1 = (uint32_t)min(s + 120, 254) * 0x00800080u, f2 = (uint32_t)max(s - 7, 127) * 0x00800080u;
-          const bool far = __any_sync(0xffffffffu, needed && s > 134);
 #pragma unroll
           for (int blk = 0; blk < C::kDB; ++blk) {
             uint4 c = make_uint4(0, 0, 0, 0);
             if (needed) c = *reinterpret_cast<const uint4*>(from + half * (C::kGroup / 2) + blk * 512);
-            const uint32_t w[4] = {c.x, c.y, c.z, c.w};
             uint32_t out[8];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t p = __byte_perm(w[k], 0, 0x3120);  // bytes 0, 1 to the even places, 2, 3 to the odd
-              out[2 * k] = q8_bf16x2((p << 4 & 0x07f007f0u) | (p << 8 & 0x80008000u), f1);
-              out[2 * k + 1] = q8_bf16x2((p >> 4 & 0x07f007f0u) | (p & 0x80008000u), f1);
-            }
-            if (far) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) out[k] = q8_bf16x2(out[k], f2);
-            }
+            q8_half4(c.x, out[0], out[1]);
+            q8_half4(c.y, out[2], out[3]);
+            q8_half4(c.z, out[4], out[5]);
+            q8_half4(c.w, out[6], out[7]);
             unsigned char* row_to = to + half * C::kGroup + blk * 1024;
             const int ch = (lane & 3) * 2;
             *reinterpret_cast<uint4*>(row_to + ((ch ^ r7) << 4)) = make_uint4(out[0], out[1], out[2], out[3]);
@@ -868,6 +977,27 @@ __global__ void __launch_bounds__(PtCfg<D, kQ8>::kThreads, 1)
       for (int t = 0; ok && t < ntm; ++t) {
         const unsigned tx = dx + t;
         const int buf = tx & 1;
+        // kQ8: the tile's scales, read before its scores are there: with the products' operands on the way, shared
+        // memory takes long to answer
+        const float4* scales = s_scale + (kFine ? (kt + t) % kPtSlots * kPtKeys : ((rounds + t / 8) & 3) * 16 + t % 8 * 2);
+        float gf[4], ge[4];
+        if constexpr (kQ8) {
+          if (kFine || t % 8 == 0) {
+            const unsigned n = kFine ? (kt + t) / kPtSlots : (rounds + t / 8) / 4;
+            ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars->scale_full[kFine ? (kt + t) % kPtSlots : (rounds + t / 8) & 3],
+                                                        n & 1, abort_flag));
+            if (!ok) break;
+          }
+          if constexpr (!kFine) {
+            const float4 ks = scales[0], vs = scales[1];
+            gf[0] = ks.x * row_f, gf[1] = ks.y * row_f, gf[2] = ks.z * row_f, gf[3] = ks.w * row_f;
+            ge[0] = vs.x, ge[1] = vs.y, ge[2] = vs.z, ge[3] = vs.w;
+          }
+        }
+        auto scale_keys = [&](float(&v)[64]) {
+#pragma unroll
+          for (int j = 0; j < 64; ++j) v[j] *= ((const volatile float4*)scales)[j].x * row_f;
+        };
         ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars->s_full[x][buf], (tx >> 1) & 1, abort_flag));
         if (!ok) break;
         ptx::tc_fence_after();
@@ -884,37 +1014,11 @@ __global__ void __launch_bounds__(PtCfg<D, kQ8>::kThreads, 1)
             }
           }
         }
-        // kQ8: a factor for each 16 keys, never 0 (a masked score is -inf) nor infinite (a score may be 0)
-        constexpr int kFactors = kQ8 ? 4 : 1;
-        float gf[kFactors];
-        const float* kscale = s_kscale + (kt + t) % kPtSlots * kPtKeys;
-        bool by_key = false;
-        if constexpr (kQ8) {
-          ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars->scale_full[(kt + t) % kPtSlots], ((kt + t) / kPtSlots) & 1,
-                                                      abort_flag));
-          if (!ok) break;
-          by_key = a.block_shift < 4;
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            gf[k] = fminf(fmaxf(by_key ? row_f : row_f * kscale[16 * k], 1.1754944e-38f), 3.4028234e38f);
-        } else {
-          gf[0] = 1.f;
-        }
         float sv[64];
         ptx::tmem_ld32(colS + buf * kPtKeys, sv);
         ptx::tmem_ld32(colS + buf * kPtKeys + 32, sv + 32);
         ptx::tmem_wait_ld();
-        auto scale_keys = [&] {  // short blocks: a factor a key
-          if (!by_key) return;
-#pragma unroll
-          for (int j = 0; j < 64; j += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(kscale + j);
-            const float2 lo2 = __fmul2_rn(make_float2(sv[j], sv[j + 1]), make_float2(f.x, f.y));
-            const float2 hi2 = __fmul2_rn(make_float2(sv[j + 2], sv[j + 3]), make_float2(f.z, f.w));
-            sv[j] = lo2.x, sv[j + 1] = lo2.y, sv[j + 2] = hi2.x, sv[j + 3] = hi2.y;
-          }
-        };
-        scale_keys();
+        if constexpr (kFine) scale_keys(sv);
         if constexpr (kCap == kTanhCap) {
           if (vis != ~0ull) {
 #pragma unroll
@@ -922,13 +1026,13 @@ __global__ void __launch_bounds__(PtCfg<D, kQ8>::kThreads, 1)
               if (!((vis >> j) & 1ull)) sv[j] = 0.f;
           }
 #pragma unroll
-          for (int j = 0; j < 64; j += 4) soft_tanh4(sv + j, kQ8 ? ck * gf[j * kFactors / 64] : ck);
+          for (int j = 0; j < 64; j += 4) soft_tanh4(sv + j, kQ == kPtQ8 ? ck * gf[j / 16] : ck);
         } else if constexpr (kCap == kLargeCap) {
           // nearly all scores lie below 0.45 of such a cap; where one does not, the tile is read again
           float z_max = 0.f;
 #pragma unroll
           for (int j = 0; j < 64; ++j) {
-            const float t = sv[j] * (kQ8 ? a.scale * gf[j * kFactors / 64] : a.scale), x = t * ck, z = x * x;
+            const float t = sv[j] * (kQ == kPtQ8 ? a.scale * gf[j / 16] : a.scale), x = t * ck, z = x * x;
             z_max = fmaxf(z_max, z);
             sv[j] = fmaf(t * z, tanh_tail(z), t);
           }
@@ -936,13 +1040,13 @@ __global__ void __launch_bounds__(PtCfg<D, kQ8>::kThreads, 1)
             ptx::tmem_ld32(colS + buf * kPtKeys, sv);
             ptx::tmem_ld32(colS + buf * kPtKeys + 32, sv + 32);
             ptx::tmem_wait_ld();
-            scale_keys();
+            if constexpr (kFine) scale_keys(sv);
 #pragma unroll
             for (int j = 0; j < 64; ++j)
-              sv[j] = capped_score(sv[j] * (kQ8 ? a.scale * gf[j * kFactors / 64] : a.scale), a.cap, ck);
+              sv[j] = capped_score(sv[j] * (kQ == kPtQ8 ? a.scale * gf[j / 16] : a.scale), a.cap, ck);
           }
         }
-        if (vis != ~0ull) {
+        if (__builtin_expect(vis != ~0ull, 0)) {
 #pragma unroll
           for (int j = 0; j < 64; ++j)
             if (!((vis >> j) & 1ull)) sv[j] = -INFINITY;
@@ -950,25 +1054,59 @@ __global__ void __launch_bounds__(PtCfg<D, kQ8>::kThreads, 1)
         // P = 2^(c S - m_run) against a running reference that moves (with a rescale of O) only
         // when a score exceeds it by 2^8: such a score brings the tile's sum to 2^8, so the
         // maximum is taken only then and for the first tile with a visible key
+        if constexpr (kQ == kPtQ8) {
+          // what the scores are multiplied by; not 0 where one is -inf
 #pragma unroll
-        for (int k = 0; k < kFactors; ++k) gf[k] = kQ8 && !kCap ? fminf(fmaxf(gf[k] * c, 1.1754944e-38f), 3.4028234e38f) : c;
-        float alpha = 1.f;
-        bool need = false, checked = false;
-        if (m_run == -INFINITY) {
-          m_run = pt_max64(sv, gf);
-          checked = true;
+          for (int g = 0; g < 4; ++g) {
+            gf[g] = kCap ? c : gf[g] * c;
+            if (vis != ~0ull) gf[g] = fmaxf(gf[g], 1.1754944e-38f);
+          }
         }
+        auto tile_max = [&]() -> float {
+          if constexpr (kFine) return pt_max64_fine(sv, c, scales);
+          return pt_max64_q8(sv, gf, ge);
+        };
+        float alpha = 1.f, lsum;
+        bool need = false;
         uint32_t pw[32];
-        float lsum;
-        for (;;) {
-          lsum = pt_exp64(sv, gf, m_run, pw);
-          if (checked || lsum < kPtRescaleSum) break;
-          checked = true;
-          const float tms = pt_max64(sv, gf);
-          if (!(tms > m_run + kPtRescaleLog2)) break;
-          alpha = ptx::ex2(m_run - tms);
-          need = true;
-          m_run = tms;
+        if constexpr (kQ8) {
+          bool checked = false, look = m_run == -INFINITY;
+          for (;;) {
+            if (__builtin_expect(look, 0)) {
+              const float tms = tile_max();
+              checked = true;
+              if (m_run == -INFINITY) {
+                m_run = tms;
+              } else if (tms > m_run + kPtRescaleLog2) {
+                alpha = ptx::ex2(m_run - tms);
+                need = true;
+                m_run = tms;
+              }
+            }
+            float psum;  // of P: where it is small, no score is far above the reference
+            if constexpr (kFine)
+              psum = pt_exp64_fine(sv, c, scales, m_run, pw, lsum);
+            else
+              psum = pt_exp64_q8(sv, gf, ge, m_run, pw, lsum);
+            if (checked || psum < 128.f * kPtRescaleSum) break;
+            look = true;
+          }
+        } else {
+          bool checked = false;
+          if (m_run == -INFINITY) {
+            m_run = pt_max64(sv) * c;
+            checked = true;
+          }
+          for (;;) {
+            lsum = pt_exp64(sv, c, m_run, pw);
+            if (checked || lsum < kPtRescaleSum) break;
+            checked = true;
+            const float tms = pt_max64(sv) * c;
+            if (!(tms > m_run + kPtRescaleLog2)) break;
+            alpha = ptx::ex2(m_run - tms);
+            need = true;
+            m_run = tms;
+          }
         }
         ptx::tmem_st32u(colS + buf * kPtKeys, pw);
         if (__any_sync(0xffffffffu, need) && t > 0) {
@@ -977,7 +1115,7 @@ __global__ void __launch_bounds__(PtCfg<D, kQ8>::kThreads, 1)
                           ptx::mbar_wait(&bars->pv_done[x][(tx - 1) & 1], ((tx - 1) >> 1) & 1, abort_flag));
           if (!ok) break;
           ptx::tc_fence_after();
-#pragma unroll
+#pragma unroll(kQ8 ? 1 : D / 32)
           for (int c0 = 0; c0 < D; c0 += 32) {
             float ov[32];
             ptx::tmem_ld32(colO + c0, ov);
@@ -1161,6 +1299,7 @@ __global__ void __launch_bounds__(PtCfg<D, kQ8>::kThreads, 1)
       if (warp != 0 && lane == 0) ptx::mbar_arrive(&bars->piece_empty[np % kPtPieces]);
     }
     kt += nt;
+    rounds += (nt + 7) / 8;
     done_x[0] += ntx[0];
     done_x[1] += ntx[1];
     pieces += nt > 0;
@@ -1190,12 +1329,12 @@ __global__ void __launch_bounds__(PtCfg<D, kQ8>::kThreads, 1)
 
 // ---- host side
 
-template <int D, int kCap, bool kStream, bool kQ8>
+template <int D, int kCap, bool kStream, int kQ>
 static cudaError_t launch_pt(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a,
                              const PtPlan& p, cudaStream_t stream) {
-  using C = PtCfg<D, kQ8>;
+  using C = PtCfg<D, kQ>;
   constexpr int smem = C::kSmemAlloc;
-  const auto fn = paged_tc_kernel<D, kCap, kStream, kQ8>;
+  const auto fn = paged_tc_kernel<D, kCap, kStream, kQ>;
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const PtArgs pa{p.NT, p.tiles, p.MP, p.splits, a.D == 128};
@@ -1211,37 +1350,37 @@ static cudaError_t launch_pt(const CUtensorMap& mq, const CUtensorMap& mk, const
                     dim3(C::kThreads), smem, stream, attr, 1, mq, mk, mv, a, pa);
 }
 
-template <int D, int kCap, bool kQ8>
+template <int D, int kCap, int kQ>
 static cudaError_t launch_pt_c(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a,
                                const PtPlan& p, cudaStream_t stream) {
-  return p.splits ? launch_pt<D, kCap, false, kQ8>(mq, mk, mv, a, p, stream)
-                  : launch_pt<D, kCap, true, kQ8>(mq, mk, mv, a, p, stream);
+  return p.splits ? launch_pt<D, kCap, false, kQ>(mq, mk, mv, a, p, stream)
+                  : launch_pt<D, kCap, true, kQ>(mq, mk, mv, a, p, stream);
 }
-template <int D, bool kQ8>
+template <int D, int kQ>
 static cudaError_t launch_pt_d(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a,
                                const PtPlan& p, cudaStream_t stream) {
   switch (cap_mode(a.cap)) {
     case kLargeCap:
-      return launch_pt_c<D, kLargeCap, kQ8>(mq, mk, mv, a, p, stream);
+      return launch_pt_c<D, kLargeCap, kQ>(mq, mk, mv, a, p, stream);
     case kTanhCap:
-      return launch_pt_c<D, kTanhCap, kQ8>(mq, mk, mv, a, p, stream);
+      return launch_pt_c<D, kTanhCap, kQ>(mq, mk, mv, a, p, stream);
     default:
-      return launch_pt_c<D, kNoCap, kQ8>(mq, mk, mv, a, p, stream);
+      return launch_pt_c<D, kNoCap, kQ>(mq, mk, mv, a, p, stream);
   }
 }
 
-template <bool kQ8>
+template <int kQ>
 static cudaError_t launch_pt_all(PagedAttn a, char* ws, cudaStream_t stream) {
   const PtPlan p = paged_tc_plan(a.B, a.Hq, a.Hkv, a.D, a.N, a.sms);
   a.cnt = reinterpret_cast<unsigned*>(ws);
   a.ws_ml = reinterpret_cast<float2*>(ws + kPagedCntBytes);
   a.ws_o = reinterpret_cast<float*>(ws + kPagedCntBytes + p.slots * 2 * kPtRows * 8);
   CUtensorMap mq, mk, mv;
-  const bool made = kQ8 ? paged_q8_rows_tmap(&mk, a.k, a) && paged_q8_tmap(&mv, a.v, a, false)
+  const bool made = kQ != kPtBf16 ? paged_q8_rows_tmap(&mk, a.k, a) && paged_q8_tmap(&mv, a.v, a, false)
                         : paged_q_tmap(&mq, a, p.NT) && paged_kv_tmap(&mk, a.k, a) && paged_kv_tmap(&mv, a.v, a);
   if (!made) return cudaErrorInvalidValue;
-  if (kQ8) mq = mk;  // Q comes without one
-  return a.D <= 64 ? launch_pt_d<64, kQ8>(mq, mk, mv, a, p, stream) : launch_pt_d<128, kQ8>(mq, mk, mv, a, p, stream);
+  if (kQ != kPtBf16) mq = mk;  // Q comes without one
+  return a.D <= 64 ? launch_pt_d<64, kQ>(mq, mk, mv, a, p, stream) : launch_pt_d<128, kQ>(mq, mk, mv, a, p, stream);
 }
 
 }  // namespace tv

@@ -64,11 +64,11 @@ __device__ __forceinline__ float4 q8_numbers(uint32_t w, float scale) {
 __device__ __forceinline__ uint32_t q8_code4(float a, float b, float c, float d) {
   return q8_code2(a, b) | q8_code2(c, d) << 16;
 }
-// bf16 pairs times a pair
-__device__ __forceinline__ uint32_t q8_bf16x2(uint32_t x, uint32_t f) {
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(f));
-  return r;
+// four codes to two f16x2
+__device__ __forceinline__ void q8_half4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
 // four codes under the scale 2^from, coded for 2^to >= 2^from
 __device__ __forceinline__ uint32_t q8_recode(uint32_t w, float ratio) {
