@@ -21,18 +21,19 @@
 // cost little).  More units are divided equally, tile by tile, over a persistent grid
 // (paged.cuh), and the parts of cut units merged through the workspace.
 //
-// Pages in 8 bits (kQ8, q8.cuh) are the same stream with half the bytes.  Codes become fp16 numbers, which
-// hold them exactly, in registers on the way to the products: one conversion for two codes (4.5
-// instructions with bf16, whose exponent is another; the conversions then took more issue slots than
-// the copies leave).  fp16's range is not that of the numbers, so nothing but codes goes through it
-// unscaled: queries are held as q 2^k with their row's largest below 2^14 (what that loses is 2^-39 of the largest);
-// a key's scale and 2^-k multiply its scores, in fp32; and P carries the values' scales, 2^(z + e - m') with
-// e the value block's exponent and m' a running reference of z + e, apart from the sum's own
-// reference m.  So a weight is rounded to 11 bits, and lost only below 2^-32 of the largest term of its row's
-// sum.  K's fragments need no transpose and any order of columns, if Q's have the same: a lane
-// takes 16 columns of a key in one load, rows of 64 bytes without a swizzle, so that eight lanes read 128
-// bytes in a row.  V's come by transposing loads of 16-bit pairs (two columns of a key), whose bytes are
-// dealt to two product rows.
+// Pages in 8 bits (kQ8, q8.cuh) are the same stream with half the bytes, in tiles of 128 keys, 32 a warp.
+// K's codes go into e4m3 products as they are, with the queries' rows, times a power of two that brings the
+// largest element below 448, as sums of two e4m3 numbers (off by 2^-18 of the largest at most).  V's
+// become fp16 numbers, which hold them exactly, in registers on the way: one conversion for two codes, where bf16,
+// whose exponent is another, takes 4.5 instructions and more issue slots than the copies leave.  fp16's range is
+// not that of the numbers, so V's scales stay out of it: with e the exponent of the value's block, P = 2^(z + e - m)
+// and m is the running reference of z + e, so that a weight is rounded to 11 bits and lost only below 2^-32 of the
+// largest term of its row's sum; the sum takes 2^-e times P.  A key's scale multiplies its scores, in fp32.  K's
+// fragments need no transpose and any order of columns, if Q's have the same: a lane takes 16 columns of a key
+// in one load, rows of 64 bytes without a swizzle, so that eight lanes read 128 bytes in a row.  V's
+// come by transposing loads of 16-bit pairs (two columns of a key), whose bytes are dealt to two product
+// rows.  With K in fp16 too, 64 keys a tile, 16 a warp, and scales looked up for each key of a tile: 1900
+// instructions for 64 keys and 390 us for 64 tokens over 8192 to 16384.
 #pragma once
 
 #include "paged.cuh"
@@ -48,7 +49,7 @@ constexpr int kPmMinTiles = 2;   // tiles of a CTA's range: fewer only add parts
 // A unit's set-up and end count as 8 tiles, and cuts less than 8 from a unit's edge move to it
 // (paged.cuh).  0 and 0 / 8 and 8: one token each of 64 sequences of 150 to 300 tokens 36.4 / 26.8 us,
 // of 500 to 1000 50.8 / 46.4, of 8192 to 16384 465 / 461.
-constexpr int kPmTol = 8, kPmFix = 8;
+constexpr int kPmTol = 8, kPmFix = 8;  // in tiles of 64 keys
 
 template <int kD, int kRT, bool kQ8>
 struct PmCfg {
@@ -58,17 +59,18 @@ struct PmCfg {
   static constexpr int kWarps = kD == 256 || kD / 16 * kNT * 4 > 64 ? 4 : 8;
   static constexpr int kConsumers = kWarps * 32;
   static constexpr int kThreads = kConsumers + 32 * kPmProducers;
+  static constexpr int kKeys = kQ8 ? 2 * kPmKeys : kPmKeys;  // of a tile
+  static constexpr int kWarpKeys = kKeys / 4;
+  static constexpr int kTol = kPmTol * kPmKeys / kKeys, kFix = kPmFix * kPmKeys / kKeys;
   static constexpr int kElt = kQ8 ? 1 : 2;
   static constexpr int kBlock = 512 * kElt;             // 8 rows of 64 columns
   static constexpr int kGroup = kDB * kBlock;           // 8 rows of a K or V tile: [column block][8][64 columns]
-  static constexpr int kTile = kPmKeys / 8 * kGroup;
-  static constexpr int kStages = (kD == 64 ? 8 : kD == 128 ? (kRT <= 16 ? 6 : 5) : 3) * (kQ8 ? 2 : 1);  // of K and V
-  static constexpr int kBars = kQ8 ? 16 : 8;            // barriers for as many
+  static constexpr int kTile = kKeys / 8 * kGroup;
+  static constexpr int kStages = kD == 64 ? 8 : kD == 128 ? (kRT <= 16 ? 6 : 5) : 3;  // of K and V
   // bytes: ldmatrix rows, or (kQ8) the 8-byte loads of four rows, on different banks
   static constexpr int kQStride = kD * 2 + (kQ8 ? 8 : 16);
-  // K or V fragments loaded at once (kQ8: of V; as registers allow)
-  static constexpr int kBatch = kQ8 && kNT > 2 ? 2 : kQ8 && kNT > 1 ? 4 : kD == 64 || kNT > 2 ? 4 : 8;
-  static constexpr int kAhead = kNT == 1 ? 4 : 2;       // kQ8: turns that scales are looked up ahead
+  // K or V fragments loaded at once (kQ8: of V, as registers allow)
+  static constexpr int kBatch = kQ8 && kNT > 2 ? 2 : (kQ8 && kNT > 1) || kD == 64 || kNT > 2 ? 4 : 8;
   static constexpr bool kQRegs = kNT * kD <= 256;       // queries stay in registers
   // the unit's queries, masks and tree; its O at the end
   static constexpr int kOffU = kStages * 2 * kTile;
@@ -80,7 +82,7 @@ struct PmCfg {
   static constexpr int kRegions = kD == 256 ? 1 : kD == 128 && kRT == 16 ? 2 : kWarps / 2;
   static constexpr int kOBytes = kRegions * kRT * kOStride * 4;
   static constexpr int kOffBar = kOffU + (kInBytes > kOBytes ? kInBytes : kOBytes);
-  static constexpr int kSmem = kOffBar + 32 * kBars + 1024;
+  static constexpr int kSmem = kOffBar + 256 + 1024;
   // a slot's tiles alternate between no two groups: a group that skipped a slot's earlier tile
   // could take that tile's unfinished phase for its own finished one
   static_assert(kWarps == 4 || kStages % 2 == 0, "each slot belongs to one group");
@@ -89,10 +91,9 @@ struct PmCfg {
   static_assert(kD / 16 * kNT * 4 <= 128, "O fits in registers");
 };
 
-template <int kBars>
 struct PmBars {
-  uint64_t full[kBars];
-  uint64_t empty[kBars];
+  uint64_t full[8];
+  uint64_t empty[8];
   int abort;
 };
 
@@ -131,20 +132,28 @@ __device__ __forceinline__ void pm_mma_f16(float (&d)[4], const uint32_t (&a)[4]
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void pm_mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                            uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 __device__ __forceinline__ uint32_t pm_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// Queries are held times 2^this, by the largest exponent field of their row: below 2^14.  A row that is not
+// Queries are held times 2^this, by the largest exponent field of their row: below 2^8.  A row that is not
 // finite stays as it is.
-__device__ __forceinline__ int pm_query_shift(int exponent) { return exponent == 255 ? 0 : min(127, 140 - exponent); }
+__device__ __forceinline__ int pm_query_shift(int exponent) { return exponent == 255 ? 0 : min(127, 134 - exponent); }
 
 // The next unit of this CTA: of its range, or the cluster's one unit, whether it has work or not.
 // The producers and the consumers walk the same sequence of them.
-template <int kRT, bool kStream>
+template <int kRT, bool kStream, int kKeys>
 __device__ __forceinline__ bool pm_next(const PagedAttn& a, UnitWalk& w, int splits) {
-  if constexpr (kStream) return unit_next(a, w, kRT, kPmKeys);
+  if constexpr (kStream) return unit_next(a, w, kRT, kKeys);
   if (w.loaded == w.b) return false;
   bool bad;
   w.loaded = w.b;
@@ -152,7 +161,7 @@ __device__ __forceinline__ bool pm_next(const PagedAttn& a, UnitWalk& w, int spl
   w.n = paged_rows(a, w.b, w.P, &bad);
   if (w.n == 0) w.P = 0;
   if (threadIdx.x == 0 && (bad || paged_cut(a, w.b, w.P, w.n))) set_dev_status(a.dev_status, TV_DEV_BAD_PAGE);
-  const int T_u = unit_tiles(a, w.P, w.n, w.rt, kRT, kPmKeys), part = blockIdx.x;
+  const int T_u = unit_tiles(a, w.P, w.n, w.rt, kRT, kKeys), part = blockIdx.x;
   w.t0 = (int)((long long)T_u * part / splits);
   w.t1 = (int)((long long)T_u * (part + 1) / splits);
   return true;
@@ -163,12 +172,10 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
     paged_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, PagedAttn a,
                      int splits, int row_tiles, int wide) {
   using C = PmCfg<kD, kRT, kQ8>;
-  using Bars = PmBars<C::kBars>;
-  static_assert(sizeof(Bars) <= 32 * C::kBars && C::kStages <= C::kBars, "room for the barriers");
   ptx::griddep_launch_dependents();
   extern __shared__ unsigned char pm_raw[];
   unsigned char* sm = pm_raw + ((1024u - (ptx::smem_addr(pm_raw) & 1023u)) & 1023u);
-  Bars* bars = reinterpret_cast<Bars*>(sm + C::kOffBar);
+  PmBars* bars = reinterpret_cast<PmBars*>(sm + C::kOffBar);
   volatile int* abort_flag = &bars->abort;
   __shared__ unsigned long long s_red[kPagedRed];
   __shared__ int s_lo[kRT], s_hi[kRT], s_first_pad, s_last;
@@ -192,7 +199,7 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
   UnitWalk w{};
   w.loaded = -1;
   if constexpr (kStream) {
-    sp = paged_span(a, kRT, kPmKeys, kPmMinTiles, s_red, kPmTol, kPmFix);
+    sp = paged_span(a, kRT, C::kKeys, kPmMinTiles, s_red, C::kTol, C::kFix);
     __syncthreads();
     w = unit_walk(sp);
   } else {
@@ -210,7 +217,7 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
     // ahead and checked when it is used
     const int per_piece = 2 * (wide ? 1 : C::kDB);
     const int box_shift = min(a.page_shift, C::kDB == 1 || wide ? 6 : 3);
-    const int boxes = (kPmKeys >> box_shift) * per_piece;
+    const int boxes = (C::kKeys >> box_shift) * per_piece;
     const int mine = boxes / kPmProducers + (warp - C::kWarps < boxes % kPmProducers);
     const int box = lane * kPmProducers + warp - C::kWarps;  // this lane's
     const int pi = box / per_piece, part = box % per_piece;
@@ -218,7 +225,7 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
     // where it goes in a stage: K or V, 8-row group, column block
     const int off = (part & 1) * C::kTile + ((pi << box_shift) >> 3) * C::kGroup + (part >> 1) * C::kBlock;
     int issued = 0, counted = -1, active = 0;  // a sequence's active rows, once counted
-    while (pm_next<kRT, kStream>(a, w, splits)) {
+    while (pm_next<kRT, kStream, C::kKeys>(a, w, splits)) {
       if (counted != w.b) {
         int pad = w.n;
         if (a.parent)
@@ -228,16 +235,16 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
         counted = w.b;
       }
       const int unit = unit_rows(a, w.n, w.rt, kRT);
-      const int lo = unit_lo(a, w.P, w.rt, kRT), tile0 = lo / kPmKeys;
+      const int lo = unit_lo(a, w.P, w.rt, kRT), tile0 = lo / C::kKeys;
       const int hi = min(w.P + active, w.P + (w.rt * kRT + unit - 1) / a.G + 1);
       const int32_t* table = a.table + (size_t)w.b * a.max_pages;
       // whether this lane's box in tile t holds a needed row, and its table entry
       auto needed = [&](int t) -> bool {
-        const int j = (tile0 + t) * kPmKeys + (pi << box_shift);
+        const int j = (tile0 + t) * C::kKeys + (pi << box_shift);
         return t < w.t1 && lane < mine && j < hi && j + (1 << box_shift) > lo;
       };
       auto entry = [&](int t) -> int {
-        return needed(t) ? table[((tile0 + t) * kPmKeys + (pi << box_shift)) >> a.page_shift] : 0;
+        return needed(t) ? table[((tile0 + t) * C::kKeys + (pi << box_shift)) >> a.page_shift] : 0;
       };
       int next = entry(w.t0);
       for (int t = w.t0; t < w.t1; ++t, ++it) {
@@ -256,7 +263,7 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
         if (lane == 0) ptx::mbar_arrive_expect_tx(&bars->full[slot], __popc(have) * box_bytes);
         __syncwarp();
         if (page >= 0) {
-          const int row = ((tile0 + t) * kPmKeys + (pi << box_shift)) & ((1 << a.page_shift) - 1);
+          const int row = ((tile0 + t) * C::kKeys + (pi << box_shift)) & ((1 << a.page_shift) - 1);
           unsigned char* dst = sm + slot * 2 * C::kTile + off;
           const CUtensorMap* tm = (part & 1) ? &tmV : &tmK;
           if (C::kDB > 1 && wide)
@@ -303,10 +310,10 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
         if (s_m[k][rr] != -INFINITY) L = fmaf(s_l[k][rr], ptx::ex2(s_m[k][rr] - M), L);
       return make_float2(M, L);
     };
-    while (pm_next<kRT, kStream>(a, w, splits)) {
+    while (pm_next<kRT, kStream, C::kKeys>(a, w, splits)) {
       rows = unit_rows(a, w.n, w.rt, kRT);
       r0 = w.rt * kRT;
-      const int lo = unit_lo(a, w.P, w.rt, kRT), tile0 = lo / kPmKeys;
+      const int lo = unit_lo(a, w.P, w.rt, kRT), tile0 = lo / C::kKeys;
       if (kStream) cons_sync();  // the previous unit's O has been read
       n_act = w.n;
       if (a.parent) {
@@ -353,13 +360,20 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
           if (rr >= kRT) break;
           const float f = q8_two(pm_query_shift(s_qexp[rr]));
           const uint32_t x[4] = {qraw[k].x, qraw[k].y, qraw[k].z, qraw[k].w};
-          uint2* to = reinterpret_cast<uint2*>(sQ + rr * C::kQStride + ch * 16);
-          uint32_t h[4];
+          // row: the nearest e4m3 numbers, then the nearest to what they leave
+          unsigned char* to = sQ + rr * C::kQStride + ch * 8;
+          uint32_t hi[2], left[2];
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
-            h[u] = pm_f16x2(__uint_as_float(x[u] << 16) * f, __uint_as_float(x[u] & 0xffff0000u) * f);
-          to[0] = make_uint2(h[0], h[1]);
-          to[1] = make_uint2(h[2], h[3]);
+          for (int u = 0; u < 2; ++u) {
+            const float x0 = __uint_as_float(x[2 * u] << 16) * f, x1 = __uint_as_float(x[2 * u] & 0xffff0000u) * f;
+            const float x2 = __uint_as_float(x[2 * u + 1] << 16) * f;
+            const float x3 = __uint_as_float(x[2 * u + 1] & 0xffff0000u) * f;
+            hi[u] = q8_code4(x0, x1, x2, x3);
+            const float4 y = q8_numbers(hi[u], 1.f);
+            left[u] = q8_code4(x0 - y.x, x1 - y.y, x2 - y.z, x3 - y.w);
+          }
+          *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
+          *reinterpret_cast<uint2*>(to + kD) = make_uint2(left[0], left[1]);
         }
       }
       for (int e = ct; !kQ8 && e < kRT * (kD / 8); e += C::kConsumers) {
@@ -399,8 +413,9 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
       // queries as the products' B operand: rows (lane & 7), two 16-column steps a load
       const uint32_t qaddr = ptx::smem_addr(sQ + (lane & 7) * C::kQStride + (lane >> 3) * 16);
       uint32_t qf[C::kQRegs ? kD / 32 : 1][C::kNT][4];
-      // kQ8: rows (lane >> 2) of a product, columns 64 j + 16 (lane & 3) + 4 s.. of step 4 j + s
-      const unsigned char* qrow = sQ + (lane >> 2) * C::kQStride + (lane & 3) * 32;
+      // kQ8: rows (lane >> 2) of a product, columns 64 j + 16 (lane & 3) + 8 s.. of step 2 j + s; the two parts are
+      // kD bytes apart
+      const unsigned char* qrow = sQ + (lane >> 2) * C::kQStride + (lane & 3) * 16;
       float row_f[C::kNT][2];
       if constexpr (kQ8) {
 #pragma unroll
@@ -414,8 +429,8 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
             for (int nt = 0; nt < C::kNT; ++nt)
 #pragma unroll
               for (int u = 0; u < 2; ++u) {
-                const int kk = 2 * k2 + u;
-                const uint2 v = *reinterpret_cast<const uint2*>(qrow + nt * 8 * C::kQStride + (kk >> 2) * 128 + (kk & 3) * 8);
+                const uint2 v =
+                    *reinterpret_cast<const uint2*>(qrow + nt * 8 * C::kQStride + u * kD + (k2 >> 1) * 64 + (k2 & 1) * 8);
                 qf[k2][nt][2 * u] = v.x, qf[k2][nt][2 * u + 1] = v.y;
               }
         }
@@ -427,10 +442,9 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
       }
       float o[kD / 16][C::kNT][4];
       float m[C::kNT][2], l[C::kNT][2];
-      float mw[C::kNT][2];  // kQ8: the reference of P, of weights times values' scales
 #pragma unroll
       for (int nt = 0; nt < C::kNT; ++nt) {
-        m[nt][0] = m[nt][1] = mw[nt][0] = mw[nt][1] = -INFINITY;
+        m[nt][0] = m[nt][1] = -INFINITY;
         l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
         for (int k = 0; k < kD / 16; ++k)
@@ -438,58 +452,64 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
           for (int u = 0; u < 4; ++u) o[k][nt][u] = 0.f;
       }
 
-      // kQ8: the scale bytes of this warp's 16 keys (lanes 0..15 keys', 16..31 values'), read kAhead turns of the
-      // warp ahead, and their pages, twice that.  One turn and two, 64 tokens over 8192 to 16384: 368 us
+      // kQ8: scales (K's byte, V's in bits 8..15).  Blocks of 16 keys or more: lane l looks up those of the warp's
+      // keys 16 (l & 1).. of its turn l / 2 from here, for 16 turns at once, 16 turns ahead.  Shorter ones: of its
+      // key l, two turns ahead.
       constexpr int kTurn = C::kWarps == 8 ? 2 : 1;
       const int32_t* table = a.table + (size_t)w.b * a.max_pages;
-      auto scale_key = [&](int t) -> int { return (tile0 + t) * kPmKeys + wk * 16 + (lane & 15); };
+      const bool fine = kQ8 && a.block_shift < 4;
+      auto scale_key = [&](int t) -> int {
+        return fine ? (tile0 + t) * C::kKeys + wk * 32 + lane
+                    : (tile0 + t + (lane >> 1) * kTurn) * C::kKeys + wk * 32 + (lane & 1) * 16;
+      };
       auto scale_page = [&](int t) -> int {
         const int j = scale_key(t);
-        return t < w.t1 && j >= lo && j < hi ? table[j >> a.page_shift] : -1;
+        return (fine ? t : t + (lane >> 1) * kTurn) < w.t1 && j + (fine ? 0 : 15) >= lo && j < hi ? table[j >> a.page_shift]
+                                                                                                  : -1;
       };
-      auto scale_byte = [&](int t, int page) -> int {
-        if (page < 0 || page >= a.num_pages) return 127;
-        const int in_page = scale_key(t) & ((1 << a.page_shift) - 1);
-        const size_t block = (((size_t)page * a.Hkv + w.hk) << (a.page_shift - a.block_shift)) + (in_page >> a.block_shift);
-        return lane < 16 ? a.ks[block] : a.vs[block];
+      auto scale_bytes = [&](int t, int page) -> int {
+        if (page < 0 || page >= a.num_pages) return 127 | 127 << 8;
+        const size_t block = (((size_t)page * a.Hkv + w.hk) << (a.page_shift - a.block_shift)) +
+                             ((scale_key(t) & ((1 << a.page_shift) - 1)) >> a.block_shift);
+        return a.ks[block] | a.vs[block] << 8;
       };
-      constexpr int kAhead = C::kAhead;
-      int pages_to[2 * kAhead], scales_to[kAhead];
+      const int scale_step = fine ? kTurn : 16 * kTurn;
+      int scales_now = 0, scales_next = 0, pages_next = -1, turn = 0;
       if constexpr (kQ8) {
         const int first = w.t0 + (C::kWarps == 8 && (it & 1) != group ? 1 : 0);
-#pragma unroll
-        for (int k = 0; k < 2 * kAhead; ++k) pages_to[k] = scale_page(first + k * kTurn);
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) scales_to[k] = scale_byte(first + k * kTurn, pages_to[k]);
+        const int p0 = scale_page(first), p1 = scale_page(first + scale_step);
+        pages_next = scale_page(first + 2 * scale_step);
+        scales_now = scale_bytes(first, p0);
+        scales_next = scale_bytes(first + scale_step, p1);
       }
       for (int t = w.t0; t < w.t1; ++t, ++it) {
         if (C::kWarps == 8 && (it & 1) != group) continue;
         const int slot = it % C::kStages;
-        int scale_now = 127;
+        int my_scales = 0;  // of this turn: lane 2 (turn & 15).., or every key's
         if constexpr (kQ8) {
-          scale_now = scales_to[0];
-#pragma unroll
-          for (int k = 0; k + 1 < kAhead; ++k) scales_to[k] = scales_to[k + 1];
-          scales_to[kAhead - 1] = scale_byte(t + kAhead * kTurn, pages_to[kAhead]);
-#pragma unroll
-          for (int k = kAhead; k + 1 < 2 * kAhead; ++k) pages_to[k] = pages_to[k + 1];
-          pages_to[2 * kAhead - 1] = scale_page(t + 2 * kAhead * kTurn);
+          if (turn > 0 && (fine || turn % 16 == 0)) {
+            scales_now = scales_next;
+            scales_next = scale_bytes(t + scale_step, pages_next);
+            pages_next = scale_page(t + 2 * scale_step);
+          }
+          my_scales = scales_now;
+          ++turn;
         }
         if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars->full[slot], (it / C::kStages) & 1, abort_flag));
         if (!ok) continue;
-        const int j0 = (tile0 + t) * kPmKeys + wk * 16;  // this warp's 16 keys
-        unsigned char* sK = sm + slot * 2 * C::kTile + wk * 2 * C::kGroup;
+        const int j0 = (tile0 + t) * C::kKeys + wk * C::kWarpKeys;  // this warp's keys
+        unsigned char* sK = sm + slot * 2 * C::kTile + wk * (C::kWarpKeys / 8) * C::kGroup;
         unsigned char* sV = sK + C::kTile;
-        if (j0 >= hi || j0 + 16 <= lo) {  // none of them
+        if (j0 >= hi || j0 + C::kWarpKeys <= lo) {  // none of them
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&bars->empty[slot]);
           continue;
         }
-        const bool edge = j0 < lo || j0 + 16 > hi;
+        const bool edge = j0 < lo || j0 + C::kWarpKeys > hi;
         if (edge) {
           // V rows that were not fetched or may hold anything, NaN included: zero
           constexpr int kRowChunks = 4 * C::kElt;  // 16-byte chunks of a row in a column block
-          for (int e = lane; e < 16 * C::kDB * kRowChunks; e += 32) {
+          for (int e = lane; e < C::kWarpKeys * C::kDB * kRowChunks; e += 32) {
             const int rr = e / (C::kDB * kRowChunks), rest = e % (C::kDB * kRowChunks);
             if (j0 + rr < lo || j0 + rr >= hi)
               *reinterpret_cast<uint4*>(sV + (rr >> 3) * C::kGroup + (rest / kRowChunks) * C::kBlock +
@@ -498,186 +518,250 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
           ptx::fence_proxy_async_smem();  // before the slot is refilled
           __syncwarp();
         }
-        // K as the A operand: keys (lane & 15), column chunks kk * 2 + (lane >> 4).  A batch's loads are
-        // issued before its products, so that they wait for shared memory once
-        const uint32_t kaddr = ptx::smem_addr(sK + ((lane >> 3) & 1) * C::kGroup + (lane & 7) * 128);
-        float s[C::kNT][2][4];  // two chains each: even and odd steps
-#pragma unroll
-        for (int nt = 0; nt < C::kNT; ++nt)
-#pragma unroll
-          for (int u = 0; u < 4; ++u) s[nt][0][u] = s[nt][1][u] = 0.f;
         if constexpr (kQ8) {
-          const unsigned char* krow = sK + (lane >> 2) * 64 + (lane & 3) * 16;
+          // ---- 16 keys at a time; with one row tile both together, so that their latencies overlap
+          constexpr int kSubs = C::kNT == 1 && kD <= 128 ? 2 : 1;
+          const bool masked = j0 < full_lo || j0 + 32 > full_hi || edge;
+#pragma unroll 1
+          for (int sub0 = 0; sub0 < 2; sub0 += kSubs) {
+            float s[kSubs][C::kNT][2][4];  // queries' two parts
+            uint32_t pf[kSubs][C::kNT][2];
 #pragma unroll
-          for (int j = 0; j < C::kDB; ++j) {
-            const uint4 k0 = *reinterpret_cast<const uint4*>(krow + j * C::kBlock);
-            const uint4 k1 = *reinterpret_cast<const uint4*>(krow + C::kGroup + j * C::kBlock);
-            const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+            for (int u = 0; u < kSubs; ++u) {
 #pragma unroll
-            for (int st = 0; st < 4; ++st) {
-              const int kk = 4 * j + st;
-              uint32_t kf[4];
-              q8_half4(w0[st], kf[0], kf[2]);
-              q8_half4(w1[st], kf[1], kf[3]);
+              for (int nt = 0; nt < C::kNT; ++nt)
 #pragma unroll
-              for (int nt = 0; nt < C::kNT; ++nt) {
-                if constexpr (C::kQRegs) {
-                  pm_mma_f16(s[nt][kk & 1], kf, qf[kk >> 1][nt][(kk & 1) * 2], qf[kk >> 1][nt][(kk & 1) * 2 + 1]);
-                } else {
-                  const uint2 q2 = *reinterpret_cast<const uint2*>(qrow + nt * 8 * C::kQStride + j * 128 + st * 8);
-                  pm_mma_f16(s[nt][kk & 1], kf, q2.x, q2.y);
+                for (int x = 0; x < 4; ++x) s[u][nt][0][x] = s[u][nt][1][x] = 0.f;
+              const unsigned char* krow = sK + (sub0 + u) * 2 * C::kGroup + (lane >> 2) * 64 + (lane & 3) * 16;
+#pragma unroll
+              for (int j = 0; j < C::kDB; ++j) {
+                const uint4 k0 = *reinterpret_cast<const uint4*>(krow + j * C::kBlock);
+                const uint4 k1 = *reinterpret_cast<const uint4*>(krow + C::kGroup + j * C::kBlock);
+#pragma unroll
+                for (int nt = 0; nt < C::kNT; ++nt)
+#pragma unroll
+                  for (int part = 0; part < 2; ++part) {
+                    uint2 q0, q1;
+                    if constexpr (C::kQRegs) {
+                      q0 = make_uint2(qf[2 * j][nt][2 * part], qf[2 * j][nt][2 * part + 1]);
+                      q1 = make_uint2(qf[2 * j + 1][nt][2 * part], qf[2 * j + 1][nt][2 * part + 1]);
+                    } else {
+                      const unsigned char* at = qrow + nt * 8 * C::kQStride + part * kD + j * 64;
+                      q0 = *reinterpret_cast<const uint2*>(at);
+                      q1 = *reinterpret_cast<const uint2*>(at + 8);
+                    }
+                    pm_mma_e4m3(s[u][nt][part], k0.x, k1.x, k0.y, k1.y, q0.x, q0.y);
+                    pm_mma_e4m3(s[u][nt][part], k0.z, k1.z, k0.w, k1.w, q1.x, q1.y);
+                  }
+              }
+            }
+            // scores; those of a row's running reference count with the value's scale
+            float val_e[kSubs][2], val_f[kSubs][2];  // e and 2^-e of keys kg, kg + 8
+            bool grow = false;
+#pragma unroll
+            for (int u = 0; u < kSubs; ++u) {
+              float key_f[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int from = fine ? (sub0 + u) * 16 + kg + 8 * e : ((turn - 1) & 15) * 2 + sub0 + u;
+                const int both = __shfl_sync(0xffffffffu, my_scales, from);
+                key_f[e] = __uint_as_float((uint32_t)(both & 255) << 23);
+                val_e[u][e] = (float)((both >> 8) - 127);
+                val_f[u][e] = __uint_as_float((uint32_t)max(1, 254 - (both >> 8)) << 23);
+              }
+#pragma unroll
+              for (int nt = 0; nt < C::kNT; ++nt)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                  float z = (s[u][nt][0][x] + s[u][nt][1][x]) * (key_f[x >> 1] * row_f[nt][x & 1]);
+                  if constexpr (kCap == kTanhCap) z = soft_tanh(z * ck);
+                  if constexpr (kCap == kLargeCap) z = capped_score(z * a.scale, a.cap, ck);
+                  z = fmaf(z, c, val_e[u][x >> 1]);
+                  if (masked) {
+                    const int rr = nt * 8 + rg + (x & 1), j = j0 + (sub0 + u) * 16 + kg + (x >> 1) * 8;
+                    bool vis = j >= s_lo[rr] && j < s_hi[rr];
+                    if (!vis && a.parent && j >= w.P && j < hi)
+                      vis = (s_vis[rr][(j - w.P) >> 5] >> ((j - w.P) & 31)) & 1u;
+                    if (!vis) z = -INFINITY;
+                  }
+                  s[u][nt][0][x] = z;
+                  grow |= z > m[nt][x & 1] + 8.f;
+                }
+            }
+            if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+              for (int nt = 0; nt < C::kNT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  float mx = fmaxf(s[0][nt][0][e], s[0][nt][0][e + 2]);
+                  if (kSubs == 2) mx = fmaxf(mx, fmaxf(s[kSubs - 1][nt][0][e], s[kSubs - 1][nt][0][e + 2]));
+#pragma unroll
+                  for (int x = 4; x < 32; x *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+                  if (mx > m[nt][e]) {
+                    const float f = ptx::ex2(m[nt][e] - mx);  // 0 from -inf
+                    m[nt][e] = mx;
+                    l[nt][e] *= f;
+#pragma unroll
+                    for (int k = 0; k < kD / 16; ++k) {
+                      o[k][nt][e] *= f;
+                      o[k][nt][e + 2] *= f;
+                    }
+                  }
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < C::kNT; ++nt) {
+              // P times 2^7: at most 2^15
+              const float b0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0] - 7.f;
+              const float b1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1] - 7.f;
+#pragma unroll
+              for (int u = 0; u < kSubs; ++u) {
+                const float e0 = ptx::ex2(s[u][nt][0][0] - b0), e1 = ptx::ex2(s[u][nt][0][1] - b1);
+                const float e2 = ptx::ex2(s[u][nt][0][2] - b0), e3 = ptx::ex2(s[u][nt][0][3] - b1);
+                l[nt][0] = fmaf(e0, val_f[u][0], fmaf(e2, val_f[u][1], l[nt][0]));
+                l[nt][1] = fmaf(e1, val_f[u][0], fmaf(e3, val_f[u][1], l[nt][1]));
+                pf[u][nt][0] = pm_transpose(pm_f16x2(e0, e1));
+                pf[u][nt][1] = pm_transpose(pm_f16x2(e2, e3));
+              }
+            }
+            // V^T: lane l names key (l & 7) + 8 ((l >> 3) & 1), columns 16 (k + (l >> 4)).. of two steps at once
+#pragma unroll
+            for (int u = 0; u < kSubs; ++u) {
+              const uint32_t vaddr =
+                  ptx::smem_addr(sV + (sub0 + u) * 2 * C::kGroup + ((lane >> 3) & 1) * C::kGroup + (lane & 7) * 64);
+#pragma unroll
+              for (int k0 = 0; k0 < kD / 16; k0 += C::kBatch) {
+                uint32_t raw[C::kBatch / 2][4];
+#pragma unroll
+                for (int i = 0; i < C::kBatch / 2; ++i) {
+                  const int k = k0 + 2 * i + (lane >> 4);
+                  pm_ldsm4t(raw[i], vaddr + (k >> 2) * C::kBlock + (((k & 3) ^ ((lane & 7) >> 1)) << 4));
+                }
+#pragma unroll
+                for (int i = 0; i < C::kBatch; ++i) {
+                  // a word's bytes: columns 2g, 2g + 1 of key 2c, then of key 2c + 1; a product row is one column
+                  uint32_t vf[4];
+#pragma unroll
+                  for (int x = 0; x < 2; ++x) {
+                    const uint32_t word = raw[i >> 1][(i & 1) * 2 + x];
+                    q8_half4(__byte_perm(word, 0, 0x3120), vf[2 * x], vf[2 * x + 1]);
+                  }
+#pragma unroll
+                  for (int nt = 0; nt < C::kNT; ++nt) pm_mma_f16(o[k0 + i][nt], vf, pf[u][nt][0], pf[u][nt][1]);
                 }
               }
             }
           }
-        }
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&bars->empty[slot]);
+          continue;
+        } else {
+          // K as the A operand: keys (lane & 15), column chunks kk * 2 + (lane >> 4).  A batch's loads are
+          // issued before its products, so that they wait for shared memory once
+          const uint32_t kaddr = ptx::smem_addr(sK + ((lane >> 3) & 1) * C::kGroup + (lane & 7) * 128);
+          float s[C::kNT][2][4];  // two chains each: even and odd steps
 #pragma unroll
-        for (int k0 = 0; !kQ8 && k0 < kD / 16; k0 += C::kBatch) {
-          uint32_t kf[C::kBatch][4];
+          for (int nt = 0; nt < C::kNT; ++nt)
 #pragma unroll
-          for (int i = 0; i < C::kBatch; ++i) {
-            const int kk = k0 + i, ch = (kk & 3) * 2 + (lane >> 4);
-            pm_ldsm4(kf[i], kaddr + (kk >> 2) * 1024 + ((ch ^ (lane & 7)) << 4));
-          }
+            for (int u = 0; u < 4; ++u) s[nt][0][u] = s[nt][1][u] = 0.f;
 #pragma unroll
-          for (int i = 0; i < C::kBatch; ++i) {
-            const int kk = k0 + i;
+          for (int k0 = 0; k0 < kD / 16; k0 += C::kBatch) {
+            uint32_t kf[C::kBatch][4];
 #pragma unroll
-            for (int nt = 0; nt < C::kNT; ++nt) {
-              if constexpr (C::kQRegs) {
-                pm_mma(s[nt][kk & 1], kf[i], qf[kk >> 1][nt][(kk & 1) * 2], qf[kk >> 1][nt][(kk & 1) * 2 + 1]);
-              } else {
-                uint32_t q2[2];
-                pm_ldsm2(q2, ptx::smem_addr(sQ + (nt * 8 + (lane & 7)) * C::kQStride + kk * 32 + ((lane >> 3) & 1) * 16));
-                pm_mma(s[nt][kk & 1], kf[i], q2[0], q2[1]);
+            for (int i = 0; i < C::kBatch; ++i) {
+              const int kk = k0 + i, ch = (kk & 3) * 2 + (lane >> 4);
+              pm_ldsm4(kf[i], kaddr + (kk >> 2) * 1024 + ((ch ^ (lane & 7)) << 4));
+            }
+#pragma unroll
+            for (int i = 0; i < C::kBatch; ++i) {
+              const int kk = k0 + i;
+#pragma unroll
+              for (int nt = 0; nt < C::kNT; ++nt) {
+                if constexpr (C::kQRegs) {
+                  pm_mma(s[nt][kk & 1], kf[i], qf[kk >> 1][nt][(kk & 1) * 2], qf[kk >> 1][nt][(kk & 1) * 2 + 1]);
+                } else {
+                  uint32_t q2[2];
+                  pm_ldsm2(q2, ptx::smem_addr(sQ + (nt * 8 + (lane & 7)) * C::kQStride + kk * 32 + ((lane >> 3) & 1) * 16));
+                  pm_mma(s[nt][kk & 1], kf[i], q2[0], q2[1]);
+                }
               }
             }
           }
-        }
-        // V^T as the A operand: transposed 8 x 8 blocks of (columns, keys); the first batch is
-        // fetched while the scores are turned into weights
-        const uint32_t vaddr = ptx::smem_addr(sV + (lane >> 4) * C::kGroup + (lane & 7) * 128);
-        uint32_t vf[C::kBatch][4];
-        // kQ8: lane l names key (l & 7) + 8 ((l >> 3) & 1), columns 16 (k + (l >> 4)).. of two steps at once
-        const uint32_t vaddr8 = ptx::smem_addr(sV + ((lane >> 3) & 1) * C::kGroup + (lane & 7) * 64);
-        auto load_v = [&](int k0) {
-          if constexpr (kQ8) {
-#pragma unroll
-            for (int i = 0; i < C::kBatch; i += 2) {
-              const int k = k0 + i + (lane >> 4);
-              uint32_t r[4];
-              pm_ldsm4t(r, vaddr8 + (k >> 2) * C::kBlock + (((k & 3) ^ ((lane & 7) >> 1)) << 4));
-#pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                // bytes: column 2g of keys 2c, 2c + 1, then column 2g + 1 of them
-                const uint32_t by_column = __byte_perm(r[u], 0, 0x3120);
-                q8_half4(by_column, vf[i + (u >> 1)][(u & 1) * 2], vf[i + (u >> 1)][(u & 1) * 2 + 1]);
-              }
-            }
-          } else {
+          // V^T as the A operand: transposed 8 x 8 blocks of (columns, keys); the first batch is
+          // fetched while the scores are turned into weights
+          const uint32_t vaddr = ptx::smem_addr(sV + (lane >> 4) * C::kGroup + (lane & 7) * 128);
+          uint32_t vf[C::kBatch][4];
+          auto load_v = [&](int k0) {
 #pragma unroll
             for (int i = 0; i < C::kBatch; ++i) {
               const int k = k0 + i, ch = (k & 3) * 2 + ((lane >> 3) & 1);
               pm_ldsm4t(vf[i], vaddr + (k >> 2) * 1024 + ((ch ^ (lane & 7)) << 4));
             }
-          }
-        };
-        load_v(0);
-        const bool masked = j0 < full_lo || j0 + 16 > full_hi || edge;
-        bool grow = false;
-        float key_f[2] = {1.f, 1.f}, val_e[2] = {0.f, 0.f};  // kQ8: of keys kg, kg + 8
-        if constexpr (kQ8) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            key_f[e] = __uint_as_float((uint32_t)__shfl_sync(0xffffffffu, scale_now, kg + 8 * e) << 23);
-            val_e[e] = (float)(__shfl_sync(0xffffffffu, scale_now, 16 + kg + 8 * e) - 127);
-          }
-        }
-#pragma unroll
-        for (int nt = 0; nt < C::kNT; ++nt)
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            float z = s[nt][0][u] + s[nt][1][u];
-            if constexpr (kQ8) z *= key_f[u >> 1] * row_f[nt][u & 1];
-            if constexpr (kCap == kTanhCap) z = soft_tanh(z * ck);
-            if constexpr (kCap == kLargeCap) z = capped_score(z * a.scale, a.cap, ck);
-            z *= c;
-            if (masked) {
-              const int rr = nt * 8 + rg + (u & 1), j = j0 + kg + (u >> 1) * 8;
-              bool vis = j >= s_lo[rr] && j < s_hi[rr];
-              if (!vis && a.parent && j >= w.P && j < hi)
-                vis = (s_vis[rr][(j - w.P) >> 5] >> ((j - w.P) & 31)) & 1u;
-              if (!vis) z = -INFINITY;
-            }
-            s[nt][0][u] = z;
-            grow |= z > m[nt][u & 1] + 8.f;
-            if constexpr (kQ8) grow |= z + val_e[u >> 1] > mw[nt][u & 1] + 8.f;
-          }
-        // a row's running reference moves when a score exceeds it by 2^8
-        if (__any_sync(0xffffffffu, grow)) {
+          };
+          load_v(0);
+          const bool masked = j0 < full_lo || j0 + 16 > full_hi || edge;
+          bool grow = false;
 #pragma unroll
           for (int nt = 0; nt < C::kNT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float mx = fmaxf(s[nt][0][e], s[nt][0][e + 2]);
+            for (int u = 0; u < 4; ++u) {
+              float z = s[nt][0][u] + s[nt][1][u];
+              if constexpr (kCap == kTanhCap) z = soft_tanh(z * ck);
+              if constexpr (kCap == kLargeCap) z = capped_score(z * a.scale, a.cap, ck);
+              z *= c;
+              if (masked) {
+                const int rr = nt * 8 + rg + (u & 1), j = j0 + kg + (u >> 1) * 8;
+                bool vis = j >= s_lo[rr] && j < s_hi[rr];
+                if (!vis && a.parent && j >= w.P && j < hi)
+                  vis = (s_vis[rr][(j - w.P) >> 5] >> ((j - w.P) & 31)) & 1u;
+                if (!vis) z = -INFINITY;
+              }
+              s[nt][0][u] = z;
+              grow |= z > m[nt][u & 1] + 8.f;
+            }
+          // a row's running reference moves when a score exceeds it by 2^8
+          if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-              for (int x = 4; x < 32; x *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-              if constexpr (kQ8) {
-                if (mx > m[nt][e]) {
-                  l[nt][e] *= ptx::ex2(m[nt][e] - mx);  // 0 from -inf
-                  m[nt][e] = mx;
-                }
-                mx = fmaxf(s[nt][0][e] + val_e[0], s[nt][0][e + 2] + val_e[1]);
+            for (int nt = 0; nt < C::kNT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float mx = fmaxf(s[nt][0][e], s[nt][0][e + 2]);
 #pragma unroll
                 for (int x = 4; x < 32; x *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-              }
-              float(&ref)[C::kNT][2] = kQ8 ? mw : m;
-              if (mx > ref[nt][e]) {
-                const float f = ptx::ex2(ref[nt][e] - mx);  // 0 from -inf
-                ref[nt][e] = mx;
-                if constexpr (!kQ8) l[nt][e] *= f;
+                if (mx > m[nt][e]) {
+                  const float f = ptx::ex2(m[nt][e] - mx);  // 0 from -inf
+                  m[nt][e] = mx;
+                  l[nt][e] *= f;
 #pragma unroll
-                for (int k = 0; k < kD / 16; ++k) {
-                  o[k][nt][e] *= f;
-                  o[k][nt][e + 2] *= f;
+                  for (int k = 0; k < kD / 16; ++k) {
+                    o[k][nt][e] *= f;
+                    o[k][nt][e + 2] *= f;
+                  }
                 }
               }
-            }
-        }
-        uint32_t pf[C::kNT][2];
-#pragma unroll
-        for (int nt = 0; nt < C::kNT; ++nt) {
-          const float b0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], b1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
-          const float e0 = ptx::ex2(s[nt][0][0] - b0), e1 = ptx::ex2(s[nt][0][1] - b1);
-          const float e2 = ptx::ex2(s[nt][0][2] - b0), e3 = ptx::ex2(s[nt][0][3] - b1);
-          l[nt][0] += e0 + e2;
-          l[nt][1] += e1 + e3;
-          if constexpr (kQ8) {
-            // P times 2^7: at most 2^15
-            const float w0 = mw[nt][0] == -INFINITY ? 0.f : mw[nt][0] - 7.f;
-            const float w1 = mw[nt][1] == -INFINITY ? 0.f : mw[nt][1] - 7.f;
-            pf[nt][0] = pm_transpose(pm_f16x2(ptx::ex2(s[nt][0][0] + val_e[0] - w0), ptx::ex2(s[nt][0][1] + val_e[0] - w1)));
-            pf[nt][1] = pm_transpose(pm_f16x2(ptx::ex2(s[nt][0][2] + val_e[1] - w0), ptx::ex2(s[nt][0][3] + val_e[1] - w1)));
-            continue;
           }
-          pf[nt][0] = pm_transpose(ptx::cvt_bf16x2(e0, e1));
-          pf[nt][1] = pm_transpose(ptx::cvt_bf16x2(e2, e3));
+          uint32_t pf[C::kNT][2];
+#pragma unroll
+          for (int nt = 0; nt < C::kNT; ++nt) {
+            const float b0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], b1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+            const float e0 = ptx::ex2(s[nt][0][0] - b0), e1 = ptx::ex2(s[nt][0][1] - b1);
+            const float e2 = ptx::ex2(s[nt][0][2] - b0), e3 = ptx::ex2(s[nt][0][3] - b1);
+            l[nt][0] += e0 + e2;
+            l[nt][1] += e1 + e3;
+            pf[nt][0] = pm_transpose(ptx::cvt_bf16x2(e0, e1));
+            pf[nt][1] = pm_transpose(ptx::cvt_bf16x2(e2, e3));
+          }
+#pragma unroll
+          for (int k0 = 0; k0 < kD / 16; k0 += C::kBatch) {
+            if (k0) load_v(k0);
+#pragma unroll
+            for (int i = 0; i < C::kBatch; ++i)
+#pragma unroll
+              for (int nt = 0; nt < C::kNT; ++nt) pm_mma(o[k0 + i][nt], vf[i], pf[nt][0], pf[nt][1]);
+          }
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&bars->empty[slot]);
         }
-#pragma unroll
-        for (int k0 = 0; k0 < kD / 16; k0 += C::kBatch) {
-          if (k0) load_v(k0);
-#pragma unroll
-          for (int i = 0; i < C::kBatch; ++i)
-#pragma unroll
-            for (int nt = 0; nt < C::kNT; ++nt) {
-              if constexpr (kQ8)
-                pm_mma_f16(o[k0 + i][nt], vf[i], pf[nt][0], pf[nt][1]);
-              else
-                pm_mma(o[k0 + i][nt], vf[i], pf[nt][0], pf[nt][1]);
-            }
-        }
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&bars->empty[slot]);
       }
 
       // ---- the warps' results, added in order
@@ -697,8 +781,7 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
       for (int nt = 0; nt < C::kNT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float f = m[nt][e] == -INFINITY ? 0.f : ptx::ex2(m[nt][e] - row_max(nt * 8 + rg + e));
-          if constexpr (kQ8) f = m[nt][e] == -INFINITY ? 0.f : ptx::ex2(mw[nt][e] - 7.f - row_max(nt * 8 + rg + e));
+          const float f = m[nt][e] == -INFINITY ? 0.f : ptx::ex2(m[nt][e] - row_max(nt * 8 + rg + e));
 #pragma unroll
           for (int k = 0; k < kD / 16; ++k) {
             o[k][nt][e] *= f;
