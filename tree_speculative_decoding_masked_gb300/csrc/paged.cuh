@@ -392,10 +392,10 @@ cudaError_t launch_paged_simt(PagedAttn a, char* ws, cudaStream_t stream);
 // blocks and min(page_size, 64) rows, as 8-row groups [block][8][128 bytes].  Other D: 3-D boxes
 // of one column block, of min(page_size, 64) rows (D <= 64) or 8.
 bool paged_kv_tmap(CUtensorMap* m, const void* base, const PagedAttn& a);
-// Likewise of 8-bit pages, in column blocks of 64 bytes; with a 64-byte swizzle or none.
-bool paged_q8_tmap(CUtensorMap* m, const void* base, const PagedAttn& a, bool swizzled);
-// Likewise in rows of 128 bytes (zeros behind D), 128-byte swizzle.
-bool paged_q8_rows_tmap(CUtensorMap* m, const void* base, const PagedAttn& a);
+// Likewise of 8-bit pages: rows of 128 bytes with a 128-byte swizzle, or column blocks of 64 bytes with a
+// 64-byte swizzle or none; boxes of min(page_size, rows) rows, or 8 where D is no whole number of columns.
+enum PagedQ8Box { kQ8Plain, kQ8Swizzled, kQ8Rows128 };
+bool paged_q8_tmap(CUtensorMap* m, const void* base, const PagedAttn& a, PagedQ8Box kind, int rows = 64);
 // Tensor map of queries, in boxes of 64 columns and `rows` rows.
 bool paged_q_tmap(CUtensorMap* m, const PagedAttn& a, int rows);
 

@@ -30,9 +30,10 @@
 // and m is the running reference of z + e, so that a weight is rounded to 11 bits and lost only below 2^-32 of the
 // largest term of its row's sum; the sum takes 2^-e times P.  A key's scale multiplies its scores, in fp32.  K's
 // fragments need no transpose and any order of columns, if Q's have the same: a lane takes 16 columns of a key
-// in one load, rows of 64 bytes without a swizzle, so that eight lanes read 128 bytes in a row.  V's
+// in one load.  Eight lanes take four such chunks of two keys, which the swizzle of 128-byte rows lays on
+// different banks if the keys are four apart: so product row g is key g / 2 + 4 (g % 2) of its eight.  V's
 // come by transposing loads of 16-bit pairs (two columns of a key), whose bytes are dealt to two product
-// rows.  With K in fp16 too, 64 keys a tile, 16 a warp, and scales looked up for each key of a tile: 1900
+// rows.  Boxes of 64-byte rows, without that: the copies alone took 260 us for 64 tokens over 8192 to 16384.  With K in fp16 too, 64 keys a tile, 16 a warp, and scales looked up for each key of a tile: 1900
 // instructions for 64 keys and 390 us for 64 tokens over 8192 to 16384.
 #pragma once
 
@@ -53,7 +54,8 @@ constexpr int kPmTol = 8, kPmFix = 8;  // in tiles of 64 keys
 
 template <int kD, int kRT, bool kQ8>
 struct PmCfg {
-  static constexpr int kDB = kD / 64;
+  static constexpr int kCols = kQ8 && kD > 64 ? 128 : 64;  // of a column block
+  static constexpr int kDB = kD / kCols;
   static constexpr int kNT = kRT / 8;                   // row tiles of the products
   // consumers: two groups of four; one where O takes 128 registers a thread
   static constexpr int kWarps = kD == 256 || kD / 16 * kNT * 4 > 64 ? 4 : 8;
@@ -63,8 +65,9 @@ struct PmCfg {
   static constexpr int kWarpKeys = kKeys / 4;
   static constexpr int kTol = kPmTol * kPmKeys / kKeys, kFix = kPmFix * kPmKeys / kKeys;
   static constexpr int kElt = kQ8 ? 1 : 2;
-  static constexpr int kBlock = 512 * kElt;             // 8 rows of 64 columns
-  static constexpr int kGroup = kDB * kBlock;           // 8 rows of a K or V tile: [column block][8][64 columns]
+  static constexpr int kRow = kCols * kElt;             // bytes of a row in a block
+  static constexpr int kBlock = 8 * kRow;
+  static constexpr int kGroup = kDB * kBlock;           // 8 rows of a K or V tile: [column block][8][columns]
   static constexpr int kTile = kKeys / 8 * kGroup;
   static constexpr int kStages = kD == 64 ? 8 : kD == 128 ? (kRT <= 16 ? 6 : 5) : 3;  // of K and V
   // bytes: ldmatrix rows, or (kQ8) the 8-byte loads of four rows, on different banks
@@ -221,7 +224,7 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
     const int mine = boxes / kPmProducers + (warp - C::kWarps < boxes % kPmProducers);
     const int box = lane * kPmProducers + warp - C::kWarps;  // this lane's
     const int pi = box / per_piece, part = box % per_piece;
-    const uint32_t box_bytes = (uint32_t)(128 * C::kElt * C::kDB / per_piece) << box_shift;
+    const uint32_t box_bytes = (uint32_t)(2 * kD * C::kElt / per_piece) << box_shift;
     // where it goes in a stage: K or V, 8-row group, column block
     const int off = (part & 1) * C::kTile + ((pi << box_shift) >> 3) * C::kGroup + (part >> 1) * C::kBlock;
     int issued = 0, counted = -1, active = 0;  // a sequence's active rows, once counted
@@ -269,7 +272,7 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
           if (C::kDB > 1 && wide)
             ptx::tma_load_5d(dst, tm, &bars->full[slot], 0, 0, 0, row >> 3, page * a.Hkv + w.hk);
           else
-            ptx::tma_load_3d(dst, tm, &bars->full[slot], (part >> 1) * 64, row, page * a.Hkv + w.hk);
+            ptx::tma_load_3d(dst, tm, &bars->full[slot], (part >> 1) * C::kCols, row, page * a.Hkv + w.hk);
         }
         __syncwarp();
       }
@@ -508,18 +511,20 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
         const bool edge = j0 < lo || j0 + C::kWarpKeys > hi;
         if (edge) {
           // V rows that were not fetched or may hold anything, NaN included: zero
-          constexpr int kRowChunks = 4 * C::kElt;  // 16-byte chunks of a row in a column block
+          constexpr int kRowChunks = C::kRow / 16;  // 16-byte chunks of a row in a column block
           for (int e = lane; e < C::kWarpKeys * C::kDB * kRowChunks; e += 32) {
             const int rr = e / (C::kDB * kRowChunks), rest = e % (C::kDB * kRowChunks);
             if (j0 + rr < lo || j0 + rr >= hi)
               *reinterpret_cast<uint4*>(sV + (rr >> 3) * C::kGroup + (rest / kRowChunks) * C::kBlock +
-                                        (rr & 7) * 64 * C::kElt + rest % kRowChunks * 16) = make_uint4(0, 0, 0, 0);
+                                        (rr & 7) * C::kRow + rest % kRowChunks * 16) = make_uint4(0, 0, 0, 0);
           }
           ptx::fence_proxy_async_smem();  // before the slot is refilled
           __syncwarp();
         }
         if constexpr (kQ8) {
           // ---- 16 keys at a time; with one row tile both together, so that their latencies overlap
+          auto key_of_row = [](int g) -> int { return C::kCols == 64 ? g : g >> 1 | (g & 1) << 2; };
+          const int kk = key_of_row(kg);  // this lane's keys: kk, kk + 8
           constexpr int kSubs = C::kNT == 1 && kD <= 128 ? 2 : 1;
           const bool masked = j0 < full_lo || j0 + 32 > full_hi || edge;
 #pragma unroll 1
@@ -532,11 +537,14 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
               for (int nt = 0; nt < C::kNT; ++nt)
 #pragma unroll
                 for (int x = 0; x < 4; ++x) s[u][nt][0][x] = s[u][nt][1][x] = 0.f;
-              const unsigned char* krow = sK + (sub0 + u) * 2 * C::kGroup + (lane >> 2) * 64 + (lane & 3) * 16;
+              const unsigned char* krow = sK + (sub0 + u) * 2 * C::kGroup + key_of_row(lane >> 2) * C::kRow;
 #pragma unroll
-              for (int j = 0; j < C::kDB; ++j) {
-                const uint4 k0 = *reinterpret_cast<const uint4*>(krow + j * C::kBlock);
-                const uint4 k1 = *reinterpret_cast<const uint4*>(krow + C::kGroup + j * C::kBlock);
+              for (int j = 0; j < kD / 64; ++j) {
+                const unsigned char* at =
+                    C::kCols == 64 ? krow + (lane & 3) * 16
+                                   : krow + (j >> 1) * C::kBlock + (((j & 1) * 4 + (lane & 3)) ^ key_of_row(lane >> 2)) * 16;
+                const uint4 k0 = *reinterpret_cast<const uint4*>(at);
+                const uint4 k1 = *reinterpret_cast<const uint4*>(at + C::kGroup);
 #pragma unroll
                 for (int nt = 0; nt < C::kNT; ++nt)
 #pragma unroll
@@ -556,14 +564,14 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
               }
             }
             // scores; those of a row's running reference count with the value's scale
-            float val_e[kSubs][2], val_f[kSubs][2];  // e and 2^-e of keys kg, kg + 8
+            float val_e[kSubs][2], val_f[kSubs][2];  // e and 2^-e of keys kk, kk + 8
             bool grow = false;
 #pragma unroll
             for (int u = 0; u < kSubs; ++u) {
               float key_f[2];
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const int from = fine ? (sub0 + u) * 16 + kg + 8 * e : ((turn - 1) & 15) * 2 + sub0 + u;
+                const int from = fine ? (sub0 + u) * 16 + kk + 8 * e : ((turn - 1) & 15) * 2 + sub0 + u;
                 const int both = __shfl_sync(0xffffffffu, my_scales, from);
                 key_f[e] = __uint_as_float((uint32_t)(both & 255) << 23);
                 val_e[u][e] = (float)((both >> 8) - 127);
@@ -578,7 +586,7 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
                   if constexpr (kCap == kLargeCap) z = capped_score(z * a.scale, a.cap, ck);
                   z = fmaf(z, c, val_e[u][x >> 1]);
                   if (masked) {
-                    const int rr = nt * 8 + rg + (x & 1), j = j0 + (sub0 + u) * 16 + kg + (x >> 1) * 8;
+                    const int rr = nt * 8 + rg + (x & 1), j = j0 + (sub0 + u) * 16 + kk + (x >> 1) * 8;
                     bool vis = j >= s_lo[rr] && j < s_hi[rr];
                     if (!vis && a.parent && j >= w.P && j < hi)
                       vis = (s_vis[rr][(j - w.P) >> 5] >> ((j - w.P) & 31)) & 1u;
@@ -624,18 +632,20 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
                 pf[u][nt][1] = pm_transpose(pm_f16x2(e2, e3));
               }
             }
-            // V^T: lane l names key (l & 7) + 8 ((l >> 3) & 1), columns 16 (k + (l >> 4)).. of two steps at once
+            // V^T: lane l names the key of row l & 7, of eight (l >> 3) & 1, and columns 16 (k + (l >> 4)).. of two steps
 #pragma unroll
             for (int u = 0; u < kSubs; ++u) {
+              const int vk = key_of_row(lane & 7);
               const uint32_t vaddr =
-                  ptx::smem_addr(sV + (sub0 + u) * 2 * C::kGroup + ((lane >> 3) & 1) * C::kGroup + (lane & 7) * 64);
+                  ptx::smem_addr(sV + (sub0 + u) * 2 * C::kGroup + ((lane >> 3) & 1) * C::kGroup + vk * C::kRow);
 #pragma unroll
               for (int k0 = 0; k0 < kD / 16; k0 += C::kBatch) {
                 uint32_t raw[C::kBatch / 2][4];
 #pragma unroll
                 for (int i = 0; i < C::kBatch / 2; ++i) {
                   const int k = k0 + 2 * i + (lane >> 4);
-                  pm_ldsm4t(raw[i], vaddr + (k >> 2) * C::kBlock + (((k & 3) ^ ((lane & 7) >> 1)) << 4));
+                  pm_ldsm4t(raw[i], C::kCols == 64 ? vaddr + (((k & 3) ^ (vk >> 1)) << 4)
+                                                   : vaddr + (k >> 3) * C::kBlock + (((k & 7) ^ vk) << 4));
                 }
 #pragma unroll
                 for (int i = 0; i < C::kBatch; ++i) {
@@ -1038,7 +1048,8 @@ static cudaError_t launch_pm_all(PagedAttn a, char* ws, cudaStream_t stream) {
     a.ws_o = reinterpret_cast<float*>(ws + kPagedCntBytes + p.rows * 8);
   }
   CUtensorMap mk, mv;
-  const bool made = kQ8 ? paged_q8_tmap(&mk, a.k, a, false) && paged_q8_tmap(&mv, a.v, a, true)
+  const bool made = kQ8 ? paged_q8_tmap(&mk, a.k, a, a.D <= 64 ? kQ8Plain : kQ8Rows128) &&
+                              paged_q8_tmap(&mv, a.v, a, a.D <= 64 ? kQ8Swizzled : kQ8Rows128)
                         : paged_kv_tmap(&mk, a.k, a) && paged_kv_tmap(&mv, a.v, a);
   if (!made) return cudaErrorInvalidValue;
   if (a.D <= 64) return launch_pm_d<64, kQ8>(mk, mv, a, p, stream);

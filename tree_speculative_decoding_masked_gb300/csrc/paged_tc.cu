@@ -55,30 +55,25 @@ bool paged_q_tmap(CUtensorMap* m, const PagedAttn& a, int rows) {
   return pt_tmap(m, a.q, a.D, a.N, (long long)a.B * a.Hq, rows);
 }
 
-bool paged_q8_rows_tmap(CUtensorMap* m, const void* base, const PagedAttn& a) {
-  const int ps = 1 << a.page_shift;
-  const cuuint64_t dims[3] = {(cuuint64_t)a.D, (cuuint64_t)ps, (cuuint64_t)a.num_pages * a.Hkv};
-  const cuuint64_t strides[2] = {(cuuint64_t)a.D, (cuuint64_t)ps * a.D};
-  // the rows that a lane of the kernel's producer takes: fewer where V's boxes are column blocks
-  const cuuint32_t boxes[3] = {128, (cuuint32_t)(a.D == 128 || a.D <= 64 ? min(ps, 64) : 8), 1};
-  return pt_encode(m, base, 3, dims, strides, boxes, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B);
-}
-
-bool paged_q8_tmap(CUtensorMap* m, const void* base, const PagedAttn& a, bool swizzled) {
-  const int ps = 1 << a.page_shift, box = min(ps, 64);
+bool paged_q8_tmap(CUtensorMap* m, const void* base, const PagedAttn& a, PagedQ8Box kind, int rows) {
+  const int ps = 1 << a.page_shift, box = min(ps, rows);
   const cuuint64_t planes = (cuuint64_t)a.num_pages * a.Hkv, D = (cuuint64_t)a.D;
-  const CUtensorMapSwizzle swizzle = swizzled ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE;
-  if (a.D == 128 || a.D == 256) {
-    // {64 columns, 8 rows, column blocks, row groups, planes}
-    const cuuint64_t dims[5] = {64, 8, D / 64, (cuuint64_t)ps / 8, planes};
-    const cuuint64_t strides[4] = {D, 64, D * 8, (cuuint64_t)ps * D};
-    const cuuint32_t boxes[5] = {64, 8, (cuuint32_t)a.D / 64, (cuuint32_t)box / 8, 1};
+  const CUtensorMapSwizzle swizzle = kind == kQ8Rows128   ? CU_TENSOR_MAP_SWIZZLE_128B
+                                     : kind == kQ8Swizzled ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                           : CU_TENSOR_MAP_SWIZZLE_NONE;
+  const cuuint32_t cols = kind == kQ8Rows128 ? 128 : 64;
+  const bool one = a.D <= (int)cols;  // column block, or less of one: zeros behind
+  if (!one && (a.D == 128 || a.D == 256)) {
+    // {columns, 8 rows, column blocks, row groups, planes}
+    const cuuint64_t dims[5] = {cols, 8, D / cols, (cuuint64_t)ps / 8, planes};
+    const cuuint64_t strides[4] = {D, cols, D * 8, (cuuint64_t)ps * D};
+    const cuuint32_t boxes[5] = {cols, 8, (cuuint32_t)(a.D / cols), (cuuint32_t)box / 8, 1};
     return pt_encode(m, base, 5, dims, strides, boxes, CU_TENSOR_MAP_DATA_TYPE_UINT8, swizzle);
   }
-  // one column block, or a narrower last one: then a box is one 8-row group of a block
+  // else a box is one 8-row group of a block
   const cuuint64_t dims[3] = {D, (cuuint64_t)ps, planes};
   const cuuint64_t strides[2] = {D, (cuuint64_t)ps * D};
-  const cuuint32_t boxes[3] = {64, (cuuint32_t)(a.D <= 64 ? box : 8), 1};
+  const cuuint32_t boxes[3] = {cols, (cuuint32_t)(one ? box : 8), 1};
   return pt_encode(m, base, 3, dims, strides, boxes, CU_TENSOR_MAP_DATA_TYPE_UINT8, swizzle);
 }
 

@@ -1376,7 +1376,7 @@ static cudaError_t launch_pt_all(PagedAttn a, char* ws, cudaStream_t stream) {
   a.ws_ml = reinterpret_cast<float2*>(ws + kPagedCntBytes);
   a.ws_o = reinterpret_cast<float*>(ws + kPagedCntBytes + p.slots * 2 * kPtRows * 8);
   CUtensorMap mq, mk, mv;
-  const bool made = kQ != kPtBf16 ? paged_q8_rows_tmap(&mk, a.k, a) && paged_q8_tmap(&mv, a.v, a, false)
+  const bool made = kQ != kPtBf16 ? paged_q8_tmap(&mk, a.k, a, kQ8Rows128, a.D == 96 ? 8 : 64) && paged_q8_tmap(&mv, a.v, a, kQ8Plain)
                         : paged_q_tmap(&mq, a, p.NT) && paged_kv_tmap(&mk, a.k, a) && paged_kv_tmap(&mv, a.v, a);
   if (!made) return cudaErrorInvalidValue;
   if (kQ != kPtBf16) mq = mk;  // Q comes without one
