@@ -335,20 +335,27 @@ __device__ __forceinline__ void pt_drain(uint64_t* bar, uint32_t parity, volatil
   if (!ptx::mbar_wait(bar, parity, &quiet)) *abort_flag = 1;
 }
 
-// mbar_wait of a role that runs ahead of the others: asleep between looks, so that it leaves the issue
-// slots, and the instruction caches, to them
-__device__ __forceinline__ bool pt_wait_ahead(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  uint64_t t0 = 0;
-  while (!ptx::mbar_try_wait(bar, parity)) {
-    __nanosleep(64);
-    const uint64_t now = globaltimer_ns();
-    if (t0 == 0) t0 = now;
-    if (*abort || now - t0 > TV_WAIT_NS) {
+// kQ8's bounded waits, short: the roles' loops share the instruction caches, and what one of them takes more,
+// the softmax warps wait for (misses a step 77, of the bf16 kernel 18).  kNap: a role that runs ahead of
+// the others sleeps between looks.  Gives up after kPtLooks looks, some seconds, or when another has.
+constexpr uint32_t kPtLooks = 1u << 26;
+template <bool kNap>
+__device__ __forceinline__ bool pt_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+#pragma unroll 1
+  for (uint32_t n = 0; !ptx::mbar_try_wait(bar, parity);) {
+    if (kNap) __nanosleep(64);
+    n += kNap ? 16 : 1;
+    if (__builtin_expect((n & 1023u) == 0, 0) && (*abort || n >= kPtLooks)) {
       *abort = 1;
       return false;
     }
   }
   return true;
+}
+template <bool kQ8>
+__device__ __forceinline__ bool pt_wait_for(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if constexpr (kQ8) return pt_wait<false>(bar, parity, abort);
+  return ptx::mbar_wait(bar, parity, abort);
 }
 
 __device__ __forceinline__ void pt_bars_init(PtBars* bars, bool q8, bool fine, int warps) {
@@ -368,9 +375,9 @@ __device__ __forceinline__ void pt_bars_init(PtBars* bars, bool q8, bool fine, i
   }
   for (int s = 0; s < kPtSlots; ++s) {
     ptx::mbar_init(&bars->k_full[s], 1);
-    ptx::mbar_init(&bars->k_empty[s], 2);  // both S issuers
+    ptx::mbar_init(&bars->k_empty[s], q8 ? 6 : 2);  // both S issuers (q8: K and V share a barrier; the converters)
     ptx::mbar_init(&bars->v_full[s], 1);
-    ptx::mbar_init(&bars->v_empty[s], q8 ? 4 : 1);
+    ptx::mbar_init(&bars->v_empty[s], 1);
   }
   for (int x = 0; x < 2; ++x)
     for (int u = 0; u < 2; ++u) {
@@ -597,7 +604,7 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
       const int box_shift = min(a.page_shift, C::kDB == 1 || pa.wide ? 6 : 3);
       const int db = lane % per_piece, pi = lane / per_piece;
       const bool in_tile = (pi << box_shift) < kPtKeys;
-      const uint32_t box_bytes = (uint32_t)((kQ8 ? 64 : 128) * C::kDB / per_piece) << box_shift;
+      const uint32_t box_bytes = (uint32_t)((kQ8 ? 64 : 128) * C::kDB / per_piece) << box_shift;  // kQ8: of V
       const int32_t* table = a.table + (size_t)b * a.max_pages;
       // whether this lane's box in tile t holds a needed row, and its table entry (read two tiles
       // ahead, checked when it is used)
@@ -615,52 +622,73 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
         return -1;
       };
       int raw0 = entry(0), raw1 = entry(1), before = -1;
-      // this lane's box of tile t into its ring slot; false after an abort
-      auto fetch = [&](unsigned char* ring, const CUtensorMap* tm, uint64_t* full, uint64_t* empty, int t, int pg,
-                       bool is_k) -> bool {
-        const unsigned gt = kt + t;
-        const int slot = gt % kPtSlots;
-        bool got = true;
-        if (gt >= kPtSlots) {
-          if constexpr (kQ8)
-            got = pt_wait_ahead(&empty[slot], ((gt / kPtSlots) - 1) & 1, abort_flag);
-          else
-            got = ptx::mbar_wait(&empty[slot], ((gt / kPtSlots) - 1) & 1, abort_flag);
+      if constexpr (kQ8) {
+        // K and V of a tile come together: a K box holds whole 128-byte rows, column blocks or not
+#pragma unroll 1
+        for (int t = 0; t < nt; ++t) {
+          const int page = checked(t, raw0);
+          raw0 = raw1;
+          raw1 = entry(t + 2);
+          const unsigned gt = kt + t;
+          const int slot = gt % kPtSlots;
+          bool got = true;
+          if (gt >= kPtSlots) got = pt_wait<true>(&bars->k_empty[slot], ((gt / kPtSlots) - 1) & 1, abort_flag);
+          if (!(ok = __all_sync(0xffffffffu, got))) break;
+          const uint32_t v_boxes = __popc(__ballot_sync(0xffffffffu, page >= 0));
+          const uint32_t k_boxes = __popc(__ballot_sync(0xffffffffu, page >= 0 && db == 0));
+          if (lane == 0)
+            ptx::mbar_arrive_expect_tx(&bars->k_full[slot], v_boxes * box_bytes + (k_boxes * 128u << box_shift));
+          __syncwarp();
+          if (page >= 0) {
+            const int row = ((t_begin + t) * kPtKeys + (pi << box_shift)) & ((1 << a.page_shift) - 1);
+            const int group = (pi << box_shift) >> 3, plane = page * a.Hkv + hk;
+            unsigned char* to_v = sV + slot * C::kVTile + group * (C::kGroup / 2) + db * 512;
+            if (db == 0)
+              ptx::tma_load_3d(sK + slot * C::kKTile + group * 1024, &tmK, &bars->k_full[slot], 0, row, plane);
+            if (C::kDB > 1 && pa.wide)
+              ptx::tma_load_5d(to_v, &tmV, &bars->k_full[slot], 0, 0, 0, row >> 3, plane);
+            else
+              ptx::tma_load_3d(to_v, &tmV, &bars->k_full[slot], db * 64, row, plane);
+          }
+          __syncwarp();
+          k_issued = gt + 1;
         }
-        if (!__all_sync(0xffffffffu, got)) return false;
-        // kQ8: a K box holds whole 128-byte rows, column blocks or not
-        const bool mine = pg >= 0 && !(kQ8 && is_k && db > 0);
-        const uint32_t boxes = __ballot_sync(0xffffffffu, mine), bytes = kQ8 && is_k ? 128u << box_shift : box_bytes;
-        if (lane == 0) ptx::mbar_arrive_expect_tx(&full[slot], __popc(boxes) * bytes);
-        __syncwarp();
-        if (mine) {
-          const int row = ((t_begin + t) * kPtKeys + (pi << box_shift)) & ((1 << a.page_shift) - 1);
-          const int group = (pi << box_shift) >> 3;
-          unsigned char* dst = kQ8 ? (is_k ? ring + slot * C::kKTile + group * 1024
-                                           : ring + slot * C::kVTile + group * (C::kGroup / 2) + db * 512)
-                                   : ring + slot * C::kTileBytes + group * C::kGroup + db * 1024;
-          if (kQ8 && is_k)
-            ptx::tma_load_3d(dst, tm, &full[slot], 0, row, pg * a.Hkv + hk);
-          else if (C::kDB > 1 && pa.wide)
-            ptx::tma_load_5d(dst, tm, &full[slot], 0, 0, 0, row >> 3, pg * a.Hkv + hk);
-          else
-            ptx::tma_load_3d(dst, tm, &full[slot], db * 64, row, pg * a.Hkv + hk);
+      } else {
+        // this lane's box of tile t into its ring slot; false after an abort
+        auto fetch = [&](unsigned char* ring, const CUtensorMap* tm, uint64_t* full, uint64_t* empty, int t,
+                         int pg) -> bool {
+          const unsigned gt = kt + t;
+          const int slot = gt % kPtSlots;
+          bool got = true;
+          if (gt >= kPtSlots) got = pt_wait_for<kQ8>(&empty[slot], ((gt / kPtSlots) - 1) & 1, abort_flag);
+          if (!__all_sync(0xffffffffu, got)) return false;
+          const uint32_t boxes = __ballot_sync(0xffffffffu, pg >= 0);
+          if (lane == 0) ptx::mbar_arrive_expect_tx(&full[slot], __popc(boxes) * box_bytes);
+          __syncwarp();
+          if (pg >= 0) {
+            const int row = ((t_begin + t) * kPtKeys + (pi << box_shift)) & ((1 << a.page_shift) - 1);
+            unsigned char* dst = ring + slot * C::kTileBytes + ((pi << box_shift) >> 3) * C::kGroup + db * 1024;
+            if (C::kDB > 1 && pa.wide)
+              ptx::tma_load_5d(dst, tm, &full[slot], 0, 0, 0, row >> 3, pg * a.Hkv + hk);
+            else
+              ptx::tma_load_3d(dst, tm, &full[slot], db * 64, row, pg * a.Hkv + hk);
+          }
+          return true;
+        };
+        for (int t = 0; ok && t <= nt && nt > 0; ++t) {
+          const int page = checked(t, raw0);
+          raw0 = raw1;
+          raw1 = entry(t + 2);
+          if (t < nt) {
+            if (!(ok = fetch(sK, &tmK, bars->k_full, bars->k_empty, t, page))) break;
+            k_issued = kt + t + 1;
+          }
+          if (t > 0) {
+            if (!(ok = fetch(sV, &tmV, bars->v_full, bars->v_empty, t - 1, before))) break;
+            v_issued = kt + t;
+          }
+          before = page;
         }
-        return true;
-      };
-      for (int t = 0; ok && t <= nt && nt > 0; ++t) {
-        const int page = checked(t, raw0);
-        raw0 = raw1;
-        raw1 = entry(t + 2);
-        if (t < nt) {
-          if (!(ok = fetch(sK, &tmK, bars->k_full, bars->k_empty, t, page, true))) break;
-          k_issued = kt + t + 1;
-        }
-        if (t > 0) {
-          if (!(ok = fetch(sV, &tmV, bars->v_full, bars->v_empty, t - 1, before, false))) break;
-          v_issued = kt + t;
-        }
-        before = page;
       }
       if (!kStream && lane == 0) drain();
     } else if (kWho != kSoftmax && (warp == 1 || warp == 11)) {
@@ -671,7 +699,7 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
         const unsigned dx = pt_of(done_x, x);
         if constexpr (kQ8) {
           // also where the tile has no rows: the converters go by s_done, which may not run ahead of them
-          if (nt > 0) ok = ok && ptx::mbar_wait(&bars->q_full[x], pieces & 1, abort_flag);
+          if (nt > 0) ok = ok && pt_wait_for<kQ8>(&bars->q_full[x], pieces & 1, abort_flag);
         } else if (ntm > 0) {
           ptx::mbar_arrive_expect_tx(&bars->q_full[x], (uint32_t)(rows_used * 128 * C::kDB));
           for (int g = 0; g < a.G; ++g)
@@ -689,12 +717,12 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
             adq[kk] = ptx::sdesc_sw128(qaddr + (kk >> 2) * C::kQBlock + (kk & 3) * 32, 16, 1024);
           for (int t = 0; ok && t < nt; ++t) {
             const int ks = (kt + t) % kPtSlots;
-            if (!(ok = ptx::mbar_wait(&bars->k_full[ks], ((kt + t) / kPtSlots) & 1, abort_flag))) break;
+            if (!(ok = pt_wait_for<kQ8>(&bars->k_full[ks], ((kt + t) / kPtSlots) & 1, abort_flag))) break;
             if (t < ntm) {
               // S_X(t) overwrites P_X of two tiles before in this buffer
               const unsigned tx = dx + t;
               const int buf = tx & 1;
-              if (tx >= 2 && !(ok = ptx::mbar_wait(&bars->pv_done[x][buf], ((tx - 2) >> 1) & 1, abort_flag))) break;
+              if (tx >= 2 && !(ok = pt_wait_for<kQ8>(&bars->pv_done[x][buf], ((tx - 2) >> 1) & 1, abort_flag))) break;
               ptx::tc_fence_after();
               if constexpr (kQ8)
                 pt_s_product_q8(tmem + x * kPtRows + buf * kPtKeys, adq[0],
@@ -726,7 +754,7 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
       };
       auto zero_rows = [&](int t) {
         const int vs = (kt + t) % kPtSlots, j0 = (t_begin + t) * kPtKeys;
-        if (!ptx::mbar_wait(&bars->v_full[vs], ((kt + t) / kPtSlots) & 1, abort_flag)) return;
+        if (!pt_wait_for<kQ8>(&bars->v_full[vs], ((kt + t) / kPtSlots) & 1, abort_flag)) return;
         for (int r = lane; r < kPtKeys; r += 32)
           if (j0 + r < lo || j0 + r >= key_end)
             for (int db = 0; db < C::kDB; ++db) {
@@ -740,7 +768,7 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
       auto issue = [&](int t) -> bool {
         constexpr int kSlots = kQ8 ? kPtVbSlots : kPtSlots;
         const int vs = (kt + t) % kSlots;
-        if (!ptx::mbar_wait(kQ8 ? &bars->vb_full[vs] : &bars->v_full[vs], ((kt + t) / kSlots) & 1, abort_flag))
+        if (!pt_wait_for<kQ8>(kQ8 ? &bars->vb_full[vs] : &bars->v_full[vs], ((kt + t) / kSlots) & 1, abort_flag))
           return false;
         const uint64_t vd =
             ptx::sdesc_sw128(ptx::smem_addr((kQ8 ? sm + C::kOffVb : sV) + vs * C::kTileBytes), 1024, C::kGroup);
@@ -749,7 +777,7 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
           if (t >= ntx[x]) continue;
           const unsigned tx = done_x[x] + t;
           const int buf = tx & 1;
-          if (!ptx::mbar_wait(&bars->p_full[x][buf], (tx >> 1) & 1, abort_flag)) return false;
+          if (!pt_wait_for<kQ8>(&bars->p_full[x][buf], (tx >> 1) & 1, abort_flag)) return false;
           ptx::tc_fence_after();
           pt_pv_product(tmem + C::kColO + x * kPtRows, tmem + x * kPtRows + buf * kPtKeys, vd, 2 * C::kGroup / 16, idO,
                         t > 0 ? 1u : 0u);  // P: 8 columns per 16 keys
@@ -768,7 +796,7 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
         // the piece before's O has been read
         if (kStream && part == 0 && pieces > 0 && nt > 0)
           for (int x = 0; x < 2; ++x)
-            ok = __all_sync(0xffffffffu, ok && ptx::mbar_wait(&bars->o_free[x], (pieces - 1) & 1, abort_flag));
+            ok = __all_sync(0xffffffffu, ok && pt_wait_for<kQ8>(&bars->o_free[x], (pieces - 1) & 1, abort_flag));
         if (lane == 0)
           for (; ok && t < to; ++t) ok = issue(t);
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
@@ -785,8 +813,8 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
       for (int x = 0; ok && x < 2 && nt > 0; ++x) {
         // the piece before's products have read Q, and its rows their scales
         if (pieces > 0)
-          ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars->s_done[x], (pieces - 1) & 1, abort_flag) &&
-                                           ptx::mbar_wait(&bars->rows_read[x], (pieces - 1) & 1, abort_flag));
+          ok = __all_sync(0xffffffffu, pt_wait_for<kQ8>(&bars->s_done[x], (pieces - 1) & 1, abort_flag) &&
+                                           pt_wait_for<kQ8>(&bars->rows_read[x], (pieces - 1) & 1, abort_flag));
         if (!ok) break;
         unsigned char* sQx = sQ + x * C::kQTile;
         const int part = lane & 7;
@@ -881,7 +909,7 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
         const unsigned gt = kt + t;
         const int vs = gt % kPtSlots, vb = gt % kPtVbSlots;
         bool got = true;
-        if (gt >= kPtVbSlots) got = pt_wait_ahead(&bars->vb_empty[vb], (gt / kPtVbSlots - 1) & 1, abort_flag);
+        if (gt >= kPtVbSlots) got = pt_wait<true>(&bars->vb_empty[vb], (gt / kPtVbSlots - 1) & 1, abort_flag);
         if constexpr (kFine) {
           const int bytes = next_bytes(t), ks = __shfl_sync(0xffffffffu, bytes, 16 + (lane & 15));
           if (lane < 16)
@@ -902,7 +930,7 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
             if (lane == 0) ptx::mbar_arrive(&bars->scale_full[(rounds + r / 8) & 3]);
           }
         }
-        got = got && pt_wait_ahead(&bars->v_full[vs], (gt / kPtSlots) & 1, abort_flag);
+        got = got && pt_wait<true>(&bars->k_full[vs], (gt / kPtSlots) & 1, abort_flag);
         ok = __all_sync(0xffffffffu, got);
         if (!ok) break;
         const int j0 = (t_begin + t) * kPtKeys + cw * 16;
@@ -932,7 +960,7 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
         __syncwarp();
         if (lane == 0) {
           ptx::mbar_arrive(&bars->vb_full[vb]);
-          ptx::mbar_arrive(&bars->v_empty[vs]);
+          ptx::mbar_arrive(&bars->k_empty[vs]);
         }
       }
       __syncwarp();
@@ -969,7 +997,7 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
       // kQ8: the row's power of two, for all of the piece
       float row_f = 1.f;
       if (kQ8 && nt > 0) {
-        ok = ok && __all_sync(0xffffffffu, ptx::mbar_wait(&bars->q_full[x], pieces & 1, abort_flag));
+        ok = ok && __all_sync(0xffffffffu, pt_wait_for<kQ8>(&bars->q_full[x], pieces & 1, abort_flag));
         row_f = s_rscale[x * kPtRows + r];
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&bars->rows_read[x]);
@@ -984,7 +1012,7 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
         if constexpr (kQ8) {
           if (kFine || t % 8 == 0) {
             const unsigned n = kFine ? (kt + t) / kPtSlots : (rounds + t / 8) / 4;
-            ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars->scale_full[kFine ? (kt + t) % kPtSlots : (rounds + t / 8) & 3],
+            ok = __all_sync(0xffffffffu, pt_wait_for<kQ8>(&bars->scale_full[kFine ? (kt + t) % kPtSlots : (rounds + t / 8) & 3],
                                                         n & 1, abort_flag));
             if (!ok) break;
           }
@@ -998,7 +1026,7 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 64; ++j) v[j] *= ((const volatile float4*)scales)[j].x * row_f;
         };
-        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars->s_full[x][buf], (tx >> 1) & 1, abort_flag));
+        ok = __all_sync(0xffffffffu, pt_wait_for<kQ8>(&bars->s_full[x][buf], (tx >> 1) & 1, abort_flag));
         if (!ok) break;
         ptx::tc_fence_after();
         const int j0 = (t_begin + t) * kPtKeys;
@@ -1112,7 +1140,7 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
         if (__any_sync(0xffffffffu, need) && t > 0) {
           // O_X must hold all of PV_X(t - 1) before it is rescaled
           ok = __all_sync(0xffffffffu,
-                          ptx::mbar_wait(&bars->pv_done[x][(tx - 1) & 1], ((tx - 1) >> 1) & 1, abort_flag));
+                          pt_wait_for<kQ8>(&bars->pv_done[x][(tx - 1) & 1], ((tx - 1) >> 1) & 1, abort_flag));
           if (!ok) break;
           ptx::tc_fence_after();
 #pragma unroll(kQ8 ? 1 : D / 32)
@@ -1134,7 +1162,7 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
       // ---- epilogue: every MMA is complete at o_done
       if (isnan(l_run)) m_run = l_run;  // a NaN query's part: no part without a visible key, which merges leave out
       if (nt > 0) {
-        ok = ok && __all_sync(0xffffffffu, ptx::mbar_wait(&bars->o_done, pieces & 1, abort_flag));
+        ok = ok && __all_sync(0xffffffffu, pt_wait_for<kQ8>(&bars->o_done, pieces & 1, abort_flag));
         have_o = ok && ntm > 0;
         if (ok) ptx::tc_fence_after();
       }
