@@ -101,7 +101,7 @@ struct PtCfg {
   // kQ8: scales, and those of a piece's rows.  Blocks of 16 rows or more: four rounds of 8 tiles, of each four of
   // K's and four of V's exponents e; shorter ones: a tile in each ring slot, {K's, e, 2^-e} of every key
   static constexpr int kOffScale = kOffPar + kMaxNodes * 4;
-  static constexpr int kScaleBytes = !kQ8 ? 0 : kQ == kPtQ8Fine ? kPtSlots * kPtKeys * 16 : 4 * 8 * 32;
+  static constexpr int kScaleBytes = !kQ8 ? 0 : kQ == kPtQ8Fine ? kPtSlots * kPtKeys * 12 : 4 * 8 * 32;
   static constexpr int kOffBar = kOffScale + kScaleBytes + (kQ8 ? 2 * kPtRows * 4 : 0);
   static constexpr int kSmemAlloc = kOffBar + 640 + 1024;  // slack for 1024-byte alignment
   static constexpr uint32_t kColO = 256;
@@ -306,26 +306,36 @@ __device__ __forceinline__ float pt_max64_q8(const float (&sv)[64], const float 
   }
   return m;
 }
-// the same with sc[j] of every key (the factor is in sv already)
-__device__ __forceinline__ float pt_exp64_fine(const float (&sv)[64], float c, const float4* sc, float m,
+// The same with a factor of every key, which is in sv already, and its e and 2^-e (sc[kPtKeys ..] and
+// sc[2 kPtKeys ..]).  They are read where they are used, 16 keys' at a time: 64 do not fit the registers.
+__device__ __forceinline__ float pt_exp64_fine(const float (&sv)[64], float c, const float* sc, float m,
                                                uint32_t (&pw)[32], float& lsum) {
   const float nm = m == -INFINITY ? 0.f : kPtShift - m;
   float psum = 0.f;
   lsum = 0.f;
 #pragma unroll
-  for (int k = 0; k < 32; ++k) {
-    const volatile float4* at = sc + 2 * k;  // read here: 64 keys' would not fit the registers
-    const float e0 = ptx::ex2(fmaf(sv[2 * k], c, at[0].y + nm)), e1 = ptx::ex2(fmaf(sv[2 * k + 1], c, at[1].y + nm));
-    psum += e0 + e1;
-    lsum = fmaf(e0, at[0].z, fmaf(e1, at[1].z, lsum));
-    pw[k] = pt_f16x2(e0, e1);
+  for (int j = 0; j < 64; j += 4) {
+    const float4 e = *reinterpret_cast<const float4*>(sc + kPtKeys + j);
+    const float4 f = *reinterpret_cast<const float4*>(sc + 2 * kPtKeys + j);
+    const float e0 = ptx::ex2(fmaf(sv[j], c, e.x + nm)), e1 = ptx::ex2(fmaf(sv[j + 1], c, e.y + nm));
+    const float e2 = ptx::ex2(fmaf(sv[j + 2], c, e.z + nm)), e3 = ptx::ex2(fmaf(sv[j + 3], c, e.w + nm));
+    psum += (e0 + e1) + (e2 + e3);
+    lsum = fmaf(e0, f.x, fmaf(e1, f.y, fmaf(e2, f.z, fmaf(e3, f.w, lsum))));
+    pw[j / 2] = pt_f16x2(e0, e1);
+    pw[j / 2 + 1] = pt_f16x2(e2, e3);
+    if (j % 16 == 12) asm volatile("" ::: "memory");
   }
   return psum;
 }
-__device__ __forceinline__ float pt_max64_fine(const float (&sv)[64], float c, const float4* sc) {
+__device__ __forceinline__ float pt_max64_fine(const float (&sv)[64], float c, const float* sc) {
   float m = -INFINITY;
 #pragma unroll
-  for (int j = 0; j < 64; ++j) m = fmaxf(m, fmaf(sv[j], c, ((const volatile float4*)sc)[j].y));
+  for (int j = 0; j < 64; j += 4) {
+    const float4 e = *reinterpret_cast<const float4*>(sc + kPtKeys + j);
+    m = fmaxf(fmaxf(m, fmaf(sv[j], c, e.x)), fmaf(sv[j + 1], c, e.y));
+    m = fmaxf(fmaxf(m, fmaf(sv[j + 2], c, e.z)), fmaf(sv[j + 3], c, e.w));
+    if (j % 16 == 12) asm volatile("" ::: "memory");
+  }
   return m;
 }
 
@@ -416,7 +426,7 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
   // warp: the role, in the order of the bf16 kernel's warps (12..15: converters)
   const int hw_warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int warp = !kQ8 || hw_warp >= 12 ? hw_warp : hw_warp < 2 ? hw_warp : hw_warp < 4 ? hw_warp + 8 : hw_warp - 2;
-  float4* s_scale = reinterpret_cast<float4*>(sm + C::kOffScale);
+  float* s_scale = reinterpret_cast<float*>(sm + C::kOffScale);
   float* s_rscale = reinterpret_cast<float*>(sm + C::kOffScale + C::kScaleBytes);
   const int NT = pa.NT, rows_used = a.G * NT, RT = pa.tiles * rows_used;
   if (warp == 1) {
@@ -912,9 +922,12 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
         if (gt >= kPtVbSlots) got = pt_wait<true>(&bars->vb_empty[vb], (gt / kPtVbSlots - 1) & 1, abort_flag);
         if constexpr (kFine) {
           const int bytes = next_bytes(t), ks = __shfl_sync(0xffffffffu, bytes, 16 + (lane & 15));
-          if (lane < 16)
-            s_scale[vs * kPtKeys + cw * 16 + lane] =
-                make_float4(q8_scale(ks), (float)(bytes - 127), q8_two(127 - bytes), 0.f);
+          if (lane < 16) {
+            float* to = s_scale + vs * 3 * kPtKeys + cw * 16 + lane;
+            to[0] = q8_scale(ks);
+            to[kPtKeys] = (float)(bytes - 127);
+            to[2 * kPtKeys] = q8_two(127 - bytes);
+          }
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&bars->scale_full[vs]);
         } else if (cw == 0 && (t == 0 || t % 8 == 4)) {
@@ -923,7 +936,7 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
 #pragma unroll 1
           for (int r = t == 0 ? 0 : t + 4; r < nt && r <= t + 4; r += 8) {
             const int bytes = next_bytes(r);
-            float* to = reinterpret_cast<float*>(s_scale) + ((rounds + r / 8) & 3) * 64 + (lane >> 2) * 8 + (lane & 3);
+            float* to = s_scale + ((rounds + r / 8) & 3) * 64 + (lane >> 2) * 8 + (lane & 3);
             to[0] = q8_scale(bytes & 255);
             to[4] = (float)((bytes >> 8) - 127);
             __syncwarp();
@@ -1007,7 +1020,8 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
         const int buf = tx & 1;
         // kQ8: the tile's scales, read before its scores are there: with the products' operands on the way, shared
         // memory takes long to answer
-        const float4* scales = s_scale + (kFine ? (kt + t) % kPtSlots * kPtKeys : ((rounds + t / 8) & 3) * 16 + t % 8 * 2);
+        const float* scales =
+            s_scale + (kFine ? (kt + t) % kPtSlots * 3 * kPtKeys : ((rounds + t / 8) & 3) * 64 + t % 8 * 8);
         float gf[4], ge[4];
         if constexpr (kQ8) {
           if (kFine || t % 8 == 0) {
@@ -1017,14 +1031,18 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
             if (!ok) break;
           }
           if constexpr (!kFine) {
-            const float4 ks = scales[0], vs = scales[1];
+            const float4 ks = *reinterpret_cast<const float4*>(scales), vs = *reinterpret_cast<const float4*>(scales + 4);
             gf[0] = ks.x * row_f, gf[1] = ks.y * row_f, gf[2] = ks.z * row_f, gf[3] = ks.w * row_f;
             ge[0] = vs.x, ge[1] = vs.y, ge[2] = vs.z, ge[3] = vs.w;
           }
         }
         auto scale_keys = [&](float(&v)[64]) {
 #pragma unroll
-          for (int j = 0; j < 64; ++j) v[j] *= ((const volatile float4*)scales)[j].x * row_f;
+          for (int j = 0; j < 64; j += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(scales + j);
+            v[j] *= f.x * row_f, v[j + 1] *= f.y * row_f, v[j + 2] *= f.z * row_f, v[j + 3] *= f.w * row_f;
+            if (j % 16 == 12) asm volatile("" ::: "memory");
+          }
         };
         ok = __all_sync(0xffffffffu, pt_wait_for<kQ8>(&bars->s_full[x][buf], (tx >> 1) & 1, abort_flag));
         if (!ok) break;
@@ -1043,42 +1061,45 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
           }
         }
         float sv[64];
-        ptx::tmem_ld32(colS + buf * kPtKeys, sv);
-        ptx::tmem_ld32(colS + buf * kPtKeys + 32, sv + 32);
-        ptx::tmem_wait_ld();
-        if constexpr (kFine) scale_keys(sv);
-        if constexpr (kCap == kTanhCap) {
-          if (vis != ~0ull) {
+        auto read_scores = [&] {
+          ptx::tmem_ld32(colS + buf * kPtKeys, sv);
+          ptx::tmem_ld32(colS + buf * kPtKeys + 32, sv + 32);
+          ptx::tmem_wait_ld();
+          if constexpr (kFine) scale_keys(sv);
+          if constexpr (kCap == kTanhCap) {
+            if (vis != ~0ull) {
+#pragma unroll
+              for (int j = 0; j < 64; ++j)
+                if (!((vis >> j) & 1ull)) sv[j] = 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < 64; j += 4) soft_tanh4(sv + j, kQ == kPtQ8 ? ck * gf[j / 16] : ck);
+          } else if constexpr (kCap == kLargeCap) {
+            // nearly all scores lie below 0.45 of such a cap; where one does not, the tile is read again
+            float z_max = 0.f;
+#pragma unroll
+            for (int j = 0; j < 64; ++j) {
+              const float t = sv[j] * (kQ == kPtQ8 ? a.scale * gf[j / 16] : a.scale), x = t * ck, z = x * x;
+              z_max = fmaxf(z_max, z);
+              sv[j] = fmaf(t * z, tanh_tail(z), t);
+            }
+            if (__any_sync(0xffffffffu, z_max >= kTanhNear)) {
+              ptx::tmem_ld32(colS + buf * kPtKeys, sv);
+              ptx::tmem_ld32(colS + buf * kPtKeys + 32, sv + 32);
+              ptx::tmem_wait_ld();
+              if constexpr (kFine) scale_keys(sv);
+#pragma unroll
+              for (int j = 0; j < 64; ++j)
+                sv[j] = capped_score(sv[j] * (kQ == kPtQ8 ? a.scale * gf[j / 16] : a.scale), a.cap, ck);
+            }
+          }
+          if (__builtin_expect(vis != ~0ull, 0)) {
 #pragma unroll
             for (int j = 0; j < 64; ++j)
-              if (!((vis >> j) & 1ull)) sv[j] = 0.f;
+              if (!((vis >> j) & 1ull)) sv[j] = -INFINITY;
           }
-#pragma unroll
-          for (int j = 0; j < 64; j += 4) soft_tanh4(sv + j, kQ == kPtQ8 ? ck * gf[j / 16] : ck);
-        } else if constexpr (kCap == kLargeCap) {
-          // nearly all scores lie below 0.45 of such a cap; where one does not, the tile is read again
-          float z_max = 0.f;
-#pragma unroll
-          for (int j = 0; j < 64; ++j) {
-            const float t = sv[j] * (kQ == kPtQ8 ? a.scale * gf[j / 16] : a.scale), x = t * ck, z = x * x;
-            z_max = fmaxf(z_max, z);
-            sv[j] = fmaf(t * z, tanh_tail(z), t);
-          }
-          if (__any_sync(0xffffffffu, z_max >= kTanhNear)) {
-            ptx::tmem_ld32(colS + buf * kPtKeys, sv);
-            ptx::tmem_ld32(colS + buf * kPtKeys + 32, sv + 32);
-            ptx::tmem_wait_ld();
-            if constexpr (kFine) scale_keys(sv);
-#pragma unroll
-            for (int j = 0; j < 64; ++j)
-              sv[j] = capped_score(sv[j] * (kQ == kPtQ8 ? a.scale * gf[j / 16] : a.scale), a.cap, ck);
-          }
-        }
-        if (__builtin_expect(vis != ~0ull, 0)) {
-#pragma unroll
-          for (int j = 0; j < 64; ++j)
-            if (!((vis >> j) & 1ull)) sv[j] = -INFINITY;
-        }
+        };
+        if constexpr (!kFine) read_scores();
         // P = 2^(c S - m_run) against a running reference that moves (with a rescale of O) only
         // when a score exceeds it by 2^8: such a score brings the tile's sum to 2^8, so the
         // maximum is taken only then and for the first tile with a visible key
@@ -1100,6 +1121,7 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
         if constexpr (kQ8) {
           bool checked = false, look = m_run == -INFINITY;
           for (;;) {
+            if constexpr (kFine) read_scores();  // each time: scores, scales and P together do not fit the registers
             if (__builtin_expect(look, 0)) {
               const float tms = tile_max();
               checked = true;
@@ -1116,8 +1138,13 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
               psum = pt_exp64_fine(sv, c, scales, m_run, pw, lsum);
             else
               psum = pt_exp64_q8(sv, gf, ge, m_run, pw, lsum);
-            if (checked || psum < 128.f * kPtRescaleSum) break;
-            look = true;
+            const bool again = !checked && psum >= 128.f * kPtRescaleSum;
+            if constexpr (kFine) {
+              if (!__any_sync(0xffffffffu, again)) break;  // the warp's rows together; the others' P comes out as it was
+            } else if (!again) {
+              break;
+            }
+            look = look || again;
           }
         } else {
           bool checked = false;
