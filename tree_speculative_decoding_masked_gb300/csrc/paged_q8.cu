@@ -4,29 +4,30 @@
 
 namespace tv {
 
-constexpr int kQaThreads = 256;
+constexpr int kQaThreads = 512;  // at most
 constexpr int kQaMaxRows = 128;  // rows of a tile
+constexpr int kQaHeads = 2;      // heads whose loads are in flight together, and two more while they are worked on
 
 // ---- append: new keys (normed, turned) and values into the pages, queries normed and turned
 //
 // A block's scale is 2^e with the least e that covers its new rows, and the scale of the committed
 // rows that the block begins with; where those grow, their codes are written anew (exactly, but
 // where one falls below e4m3's normal numbers).  So the scale needs the maximum over a block before
-// its first code is stored: a CTA holds whole blocks of one head, a tile of up to 64 rows (128 of 32
-// elements), in registers, the maxima meet in shared memory, and every row is read once.  Order does
-// not matter to a maximum, so results do not depend on timing.
+// its first code is stored: a CTA holds whole blocks of a head, a tile of rows, in registers, the
+// maxima meet in shared memory, and every row is read once.  Order does not matter to a maximum, so
+// results do not depend on timing.
 //
-// Threads: `lanes` neighbours a row, each 8 elements and their 8 pair partners (as in rotary_kernel),
-// kI rows a thread.  Grid: x over (sequence, tile), y over groups of hg heads of q, k and v in turn.
-template <typename T, bool kWide>
+// Threads: `lanes` neighbours a row, each 8 elements and their 8 pair partners (rot_to_pairs), kI rows a
+// thread.  Grid: x over (sequence, tile), y over groups of hg heads of q, k and v in turn.  64 tokens of 32 + 2 x 8
+// heads of 128 bf16, normed: 5.7 us, a chain of some five reads, one behind the other.  4 x 2048 of them, 180 MB: 49.9
+// us, 3.6 TB/s; without loads ahead of the work 59, with a branch a head 65.
+template <typename T>
 __device__ __forceinline__ void qa_load(const T* src, int ea, int eb, uint4 (&r)[sizeof(T)]) {
-  if constexpr (kWide) {
-    constexpr int kHalf = sizeof(T) / 2;  // 16-byte loads of eight elements
+  constexpr int kHalf = sizeof(T) / 2;  // 16-byte loads of eight elements
 #pragma unroll
-    for (int k = 0; k < kHalf; ++k) {
-      r[k] = *reinterpret_cast<const uint4*>(src + ea + k * (16 / sizeof(T)));
-      r[kHalf + k] = *reinterpret_cast<const uint4*>(src + eb + k * (16 / sizeof(T)));
-    }
+  for (int k = 0; k < kHalf; ++k) {
+    r[k] = *reinterpret_cast<const uint4*>(src + ea + k * (16 / sizeof(T)));
+    r[kHalf + k] = *reinterpret_cast<const uint4*>(src + eb + k * (16 / sizeof(T)));
   }
 }
 template <typename T>
@@ -53,18 +54,73 @@ __device__ __forceinline__ float qa_number(T v) {
     return v;
 }
 
-// kWide: 16-byte loads, rot a multiple of 16.  Else single elements, a thread's 16 in a row, each with its
-// pair partner (read and normed again).
-template <typename T, int kI, bool kWide>
+template <typename T>
+__device__ __forceinline__ void qa_store(T* dst, int ea, int eb, bool wide, const float (&x)[8], const float (&y)[8]) {
+  if (!wide) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) dst[ea + k] = rot_pack<T, 1>({x[k]}), dst[eb + k] = rot_pack<T, 1>({y[k]});
+  } else if constexpr (sizeof(T) == 2) {
+    *reinterpret_cast<uint4*>(dst + ea) = rot_pack<T, 8>(x);
+    *reinterpret_cast<uint4*>(dst + eb) = rot_pack<T, 8>(y);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; k += 4) {
+      *reinterpret_cast<float4*>(dst + ea + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+      *reinterpret_cast<float4*>(dst + eb + k) = make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]);
+    }
+  }
+}
+// A row that allows single elements only: a thread's 16 in a row, each with its pair partner, read and normed again.
+template <typename T>
+__device__ __forceinline__ void qa_single(const RotaryArgs& a, int part, const T* src, const T* weight, long long pos,
+                                          int ea, bool mine, int lanes, uint32_t peers, float inv_d, float (&x)[8],
+                                          float (&y)[8]) {
+  float r = 1.f;
+  if (weight) {
+    float ss = 0.f;
+    if (mine)
+      for (int k = 0; k < 16; ++k) ss = fmaf(qa_number(src[ea + k]), qa_number(src[ea + k]), ss);
+    for (int o = 1; o < lanes; o *= 2) ss += __shfl_xor_sync(peers, ss, o);
+    r = __frsqrt_rn(fmaf(ss, inv_d, a.eps));
+  }
+  auto num = [&](int d) -> float {
+    const float f = qa_number(src[d]);
+    return weight ? f * r * qa_number(weight[d]) : f;
+  };
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    float f = 0.f;
+    const int d = ea + k;
+    if (mine) {
+      f = num(d);
+      if (part < 2 && d < a.rot) {
+        const int pair = a.interleaved ? d >> 1 : d % (a.rot / 2);
+        const bool upper = a.interleaved ? d & 1 : d >= a.rot / 2;
+        const float other = num(a.interleaved ? d ^ 1 : upper ? d - a.rot / 2 : d + a.rot / 2);
+        const float2 sc = sincos_turns((uint64_t)pos * a.freq[pair]);
+        const float c = sc.y * a.amplitude, s = sc.x * a.amplitude;
+        f = upper ? f * c + other * s : f * c - other * s;
+      }
+    }
+    if (k < 8)
+      x[k] = f;
+    else
+      y[k - 8] = f;
+  }
+}
+
+// kWide: 16-byte loads, rot a multiple of 16; else single elements.
+template <typename T, int kI, bool kWide, bool kInter>
 __global__ void __launch_bounds__(kQaThreads) q8_append_kernel(RotaryArgs a, Q8Pages p, int tiles, int tile_rows,
                                                                int lanes, int hg) {
-  __shared__ int s_amax[2][kQaMaxRows];
+  constexpr int kH = kWide && kI == 1 ? kQaHeads : 1;
+  __shared__ int s_amax[2][kH][kQaMaxRows];
   const int b = blockIdx.x / tiles, tile = blockIdx.x % tiles;
   const int qg = (a.Hq + hg - 1) / hg, kg = (a.Hkv + hg - 1) / hg;
   const int part = (int)blockIdx.y < qg ? 0 : (int)blockIdx.y < qg + kg ? 1 : 2;
   const int h0 = ((int)blockIdx.y - (part == 0 ? 0 : part == 1 ? qg : qg + kg)) * hg;
   const int h1 = min(part ? a.Hkv : a.Hq, h0 + hg);
-  for (int k = threadIdx.x; k < 2 * kQaMaxRows; k += blockDim.x) s_amax[0][k] = -1;
+  for (int k = threadIdx.x; k < 2 * kH * kQaMaxRows; k += blockDim.x) s_amax[0][0][k] = -1;
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int P = a.base[b], n = a.n_rows ? a.n_rows[b] : a.N;
@@ -80,20 +136,44 @@ __global__ void __launch_bounds__(kQaThreads) q8_append_kernel(RotaryArgs a, Q8P
   const int cols = a.D / 16, col = threadIdx.x % lanes, row0 = threadIdx.x / lanes, step = blockDim.x / lanes;
   const uint32_t peers = lanes == 32 ? ~0u : ((1u << lanes) - 1u) << (threadIdx.x & 31 & -lanes);
   const bool in_row = col < cols;
-  // this thread's columns: ea.. and eb..
-  const int rot_cols = kWide ? a.rot / 16 : 0;
-  const bool turn = kWide && part < 2 && col < rot_cols;
+  // this thread's columns: ea.. and eb..; lanes behind the row read its last ones, and bring nothing
+  const int rot_cols = kWide ? a.rot / 16 : 0, c = min(col, cols - 1);
+  const bool turn = kWide && part < 2 && c < rot_cols;
   int ea, eb;
   if (!kWide) {
-    ea = 16 * col, eb = ea + 8;
-  } else if (col < rot_cols) {
-    ea = 8 * col, eb = ea + a.rot / 2;
+    ea = 16 * c, eb = ea + 8;
+  } else if (turn || c < rot_cols) {
+    ea = 8 * c, eb = ea + a.rot / 2;
   } else {
-    ea = a.rot + 8 * (col - rot_cols), eb = ea + 8 * (cols - rot_cols);
+    ea = a.rot + 8 * (c - rot_cols), eb = ea + 8 * (cols - rot_cols);
   }
+  const T* weight = part < 2 ? reinterpret_cast<const T*>(a.weight[part]) : nullptr;
+  const float inv_d = 1.f / a.D;
+  // rows behind the tile read its last one, and bring nothing either
+  const long long sh = a.sh[part];
+  const T* src[kI];
+#pragma unroll
+  for (int i = 0; i < kI; ++i)
+    src[i] = reinterpret_cast<const T*>(a.src[part]) + b * a.sb[part] +
+             (long long)min(t_lo + row0 + i * step, t_hi - 1) * a.sn[part];
+  // the loads of heads h and on, kH of them or one, ahead of the work on those before
+  uint4 raw[kH][kI][sizeof(T)];
+  auto load = [&](int h) {
+    if (!kWide || h >= h1) return;
+    if (h + kH <= h1) {
+#pragma unroll
+      for (int u = 0; u < kH; ++u)
+#pragma unroll
+        for (int i = 0; i < kI; ++i) qa_load<T>(src[i] + (h + u) * sh, ea, eb, raw[u][i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kI; ++i) qa_load<T>(src[i] + h * sh, ea, eb, raw[0][i]);
+    }
+  };
+  load(h0);
   bool live[kI];
   long long pos[kI], page_row[kI];
-  float cs[kI][8], sn[kI][8];
+  RotTurn<8> turns[kI];
 #pragma unroll
   for (int i = 0; i < kI; ++i) {
     const int t = t_lo + row0 + i * step;
@@ -104,14 +184,18 @@ __global__ void __launch_bounds__(kQaThreads) q8_append_kernel(RotaryArgs a, Q8P
       live[i] = at.live && (part == 0 || at.page_row >= 0);
       pos[i] = at.pos, page_row[i] = at.page_row;
     }
-    if (turn && live[i]) {
+    if (kWide && part < 2) {
+      float2 wa[4], wb[4];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int pair = a.interleaved ? (u < 4 ? 0 : a.rot / 4 - 4) + 4 * col + u : 8 * col + u;
-        const float2 sc = sincos_turns((uint64_t)pos[i] * a.freq[pair]);
-        sn[i][u] = sc.x * a.amplitude;
-        cs[i][u] = sc.y * a.amplitude;
+      for (int k = 0; k < 4; ++k) wa[k] = wb[k] = make_float2(1.f, 1.f);
+      if (weight) {
+        uint4 w[sizeof(T)];
+        float x[8], y[8];
+        qa_load<T>(weight, ea, eb, w);
+        qa_unpack<T>(w, x, y);
+        rot_to_pairs<8, kInter>(x, y, wa, wb);
       }
+      rot_turn_set<8, kInter>(a, pos[i], turn, c, wa, wb, turns[i]);
     }
   }
   // the page that holds the tile's first row, where that block begins with committed rows
@@ -123,197 +207,179 @@ __global__ void __launch_bounds__(kQaThreads) q8_append_kernel(RotaryArgs a, Q8P
   const int in_page = (1 << a.page_shift) - 1, blocks_shift = a.page_shift - bs;
   unsigned char* cache = reinterpret_cast<unsigned char*>(part == 2 ? a.v_cache : a.k_cache);
   uint8_t* scales = part == 2 ? p.vs : p.ks;
-
-  __syncthreads();  // s_amax is set
-  for (int h = h0, buf = 0; h < h1; ++h, buf ^= 1) {
-    float x[kI][8], y[kI][8];
-    uint4 raw[kI][sizeof(T)];
-#pragma unroll
-    for (int i = 0; i < kI; ++i)
-      if (kWide && live[i] && in_row)
-        qa_load<T, kWide>(reinterpret_cast<const T*>(a.src[part]) + b * a.sb[part] + h * a.sh[part] +
-                              (long long)(t_lo + row0 + i * step) * a.sn[part],
-                          ea, eb, raw[i]);
-    int old = 0;  // the scale of the held rows
-    const size_t held_scale =
-        held_page < 0 ? 0 : (((size_t)held_page * a.Hkv + h) << blocks_shift) + ((int)(first & in_page) >> bs);
-    if (held_page >= 0) old = scales[held_scale];
-#pragma unroll
-    for (int i = 0; i < kI; ++i) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) x[i][k] = y[i][k] = 0.f;
-      if (kWide) {
-        if (live[i] && in_row) qa_unpack<T>(raw[i], x[i], y[i]);
-        if (part < 2 && a.weight[part]) {
-          // sums of squares meet over the row's lanes, live or not alike
-          float ss = 0.f;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) ss = fmaf(x[i][k], x[i][k], fmaf(y[i][k], y[i][k], ss));
-          for (int o = 1; o < lanes; o *= 2) ss += __shfl_xor_sync(peers, ss, o);
-          const float r = 1.f / sqrtf(ss / a.D + a.eps);
-          if (in_row) {
-            const T* weight = reinterpret_cast<const T*>(a.weight[part]);
-            uint4 wr[sizeof(T)];
-            float wx[8], wy[8];
-            qa_load<T, kWide>(weight, ea, eb, wr);
-            qa_unpack<T>(wr, wx, wy);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) x[i][k] = x[i][k] * r * wx[k], y[i][k] = y[i][k] * r * wy[k];
-          }
-        }
-        if (turn) {
-          if (a.interleaved) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float e0 = x[i][2 * k], o0 = x[i][2 * k + 1], e1 = y[i][2 * k], o1 = y[i][2 * k + 1];
-              x[i][2 * k] = e0 * cs[i][k] - o0 * sn[i][k];
-              x[i][2 * k + 1] = o0 * cs[i][k] + e0 * sn[i][k];
-              y[i][2 * k] = e1 * cs[i][4 + k] - o1 * sn[i][4 + k];
-              y[i][2 * k + 1] = o1 * cs[i][4 + k] + e1 * sn[i][4 + k];
-            }
-          } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float e = x[i][k], o = y[i][k];
-              x[i][k] = e * cs[i][k] - o * sn[i][k];
-              y[i][k] = o * cs[i][k] + e * sn[i][k];
-            }
-          }
-        }
-      } else {
-        const T* src = reinterpret_cast<const T*>(a.src[part]) + b * a.sb[part] + h * a.sh[part] +
-                       (long long)(t_lo + row0 + i * step) * a.sn[part];
-        const bool mine = live[i] && in_row;
-        float r = 1.f;
-        const T* weight = part < 2 ? reinterpret_cast<const T*>(a.weight[part]) : nullptr;
-        if (weight) {
-          float ss = 0.f;
-          if (mine)
-            for (int k = 0; k < 16; ++k) ss = fmaf(qa_number(src[ea + k]), qa_number(src[ea + k]), ss);
-          for (int o = 1; o < lanes; o *= 2) ss += __shfl_xor_sync(peers, ss, o);
-          r = 1.f / sqrtf(ss / a.D + a.eps);
-        }
-        auto num = [&](int d) -> float {
-          const float f = qa_number(src[d]);
-          return weight ? f * r * qa_number(weight[d]) : f;
-        };
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          float f = 0.f;
-          const int d = ea + k;
-          if (mine) {
-            f = num(d);
-            if (part < 2 && d < a.rot) {
-              const int pair = a.interleaved ? d >> 1 : d % (a.rot / 2);
-              const bool upper = a.interleaved ? d & 1 : d >= a.rot / 2;
-              const float other = num(a.interleaved ? d ^ 1 : upper ? d - a.rot / 2 : d + a.rot / 2);
-              const float2 sc = sincos_turns((uint64_t)pos[i] * a.freq[pair]);
-              const float c = sc.y * a.amplitude, s = sc.x * a.amplitude;
-              f = upper ? f * c + other * s : f * c - other * s;
-            }
-          }
-          if (k < 8)
-            x[i][k] = f;
-          else
-            y[i][k - 8] = f;
-        }
-      }
-    }
-    if (part == 0) {
-      if (!kWide) __syncthreads();  // in place: the partners have been read
+  // the values of heads h + u, rows i, which have been loaded, to sink(u, i, x, y)
+  auto values = [&](auto many, int h, auto sink) {
+    constexpr int kMany = decltype(many)::value;
+    if constexpr (!kWide) {
+      static_assert(kMany == 1, "one head at a time");
 #pragma unroll
       for (int i = 0; i < kI; ++i) {
-        if (!live[i] || !in_row) continue;
-        T* dst = reinterpret_cast<T*>(a.q_out) +
-                 (((long long)b * a.Hq + h) * a.N + t_lo + row0 + i * step) * a.D;
-        if (p.wide_out) {
-          if constexpr (sizeof(T) == 2) {
-            *reinterpret_cast<uint4*>(dst + ea) = rot_pack<T, 8>(x[i]);
-            *reinterpret_cast<uint4*>(dst + eb) = rot_pack<T, 8>(y[i]);
-          } else {
+        float x[8], y[8];
+        qa_single<T>(a, part, src[i] + h * sh, weight, pos[i], ea, live[i] && in_row, lanes, peers, inv_d, x, y);
+        sink(0, i, x, y);
+      }
+    } else {
+      if (part == 2) {
+        float x[kMany][kI][8], y[kMany][kI][8];
 #pragma unroll
-            for (int k = 0; k < 8; k += 4) {
-              *reinterpret_cast<float4*>(dst + ea + k) = make_float4(x[i][k], x[i][k + 1], x[i][k + 2], x[i][k + 3]);
-              *reinterpret_cast<float4*>(dst + eb + k) = make_float4(y[i][k], y[i][k + 1], y[i][k + 2], y[i][k + 3]);
-            }
-          }
-        } else {
+        for (int u = 0; u < kMany; ++u)
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            if constexpr (sizeof(T) == 2) {
-              dst[ea + k] = (T)(ptx::cvt_bf16x2(x[i][k], 0.f) & 0xffffu);
-              dst[eb + k] = (T)(ptx::cvt_bf16x2(y[i][k], 0.f) & 0xffffu);
-            } else {
-              dst[ea + k] = x[i][k];
-              dst[eb + k] = y[i][k];
-            }
-          }
+          for (int i = 0; i < kI; ++i) qa_unpack<T>(raw[u][i], x[u][i], y[u][i]);
+        load(h + kMany);
+#pragma unroll
+        for (int u = 0; u < kMany; ++u)
+#pragma unroll
+          for (int i = 0; i < kI; ++i) sink(u, i, x[u][i], y[u][i]);
+        return;
+      }
+      float2 pa[kMany][kI][4], pb[kMany][kI][4];
+      float ss[kMany][kI];
+#pragma unroll
+      for (int u = 0; u < kMany; ++u)
+#pragma unroll
+        for (int i = 0; i < kI; ++i) {
+          float x[8], y[8];
+          qa_unpack<T>(raw[u][i], x, y);
+          rot_to_pairs<8, kInter>(x, y, pa[u][i], pb[u][i]);
+          ss[u][i] = in_row ? rot_squares<8>(pa[u][i], pb[u][i]) : 0.f;
+        }
+      load(h + kMany);
+      if (weight) {
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+          if (o >= lanes) continue;
+#pragma unroll
+          for (int u = 0; u < kMany; ++u)
+#pragma unroll
+            for (int i = 0; i < kI; ++i) ss[u][i] += __shfl_xor_sync(peers, ss[u][i], o);
         }
       }
-      continue;
+#pragma unroll
+      for (int u = 0; u < kMany; ++u)
+#pragma unroll
+        for (int i = 0; i < kI; ++i) {
+          float x[8], y[8];
+          rot_turn<8>(turns[i], weight != nullptr, __frsqrt_rn(fmaf(ss[u][i], inv_d, a.eps)), turn, pa[u][i], pb[u][i]);
+          rot_from_pairs<8, kInter>(pa[u][i], pb[u][i], x, y);
+          sink(u, i, x, y);
+        }
     }
+  };
+  auto queries = [&](auto many, int h) {
+    const long long at = (((long long)b * a.Hq + h) * a.N + t_lo + row0) * a.D;
+    values(many, h, [&](int u, int i, const float(&x)[8], const float(&y)[8]) {
+      if (!kWide) __syncthreads();  // in place: the partners have been read
+      if (live[i] && in_row)
+        qa_store<T>(reinterpret_cast<T*>(a.q_out) + at + ((long long)u * a.N + i * step) * a.D, ea, eb, p.wide_out, x, y);
+    });
+  };
+  auto rows = [&](auto many, int h, int buf) {
+    constexpr int kMany = decltype(many)::value;
+    float x[kMany][kI][8], y[kMany][kI][8];
+    int old[kMany];  // the scales of the held rows
+#pragma unroll
+    for (int u = 0; u < kMany; ++u) {
+      old[u] = 0;
+      if (held_page >= 0)
+        old[u] = scales[(((size_t)held_page * a.Hkv + h + u) << blocks_shift) + ((int)(first & in_page) >> bs)];
+    }
+    values(many, h, [&](int u, int i, const float(&v)[8], const float(&w)[8]) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[u][i][k] = v[k], y[u][i][k] = w[k];
+    });
     // ---- the blocks' maxima, over what is finite
+    float m[kMany][kI];
+#pragma unroll
+    for (int u = 0; u < kMany; ++u)
+#pragma unroll
+      for (int i = 0; i < kI; ++i) {
+        m[u][i] = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float f = fabsf(x[u][i][k]), g = fabsf(y[u][i][k]);
+          m[u][i] = fmaxf(m[u][i], f <= 3.4028234e38f ? f : 0.f);
+          m[u][i] = fmaxf(m[u][i], g <= 3.4028234e38f ? g : 0.f);
+        }
+        if (!in_row) m[u][i] = 0.f;
+      }
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      if (o >= lanes) continue;
+#pragma unroll
+      for (int u = 0; u < kMany; ++u)
+#pragma unroll
+        for (int i = 0; i < kI; ++i) m[u][i] = fmaxf(m[u][i], __shfl_xor_sync(peers, m[u][i], o));
+    }
     int blk[kI];
 #pragma unroll
     for (int i = 0; i < kI; ++i) {
-      float m = 0.f;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float u = fabsf(x[i][k]), w = fabsf(y[i][k]);
-        m = fmaxf(m, u <= 3.4028234e38f ? u : 0.f);
-        m = fmaxf(m, w <= 3.4028234e38f ? w : 0.f);
-      }
-      for (int o = 1; o < lanes; o *= 2) m = fmaxf(m, __shfl_xor_sync(peers, m, o));
       blk[i] = (int)((P + (long long)(t_lo + row0 + i * step) - first) >> bs);
-      if (live[i] && col == 0) atomicMax(&s_amax[buf][blk[i]], __float_as_int(m));
+      if (!live[i] || col != 0) continue;
+#pragma unroll
+      for (int u = 0; u < kMany; ++u) atomicMax(&s_amax[buf][u][blk[i]], __float_as_int(m[u][i]));
     }
     __syncthreads();
-    const int first_amax = s_amax[buf][0];
+    int first_amax[kMany];
+#pragma unroll
+    for (int u = 0; u < kMany; ++u) first_amax[u] = s_amax[buf][u][0];
 #pragma unroll
     for (int i = 0; i < kI; ++i) {
       if (!live[i]) continue;
-      int e = q8_exponent(__int_as_float(s_amax[buf][blk[i]]));
-      if (blk[i] == 0 && held_page >= 0) e = max(e, old - 127);
-      const float f = q8_two(-e);
-      const size_t row = (size_t)page_row[i] + ((size_t)h << a.page_shift);
-      if (in_row) {
-        unsigned char* dst = cache + row * a.D;
-        uint2 lo, hi;
-        lo.x = q8_code4(x[i][0] * f, x[i][1] * f, x[i][2] * f, x[i][3] * f);
-        lo.y = q8_code4(x[i][4] * f, x[i][5] * f, x[i][6] * f, x[i][7] * f);
-        hi.x = q8_code4(y[i][0] * f, y[i][1] * f, y[i][2] * f, y[i][3] * f);
-        hi.y = q8_code4(y[i][4] * f, y[i][5] * f, y[i][6] * f, y[i][7] * f);
-        *reinterpret_cast<uint2*>(dst + ea) = lo;
-        *reinterpret_cast<uint2*>(dst + eb) = hi;
+#pragma unroll
+      for (int u = 0; u < kMany; ++u) {
+        int e = q8_exponent(__int_as_float(s_amax[buf][u][blk[i]]));
+        if (blk[i] == 0 && held_page >= 0) e = max(e, old[u] - 127);
+        const float f = q8_two(-e);
+        const size_t row = (size_t)page_row[i] + ((size_t)(h + u) << a.page_shift);
+        if (in_row) {
+          unsigned char* dst = cache + row * a.D;
+          const float(&v)[8] = x[u][i], (&w)[8] = y[u][i];
+          *reinterpret_cast<uint2*>(dst + ea) = make_uint2(q8_code4(v[0] * f, v[1] * f, v[2] * f, v[3] * f),
+                                                           q8_code4(v[4] * f, v[5] * f, v[6] * f, v[7] * f));
+          *reinterpret_cast<uint2*>(dst + eb) = make_uint2(q8_code4(w[0] * f, w[1] * f, w[2] * f, w[3] * f),
+                                                           q8_code4(w[4] * f, w[5] * f, w[6] * f, w[7] * f));
+        }
+        // every live row of a block writes the same byte
+        if (col == 0) scales[row >> bs] = (uint8_t)(e + 127);
       }
-      // every live row of a block writes the same byte
-      if (col == 0) scales[row >> bs] = (uint8_t)(e + 127);
     }
     // ---- committed rows of a block whose scale has grown
-    if (held_page >= 0 && first_amax >= 0) {
-      const int e = q8_exponent(__int_as_float(first_amax));
-      if (e > old - 127) {
-        const float ratio = q8_two(old - 127 - e);
-        uint4* rows = reinterpret_cast<uint4*>(
-            cache + ((((size_t)held_page * a.Hkv + h) << a.page_shift) + (size_t)(first & in_page)) * a.D);
-        for (int k = threadIdx.x; k < held * cols; k += blockDim.x) {
-          uint4 v = rows[k];
-          v.x = q8_recode(v.x, ratio), v.y = q8_recode(v.y, ratio);
-          v.z = q8_recode(v.z, ratio), v.w = q8_recode(v.w, ratio);
-          rows[k] = v;
-        }
+#pragma unroll
+    for (int u = 0; u < kMany; ++u) {
+      if (held_page < 0 || first_amax[u] < 0) continue;
+      const int e = q8_exponent(__int_as_float(first_amax[u]));
+      if (e <= old[u] - 127) continue;
+      const float ratio = q8_two(old[u] - 127 - e);
+      uint4* at = reinterpret_cast<uint4*>(
+          cache + ((((size_t)held_page * a.Hkv + h + u) << a.page_shift) + (size_t)(first & in_page)) * a.D);
+      for (int k = threadIdx.x; k < held * cols; k += blockDim.x) {
+        uint4 v = at[k];
+        v.x = q8_recode(v.x, ratio), v.y = q8_recode(v.y, ratio);
+        v.z = q8_recode(v.z, ratio), v.w = q8_recode(v.w, ratio);
+        at[k] = v;
       }
     }
-    // the other buffer is next; this one is cleared once everybody has read it, a head later
-    for (int k = threadIdx.x; k < kQaMaxRows; k += blockDim.x) s_amax[buf ^ 1][k] = -1;
+    // the other buffer is next; this one is cleared once everybody has read it, a turn later
+    for (int k = threadIdx.x; k < kH * kQaMaxRows; k += blockDim.x) s_amax[buf ^ 1][0][k] = -1;
     __syncthreads();
+  };
+
+  int h = h0;
+  if (part == 0) {
+    for (; h + kH <= h1; h += kH) queries(std::integral_constant<int, kH>(), h);
+    for (; kH > 1 && h < h1; ++h) queries(std::integral_constant<int, 1>(), h);
+    return;
   }
+  __syncthreads();  // s_amax is set
+  int buf = 0;
+  for (; h + kH <= h1; h += kH, buf ^= 1) rows(std::integral_constant<int, kH>(), h, buf);
+  for (; kH > 1 && h < h1; ++h, buf ^= 1) rows(std::integral_constant<int, 1>(), h, buf);
 }
 
-template <typename T, int kI, bool kWide>
-static cudaError_t launch_qa(const RotaryArgs& a, const Q8Pages& p, int threads, int lanes, cudaStream_t stream) {
+template <typename T, int kI, bool kWide, bool kInter>
+static cudaError_t launch_qa(const RotaryArgs& a, const Q8Pages& p, int tile_rows, int threads, int lanes,
+                             cudaStream_t stream) {
   const int blk = 1 << p.block_shift;
-  const int tile_rows = max(64, 256 / lanes);
   const long long tiles = ((long long)a.N + blk - 1 + tile_rows - 1) / tile_rows;
   if (tiles * a.B > 0x7fffffffLL) return cudaErrorInvalidValue;
   // heads share a CTA, its sines and its page lookups once the grid has a few CTAs an SM without that
@@ -322,8 +388,8 @@ static cudaError_t launch_qa(const RotaryArgs& a, const Q8Pages& p, int threads,
   auto groups = [&](int g) { return (long long)(a.Hq + g - 1) / g + 2ll * ((a.Hkv + g - 1) / g); };
   while (hg < most && tiles * a.B * groups(hg) > 152 * 16) hg *= 2;
   const dim3 grid((unsigned)(tiles * a.B), (unsigned)groups(hg));
-  return launch_pdl(q8_append_kernel<T, kI, kWide>, grid, dim3(threads), 0, stream, nullptr, 0, a, p, (int)tiles,
-                    tile_rows, lanes, hg);
+  return launch_pdl(q8_append_kernel<T, kI, kWide, kInter>, grid, dim3(threads), 0, stream, nullptr, 0, a, p,
+                    (int)tiles, tile_rows, lanes, hg);
 }
 
 template <typename T>
@@ -338,17 +404,16 @@ static cudaError_t launch_qa_t(const RotaryArgs& a, Q8Pages p, cudaStream_t stre
   p.wide_out = reinterpret_cast<uintptr_t>(a.q_out) % 16 == 0;
   int lanes = 2;  // D / 16 columns, up to the next power of two
   while (lanes * 16 < a.D) lanes *= 2;
-  // a tile's rows, 64 or more, over 256 threads; calls of few rows need no more than those
-  if ((long long)a.N * lanes <= kQaThreads || lanes <= 4) {
-    const int threads = min(kQaThreads, (a.N * lanes + 31) / 32 * 32);
-    return wide ? launch_qa<T, 1, true>(a, p, threads, lanes, stream)
-                : launch_qa<T, 1, false>(a, p, threads, lanes, stream);
-  }
-  if (lanes == 8)
-    return wide ? launch_qa<T, 2, true>(a, p, kQaThreads, lanes, stream)
-                : launch_qa<T, 2, false>(a, p, kQaThreads, lanes, stream);
-  return wide ? launch_qa<T, 4, true>(a, p, kQaThreads, lanes, stream)
-              : launch_qa<T, 4, false>(a, p, kQaThreads, lanes, stream);
+  // whole blocks, a row a thread where 512 threads allow it; calls of few rows need no more threads than those
+  const int tile_rows = max(1 << p.block_shift, 256 / lanes), all = tile_rows * lanes;
+  const int threads = (int)min((long long)min(all, kQaThreads), ((long long)a.N * lanes + 31) / 32 * 32);
+  if (all > kQaThreads && a.N * lanes > kQaThreads)
+    return !wide           ? launch_qa<T, 2, false, false>(a, p, tile_rows, threads, lanes, stream)
+           : a.interleaved ? launch_qa<T, 2, true, true>(a, p, tile_rows, threads, lanes, stream)
+                           : launch_qa<T, 2, true, false>(a, p, tile_rows, threads, lanes, stream);
+  return !wide           ? launch_qa<T, 1, false, false>(a, p, tile_rows, threads, lanes, stream)
+         : a.interleaved ? launch_qa<T, 1, true, true>(a, p, tile_rows, threads, lanes, stream)
+                         : launch_qa<T, 1, true, false>(a, p, tile_rows, threads, lanes, stream);
 }
 
 cudaError_t launch_q8_append(const RotaryArgs& a, const Q8Pages& p, tv_dtype dtype, cudaStream_t stream) {

@@ -23,14 +23,13 @@ namespace tv {
 constexpr int kRotThreads = 256;
 constexpr int kRotHeads = 3;  // heads whose loads are in flight together
 constexpr long long kRotBlocks = 152 * 16;  // blocks up to which a token's heads go to separate ones
+constexpr int kNormHeads = 3;               // the same two with norms
+constexpr long long kNormBlocks = 152 * 8;
 
 // Grid: x over (token, column) pairs, y over groups of `hg` of the Hq + 2 Hkv heads.  A column
 // is kVec pairs (rotated part) or up to 2 kVec elements behind it.
-// kNorm: queries and keys are first divided by their root mean square over the head and multiplied by a
-// weight, in 32 bits; the `cols` (a power of two up to 32) threads of a token are neighbours in a warp and
-// add up their squares by shuffles.
-template <typename T, int kVec, bool kNorm>
-__global__ void __launch_bounds__(kRotThreads, kNorm ? 3 : 4) rotary_kernel(RotaryArgs a, int cols, int rot_cols, int hg) {
+template <typename T, int kVec>
+__global__ void __launch_bounds__(kRotThreads, 4) rotary_kernel(RotaryArgs a, int cols, int rot_cols, int hg) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const long long id = (long long)blockIdx.x * kRotThreads + threadIdx.x;
@@ -79,7 +78,6 @@ __global__ void __launch_bounds__(kRotThreads, kNorm ? 3 : 4) rotary_kernel(Rota
   };
   const bool two = eb < a.D;
   using Raw = typename RotRaw<T, kVec>::type;
-  const uint32_t peers = kNorm ? (cols == 32 ? ~0u : ((1u << cols) - 1u) << (threadIdx.x & 31 & -cols)) : 0u;
   for (int hb = h0; hb < h1; hb += kRotHeads) {
     // the batch's loads first: they are in flight together (a row may be rotated in place, so the
     // compiler would not move a load past an earlier head's store)
@@ -96,18 +94,11 @@ __global__ void __launch_bounds__(kRotThreads, kNorm ? 3 : 4) rotary_kernel(Rota
       if (hb + u >= h1) break;
       T* dst = target(hb + u);
       if (!dst) continue;
-      const bool normed = kNorm && hb + u < a.Hq + a.Hkv;
-      if (normed || (turn && hb + u < a.Hq + a.Hkv)) {
+      if (turn && hb + u < a.Hq + a.Hkv) {
         float x[kVec], y[kVec];
         rot_unpack<T, kVec>(ra[u], x);
-        if (turn || two) {
-          rot_unpack<T, kVec>(rb[u], y);
-        } else {
-#pragma unroll
-          for (int k = 0; k < kVec; ++k) y[k] = 0.f;
-        }
-        if constexpr (kNorm) rot_norm<T, kVec>(a, hb + u < a.Hq ? 0 : 1, ea, eb, two, cols, peers, x, y);
-        if (turn && pairs_inside) {
+        rot_unpack<T, kVec>(rb[u], y);
+        if (pairs_inside) {
 #pragma unroll
           for (int k = 0; k < kVec / 2; ++k) {
             const float e0 = x[2 * k], o0 = x[2 * k + 1], e1 = y[2 * k], o1 = y[2 * k + 1];
@@ -116,7 +107,7 @@ __global__ void __launch_bounds__(kRotThreads, kNorm ? 3 : 4) rotary_kernel(Rota
             y[2 * k] = e1 * cs[kVec / 2 + k] - o1 * sn[kVec / 2 + k];
             y[2 * k + 1] = o1 * cs[kVec / 2 + k] + e1 * sn[kVec / 2 + k];
           }
-        } else if (turn) {
+        } else {
 #pragma unroll
           for (int k = 0; k < kVec; ++k) {
             const float e = x[k], o = y[k];
@@ -134,7 +125,107 @@ __global__ void __launch_bounds__(kRotThreads, kNorm ? 3 : 4) rotary_kernel(Rota
   }
 }
 
-// The same with norms for heads and rows that rotary_kernel's columns do not fit (no power of two of
+// The same with norms: queries and keys are first divided by their root mean square over the head and multiplied
+// by a weight, in 32 bits.  The `cols` (a power of two up to 32) threads of a token are neighbours in a warp and add
+// up their squares by shuffles; the weight goes into the sines and cosines, which a thread takes once for its
+// group's heads, all of them queries, keys or values, and the arithmetic is two numbers an instruction.  268 MB (4 x
+// 4096 rows of 32 heads of 128 bf16, 64 turned): 51.8 us, 5.2 TB/s; two heads in flight 53.3, four 58.7 (spills); four
+// that are not loaded ahead of the work on those before 54.5, two of them 66; with a branch a head 75.  64 tokens: 3.3 us.
+template <typename T, int kVec, bool kInter>
+__global__ void __launch_bounds__(kRotThreads, 2) norm_rotary_kernel(RotaryArgs a, int cols, int rot_cols, int hg) {
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int col = threadIdx.x & (cols - 1);
+  const long long token = (long long)blockIdx.x * (kRotThreads / cols) + threadIdx.x / cols;
+  if (token >= (long long)a.B * a.N) return;
+  const int b = (int)token / a.N, t = (int)token - b * a.N;  // kMaxRotaryRows fits an int
+  const int qg = (a.Hq + hg - 1) / hg, kg = (a.Hkv + hg - 1) / hg;
+  const int part = (int)blockIdx.y < qg ? 0 : (int)blockIdx.y < qg + kg ? 1 : 2;
+  const int h0 = ((int)blockIdx.y - (part == 0 ? 0 : part == 1 ? qg : qg + kg)) * hg;
+  const int heads = min(part ? a.Hkv : a.Hq, h0 + hg) - h0;
+  const RotPlace at = rot_place(a, token, b, t, col == 0 && blockIdx.y == 0, part > 0);
+  if (!at.live || (part > 0 && at.page_row < 0)) return;
+  const bool turn = col < rot_cols && part < 2;
+  const int ea = col < rot_cols ? kVec * col : a.rot + kVec * (col - rot_cols);
+  const int eb = ea + (col < rot_cols ? a.rot / 2 : kVec * (cols - rot_cols));
+  using Raw = typename RotRaw<T, kVec>::type;
+  // the loads of heads h and on, kNormHeads of them or one, ahead of the work on those before
+  const long long sh = a.sh[part];
+  const T* src = reinterpret_cast<const T*>(a.src[part]) + b * a.sb[part] + h0 * sh + t * a.sn[part];
+  Raw ra[kNormHeads], rb[kNormHeads];
+  auto load = [&](int h) {
+    const T* from = src + h * sh;
+    if (h + kNormHeads <= heads) {
+#pragma unroll
+      for (int u = 0; u < kNormHeads; ++u) {
+        ra[u] = *reinterpret_cast<const Raw*>(from + u * sh + ea);
+        rb[u] = *reinterpret_cast<const Raw*>(from + u * sh + eb);
+      }
+    } else if (h < heads) {
+      ra[0] = *reinterpret_cast<const Raw*>(from + ea);
+      rb[0] = *reinterpret_cast<const Raw*>(from + eb);
+    }
+  };
+  load(0);
+  RotTurn<kVec> turns;
+  if (part < 2) {
+    const T* weight = reinterpret_cast<const T*>(a.weight[part]);
+    float x[kVec], y[kVec];
+    rot_unpack<T, kVec>(*reinterpret_cast<const Raw*>(weight + ea), x);
+    rot_unpack<T, kVec>(*reinterpret_cast<const Raw*>(weight + eb), y);
+    float2 wa[kVec / 2], wb[kVec / 2];
+    rot_to_pairs<kVec, kInter>(x, y, wa, wb);
+    rot_turn_set<kVec, kInter>(a, at.pos, turn, col, wa, wb, turns);
+  }
+  const long long step = part ? (long long)a.D << a.page_shift : (long long)a.N * a.D;  // a head's, of the target
+  T* dst = part == 0 ? reinterpret_cast<T*>(a.q_out) + (((long long)b * a.Hq + h0) * a.N + t) * a.D
+                     : reinterpret_cast<T*>(part == 1 ? a.k_cache : a.v_cache) +
+                           (at.page_row + ((long long)h0 << a.page_shift)) * a.D;
+  const uint32_t peers = cols == 32 ? ~0u : ((1u << cols) - 1u) << (threadIdx.x & 31 & -cols);
+  const float inv_d = 1.f / a.D;
+  // heads h.., which have been loaded, without a branch among them
+  auto turn_heads = [&](auto many, int h) {
+    constexpr int kMany = decltype(many)::value;
+    float2 pa[kMany][kVec / 2], pb[kMany][kVec / 2];
+    float ss[kMany];
+#pragma unroll
+    for (int u = 0; u < kMany; ++u) {
+      float x[kVec], y[kVec];
+      rot_unpack<T, kVec>(ra[u], x);
+      rot_unpack<T, kVec>(rb[u], y);
+      rot_to_pairs<kVec, kInter>(x, y, pa[u], pb[u]);
+      ss[u] = rot_squares<kVec>(pa[u], pb[u]);
+    }
+    load(h + kMany);
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      if (o >= cols) continue;
+#pragma unroll
+      for (int u = 0; u < kMany; ++u) ss[u] += __shfl_xor_sync(peers, ss[u], o);
+    }
+#pragma unroll
+    for (int u = 0; u < kMany; ++u) {
+      float x[kVec], y[kVec];
+      rot_turn<kVec>(turns, true, __frsqrt_rn(fmaf(ss[u], inv_d, a.eps)), turn, pa[u], pb[u]);
+      rot_from_pairs<kVec, kInter>(pa[u], pb[u], x, y);
+      *reinterpret_cast<Raw*>(dst + (h + u) * step + ea) = rot_pack<T, kVec>(x);
+      *reinterpret_cast<Raw*>(dst + (h + u) * step + eb) = rot_pack<T, kVec>(y);
+    }
+  };
+  if (part == 2) {
+    for (int h = 0; h < heads; ++h) {
+      const Raw x = *reinterpret_cast<const Raw*>(src + h * sh + ea), y = *reinterpret_cast<const Raw*>(src + h * sh + eb);
+      *reinterpret_cast<Raw*>(dst + h * step + ea) = x;
+      *reinterpret_cast<Raw*>(dst + h * step + eb) = y;
+    }
+    return;
+  }
+  int h = 0;
+  for (; h + kNormHeads <= heads; h += kNormHeads) turn_heads(std::integral_constant<int, kNormHeads>(), h);
+  for (; h < heads; ++h) turn_heads(std::integral_constant<int, 1>(), h);
+}
+
+// The same with norms for heads and rows that norm_rotary_kernel's columns do not fit (no power of two of
 // columns, or not 16 bytes each): a warp a row, an element and its pair partner a lane.
 template <typename T>
 __global__ void __launch_bounds__(kRotThreads) norm_rows_kernel(RotaryArgs a) {
@@ -190,7 +281,20 @@ __global__ void __launch_bounds__(kRotThreads) norm_rows_kernel(RotaryArgs a) {
   }
 }
 
-template <typename T, int kVec, bool kNorm>
+template <typename T, int kVec>
+static cudaError_t launch_norm_rot(const RotaryArgs& a, cudaStream_t stream) {
+  const int cols = a.D / (2 * kVec);
+  const long long blocks = ((long long)a.B * a.N * cols + kRotThreads - 1) / kRotThreads;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  auto groups = [&](int g) { return (long long)(a.Hq + g - 1) / g + 2ll * ((a.Hkv + g - 1) / g); };
+  int hg = 1;
+  while (hg < max(a.Hq, a.Hkv) && blocks * groups(hg) > kNormBlocks) hg *= 2;
+  return launch_pdl(a.interleaved ? norm_rotary_kernel<T, kVec, true> : norm_rotary_kernel<T, kVec, false>,
+                    dim3((unsigned)blocks, (unsigned)groups(hg)), dim3(kRotThreads), 0, stream, nullptr, 0, a, cols,
+                    a.rot / (2 * kVec), hg);
+}
+
+template <typename T, int kVec>
 static cudaError_t launch_rot(const RotaryArgs& a, cudaStream_t stream) {
   const int rot_cols = a.rot / (2 * kVec);
   const int rest = a.D - a.rot;
@@ -202,7 +306,7 @@ static cudaError_t launch_rot(const RotaryArgs& a, cudaStream_t stream) {
   int hg = 1;
   while (hg < heads && blocks * ((heads + hg - 1) / hg) > kRotBlocks) hg *= 2;
   const dim3 grid((unsigned)blocks, (unsigned)((heads + hg - 1) / hg));
-  return launch_pdl(rotary_kernel<T, kVec, kNorm>, grid, dim3(kRotThreads), 0, stream, nullptr, 0, a, cols, rot_cols, hg);
+  return launch_pdl(rotary_kernel<T, kVec>, grid, dim3(kRotThreads), 0, stream, nullptr, 0, a, cols, rot_cols, hg);
 }
 
 cudaError_t launch_rotary(const RotaryArgs& a, tv_dtype dtype, cudaStream_t stream) {
@@ -221,7 +325,7 @@ cudaError_t launch_rotary(const RotaryArgs& a, tv_dtype dtype, cudaStream_t stre
     const int cols = a.D / (2 * vec);
     // the columns of a head: a power of two up to a warp, none of them half empty
     if (wide && a.D % (2 * vec) == 0 && cols <= 32 && (cols & (cols - 1)) == 0)
-      return dtype == TV_BF16 ? launch_rot<uint16_t, 8, true>(a, stream) : launch_rot<float, 4, true>(a, stream);
+      return dtype == TV_BF16 ? launch_norm_rot<uint16_t, 8>(a, stream) : launch_norm_rot<float, 4>(a, stream);
     const long long blocks = ((long long)a.B * a.N + kRotThreads / 32 - 1) / (kRotThreads / 32);
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
     const dim3 grid((unsigned)blocks, (unsigned)(a.Hq + 2 * a.Hkv));
@@ -229,8 +333,8 @@ cudaError_t launch_rotary(const RotaryArgs& a, tv_dtype dtype, cudaStream_t stre
                       dim3(kRotThreads), 0, stream, nullptr, 0, a);
   }
   if (dtype == TV_BF16)
-    return wide ? launch_rot<uint16_t, 8, false>(a, stream) : launch_rot<uint16_t, 1, false>(a, stream);
-  return wide ? launch_rot<float, 4, false>(a, stream) : launch_rot<float, 1, false>(a, stream);
+    return wide ? launch_rot<uint16_t, 8>(a, stream) : launch_rot<uint16_t, 1>(a, stream);
+  return wide ? launch_rot<float, 4>(a, stream) : launch_rot<float, 1>(a, stream);
 }
 
 // Frequencies in 2^-64 turns a position.  With r_i = base^(-2i/R) radians:

@@ -99,25 +99,95 @@ __device__ __forceinline__ RotPlace rot_place(const RotaryArgs& a, long long tok
   return r;
 }
 
-// x and y over the head's root mean square, times the weight: `part` 0 queries, 1 keys
-template <typename T, int kVec>
-__device__ __forceinline__ void rot_norm(const RotaryArgs& a, int part, int ea, int eb, bool two, int cols,
-                                         uint32_t peers, float (&x)[kVec], float (&y)[kVec]) {
-  float ss = 0.f;
+// 16 bytes and their pair partners of a head as pairs (a[u], b[u]): element u of each of them, or, where neighbours
+// turn together, an element and the next.  Two pairs to a word, for arithmetic that takes two numbers at once.
+template <int kVec, bool kInter>
+__device__ __forceinline__ void rot_to_pairs(const float (&x)[kVec], const float (&y)[kVec], float2 (&a)[kVec / 2],
+                                             float2 (&b)[kVec / 2]) {
 #pragma unroll
-  for (int k = 0; k < kVec; ++k) ss = fmaf(x[k], x[k], fmaf(y[k], y[k], ss));
-  for (int o = 1; o < cols; o *= 2) ss += __shfl_xor_sync(peers, ss, o);
-  const float r = 1.f / sqrtf(ss / a.D + a.eps);
-  const T* weight = reinterpret_cast<const T*>(a.weight[part]);
-  using Raw = typename RotRaw<T, kVec>::type;
-  float w[kVec];
-  rot_unpack<T, kVec>(__ldg(reinterpret_cast<const Raw*>(weight + ea)), w);
+  for (int k = 0; k < kVec / 2; ++k) {
+    if constexpr (kInter) {
+      const float* f = k < kVec / 4 ? x + 4 * k : y + 4 * (k - kVec / 4);
+      a[k] = make_float2(f[0], f[2]), b[k] = make_float2(f[1], f[3]);
+    } else {
+      a[k] = make_float2(x[2 * k], x[2 * k + 1]), b[k] = make_float2(y[2 * k], y[2 * k + 1]);
+    }
+  }
+}
+template <int kVec, bool kInter>
+__device__ __forceinline__ void rot_from_pairs(const float2 (&a)[kVec / 2], const float2 (&b)[kVec / 2], float (&x)[kVec],
+                                               float (&y)[kVec]) {
 #pragma unroll
-  for (int k = 0; k < kVec; ++k) x[k] = x[k] * r * w[k];
-  if (!two) return;
-  rot_unpack<T, kVec>(__ldg(reinterpret_cast<const Raw*>(weight + eb)), w);
+  for (int k = 0; k < kVec / 2; ++k) {
+    if constexpr (kInter) {
+      float* f = k < kVec / 4 ? x + 4 * k : y + 4 * (k - kVec / 4);
+      f[0] = a[k].x, f[1] = b[k].x, f[2] = a[k].y, f[3] = b[k].y;
+    } else {
+      x[2 * k] = a[k].x, x[2 * k + 1] = a[k].y, y[2 * k] = b[k].x, y[2 * k + 1] = b[k].y;
+    }
+  }
+}
+// the number of pair u of column `col`
+template <int kVec, bool kInter>
+__device__ __forceinline__ int rot_pair(int rot, int col, int u) {
+  return kInter ? (u < kVec / 2 ? 0 : rot / 4 - kVec / 2) + kVec / 2 * col + u : kVec * col + u;
+}
+// What a row's pairs are multiplied by, the norm's weight taken in: (a, b) -> (a ca + b nb, b cb + a sa).  Once
+// for all the heads that a thread turns.
+template <int kVec>
+struct RotTurn {
+  float2 ca[kVec / 2], nb[kVec / 2], cb[kVec / 2], sa[kVec / 2];
+};
+// w: the weights of the pairs (1 without a norm); columns that do not turn use ca and cb alone
+template <int kVec, bool kInter>
+__device__ __forceinline__ void rot_turn_set(const RotaryArgs& a, long long pos, bool turn, int col,
+                                             const float2 (&wa)[kVec / 2], const float2 (&wb)[kVec / 2],
+                                             RotTurn<kVec>& t) {
 #pragma unroll
-  for (int k = 0; k < kVec; ++k) y[k] = y[k] * r * w[k];
+  for (int k = 0; k < kVec / 2; ++k) {
+    t.ca[k] = wa[k], t.cb[k] = wb[k];
+    if (!turn) continue;
+    const float2 p = sincos_turns((uint64_t)pos * a.freq[rot_pair<kVec, kInter>(a.rot, col, 2 * k)]);
+    const float2 q = sincos_turns((uint64_t)pos * a.freq[rot_pair<kVec, kInter>(a.rot, col, 2 * k + 1)]);
+    const float2 sn = make_float2(p.x * a.amplitude, q.x * a.amplitude);
+    const float2 cs = make_float2(p.y * a.amplitude, q.y * a.amplitude);
+    t.sa[k] = __fmul2_rn(wa[k], sn);
+    t.nb[k] = __fmul2_rn(wb[k], make_float2(-sn.x, -sn.y));
+    t.ca[k] = __fmul2_rn(wa[k], cs);
+    t.cb[k] = __fmul2_rn(wb[k], cs);
+  }
+}
+template <int kVec>
+__device__ __forceinline__ float rot_squares(const float2 (&a)[kVec / 2], const float2 (&b)[kVec / 2]) {
+  float2 s = __fmul2_rn(a[0], a[0]);
+#pragma unroll
+  for (int k = 1; k < kVec / 2; ++k) s = __ffma2_rn(a[k], a[k], s);
+#pragma unroll
+  for (int k = 0; k < kVec / 2; ++k) s = __ffma2_rn(b[k], b[k], s);
+  return s.x + s.y;
+}
+// r: 1 over the head's root mean square (normed), else unread
+template <int kVec>
+__device__ __forceinline__ void rot_turn(const RotTurn<kVec>& t, bool normed, float r, bool turn, float2 (&a)[kVec / 2],
+                                         float2 (&b)[kVec / 2]) {
+  if (normed) {
+#pragma unroll
+    for (int k = 0; k < kVec / 2; ++k) {
+      a[k] = __fmul2_rn(a[k], make_float2(r, r));
+      b[k] = __fmul2_rn(b[k], make_float2(r, r));
+    }
+  }
+  if (turn) {
+#pragma unroll
+    for (int k = 0; k < kVec / 2; ++k) {
+      const float2 x = a[k];
+      a[k] = __ffma2_rn(b[k], t.nb[k], __fmul2_rn(x, t.ca[k]));
+      b[k] = __ffma2_rn(x, t.sa[k], __fmul2_rn(b[k], t.cb[k]));
+    }
+  } else if (normed) {
+#pragma unroll
+    for (int k = 0; k < kVec / 2; ++k) a[k] = __fmul2_rn(a[k], t.ca[k]), b[k] = __fmul2_rn(b[k], t.cb[k]);
+  }
 }
 
 }  // namespace tv
