@@ -385,7 +385,8 @@ cudaError_t launch_paged_mma(PagedAttn a, char* ws, cudaStream_t stream);
 cudaError_t launch_paged_q8_mma(PagedAttn a, char* ws, cudaStream_t stream);
 PagedWs paged_f32_ws(int B, int Hq, int Hkv, int D, int N);
 cudaError_t launch_paged_f32(PagedAttn a, char* ws, cudaStream_t stream);
-cudaError_t launch_paged_q8_f32(PagedAttn a, char* ws, tv_dtype dtype, cudaStream_t stream);
+PagedWs paged_q8_f32_ws(int B, int Hq, int Hkv, int D, int N);
+cudaError_t launch_paged_q8_f32(PagedAttn a, char* ws, cudaStream_t stream);
 PagedWs paged_simt_ws(int D);
 cudaError_t launch_paged_simt(PagedAttn a, char* ws, cudaStream_t stream);
 // Tensor map of bf16 pages, 128-byte swizzle.  D = 128 and 256: 5-D, a box spans all column

@@ -47,12 +47,12 @@ cudaError_t launch_paged_attn(PagedAttn a, tv_dtype dtype, char* ws, cudaStream_
 
 // Over pages in 8 bits: fp32 on CUDA cores, bf16 as over bf16 pages.
 PagedWs paged_q8_attn_ws(int B, int Hq, int Hkv, int D, int N, tv_dtype dtype, int sms) {
-  if (dtype == TV_F32) return paged_f32_ws(B, Hq, Hkv, D, N);
+  if (dtype == TV_F32) return paged_q8_f32_ws(B, Hq, Hkv, D, N);
   return paged_tc_takes(Hq, Hkv, D, N) ? paged_tc_ws(B, Hq, Hkv, D, N) : paged_mma_ws(B, Hq, Hkv, D, N, sms);
 }
 
 cudaError_t launch_paged_q8_attn(PagedAttn a, tv_dtype dtype, char* ws, cudaStream_t stream) {
-  if (dtype == TV_F32) return launch_paged_q8_f32(a, ws, dtype, stream);
+  if (dtype == TV_F32) return launch_paged_q8_f32(a, ws, stream);
   return paged_tc_takes(a.Hq, a.Hkv, a.D, a.N) ? launch_paged_q8_tc(a, ws, stream) : launch_paged_q8_mma(a, ws, stream);
 }
 

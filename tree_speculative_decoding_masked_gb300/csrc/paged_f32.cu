@@ -9,7 +9,7 @@ PagedWs paged_f32_ws(int B, int Hq, int Hkv, int D, int N) {
 }
 
 cudaError_t launch_paged_f32(PagedAttn a, char* ws, cudaStream_t stream) {
-  return launch_pf_d<false, float>(a, ws, stream);
+  return launch_pf_d<false>(a, ws, stream);
 }
 
 }  // namespace tv

@@ -51,7 +51,7 @@ __device__ __forceinline__ void pf_put2(uint16_t* p, float x, float y) {
 
 // kQ8: K and V are e4m3 codes with block scales (q8.cuh), turned into fp32 numbers as they are stored to
 // shared memory: a tile's codes wait in registers while the tile before is used.
-template <int kD, bool kStream, bool kQ8, typename IO>
+template <int kD, bool kStream, bool kQ8>
 __global__ void __launch_bounds__(kPfThreads, kD <= 64 ? 2 : 1)
     paged_f32_kernel(PagedAttn a, int splits, int row_tiles) {
   using S = PfSmem<kD>;
@@ -67,8 +67,8 @@ __global__ void __launch_bounds__(kPfThreads, kD <= 64 ? 2 : 1)
   __shared__ int s_par[kMaxNodes];
   __shared__ int s_lo[kPfRows], s_hi[kPfRows], s_page[2][kPfKeys / 8], s_first_pad, s_last;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const IO* q = reinterpret_cast<const IO*>(a.q);
-  IO* out = reinterpret_cast<IO*>(a.out);
+  const float* q = reinterpret_cast<const float*>(a.q);
+  float* out = reinterpret_cast<float*>(a.out);
   constexpr int kC = kQ8 ? (kPfKeys * (kD / 16) + kPfThreads - 1) / kPfThreads : 1;  // 16 codes each
   uint4 k_raw[kC], v_raw[kC];
   float k_scale[kC], v_scale[kC];
@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(kPfThreads, kD <= 64 ? 2 : 1)
       for (int o = 1; o < 16; o *= 2) l[x] += __shfl_xor_sync(0xffffffffu, l[x], o);
       if (rr >= rows || i >= n_act) continue;
       if (c0 == c1) {
-        IO* to = out + (((size_t)b * a.Hq + hk * a.G + g) * a.N + i) * kD;
+        float* to = out + (((size_t)b * a.Hq + hk * a.G + g) * a.N + i) * kD;
         const float f = 1.f / l[x];
 #pragma unroll
         for (int u = 0; u < kU; ++u) pf_put2(to + tx * 2 + 32 * u, acc[x][u][0] * f, acc[x][u][1] * f);
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(kPfThreads, kD <= 64 ? 2 : 1)
         }
       }
       const float f = 1.f / L;
-      IO* to = out + (((size_t)b * a.Hq + hk * a.G + g) * a.N + i) * kD + ch * 4;
+      float* to = out + (((size_t)b * a.Hq + hk * a.G + g) * a.N + i) * kD + ch * 4;
       pf_put2(to, o.x * f, o.y * f);
       pf_put2(to + 2, o.z * f, o.w * f);
     }
@@ -480,9 +480,9 @@ static PfPlan pf_plan(int B, int Hq, int Hkv, int D, int N, int sms) {
   return p;
 }
 
-template <int kD, bool kStream, bool kQ8, typename IO>
+template <int kD, bool kStream, bool kQ8>
 static cudaError_t launch_pf_s(PagedAttn a, const PfPlan& p, cudaStream_t stream) {
-  const auto fn = paged_f32_kernel<kD, kStream, kQ8, IO>;
+  const auto fn = paged_f32_kernel<kD, kStream, kQ8>;
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, PfSmem<kD>::kBytes);
   if (e != cudaSuccess) return e;
   if (kStream)
@@ -497,34 +497,34 @@ static cudaError_t launch_pf_s(PagedAttn a, const PfPlan& p, cudaStream_t stream
                     PfSmem<kD>::kBytes, stream, attr, 1, a, p.splits, p.row_tiles);
 }
 
-template <int kD, bool kQ8, typename IO>
+template <int kD, bool kQ8>
 static cudaError_t launch_pf(PagedAttn a, char* ws, cudaStream_t stream) {
   const PfPlan p = pf_plan(a.B, a.Hq, a.Hkv, a.D, a.N, a.sms);
   a.cnt = reinterpret_cast<unsigned*>(ws);
   a.ws_ml = reinterpret_cast<float2*>(ws + kPagedCntBytes);
   a.ws_o = reinterpret_cast<float*>(ws + kPagedCntBytes + p.rows * 8);
-  return p.splits ? launch_pf_s<kD, false, kQ8, IO>(a, p, stream) : launch_pf_s<kD, true, kQ8, IO>(a, p, stream);
+  return p.splits ? launch_pf_s<kD, false, kQ8>(a, p, stream) : launch_pf_s<kD, true, kQ8>(a, p, stream);
 }
 
-template <bool kQ8, typename IO>
+template <bool kQ8>
 static cudaError_t launch_pf_d(const PagedAttn& a, char* ws, cudaStream_t stream) {
   switch (a.D / 32) {
     case 1:
-      return launch_pf<32, kQ8, IO>(a, ws, stream);
+      return launch_pf<32, kQ8>(a, ws, stream);
     case 2:
-      return launch_pf<64, kQ8, IO>(a, ws, stream);
+      return launch_pf<64, kQ8>(a, ws, stream);
     case 3:
-      return launch_pf<96, kQ8, IO>(a, ws, stream);
+      return launch_pf<96, kQ8>(a, ws, stream);
     case 4:
-      return launch_pf<128, kQ8, IO>(a, ws, stream);
+      return launch_pf<128, kQ8>(a, ws, stream);
     case 5:
-      return launch_pf<160, kQ8, IO>(a, ws, stream);
+      return launch_pf<160, kQ8>(a, ws, stream);
     case 6:
-      return launch_pf<192, kQ8, IO>(a, ws, stream);
+      return launch_pf<192, kQ8>(a, ws, stream);
     case 7:
-      return launch_pf<224, kQ8, IO>(a, ws, stream);
+      return launch_pf<224, kQ8>(a, ws, stream);
     case 8:
-      return launch_pf<256, kQ8, IO>(a, ws, stream);
+      return launch_pf<256, kQ8>(a, ws, stream);
     default:
       return cudaErrorInvalidValue;
   }

@@ -56,10 +56,15 @@ __device__ __forceinline__ float q8_half_hi(uint32_t h) {
   asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 %0, hi;\n\t}" : "=f"(f) : "r"(h));
   return f;
 }
+// four codes
+__device__ __forceinline__ float4 q8_quad(uint32_t w) {
+  const uint32_t a = q8_half2((uint16_t)w), b = q8_half2((uint16_t)(w >> 16));
+  return make_float4(q8_half_lo(a), q8_half_hi(a), q8_half_lo(b), q8_half_hi(b));
+}
 // four codes times a scale
 __device__ __forceinline__ float4 q8_numbers(uint32_t w, float scale) {
-  const uint32_t a = q8_half2((uint16_t)w), b = q8_half2((uint16_t)(w >> 16));
-  return make_float4(q8_half_lo(a) * scale, q8_half_hi(a) * scale, q8_half_lo(b) * scale, q8_half_hi(b) * scale);
+  const float4 f = q8_quad(w);
+  return make_float4(f.x * scale, f.y * scale, f.z * scale, f.w * scale);
 }
 __device__ __forceinline__ uint32_t q8_code4(float a, float b, float c, float d) {
   return q8_code2(a, b) | q8_code2(c, d) << 16;
