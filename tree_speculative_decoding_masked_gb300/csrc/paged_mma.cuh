@@ -1039,6 +1039,10 @@ static cudaError_t launch_pm_d(const CUtensorMap& mk, const CUtensorMap& mv, con
   return launch_pm_c<kD, 16, kQ8>(mk, mv, a, p, stream);
 }
 
+// launch_pm_d<256, true>, a file of its own to compile
+cudaError_t launch_pm_q8_wide(const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a, const PmPlan& p,
+                              cudaStream_t stream);
+
 template <bool kQ8>
 static cudaError_t launch_pm_all(PagedAttn a, char* ws, cudaStream_t stream) {
   const PmPlan p = pm_plan(a.B, a.Hq, a.Hkv, a.D, a.N, a.sms);
@@ -1054,7 +1058,10 @@ static cudaError_t launch_pm_all(PagedAttn a, char* ws, cudaStream_t stream) {
   if (!made) return cudaErrorInvalidValue;
   if (a.D <= 64) return launch_pm_d<64, kQ8>(mk, mv, a, p, stream);
   if (a.D <= 128) return launch_pm_d<128, kQ8>(mk, mv, a, p, stream);
-  return launch_pm_d<256, kQ8>(mk, mv, a, p, stream);
+  if constexpr (kQ8)
+    return launch_pm_q8_wide(mk, mv, a, p, stream);
+  else
+    return launch_pm_d<256, false>(mk, mv, a, p, stream);
 }
 
 }  // namespace tv

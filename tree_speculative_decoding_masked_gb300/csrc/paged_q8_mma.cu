@@ -1,4 +1,5 @@
-// Paged attention of few rows over pages in 8 bits: paged_mma.cuh's kernel.
+// Paged attention of few rows over pages in 8 bits: paged_mma.cuh's kernel (heads of more than 128:
+// paged_q8_mma_wide.cu).
 #include "paged_mma.cuh"
 
 namespace tv {
