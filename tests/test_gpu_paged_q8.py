@@ -147,6 +147,24 @@ def test_norm_rotary(D, rot, inter, bf16):
     assert torch.equal(y, got)
 
 
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("inter", [False, True])
+def test_norm_heads_share_a_group(inter, bf16):
+    """Enough rows that heads share a thread, in numbers that its turns do not divide."""
+    g = synth.rng(3050)
+    B, H, N, D, rot = 3, 7, 20001, 64, 32
+    x = synth.normal(g, (B, H, N, D), 1.0, bf16)
+    weight = synth.normal(g, (D,), 1.0, bf16)
+    pos = g.integers(0, 1 << 20, (B, N)).astype(np.int32)
+    rope, ref_rope = tv.rotary_frequencies(rot, 500000.0), rotary.frequencies(rot, 500000.0)
+    ref = rotary.rotate(q8.norm(x, weight, 1e-5), pos[:, None], *ref_rope, inter)
+    tol = _norm_tol(x, weight, 1e-5, pos, ref_rope, inter, bf16, ref)
+    xd, wd = to_dev(x, bf16), to_dev(weight, bf16)
+    got = tv.norm_rotary(xd, wd, i32(pos), rope, eps=1e-5, interleaved=inter)
+    assert np.all(np.abs(host(got).astype(np.float64) - ref) <= tol)
+    assert torch.equal(tv.norm_rotary(xd, wd, i32(pos), rope, eps=1e-5, interleaved=inter, out=xd), got)
+
+
 def test_norm_of_zeros_and_one_row():
     for bf16 in (True, False):
         x = torch.zeros((1, 1, 1, 64), dtype=torch.bfloat16 if bf16 else torch.float32, device=dev())
@@ -293,6 +311,24 @@ def test_append_heads(D, rot, norm, inter, bf16):
 
 
 @pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("D,rot,inter", [(256, 256, False), (160, 64, True)])
+def test_append_wide_heads_and_long_blocks(D, rot, inter, norm, bf16):
+    """More elements in a block of rows than a CTA has threads for: two rows a thread."""
+    _append_check(synth.rng(3320 + D), 2, 3, 2, 150, D, rot, 128, 64, [5, 190], inter=inter, norm=norm, bf16=bf16)
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("D,rot,inter", [(64, 64, False), (96, 64, True)])
+def test_append_heads_share_a_group(D, rot, inter, norm, bf16):
+    """Enough rows that heads share a CTA, in numbers that its turns do not divide."""
+    B, Hq, Hkv, N = 90, 7, 3, 100
+    prefix = [int(p) for p in synth.rng(3330).integers(0, 70, B)]
+    _append_check(synth.rng(3340 + D), B, Hq, Hkv, N, D, rot, 32, 16, prefix, inter=inter, norm=norm, bf16=bf16)
+
+
+@pytest.mark.parametrize("bf16", [True, False])
 @pytest.mark.parametrize("std", [2.0 ** -60, 2.0 ** -140, 2.0 ** 100])
 def test_append_far_scales(std, bf16):
     if bf16 and std < 2.0 ** -120:
@@ -428,6 +464,29 @@ def test_attend(shape, blk, bf16):
     B, Hq, Hkv, D, ps, prefix, N = shape
     _q8_attend_check(synth.rng(4000 + sum(shape[:5]) + N), B, Hq, Hkv, D, ps, prefix, N, blk=min(blk, ps), bf16=bf16,
                      wide=blk == 8)
+
+
+@pytest.mark.parametrize("Hq,Hkv,N", [(2, 2, 1), (4, 2, 1), (3, 1, 1), (8, 2, 1), (2, 2, 2), (2, 2, 3), (4, 2, 2)])
+@pytest.mark.parametrize("D", [32, 64, 96, 128, 192, 256])
+def test_attend_few_fp32_rows(D, Hq, Hkv, N):
+    g = synth.rng(4150 + D + Hq + N)
+    par, _ = W.trees(g, 3, N, 3, 50)
+    _q8_attend_check(g, 3, Hq, Hkv, D, 16, [700, 0, 333], N, blk=16, bf16=False, wide=True)
+    _q8_attend_check(g, 3, Hq, Hkv, D, 16, [700, 0, 333], N, blk=2, parent=par, softcap=20.0, bf16=False)
+    _q8_attend_check(g, 3, Hq, Hkv, D, 16, [700, 0, 333], N, blk=16, window=65, bf16=False)
+
+
+@pytest.mark.parametrize("N", [1, 2, 9])
+def test_attend_fp32_queries_beyond_the_codes_range(N):
+    # q of 2^121 and scales of 2^-117: a product with a code alone would not fit
+    g = synth.rng(4160 + N)
+    kc, ks, vc, vs, table = _pages8(g, 1, 2, 64, 16, 16, [50 + N], 50 + N, std=16.0)
+    q = synth.normal(g, (1, 4, N, 64), 128.0, False)
+    st = _status()
+    got = [tv.paged_attention(to_dev(q * np.float32(2.0 ** e), False), _codes(kc), _codes(vc), i32(table), i32([50]),
+                              k_scale=torch.from_numpy((ks - e).astype(np.uint8)).to(dev()),
+                              v_scale=torch.from_numpy(vs).to(dev()), dev_status=st) for e in (0, 114)]
+    assert torch.equal(got[0], got[1]) and torch.isfinite(got[0]).all() and int(st.item()) == 0
 
 
 @pytest.mark.parametrize("bf16", [True, False])

@@ -18,9 +18,10 @@ constexpr int kQaHeads = 2;      // heads whose loads are in flight together, an
 // results do not depend on timing.
 //
 // Threads: `lanes` neighbours a row, each 8 elements and their 8 pair partners (rot_to_pairs), kI rows a
-// thread.  Grid: x over (sequence, tile), y over groups of hg heads of q, k and v in turn.  64 tokens of 32 + 2 x 8
-// heads of 128 bf16, normed: 5.7 us, a chain of some five reads, one behind the other.  4 x 2048 of them, 180 MB: 49.9
-// us, 3.6 TB/s; without loads ahead of the work 59, with a branch a head 65.
+// thread.  Grid: x over (sequence, tile), y over groups of hg heads of k, v and q in turn: those that wait for a
+// maximum first.  64 tokens of 32 + 2 x 8 heads of 128 bf16, normed: 5.5 us, a chain of some five reads, one behind
+// the other.  4 x 2048 of them, 180 MB: 48.3 us, 3.7 TB/s, bound by 16 warps an SM at 122 registers; queries first
+// 49.9, k and v in groups of two heads 58 (more sines), without loads ahead of the work 59, with a branch a head 65.
 template <typename T>
 __device__ __forceinline__ void qa_load(const T* src, int ea, int eb, uint4 (&r)[sizeof(T)]) {
   constexpr int kHalf = sizeof(T) / 2;  // 16-byte loads of eight elements
@@ -116,10 +117,10 @@ __global__ void __launch_bounds__(kQaThreads) q8_append_kernel(RotaryArgs a, Q8P
   constexpr int kH = kWide && kI == 1 ? kQaHeads : 1;
   __shared__ int s_amax[2][kH][kQaMaxRows];
   const int b = blockIdx.x / tiles, tile = blockIdx.x % tiles;
-  const int qg = (a.Hq + hg - 1) / hg, kg = (a.Hkv + hg - 1) / hg;
-  const int part = (int)blockIdx.y < qg ? 0 : (int)blockIdx.y < qg + kg ? 1 : 2;
-  const int h0 = ((int)blockIdx.y - (part == 0 ? 0 : part == 1 ? qg : qg + kg)) * hg;
-  const int h1 = min(part ? a.Hkv : a.Hq, h0 + hg);
+  const int kg = (a.Hkv + hg - 1) / hg;
+  const int part = (int)blockIdx.y < kg ? 1 : (int)blockIdx.y < 2 * kg ? 2 : 0;
+  const int h0 = part ? ((int)blockIdx.y - (part - 1) * kg) * hg : ((int)blockIdx.y - 2 * kg) * hg;
+  const int h1 = part ? min(a.Hkv, h0 + hg) : min(a.Hq, h0 + hg);
   for (int k = threadIdx.x; k < 2 * kH * kQaMaxRows; k += blockDim.x) s_amax[0][0][k] = -1;
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();

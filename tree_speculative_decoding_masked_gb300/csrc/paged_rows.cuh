@@ -91,9 +91,10 @@ struct PrCfg {
 };
 
 // kQ8: K and V are e4m3 codes with block scales (q8.cuh).  A lane holds kDPL words of four, and turns them into
-// numbers where they are used; K's scale multiplies the score and V's the weight.  32 sequences of 4000 to 8000
-// tokens, 8 KV heads of 128, one row each: 135 us (2.6 TB/s; 64 rows a tile, as for many rows, 992), bound by
-// turning and multiplying the codes in 32 bits: two rows 176, four 311.  Half the tiles in flight 150, 183 and 430.
+// numbers where they are used; V's scale multiplies the weight.  32 sequences of 4000 to 8000
+// tokens, 8 KV heads of 128, one row each: 142 us (2.5 TB/s; 64 rows a tile, as for many rows, 992), two rows 175,
+// four 306: eight warps an SM at up to 255 registers wait for what they turn and multiply.  Half the tiles in flight
+// 150, 183 and 430.
 template <int kDPL, int kR, bool kQ8>
 __global__ void __launch_bounds__(kPsWarps * 32, 1) paged_rows_kernel(PagedAttn a) {
   using S = PrCfg<kDPL, kR>;
@@ -240,18 +241,24 @@ __global__ void __launch_bounds__(kPsWarps * 32, 1) paged_rows_kernel(PagedAttn 
       if constexpr (kQ8) {
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-          float4 part[kR];
+          // numbers, not codes: a large query's products with codes might not fit before the scale
+          const float2 scale = make_float2(q8_scale(ks[u]), q8_scale(ks[u]));
+          float2 part[kR][2];
 #pragma unroll
-          for (int r = 0; r < kR; ++r) part[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int r = 0; r < kR; ++r) part[r][0] = part[r][1] = make_float2(0.f, 0.f);
 #pragma unroll
           for (int c = 0; c < kDPL; ++c) {
             const float4 k = q8_quad(kf[u][c]);
+            const float2 k0 = __fmul2_rn(make_float2(k.x, k.y), scale), k1 = __fmul2_rn(make_float2(k.z, k.w), scale);
 #pragma unroll
-            for (int r = 0; r < kR; ++r) score(part[r], *reinterpret_cast<const float4*>(s_q + r * kD + place(c) * 4), k);
+            for (int r = 0; r < kR; ++r) {
+              const float4 qf = *reinterpret_cast<const float4*>(s_q + r * kD + place(c) * 4);
+              part[r][0] = __ffma2_rn(make_float2(qf.x, qf.y), k0, part[r][0]);
+              part[r][1] = __ffma2_rn(make_float2(qf.z, qf.w), k1, part[r][1]);
+            }
           }
-          const float scale = q8_scale(ks[u]);
 #pragma unroll
-          for (int r = 0; r < kR; ++r) z[u][r] = ((part[r].x + part[r].y) + (part[r].z + part[r].w)) * scale;
+          for (int r = 0; r < kR; ++r) z[u][r] = (part[r][0].x + part[r][0].y) + (part[r][1].x + part[r][1].y);
         }
       } else {
 #pragma unroll
@@ -323,10 +330,10 @@ __global__ void __launch_bounds__(kPsWarps * 32, 1) paged_rows_kernel(PagedAttn 
             const float4 v = q8_quad(vf[u][c]);
 #pragma unroll
             for (int r = 0; r < kR; ++r) {
-              acc[r][c].x = fmaf(p[r], v.x, acc[r][c].x);
-              acc[r][c].y = fmaf(p[r], v.y, acc[r][c].y);
-              acc[r][c].z = fmaf(p[r], v.z, acc[r][c].z);
-              acc[r][c].w = fmaf(p[r], v.w, acc[r][c].w);
+              const float2 w = make_float2(p[r], p[r]);
+              const float2 a0 = __ffma2_rn(w, make_float2(v.x, v.y), make_float2(acc[r][c].x, acc[r][c].y));
+              const float2 a1 = __ffma2_rn(w, make_float2(v.z, v.w), make_float2(acc[r][c].z, acc[r][c].w));
+              acc[r][c] = make_float4(a0.x, a0.y, a1.x, a1.y);
             }
           }
         }
