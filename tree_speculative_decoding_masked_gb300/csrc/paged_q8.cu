@@ -19,9 +19,10 @@ constexpr int kQaHeads = 2;      // heads whose loads are in flight together, an
 //
 // Threads: `lanes` neighbours a row, each 8 elements and their 8 pair partners (rot_to_pairs), kI rows a
 // thread.  Grid: x over (sequence, tile), y over groups of hg heads of k, v and q in turn: those that wait for a
-// maximum first.  64 tokens of 32 + 2 x 8 heads of 128 bf16, normed: 5.5 us, a chain of some five reads, one behind
-// the other.  4 x 2048 of them, 180 MB: 48.3 us, 3.7 TB/s, bound by 16 warps an SM at 122 registers; queries first
-// 49.9, k and v in groups of two heads 58 (more sines), without loads ahead of the work 59, with a branch a head 65.
+// maximum first.  64 tokens of 32 + 2 x 8 heads of 128 bf16, normed: 5.6 us, a chain of some five reads, one behind
+// the other.  4 x 2048 of them, 180 MB: 44.6 us, 4.0 TB/s, bound by 16 warps an SM at 128 registers, each with some
+// 250 instructions a row and head; with every number tested for being finite 48.3, queries first 49.9, without loads
+// ahead of the work 59, with a branch a head 65.
 template <typename T>
 __device__ __forceinline__ void qa_load(const T* src, int ea, int eb, uint4 (&r)[sizeof(T)]) {
   constexpr int kHalf = sizeof(T) / 2;  // 16-byte loads of eight elements
@@ -114,7 +115,7 @@ __device__ __forceinline__ void qa_single(const RotaryArgs& a, int part, const T
 template <typename T, int kI, bool kWide, bool kInter>
 __global__ void __launch_bounds__(kQaThreads) q8_append_kernel(RotaryArgs a, Q8Pages p, int tiles, int tile_rows,
                                                                int lanes, int hg) {
-  constexpr int kH = kWide && kI == 1 ? kQaHeads : 1;
+  constexpr int kH = kWide && kI == 1 && sizeof(T) == 2 ? kQaHeads : 1;  // as registers allow
   __shared__ int s_amax[2][kH][kQaMaxRows];
   const int b = blockIdx.x / tiles, tile = blockIdx.x % tiles;
   const int kg = (a.Hkv + hg - 1) / hg;
@@ -290,16 +291,27 @@ __global__ void __launch_bounds__(kQaThreads) q8_append_kernel(RotaryArgs a, Q8P
     });
     // ---- the blocks' maxima, over what is finite
     float m[kMany][kI];
+    bool odd[kMany][kI];  // something is not finite
 #pragma unroll
     for (int u = 0; u < kMany; ++u)
 #pragma unroll
       for (int i = 0; i < kI; ++i) {
+        float2 zero = make_float2(0.f, 0.f);  // what is finite adds 0
         m[u][i] = 0.f;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const float f = fabsf(x[u][i][k]), g = fabsf(y[u][i][k]);
-          m[u][i] = fmaxf(m[u][i], f <= 3.4028234e38f ? f : 0.f);
-          m[u][i] = fmaxf(m[u][i], g <= 3.4028234e38f ? g : 0.f);
+          zero = __ffma2_rn(make_float2(x[u][i][k], y[u][i][k]), make_float2(0.f, 0.f), zero);
+          m[u][i] = fmaxf(m[u][i], fmaxf(fabsf(x[u][i][k]), fabsf(y[u][i][k])));
+        }
+        odd[u][i] = !(zero.x + zero.y == 0.f);
+        if (odd[u][i]) {
+          m[u][i] = 0.f;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float f = fabsf(x[u][i][k]), g = fabsf(y[u][i][k]);
+            m[u][i] = fmaxf(m[u][i], f <= 3.4028234e38f ? f : 0.f);
+            m[u][i] = fmaxf(m[u][i], g <= 3.4028234e38f ? g : 0.f);
+          }
         }
         if (!in_row) m[u][i] = 0.f;
       }
@@ -334,11 +346,21 @@ __global__ void __launch_bounds__(kQaThreads) q8_append_kernel(RotaryArgs a, Q8P
         const size_t row = (size_t)page_row[i] + ((size_t)(h + u) << a.page_shift);
         if (in_row) {
           unsigned char* dst = cache + row * a.D;
-          const float(&v)[8] = x[u][i], (&w)[8] = y[u][i];
-          *reinterpret_cast<uint2*>(dst + ea) = make_uint2(q8_code4(v[0] * f, v[1] * f, v[2] * f, v[3] * f),
-                                                           q8_code4(v[4] * f, v[5] * f, v[6] * f, v[7] * f));
-          *reinterpret_cast<uint2*>(dst + eb) = make_uint2(q8_code4(w[0] * f, w[1] * f, w[2] * f, w[3] * f),
-                                                           q8_code4(w[4] * f, w[5] * f, w[6] * f, w[7] * f));
+          float(&v)[8] = x[u][i], (&w)[8] = y[u][i];
+          if (odd[u][i]) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = q8_finite(v[k]), w[k] = q8_finite(w[k]);
+          }
+          const float2 ff = make_float2(f, f);
+          uint32_t code[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float* z = k < 2 ? v + 4 * k : w + 4 * (k - 2);
+            const float2 lo = __fmul2_rn(make_float2(z[0], z[1]), ff), hi = __fmul2_rn(make_float2(z[2], z[3]), ff);
+            code[k] = q8_cvt2(lo.x, lo.y) | q8_cvt2(hi.x, hi.y) << 16;
+          }
+          *reinterpret_cast<uint2*>(dst + ea) = make_uint2(code[0], code[1]);
+          *reinterpret_cast<uint2*>(dst + eb) = make_uint2(code[2], code[3]);
         }
         // every live row of a block writes the same byte
         if (col == 0) scales[row >> bs] = (uint8_t)(e + 127);
@@ -383,11 +405,12 @@ static cudaError_t launch_qa(const RotaryArgs& a, const Q8Pages& p, int tile_row
   const int blk = 1 << p.block_shift;
   const long long tiles = ((long long)a.N + blk - 1 + tile_rows - 1) / tile_rows;
   if (tiles * a.B > 0x7fffffffLL) return cudaErrorInvalidValue;
-  // heads share a CTA, its sines and its page lookups once the grid has a few CTAs an SM without that
+  // heads share a CTA, its sines and its page lookups until the grid's warps are the 16 an SM that run at once.  As
+  // many again: 4 x 2048 rows the same, one of 2048 16.6 us for 13.9, 64 single rows 6.5 for 5.5, 16 x 64 10.3 for 13.3.
   const int most = max(a.Hq, a.Hkv);
   int hg = 1;
   auto groups = [&](int g) { return (long long)(a.Hq + g - 1) / g + 2ll * ((a.Hkv + g - 1) / g); };
-  while (hg < most && tiles * a.B * groups(hg) > 152 * 16) hg *= 2;
+  while (hg < most && tiles * a.B * groups(hg) * (threads / 32) > 152 * 16) hg *= 2;
   const dim3 grid((unsigned)(tiles * a.B), (unsigned)groups(hg));
   return launch_pdl(q8_append_kernel<T, kI, kWide, kInter>, grid, dim3(threads), 0, stream, nullptr, 0, a, p,
                     (int)tiles, tile_rows, lanes, hg);

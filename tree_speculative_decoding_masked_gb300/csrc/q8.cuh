@@ -31,15 +31,15 @@ __device__ __forceinline__ int q8_exponent(float amax) {
   return max(e, kQ8Least);
 }
 
-// two numbers to e4m3 (nearest, ties to even), `lo` in the low byte; what is not finite becomes NaN
-__device__ __forceinline__ uint32_t q8_code2(float lo, float hi) {
-  const float big = 3.4028234e38f;
-  lo = fabsf(lo) <= big ? lo : __uint_as_float(0x7fffffffu);
-  hi = fabsf(hi) <= big ? hi : __uint_as_float(0x7fffffffu);
+// two finite numbers or NaNs to e4m3 (nearest, ties to even), `lo` in the low byte
+__device__ __forceinline__ uint32_t q8_cvt2(float lo, float hi) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// a number, or NaN for what is not finite
+__device__ __forceinline__ float q8_finite(float x) { return fabsf(x) <= 3.4028234e38f ? x : __uint_as_float(0x7fffffffu); }
+__device__ __forceinline__ uint32_t q8_code2(float lo, float hi) { return q8_cvt2(q8_finite(lo), q8_finite(hi)); }
 // two codes to f16x2, exact
 __device__ __forceinline__ uint32_t q8_half2(uint16_t codes) {
   uint32_t r;
@@ -78,7 +78,7 @@ __device__ __forceinline__ void q8_half4(uint32_t w, uint32_t& lo, uint32_t& hi)
 // four codes under the scale 2^from, coded for 2^to >= 2^from
 __device__ __forceinline__ uint32_t q8_recode(uint32_t w, float ratio) {
   const float4 f = q8_numbers(w, ratio);
-  return q8_code4(f.x, f.y, f.z, f.w);
+  return q8_cvt2(f.x, f.y) | q8_cvt2(f.z, f.w) << 16;
 }
 
 }  // namespace tv
