@@ -447,7 +447,8 @@ cudaError_t launch_q8_append(const RotaryArgs& a, const Q8Pages& p, tv_dtype dty
 // ---- read back: rows first_b + r < length_b of the cache to row r of contiguous [B][Hkv][rows][D]
 //
 // One pass over memory, 8 codes a thread and row: a row's codes are read in order and its numbers written
-// in order.  Exact in bf16: a code has four significant bits.
+// in order.  Exact in bf16: a code has four significant bits.  8 sequences of 8192 to 16384 rows, 8 heads of 128, 500
+// MB: 89 us, 5.6 TB/s, memory; one of 2048: 4.3 us.
 constexpr int kQrThreads = 256;
 constexpr int kQrRows = 4;  // rows a thread has in flight
 
@@ -519,7 +520,8 @@ cudaError_t launch_q8_read(const Q8Read& a, tv_dtype dtype, cudaStream_t stream)
 // rows that change their scale, the live ones before the path in the first block among them, are coded
 // anew.  One CTA a (sequence, KV head, K or V), tile after tile of 64 destination rows in whole blocks: a
 // tile's sources, and their scales, are all read before anything of it is written, and since a_k >= k
-// and the a_k increase, no later tile reads a row or a scale that an earlier one wrote.
+// and the a_k increase, no later tile reads a row or a scale that an earlier one wrote.  64 paths of 8 to 16 rows, 8
+// heads of 128: 5.7 us, one of 5 2.8: dependent reads (lengths, path, pages, rows and scales) and four barriers.
 constexpr int kQcThreads = 256;
 constexpr int kQcRows = 64;
 

@@ -49,8 +49,12 @@
 // the row's largest term; the sum takes 2^-e times a block's P.  Warps then: 0 producer, 1 S issuer A,
 // 2 PV issuer, 3 S issuer B, 4-11 softmax, 12-15 converters, with registers moved from the others to the
 // softmax's (168 and 88 a thread).  V in bf16 with its scales, four times the conversion's instructions, and a
-// factor a key or 16 keys by a branch in one kernel: eight 128-node trees 612 us.  Blocks of less than 16
-// rows have an instance of their own.
+// factor a key or 16 keys by a branch in one kernel: eight 128-node trees over 32768 tokens 612 us.  Blocks of less
+// than 16 rows have an instance of their own.  These trees take 341 us now (bf16 pages 298), two chunks of 2048 rows over
+// 3000 to 6000 417 (302), a 64-node tree over 2048 16.6 (12.7), the trees with one key a block 661 in the second
+// instance.  A step, 0.66 us, is bound by what the softmax warps and the converters issue, 0.54 of all slots,
+// and by instruction fetches: waits in few lines, loops that are not unrolled and one barrier for a tile's K and V
+// took the missed lines of a step from 77 to 26 (bf16: 18) and the trees from 386 us.
 #pragma once
 
 #include <atomic>
