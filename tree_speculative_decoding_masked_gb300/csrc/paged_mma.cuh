@@ -33,9 +33,9 @@
 // in one load.  Eight lanes take four such chunks of two keys, which the swizzle of 128-byte rows lays on
 // different banks if the keys are four apart: so product row g is key g / 2 + 4 (g % 2) of its eight.  V's
 // come by transposing loads of 16-bit pairs (two columns of a key), whose bytes are dealt to two product
-// rows.  64 tokens over 8192 to 16384: 285 us, 5.6 TB/s; without the products the copies alone take 252, in boxes of
+// rows.  64 tokens over 8192 to 16384: 275 us, 5.8 TB/s; without the products the copies alone take 252, in boxes of
 // 64-byte rows 260.  With K in fp16 too, 64 keys a tile, 16 a warp, and scales looked up for each key of a tile: 1900
-// instructions for 64 keys and 390 us.  One token over 2048: 8.5 us; with a key a block 64 take 362.
+// instructions for 64 keys and 390 us.  One token over 2048: 8.5 us; with a key a block 64 take 354.
 #pragma once
 
 #include "paged.cuh"
@@ -176,6 +176,11 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
     paged_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, PagedAttn a,
                      int splits, int row_tiles, int wide) {
   using C = PmCfg<kD, kRT, kQ8>;
+  // kQ8: registers move from the producers to the consumers, 72 and 216 a thread of the launch's 168 (the launch bound's,
+  // which ptxas takes for every kernel that moves any: 12 warps of 168 are 4 of 72 and 8 of 216).  Two
+  // row tiles spilled without (16 rows over 8192 to 16384, 64 sequences: 580 us, now 466; 8 rows 285, now 275);
+  // one token of one sequence takes 8.5 us, and 8.9 with it.
+  constexpr bool kShift = kQ8 && C::kWarps == 8 && (kStream || C::kNT > 1);
   ptx::griddep_launch_dependents();
   extern __shared__ unsigned char pm_raw[];
   unsigned char* sm = pm_raw + ((1024u - (ptx::smem_addr(pm_raw) & 1023u)) & 1023u);
@@ -216,6 +221,7 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
 
   if (warp >= C::kWarps) {
     // ------------------------------------------------------------------ producers
+    if constexpr (kShift) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     // the boxes of a tile - (row piece, column block without 5-D boxes, K or V) - dealt to the
     // producer warps in turn; lane i of a warp looks up the page of its i-th box, read a tile
     // ahead and checked when it is used
@@ -286,8 +292,10 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
         ptx::mbar_wait(&bars->full[s], ((issued - 1 - s) / C::kStages) & 1, &quiet);
     }
     __syncwarp();
+    if constexpr (kShift) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
   } else {
     // ------------------------------------------------------------------ consumers
+    if constexpr (kShift) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     auto cons_sync = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(C::kConsumers) : "memory"); };
     const int wk = warp & 3, group = warp >> 2;  // key quarter of a tile, and which of two tiles in turn
     const int ct = threadIdx.x;
@@ -921,6 +929,8 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
         }
       }
     }
+    __syncwarp();
+    if constexpr (kShift) asm volatile("setmaxnreg.dec.sync.aligned.u32 168;");
   }
   if constexpr (!kStream) {
     __syncwarp();
