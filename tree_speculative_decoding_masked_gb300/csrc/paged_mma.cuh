@@ -177,10 +177,11 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
                      int splits, int row_tiles, int wide) {
   using C = PmCfg<kD, kRT, kQ8>;
   // kQ8: registers move from the producers to the consumers, 72 and 216 a thread of the launch's 168 (the launch bound's,
-  // which ptxas takes for every kernel that moves any: 12 warps of 168 are 4 of 72 and 8 of 216).  Two
-  // row tiles spilled without (16 rows over 8192 to 16384, 64 sequences: 580 us, now 466; 8 rows 285, now 275);
-  // one token of one sequence takes 8.5 us, and 8.9 with it.
-  constexpr bool kShift = kQ8 && C::kWarps == 8 && (kStream || C::kNT > 1);
+  // which ptxas takes for every kernel that moves any: 12 warps of 168 are 4 of 72 and 8 of 216).  They move once: a
+  // second move would need each warpgroup's warps to meet before it, and producers never meet, so clusters, whose warps
+  // share code at the end, move none.  Two row tiles spilled without (16 rows over 8192 to 16384, 64 sequences: 580
+  // us, now 466; 8 rows 285, now 274).
+  constexpr bool kShift = kQ8 && C::kWarps == 8 && kStream;
   ptx::griddep_launch_dependents();
   extern __shared__ unsigned char pm_raw[];
   unsigned char* sm = pm_raw + ((1024u - (ptx::smem_addr(pm_raw) & 1023u)) & 1023u);
@@ -292,7 +293,6 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
         ptx::mbar_wait(&bars->full[s], ((issued - 1 - s) / C::kStages) & 1, &quiet);
     }
     __syncwarp();
-    if constexpr (kShift) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
   } else {
     // ------------------------------------------------------------------ consumers
     if constexpr (kShift) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
@@ -929,8 +929,6 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
         }
       }
     }
-    __syncwarp();
-    if constexpr (kShift) asm volatile("setmaxnreg.dec.sync.aligned.u32 168;");
   }
   if constexpr (!kStream) {
     __syncwarp();
