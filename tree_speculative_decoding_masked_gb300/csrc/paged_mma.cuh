@@ -27,15 +27,15 @@
 // become fp16 numbers, which hold them exactly, in registers on the way: one conversion for two codes, where bf16,
 // whose exponent is another, takes 4.5 instructions and more issue slots than the copies leave.  fp16's range is
 // not that of the numbers, so V's scales stay out of it: with e the exponent of the value's block, P = 2^(z + e - m)
-// and m is the running reference of z + e, so that a weight is rounded to 11 bits and lost only below 2^-32 of the
-// largest term of its row's sum; the sum takes 2^-e times P.  A key's scale multiplies its scores, in fp32.  K's
+// and m is the running reference of z + e; the sum takes 2^-e times P, or, once an e is far from 0 (a block of zeros:
+// q8_far), goes by z alone against a reference of its own, of each lane.  A key's scale multiplies its scores, in fp32.  K's
 // fragments need no transpose and any order of columns, if Q's have the same: a lane takes 16 columns of a key
 // in one load.  Eight lanes take four such chunks of two keys, which the swizzle of 128-byte rows lays on
 // different banks if the keys are four apart: so product row g is key g / 2 + 4 (g % 2) of its eight.  V's
 // come by transposing loads of 16-bit pairs (two columns of a key), whose bytes are dealt to two product
-// rows.  64 tokens over 8192 to 16384: 275 us, 5.8 TB/s; without the products the copies alone take 252, in boxes of
+// rows.  64 tokens over 8192 to 16384: 278 us, 5.7 TB/s (with values of zeros throughout 330); without the products the copies alone take 252, in boxes of
 // 64-byte rows 260.  With K in fp16 too, 64 keys a tile, 16 a warp, and scales looked up for each key of a tile: 1900
-// instructions for 64 keys and 390 us.  One token over 2048: 8.5 us; with a key a block 64 take 354.
+// instructions for 64 keys and 390 us.  One token over 2048: 8.9 us; with a key a block 64 take 359.
 #pragma once
 
 #include "paged.cuh"
@@ -52,6 +52,7 @@ constexpr int kPmMinTiles = 2;   // tiles of a CTA's range: fewer only add parts
 // (paged.cuh).  0 and 0 / 8 and 8: one token each of 64 sequences of 150 to 300 tokens 36.4 / 26.8 us,
 // of 500 to 1000 50.8 / 46.4, of 8192 to 16384 465 / 461.
 constexpr int kPmTol = 8, kPmFix = 8;  // in tiles of 64 keys
+constexpr float kPmShift = 7.f;        // kQ8: P is held times 2^7
 
 template <int kD, int kRT, bool kQ8>
 struct PmCfg {
@@ -86,7 +87,8 @@ struct PmCfg {
   static constexpr int kRegions = kD == 256 ? 1 : kD == 128 && kRT == 16 ? 2 : kWarps / 2;
   static constexpr int kOBytes = kRegions * kRT * kOStride * 4;
   static constexpr int kOffBar = kOffU + (kInBytes > kOBytes ? kInBytes : kOBytes);
-  static constexpr int kSmem = kOffBar + 256 + 1024;
+  static constexpr int kOffFar = kOffBar + 256;         // kQ8: sums of the threads' rows under far scales
+  static constexpr int kSmem = kOffFar + (kQ8 ? kConsumers * 2 * kNT * 8 : 0) + 1024;
   // a slot's tiles alternate between no two groups: a group that skipped a slot's earlier tile
   // could take that tile's unfinished phase for its own finished one
   static_assert(kWarps == 4 || kStages % 2 == 0, "each slot belongs to one group");
@@ -180,7 +182,7 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
   // which ptxas takes for every kernel that moves any: 12 warps of 168 are 4 of 72 and 8 of 216).  They move once: a
   // second move would need each warpgroup's warps to meet before it, and producers never meet, so clusters, whose warps
   // share code at the end, move none.  Two row tiles spilled without (16 rows over 8192 to 16384, 64 sequences: 580
-  // us, now 466; 8 rows 285, now 274).
+  // us, now 452; 8 rows 285, now 278).
   constexpr bool kShift = kQ8 && C::kWarps == 8 && kStream;
   ptx::griddep_launch_dependents();
   extern __shared__ unsigned char pm_raw[];
@@ -454,6 +456,10 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
       }
       float o[kD / 16][C::kNT][4];
       float m[C::kNT][2], l[C::kNT][2];
+      // kQ8: once a far scale has come, the sum of this lane and row is that of z alone, y times 2^x, in shared memory as few
+      // calls have one.  To go back behind it, as paged_tc.cuh does, costs calls without one 1 to 3 % more
+      bool far_on = false;
+      auto far_sum = [&](int row) -> float2* { return reinterpret_cast<float2*>(sm + C::kOffFar) + row * C::kConsumers + ct; };
 #pragma unroll
       for (int nt = 0; nt < C::kNT; ++nt) {
         m[nt][0] = m[nt][1] = -INFINITY;
@@ -574,7 +580,7 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
             }
             // scores; those of a row's running reference count with the value's scale
             float val_e[kSubs][2], val_f[kSubs][2];  // e and 2^-e of keys kk, kk + 8
-            bool grow = false;
+            bool grow = far_on;
 #pragma unroll
             for (int u = 0; u < kSubs; ++u) {
               float key_f[2];
@@ -585,6 +591,7 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
                 key_f[e] = __uint_as_float((uint32_t)(both & 255) << 23);
                 val_e[u][e] = (float)((both >> 8) - 127);
                 val_f[u][e] = __uint_as_float((uint32_t)max(1, 254 - (both >> 8)) << 23);
+                grow |= q8_far(val_e[u][e]);
               }
 #pragma unroll
               for (int nt = 0; nt < C::kNT; ++nt)
@@ -606,6 +613,35 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
                 }
             }
             if (__any_sync(0xffffffffu, grow)) {
+              bool far = false;
+#pragma unroll
+              for (int u = 0; u < kSubs; ++u) far |= q8_far(val_e[u][0]) || q8_far(val_e[u][1]);
+              if (__builtin_expect(__any_sync(0xffffffffu, far || far_on), 0)) {
+                // few lines, as they sit among those of every turn: a loop over the rows, whose registers are selected
+#pragma unroll 1
+                for (int r = 0; r < 2 * C::kNT; ++r) {
+                  float z[2 * kSubs], was_m = m[0][0] - kPmShift, was_l = l[0][0];
+#pragma unroll
+                  for (int k = 0; k < 2 * kSubs; ++k) z[k] = s[k >> 1][0][0][2 * (k & 1)];
+#pragma unroll
+                  for (int x = 1; x < 2 * C::kNT; ++x)
+                    if (r == x) {
+                      was_m = m[x >> 1][x & 1] - kPmShift, was_l = l[x >> 1][x & 1];
+#pragma unroll
+                      for (int k = 0; k < 2 * kSubs; ++k) z[k] = s[k >> 1][x >> 1][0][2 * (k & 1) + (x & 1)];
+                    }
+                  if (far_on) was_m = far_sum(r)->x, was_l = far_sum(r)->y;
+                  float top = was_m;
+#pragma unroll
+                  for (int k = 0; k < 2 * kSubs; ++k) top = fmaxf(top, z[k] -= val_e[k >> 1][k & 1]);
+                  const float base = top == -INFINITY ? 0.f : top;  // nothing seen yet: adds 0, or a NaN query's NaN
+                  float sum = was_l * (top == was_m ? 1.f : ptx::ex2(was_m - top));
+#pragma unroll
+                  for (int k = 0; k < 2 * kSubs; ++k) sum += ptx::ex2(z[k] - base);
+                  *far_sum(r) = make_float2(top, sum);
+                }
+                far_on = true;
+              }
 #pragma unroll
               for (int nt = 0; nt < C::kNT; ++nt)
 #pragma unroll
@@ -628,9 +664,9 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
             }
 #pragma unroll
             for (int nt = 0; nt < C::kNT; ++nt) {
-              // P times 2^7: at most 2^15
-              const float b0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0] - 7.f;
-              const float b1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1] - 7.f;
+              // at most 2^15
+              const float b0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0] - kPmShift;
+              const float b1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1] - kPmShift;
 #pragma unroll
               for (int u = 0; u < kSubs; ++u) {
                 const float e0 = ptx::ex2(s[u][nt][0][0] - b0), e1 = ptx::ex2(s[u][nt][0][1] - b1);
@@ -795,17 +831,38 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
             s_l[warp][nt * 8 + rg + e] = l[nt][e];
           }
         }
+      if (kQ8 && __builtin_expect(far_on, 0)) {  // the sums' own references instead, and below O's
+#pragma unroll 1
+        for (int r = 0; r < 2 * C::kNT; ++r) {
+          const float2 mine = *far_sum(r);
+          float ref = mine.x;
+#pragma unroll
+          for (int x = 4; x < 32; x *= 2) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, x));
+          float sum = mine.y * (mine.x == ref ? 1.f : ptx::ex2(mine.x - ref));
+#pragma unroll
+          for (int x = 4; x < 32; x *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+          ref += (float)q8_norm(sum) + kPmShift;
+          if (kg == 0) {
+            s_m[warp][(r >> 1) * 8 + rg + (r & 1)] = sum == 0.f ? -INFINITY : ref;
+            s_l[warp][(r >> 1) * 8 + rg + (r & 1)] = sum;
+          }
+        }
+      }
       cons_sync();  // and every warp is done with the queries and masks, which O now overwrites
 #pragma unroll
       for (int nt = 0; nt < C::kNT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float f = m[nt][e] == -INFINITY ? 0.f : ptx::ex2(m[nt][e] - row_max(nt * 8 + rg + e));
+          float up = m[nt][e] - row_max(nt * 8 + rg + e);
+          if (kQ8 && far_on) up *= 0.5f;  // half the exponent at a time: the whole may leave fp32's range
+          const float f = m[nt][e] == -INFINITY ? 0.f : ptx::ex2(up);
+#pragma unroll 1
+          for (int twice = kQ8 && far_on; twice >= 0; --twice)
 #pragma unroll
-          for (int k = 0; k < kD / 16; ++k) {
-            o[k][nt][e] *= f;
-            o[k][nt][e + 2] *= f;
-          }
+            for (int k = 0; k < kD / 16; ++k) {
+              o[k][nt][e] *= f;
+              o[k][nt][e + 2] *= f;
+            }
         }
       // this lane's O of the unit's rows to or from a region: columns kg and kg + 8 of a step, or (kQ8) 2 kg and
       // 2 kg + 1

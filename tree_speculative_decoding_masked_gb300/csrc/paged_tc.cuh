@@ -45,14 +45,14 @@
 // numbers, which hold them exactly (a conversion for two codes), in a second ring, which four converter
 // warps fill; they also zero the rows that no row needs, and bring Q and the scales.  fp16's range is not
 // that of the numbers, so V's scales stay out of it: with e the exponent of the value block, P = 2^(z + e - m) and m
-// is the running reference of z + e, so that P is at most 2^8 (held times 2^7) and is lost only below 2^-32 of
-// the row's largest term; the sum takes 2^-e times a block's P.  Warps then: 0 producer, 1 S issuer A,
+// is the running reference of z + e, so that P is at most 2^8 (held times 2^7); the sum takes 2^-e times a block's
+// P, or, once an e is far from 0 (a block of zeros: q8_far), goes by z alone.  Warps then: 0 producer, 1 S issuer A,
 // 2 PV issuer, 3 S issuer B, 4-11 softmax, 12-15 converters, with registers moved from the others to the
 // softmax's (168 and 88 a thread).  V in bf16 with its scales, four times the conversion's instructions, and a
 // factor a key or 16 keys by a branch in one kernel: eight 128-node trees over 32768 tokens 612 us.  Blocks of less
-// than 16 rows have an instance of their own.  These trees take 341 us now (bf16 pages 298), two chunks of 2048 rows over
-// 3000 to 6000 417 (302), a 64-node tree over 2048 16.6 (12.7), the trees with one key a block 661 in the second
-// instance.  A step, 0.66 us, is bound by what the softmax warps and the converters issue, 0.54 of all slots,
+// than 16 rows have an instance of their own.  These trees take 342 us now (bf16 pages 298), two chunks of 2048 rows over
+// 3000 to 6000 413 (302), a 64-node tree over 2048 16.9 (12.7), the trees with one key a block 540 in the second
+// instance; with values of zeros throughout 705 and 1260.  A step, 0.66 us, is bound by what the softmax warps and the converters issue, 0.54 of all slots,
 // and by instruction fetches: waits in few lines, loops that are not unrolled and one barrier for a tile's K and V
 // took the missed lines of a step from 77 to 26 (bf16: 18) and the trees from 386 us.
 #pragma once
@@ -70,6 +70,7 @@ constexpr int kPtKeys = 64;
 constexpr int kPtSlots = 4;      // K ring and V ring depth
 constexpr int kPtVbSlots = 3;    // kQ8: ring of converted V tiles
 constexpr int kPtAhead = 4;      // kQ8: tiles that scales are looked up ahead
+constexpr int kPtRound = 68;     // kQ8: floats of a round's scales
 constexpr int kPtPieces = 4;     // pieces known ahead
 constexpr int kPtMaxSplits = 8;  // portable cluster size
 // A unit's set-up and end count as 8 steps, and cuts less than 12 from a unit's edge move to it
@@ -103,9 +104,10 @@ struct PtCfg {
   static constexpr int kOffVb = kOffV + kPtSlots * kVTile;
   static constexpr int kOffPar = kOffVb + (kQ8 ? kPtVbSlots * kTileBytes : 0);
   // kQ8: scales, and those of a piece's rows.  Blocks of 16 rows or more: four rounds of 8 tiles, of each four of
-  // K's and four of V's exponents e; shorter ones: a tile in each ring slot, {K's, e, 2^-e} of every key
+  // K's and four of V's exponents e, and whether one of those is far (q8_far); shorter ones: a tile in each ring slot,
+  // {K's, e, 2^-e} of every key, no number for the last where e is far
   static constexpr int kOffScale = kOffPar + kMaxNodes * 4;
-  static constexpr int kScaleBytes = !kQ8 ? 0 : kQ == kPtQ8Fine ? kPtSlots * kPtKeys * 12 : 4 * 8 * 32;
+  static constexpr int kScaleBytes = !kQ8 ? 0 : kQ == kPtQ8Fine ? kPtSlots * kPtKeys * 12 : 4 * kPtRound * 4;
   static constexpr int kOffBar = kOffScale + kScaleBytes + (kQ8 ? 2 * kPtRows * 4 : 0);
   static constexpr int kSmemAlloc = kOffBar + 640 + 1024;  // slack for 1024-byte alignment
   static constexpr uint32_t kColO = 256;
@@ -341,6 +343,13 @@ __device__ __forceinline__ float pt_max64_fine(const float (&sv)[64], float c, c
     if (j % 16 == 12) asm volatile("" ::: "memory");
   }
   return m;
+}
+
+// y 2^x += l 2^ref, l >= 0 or NaN
+__device__ __forceinline__ void pt_add(float& y, float& x, float l, float ref) {
+  const float top = fmaxf(x, ref), base = top == -INFINITY ? 0.f : top;
+  y = y * ptx::ex2(x - base) + l * ptx::ex2(ref - base);
+  x = top;
 }
 
 // Wait for this piece's own copies or products even when another wait has run out.
@@ -611,6 +620,10 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
 
     float m_run = -INFINITY, l_run = 0.f;
     bool have_o = false;
+    // kQ8: the weights of tiles with a far scale (q8_far; now), from one with a large scale on of all (high), add up to
+    // l_far times 2^z_ref
+    float l_far = 0.f, z_ref = -INFINITY;
+    bool now = false, high = false;
     if (kWho != kSoftmax && warp == 0) {
       // ---------------------------------------------------------------- producer
       // lane: row piece pi of a tile (and, without 5-D boxes, its column block db)
@@ -930,7 +943,7 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
             float* to = s_scale + vs * 3 * kPtKeys + cw * 16 + lane;
             to[0] = q8_scale(ks);
             to[kPtKeys] = (float)(bytes - 127);
-            to[2 * kPtKeys] = q8_two(127 - bytes);
+            to[2 * kPtKeys] = q8_far(bytes - 127) ? __uint_as_float(0x7fffffffu) : q8_two(127 - bytes);
           }
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&bars->scale_full[vs]);
@@ -940,9 +953,12 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
 #pragma unroll 1
           for (int r = t == 0 ? 0 : t + 4; r < nt && r <= t + 4; r += 8) {
             const int bytes = next_bytes(r);
-            float* to = s_scale + ((rounds + r / 8) & 3) * 64 + (lane >> 2) * 8 + (lane & 3);
+            float* of = s_scale + ((rounds + r / 8) & 3) * kPtRound;
+            float* to = of + (lane >> 2) * 8 + (lane & 3);
             to[0] = q8_scale(bytes & 255);
             to[4] = (float)((bytes >> 8) - 127);
+            const bool far = __any_sync(0xffffffffu, q8_far((bytes >> 8) - 127));
+            if (lane == 0) of[64] = far ? 1.f : 0.f;
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&bars->scale_full[(rounds + r / 8) & 3]);
           }
@@ -1025,7 +1041,7 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
         // kQ8: the tile's scales, read before its scores are there: with the products' operands on the way, shared
         // memory takes long to answer
         const float* scales =
-            s_scale + (kFine ? (kt + t) % kPtSlots * 3 * kPtKeys : ((rounds + t / 8) & 3) * 64 + t % 8 * 8);
+            s_scale + (kFine ? (kt + t) % kPtSlots * 3 * kPtKeys : ((rounds + t / 8) & 3) * kPtRound + t % 8 * 8);
         float gf[4], ge[4];
         if constexpr (kQ8) {
           if (kFine || t % 8 == 0) {
@@ -1033,6 +1049,7 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
             ok = __all_sync(0xffffffffu, pt_wait_for<kQ8>(&bars->scale_full[kFine ? (kt + t) % kPtSlots : (rounds + t / 8) & 3],
                                                         n & 1, abort_flag));
             if (!ok) break;
+            if (!kFine) now = scales[64] != 0.f;
           }
           if constexpr (!kFine) {
             const float4 ks = *reinterpret_cast<const float4*>(scales), vs = *reinterpret_cast<const float4*>(scales + 4);
@@ -1119,13 +1136,51 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
           if constexpr (kFine) return pt_max64_fine(sv, c, scales);
           return pt_max64_q8(sv, gf, ge);
         };
+        // The tile's weights by z alone, as P may not hold them.  Scores are read again, eight at a time: these lines sit
+        // among those of every tile, and 32 at a time cost tiles without a far scale 3 to 14 %
+        auto sum_far = [&](bool mine, float m_before) {
+          float large = 0.f;
+#pragma unroll 1
+          for (int c0 = 0; c0 < kPtKeys; c0 += 8) {
+            float z[8], top = z_ref;
+            ptx::tmem_ld8(colS + buf * kPtKeys + c0, z);
+            ptx::tmem_wait_ld();
+            const unsigned seen = (unsigned)(vis >> c0);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              z[j] *= scales[kFine ? c0 + j : c0 / 16] * row_f;
+              if constexpr (kCap == kTanhCap) z[j] = soft_tanh(z[j] * ck);
+              if constexpr (kCap == kLargeCap) z[j] = capped_score(z[j] * a.scale, a.cap, ck);
+              z[j] = seen >> j & 1u ? z[j] * c : -INFINITY;
+              top = fmaxf(top, z[j]);
+              large = fmaxf(large, scales[kFine ? kPtKeys + c0 + j : 4 + c0 / 16]);
+            }
+            if (!mine) continue;
+            const float base = top == -INFINITY ? 0.f : top;  // nothing seen yet: adds 0, or a NaN query's NaN
+            l_far *= ptx::ex2(z_ref - base);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) l_far += ptx::ex2(z[j] - base);
+            z_ref = top;
+          }
+          if (mine && !high && q8_far(large)) {  // m may leave z behind from here on
+            high = true;
+            pt_add(l_far, z_ref, l_run, m_before - kPtShift);
+            l_run = 0.f;
+          }
+        };
         float alpha = 1.f, lsum;
         bool need = false;
         uint32_t pw[32];
         if constexpr (kQ8) {
-          bool checked = false, look = m_run == -INFINITY;
+          bool checked = false, look = m_run == -INFINITY, sum = high;  // sum: kFine, still to be taken
+          const float m_before = m_run;
+          if (kFine) now = high;
           for (;;) {
-            if constexpr (kFine) read_scores();  // each time: scores, scales and P together do not fit the registers
+            if constexpr (kFine) {
+              if (__builtin_expect(__any_sync(0xffffffffu, sum), 0)) sum_far(sum, m_before);
+              sum = false;
+              read_scores();  // each time: scores, scales and P together do not fit the registers
+            }
             if (__builtin_expect(look, 0)) {
               const float tms = tile_max();
               checked = true;
@@ -1144,12 +1199,17 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
               psum = pt_exp64_q8(sv, gf, ge, m_run, pw, lsum);
             const bool again = !checked && psum >= 128.f * kPtRescaleSum;
             if constexpr (kFine) {
-              if (!__any_sync(0xffffffffu, again)) break;  // the warp's rows together; the others' P comes out as it was
+              const bool far = isnan(lsum) && !now;  // or the query is NaN: so is the row either way
+              // the warp's rows together; the others' P comes out as it was
+              if (!__any_sync(0xffffffffu, again || far)) break;
+              if (far) now = sum = true;
             } else if (!again) {
               break;
             }
             look = look || again;
           }
+          if (!kFine && __builtin_expect(now || high, 0)) sum_far(true, m_before);
+          if (now || high) lsum = 0.f;
         } else {
           bool checked = false;
           if (m_run == -INFINITY) {
@@ -1191,12 +1251,35 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
         if (lane == 0) ptx::mbar_arrive(&bars->p_full[x][buf]);
       }
       // ---- epilogue: every MMA is complete at o_done
-      if (isnan(l_run)) m_run = l_run;  // a NaN query's part: no part without a visible key, which merges leave out
       if (nt > 0) {
         ok = ok && __all_sync(0xffffffffu, pt_wait_for<kQ8>(&bars->o_done, pieces & 1, abort_flag));
         have_o = ok && ntm > 0;
         if (ok) ptx::tc_fence_after();
       }
+      const bool far = l_far != 0.f;
+      if (kQ8 && __builtin_expect(__any_sync(0xffffffffu, far), 0)) {
+        // m_run becomes the sum's reference and O's with it, half the exponent at a time, as the whole may leave
+        // fp32's range
+        float f = 1.f;
+        if (far) {
+          pt_add(l_far, z_ref, l_run, m_run - kPtShift);
+          l_run = l_far;
+          z_ref += (float)q8_norm(l_run);
+          f = ptx::ex2(0.5f * (m_run - kPtShift - z_ref));
+          m_run = z_ref + kPtShift;
+        }
+#pragma unroll 1
+        for (int c0 = 0; have_o && c0 < D; c0 += 8) {
+          float ov[8];
+          ptx::tmem_ld8(colO + c0, ov);
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) ov[k] = ov[k] * f * f;
+          ptx::tmem_st8(colO + c0, ov);
+          ptx::tmem_wait_st();
+        }
+      }
+      if (isnan(l_run)) m_run = l_run;  // a NaN query's part: no part without a visible key, which merges leave out
       // read here, not kept through the loop
       const volatile PtPiece& at = s_piece[np % kPtPieces];
       const bool whole = kStream && at.c1 <= at.c0;

@@ -75,6 +75,23 @@ __device__ __forceinline__ void q8_half4(uint32_t w, uint32_t& lo, uint32_t& hi)
       : "=r"(lo), "=r"(hi)
       : "r"(w));
 }
+// Attention with P = 2^(z + e - m + 7), e the value's exponent and m at most 8 below the row's largest z + e, takes the
+// row's sum of weights from 2^-e P while every e is at most 40 either way.  With z' the largest z, m <= z' + 40, so a P
+// below fp32's 2^-126 has z < z' - 53; a term 2^(z - m + 7) is at most 2^(8 - e + 7), 2^55, and that of the key
+// that m comes from at least 2^-33.  Of tiles with an e beyond that (2^-117, say, of a block of zeros) it is taken from z
+// alone, and of all tiles once an e is that large, which lifts m over z.
+constexpr float kQ8Near = 40.f;
+__device__ __forceinline__ bool q8_far(float e) { return !(fabsf(e) <= kQ8Near); }
+// l > 0 to 2^-12..2^-11 times a power of two, whose exponent it returns; 0 and NaN stay.  O against the same
+// reference is then the values' mean times that: the sum of a row's parts, whose weights add up to less than 1, stays
+// below the largest value, and the least, 2^-126, keeps more bits than bf16's 2^-133.
+__device__ __forceinline__ int q8_norm(float& l) {
+  if (!(l > 0.f)) return 0;
+  const int k = (int)(__float_as_uint(l) >> 23) - 127 + 12;
+  l *= q8_two(-k);
+  return k;
+}
+
 // four codes under the scale 2^from, coded for 2^to >= 2^from
 __device__ __forceinline__ uint32_t q8_recode(uint32_t w, float ratio) {
   const float4 f = q8_numbers(w, ratio);
