@@ -237,3 +237,22 @@ def test_appended_zero_values_are_attended(N):
     assert (got[:, :4] == 0).all()
     _compare(got, q, *(x.view(torch.uint8).cpu().numpy() for x in (kc, ks, vc, vs)), table.cpu().numpy(), [P], [N], [P + N],
              [0], None, None, True)
+
+
+def test_append_of_more_declared_rows_than_an_int_of_lanes():
+    # 2^27 declared rows of 160 elements (16 lanes each), of which 100 are active: a view that repeats one row
+    ps, D = 64, 160
+    x = to_dev(synth.normal(synth.rng(7800), (2, 1, 1, 1, D), 1.0, True), True)
+
+    def run(N):
+        kc, vc = (torch.zeros(3, 1, ps, D, dtype=torch.uint8, device=dev()).view(torch.float8_e4m3fn) for _ in range(2))
+        ks, vs = (torch.zeros(3, 1, 1, dtype=torch.uint8, device=dev()) for _ in range(2))
+        st = _status()
+        tv.append_kv_paged(x[0].expand(1, 1, N, D), x[1].expand(1, 1, N, D), kc, vc, i32([[2, 0, 1]]), i32([7]),
+                           n_rows=i32([100]), k_scale=ks, v_scale=vs, dev_status=st)
+        assert int(st.item()) == 0
+        return [t.view(torch.uint8) for t in (kc, vc, ks, vs)]
+    ref, got = run(100), run(1 << 27)
+    assert all((ref[i][2, 0, 7:] != 0).any(-1).all() and (ref[i][0, 0, :43] != 0).any(-1).all() for i in (0, 1))
+    for a, b in zip(ref, got):
+        assert torch.equal(a, b)

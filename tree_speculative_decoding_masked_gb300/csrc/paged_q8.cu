@@ -431,7 +431,7 @@ static cudaError_t launch_qa_t(const RotaryArgs& a, Q8Pages p, cudaStream_t stre
   // whole blocks, a row a thread where 512 threads allow it; calls of few rows need no more threads than those
   const int tile_rows = max(1 << p.block_shift, 256 / lanes), all = tile_rows * lanes;
   const int threads = (int)min((long long)min(all, kQaThreads), ((long long)a.N * lanes + 31) / 32 * 32);
-  if (all > kQaThreads && a.N * lanes > kQaThreads)
+  if (all > kQaThreads && (long long)a.N * lanes > kQaThreads)
     return !wide           ? launch_qa<T, 2, false, false>(a, p, tile_rows, threads, lanes, stream)
            : a.interleaved ? launch_qa<T, 2, true, true>(a, p, tile_rows, threads, lanes, stream)
                            : launch_qa<T, 2, true, false>(a, p, tile_rows, threads, lanes, stream);
