@@ -72,7 +72,6 @@ struct TcArgs {
   void* out;
   const int32_t* parent;
   int B, Hq, Hkv, N, P, G, NT, MT, splits;
-  int mcast;  // attn_pair2_kernel: tile pairs 2c and 2c + 1 form a cluster sharing each K/V tile
   float c;  // softmax scale * log2(e)
   int32_t* dev_status;
 };
@@ -1174,17 +1173,13 @@ __global__ void __launch_bounds__(kP2Threads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int mp = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
   const int hk = blockIdx.y, b = blockIdx.z;
-  // K/V multicast: the two tile pairs of a cluster each load half of every K and V tile
-  // (32 of its 64 rows) into both CTAs' rings; a slot is refilled once both CTAs' products
-  // are done with it (their commits arrive on both CTAs' empty barriers)
-  const bool mc = !kPair && a.mcast != 0;
   // SM pair (kPair): the two CTAs of a cluster (tile pairs 2c and 2c + 1, one KV head)
   // compute every product as one M = 256 MMA issued by the even CTA: the 128 rows of
   // each CTA's row tile X form half of product X.  Each CTA loads its half of every K tile
   // (32 of the 64 keys, both column blocks) and of every V tile (64 of the 128 value
   // columns); the copies complete on the even CTA's barriers, the MMAs' commits arrive on
   // both CTAs' barriers, and both CTAs' softmax warps report P on the even CTA's barrier.
-  const uint32_t crank = (mc || kPair) ? (blockIdx.x & 1u) : 0u;
+  const uint32_t crank = kPair ? (blockIdx.x & 1u) : 0u;
   const bool issuer_cta = !kPair || crank == 0;
   int i0[2];
 #pragma unroll
@@ -1196,9 +1191,9 @@ __global__ void __launch_bounds__(kP2Threads, 1)
     ptx::mbar_init(&bars->q_full, 1);
     for (int s = 0; s < kPair2Slots; ++s) {
       ptx::mbar_init(&bars->k_full[s], 1);
-      ptx::mbar_init(&bars->k_empty[s], mc ? 4 : 2);  // both S issuers (of both CTAs)
+      ptx::mbar_init(&bars->k_empty[s], 2);  // both S issuers
       ptx::mbar_init(&bars->v_full[s], 1);
-      ptx::mbar_init(&bars->v_empty[s], mc ? 2 : 1);
+      ptx::mbar_init(&bars->v_empty[s], 1);
     }
     for (int x = 0; x < 2; ++x)
       for (int u = 0; u < 2; ++u) {
@@ -1256,7 +1251,7 @@ __global__ void __launch_bounds__(kP2Threads, 1)
     ptx::fence_proxy_async_smem();
   }
   ptx::tc_fence_before();
-  if (mc || kPair)
+  if (kPair)
     ptx::cluster_sync();  // the peer's barriers are initialised before anything arrives on them
   else
     __syncthreads();
@@ -1283,21 +1278,11 @@ __global__ void __launch_bounds__(kP2Threads, 1)
 #pragma unroll
   for (int x = 0; x < 2; ++x) ntx[x] = max(0, min(t_allx[x], t_begin + tps) - t_begin);
   const int nt = max(ntx[0], ntx[1]);
-  // K/V tiles streamed: with multicast both CTAs of the cluster stream the longer of their
-  // two ranges (the other one's extra tiles are loaded and released, never computed)
-  int nts = nt;
-  if (mc) {
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int i0p = (2 * (mp ^ 1) + x) * a.NT;
-      if (i0p < n_act) nts = max(nts, (a.P + min(n_act, i0p + a.NT) + kBN2 - 1) / kBN2);
-    }
-  }
   constexpr uint16_t kPairMask = 0x3;
 
   if (warp == 0) {
     // ------------------------------------------------------------------ producers
-    if (lane == 0 && nts > 0) {
+    if (lane == 0 && nt > 0) {
       int issued[kPair2Slots] = {0, 0, 0, 0};
       uint32_t qbytes = 0;
 #pragma unroll
@@ -1317,7 +1302,7 @@ __global__ void __launch_bounds__(kP2Threads, 1)
               else
                 ptx::tma_load_3d(dq, &tmQ, &bars->q_full, db * 64, i0[x], b * a.Hq + hk * a.G + g);
             }
-      for (int t = 0; t < nts; ++t) {
+      for (int t = 0; t < nt; ++t) {
         const int ks = t % kPair2Slots;
         if (t >= kPair2Slots && !ptx::mbar_wait(&bars->k_empty[ks], ((t / kPair2Slots) - 1) & 1, abort_flag))
           break;
@@ -1335,13 +1320,8 @@ __global__ void __launch_bounds__(kP2Threads, 1)
           continue;
         }
         ptx::mbar_arrive_expect_tx(&bars->k_full[ks], (uint32_t)C::kTileBytes);
-        for (int db = 0; db < C::kDB; ++db) {
-          if (mc)
-            ptx::tma_load_3d_mc(dst + db * C::kKVBlock + crank * (kBN2 / 2) * 128, &tmK, &bars->k_full[ks], db * 64,
-                                j0 + (int)crank * (kBN2 / 2), b * a.Hkv + hk, kPairMask);
-          else
-            ptx::tma_load_3d(dst + db * C::kKVBlock, &tmK, &bars->k_full[ks], db * 64, j0, b * a.Hkv + hk);
-        }
+        for (int db = 0; db < C::kDB; ++db)
+          ptx::tma_load_3d(dst + db * C::kKVBlock, &tmK, &bars->k_full[ks], db * 64, j0, b * a.Hkv + hk);
         ++issued[ks];
       }
       if constexpr (kPair) {
@@ -1355,9 +1335,9 @@ __global__ void __launch_bounds__(kP2Threads, 1)
         for (int s = 0; s < kPair2Slots; ++s)
           if (issued[s]) ptx::mbar_wait(&bars->k_full[s], (issued[s] - 1) & 1, abort_flag);
       }
-    } else if (lane == 1 && nts > 0) {
+    } else if (lane == 1 && nt > 0) {
       int issued[kPair2Slots] = {0, 0, 0, 0};
-      for (int t = 0; t < nts; ++t) {
+      for (int t = 0; t < nt; ++t) {
         const int vs = t % kPair2Slots;
         if (t >= kPair2Slots && !ptx::mbar_wait(&bars->v_empty[vs], ((t / kPair2Slots) - 1) & 1, abort_flag))
           break;
@@ -1372,13 +1352,8 @@ __global__ void __launch_bounds__(kP2Threads, 1)
           continue;
         }
         ptx::mbar_arrive_expect_tx(&bars->v_full[vs], (uint32_t)C::kTileBytes);
-        for (int db = 0; db < C::kDB; ++db) {
-          if (mc)
-            ptx::tma_load_3d_mc(dst + db * C::kKVBlock + crank * (kBN2 / 2) * 128, &tmV, &bars->v_full[vs], db * 64,
-                                j0 + (int)crank * (kBN2 / 2), b * a.Hkv + hk, kPairMask);
-          else
-            ptx::tma_load_3d(dst + db * C::kKVBlock, &tmV, &bars->v_full[vs], db * 64, j0, b * a.Hkv + hk);
-        }
+        for (int db = 0; db < C::kDB; ++db)
+          ptx::tma_load_3d(dst + db * C::kKVBlock, &tmV, &bars->v_full[vs], db * 64, j0, b * a.Hkv + hk);
         ++issued[vs];
       }
       for (int s = 0; s < kPair2Slots; ++s)
@@ -1392,14 +1367,14 @@ __global__ void __launch_bounds__(kP2Threads, 1)
     // issued in parallel
     const int x = warp == 1 ? 0 : 1;
     if (lane == 0 && issuer_cta) {
-      if (nts > 0 && ptx::mbar_wait(&bars->q_full, 0, abort_flag)) {
+      if (nt > 0 && ptx::mbar_wait(&bars->q_full, 0, abort_flag)) {
         constexpr uint32_t idS = ptx::idesc_bf16(kPair ? 2 * kRows : kRows, kBN2, false, false);
         const uint32_t qaddr = ptx::smem_addr(sQ + x * C::kQTile);
         uint64_t adq[8];  // the Q tile's A descriptors, one per 16-element K step
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
           adq[kk] = ptx::sdesc_sw128(qaddr + (kk >> 2) * C::kQBlock + (kk & 3) * 32, 16, 1024);
-        for (int t = 0; t < nts; ++t) {
+        for (int t = 0; t < nt; ++t) {
           const int ks = t % kPair2Slots, buf = t & 1;
           if (!ptx::mbar_wait(&bars->k_full[ks], (t / kPair2Slots) & 1, abort_flag)) break;
           if (t < ntx[x]) {
@@ -1429,8 +1404,6 @@ __global__ void __launch_bounds__(kP2Threads, 1)
           }
           if constexpr (kPair)
             ptx::mma_commit_pair_mc(&bars->k_empty[ks], kPairMask);
-          else if (mc)  // this tile is done with the K slot (in both CTAs' rings)
-            ptx::mma_commit_mc(&bars->k_empty[ks], kPairMask);
           else
             ptx::mma_commit(&bars->k_empty[ks]);
         }
@@ -1447,7 +1420,7 @@ __global__ void __launch_bounds__(kP2Threads, 1)
     if (lane == 0 && issuer_cta) {
       constexpr uint32_t idO = ptx::idesc_bf16(kPair ? 2 * kRows : kRows, D, false, true);
       bool ok = true;
-      for (int t = 0; ok && t < nts; ++t) {
+      for (int t = 0; ok && t < nt; ++t) {
         const int vs = t % kPair2Slots, buf = t & 1;
         if (!ptx::mbar_wait(&bars->v_full[vs], (t / kPair2Slots) & 1, abort_flag)) break;
         const uint32_t vaddr = ptx::smem_addr(sV + vs * C::kTileBytes);
@@ -1481,8 +1454,6 @@ __global__ void __launch_bounds__(kP2Threads, 1)
         if (ok) {
           if constexpr (kPair)
             ptx::mma_commit_pair_mc(&bars->v_empty[vs], kPairMask);
-          else if (mc)
-            ptx::mma_commit_mc(&bars->v_empty[vs], kPairMask);
           else
             ptx::mma_commit(&bars->v_empty[vs]);
         }
@@ -1699,9 +1670,9 @@ __global__ void __launch_bounds__(kP2Threads, 1)
     ptx::cluster_sync();
   }
   __syncthreads();
-  // the peer's multicasts and commit arrivals into this CTA are done (SM pair: and the
-  // pair's MMAs, which read and write both CTAs)
-  if (mc || kPair) ptx::cluster_sync();
+  // the peer's commit arrivals into this CTA are done, and the pair's MMAs, which read and
+  // write both CTAs
+  if (kPair) ptx::cluster_sync();
   if (warp == 1) {
     ptx::tc_fence_after();
     if constexpr (kPair)
@@ -2481,8 +2452,8 @@ static cudaError_t launch_tc_d(const CUtensorMap& mq, const CUtensorMap& mk, con
   const dim3 grid(units * a.splits, Hkv, B), block(tc_threads(kVar), 1, 1);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  // SM pairs, K/V-sharing tile pairs, or KV splits
-  attr[0].val.clusterDim.x = (kVar == 5 || a.mcast) ? 2u : (unsigned)a.splits;
+  // SM pairs, or KV splits
+  attr[0].val.clusterDim.x = kVar == 5 ? 2u : (unsigned)a.splits;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   if constexpr (kVar == 1)
@@ -2537,7 +2508,6 @@ cudaError_t launch_attn_tc(const void* q, const void* k, const void* v, void* ou
   a.MT = plan.mtiles;
   a.c = scale * kLog2e;
   a.dev_status = dev_status;
-  a.mcast = 0;
   int var = 1;
   StreamArgs sa{};
   if (D == 64)
@@ -2558,18 +2528,9 @@ cudaError_t launch_attn_tc(const void* q, const void* k, const void* v, void* ou
                                            align256((size_t)2 * sa.C * 2 * kRows * 8));
     }
   }
-  // the paired 64-key kernel without KV splits shares each K/V tile between the two tile
-  // pairs of a cluster (each loads half of its rows, multicast to both) where the tile
-  // pairs of a (sequence, KV head) come in twos and the prefix dominates the key range:
-  // half the L2-to-SM traffic lowers power at the power limit (long-context attention
-  // 427.7 -> 417.7 us in a long loop, SM clock 1905 -> 1972 MHz), while with short
-  // prefixes the two CTAs' lockstep and the pair's extra tile cost more (budget-sweep
-  // trees with P = 4 N: +2.5 %)
-  const int pairs = (plan.mtiles + 1) / 2;
-  a.mcast = (var == 3 && a.splits == 1 && pairs % 2 == 0 && (long long)P >= 64LL * N) ? 1 : 0;
   // rows of one K / V box: each CTA of an SM pair loads 32 keys of a K tile and all 64
   // keys of its half of a V tile
-  const int kkeys = (var == 5 || a.mcast) ? kBN2 / 2 : tc_keys(var);
+  const int kkeys = var == 5 ? kBN2 / 2 : tc_keys(var);
   const int vkeys = var == 5 ? kBN2 : kkeys;
   CUtensorMap mq, mk, mv;
   if (!encode_3d(&mq, q, D, N, (long long)B * Hq, D, (long long)N * D, plan.nt)) return cudaErrorInvalidValue;

@@ -134,16 +134,6 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const void* tmap, uint64_
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v), "r"(smem_addr(bar))
       : "memory");
 }
-// the 3-D box multicast to the CTAs of this cluster in `mask`: written at the same
-// shared-memory offset in each, completing bytes on the mbarrier at the same offset in each
-__device__ __forceinline__ void tma_load_3d_mc(void* dst, const void* tmap, uint64_t* bar, int x, int y, int z,
-                                               uint16_t mask) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], "
-      "[%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_addr(dst)),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar)), "h"(mask)
-      : "memory");
-}
 // SM-pair form (tcgen05 cta_group::2): the box lands in this CTA's shared memory and its
 // bytes complete on the mbarrier at shared::cluster address `bar_cluster`, which may be
 // the peer CTA's (the one issuing the pair's MMAs)
@@ -240,13 +230,6 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
 // mbarrier arrives once every previously issued tcgen05.mma of this thread has completed
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-               : "memory");
-}
-// the same, arriving on the mbarrier at this offset in each CTA of the cluster in `mask`
-__device__ __forceinline__ void mma_commit_mc(uint64_t* bar, uint16_t mask) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-                   smem_addr(bar)),
-               "h"(mask)
                : "memory");
 }
 
