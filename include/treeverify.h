@@ -728,8 +728,14 @@ TV_API tv_status tv_read_kv_paged_q8(const tv_paged_kv* kv, const tv_kv_scale* s
                                      int32_t* dev_status, tv_stream_t stream);
 
 /* tv_paged_attention_q8 - tv_paged_attention over pages in 8 bits; q and out are of dtype.
- * Precision as there, the cached numbers taken as they are.  Limits, workspace (of
- * tv_paged_attention_q8_workspace_size bytes) and errors as there, and those of kv_scale.
+ * Precision as there, the cached numbers taken as they are, but for bf16 rows: a query's elements
+ * are off by up to 2^-17 of its largest, and a weight is held in fp16 times the scale of its value's
+ * block.  It keeps 11 bits while that product is at least 2^-21 of the row's largest one, a bit less
+ * for each factor of 2 below, and none below 2^-32: a block whose scale is that far above the others'
+ * takes those bits from their values in every column.  The sum of weights is held in fp32 whatever
+ * the scales.  With fp32 rows the weighted sum of values must fit fp32 before its division.
+ * Limits, workspace (of tv_paged_attention_q8_workspace_size bytes) and errors as there, and
+ * those of kv_scale.
  */
 TV_API size_t tv_paged_attention_q8_workspace_size(int B, int Hq, int Hkv, int D, int N, int page_size,
                                                    int max_pages, tv_dtype dtype);

@@ -917,7 +917,8 @@ def paged_attention(q, k_cache, v_cache, page_table, prefix_len, *, parent=None,
     kept between calls (omitted, it is allocated and zero-filled at each, which takes some
     20 us; its size is checked by the library).  out: other storage than q's.  Caches of
     torch.float8_e4m3fn come with k_scale and v_scale, as append_kv_paged writes them (workspace:
-    the query's with cache_dtype)."""
+    the query's with cache_dtype); with bf16 queries a weight times its value block's scale keeps
+    11 bits down to 2^-21 of the row's largest such product, fewer below."""
     index = _device_index("q", q)
     kv, B, Hkv, ps, width, D = _paged_kv(k_cache, v_cache, page_table, prefix_len, index)
     if q.ndim != 4:

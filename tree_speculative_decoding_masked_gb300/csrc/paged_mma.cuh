@@ -23,12 +23,13 @@
 //
 // Pages in 8 bits (kQ8, q8.cuh) are the same stream with half the bytes, in tiles of 128 keys, 32 a warp.
 // K's codes go into e4m3 products as they are, with the queries' rows, times a power of two that brings the
-// largest element below 448, as sums of two e4m3 numbers (off by 2^-18 of the largest at most).  V's
+// largest element to 2^7..2^8, as sums of two e4m3 numbers (off by half a step, 2^-10, or 2^-17 of the largest at most).  V's
 // become fp16 numbers, which hold them exactly, in registers on the way: one conversion for two codes, where bf16,
 // whose exponent is another, takes 4.5 instructions and more issue slots than the copies leave.  fp16's range is
 // not that of the numbers, so V's scales stay out of it: with e the exponent of the value's block, P = 2^(z + e - m)
 // and m is the running reference of z + e; the sum takes 2^-e times P, or, once an e is far from 0 (a block of zeros:
-// q8_far), goes by z alone against a reference of its own, of each lane.  A key's scale multiplies its scores, in fp32.  K's
+// q8_far), goes by z alone against a reference of its own, of each lane.  A weight keeps 11 bits while its product with 2^e
+// is at least 2^-21 of the row's largest such product, fewer below, none below 2^-32.  A key's scale multiplies its scores, in fp32.  K's
 // fragments need no transpose and any order of columns, if Q's have the same: a lane takes 16 columns of a key
 // in one load.  Eight lanes take four such chunks of two keys, which the swizzle of 128-byte rows lays on
 // different banks if the keys are four apart: so product row g is key g / 2 + 4 (g % 2) of its eight.  V's

@@ -37,8 +37,8 @@
 // tokens took 264 us, now 238; two of 2048 rows over 3000 to 6000 326, now 310.
 //
 // Pages in 8 bits (kQ8, q8.cuh).  S = Q K^T takes K's codes as they are, as e4m3 products: a row of Q,
-// times a power of two that brings its largest element below 448, is the sum of two rows of e4m3
-// numbers, the nearest ones and the nearest to what those leave, off by 2^-18 of the largest element at most
+// times a power of two that brings its largest element to 2^7..2^8, is the sum of two rows of e4m3
+// numbers, the nearest ones and the nearest to what those leave, off by 2^-17 of the largest element at most
 // (bf16 elements down to 2^-10 of it exactly).  Two products at twice the rate take what one in bf16 did, and
 // K's half comes through L2 and shared memory in half the bytes.  A block's scale of K joins the row's
 // power of two in the factor that the softmax multiplies by anyhow, one for 16 keys.  V's codes become fp16
@@ -46,7 +46,8 @@
 // warps fill; they also zero the rows that no row needs, and bring Q and the scales.  fp16's range is not
 // that of the numbers, so V's scales stay out of it: with e the exponent of the value block, P = 2^(z + e - m) and m
 // is the running reference of z + e, so that P is at most 2^8 (held times 2^7); the sum takes 2^-e times a block's
-// P, or, once an e is far from 0 (a block of zeros: q8_far), goes by z alone.  Warps then: 0 producer, 1 S issuer A,
+// P, or, where an e is far from 0 (a block of zeros: q8_far), goes by z alone.  In fp16 P keeps 11 bits down to 2^-14, 2^-21
+// of the row's largest term, fewer below, none below 2^-32 of it.  Warps then: 0 producer, 1 S issuer A,
 // 2 PV issuer, 3 S issuer B, 4-11 softmax, 12-15 converters, with registers moved from the others to the
 // softmax's (168 and 88 a thread).  V in bf16 with its scales, four times the conversion's instructions, and a
 // factor a key or 16 keys by a branch in one kernel: eight 128-node trees over 32768 tokens 612 us.  Blocks of less
@@ -127,7 +128,7 @@ struct PtBars {
   uint64_t s_done[2];
   uint64_t o_free[2];  // tile x's warps have read O
   uint64_t rows_met;   // the softmax warps meet
-  uint64_t vb_full[kPtVbSlots];   // kQ8: V tiles as bf16
+  uint64_t vb_full[kPtVbSlots];   // kQ8: V tiles as fp16
   uint64_t vb_empty[kPtVbSlots];
   uint64_t scale_full[kPtSlots];  // the keys' scales: a tile's, or a round's
   uint64_t rows_read[2];          // tile x's warps have read their rows' scales
