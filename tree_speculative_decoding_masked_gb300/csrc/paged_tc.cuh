@@ -359,7 +359,7 @@ __device__ __forceinline__ void pt_drain(uint64_t* bar, uint32_t parity, volatil
   if (!ptx::mbar_wait(bar, parity, &quiet)) *abort_flag = 1;
 }
 
-// kQ8's bounded waits, short: the roles' loops share the instruction caches, and what one of them takes more,
+// Bounded waits in few lines (kShort): the roles' loops share the instruction caches, and what one of them takes more,
 // the softmax warps wait for (misses a step 77, of the bf16 kernel 18).  kNap: a role that runs ahead of
 // the others sleeps between looks.  Gives up after kPtLooks looks, some seconds, or when another has.
 constexpr uint32_t kPtLooks = 1u << 26;
@@ -376,9 +376,9 @@ __device__ __forceinline__ bool pt_wait(uint64_t* bar, uint32_t parity, volatile
   }
   return true;
 }
-template <bool kQ8>
+template <bool kShort>
 __device__ __forceinline__ bool pt_wait_for(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  if constexpr (kQ8) return pt_wait<false>(bar, parity, abort);
+  if constexpr (kShort) return pt_wait<false>(bar, parity, abort);
   return ptx::mbar_wait(bar, parity, abort);
 }
 
@@ -424,6 +424,9 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
   ptx::griddep_launch_dependents();
   using C = PtCfg<D, kQ>;
   constexpr bool kQ8 = C::kQ8, kFine = kQ == kPtQ8Fine;
+  // capped scores over bf16 pages too: two chunks of 2048 rows over 3000 to 4000 took 474 us with the longer waits, now
+  // 360; without a cap those are 1 to 2 % faster
+  constexpr bool kShort = kQ8 || kCap != kNoCap;
   extern __shared__ unsigned char smem_raw[];
   const uint32_t mis = ptx::smem_addr(smem_raw) & 1023u;
   unsigned char* sm = smem_raw + ((1024u - mis) & 1023u);
@@ -688,7 +691,7 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
           const unsigned gt = kt + t;
           const int slot = gt % kPtSlots;
           bool got = true;
-          if (gt >= kPtSlots) got = pt_wait_for<kQ8>(&empty[slot], ((gt / kPtSlots) - 1) & 1, abort_flag);
+          if (gt >= kPtSlots) got = pt_wait_for<kShort>(&empty[slot], ((gt / kPtSlots) - 1) & 1, abort_flag);
           if (!__all_sync(0xffffffffu, got)) return false;
           const uint32_t boxes = __ballot_sync(0xffffffffu, pg >= 0);
           if (lane == 0) ptx::mbar_arrive_expect_tx(&full[slot], __popc(boxes) * box_bytes);
@@ -727,7 +730,7 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
         const unsigned dx = pt_of(done_x, x);
         if constexpr (kQ8) {
           // also where the tile has no rows: the converters go by s_done, which may not run ahead of them
-          if (nt > 0) ok = ok && pt_wait_for<kQ8>(&bars->q_full[x], pieces & 1, abort_flag);
+          if (nt > 0) ok = ok && pt_wait_for<kShort>(&bars->q_full[x], pieces & 1, abort_flag);
         } else if (ntm > 0) {
           ptx::mbar_arrive_expect_tx(&bars->q_full[x], (uint32_t)(rows_used * 128 * C::kDB));
           for (int g = 0; g < a.G; ++g)
@@ -745,12 +748,12 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
             adq[kk] = ptx::sdesc_sw128(qaddr + (kk >> 2) * C::kQBlock + (kk & 3) * 32, 16, 1024);
           for (int t = 0; ok && t < nt; ++t) {
             const int ks = (kt + t) % kPtSlots;
-            if (!(ok = pt_wait_for<kQ8>(&bars->k_full[ks], ((kt + t) / kPtSlots) & 1, abort_flag))) break;
+            if (!(ok = pt_wait_for<kShort>(&bars->k_full[ks], ((kt + t) / kPtSlots) & 1, abort_flag))) break;
             if (t < ntm) {
               // S_X(t) overwrites P_X of two tiles before in this buffer
               const unsigned tx = dx + t;
               const int buf = tx & 1;
-              if (tx >= 2 && !(ok = pt_wait_for<kQ8>(&bars->pv_done[x][buf], ((tx - 2) >> 1) & 1, abort_flag))) break;
+              if (tx >= 2 && !(ok = pt_wait_for<kShort>(&bars->pv_done[x][buf], ((tx - 2) >> 1) & 1, abort_flag))) break;
               ptx::tc_fence_after();
               if constexpr (kQ8)
                 pt_s_product_q8(tmem + x * kPtRows + buf * kPtKeys, adq[0],
@@ -782,7 +785,7 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
       };
       auto zero_rows = [&](int t) {
         const int vs = (kt + t) % kPtSlots, j0 = (t_begin + t) * kPtKeys;
-        if (!pt_wait_for<kQ8>(&bars->v_full[vs], ((kt + t) / kPtSlots) & 1, abort_flag)) return;
+        if (!pt_wait_for<kShort>(&bars->v_full[vs], ((kt + t) / kPtSlots) & 1, abort_flag)) return;
         for (int r = lane; r < kPtKeys; r += 32)
           if (j0 + r < lo || j0 + r >= key_end)
             for (int db = 0; db < C::kDB; ++db) {
@@ -796,7 +799,7 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
       auto issue = [&](int t) -> bool {
         constexpr int kSlots = kQ8 ? kPtVbSlots : kPtSlots;
         const int vs = (kt + t) % kSlots;
-        if (!pt_wait_for<kQ8>(kQ8 ? &bars->vb_full[vs] : &bars->v_full[vs], ((kt + t) / kSlots) & 1, abort_flag))
+        if (!pt_wait_for<kShort>(kQ8 ? &bars->vb_full[vs] : &bars->v_full[vs], ((kt + t) / kSlots) & 1, abort_flag))
           return false;
         const uint64_t vd =
             ptx::sdesc_sw128(ptx::smem_addr((kQ8 ? sm + C::kOffVb : sV) + vs * C::kTileBytes), 1024, C::kGroup);
@@ -805,7 +808,7 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
           if (t >= ntx[x]) continue;
           const unsigned tx = done_x[x] + t;
           const int buf = tx & 1;
-          if (!pt_wait_for<kQ8>(&bars->p_full[x][buf], (tx >> 1) & 1, abort_flag)) return false;
+          if (!pt_wait_for<kShort>(&bars->p_full[x][buf], (tx >> 1) & 1, abort_flag)) return false;
           ptx::tc_fence_after();
           pt_pv_product(tmem + C::kColO + x * kPtRows, tmem + x * kPtRows + buf * kPtKeys, vd, 2 * C::kGroup / 16, idO,
                         t > 0 ? 1u : 0u);  // P: 8 columns per 16 keys
@@ -824,7 +827,7 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
         // the piece before's O has been read
         if (kStream && part == 0 && pieces > 0 && nt > 0)
           for (int x = 0; x < 2; ++x)
-            ok = __all_sync(0xffffffffu, ok && pt_wait_for<kQ8>(&bars->o_free[x], (pieces - 1) & 1, abort_flag));
+            ok = __all_sync(0xffffffffu, ok && pt_wait_for<kShort>(&bars->o_free[x], (pieces - 1) & 1, abort_flag));
         if (lane == 0)
           for (; ok && t < to; ++t) ok = issue(t);
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
@@ -841,8 +844,8 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
       for (int x = 0; ok && x < 2 && nt > 0; ++x) {
         // the piece before's products have read Q, and its rows their scales
         if (pieces > 0)
-          ok = __all_sync(0xffffffffu, pt_wait_for<kQ8>(&bars->s_done[x], (pieces - 1) & 1, abort_flag) &&
-                                           pt_wait_for<kQ8>(&bars->rows_read[x], (pieces - 1) & 1, abort_flag));
+          ok = __all_sync(0xffffffffu, pt_wait_for<kShort>(&bars->s_done[x], (pieces - 1) & 1, abort_flag) &&
+                                           pt_wait_for<kShort>(&bars->rows_read[x], (pieces - 1) & 1, abort_flag));
         if (!ok) break;
         unsigned char* sQx = sQ + x * C::kQTile;
         const int part = lane & 7;
@@ -1031,7 +1034,7 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
       // kQ8: the row's power of two, for all of the piece
       float row_f = 1.f;
       if (kQ8 && nt > 0) {
-        ok = ok && __all_sync(0xffffffffu, pt_wait_for<kQ8>(&bars->q_full[x], pieces & 1, abort_flag));
+        ok = ok && __all_sync(0xffffffffu, pt_wait_for<kShort>(&bars->q_full[x], pieces & 1, abort_flag));
         row_f = s_rscale[x * kPtRows + r];
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&bars->rows_read[x]);
@@ -1047,7 +1050,7 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
         if constexpr (kQ8) {
           if (kFine || t % 8 == 0) {
             const unsigned n = kFine ? (kt + t) / kPtSlots : (rounds + t / 8) / 4;
-            ok = __all_sync(0xffffffffu, pt_wait_for<kQ8>(&bars->scale_full[kFine ? (kt + t) % kPtSlots : (rounds + t / 8) & 3],
+            ok = __all_sync(0xffffffffu, pt_wait_for<kShort>(&bars->scale_full[kFine ? (kt + t) % kPtSlots : (rounds + t / 8) & 3],
                                                         n & 1, abort_flag));
             if (!ok) break;
             if (!kFine) now = scales[64] != 0.f;
@@ -1066,7 +1069,7 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
             if (j % 16 == 12) asm volatile("" ::: "memory");
           }
         };
-        ok = __all_sync(0xffffffffu, pt_wait_for<kQ8>(&bars->s_full[x][buf], (tx >> 1) & 1, abort_flag));
+        ok = __all_sync(0xffffffffu, pt_wait_for<kShort>(&bars->s_full[x][buf], (tx >> 1) & 1, abort_flag));
         if (!ok) break;
         ptx::tc_fence_after();
         const int j0 = (t_begin + t) * kPtKeys;
@@ -1232,10 +1235,10 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
         if (__any_sync(0xffffffffu, need) && t > 0) {
           // O_X must hold all of PV_X(t - 1) before it is rescaled
           ok = __all_sync(0xffffffffu,
-                          pt_wait_for<kQ8>(&bars->pv_done[x][(tx - 1) & 1], ((tx - 1) >> 1) & 1, abort_flag));
+                          pt_wait_for<kShort>(&bars->pv_done[x][(tx - 1) & 1], ((tx - 1) >> 1) & 1, abort_flag));
           if (!ok) break;
           ptx::tc_fence_after();
-#pragma unroll(kQ8 ? 1 : D / 32)
+#pragma unroll(kShort ? 1 : D / 32)
           for (int c0 = 0; c0 < D; c0 += 32) {
             float ov[32];
             ptx::tmem_ld32(colO + c0, ov);
@@ -1253,7 +1256,7 @@ __global__ void __launch_bounds__(PtCfg<D, kQ>::kThreads, 1)
       }
       // ---- epilogue: every MMA is complete at o_done
       if (nt > 0) {
-        ok = ok && __all_sync(0xffffffffu, pt_wait_for<kQ8>(&bars->o_done, pieces & 1, abort_flag));
+        ok = ok && __all_sync(0xffffffffu, pt_wait_for<kShort>(&bars->o_done, pieces & 1, abort_flag));
         have_o = ok && ntm > 0;
         if (ok) ptx::tc_fence_after();
       }
