@@ -65,15 +65,20 @@ def _far_check(g, B, Hq, Hkv, D, ps, prefix, N, factor, *, blk, bf16, parent=Non
     kc, ks = q8.quantise(kc, blk)
     vc, vs = q8.quantise(vc, blk)
     st = _status()
-    got = tv.paged_attention(to_dev(q, bf16), torch.from_numpy(kc).to(dev()).view(torch.float8_e4m3fn),
-                             torch.from_numpy(vc).to(dev()).view(torch.float8_e4m3fn), i32(table), i32(prefix),
-                             parent=None if parent is None else i32(parent), n_rows=None if n_rows is None else i32(n_rows),
-                             softcap=softcap, window=window, dev_status=st, k_scale=torch.from_numpy(ks).to(dev()),
-                             v_scale=torch.from_numpy(vs).to(dev()))
-    torch.cuda.synchronize()
-    assert int(st.item()) == 0
-    with np.errstate(invalid="ignore"):  # inactive rows hold anything
-        got = host(got).astype(np.float64)
+    out = torch.full((B, Hq, N, D), 7.0, dtype=torch.bfloat16 if bf16 else torch.float32, device=dev())
+
+    def call():
+        return tv.paged_attention(to_dev(q, bf16), torch.from_numpy(kc).to(dev()).view(torch.float8_e4m3fn),
+                                  torch.from_numpy(vc).to(dev()).view(torch.float8_e4m3fn), i32(table), i32(prefix),
+                                  parent=None if parent is None else i32(parent),
+                                  n_rows=None if n_rows is None else i32(n_rows), softcap=softcap, window=window, out=out,
+                                  dev_status=st, k_scale=torch.from_numpy(ks).to(dev()),
+                                  v_scale=torch.from_numpy(vs).to(dev())).clone()
+    got = call()
+    assert torch.equal(call(), got) and int(st.item()) == 0
+    got = host(got).astype(np.float64)
+    for b in range(B):
+        assert np.all(got[b, :, act[b]:] == 7.0), "inactive rows were written"
     _compare(got, q, kc, ks, vc, vs, table, prefix, act, lens, low, parent, n_rows, bf16, window, softcap)
     return got
 
@@ -144,6 +149,14 @@ def test_attend_zero_values_behind_a_window(window, N, bf16):
     # a far block within the window of some rows and behind that of others
     for where in ("300", "last", "every other 16"):
         _far_check(synth.rng(7300 + N), 1, 8, 2, 128, 16, [900], N, _zeros(where), blk=16, bf16=bf16, window=window)
+
+
+@pytest.mark.parametrize("softcap", [20.0, 1000.0])
+@pytest.mark.parametrize("blk", [1, 16])
+@pytest.mark.parametrize("N", [1, 4, 70])
+def test_attend_zero_values_under_a_cap(N, blk, softcap):
+    for where in ("64", "beside 2^30", "2^-90 to 2^90"):
+        _far_check(synth.rng(7350 + N), 1, 8, 2, 128, 16, [500], N, _zeros(where), blk=blk, bf16=True, softcap=softcap)
 
 
 def _bytes_check(N, blk, draw, prefix=700):
