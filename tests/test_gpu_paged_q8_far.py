@@ -269,3 +269,31 @@ def test_append_of_more_declared_rows_than_an_int_of_lanes():
     assert all((ref[i][2, 0, 7:] != 0).any(-1).all() and (ref[i][0, 0, :43] != 0).any(-1).all() for i in (0, 1))
     for a, b in zip(ref, got):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("q8_pages", [True, False])
+@pytest.mark.parametrize("N,D", [(1, 128), (4, 128), (1, 64), (2, 256)])
+def test_long_batches_repeat_bit_for_bit(N, D, q8_pages):
+    # a persistent grid that streams a gigabyte: slots of its ring are refilled while their readers still run
+    g = torch.Generator(device=dev()).manual_seed(7900 + N + D)
+    B, Hkv, ps = 24 if q8_pages else 12, 8, 16
+    width = 16384 // ps
+    lens = torch.randint(8192, 16384 - N, (B,), generator=g, device=dev()).int()
+    table = torch.randperm(B * width, generator=g, device=dev()).int().view(B, width)
+    shape = (B * width, Hkv, ps, D)
+    kw = {}
+    if q8_pages:
+        kc, vc = (torch.randint(0, 112, shape, generator=g, device=dev(), dtype=torch.uint8) for _ in range(2))
+        kc, vc = (x.bitwise_or_(torch.randint(0, 2, shape, generator=g, device=dev(), dtype=torch.uint8) << 7)
+                  .view(torch.float8_e4m3fn) for x in (kc, vc))
+        kw = dict(k_scale=torch.randint(119, 121, (B * width, Hkv, 1), generator=g, device=dev(), dtype=torch.uint8),
+                  v_scale=torch.randint(119, 121, (B * width, Hkv, 1), generator=g, device=dev(), dtype=torch.uint8))
+    else:
+        kc, vc = (torch.randn(shape, generator=g, device=dev(), dtype=torch.bfloat16) for _ in range(2))
+    q = torch.randn((B, 4 * Hkv, N, D), generator=g, device=dev(), dtype=torch.bfloat16)
+    ws = torch.zeros(tv.paged_attention_workspace_size(B, 4 * Hkv, Hkv, D, N, ps, width, torch.bfloat16, cache_dtype=kc.dtype),
+                     dtype=torch.uint8, device=dev())
+    first = tv.paged_attention(q, kc, vc, table, lens, workspace=ws, **kw)
+    assert torch.isfinite(first).all()
+    different = sum(not torch.equal(tv.paged_attention(q, kc, vc, table, lens, workspace=ws, **kw), first) for _ in range(60))
+    assert different == 0

@@ -534,9 +534,15 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
               *reinterpret_cast<uint4*>(sV + (rr >> 3) * C::kGroup + (rest / kRowChunks) * C::kBlock +
                                         (rr & 7) * C::kRow + rest % kRowChunks * 16) = make_uint4(0, 0, 0, 0);
           }
-          ptx::fence_proxy_async_smem();  // before the slot is refilled
           __syncwarp();
         }
+        // The slot goes back to the copies.  The fence orders this lane's reads and zeroes before their writes, which are
+        // the async proxy's: without it the last ldmatrix of a tile read the next tile's values now and then
+        auto free_slot = [&] {
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&bars->empty[slot]);
+        };
         if constexpr (kQ8) {
           // ---- 16 keys at a time; with one row tile both together, so that their latencies overlap
           auto key_of_row = [](int g) -> int { return C::kCols == 64 ? g : g >> 1 | (g & 1) << 2; };
@@ -708,8 +714,7 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
               }
             }
           }
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&bars->empty[slot]);
+          free_slot();
           continue;
         } else {
           // K as the A operand: keys (lane & 15), column chunks kk * 2 + (lane >> 4).  A batch's loads are
@@ -815,8 +820,7 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
 #pragma unroll
               for (int nt = 0; nt < C::kNT; ++nt) pm_mma(o[k0 + i][nt], vf[i], pf[nt][0], pf[nt][1]);
           }
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&bars->empty[slot]);
+          free_slot();
         }
       }
 
