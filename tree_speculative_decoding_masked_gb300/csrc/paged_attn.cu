@@ -9,8 +9,8 @@
 // row tiles 539; at 32 (8 nodes) the stream's warp-level products set the pace, 768 us against
 // 540.  Over 500 to 1000 tokens 75 against 69 us at 16 rows and 115 against 69 at 32; one sequence
 // of 2048 12.0 against 11.5 and 15.2 against 11.5: the rule gives short ranges' 5 % for long ones' 10.
-// Over 8-bit pages the same rule: at 16 rows the stream takes 466, 76 and 13.9 us for these three and row tiles 553,
-// 102 and 14.0; at 32 rows row tiles 550, 104 and 14.0.  fp32 rows over 8-bit pages: at most 4 paged_rows_kernel,
+// Over 8-bit pages the same rule: at 16 rows the stream takes 455, 75 and 14.2 us for these three and row tiles 553,
+// 102 and 14.0; at 32 rows row tiles 568, 104 and 14.4.  fp32 rows over 8-bit pages: at most 4 paged_rows_kernel,
 // more paged_f32_kernel (both sides: paged_rows.cuh).
 #include <atomic>
 

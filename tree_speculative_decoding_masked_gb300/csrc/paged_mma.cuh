@@ -34,9 +34,9 @@
 // in one load.  Eight lanes take four such chunks of two keys, which the swizzle of 128-byte rows lays on
 // different banks if the keys are four apart: so product row g is key g / 2 + 4 (g % 2) of its eight.  V's
 // come by transposing loads of 16-bit pairs (two columns of a key), whose bytes are dealt to two product
-// rows.  64 tokens over 8192 to 16384: 278 us, 5.7 TB/s (with values of zeros throughout 330); without the products the copies alone take 252, in boxes of
+// rows.  64 tokens over 8192 to 16384: 279 us, 5.7 TB/s (with values of zeros throughout 330); without the products the copies alone take 252, in boxes of
 // 64-byte rows 260.  With K in fp16 too, 64 keys a tile, 16 a warp, and scales looked up for each key of a tile: 1900
-// instructions for 64 keys and 390 us.  One token over 2048: 8.9 us; with a key a block 64 take 359.
+// instructions for 64 keys and 390 us.  One token over 2048: 8.9 us; with a key a block 64 take 360.
 #pragma once
 
 #include "paged.cuh"
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(PmCfg<kD, kRT, kQ8>::kThreads, 1)
   // which ptxas takes for every kernel that moves any: 12 warps of 168 are 4 of 72 and 8 of 216).  They move once: a
   // second move would need each warpgroup's warps to meet before it, and producers never meet, so clusters, whose warps
   // share code at the end, move none.  Two row tiles spilled without (16 rows over 8192 to 16384, 64 sequences: 580
-  // us, now 452; 8 rows 285, now 278).
+  // us, now 455; 8 rows 285, now 279).
   constexpr bool kShift = kQ8 && C::kWarps == 8 && kStream;
   ptx::griddep_launch_dependents();
   extern __shared__ unsigned char pm_raw[];
