@@ -299,7 +299,7 @@ __device__ __forceinline__ int unit_slot(long long c, long long per, long long u
 // How scores are capped in the bf16 kernels: not at all; by soft_tanh; or, past kPlainCap, by capped_score.
 // soft_tanh is off by some 2^-22 of 1 however small its argument, and a score by that times the cap:
 // at 256 a weight by 2^-14, little beside its rounding to bf16.  Two chunks of 2048 rows over 3000 to 6000
-// tokens: 436 us by soft_tanh4, 614 by the series; one token each of 32 sequences 126 by either.
+// tokens: 463 us by soft_tanh4, 654 by the series; one token each of 32 sequences 126 by either.
 enum { kNoCap, kTanhCap, kLargeCap };
 constexpr float kPlainCap = 256.f;
 inline int cap_mode(float cap) { return cap > kPlainCap ? kLargeCap : cap > 0.f ? kTanhCap : kNoCap; }
